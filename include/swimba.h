@@ -391,6 +391,177 @@ int swimba_scan_streams_plan(const swimba_stream_args* a, int* chunk, int* nchun
 int swimba_scan_streams(const swimba_stream_args* a, void* ws, size_t ws_bytes,
                         hipStream_t stream);
 
+/*
+ * Tokens by expert.  Between the router and the experts' own projections (the
+ * products that emit the per-slot streams of swimba_scan_streams) a token's
+ * row is copied to its k selected experts and their outputs are brought back
+ * weighted by the gates ([SW] Dutch summary "Kernmechanisme van Swimba": the
+ * active experts of a token and their weights).  Slot t * k + j is token t's
+ * j-th choice.
+ *
+ * swimba_sort_tokens -- a stable sort of the slots by expert.
+ *   idx     [T, k]    experts; a value outside [0, E) is a slot without an
+ *                     expert (a dropped slot, a padded token): it takes no row
+ *   order   [T * k]   out, or NULL: the slot of each row; -1 behind the last
+ *   pos     [T, k]    out: the row of each slot; -1 without an expert
+ *   offsets [E + 1]   out: expert e holds rows offsets[e] .. offsets[e+1] - 1,
+ *                     in order of their slots
+ *   ws, ws_bytes: device workspace of at least
+ *   swimba_sort_tokens_workspace_size(T, E, k) bytes, 256-byte aligned.
+ * Constraints: T >= 0, 1 <= k <= E <= SWIMBA_MAX_EXPERTS, T * k <= 2^30
+ * (SWIMBA_EUNSUPPORTED above).  T == 0 writes zero offsets.
+ */
+size_t swimba_sort_tokens_workspace_size(int64_t T, int E, int k);
+int swimba_sort_tokens(const int32_t* idx, int64_t T, int E, int k, int32_t* order, int32_t* pos,
+                       int32_t* offsets, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * swimba_dispatch_tokens -- rows[pos[t, j], :] = x[t, :].
+ *   x     [T, D], rows [T * k, D] out, both of dtype x_dtype
+ *   pos   [T, k]  rows of the slots, each used once; a value outside
+ *                 [0, T * k) is a slot without a row
+ * Rows that no slot has are left as they were.  Its gradient is
+ * swimba_combine_tokens of the rows' gradients without gates.
+ */
+int swimba_dispatch_tokens(const void* x, swimba_dtype x_dtype, const int32_t* pos, int64_t T,
+                           int D, int k, void* rows, hipStream_t stream);
+
+/*
+ * swimba_combine_tokens -- y[t, :] = sum_j gate[t, j] rows[pos[t, j], :], over
+ * the slots that have a row, in slot order, in fp32 (zero without any).
+ *   gate  [T, k] fp32, or NULL for ones;  y [T, D] out, dtype y_dtype
+ */
+int swimba_combine_tokens(const void* rows, swimba_dtype rows_dtype, const int32_t* pos,
+                          const float* gate, int64_t T, int D, int k, void* y,
+                          swimba_dtype y_dtype, hipStream_t stream);
+
+/*
+ * swimba_combine_tokens_backward -- gradients of swimba_combine_tokens:
+ *   drows[pos[t, j], :] = gate[t, j] dy[t, :]      [T * k, D] out, drows_dtype
+ *   dgate[t, j] = <dy[t, :], rows[pos[t, j], :]>   [T, k] out, fp32; 0 without a row
+ * Rows of drows that no slot has are left as they were.  drows must not
+ * overlap rows or dy.
+ */
+int swimba_combine_tokens_backward(const void* rows, swimba_dtype rows_dtype, const int32_t* pos,
+                                   const float* gate, const void* dy, swimba_dtype dy_dtype,
+                                   int64_t T, int D, int k, void* drows, swimba_dtype drows_dtype,
+                                   float* dgate, hipStream_t stream);
+
+/*
+ * swimba_route_backward -- gradients of swimba_route's gates for dL/dgate (as
+ * swimba_scan_backward and swimba_combine_tokens_backward give it).  The
+ * selection itself has no gradient: with s_j = gate_j (dgate_j - sum_i gate_i
+ * dgate_i),
+ *   dx[t, :]  = sum_j s_j Wr[:, idx[t, j]]                 [T, D] out, dx_dtype
+ *   dWr[:, e] = sum over the slots of expert e of s x[t, :]  [D, E] out, fp32
+ *   x, Wr, idx, gate: swimba_route's arguments and results; dgate [T, k] fp32
+ *   ws, ws_bytes: device workspace of at least
+ *   swimba_route_backward_workspace_size(T, D, E) bytes, 256-byte aligned.
+ * An expert listed twice for one token adds twice; a value outside [0, E)
+ * adds nothing, and x of a token without any expert is not read.  With k == 1
+ * the gate is constant and both gradients are zero.  Sums are fp32 in a fixed
+ * order (deterministic).  Values of x must be finite: an infinity or a NaN in
+ * a token that has an expert makes its channel of dWr NaN for every expert.
+ * Constraints: those of swimba_route.  T == 0 writes dWr = 0.
+ */
+size_t swimba_route_backward_workspace_size(int64_t T, int D, int E);
+int swimba_route_backward(const void* x, swimba_dtype x_dtype, const float* Wr, const int32_t* idx,
+                          const float* gate, const float* dgate, int64_t T, int D, int E, int k,
+                          void* dx, swimba_dtype dx_dtype, float* dWr, void* ws, size_t ws_bytes,
+                          hipStream_t stream);
+
+/*
+ * Linear attention with a decay per head: the selective recurrence with one
+ * scalar transition per head and a state of N keys by P values ([SW] Spanish
+ * summary "Arquitectura de Swimba", French "Architecture de Swimba": Mamba-2,
+ * whose SSD operator this is; [MB] "SSMs": h_t = A h_{t-1} + B x_t, y_t = C h_t
+ * with C = q, B = k, x = v):
+ *   h_t = exp(log_decay_t) h_{t-1} + k_t v_t^T,   y_t = h_t^T q_t.
+ */
+typedef enum { SWIMBA_DECAY_HEAD = 0, SWIMBA_DECAY_TOKEN = 1 } swimba_decay_form;
+
+typedef struct {
+  int B, L, H, G, N, P;         /* batch, length, heads, heads of q and k (G divides H:
+                                   head h reads q and k of h / (H / G)), key and value size */
+  swimba_dtype in_dtype;        /* dtype of q, k, v                                       */
+  swimba_dtype y_dtype;         /* dtype of y                                             */
+  swimba_decay_form decay_form; /* log_decay is [H] (HEAD) or [B, L, H] (TOKEN)           */
+  const void* q;                /* [B, L, G, N]                                           */
+  const void* k;                /* [B, L, G, N]                                           */
+  const void* v;                /* [B, L, H, P]                                           */
+  const float* log_decay;       /* natural logarithm of the decay, <= 0; -INFINITY clears
+                                   the state (the first token of a packed document).
+                                   Values above 0 are taken as they are                   */
+  const float* h0;              /* NULL = zeros; [B, H, N, P]                             */
+  void* y;                      /* [B, L, H, P]  out                                      */
+  float* h_final;               /* NULL = not written; [B, H, N, P]                       */
+} swimba_linear_attention_args;
+
+/*
+ * swimba_linear_attention -- the whole sequence, 64 tokens at a time on the matrix
+ * units.
+ *   ws, ws_bytes: device workspace of at least
+ *   swimba_linear_attention_workspace_size(a) bytes, 256-byte aligned; needed where a
+ *   long sequence is walked in segments.  Planned for the current device by
+ *   the query and for the device of `stream` by the call.
+ * bf16 inputs multiply exactly and sum in fp32; states are fp32.  Non-finite
+ * inputs reach every later output of their sequence and head, also across a
+ * cleared state, and the outputs up to 63 tokens before them.
+ * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256
+ * (SWIMBA_EUNSUPPORTED above).  L == 0 writes h_final = h0 (or zeros).
+ */
+size_t swimba_linear_attention_workspace_size(const swimba_linear_attention_args* a);
+int swimba_linear_attention(const swimba_linear_attention_args* a, void* ws, size_t ws_bytes,
+                     hipStream_t stream);
+
+typedef struct {
+  swimba_linear_attention_args fwd;    /* the forward call's arguments; its y and h_final are not
+                                   used                                                    */
+  const void* dy;               /* [B, L, H, P]  dL/dy, dtype in_dtype                     */
+  const float* dh_final;        /* [B, H, N, P]  dL/dh_final, or NULL for zero             */
+  swimba_dtype grad_dtype;      /* dtype of dq, dk, dv                                     */
+  void* dq;                     /* [B, L, G, N]  out, summed over the heads that share it  */
+  void* dk;                     /* [B, L, G, N]  out, summed over the heads that share it  */
+  void* dv;                     /* [B, L, H, P]  out                                       */
+  float* dlog_decay;            /* [H] (summed over batch and tokens) or [B, L, H]  out; 0
+                                   where exp(log_decay) is 0                               */
+  float* dh0;                   /* [B, H, N, P]  out, or NULL                              */
+} swimba_linear_attention_grad_args;
+
+/*
+ * swimba_linear_attention_backward -- gradients of swimba_linear_attention, from its inputs
+ * (nothing of the forward pass is kept).  Workspace as there, sized by
+ * swimba_linear_attention_backward_workspace_size(g).  Every output is deterministic.
+ * Constraints: those of swimba_linear_attention, and P <= 256.  L == 0 or B == 0
+ * writes dh0 = dh_final (or zeros) and a zero dlog_decay [H].
+ */
+size_t swimba_linear_attention_backward_workspace_size(
+    const swimba_linear_attention_grad_args* g);
+int swimba_linear_attention_backward(const swimba_linear_attention_grad_args* g, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+typedef struct {
+  int B, H, G, N, P;
+  swimba_dtype in_dtype, y_dtype;
+  swimba_decay_form decay_form; /* log_decay is [H] (HEAD) or [B, H] (TOKEN)               */
+  const void* q;                /* [B, G, N]                                               */
+  const void* k;                /* [B, G, N]                                               */
+  const void* v;                /* [B, H, P]                                               */
+  const float* log_decay;
+  float* state;                 /* [B, H, N, P] fp32, read; updated in place unless
+                                   state_out is given                                      */
+  float* state_out;             /* NULL, or [B, H, N, P] out: `state` itself or a buffer
+                                   that does not overlap it                                */
+  void* y;                      /* [B, H, P] out                                           */
+} swimba_linear_attention_step_args;
+
+/*
+ * swimba_linear_attention_step -- one decoding step of swimba_linear_attention on a
+ * persistent state: the same as a sequence of one token with h0 = state and
+ * h_final = state_out (or state).  Constraints: those of swimba_linear_attention.
+ */
+int swimba_linear_attention_step(const swimba_linear_attention_step_args* a, hipStream_t stream);
+
 /* Static string for a status code. */
 const char* swimba_status_string(int status);
 

@@ -1,0 +1,583 @@
+// Linear attention: host side of the walks (attention.hpp), the carry between
+// segments, the gradients of the decays and the single-token step.
+#include "attention.hpp"
+
+namespace swimba {
+namespace {
+
+int checked() { return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP; }
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// First state of every segment from the segments' end states (in place):
+// first(0) = s0, first(i + 1) = decay(i) first(i) + end(i).  One thread per
+// state entry; the loads of the next segments do not wait for the sums.
+__global__ __launch_bounds__(256) void attn_carry_kernel(AttnParams p) {
+  const int64_t n = (int64_t)p.Kd * p.Cd, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t bh = blockIdx.y;
+  if (e >= n) return;
+  const int64_t row = e / p.Cd, c = e - row * p.Cd;
+  float cur = p.s0 != nullptr ? p.s0[bh * n + row * p.sk + c * p.sc] : 0.f;
+  float* st = p.seg_state + bh * p.nseg * n + e;
+  const float* dec = p.seg_decay + bh * p.nseg;
+  constexpr int kAhead = 8;
+  float end[kAhead];
+  for (int s = 0; s < p.nseg; s += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) end[i] = s + i < p.nseg - 1 ? st[(s + i) * n] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s + i >= p.nseg) break;
+      st[(s + i) * n] = cur;
+      if (s + i < p.nseg - 1) cur = fmaf(dec[s + i], cur, end[i]);
+    }
+  }
+}
+
+// out[b, h] = <a, b> over a state, in 64 bits.
+__global__ __launch_bounds__(256) void attn_dot_kernel(const float* a, const float* b, double* out,
+                                                       int64_t n) {
+  __shared__ double part[256];
+  const int64_t at = (int64_t)blockIdx.x * n;
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 256) s += (double)a[at + i] * (double)b[at + i];
+  part[threadIdx.x] = s;
+  __syncthreads();
+  for (int w = 128; w > 0; w >>= 1) {
+    if ((int)threadIdx.x < w) part[threadIdx.x] += part[threadIdx.x + w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) out[blockIdx.x] = part[0];
+}
+
+// Gradients of the log decays.  In a chunk, with row_r and col_s the sums of
+// (q_r . k_s)(dy_r . v_s) D[r][s] over the pairs s <= r of the chunk (the walks'
+// <q, dq> and <k, dk> inside the chunk), a_r what r reads of the chunk's first
+// state and b_s what later chunks read of s:
+//   dg_t = sum_{r >= t} (row_r - col_r + a_r) + sum_{s < t} b_s + through
+// where `through` is what later chunks read of the first state: with X the
+// product of state and adjoint at a chunk's end, through = X - sum b, and X at
+// its beginning is through + sum a.  The cancelling sums stay inside a chunk.
+struct DecayGradParams {
+  const float *zq, *zk;   // [B, H, ctiles, 2, L] of the dq and dk walks
+  const double* x_end;    // [B, H] X behind the last chunk, or null for zero
+  double* diff;           // [B, H, chunks] sum a - sum b
+  double* part;           // [B, H, chunks] sums of dg (a decay per head), or null
+  const float* g;
+  float* dg;              // [B, L, H] or [H]
+  int B, L, H, ctiles, nc, token_decay;
+};
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+struct DecayTerms {
+  double inside, a, b;
+};
+
+__device__ __forceinline__ DecayTerms decay_terms(const DecayGradParams& p, int64_t bh, int t) {
+  DecayTerms r = {0.0, 0.0, 0.0};
+  if (t < p.L) {
+    for (int i = 0; i < p.ctiles; ++i) {
+      const int64_t at = (bh * p.ctiles + i) * 2 * p.L + t;
+      r.inside += (double)p.zq[at] - (double)p.zk[at];
+      r.a += p.zq[at + p.L];
+      r.b += p.zk[at + p.L];
+    }
+  }
+  return r;
+}
+
+__global__ __launch_bounds__(256) void attn_decay_diff_kernel(DecayGradParams p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (w >= (int64_t)p.B * p.H * p.nc) return;
+  const int64_t bh = w / p.nc;
+  const int c = (int)(w - bh * p.nc);
+  const DecayTerms r = decay_terms(p, bh, c * kChunk + lane);
+  const double d = wave_sum(r.a - r.b);
+  if (lane == 0) p.diff[w] = d;
+}
+
+__global__ __launch_bounds__(256) void attn_decay_grad_kernel(DecayGradParams p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (w >= (int64_t)p.B * p.H * p.nc) return;
+  const int64_t bh = w / p.nc;
+  const int c = (int)(w - bh * p.nc), h = (int)(bh % p.H), t = c * kChunk + lane;
+  double x = 0.0;
+  for (int i = c + 1 + lane; i < p.nc; i += 64) x += p.diff[bh * p.nc + i];
+  x = wave_sum(x) + (p.x_end != nullptr ? p.x_end[bh] : 0.0);
+  const DecayTerms r = decay_terms(p, bh, t);
+  double after = r.inside + r.a, before = r.b;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const double o = __shfl_down(after, m), q = __shfl_up(before, m);
+    if (lane + m < 64) after += o;
+    if (lane >= m) before += q;
+  }
+  // x - (all b) + (earlier b): minus this and the later ones
+  const double later = __shfl(before, 63) - (before - r.b);
+  double dg = after + (x - later);
+  if (t < p.L) {
+    const float g = p.token_decay ? p.g[(bh / p.H * p.L + t) * p.H + h] : p.g[h];
+    if (hw_exp2(g * kLog2e) == 0.f) dg = 0.0;  // nothing passes, whatever g is near by
+    if (p.token_decay) p.dg[(bh / p.H * p.L + t) * p.H + h] = (float)dg;
+  } else {
+    dg = 0.0;
+  }
+  if (p.part != nullptr) {
+    dg = wave_sum(dg);
+    if (lane == 0) p.part[w] = dg;
+  }
+}
+
+// dg[h] = sum over sequences and chunks, one workgroup per head.
+__global__ __launch_bounds__(256) void attn_decay_sum_kernel(const double* part, float* dg, int B,
+                                                             int H, int nc) {
+  __shared__ double s[256];
+  const int h = blockIdx.x;
+  double v = 0.0;
+  for (int64_t i = threadIdx.x; i < (int64_t)B * nc; i += 256) {
+    const int64_t b = i / nc;
+    v += part[(b * H + h) * nc + (i - b * nc)];
+  }
+  s[threadIdx.x] = v;
+  __syncthreads();
+  for (int w = 128; w > 0; w >>= 1) {
+    if ((int)threadIdx.x < w) s[threadIdx.x] += s[threadIdx.x + w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) dg[h] = (float)s[0];
+}
+
+// out[t, g, :] = sum over the heads of group g, in order, of in[t, h, :].
+template <typename TO>
+__global__ __launch_bounds__(256) void attn_share_sum_kernel(const float* in, TO* out, int64_t rows,
+                                                             int share, int N) {
+  const int ppr = (N + kPack - 1) / kPack;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = i / ppr;
+  if (r >= rows) return;
+  const int c = (int)(i - r * ppr) * kPack;
+  float acc[kPack] = {};
+  for (int s = 0; s < share; ++s) {
+    const Pack<float> v = load_pack(in + (r * share + s) * N + c, N - c);
+#pragma unroll
+    for (int k = 0; k < kPack; ++k) acc[k] += v.v[k];
+  }
+  Pack<TO> o;
+#pragma unroll
+  for (int k = 0; k < kPack; ++k) o.v[k] = from_f32<TO>(acc[k]);
+  store_pack(out + r * N + c, o, N - c);
+}
+
+// One token: h' = e^g h + k v^T, y = h'^T q.  The state is read and written
+// once (8 bytes per entry against 2 multiply-adds), so the rest only has to
+// stay out of the way.  A workgroup takes `slice` columns of one head's state:
+// V of them per thread, rows spread over the workgroup's row lanes, and adds
+// the row lanes' parts of y in LDS in order.
+struct AttnStepParams {
+  const void *q, *k, *v;
+  const float* g;
+  const float* state;
+  float* out;
+  void* y;
+  int H, share, N, P, token_decay, y_bf16;
+  int slice, slices, cg;  // columns per workgroup, workgroups per head, column groups
+};
+
+constexpr int kMaxRows = 256;  // N
+
+template <typename TI, int V>
+__global__ __launch_bounds__(256) void attn_step_kernel(AttnStepParams p) {
+  __shared__ float sq[kMaxRows], sk[kMaxRows];
+  __shared__ float part[256 * V];
+  const int64_t bh = blockIdx.x / p.slices;
+  const int c0 = (int)(blockIdx.x % p.slices) * p.slice;
+  const int64_t b = bh / p.H;
+  const int h = (int)(bh - b * p.H);
+  const int rl = 256 / p.cg;  // row lanes
+  const int r0 = threadIdx.x / p.cg, cg = threadIdx.x % p.cg, c = c0 + cg * V;
+  const int end = c0 + p.slice < p.P ? c0 + p.slice : p.P;
+  const bool on = r0 < rl && c < end;  // V divides P where it is not one
+  const float* st = p.state + bh * p.N * p.P + c;
+  float* so = p.out + bh * p.N * p.P + c;
+
+  constexpr int kAhead = 16 / V > 8 ? 8 : (V == 4 ? 8 : 16);
+  float cur[kAhead][V];
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int n = base + i * rl;
+      if (on && n < p.N) {
+        if constexpr (V == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(st + (int64_t)n * p.P);
+          cur[i][0] = f.x; cur[i][1] = f.y; cur[i][2] = f.z; cur[i][3] = f.w;
+        } else {
+          cur[i][0] = st[(int64_t)n * p.P];
+        }
+      }
+    }
+  };
+  fetch(r0);  // in flight while q, k and the decay come
+  const TI* q = static_cast<const TI*>(p.q) + (b * (p.H / p.share) + h / p.share) * p.N;
+  const TI* k = static_cast<const TI*>(p.k) + (b * (p.H / p.share) + h / p.share) * p.N;
+  if ((int)threadIdx.x < p.N) {
+    sq[threadIdx.x] = to_f32(q[threadIdx.x]);
+    sk[threadIdx.x] = to_f32(k[threadIdx.x]);
+  }
+  float vv[V], acc[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    vv[j] = on ? to_f32(static_cast<const TI*>(p.v)[bh * p.P + c + j]) : 0.f;
+    acc[j] = 0.f;
+  }
+  const float e = hw_exp2(p.g[p.token_decay ? bh : h] * kLog2e);
+  __syncthreads();
+  for (int base = r0; base < p.N; base += kAhead * rl) {
+    if (base != r0) fetch(base);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int n = base + i * rl;
+      if (!on || n >= p.N) continue;
+      const float kn = sk[n], qn = sq[n];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        cur[i][j] = fmaf(e, cur[i][j], kn * vv[j]);
+        acc[j] = fmaf(qn, cur[i][j], acc[j]);
+      }
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(so + (int64_t)n * p.P) =
+            make_float4(cur[i][0], cur[i][1], cur[i][2], cur[i][3]);
+      else
+        so[(int64_t)n * p.P] = cur[i][0];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) part[threadIdx.x * V + j] = acc[j];
+  __syncthreads();
+  const int col = threadIdx.x;
+  if (col < p.cg * V && c0 + col < end) {
+    float s = 0.f;
+    for (int r = 0; r < rl; ++r) s += part[r * p.cg * V + col];
+    const int64_t at = bh * p.P + c0 + col;
+    if (p.y_bf16) static_cast<bf16_t*>(p.y)[at] = from_f32<bf16_t>(s);
+    else static_cast<float*>(p.y)[at] = s;
+  }
+}
+
+__global__ __launch_bounds__(256) void attn_copy_kernel(const float* in, float* out, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) out[i] = in != nullptr ? in[i] : 0.f;
+}
+
+int copy_or_zero(const float* in, float* out, int64_t n, hipStream_t s) {
+  if (n <= 0) return SWIMBA_OK;
+  hipLaunchKernelGGL(attn_copy_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, in, out,
+                     n);
+  return checked();
+}
+
+// How one walk is laid out over the device.
+struct WalkPlan {
+  int waves = 1, nseg = 1, seg_chunks = 1;
+  size_t state_bytes = 0, decay_bytes = 0;
+  size_t bytes() const { return state_bytes + decay_bytes; }
+};
+
+WalkPlan plan_walk(bool f32, int B, int L, int H, int share, int Kd, int Cd, int dev) {
+  WalkPlan w;
+  const int ctiles = (Cd + 31) / 32;
+  const int64_t units = (int64_t)share * ctiles;
+  w.waves = units >= 3 ? 4 : (int)units;
+  if (f32 && Kd > 128) w.waves = 1;
+  const int64_t nc = (L + kChunk - 1) / kChunk;
+  const int64_t base = (int64_t)B * (H / share) * ((units + w.waves - 1) / w.waves);
+  // eight waves per CU from the independent walks, or from segments of them
+  // (whose first states cost a pass over k and v) of four chunks or more
+  int64_t want = 8LL * device_cus(dev) / (base * w.waves > 0 ? base * w.waves : 1);
+  if (want > nc / 4) want = nc / 4;
+  if (want < 2) want = 1;
+  w.seg_chunks = (int)((nc + want - 1) / want);
+  if (w.seg_chunks < 1) w.seg_chunks = 1;
+  w.nseg = nc > 0 ? (int)((nc + w.seg_chunks - 1) / w.seg_chunks) : 1;
+  if (w.nseg > 1) {
+    w.state_bytes = align256((size_t)B * H * w.nseg * Kd * Cd * sizeof(float));
+    w.decay_bytes = align256((size_t)B * H * w.nseg * sizeof(float));
+  }
+  return w;
+}
+
+int dispatch(const AttnParams& p, bool f32, int waves, bool state, bool exact, hipStream_t s) {
+  const int k = p.Kd;
+  if (f32) {
+    if (k <= 32) return attn_f32_32(p, waves, state, exact, s);
+    if (k <= 64) return attn_f32_64(p, waves, state, exact, s);
+    if (k <= 128) return attn_f32_128(p, waves, state, exact, s);
+    return attn_f32_256(p, waves, state, exact, s);
+  }
+  if (k <= 32) return attn_bf16_32(p, waves, state, exact, s);
+  if (k <= 64) return attn_bf16_64(p, waves, state, exact, s);
+  if (k <= 128) return attn_bf16_128(p, waves, state, exact, s);
+  return attn_bf16_256(p, waves, state, exact, s);
+}
+
+// One walk; ws holds the plan's segment states.
+int walk(AttnParams p, const WalkPlan& w, bool f32, bool exact, unsigned char* ws, hipStream_t s) {
+  p.nseg = w.nseg;
+  p.seg_chunks = w.seg_chunks;
+  p.ctiles = (p.Cd + 31) / 32;
+  if (w.nseg > 1) {
+    p.seg_state = reinterpret_cast<float*>(ws);
+    p.seg_decay = reinterpret_cast<float*>(ws + w.state_bytes);
+    const int rc = dispatch(p, f32, w.waves, true, true, s);
+    if (rc != SWIMBA_OK) return rc;
+    const int64_t n = (int64_t)p.Kd * p.Cd;
+    hipLaunchKernelGGL(attn_carry_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)(p.B * p.H)),
+                       dim3(256), 0, s, p);
+    if (checked() != SWIMBA_OK) return SWIMBA_EHIP;
+  }
+  return dispatch(p, f32, w.waves, false, exact, s);
+}
+
+AttnParams base_params(const swimba_linear_attention_args* a) {
+  AttnParams p = {};
+  p.g = a->log_decay;
+  p.B = a->B;
+  p.L = a->L;
+  p.H = a->H;
+  p.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
+  return p;
+}
+
+struct GradPlan {
+  WalkPlan q, v;  // dq and dk walk (states [P][N]), dv walk (states [N][P])
+  size_t off_zq = 0, off_zk = 0, off_diff = 0, off_part = 0, off_x = 0, off_end = 0, off_rows = 0;
+  size_t bytes = 0;
+  int nc = 0, ntiles = 0;
+};
+
+GradPlan plan_grad(const swimba_linear_attention_grad_args* g, int dev) {
+  const swimba_linear_attention_args* a = &g->fwd;
+  const bool f32 = a->in_dtype == SWIMBA_F32;
+  GradPlan r;
+  r.q = plan_walk(f32, a->B, a->L, a->H, 1, a->P, a->N, dev);
+  r.v = plan_walk(f32, a->B, a->L, a->H, a->H / a->G, a->N, a->P, dev);
+  r.nc = (a->L + kChunk - 1) / kChunk;
+  r.ntiles = (a->N + 31) / 32;
+  size_t o = r.q.bytes() > r.v.bytes() ? r.q.bytes() : r.v.bytes();  // one walk after the other
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  const size_t bh = (size_t)a->B * a->H;
+  r.off_zq = take(bh * r.ntiles * 2 * a->L * sizeof(float));
+  r.off_zk = take(bh * r.ntiles * 2 * a->L * sizeof(float));
+  r.off_diff = take(bh * r.nc * sizeof(double));
+  r.off_part = take(a->decay_form == SWIMBA_DECAY_HEAD ? bh * r.nc * sizeof(double) : 0);
+  r.off_x = take(bh * sizeof(double));
+  r.off_end = take(g->dh_final != nullptr ? bh * a->N * a->P * sizeof(float) : 0);
+  // per-head rows of dq, then of dk, where heads share them
+  r.off_rows = take(a->H != a->G ? bh * a->L * a->N * sizeof(float) : 0);
+  r.bytes = o;
+  return r;
+}
+
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<unsigned char*>(ws) + off);
+}
+
+int share_sum(const float* rows, void* out, swimba_dtype d, const swimba_linear_attention_args* a,
+              hipStream_t s) {
+  const int64_t r = (int64_t)a->B * a->L * a->G;
+  const int64_t packs = r * ((a->N + kPack - 1) / kPack);
+  const dim3 grid((unsigned)((packs + 255) / 256));
+  if (d == SWIMBA_BF16)
+    hipLaunchKernelGGL((attn_share_sum_kernel<bf16_t>), grid, dim3(256), 0, s, rows,
+                       static_cast<bf16_t*>(out), r, a->H / a->G, a->N);
+  else
+    hipLaunchKernelGGL((attn_share_sum_kernel<float>), grid, dim3(256), 0, s, rows,
+                       static_cast<float*>(out), r, a->H / a->G, a->N);
+  return checked();
+}
+
+}  // namespace
+
+size_t attention_bytes(const swimba_linear_attention_args* a, int dev) {
+  if (a->B == 0 || a->L == 0) return 0;
+  return plan_walk(a->in_dtype == SWIMBA_F32, a->B, a->L, a->H, a->H / a->G, a->N, a->P, dev)
+      .bytes();
+}
+
+int launch_attention(const swimba_linear_attention_args* a, void* ws, int dev, hipStream_t s) {
+  const int64_t states = (int64_t)a->B * a->H * a->N * a->P;
+  if (a->B == 0 || a->L == 0)
+    return a->h_final != nullptr ? copy_or_zero(a->h0, a->h_final, states, s) : SWIMBA_OK;
+  const bool f32 = a->in_dtype == SWIMBA_F32;
+  const WalkPlan w = plan_walk(f32, a->B, a->L, a->H, a->H / a->G, a->N, a->P, dev);
+  AttnParams p = base_params(a);
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.y = a->y;
+  p.qshare = a->H / a->G;
+  p.vshare = 1;
+  p.Kd = a->N;
+  p.Cd = a->P;
+  p.y_bf16 = a->y_dtype == SWIMBA_BF16;
+  p.s0 = a->h0;
+  p.s_final = a->h_final;
+  p.sk = a->P;
+  p.sc = 1;
+  return walk(p, w, f32, a->y_dtype == SWIMBA_F32, static_cast<unsigned char*>(ws), s);
+}
+
+size_t attention_backward_bytes(const swimba_linear_attention_grad_args* g, int dev) {
+  if (g->fwd.B == 0 || g->fwd.L == 0) return 0;
+  return plan_grad(g, dev).bytes;
+}
+
+int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* ws, int dev,
+                              hipStream_t s) {
+  const swimba_linear_attention_args* a = &g->fwd;
+  const int64_t states = (int64_t)a->B * a->H * a->N * a->P;
+  if (a->B == 0 || a->L == 0) {
+    int rc = SWIMBA_OK;
+    if (g->dh0 != nullptr) rc = copy_or_zero(g->dh_final, g->dh0, states, s);
+    if (rc == SWIMBA_OK && a->decay_form == SWIMBA_DECAY_HEAD)
+      rc = copy_or_zero(nullptr, g->dlog_decay, a->H, s);
+    return rc;
+  }
+  const bool f32 = a->in_dtype == SWIMBA_F32, shared = a->H != a->G;
+  const GradPlan r = plan_grad(g, dev);
+  unsigned char* seg = static_cast<unsigned char*>(ws);
+  float *zq = at<float>(ws, r.off_zq), *zk = at<float>(ws, r.off_zk);
+  float *rows = at<float>(ws, r.off_rows), *end = at<float>(ws, r.off_end);
+
+  // dq = walk(dY, V, K)
+  AttnParams p = base_params(a);
+  p.q = g->dy;
+  p.k = a->v;
+  p.v = a->k;
+  p.qshare = 1;
+  p.vshare = a->H / a->G;
+  p.Kd = a->P;
+  p.Cd = a->N;
+  p.sk = 1;
+  p.sc = a->P;
+  p.s0 = a->h0;
+  p.s_final = g->dh_final != nullptr ? end : nullptr;
+  p.z = a->q;
+  p.zsum = zq;
+  p.y = shared ? static_cast<void*>(rows) : g->dq;
+  p.y_bf16 = !shared && g->grad_dtype == SWIMBA_BF16;
+  int rc = walk(p, r.q, f32, true, seg, s);
+  if (rc == SWIMBA_OK && shared) rc = share_sum(rows, g->dq, g->grad_dtype, a, s);
+  if (rc != SWIMBA_OK) return rc;
+
+  // dk = backward walk(V, dY, Q)
+  p.q = a->v;
+  p.k = g->dy;
+  p.v = a->q;
+  p.reverse = 1;
+  p.s0 = g->dh_final;
+  p.s_final = nullptr;
+  p.z = a->k;
+  p.zsum = zk;
+  p.y = shared ? static_cast<void*>(rows) : g->dk;
+  rc = walk(p, r.q, f32, true, seg, s);
+  if (rc == SWIMBA_OK && shared) rc = share_sum(rows, g->dk, g->grad_dtype, a, s);
+  if (rc != SWIMBA_OK) return rc;
+
+  // dv = backward walk(K, Q, dY), whose last state is dh0
+  p = base_params(a);
+  p.q = a->k;
+  p.k = a->q;
+  p.v = g->dy;
+  p.qshare = a->H / a->G;
+  p.vshare = 1;
+  p.Kd = a->N;
+  p.Cd = a->P;
+  p.sk = a->P;
+  p.sc = 1;
+  p.reverse = 1;
+  p.s0 = g->dh_final;
+  p.s_final = g->dh0;
+  p.y = g->dv;
+  p.y_bf16 = g->grad_dtype == SWIMBA_BF16;
+  rc = walk(p, r.v, f32, g->grad_dtype == SWIMBA_F32, seg, s);
+  if (rc != SWIMBA_OK) return rc;
+
+  DecayGradParams d;
+  d.zq = zq;
+  d.zk = zk;
+  d.x_end = nullptr;
+  d.diff = at<double>(ws, r.off_diff);
+  d.part = a->decay_form == SWIMBA_DECAY_HEAD ? at<double>(ws, r.off_part) : nullptr;
+  d.g = a->log_decay;
+  d.dg = g->dlog_decay;
+  d.B = a->B;
+  d.L = a->L;
+  d.H = a->H;
+  d.ctiles = r.ntiles;
+  d.nc = r.nc;
+  d.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
+  if (g->dh_final != nullptr) {
+    double* x = at<double>(ws, r.off_x);
+    hipLaunchKernelGGL(attn_dot_kernel, dim3(a->B * a->H), dim3(256), 0, s, end, g->dh_final, x,
+                       (int64_t)a->N * a->P);
+    d.x_end = x;
+  }
+  const unsigned wg = (unsigned)(((int64_t)a->B * a->H * r.nc + 3) / 4);
+  hipLaunchKernelGGL(attn_decay_diff_kernel, dim3(wg), dim3(256), 0, s, d);
+  hipLaunchKernelGGL(attn_decay_grad_kernel, dim3(wg), dim3(256), 0, s, d);
+  if (d.part != nullptr)
+    hipLaunchKernelGGL(attn_decay_sum_kernel, dim3(a->H), dim3(256), 0, s, d.part, g->dlog_decay,
+                       a->B, a->H, r.nc);
+  return checked();
+}
+
+int launch_attention_step(const swimba_linear_attention_step_args* a, int dev, hipStream_t s) {
+  AttnStepParams p;
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.g = a->log_decay;
+  p.state = a->state;
+  p.out = a->state_out != nullptr ? a->state_out : a->state;
+  p.y = a->y;
+  p.H = a->H;
+  p.share = a->H / a->G;
+  p.N = a->N;
+  p.P = a->P;
+  p.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
+  p.y_bf16 = a->y_dtype == SWIMBA_BF16;
+  const bool vec = a->P % 4 == 0 && ((reinterpret_cast<uintptr_t>(p.state) |
+                                      reinterpret_cast<uintptr_t>(p.out)) & 15) == 0;
+  const int V = vec ? 4 : 1;
+  // columns per workgroup: narrower slices, down to 64-byte rows, where the
+  // heads alone do not give two workgroups per CU
+  int slice = vec ? 128 : 64;
+  const int64_t heads = (int64_t)a->B * a->H, target = 2LL * device_cus(dev);
+  while (slice > 16 && heads * ((a->P + slice - 1) / slice) < target) slice >>= 1;
+  p.slice = slice < a->P ? slice : a->P;
+  p.slices = (a->P + p.slice - 1) / p.slice;
+  p.cg = (p.slice + V - 1) / V;
+  const int64_t grid = heads * p.slices;
+  if (grid > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
+  const dim3 g((unsigned)grid), t(256);
+  const bool bf = a->in_dtype == SWIMBA_BF16;
+  if (vec && bf) hipLaunchKernelGGL((attn_step_kernel<bf16_t, 4>), g, t, 0, s, p);
+  else if (vec) hipLaunchKernelGGL((attn_step_kernel<float, 4>), g, t, 0, s, p);
+  else if (bf) hipLaunchKernelGGL((attn_step_kernel<bf16_t, 1>), g, t, 0, s, p);
+  else hipLaunchKernelGGL((attn_step_kernel<float, 1>), g, t, 0, s, p);
+  return checked();
+}
+
+}  // namespace swimba

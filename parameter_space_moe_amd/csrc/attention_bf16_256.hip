@@ -1,0 +1,8 @@
+// Linear attention walks, bf16 operands, rows of up to 256 (attention.hpp).
+#include "attention.hpp"
+
+namespace swimba {
+int attn_bf16_256(const AttnParams& p, int waves, bool state, bool exact, hipStream_t s) {
+  return attn_launch_waves<bf16_t, 8>(p, waves, state, exact, s);
+}
+}  // namespace swimba

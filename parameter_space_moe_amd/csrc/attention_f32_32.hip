@@ -1,0 +1,8 @@
+// Linear attention walks, f32 operands, rows of up to 32 (attention.hpp).
+#include "attention.hpp"
+
+namespace swimba {
+int attn_f32_32(const AttnParams& p, int waves, bool state, bool exact, hipStream_t s) {
+  return attn_launch_waves<float, 1>(p, waves, state, exact, s);
+}
+}  // namespace swimba

@@ -422,6 +422,58 @@ int run_scan_noalloc(const swimba_scan_args* a, hipStream_t s) {
   return run_scan(a, ws, p.bytes > 0 ? kScratchBytes : 0, s, 0);
 }
 
+bool aligned_to(const void* p, uintptr_t mask) {
+  return (reinterpret_cast<uintptr_t>(p) & mask) == 0;
+}
+bool aligned_as(const void* p, swimba_dtype d) { return aligned_to(p, d == SWIMBA_BF16 ? 1 : 3); }
+
+// A caller's workspace of at least `need` bytes.
+bool workspace_ok(const void* ws, size_t ws_bytes, size_t need) {
+  return need == 0 || (ws != nullptr && ws_bytes >= need && aligned_to(ws, 255));
+}
+
+int validate_tokens(int64_t T, int D, int k) {
+  if (T < 0 || D < 1 || k < 1) return SWIMBA_EINVAL;
+  if (T > (int64_t(1) << 30) / k) return SWIMBA_EUNSUPPORTED;
+  return SWIMBA_OK;
+}
+
+int validate_attention(int B, int L, int H, int G, int N, int P, swimba_dtype in, swimba_dtype out,
+                       swimba_decay_form form) {
+  if (B < 0 || L < 0 || H < 1 || G < 1 || N < 1 || P < 1 || H % G != 0) return SWIMBA_EINVAL;
+  if (!dtype_ok(in) || !dtype_ok(out)) return SWIMBA_EINVAL;
+  if (form != SWIMBA_DECAY_HEAD && form != SWIMBA_DECAY_TOKEN) return SWIMBA_EINVAL;
+  if (N > 256) return SWIMBA_EUNSUPPORTED;
+  // workgroups are counted in 31 bits
+  if ((int64_t)B * H * ((P + 15) / 16) > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
+  return SWIMBA_OK;
+}
+
+int validate_attention(const swimba_linear_attention_args* a) {
+  if (a == nullptr) return SWIMBA_EINVAL;
+  return validate_attention(a->B, a->L, a->H, a->G, a->N, a->P, a->in_dtype, a->y_dtype,
+                            a->decay_form);
+}
+
+int validate_attention_inputs(const swimba_linear_attention_args* a) {
+  if (a->B == 0 || a->L == 0) return SWIMBA_OK;
+  if (a->q == nullptr || a->k == nullptr || a->v == nullptr || a->log_decay == nullptr)
+    return SWIMBA_EINVAL;
+  if (!aligned_as(a->q, a->in_dtype) || !aligned_as(a->k, a->in_dtype) ||
+      !aligned_as(a->v, a->in_dtype))
+    return SWIMBA_EINVAL;
+  return SWIMBA_OK;
+}
+
+int validate_attention_grad(const swimba_linear_attention_grad_args* g) {
+  if (g == nullptr) return SWIMBA_EINVAL;
+  const int rc = validate_attention(&g->fwd);
+  if (rc != SWIMBA_OK) return rc;
+  if (!dtype_ok(g->grad_dtype)) return SWIMBA_EINVAL;
+  // the values are rows of the dq and dk walks
+  return g->fwd.P > 256 ? SWIMBA_EUNSUPPORTED : SWIMBA_OK;
+}
+
 }  // namespace
 }  // namespace swimba
 
@@ -526,6 +578,140 @@ int swimba_step(const swimba_step_args* a, hipStream_t stream) {
       (a->a_form == SWIMBA_A_DIAGONAL && (reinterpret_cast<uintptr_t>(a->A) & 15)))
     return SWIMBA_EINVAL;
   return launch_step(a, stream);
+}
+
+size_t swimba_sort_tokens_workspace_size(int64_t T, int E, int k) {
+  if (T < 0 || k < 1 || k > E || E > SWIMBA_MAX_EXPERTS || validate_tokens(T, 1, k) != SWIMBA_OK)
+    return 0;
+  return sort_tokens_bytes(T, E, k);
+}
+
+int swimba_sort_tokens(const int32_t* idx, int64_t T, int E, int k, int32_t* order, int32_t* pos,
+                       int32_t* offsets, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (E < 1 || k < 1 || k > E) return SWIMBA_EINVAL;
+  const int rc = validate_tokens(T, 1, k);
+  if (rc != SWIMBA_OK) return rc;
+  if (E > SWIMBA_MAX_EXPERTS) return SWIMBA_EUNSUPPORTED;
+  if (offsets == nullptr || (T > 0 && (idx == nullptr || pos == nullptr))) return SWIMBA_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, sort_tokens_bytes(T, E, k))) return SWIMBA_EWORKSPACE;
+  return launch_sort_tokens(idx, T, E, k, order, pos, offsets, ws, stream);
+}
+
+int swimba_dispatch_tokens(const void* x, swimba_dtype x_dtype, const int32_t* pos, int64_t T,
+                           int D, int k, void* rows, hipStream_t stream) {
+  if (!dtype_ok(x_dtype)) return SWIMBA_EINVAL;
+  const int rc = validate_tokens(T, D, k);
+  if (rc != SWIMBA_OK) return rc;
+  if (T == 0) return SWIMBA_OK;
+  if (x == nullptr || pos == nullptr || rows == nullptr || !aligned_as(x, x_dtype) ||
+      !aligned_as(rows, x_dtype))
+    return SWIMBA_EINVAL;
+  return launch_dispatch_tokens(x, x_dtype, pos, T, D, k, rows, stream);
+}
+
+int swimba_combine_tokens(const void* rows, swimba_dtype rows_dtype, const int32_t* pos,
+                          const float* gate, int64_t T, int D, int k, void* y,
+                          swimba_dtype y_dtype, hipStream_t stream) {
+  if (!dtype_ok(rows_dtype) || !dtype_ok(y_dtype)) return SWIMBA_EINVAL;
+  const int rc = validate_tokens(T, D, k);
+  if (rc != SWIMBA_OK) return rc;
+  if (T == 0) return SWIMBA_OK;
+  if (rows == nullptr || pos == nullptr || y == nullptr || !aligned_as(rows, rows_dtype) ||
+      !aligned_as(y, y_dtype))
+    return SWIMBA_EINVAL;
+  return launch_combine_tokens(rows, rows_dtype, pos, gate, T, D, k, y, y_dtype, stream);
+}
+
+int swimba_combine_tokens_backward(const void* rows, swimba_dtype rows_dtype, const int32_t* pos,
+                                   const float* gate, const void* dy, swimba_dtype dy_dtype,
+                                   int64_t T, int D, int k, void* drows, swimba_dtype drows_dtype,
+                                   float* dgate, hipStream_t stream) {
+  if (!dtype_ok(rows_dtype) || !dtype_ok(dy_dtype) || !dtype_ok(drows_dtype)) return SWIMBA_EINVAL;
+  const int rc = validate_tokens(T, D, k);
+  if (rc != SWIMBA_OK) return rc;
+  if (T == 0) return SWIMBA_OK;
+  if (rows == nullptr || pos == nullptr || gate == nullptr || dy == nullptr || drows == nullptr ||
+      dgate == nullptr || !aligned_as(rows, rows_dtype) || !aligned_as(dy, dy_dtype) ||
+      !aligned_as(drows, drows_dtype))
+    return SWIMBA_EINVAL;
+  return launch_combine_tokens_backward(rows, rows_dtype, pos, gate, dy, dy_dtype, T, D, k, drows,
+                                        drows_dtype, dgate, stream);
+}
+
+size_t swimba_route_backward_workspace_size(int64_t T, int D, int E) {
+  if (T < 0 || D < 1 || E < 1 || E > SWIMBA_MAX_EXPERTS) return 0;
+  return route_backward_bytes(T, D, E, -1);
+}
+
+int swimba_route_backward(const void* x, swimba_dtype x_dtype, const float* Wr, const int32_t* idx,
+                          const float* gate, const float* dgate, int64_t T, int D, int E, int k,
+                          void* dx, swimba_dtype dx_dtype, float* dWr, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+  if (T < 0 || D < 1 || E < 1 || k < 1 || k > E || !dtype_ok(x_dtype) || !dtype_ok(dx_dtype))
+    return SWIMBA_EINVAL;
+  if (E > SWIMBA_MAX_EXPERTS) return SWIMBA_EUNSUPPORTED;
+  if (Wr == nullptr || dWr == nullptr) return SWIMBA_EINVAL;
+  if (T > 0 && (x == nullptr || idx == nullptr || gate == nullptr || dgate == nullptr ||
+                dx == nullptr || !aligned_as(x, x_dtype) || !aligned_as(dx, dx_dtype)))
+    return SWIMBA_EINVAL;
+  const int dev = stream_device(stream);
+  if (!workspace_ok(ws, ws_bytes, route_backward_bytes(T, D, E, dev))) return SWIMBA_EWORKSPACE;
+  return launch_route_backward(x, x_dtype, Wr, idx, gate, dgate, T, D, E, k, dx, dx_dtype, dWr, ws,
+                               dev, stream);
+}
+
+size_t swimba_linear_attention_workspace_size(const swimba_linear_attention_args* a) {
+  return validate_attention(a) == SWIMBA_OK ? attention_bytes(a, -1) : 0;
+}
+
+int swimba_linear_attention(const swimba_linear_attention_args* a, void* ws, size_t ws_bytes,
+                     hipStream_t stream) {
+  int rc = validate_attention(a);
+  if (rc != SWIMBA_OK) return rc;
+  rc = validate_attention_inputs(a);
+  if (rc != SWIMBA_OK) return rc;
+  if (a->B > 0 && a->L > 0 && (a->y == nullptr || !aligned_as(a->y, a->y_dtype)))
+    return SWIMBA_EINVAL;
+  const int dev = stream_device(stream);
+  if (!workspace_ok(ws, ws_bytes, attention_bytes(a, dev))) return SWIMBA_EWORKSPACE;
+  return launch_attention(a, ws, dev, stream);
+}
+
+size_t swimba_linear_attention_backward_workspace_size(
+    const swimba_linear_attention_grad_args* g) {
+  return validate_attention_grad(g) == SWIMBA_OK ? attention_backward_bytes(g, -1) : 0;
+}
+
+int swimba_linear_attention_backward(const swimba_linear_attention_grad_args* g, void* ws, size_t ws_bytes,
+                              hipStream_t stream) {
+  int rc = validate_attention_grad(g);
+  if (rc != SWIMBA_OK) return rc;
+  rc = validate_attention_inputs(&g->fwd);
+  if (rc != SWIMBA_OK) return rc;
+  if (g->dlog_decay == nullptr) return SWIMBA_EINVAL;
+  if (g->fwd.B > 0 && g->fwd.L > 0) {
+    if (g->dy == nullptr || g->dq == nullptr || g->dk == nullptr || g->dv == nullptr ||
+        !aligned_as(g->dy, g->fwd.in_dtype) || !aligned_as(g->dq, g->grad_dtype) ||
+        !aligned_as(g->dk, g->grad_dtype) || !aligned_as(g->dv, g->grad_dtype))
+      return SWIMBA_EINVAL;
+  }
+  const int dev = stream_device(stream);
+  if (!workspace_ok(ws, ws_bytes, attention_backward_bytes(g, dev))) return SWIMBA_EWORKSPACE;
+  return launch_attention_backward(g, ws, dev, stream);
+}
+
+int swimba_linear_attention_step(const swimba_linear_attention_step_args* a, hipStream_t stream) {
+  if (a == nullptr) return SWIMBA_EINVAL;
+  const int rc = validate_attention(a->B, 1, a->H, a->G, a->N, a->P, a->in_dtype, a->y_dtype,
+                                    a->decay_form);
+  if (rc != SWIMBA_OK) return rc;
+  if (a->B == 0) return SWIMBA_OK;
+  if (a->q == nullptr || a->k == nullptr || a->v == nullptr || a->log_decay == nullptr ||
+      a->state == nullptr || a->y == nullptr || !aligned_as(a->q, a->in_dtype) ||
+      !aligned_as(a->k, a->in_dtype) || !aligned_as(a->v, a->in_dtype) ||
+      !aligned_as(a->y, a->y_dtype))
+    return SWIMBA_EINVAL;
+  return launch_attention_step(a, stream_device(stream), stream);
 }
 
 const char* swimba_status_string(int status) {

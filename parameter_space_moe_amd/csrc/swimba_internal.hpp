@@ -78,6 +78,30 @@ int launch_streams_ff(const swimba_stream_args* a, const ScanPlan& p, void* ws, 
 int launch_streams_fb(const swimba_stream_args* a, const ScanPlan& p, void* ws, hipStream_t s);
 int launch_streams_bf(const swimba_stream_args* a, const ScanPlan& p, void* ws, hipStream_t s);
 int launch_streams_bb(const swimba_stream_args* a, const ScanPlan& p, void* ws, hipStream_t s);
+// Tokens by expert (tokens.hip) and the router's backward (route_backward.hip).
+size_t sort_tokens_bytes(int64_t T, int E, int k);
+int launch_sort_tokens(const int32_t* idx, int64_t T, int E, int k, int32_t* order, int32_t* pos,
+                       int32_t* offsets, void* ws, hipStream_t s);
+int launch_dispatch_tokens(const void* x, swimba_dtype xd, const int32_t* pos, int64_t T, int D,
+                           int k, void* rows, hipStream_t s);
+int launch_combine_tokens(const void* rows, swimba_dtype rd, const int32_t* pos, const float* gate,
+                          int64_t T, int D, int k, void* y, swimba_dtype yd, hipStream_t s);
+int launch_combine_tokens_backward(const void* rows, swimba_dtype rd, const int32_t* pos,
+                                   const float* gate, const void* dy, swimba_dtype dyd, int64_t T,
+                                   int D, int k, void* drows, swimba_dtype drd, float* dgate,
+                                   hipStream_t s);
+size_t route_backward_bytes(int64_t T, int D, int E, int dev);
+int launch_route_backward(const void* x, swimba_dtype xd, const float* Wr, const int32_t* idx,
+                          const float* gate, const float* dgate, int64_t T, int D, int E, int k,
+                          void* dx, swimba_dtype dxd, float* dWr, void* ws, int dev,
+                          hipStream_t s);
+// Linear attention (attention.hip).  Sizes are valid; `dev` as in plan_scan.
+size_t attention_bytes(const swimba_linear_attention_args* a, int dev);
+int launch_attention(const swimba_linear_attention_args* a, void* ws, int dev, hipStream_t s);
+size_t attention_backward_bytes(const swimba_linear_attention_grad_args* g, int dev);
+int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* ws, int dev,
+                              hipStream_t s);
+int launch_attention_step(const swimba_linear_attention_step_args* a, int dev, hipStream_t s);
 // Pass 2 of the chunked scans: carried-in state per chunk (rows = 16, or 16 per
 // trajectory: E * 16 per expert, k * 16 per routing slot, with E passed as the
 // trajectory count).

@@ -7,6 +7,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -60,6 +61,26 @@ class StreamArgs(ctypes.Structure):
                 ("chunk", _ci), ("carry", _ci), ("phase_events", _vp)]
 
 
+class LinearAttentionArgs(ctypes.Structure):
+    _fields_ = [("B", _ci), ("L", _ci), ("H", _ci), ("G", _ci), ("N", _ci), ("P", _ci),
+                ("in_dtype", _ci), ("y_dtype", _ci), ("decay_form", _ci),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("log_decay", _vp), ("h0", _vp),
+                ("y", _vp), ("h_final", _vp)]
+
+
+class LinearAttentionGradArgs(ctypes.Structure):
+    _fields_ = [("fwd", LinearAttentionArgs), ("dy", _vp), ("dh_final", _vp),
+                ("grad_dtype", _ci), ("dq", _vp), ("dk", _vp), ("dv", _vp), ("dlog_decay", _vp),
+                ("dh0", _vp)]
+
+
+class LinearAttentionStepArgs(ctypes.Structure):
+    _fields_ = [("B", _ci), ("H", _ci), ("G", _ci), ("N", _ci), ("P", _ci),
+                ("in_dtype", _ci), ("y_dtype", _ci), ("decay_form", _ci),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("log_decay", _vp), ("state", _vp),
+                ("state_out", _vp), ("y", _vp)]
+
+
 class SwimbaError(RuntimeError):
     def __init__(self, fn, status):
         super().__init__("%s failed: %s (%d)" % (fn, status_string(status), status))
@@ -105,6 +126,34 @@ def load(path: str | None = None):
     lib.swimba_scan_backward.restype = _ci
     lib.swimba_step.argtypes = [ctypes.POINTER(StepArgs), _vp]
     lib.swimba_step.restype = _ci
+    _i64, _sz = ctypes.c_int64, ctypes.c_size_t
+    lib.swimba_sort_tokens_workspace_size.argtypes = [_i64, _ci, _ci]
+    lib.swimba_sort_tokens_workspace_size.restype = _sz
+    lib.swimba_sort_tokens.argtypes = [_vp, _i64, _ci, _ci, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.swimba_sort_tokens.restype = _ci
+    lib.swimba_dispatch_tokens.argtypes = [_vp, _ci, _vp, _i64, _ci, _ci, _vp, _vp]
+    lib.swimba_dispatch_tokens.restype = _ci
+    lib.swimba_combine_tokens.argtypes = [_vp, _ci, _vp, _vp, _i64, _ci, _ci, _vp, _ci, _vp]
+    lib.swimba_combine_tokens.restype = _ci
+    lib.swimba_combine_tokens_backward.argtypes = [_vp, _ci, _vp, _vp, _vp, _ci, _i64, _ci, _ci,
+                                                   _vp, _ci, _vp, _vp]
+    lib.swimba_combine_tokens_backward.restype = _ci
+    lib.swimba_route_backward_workspace_size.argtypes = [_i64, _ci, _ci]
+    lib.swimba_route_backward_workspace_size.restype = _sz
+    lib.swimba_route_backward.argtypes = [_vp, _ci, _vp, _vp, _vp, _vp, _i64, _ci, _ci, _ci, _vp,
+                                          _ci, _vp, _vp, _sz, _vp]
+    lib.swimba_route_backward.restype = _ci
+    for fn, args in ((lib.swimba_linear_attention, LinearAttentionArgs),
+                     (lib.swimba_linear_attention_backward, LinearAttentionGradArgs)):
+        fn.argtypes = [ctypes.POINTER(args), _vp, _sz, _vp]
+        fn.restype = _ci
+    for fn, args in ((lib.swimba_linear_attention_workspace_size, LinearAttentionArgs),
+                     (lib.swimba_linear_attention_backward_workspace_size,
+                      LinearAttentionGradArgs)):
+        fn.argtypes = [ctypes.POINTER(args)]
+        fn.restype = _sz
+    lib.swimba_linear_attention_step.argtypes = [ctypes.POINTER(LinearAttentionStepArgs), _vp]
+    lib.swimba_linear_attention_step.restype = _ci
     lib.swimba_status_string.argtypes = [_ci]
     lib.swimba_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -637,4 +686,340 @@ class PreparedStep:
         rc = self._fn(self._ref, self.stream)
         if rc != OK:
             raise SwimbaError("swimba_step", rc)
+        return self.y
+
+
+def _new(t, name, shape, dtype, dev):
+    """The caller's output buffer, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, shape, dtype, dev)
+    return t
+
+
+def _workspace(given, need, dev):
+    """The caller's workspace, or one of `need` bytes for this call: (tensor or None,
+    address, bytes)."""
+    if given is None:
+        if need == 0:
+            return None, None, 0
+        given = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not given.is_cuda or given.device != dev or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def _placed(fn):
+    """Runs `fn` on its first tensor's device and on the stream asked for: with
+    stream=s everything `fn` allocates belongs to s (a caller that uses the
+    results on another stream waits for s there and records them, as for any
+    tensor made on a side stream)."""
+
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            return fn(first, *args, **kw)  # refused by its own checks
+        dev = first.device
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError("stream is on %s, the tensors on %s" % (stream.device, dev))
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+
+    return call
+
+
+# ---- tokens by expert ----
+
+
+@_placed
+def sort_tokens(idx, E, order=None, pos=None, offsets=None, workspace=None):
+    """Slots sorted by expert (include/swimba.h: swimba_sort_tokens).  idx
+    [..., k] int32, values outside [0, E) without an expert.  Returns (order
+    [T*k], pos like idx, offsets [E+1]), int32."""
+    _need(idx, "idx", None, torch.int32)
+    if idx.dim() < 1 or idx.shape[-1] < 1:
+        raise ValueError("idx must be [..., k]")
+    dev, k = idx.device, idx.shape[-1]
+    T = idx.numel() // k
+    order = _new(order, "order", (T * k,), torch.int32, dev)
+    pos = _new(pos, "pos", tuple(idx.shape), torch.int32, dev)
+    offsets = _new(offsets, "offsets", (E + 1,), torch.int32, dev)
+    lib = load()
+    ws, wp, wn = _workspace(workspace, lib.swimba_sort_tokens_workspace_size(T, E, k), dev)
+    rc = lib.swimba_sort_tokens(_ptr(idx), T, E, k, _ptr(order), _ptr(pos), _ptr(offsets), wp, wn,
+                                _stream(None))
+    _check("swimba_sort_tokens", rc)
+    return order, pos, offsets
+
+
+def _pos_shape(pos, dev=None):
+    _need(pos, "pos", None, torch.int32, dev)
+    if pos.dim() < 1 or pos.shape[-1] < 1:
+        raise ValueError("pos must be [..., k]")
+    k = pos.shape[-1]
+    return tuple(pos.shape[:-1]), pos.numel() // k, k
+
+
+@_placed
+def dispatch_tokens(x, pos, rows=None):
+    """rows[pos[t, j]] = x[t] (include/swimba.h: swimba_dispatch_tokens).  x
+    [..., D], pos [..., k] from sort_tokens; returns rows [T*k, D].  Rows that no
+    slot has are left as they were (unwritten memory where `rows` is not given)."""
+    _need(x, "x")
+    lead, T, k = _pos_shape(pos, x.device)
+    D = x.shape[-1] if x.dim() else 0
+    _need(x, "x", lead + (D,))
+    rows = _new(rows, "rows", (T * k, D), x.dtype, x.device)
+    rc = load().swimba_dispatch_tokens(_ptr(x), _dt(x), _ptr(pos), T, D, k, _ptr(rows),
+                                       _stream(None))
+    _check("swimba_dispatch_tokens", rc)
+    return rows
+
+
+@_placed
+def combine_tokens(rows, pos, gate=None, y=None, y_dtype=None):
+    """y[t] = sum_j gate[t, j] rows[pos[t, j]] (include/swimba.h:
+    swimba_combine_tokens).  rows [T*k, D], pos and gate [..., k]; gate None: ones.
+    Returns y [..., D]."""
+    _need(rows, "rows")
+    lead, T, k = _pos_shape(pos, rows.device)
+    D = rows.shape[-1] if rows.dim() else 0
+    _need(rows, "rows", (T * k, D))
+    if gate is not None:
+        _need(gate, "gate", lead + (k,), torch.float32, rows.device)
+    if y is None:
+        y = torch.empty(lead + (D,), dtype=y_dtype or rows.dtype, device=rows.device)
+    _need(y, "y", lead + (D,), None, rows.device)
+    rc = load().swimba_combine_tokens(_ptr(rows), _dt(rows), _ptr(pos), _ptr(gate), T, D, k,
+                                      _ptr(y), _dt(y), _stream(None))
+    _check("swimba_combine_tokens", rc)
+    return y
+
+
+@_placed
+def dispatch_tokens_backward(drows, pos, dx=None, grad_dtype=None):
+    """The gradient of dispatch_tokens: the sum of a token's rows' gradients
+    (combine_tokens without gates).  Returns dx [..., D], by default of drows'
+    dtype."""
+    return combine_tokens(drows, pos, None, y=dx, y_dtype=grad_dtype)
+
+
+@_placed
+def combine_tokens_backward(rows, pos, gate, dy, drows=None, dgate=None, grad_dtype=None):
+    """Gradients of combine_tokens (include/swimba.h:
+    swimba_combine_tokens_backward).  Returns (drows [T*k, D], by default of rows'
+    dtype, and dgate [..., k] f32).  Rows of drows that no slot has are left as
+    they were (unwritten memory where it is not given)."""
+    _need(rows, "rows")
+    dev = rows.device
+    lead, T, k = _pos_shape(pos, dev)
+    D = rows.shape[-1] if rows.dim() else 0
+    _need(rows, "rows", (T * k, D))
+    _need(gate, "gate", lead + (k,), torch.float32, dev)
+    _need(dy, "dy", lead + (D,), None, dev)
+    if drows is None:
+        drows = torch.empty((T * k, D), dtype=grad_dtype or rows.dtype, device=dev)
+    _need(drows, "drows", (T * k, D), None, dev)
+    dgate = _new(dgate, "dgate", lead + (k,), torch.float32, dev)
+    rc = load().swimba_combine_tokens_backward(
+        _ptr(rows), _dt(rows), _ptr(pos), _ptr(gate), _ptr(dy), _dt(dy), T, D, k, _ptr(drows),
+        _dt(drows), _ptr(dgate), _stream(None))
+    _check("swimba_combine_tokens_backward", rc)
+    return drows, dgate
+
+
+@_placed
+def route_backward(x, Wr, idx, gate, dgate, dx=None, dWr=None, grad_dtype=torch.float32,
+                   workspace=None):
+    """Gradients of route's gates (include/swimba.h: swimba_route_backward) for
+    dL/dgate = dgate [..., k].  Returns (dx [..., D] of grad_dtype, dWr [D, E] f32)."""
+    _need(x, "x")
+    dev, D = x.device, x.shape[-1]
+    E = Wr.shape[1] if Wr.dim() == 2 else -1
+    _need(Wr, "Wr", (D, E), torch.float32, dev)
+    lead = tuple(x.shape[:-1])
+    k = idx.shape[-1] if idx.dim() else 0
+    _need(idx, "idx", lead + (k,), torch.int32, dev)
+    _need(gate, "gate", lead + (k,), torch.float32, dev)
+    _need(dgate, "dgate", lead + (k,), torch.float32, dev)
+    T = x.numel() // D if D else 0
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=grad_dtype, device=dev)
+    _need(dx, "dx", tuple(x.shape), None, dev)
+    dWr = _new(dWr, "dWr", (D, E), torch.float32, dev)
+    lib = load()
+    need = lib.swimba_route_backward_workspace_size(T, D, E)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    rc = lib.swimba_route_backward(_ptr(x), _dt(x), _ptr(Wr), _ptr(idx), _ptr(gate), _ptr(dgate),
+                                   T, D, E, k, _ptr(dx), _dt(dx), _ptr(dWr), wp, wn,
+                                   _stream(None))
+    _check("swimba_route_backward", rc)
+    return dx, dWr
+
+
+# ---- linear attention with a decay per head ----
+
+DECAY_HEAD, DECAY_TOKEN = 0, 1  # log_decay [H], or one per token and head
+
+
+def _linear_attention_args(q, k, v, log_decay, h0, y, h_final, need_y=True):
+    _need(v, "v")
+    if v.dim() != 4:
+        raise ValueError("v must be [B, L, H, P]")
+    B, L, H, P = v.shape
+    dev = v.device
+    _need(q, "q", None, v.dtype, dev)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, L, G, N]")
+    G, N = q.shape[2:]
+    _need(q, "q", (B, L, G, N))
+    _need(k, "k", (B, L, G, N), v.dtype, dev)
+    a = LinearAttentionArgs()
+    a.decay_form = DECAY_HEAD if log_decay.dim() == 1 else DECAY_TOKEN
+    _need(log_decay, "log_decay", (H,) if a.decay_form == DECAY_HEAD else (B, L, H),
+          torch.float32, dev)
+    if h0 is not None:
+        _need(h0, "h0", (B, H, N, P), torch.float32, dev)
+    if need_y:
+        _need(y, "y", (B, L, H, P), None, dev)
+    if h_final is not None:
+        _need(h_final, "h_final", (B, H, N, P), torch.float32, dev)
+    a.B, a.L, a.H, a.G, a.N, a.P = B, L, H, G, N, P
+    a.in_dtype = _dt(v)
+    a.y_dtype = _dt(y) if y is not None else a.in_dtype
+    a.q, a.k, a.v, a.log_decay, a.h0 = _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0)
+    a.y, a.h_final = _ptr(y), _ptr(h_final)
+    return a
+
+
+@_placed
+def linear_attention(q, k, v, log_decay, h0=None, y=None, h_final=None, y_dtype=None,
+                     want_state=True, workspace=None):
+    """Linear attention with a decay per head (include/swimba.h:
+    swimba_linear_attention).  q, k [B,L,G,N], v [B,L,H,P] (f32 or bf16, H a multiple
+    of G); log_decay [H] or [B,L,H] f32; h0 [B,H,N,P] f32.  Returns (y [B,L,H,P],
+    h_final [B,H,N,P] f32 or None)."""
+    if y is None:
+        y = torch.empty(v.shape, dtype=y_dtype or v.dtype, device=v.device)
+    if h_final is None and want_state:
+        h_final = torch.empty((v.shape[0], v.shape[2], q.shape[-1], v.shape[3]),
+                              dtype=torch.float32, device=v.device)
+    a = _linear_attention_args(q, k, v, log_decay, h0, y, h_final)
+    lib, ref = load(), ctypes.byref(a)
+    need = lib.swimba_linear_attention_workspace_size(ref) if workspace is None else 0
+    ws, wp, wn = _workspace(workspace, need, v.device)
+    _check("swimba_linear_attention", lib.swimba_linear_attention(ref, wp, wn, _stream(None)))
+    return y, h_final
+
+
+def linear_attention_workspace_bytes(q, k, v, log_decay):
+    """Workspace bytes linear_attention needs for these shapes."""
+    a = _linear_attention_args(q, k, v, log_decay, None, None, None, need_y=False)
+    with torch.cuda.device(v.device):
+        return int(load().swimba_linear_attention_workspace_size(ctypes.byref(a)))
+
+
+@_placed
+def linear_attention_backward(q, k, v, log_decay, dy, h0=None, dh_final=None, want_dh0=True,
+                              grad_dtype=torch.float32, out=None, workspace=None):
+    """Gradients of linear_attention (include/swimba.h:
+    swimba_linear_attention_backward) for dL/dy = dy (of v's dtype) and
+    dL/dh_final.  Returns a dict: dq, dk [B,L,G,N], dv [B,L,H,P] of grad_dtype;
+    dlog_decay like log_decay and dh0 [B,H,N,P] (when want_dh0), f32."""
+    a = _linear_attention_args(q, k, v, log_decay, h0, None, None, need_y=False)
+    dev = v.device
+    _need(dy, "dy", tuple(v.shape), v.dtype, dev)
+    state = (a.B, a.H, a.N, a.P)
+    if dh_final is not None:
+        _need(dh_final, "dh_final", state, torch.float32, dev)
+    out = dict(out or {})
+    shapes = {"dq": q.shape, "dk": k.shape, "dv": v.shape, "dlog_decay": log_decay.shape}
+    if want_dh0:
+        shapes["dh0"] = state
+    res = {}
+    for name, shape in shapes.items():
+        dt = grad_dtype if name in ("dq", "dk", "dv") else torch.float32
+        res[name] = _new(out.get(name), name, tuple(shape), dt, dev)
+    g = LinearAttentionGradArgs()
+    g.fwd = a
+    g.dy, g.dh_final, g.grad_dtype = _ptr(dy), _ptr(dh_final), _dt(res["dq"])
+    for name in res:
+        setattr(g, name, _ptr(res[name]))
+    lib, ref = load(), ctypes.byref(g)
+    need = lib.swimba_linear_attention_backward_workspace_size(ref) if workspace is None else 0
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _check("swimba_linear_attention_backward",
+           lib.swimba_linear_attention_backward(ref, wp, wn, _stream(None)))
+    return res
+
+
+def _linear_attention_step_args(q, k, v, log_decay, state, state_out, y, y_dtype):
+    _need(v, "v")
+    if v.dim() != 3:
+        raise ValueError("v must be [B, H, P]")
+    B, H, P = v.shape
+    dev = v.device
+    _need(q, "q", None, v.dtype, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, G, N]")
+    G, N = q.shape[1:]
+    _need(q, "q", (B, G, N))
+    _need(k, "k", (B, G, N), v.dtype, dev)
+    form = DECAY_HEAD if log_decay.dim() == 1 else DECAY_TOKEN
+    _need(log_decay, "log_decay", (H,) if form == DECAY_HEAD else (B, H), torch.float32, dev)
+    _need(state, "state", (B, H, N, P), torch.float32, dev)
+    if state_out is not None:
+        _need(state_out, "state_out", (B, H, N, P), torch.float32, dev)
+    if y is None:
+        y = torch.empty((B, H, P), dtype=y_dtype or v.dtype, device=dev)
+    _need(y, "y", (B, H, P), None, dev)
+    a = LinearAttentionStepArgs()
+    a.B, a.H, a.G, a.N, a.P = B, H, G, N, P
+    a.in_dtype, a.y_dtype, a.decay_form = _dt(v), _dt(y), form
+    a.q, a.k, a.v, a.log_decay = _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay)
+    a.state, a.state_out, a.y = _ptr(state), _ptr(state_out), _ptr(y)
+    return a, y
+
+
+@_placed
+def linear_attention_step(q, k, v, log_decay, state, state_out=None, y=None, y_dtype=None):
+    """One decode step of linear_attention (include/swimba.h:
+    swimba_linear_attention_step).  q, k [B,G,N], v [B,H,P]; log_decay [H] or [B,H]
+    f32; state [B,H,N,P] f32, updated in place unless state_out is given.
+    Returns y [B,H,P]."""
+    a, y = _linear_attention_step_args(q, k, v, log_decay, state, state_out, y, y_dtype)
+    _check("swimba_linear_attention_step",
+           load().swimba_linear_attention_step(ctypes.byref(a), _stream(None)))
+    return y
+
+
+class PreparedLinearAttentionStep:
+    """swimba_linear_attention_step marshalled once for fixed tensors (see
+    PreparedStep)."""
+
+    def __init__(self, q, k, v, log_decay, state, state_out=None, y=None, y_dtype=None,
+                 stream=None):
+        self.args, self.y = _linear_attention_step_args(q, k, v, log_decay, state, state_out, y,
+                                                        y_dtype)
+        self._keep = (q, k, v, log_decay, state, state_out)
+        self._ref = ctypes.byref(self.args)
+        self._fn = load().swimba_linear_attention_step
+        self._dev = v.device.index
+        if stream is not None and stream.device != v.device:
+            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, v.device))
+        self.stream = (stream or torch.cuda.current_stream(v.device)).cuda_stream
+
+    def __call__(self):
+        if self._dev != torch.cuda.current_device():
+            with torch.cuda.device(self._dev):
+                rc = self._fn(self._ref, self.stream)
+        else:
+            rc = self._fn(self._ref, self.stream)
+        if rc != OK:
+            raise SwimbaError("swimba_linear_attention_step", rc)
         return self.y
