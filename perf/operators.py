@@ -328,7 +328,7 @@ def _run_own(st, op):
         return {"order": order, "pos": pos, "offsets": offsets, "rows": rows}
     out = {"y": swimba.combine_tokens(st["ys"], st["pos"], st["gate"])}
     if op == "tokens_train":
-        out["dys"], out["dgate"] = swimba.combine_tokens_backward(st["ys"], st["pos"], st["gate"], st["dy"], dys=st["rows"])
+        out["dys"], out["dgate"] = swimba.combine_tokens_backward(st["ys"], st["pos"], st["gate"], st["dy"], drows=st["rows"])
         out["dx"] = swimba.dispatch_tokens_backward(st["dxs"], st["pos"])
     return out
 
