@@ -31,6 +31,8 @@
 // bits and handed on as a high and a low fp32 part: differences of large sums
 // would lose the small decays after a document boundary.
 #pragma once
+#include <type_traits>
+
 #include "pack.hpp"
 #include "swimba_internal.hpp"
 
@@ -119,28 +121,119 @@ __device__ __forceinline__ bf8x column8(const bf16_t* tile, int stride, int row,
 template <typename TI, int KT, int W>
 struct AttnShape {
   static constexpr bool kF32 = sizeof(TI) == 4;
-  static constexpr int kRows = 32 * KT;                      // padded Kd
-  static constexpr int kRowStride = kRows + (kF32 ? 4 : 16);  // banks of rows apart
+  static constexpr int kRows = 32 * KT;  // padded Kd
+  // Row strides that keep the reads of 16 lanes on different banks: Q is read
+  // along its rows (16 rows at once, 4 banks apart), K mostly by the transposing
+  // read (4 rows of 32 bytes at once, 8 banks apart), like V.
+  static constexpr int kQStride = kRows + (kF32 ? 4 : 8);
+  static constexpr int kKStride = kRows + (kF32 ? 4 : 16);
   static constexpr int kValStride = 32 + (kF32 ? 4 : 16);
   static constexpr size_t kBytes =
-      (size_t)(2 * kChunk * kRowStride + W * kChunk * kValStride) * sizeof(TI) +
+      (size_t)(kChunk * (kQStride + kKStride) + W * kChunk * kValStride) * sizeof(TI) +
       (size_t)(kChunk * kScoreStride + W * 4 * kChunk) * sizeof(float);
 };
 
-// Rows of `base` (row r at token(r) * stride) into LDS, zero beyond `len` rows
-// and `cols` columns.  PAD columns are written.
-template <typename TI, int PAD, int THREADS, typename F>
-__device__ __forceinline__ void stage_rows(const TI* base, int64_t stride, int cols, int len,
-                                           TI* dst, int dst_stride, int tid, F token) {
-  constexpr int kPer = PAD / kPack;
+// The pack at element e of a tensor of `total` (at least 8) elements, with the
+// elements from n on zero.  Always one whole-pack load inside the tensor, so
+// that a run of them is issued without branches between.
+template <typename T>
+__device__ __forceinline__ Pack<T> pack_inside(const T* base, int64_t e, int64_t total, int n) {
+  const int64_t at = e + kPack <= total ? e : total - kPack;
+  Pack<T> r = load_pack(base + at, kPack);
+  const int shift = (int)(e - at);
+  if (__ballot(shift != 0 && n > 0)) {  // the tensor's last elements
+    Pack<T> m;
 #pragma unroll
-  for (int i = 0; i < kChunk * kPer / THREADS; ++i) {
-    const int u = i * THREADS + tid;
-    const int r = u / kPer, c = (u % kPer) * kPack;
-    Pack<TI> v = {};
-    if (r < len && c < cols) v = load_pack(base + token(r) * stride + c, cols - c);
-    *reinterpret_cast<Pack<TI>*>(dst + r * dst_stride + c) = v;
+    for (int i = 0; i < kPack; ++i) {
+      m.v[i] = r.v[i];
+#pragma unroll
+      for (int j = i + 1; j < kPack; ++j) m.v[i] = shift == j - i ? r.v[j] : m.v[i];
+    }
+    r = m;
   }
+#pragma unroll
+  for (int i = 0; i < kPack; ++i) r.v[i] = i < n ? r.v[i] : T(0);
+  return r;
+}
+
+// Rows of one operand of a chunk, ROUND packs per thread at a time on their way
+// to LDS: load() issues the loads of round i without branches between them,
+// store() writes them (zero beyond `len` rows and `cols` columns).
+template <typename T, int PAD, int THREADS>
+struct RowStage {
+  static constexpr int kPer = PAD / kPack, kN = kChunk * kPer / THREADS;
+  static constexpr int kRound = kN < 8 ? kN : 8, kRounds = kN / kRound;
+  const T* base;
+  int64_t first, total, stride;  // element of row 0, column 0; elements in all; between rows
+  int cols, len, tid;
+  bool whole, down;              // rows of whole packs; tokens in falling order
+  int64_t t0;                    // token of row 0
+  Pack<T> v[kRound];
+
+  __device__ __forceinline__ int64_t at(int r, int c) const {
+    return first + (down ? t0 - r : t0 + r) * stride + c;
+  }
+
+  __device__ __forceinline__ void load(int round) {
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < kRound; ++i) {
+        const int u = (round * kRound + i) * THREADS + tid, r = u / kPer, c = (u % kPer) * kPack;
+        const bool in = r < len && c < cols;
+        v[i] = load_pack(base + (in ? at(r, c) : 0), kPack);
+      }
+    } else if (total >= kPack) {
+#pragma unroll
+      for (int i = 0; i < kRound; ++i) {
+        const int u = (round * kRound + i) * THREADS + tid, r = u / kPer, c = (u % kPer) * kPack;
+        const bool in = r < len && c < cols;
+        v[i] = pack_inside(base, in ? at(r, c) : 0, total, in ? cols - c : 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRound; ++i) {
+        const int u = (round * kRound + i) * THREADS + tid, r = u / kPer, c = (u % kPer) * kPack;
+        v[i] = Pack<T>{};
+        if (r < len && c < cols) v[i] = load_pack(base + at(r, c), cols - c);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(int round, T* dst, int dst_stride) const {
+#pragma unroll
+    for (int i = 0; i < kRound; ++i) {
+      const int u = (round * kRound + i) * THREADS + tid, r = u / kPer, c = (u % kPer) * kPack;
+      const bool in = r < len && c < cols;
+      Pack<T> p;
+#pragma unroll
+      for (int k = 0; k < kPack; ++k) p.v[k] = in ? v[i].v[k] : T(0);
+      *reinterpret_cast<Pack<T>*>(dst + r * dst_stride + c) = p;
+    }
+  }
+};
+
+// Inclusive sum over the lanes, in 64 bits, on the DPP row shifts and row
+// broadcasts (no LDS round trips: the chunk's decays are waited for).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+  const uint64_t b = __double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return v + __longlong_as_double(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_prefix(double v) {
+  v = dpp_add<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t b = __double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __longlong_as_double(((uint64_t)hi << 32) | lo);
 }
 
 // Sums of 16 registers, each over the 32 lanes of its half: lane l of a half
@@ -167,29 +260,45 @@ __device__ __forceinline__ float half_sums(const float* v, int lane) {
   return s + xor_lane<1>(s, lane);
 }
 
-// S: bf16 terms of what is computed (2 or 3); STATE: only the segment's end
-// state from zero and its decay.
-template <typename TI, int KT, int W, int S, bool STATE>
+// Row of register i of a 32 x 32 accumulator tile.
+__device__ __forceinline__ int tile_row(int i, int half) {
+  return 8 * (i >> 2) + 4 * half + (i & 3);
+}
+
+enum AttnMode {
+  kAttnState = 0,  // only the segment's end state from zero, and its decay
+  kAttnPlain = 1,
+  kAttnSums = 2    // also the sums of z with the results (the gradient of the decays)
+};
+
+// S: bf16 terms of what is computed (2 or 3).
+template <typename TI, int KT, int W, int S, int MODE>
 __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams p) {
   using Sh = AttnShape<TI, KT, W>;
-  constexpr bool kF32 = Sh::kF32;
-  constexpr int RS = Sh::kRowStride, VS = Sh::kValStride;
+  constexpr bool kF32 = Sh::kF32, STATE = MODE == kAttnState, SUMS = MODE == kAttnSums;
+  constexpr int QS = Sh::kQStride, KS = Sh::kKStride, VS = Sh::kValStride;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
   TI* sQ = reinterpret_cast<TI*>(smem_raw);
-  TI* sK = sQ + kChunk * RS;
-  TI* sVall = sK + kChunk * RS;
+  TI* sK = sQ + kChunk * QS;
+  TI* sVall = sK + kChunk * KS;
   float* sS = reinterpret_cast<float*>(sVall + W * kChunk * VS);
   float* sGall = sS + kChunk * kScoreStride;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
   TI* sV = sVall + wave * kChunk * VS;
   float* gHi = sGall + wave * 4 * kChunk;  // high and low parts of G, e^G, w
   float *gLo = gHi + kChunk, *gE = gLo + kChunk, *gW = gE + kChunk;
 
-  // workgroup -> (sequence, group of heads sharing q and k, segment, W units)
+  // workgroup -> (sequence, group of heads sharing q and k, segment, W units),
+  // neighbours (which read the same q and k) on one XCD: workgroups go to the
+  // eight of them in turn
   const int groups = p.H / p.qshare, units = p.qshare * p.ctiles, nu = (units + W - 1) / W;
   int blk = blockIdx.x;
+  {
+    const int n = gridDim.x, x = blk & 7, per = n >> 3, more = n & 7;
+    blk = x * per + (x < more ? x : more) + (blk >> 3);
+  }
   const int u = (blk % nu) * W + wave;
   blk /= nu;
   const int segs = STATE ? p.nseg - 1 : p.nseg;  // the last one's end state is not carried
@@ -203,10 +312,10 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 
   const int hv = p.H / p.vshare;
   const int64_t qstride = (int64_t)groups * p.Kd, vstride = (int64_t)hv * p.Cd;
-  const TI* qb = static_cast<const TI*>(p.q) + (int64_t)b * p.L * qstride + (int64_t)grp * p.Kd;
-  const TI* kb = static_cast<const TI*>(p.k) + (int64_t)b * p.L * qstride + (int64_t)grp * p.Kd;
-  const TI* vb = static_cast<const TI*>(p.v) + (int64_t)b * p.L * vstride +
-                 (int64_t)(head / p.vshare) * p.Cd + c0;
+  const int64_t qtotal = (int64_t)p.B * p.L * qstride, vtotal = (int64_t)p.B * p.L * vstride;
+  const int64_t qfirst = (int64_t)b * p.L * qstride + (int64_t)grp * p.Kd;
+  const int64_t vfirst = (int64_t)b * p.L * vstride + (int64_t)(head / p.vshare) * p.Cd + c0;
+  const bool qwhole = p.Kd % kPack == 0, vwhole = p.Cd % kPack == 0;
   const float* gb = p.g + (p.token_decay ? (int64_t)b * p.L * p.H : 0) + head;
   const int64_t state = ((int64_t)b * p.H + head) * p.Kd * p.Cd;
   const int64_t sstate = (((int64_t)b * p.H + head) * p.nseg + seg) * p.Kd * p.Cd;
@@ -216,7 +325,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int n = 32 * kt + 8 * (i >> 2) + 4 * half + (i & 3);
+      const int n = 32 * kt + tile_row(i, half);
       float v = 0.f;
       if (!STATE && n < p.Kd && col < cols) {
         if (p.nseg > 1) v = p.seg_state[sstate + (int64_t)n * p.Cd + c0 + col];
@@ -232,36 +341,54 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     const int t0 = (p.reverse ? nc - 1 - j : j) * kChunk;
     const int len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
     auto token = [&](int r) { return (int64_t)(p.reverse ? t0 + len - 1 - r : t0 + r); };
-    __syncthreads();
-    if (!STATE) stage_rows<TI, 32 * KT, 64 * W>(qb, qstride, p.Kd, len, sQ, RS, tid, token);
-    stage_rows<TI, 32 * KT, 64 * W>(kb, qstride, p.Kd, len, sK, RS, tid, token);
-    stage_rows<TI, 32, 64>(vb, vstride, cols, len, sV, VS, lane, token);
     double end;
+    const int64_t first = p.reverse ? t0 + len - 1 : t0;
     {
+      float g = 0.f;
+      if (!p.token_decay) {
+        g = lane < len && !(p.reverse && token(lane) + 1 >= p.L) ? gb[0] : 0.f;
+      } else {
+        const int64_t t = token(lane) + (p.reverse ? 1 : 0);
+        const bool in = lane < len && t < p.L;
+        g = gb[in ? t * p.H : 0];
+        if (!in) g = 0.f;
+      }
+      using Rows = RowStage<TI, 32 * KT, 64 * W>;
+      Rows rk = {static_cast<const TI*>(p.k), qfirst, qtotal, qstride, p.Kd, len, tid, qwhole,
+                 (bool)p.reverse, first};
+      RowStage<TI, 32, 64> rv = {static_cast<const TI*>(p.v), vfirst, vtotal, vstride, cols, len,
+                                 lane, vwhole, (bool)p.reverse, first};
+      Rows rq = rk;
+      rq.base = static_cast<const TI*>(p.q);
+      rv.load(0);
+      rk.load(0);
+      // four waves or more have all of a chunk in flight at once, fewer go by rounds
+      if (!STATE && W == 4 && Rows::kRounds == 1) rq.load(0);
+
       // log2 decays, summed over the lanes
-      double g = 0.0;
-      if (lane < len) {
-        float v;
-        if (!p.token_decay) {
-          v = p.reverse && token(lane) + 1 >= p.L ? 0.f : gb[0];
-        } else {
-          const int64_t t = token(lane) + (p.reverse ? 1 : 0);
-          v = t < p.L ? gb[t * p.H] : 0.f;
-        }
-        const double d = (double)v * 1.4426950408889634;
-        g = d < (double)kLeastLog2 ? (double)kLeastLog2 : d;
-      }
-#pragma unroll
-      for (int m = 1; m < 64; m <<= 1) {
-        const double o = __shfl_up(g, m);
-        if (lane >= m) g += o;
-      }
-      end = __shfl(g, 63);
-      const float hi = (float)g;
+      const double d = (double)g * 1.4426950408889634;
+      const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
+      end = last_lane(sum);
+      const float hi = (float)sum;
+      __syncthreads();  // everyone is done with the last chunk
       gHi[lane] = hi;
-      gLo[lane] = (float)(g - (double)hi);
+      gLo[lane] = (float)(sum - (double)hi);
       gE[lane] = hw_exp2(hi);
-      gW[lane] = hw_exp2((float)(end - g));
+      gW[lane] = hw_exp2((float)(end - sum));
+      rv.store(0, sV, VS);
+      rk.store(0, sK, KS);
+#pragma unroll
+      for (int r = 1; r < Rows::kRounds; ++r) {
+        rk.load(r);
+        rk.store(r, sK, KS);
+      }
+      if (!STATE) {
+#pragma unroll
+        for (int r = 0; r < Rows::kRounds; ++r) {
+          if (!(W == 4 && Rows::kRounds == 1)) rq.load(r);
+          rq.store(r, sQ, QS);
+        }
+      }
     }
     __syncthreads();
 
@@ -272,8 +399,8 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
         f16x a;
 #pragma unroll
         for (int i = 0; i < 16; ++i) a[i] = 0.f;
-        const TI* qr = sQ + (32 * tt + col) * RS;
-        const TI* kr = sK + (32 * ss + col) * RS;
+        const TI* qr = sQ + (32 * tt + col) * QS;
+        const TI* kr = sK + (32 * ss + col) * KS;
         if constexpr (kF32) {
 #pragma unroll 4
           for (int n = 0; n < 32 * KT; n += 8) {
@@ -292,19 +419,23 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          sS[(32 * tt + 8 * (i >> 2) + 4 * half + (i & 3)) * kScoreStride + 32 * ss + col] = a[i];
+          sS[(32 * tt + tile_row(i, half)) * kScoreStride + 32 * ss + col] = a[i];
       }
       __syncthreads();
     }
 
     const float carry = hw_exp2((float)end);
-    f16x y[2];
+    f16x ys[2];  // from the state: e^{G_t} (Q h)_t
+    f16x yi[2];  // from the chunk (SUMS: apart, and without the diagonal)
+    f16x(&y)[2] = SUMS ? yi : ys;
     if (!STATE) {
-      // from the state: e^{G_t} (Q h)_t
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[tt][i] = 0.f;
+        for (int i = 0; i < 16; ++i) {
+          ys[tt][i] = 0.f;
+          yi[tt][i] = 0.f;
+        }
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
         if constexpr (kF32) {
@@ -312,12 +443,12 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           for (int a = 0; a < 4; ++a)
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-              const float4 x = *reinterpret_cast<const float4*>(sQ + (32 * tt + col) * RS + 32 * kt +
+              const float4 x = *reinterpret_cast<const float4*>(sQ + (32 * tt + col) * QS + 32 * kt +
                                                                 8 * a + 4 * half);
-              y[tt] = mma(x.x, h[kt][4 * a], y[tt]);
-              y[tt] = mma(x.y, h[kt][4 * a + 1], y[tt]);
-              y[tt] = mma(x.z, h[kt][4 * a + 2], y[tt]);
-              y[tt] = mma(x.w, h[kt][4 * a + 3], y[tt]);
+              ys[tt] = mma(x.x, h[kt][4 * a], ys[tt]);
+              ys[tt] = mma(x.y, h[kt][4 * a + 1], ys[tt]);
+              ys[tt] = mma(x.z, h[kt][4 * a + 2], ys[tt]);
+              ys[tt] = mma(x.w, h[kt][4 * a + 3], ys[tt]);
             }
         } else {
 #pragma unroll
@@ -329,54 +460,28 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
             split_terms<S>(x, t);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-              const TI* r = sQ + (32 * tt + col) * RS + 32 * kt + 16 * k2 + 4 * half;
+              const TI* r = sQ + (32 * tt + col) * QS + 32 * kt + 16 * k2 + 4 * half;
               struct { uint2 a, b; } qa;
               qa.a = *reinterpret_cast<const uint2*>(r);
               qa.b = *reinterpret_cast<const uint2*>(r + 8);
               const bf8x a = __builtin_bit_cast(bf8x, qa);
 #pragma unroll
-              for (int s = S - 1; s >= 0; --s) y[tt] = mma(a, t[s], y[tt]);
+              for (int s = S - 1; s >= 0; --s) ys[tt] = mma(a, t[s], ys[tt]);
             }
           }
         }
+        __builtin_amdgcn_sched_barrier(0);  // keep the operands of few steps in registers
       }
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
           const float4 e = *reinterpret_cast<const float4*>(gE + 32 * tt + 8 * a + 4 * half);
-          y[tt][4 * a] *= e.x;
-          y[tt][4 * a + 1] *= e.y;
-          y[tt][4 * a + 2] *= e.z;
-          y[tt][4 * a + 3] *= e.w;
+          ys[tt][4 * a] *= e.x;
+          ys[tt][4 * a + 1] *= e.y;
+          ys[tt][4 * a + 2] *= e.z;
+          ys[tt][4 * a + 3] *= e.w;
         }
-    }
-    f16x zv[2];
-    float zstate[2] = {0.f, 0.f};
-    if (!STATE && S == 3 && p.z != nullptr) {
-      const TI* zb = static_cast<const TI*>(p.z) + (int64_t)b * p.L * vstride +
-                     (int64_t)(head / p.vshare) * p.Cd + c0;
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
-        float m[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
-          zv[tt][i] = t < len && col < cols ? to_f32(zb[token(t) * vstride + col]) : 0.f;
-          m[i] = zv[tt][i] * y[tt][i];
-          y[tt][i] = y[tt][i];
-        }
-        zstate[tt] = half_sums(m, lane);
-      }
-    }
-    f16x ystate[2];
-    if (!STATE && S == 3 && p.z != nullptr) {
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
-        ystate[tt] = y[tt];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[tt][i] = 0.f;
-      }
     }
 
 #pragma unroll
@@ -386,7 +491,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 
     // 8 (fp32) or 16 (bf16) tokens s at a time: y += M V, h += K^T (w V)
     constexpr int kStep = kF32 ? 8 : 16;
-#pragma unroll
+#pragma unroll 1
     for (int s0 = 0; s0 < kChunk; s0 += kStep) {
       constexpr int kV = kF32 ? 4 : 8;  // tokens per lane and step
       const int sl = s0 + kV * half;
@@ -412,7 +517,8 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           *reinterpret_cast<float4*>(ls + i) = *reinterpret_cast<const float4*>(gLo + sl + i);
         }
 #pragma unroll
-        for (int tt = s0 / 32; tt < 2; ++tt) {
+        for (int tt = 0; tt < 2; ++tt) {
+          if (32 * tt + 31 < s0) continue;
           const int t = 32 * tt + col;
           const float ht = gHi[t], lt = gLo[t];
           float m[kV];
@@ -420,10 +526,11 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           for (int i = 0; i < kV; i += 4)
             *reinterpret_cast<float4*>(m + i) =
                 *reinterpret_cast<const float4*>(sS + t * kScoreStride + sl + i);
+          const int before = SUMS ? t : t + 1;  // tokens that are read
 #pragma unroll
           for (int i = 0; i < kV; ++i) {
             const float d = hw_exp2((ht - hs[i]) + (lt - ls[i]));
-            m[i] = (tt > s0 / 32 || sl + i <= t) ? m[i] * d : 0.f;
+            m[i] = sl + i < before ? m[i] * d : 0.f;
           }
           if constexpr (kF32) {
 #pragma unroll
@@ -446,13 +553,13 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-          for (int i = 0; i < kV; ++i) h[kt] = mma(sK[(sl + i) * RS + 32 * kt + col], vf[i], h[kt]);
+          for (int i = 0; i < kV; ++i) h[kt] = mma(sK[(sl + i) * KS + 32 * kt + col], vf[i], h[kt]);
       } else {
         bf8x wt[3];
         split_terms<3>(vf, wt);
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-          const bf8x a = column8(sK, RS, s0, 32 * kt, lane);
+          const bf8x a = column8(sK, KS, s0, 32 * kt, lane);
 #pragma unroll
           for (int s = 2; s >= 0; --s) h[kt] = mma(a, wt[s], h[kt]);
         }
@@ -463,36 +570,78 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       whole += end;
       continue;
     }
-    if (S == 3 && p.z != nullptr) {
+    RowStage<TI, 32, 64> rz = {static_cast<const TI*>(p.z), vfirst, vtotal, vstride, cols, len,
+                               lane, vwhole, (bool)p.reverse, first};
+    if (SUMS) rz.load(0);
+    // The wave's V slab is free row by row now: z comes in through it and the
+    // results leave through it, 32 rows at a time, as whole packs.
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
-        float m[16];
+    for (int tt = 0; tt < 2; ++tt) {
+      f16x o = y[tt];
+      if constexpr (SUMS) {
+        float m[16], vd[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m[i] = zv[tt][i] * y[tt][i];
+        for (int i = 0; i < 16; ++i) {
+          const int t = 32 * tt + tile_row(i, half);
+          vd[i] = sS[t * kScoreStride + t] * to_f32(sV[t * VS + col]);  // the diagonal
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int k = 0; k < rz.kN / 2; ++k) {
+          const int i = rz.kN / 2 * tt + k, un = i * 64 + lane;
+          const int r = un / rz.kPer, c = (un % rz.kPer) * kPack;
+          const bool in = r < len && c < cols;
+          Pack<TI> zp;
+#pragma unroll
+          for (int e = 0; e < kPack; ++e) zp.v[e] = in ? rz.v[i].v[e] : TI(0);
+          *reinterpret_cast<Pack<TI>*>(sV + r * VS + c) = zp;
+        }
+        __builtin_amdgcn_wave_barrier();
+        float z[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          z[i] = to_f32(sV[(32 * tt + tile_row(i, half)) * VS + col]);
+          m[i] = z[i] * o[i];
+        }
         const float zin = half_sums(m, lane);
-        const int i = col >> 1, t = 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m[i] = z[i] * ys[tt][i];
+        const float zst = half_sums(m, lane);
+        const int t = 32 * tt + tile_row(col >> 1, half);
         if (active && (lane & 1) == 0 && t < len) {
           float* zs = p.zsum + (((int64_t)b * p.H + head) * p.ctiles + u % p.ctiles) * 2 * p.L;
           zs[token(t)] = zin;
-          zs[p.L + token(t)] = zstate[tt];
+          zs[p.L + token(t)] = zst;
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) y[tt][k] += ystate[tt][k];
+        for (int i = 0; i < 16; ++i) o[i] = (o[i] + vd[i]) + ys[tt][i];
+        __builtin_amdgcn_wave_barrier();
       }
-    }
-    const int64_t ystride = (int64_t)p.H * p.Cd;
-    const int64_t yb = (int64_t)b * p.L * ystride + (int64_t)head * p.Cd + c0 + col;
-    if (col < cols) {
+      const int64_t ystride = (int64_t)p.H * p.Cd;
+      const int64_t yfirst = (int64_t)b * p.L * ystride + (int64_t)head * p.Cd + c0;
+      auto leave = [&](auto* out) {
+        using TO = std::remove_pointer_t<decltype(out)>;
+        constexpr int OS = 32 + 16 / (int)sizeof(TO);
+        // rows at a time that fit the slab's 32 rows
+        constexpr int kOut = sizeof(TO) > sizeof(TI) ? 16 : 32;
+        TO* so = reinterpret_cast<TO*>(sV + 32 * tt * VS);
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
+        for (int r0 = 0; r0 < 32; r0 += kOut) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
-          if (t >= len) continue;
-          const int64_t at = yb + token(t) * ystride;
-          if (p.y_bf16) static_cast<bf16_t*>(p.y)[at] = from_f32<bf16_t>(y[tt][i]);
-          else static_cast<float*>(p.y)[at] = y[tt][i];
+          for (int i = r0 / 2; i < (r0 + kOut) / 2; ++i)
+            so[(tile_row(i, half) - r0) * OS + col] = from_f32<TO>(o[i]);
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int k = 0; k < kOut / 16; ++k) {
+            const int un = k * 64 + lane, r = un >> 2, c = (un & 3) * kPack, t = 32 * tt + r0 + r;
+            const Pack<TO> v = *reinterpret_cast<const Pack<TO>*>(so + r * OS + c);
+            if (t < len && c < cols) store_pack(out + yfirst + token(t) * ystride + c, v, cols - c);
+          }
+          __builtin_amdgcn_wave_barrier();
         }
+      };
+      if (p.y_bf16) leave(static_cast<bf16_t*>(p.y));
+      else leave(static_cast<float*>(p.y));
     }
   }
 
@@ -503,43 +652,46 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int n = 32 * kt + 8 * (i >> 2) + 4 * half + (i & 3);
+        const int n = 32 * kt + tile_row(i, half);
         if (n < p.Kd && col < cols) p.seg_state[sstate + (int64_t)n * p.Cd + c0 + col] = h[kt][i];
       }
   } else if (p.s_final != nullptr && seg == p.nseg - 1) {
     // walking backwards the first token's own decay is still to come
     float f = 1.f;
-    if (p.reverse) f = hw_exp2(gb[0] * kLog2e < kLeastLog2 ? kLeastLog2 : gb[0] * kLog2e);
+    if (p.reverse) {
+      const float g = gb[0] * kLog2e;
+      f = hw_exp2(g < kLeastLog2 ? kLeastLog2 : g);
+    }
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int n = 32 * kt + 8 * (i >> 2) + 4 * half + (i & 3);
-        if (n < p.Kd && col < cols)
-          p.s_final[state + n * p.sk + (c0 + col) * p.sc] = h[kt][i] * f;
+        const int n = 32 * kt + tile_row(i, half);
+        if (n < p.Kd && col < cols) p.s_final[state + n * p.sk + (c0 + col) * p.sc] = h[kt][i] * f;
       }
   }
 }
 
 // Host side: launches one walk (or its state pass).
-template <typename TI, int KT, int W, int S, bool STATE>
+template <typename TI, int KT, int W, int S, int MODE>
 int attn_launch(const AttnParams& p, hipStream_t s) {
   const int groups = p.H / p.qshare, units = p.qshare * p.ctiles;
-  const int64_t grid = (int64_t)p.B * groups * (STATE ? p.nseg - 1 : p.nseg) * ((units + W - 1) / W);
+  const int64_t grid = (int64_t)p.B * groups * (MODE == kAttnState ? p.nseg - 1 : p.nseg) * ((units + W - 1) / W);
   if (grid > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
   constexpr size_t lds = AttnShape<TI, KT, W>::kBytes;
-  allow_dynamic_lds(attn_kernel<TI, KT, W, S, STATE>, lds);
-  hipLaunchKernelGGL((attn_kernel<TI, KT, W, S, STATE>), dim3((unsigned)grid), dim3(64 * W), lds, s,
+  allow_dynamic_lds(attn_kernel<TI, KT, W, S, MODE>, lds);
+  hipLaunchKernelGGL((attn_kernel<TI, KT, W, S, MODE>), dim3((unsigned)grid), dim3(64 * W), lds, s,
                      p);
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
 template <typename TI, int KT, int W>
 int attn_launch_kind(const AttnParams& p, bool state, bool exact, hipStream_t s) {
-  if (state) return attn_launch<TI, KT, W, 3, true>(p, s);
+  if (state) return attn_launch<TI, KT, W, 3, kAttnState>(p, s);
+  if (p.z != nullptr) return attn_launch<TI, KT, W, 3, kAttnSums>(p, s);
   if constexpr (sizeof(TI) == 2)
-    if (!exact) return attn_launch<TI, KT, W, 2, false>(p, s);
-  return attn_launch<TI, KT, W, 3, false>(p, s);
+    if (!exact) return attn_launch<TI, KT, W, 2, kAttnPlain>(p, s);
+  return attn_launch<TI, KT, W, 3, kAttnPlain>(p, s);
 }
 
 template <typename TI, int KT>
