@@ -293,8 +293,7 @@ WalkPlan plan_walk(bool f32, int B, int L, int H, int share, int Kd, int Cd, int
   WalkPlan w;
   const int ctiles = (Cd + 31) / 32;
   const int64_t units = (int64_t)share * ctiles;
-  w.waves = units >= 3 ? 4 : (int)units;
-  if (f32 && Kd > 128) w.waves = 1;
+  w.waves = attn_waves(f32, Kd, Cd, units);
   const int64_t nc = (L + kChunk - 1) / kChunk;
   const int64_t base = (int64_t)B * (H / share) * ((units + w.waves - 1) / w.waves);
   // eight waves per CU from the independent walks, or from segments of them
@@ -312,18 +311,18 @@ WalkPlan plan_walk(bool f32, int B, int L, int H, int share, int Kd, int Cd, int
   return w;
 }
 
-int dispatch(const AttnParams& p, bool f32, int waves, bool state, bool exact, hipStream_t s) {
+int dispatch(const AttnParams& p, bool f32, bool state, bool exact, hipStream_t s) {
   const int k = p.Kd;
   if (f32) {
-    if (k <= 32) return attn_f32_32(p, waves, state, exact, s);
-    if (k <= 64) return attn_f32_64(p, waves, state, exact, s);
-    if (k <= 128) return attn_f32_128(p, waves, state, exact, s);
-    return attn_f32_256(p, waves, state, exact, s);
+    if (k <= 32) return attn_f32_32(p, state, exact, s);
+    if (k <= 64) return attn_f32_64(p, state, exact, s);
+    if (k <= 128) return attn_f32_128(p, state, exact, s);
+    return attn_f32_256(p, state, exact, s);
   }
-  if (k <= 32) return attn_bf16_32(p, waves, state, exact, s);
-  if (k <= 64) return attn_bf16_64(p, waves, state, exact, s);
-  if (k <= 128) return attn_bf16_128(p, waves, state, exact, s);
-  return attn_bf16_256(p, waves, state, exact, s);
+  if (k <= 32) return attn_bf16_32(p, state, exact, s);
+  if (k <= 64) return attn_bf16_64(p, state, exact, s);
+  if (k <= 128) return attn_bf16_128(p, state, exact, s);
+  return attn_bf16_256(p, state, exact, s);
 }
 
 // One walk; ws holds the plan's segment states.
@@ -334,14 +333,14 @@ int walk(AttnParams p, const WalkPlan& w, bool f32, bool exact, unsigned char* w
   if (w.nseg > 1) {
     p.seg_state = reinterpret_cast<float*>(ws);
     p.seg_decay = reinterpret_cast<float*>(ws + w.state_bytes);
-    const int rc = dispatch(p, f32, w.waves, true, true, s);
+    const int rc = dispatch(p, f32, true, true, s);
     if (rc != SWIMBA_OK) return rc;
     const int64_t n = (int64_t)p.Kd * p.Cd;
     hipLaunchKernelGGL(attn_carry_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)(p.B * p.H)),
                        dim3(256), 0, s, p);
     if (checked() != SWIMBA_OK) return SWIMBA_EHIP;
   }
-  return dispatch(p, f32, w.waves, false, exact, s);
+  return dispatch(p, f32, false, exact, s);
 }
 
 AttnParams base_params(const swimba_linear_attention_args* a) {

@@ -71,7 +71,9 @@ struct Bits8 {
 
 // Two fp32 values as bf16 in one register, the first in the low half.
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  return (uint32_t)from_f32<bf16_t>(a) | ((uint32_t)from_f32<bf16_t>(b) << 16);
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
 }
 __device__ __forceinline__ float low_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -130,84 +132,116 @@ struct AttnShape {
   static constexpr int kValStride = 32 + (kF32 ? 4 : 16);
   static constexpr size_t kBytes =
       (size_t)(kChunk * (kQStride + kKStride) + W * kChunk * kValStride) * sizeof(TI) +
-      (size_t)(kChunk * kScoreStride + W * 4 * kChunk) * sizeof(float);
+      (size_t)(kChunk * kScoreStride + kChunk + W * 4 * kChunk) * sizeof(float);
 };
 
-// The pack at element e of a tensor of `total` (at least 8) elements, with the
-// elements from n on zero.  Always one whole-pack load inside the tensor, so
-// that a run of them is issued without branches between.
-template <typename T>
-__device__ __forceinline__ Pack<T> pack_inside(const T* base, int64_t e, int64_t total, int n) {
-  const int64_t at = e + kPack <= total ? e : total - kPack;
-  Pack<T> r = load_pack(base + at, kPack);
-  const int shift = (int)(e - at);
-  if (__ballot(shift != 0 && n > 0)) {  // the tensor's last elements
-    Pack<T> m;
-#pragma unroll
-    for (int i = 0; i < kPack; ++i) {
-      m.v[i] = r.v[i];
-#pragma unroll
-      for (int j = i + 1; j < kPack; ++j) m.v[i] = shift == j - i ? r.v[j] : m.v[i];
-    }
-    r = m;
-  }
-#pragma unroll
-  for (int i = 0; i < kPack; ++i) r.v[i] = i < n ? r.v[i] : T(0);
-  return r;
-}
+typedef uint32_t u4x __attribute__((ext_vector_type(4)));
 
-// Rows of one operand of a chunk, ROUND packs per thread at a time on their way
-// to LDS: load() issues the loads of round i without branches between them,
-// store() writes them (zero beyond `len` rows and `cols` columns).
-template <typename T, int PAD, int THREADS>
+// Rows of one operand of a chunk on their way to LDS, up to eight packs per
+// thread at a time: load() issues the loads of a round, store() writes them,
+// zero beyond `len` rows and `cols` columns.  The packs stay whole registers and
+// no load waits for another: without branches between them where rows are whole
+// packs; LOOSE rows take one load per pack inside the tensor, moved back from
+// its end where it would pass it.  Memory is walked in rising order; a chunk
+// walked backwards is turned round in LDS.
+template <typename T, int PAD, int THREADS, bool LOOSE>
 struct RowStage {
   static constexpr int kPer = PAD / kPack, kN = kChunk * kPer / THREADS;
   static constexpr int kRound = kN < 8 ? kN : 8, kRounds = kN / kRound;
+  static constexpr int kStep = THREADS / kPer;      // rows between a thread's packs
+  static constexpr int kQuads = sizeof(T) / 2;      // 16-byte registers per pack
+  static constexpr int kWords = 4 * kQuads;
+  struct __attribute__((packed, aligned(sizeof(T)))) Loose { u4x q[kQuads]; };
   const T* base;
-  int64_t first, total, stride;  // element of row 0, column 0; elements in all; between rows
+  int64_t total;    // elements of the tensor
+  int64_t first;    // element of the chunk's lowest token, column 0
+  int64_t stride;   // between tokens
   int cols, len, tid;
-  bool whole, down;              // rows of whole packs; tokens in falling order
-  int64_t t0;                    // token of row 0
-  Pack<T> v[kRound];
+  u4x v[kRound][kQuads];
 
-  __device__ __forceinline__ int64_t at(int r, int c) const {
-    return first + (down ? t0 - r : t0 + r) * stride + c;
+  __device__ __forceinline__ int row(int i) const { return i * kStep + tid / kPer; }
+  __device__ __forceinline__ int column() const { return tid % kPer * kPack; }
+  __device__ __forceinline__ bool inside(int r) const { return r < len && column() < cols; }
+
+  __device__ __forceinline__ void fetch(int i, const T* at) {
+    const Loose l = *reinterpret_cast<const Loose*>(at);
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) v[i][q] = l.q[q];
   }
 
   __device__ __forceinline__ void load(int round) {
-    if (whole) {
+    const int c = column();
+    if constexpr (!LOOSE) {
+      const T* chunk = base + first;
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
-        const int u = (round * kRound + i) * THREADS + tid, r = u / kPer, c = (u % kPer) * kPack;
-        const bool in = r < len && c < cols;
-        v[i] = load_pack(base + (in ? at(r, c) : 0), kPack);
+        const int r = row(round * kRound + i);
+        fetch(i, chunk + (inside(r) ? r * stride + c : 0));
       }
     } else if (total >= kPack) {
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
-        const int u = (round * kRound + i) * THREADS + tid, r = u / kPer, c = (u % kPer) * kPack;
-        const bool in = r < len && c < cols;
-        v[i] = pack_inside(base, in ? at(r, c) : 0, total, in ? cols - c : 0);
+        const int r = row(round * kRound + i);
+        const int64_t e = inside(r) ? first + r * stride + c : 0;
+        fetch(i, base + (e + kPack <= total ? e : total - kPack));
       }
-    } else {
+    } else {  // a tensor of less than a pack
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
-        const int u = (round * kRound + i) * THREADS + tid, r = u / kPer, c = (u % kPer) * kPack;
-        v[i] = Pack<T>{};
-        if (r < len && c < cols) v[i] = load_pack(base + at(r, c), cols - c);
+        const int r = row(round * kRound + i);
+        const Pack<T> p = inside(r) ? load_pack(base + first + r * stride + c,
+                                                cols - c < 7 ? cols - c : 7)
+                                    : Pack<T>{};
+        __builtin_memcpy(v[i], &p, sizeof(p));
       }
     }
   }
 
-  __device__ __forceinline__ void store(int round, T* dst, int dst_stride) const {
+  // The pack i of this round and the chunk row it is (walk order).
+  __device__ __forceinline__ void pack(int round, int i, bool down, int* at, u4x* out) const {
+    const int r = row(round * kRound + i), c = column();
+    *at = down && r < len ? len - 1 - r : r;
+    const bool in = inside(r);
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) out[q] = in ? v[i][q] : u4x{0, 0, 0, 0};
+    if constexpr (LOOSE) {
+      uint32_t w[kWords];
+      __builtin_memcpy(w, out, sizeof(w));
+      const int64_t e = first + r * stride + c;
+      const int shift = in && total >= kPack && e + kPack > total ? (int)(e + kPack - total) : 0;
+      if (__ballot(shift != 0)) {  // the tensor's last elements
+        T m[kPack], o[kPack];
+        __builtin_memcpy(m, w, sizeof(m));
+#pragma unroll
+        for (int k = 0; k < kPack; ++k) {
+          o[k] = m[k];
+#pragma unroll
+          for (int l = k + 1; l < kPack; ++l) o[k] = shift == l - k ? m[l] : o[k];
+        }
+        __builtin_memcpy(w, o, sizeof(o));
+      }
+      const int n = cols - c;  // columns of this pack
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+          w[k] = n >= 2 * k + 2 ? w[k] : (n == 2 * k + 1 ? w[k] & 0xffffu : 0u);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[k] = n > k ? w[k] : 0u;
+      }
+      __builtin_memcpy(out, w, sizeof(w));
+    }
+  }
+
+  __device__ __forceinline__ void store(int round, T* dst, int dst_stride, bool down) const {
 #pragma unroll
     for (int i = 0; i < kRound; ++i) {
-      const int u = (round * kRound + i) * THREADS + tid, r = u / kPer, c = (u % kPer) * kPack;
-      const bool in = r < len && c < cols;
-      Pack<T> p;
+      int r;
+      u4x p[kQuads];
+      pack(round, i, down, &r, p);
+      u4x* d = reinterpret_cast<u4x*>(dst + r * dst_stride + column());
 #pragma unroll
-      for (int k = 0; k < kPack; ++k) p.v[k] = in ? v[i].v[k] : T(0);
-      *reinterpret_cast<Pack<T>*>(dst + r * dst_stride + c) = p;
+      for (int q = 0; q < kQuads; ++q) d[q] = p[q];
     }
   }
 };
@@ -271,8 +305,20 @@ enum AttnMode {
   kAttnSums = 2    // also the sums of z with the results (the gradient of the decays)
 };
 
+// 2^x of a sum in 64 bits, also where it is large: the part of x that fp32
+// leaves out multiplies the result.
+__device__ __forceinline__ float exp2_sum(double x) {
+  const float hi = (float)x;
+  return hw_exp2(hi) * fmaf((float)(x - (double)hi), kLn2, 1.f);
+}
+
+// Sums of log2 decays inside a chunk that keep e^{G_t} and e^{-G_s} apart, and
+// the scale a state may carry on top.
+constexpr float kLeastSum = -40.f, kMostSum = 16.f;
+constexpr float kLeastScale = 0x1p-24f, kMostScale = 0x1p24f;
+
 // S: bf16 terms of what is computed (2 or 3).
-template <typename TI, int KT, int W, int S, int MODE>
+template <typename TI, int KT, int W, int S, int MODE, bool LOOSE>
 __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams p) {
   using Sh = AttnShape<TI, KT, W>;
   constexpr bool kF32 = Sh::kF32, STATE = MODE == kAttnState, SUMS = MODE == kAttnSums;
@@ -282,13 +328,15 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   TI* sK = sQ + kChunk * QS;
   TI* sVall = sK + kChunk * KS;
   float* sS = reinterpret_cast<float*>(sVall + W * kChunk * VS);
-  float* sGall = sS + kChunk * kScoreStride;
+  float* sD = sS + kChunk * kScoreStride;  // the scores' diagonal (SUMS)
+  float* sGall = sD + kChunk;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
   TI* sV = sVall + wave * kChunk * VS;
-  float* gHi = sGall + wave * 4 * kChunk;  // high and low parts of G, e^G, w
-  float *gLo = gHi + kChunk, *gE = gLo + kChunk, *gW = gE + kChunk;
+  float* gHi = sGall + wave * 4 * kChunk;  // high and low parts of G
+  float *gLo = gHi + kChunk;
+  float *gRead = gLo + kChunk, *gWrite = gRead + kChunk;  // factors of y_t and of v_s
 
   // workgroup -> (sequence, group of heads sharing q and k, segment, W units),
   // neighbours (which read the same q and k) on one XCD: workgroups go to the
@@ -315,85 +363,140 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   const int64_t qtotal = (int64_t)p.B * p.L * qstride, vtotal = (int64_t)p.B * p.L * vstride;
   const int64_t qfirst = (int64_t)b * p.L * qstride + (int64_t)grp * p.Kd;
   const int64_t vfirst = (int64_t)b * p.L * vstride + (int64_t)(head / p.vshare) * p.Cd + c0;
-  const bool qwhole = p.Kd % kPack == 0, vwhole = p.Cd % kPack == 0;
   const float* gb = p.g + (p.token_decay ? (int64_t)b * p.L * p.H : 0) + head;
   const int64_t state = ((int64_t)b * p.H + head) * p.Kd * p.Cd;
   const int64_t sstate = (((int64_t)b * p.H + head) * p.nseg + seg) * p.Kd * p.Cd;
+  const bool down = p.reverse;
 
+  // The state is c * h: a chunk's decay multiplies c, not every entry.
   f16x h[KT];
+  float c = 1.f;
+  const bool walked = p.nseg > 1;  // first states of segments are in the workspace
+  const float* from = STATE ? nullptr : walked ? p.seg_state + sstate : p.s0;
+  if (from != nullptr) {
+    if (!walked) from += state;
+    const int64_t fk = walked ? p.Cd : p.sk, fc = walked ? 1 : p.sc;
+    const int64_t at = (c0 + col) * fc;
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int n = 32 * kt + tile_row(i, half);
-      float v = 0.f;
-      if (!STATE && n < p.Kd && col < cols) {
-        if (p.nseg > 1) v = p.seg_state[sstate + (int64_t)n * p.Cd + c0 + col];
-        else if (p.s0 != nullptr) v = p.s0[state + n * p.sk + (c0 + col) * p.sc];
+      for (int i = 0; i < 16; ++i) {
+        const int n = 32 * kt + tile_row(i, half);
+        h[kt][i] = from[n < p.Kd && col < cols ? n * fk + at : 0];
       }
-      h[kt][i] = v;
-    }
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (32 * kt + tile_row(i, half) >= p.Kd || col >= cols) h[kt][i] = 0.f;
+  } else {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) h[kt][i] = 0.f;
+  }
   double whole = 0.0;  // log2 decay of the segment so far (state pass)
 
+  using Rows = RowStage<TI, 32 * KT, 64 * W, LOOSE>;
+  using Vals = RowStage<TI, 32, 64, LOOSE>;
+  // the next chunk's rows travel while this one is worked on, where registers hold them
+  constexpr bool kAhead = false && !kF32 && W == 4 && KT <= 4 && !SUMS;
+  Rows rk, rq;
+  Vals rv;
+  float g = 0.f;
   const int nc = (p.L + kChunk - 1) / kChunk;
   const int j1 = (seg + 1) * p.seg_chunks < nc ? (seg + 1) * p.seg_chunks : nc;
-  for (int j = seg * p.seg_chunks; j < j1; ++j) {
-    const int t0 = (p.reverse ? nc - 1 - j : j) * kChunk;
-    const int len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
-    auto token = [&](int r) { return (int64_t)(p.reverse ? t0 + len - 1 - r : t0 + r); };
-    double end;
-    const int64_t first = p.reverse ? t0 + len - 1 : t0;
-    {
-      float g = 0.f;
-      if (!p.token_decay) {
-        g = lane < len && !(p.reverse && token(lane) + 1 >= p.L) ? gb[0] : 0.f;
-      } else {
-        const int64_t t = token(lane) + (p.reverse ? 1 : 0);
-        const bool in = lane < len && t < p.L;
-        g = gb[in ? t * p.H : 0];
-        if (!in) g = 0.f;
-      }
-      using Rows = RowStage<TI, 32 * KT, 64 * W>;
-      Rows rk = {static_cast<const TI*>(p.k), qfirst, qtotal, qstride, p.Kd, len, tid, qwhole,
-                 (bool)p.reverse, first};
-      RowStage<TI, 32, 64> rv = {static_cast<const TI*>(p.v), vfirst, vtotal, vstride, cols, len,
-                                 lane, vwhole, (bool)p.reverse, first};
-      Rows rq = rk;
+  auto chunk_first = [&](int j) { return (down ? nc - 1 - j : j) * kChunk; };
+  auto fetch = [&](int j) {
+    const int t0 = chunk_first(j), len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
+    rk.base = static_cast<const TI*>(p.k);
+    rk.total = qtotal;
+    rk.first = qfirst + t0 * qstride;
+    rk.stride = qstride;
+    rk.cols = p.Kd;
+    rk.len = len;
+    rk.tid = tid;
+    rv.base = static_cast<const TI*>(p.v);
+    rv.total = vtotal;
+    rv.first = vfirst + t0 * vstride;
+    rv.stride = vstride;
+    rv.cols = cols;
+    rv.len = len;
+    rv.tid = lane;
+    if (!p.token_decay) {
+      g = lane < len && !(down && t0 + len - 1 - lane + 1 >= p.L) ? gb[0] : 0.f;
+    } else {
+      const int t = down ? t0 + len - lane : t0 + lane;
+      const bool in = lane < len && t < p.L;
+      g = gb[in ? (int64_t)t * p.H : 0];
+      if (!in) g = 0.f;
+    }
+    rv.load(0);
+    rk.load(0);
+    if (!STATE) {
       rq.base = static_cast<const TI*>(p.q);
-      rv.load(0);
-      rk.load(0);
-      // four waves or more have all of a chunk in flight at once, fewer go by rounds
-      if (!STATE && W == 4 && Rows::kRounds == 1) rq.load(0);
+      rq.total = rk.total;
+      rq.first = rk.first;
+      rq.stride = rk.stride;
+      rq.cols = rk.cols;
+      rq.len = rk.len;
+      rq.tid = rk.tid;
+      if (Rows::kRounds == 1) rq.load(0);
+    }
+  };
+  if (kAhead) fetch(seg * p.seg_chunks);
 
-      // log2 decays, summed over the lanes
-      const double d = (double)g * 1.4426950408889634;
-      const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
-      end = last_lane(sum);
-      const float hi = (float)sum;
-      __syncthreads();  // everyone is done with the last chunk
-      gHi[lane] = hi;
-      gLo[lane] = (float)(sum - (double)hi);
-      gE[lane] = hw_exp2(hi);
-      gW[lane] = hw_exp2((float)(end - sum));
-      rv.store(0, sV, VS);
-      rk.store(0, sK, KS);
+  for (int j = seg * p.seg_chunks; j < j1; ++j) {
+    const int t0 = chunk_first(j), len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
+    auto token = [&](int r) { return (int64_t)(down ? t0 + len - 1 - r : t0 + r); };
+    if (!kAhead) fetch(j);
+
+    // log2 decays, summed over the lanes
+    const double d = (double)g * 1.4426950408889634;
+    const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
+    const double end = last_lane(sum);
+    const float hi = (float)sum;
+    // Where no sum is far from zero, D[t][s] = e^{G_t} e^{-G_s}: one factor on y_t
+    // and one on v_s, both with the state's scale c in them:
+    //   y_t = e^{G_t} c ((Q h)_t + sum_s (q_t . k_s) (e^{-G_s} / c) v_s),
+    //   h' = h + K^T ((e^{-G} / c) V),  c' = e^{G_end} c.
+    // Elsewhere (a cleared state, a NaN) every pair has its own exponential and
+    // h is scaled.
+    const bool split = __ballot(!(hi >= kLeastSum && hi <= kMostSum)) == 0;
+    if (!split || c < kLeastScale || c > kMostScale) {
 #pragma unroll
-      for (int r = 1; r < Rows::kRounds; ++r) {
-        rk.load(r);
-        rk.store(r, sK, KS);
-      }
-      if (!STATE) {
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int r = 0; r < Rows::kRounds; ++r) {
-          if (!(W == 4 && Rows::kRounds == 1)) rq.load(r);
-          rq.store(r, sQ, QS);
-        }
+        for (int i = 0; i < 16; ++i) h[kt][i] *= c;
+      c = 1.f;
+    }
+    const float read = exp2_sum(sum) * c;
+    const float write = split ? exp2_sum(-sum) / c : exp2_sum(end - sum);
+    __syncthreads();  // everyone is done with the last chunk
+    gHi[lane] = hi;
+    gLo[lane] = (float)(sum - (double)hi);
+    gRead[lane] = read;
+    gWrite[lane] = write;
+    rv.store(0, sV, VS, down);
+    rk.store(0, sK, KS, down);
+#pragma unroll
+    for (int r = 1; r < Rows::kRounds; ++r) {
+      rk.load(r);
+      rk.store(r, sK, KS, down);
+    }
+    if (!STATE) {
+#pragma unroll
+      for (int r = 0; r < Rows::kRounds; ++r) {
+        if (!(Rows::kRounds == 1)) rq.load(r);
+        rq.store(r, sQ, QS, down);
       }
     }
     __syncthreads();
+    if (kAhead && j + 1 < j1) fetch(j + 1);
 
     if (!STATE) {
-      // scores Q K^T: the three 32 x 32 tiles on and below the diagonal
+      // scores Q K^T, zero above the diagonal (SUMS: and on it): the three 32 x 32
+      // tiles that are read
       for (int tile = wave; tile < 3; tile += W) {
         const int tt = tile > 0, ss = tile > 1;
         f16x a;
@@ -417,16 +520,20 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
             a = mma(*reinterpret_cast<const bf8x*>(qr + n + 8 * half),
                     *reinterpret_cast<const bf8x*>(kr + n + 8 * half), a);
         }
+        const int lead = tt > ss ? 32 : 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          sS[(32 * tt + tile_row(i, half)) * kScoreStride + 32 * ss + col] = a[i];
+        for (int i = 0; i < 16; ++i) {
+          const int r = tile_row(i, half);
+          if (SUMS && lead == 0 && r == col) sD[32 * tt + r] = a[i];
+          const bool seen = SUMS ? col < r + lead : col <= r + lead;
+          sS[(32 * tt + r) * kScoreStride + 32 * ss + col] = seen ? a[i] : 0.f;
+        }
       }
       __syncthreads();
     }
 
-    const float carry = hw_exp2((float)end);
-    f16x ys[2];  // from the state: e^{G_t} (Q h)_t
-    f16x yi[2];  // from the chunk (SUMS: apart, and without the diagonal)
+    f16x ys[2];  // from the state
+    f16x yi[2];  // from the chunk (SUMS: apart)
     f16x(&y)[2] = SUMS ? yi : ys;
     if (!STATE) {
 #pragma unroll
@@ -472,22 +579,28 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
         }
         __builtin_amdgcn_sched_barrier(0);  // keep the operands of few steps in registers
       }
+    }
+    // y_t's factor, from the state's part before the sums or on all of it after
+    auto scale_rows = [&](f16x(&v)[2]) {
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-          const float4 e = *reinterpret_cast<const float4*>(gE + 32 * tt + 8 * a + 4 * half);
-          ys[tt][4 * a] *= e.x;
-          ys[tt][4 * a + 1] *= e.y;
-          ys[tt][4 * a + 2] *= e.z;
-          ys[tt][4 * a + 3] *= e.w;
+          const float4 e = *reinterpret_cast<const float4*>(gRead + 32 * tt + 8 * a + 4 * half);
+          v[tt][4 * a] *= e.x;
+          v[tt][4 * a + 1] *= e.y;
+          v[tt][4 * a + 2] *= e.z;
+          v[tt][4 * a + 3] *= e.w;
         }
+    };
+    if (!split) {
+      if (!STATE) scale_rows(ys);
+      const float carry = exp2_sum(end);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[kt][i] *= carry;
     }
-
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) h[kt][i] *= carry;
 
     // 8 (fp32) or 16 (bf16) tokens s at a time: y += M V, h += K^T (w V)
     constexpr int kStep = kF32 ? 8 : 16;
@@ -495,7 +608,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     for (int s0 = 0; s0 < kChunk; s0 += kStep) {
       constexpr int kV = kF32 ? 4 : 8;  // tokens per lane and step
       const int sl = s0 + kV * half;
-      float vf[kV];
+      float vf[kV], ws[kV];
       bf8x vt;
       if constexpr (kF32) {
 #pragma unroll
@@ -509,28 +622,29 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           vf[2 * i + 1] = high_f32(bits.w[i]);
         }
       }
-      if (!STATE) {
-        float hs[kV], ls[kV];
 #pragma unroll
-        for (int i = 0; i < kV; i += 4) {
-          *reinterpret_cast<float4*>(hs + i) = *reinterpret_cast<const float4*>(gHi + sl + i);
-          *reinterpret_cast<float4*>(ls + i) = *reinterpret_cast<const float4*>(gLo + sl + i);
-        }
+      for (int i = 0; i < kV; i += 4)
+        *reinterpret_cast<float4*>(ws + i) = *reinterpret_cast<const float4*>(gWrite + sl + i);
+      if (!STATE) {
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
           if (32 * tt + 31 < s0) continue;
           const int t = 32 * tt + col;
-          const float ht = gHi[t], lt = gLo[t];
           float m[kV];
 #pragma unroll
           for (int i = 0; i < kV; i += 4)
             *reinterpret_cast<float4*>(m + i) =
                 *reinterpret_cast<const float4*>(sS + t * kScoreStride + sl + i);
-          const int before = SUMS ? t : t + 1;  // tokens that are read
+          if (split) {
 #pragma unroll
-          for (int i = 0; i < kV; ++i) {
-            const float d = hw_exp2((ht - hs[i]) + (lt - ls[i]));
-            m[i] = sl + i < before ? m[i] * d : 0.f;
+            for (int i = 0; i < kV; ++i) m[i] *= ws[i];
+          } else {
+            const float ht = gHi[t], lt = gLo[t];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+              const float e = hw_exp2((ht - gHi[sl + i]) + (lt - gLo[sl + i]));
+              m[i] = sl + i <= t ? m[i] * e : 0.f;
+            }
           }
           if constexpr (kF32) {
 #pragma unroll
@@ -543,10 +657,6 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           }
         }
       }
-      float ws[kV];
-#pragma unroll
-      for (int i = 0; i < kV; i += 4)
-        *reinterpret_cast<float4*>(ws + i) = *reinterpret_cast<const float4*>(gW + sl + i);
 #pragma unroll
       for (int i = 0; i < kV; ++i) vf[i] *= ws[i];
       if constexpr (kF32) {
@@ -565,14 +675,27 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
         }
       }
     }
-
+    if (split) c *= exp2_sum(end);
     if (STATE) {
       whole += end;
       continue;
     }
-    RowStage<TI, 32, 64> rz = {static_cast<const TI*>(p.z), vfirst, vtotal, vstride, cols, len,
-                               lane, vwhole, (bool)p.reverse, first};
-    if (SUMS) rz.load(0);
+    if (split) {
+      scale_rows(ys);
+      if (SUMS) scale_rows(yi);
+    }
+
+    Vals rz;
+    if (SUMS) {
+      rz.base = static_cast<const TI*>(p.z);
+      rz.total = vtotal;
+      rz.first = vfirst + t0 * vstride;
+      rz.stride = vstride;
+      rz.cols = cols;
+      rz.len = len;
+      rz.tid = lane;
+      rz.load(0);
+    }
     // The wave's V slab is free row by row now: z comes in through it and the
     // results leave through it, 32 rows at a time, as whole packs.
 #pragma unroll
@@ -583,18 +706,19 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int t = 32 * tt + tile_row(i, half);
-          vd[i] = sS[t * kScoreStride + t] * to_f32(sV[t * VS + col]);  // the diagonal
+          vd[i] = sD[t] * to_f32(sV[t * VS + col]);  // the diagonal
         }
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int k = 0; k < rz.kN / 2; ++k) {
-          const int i = rz.kN / 2 * tt + k, un = i * 64 + lane;
-          const int r = un / rz.kPer, c = (un % rz.kPer) * kPack;
-          const bool in = r < len && c < cols;
-          Pack<TI> zp;
+        for (int k = 0; k < Vals::kN; ++k) {
+          int r;
+          u4x zp[Vals::kQuads];
+          rz.pack(0, k, down, &r, zp);
+          if ((r >> 5) == tt) {
 #pragma unroll
-          for (int e = 0; e < kPack; ++e) zp.v[e] = in ? rz.v[i].v[e] : TI(0);
-          *reinterpret_cast<Pack<TI>*>(sV + r * VS + c) = zp;
+            for (int q = 0; q < Vals::kQuads; ++q)
+              reinterpret_cast<u4x*>(sV + r * VS + rz.column())[q] = zp[q];
+          }
         }
         __builtin_amdgcn_wave_barrier();
         float z[16];
@@ -604,9 +728,11 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           m[i] = z[i] * o[i];
         }
         const float zin = half_sums(m, lane);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) m[i] = z[i] * ys[tt][i];
         const float zst = half_sums(m, lane);
+        __builtin_amdgcn_sched_barrier(0);
         const int t = 32 * tt + tile_row(col >> 1, half);
         if (active && (lane & 1) == 0 && t < len) {
           float* zs = p.zsum + (((int64_t)b * p.H + head) * p.ctiles + u % p.ctiles) * 2 * p.L;
@@ -633,34 +759,37 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           __builtin_amdgcn_wave_barrier();
 #pragma unroll
           for (int k = 0; k < kOut / 16; ++k) {
-            const int un = k * 64 + lane, r = un >> 2, c = (un & 3) * kPack, t = 32 * tt + r0 + r;
-            const Pack<TO> v = *reinterpret_cast<const Pack<TO>*>(so + r * OS + c);
-            if (t < len && c < cols) store_pack(out + yfirst + token(t) * ystride + c, v, cols - c);
+            const int un = k * 64 + lane, r = un >> 2, cc = (un & 3) * kPack, t = 32 * tt + r0 + r;
+            const Pack<TO> v = *reinterpret_cast<const Pack<TO>*>(so + r * OS + cc);
+            if (t < len && cc < cols)
+              store_pack(out + yfirst + token(t) * ystride + cc, v, cols - cc);
           }
           __builtin_amdgcn_wave_barrier();
         }
       };
       if (p.y_bf16) leave(static_cast<bf16_t*>(p.y));
       else leave(static_cast<float*>(p.y));
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
   if (STATE) {
     if (active && c0 == 0 && lane == 0)
-      p.seg_decay[((int64_t)b * p.H + head) * p.nseg + seg] = hw_exp2((float)whole);
+      p.seg_decay[((int64_t)b * p.H + head) * p.nseg + seg] = exp2_sum(whole);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int n = 32 * kt + tile_row(i, half);
-        if (n < p.Kd && col < cols) p.seg_state[sstate + (int64_t)n * p.Cd + c0 + col] = h[kt][i];
+        if (n < p.Kd && col < cols)
+          p.seg_state[sstate + (int64_t)n * p.Cd + c0 + col] = h[kt][i] * c;
       }
   } else if (p.s_final != nullptr && seg == p.nseg - 1) {
     // walking backwards the first token's own decay is still to come
-    float f = 1.f;
-    if (p.reverse) {
-      const float g = gb[0] * kLog2e;
-      f = hw_exp2(g < kLeastLog2 ? kLeastLog2 : g);
+    float f = c;
+    if (down) {
+      const float l = gb[0] * kLog2e;
+      f *= hw_exp2(l < kLeastLog2 ? kLeastLog2 : l);
     }
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
@@ -673,41 +802,57 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 }
 
 // Host side: launches one walk (or its state pass).
-template <typename TI, int KT, int W, int S, int MODE>
+template <typename TI, int KT, int W, int S, int MODE, bool LOOSE>
 int attn_launch(const AttnParams& p, hipStream_t s) {
   const int groups = p.H / p.qshare, units = p.qshare * p.ctiles;
-  const int64_t grid = (int64_t)p.B * groups * (MODE == kAttnState ? p.nseg - 1 : p.nseg) * ((units + W - 1) / W);
+  const int64_t grid = (int64_t)p.B * groups * (MODE == kAttnState ? p.nseg - 1 : p.nseg) *
+                       ((units + W - 1) / W);
   if (grid > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
   constexpr size_t lds = AttnShape<TI, KT, W>::kBytes;
-  allow_dynamic_lds(attn_kernel<TI, KT, W, S, MODE>, lds);
-  hipLaunchKernelGGL((attn_kernel<TI, KT, W, S, MODE>), dim3((unsigned)grid), dim3(64 * W), lds, s,
-                     p);
+  static_assert(lds <= 160 * 1024, "a CU's LDS");
+  allow_dynamic_lds(attn_kernel<TI, KT, W, S, MODE, LOOSE>, lds);
+  hipLaunchKernelGGL((attn_kernel<TI, KT, W, S, MODE, LOOSE>), dim3((unsigned)grid), dim3(64 * W),
+                     lds, s, p);
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
-template <typename TI, int KT, int W>
+template <typename TI, int KT, int W, bool LOOSE>
 int attn_launch_kind(const AttnParams& p, bool state, bool exact, hipStream_t s) {
-  if (state) return attn_launch<TI, KT, W, 3, kAttnState>(p, s);
-  if (p.z != nullptr) return attn_launch<TI, KT, W, 3, kAttnSums>(p, s);
+  if (state) return attn_launch<TI, KT, W, 3, kAttnState, LOOSE>(p, s);
+  if (p.z != nullptr) return attn_launch<TI, KT, W, 3, kAttnSums, LOOSE>(p, s);
   if constexpr (sizeof(TI) == 2)
-    if (!exact) return attn_launch<TI, KT, W, 2, kAttnPlain>(p, s);
-  return attn_launch<TI, KT, W, 3, kAttnPlain>(p, s);
+    if (!exact) return attn_launch<TI, KT, W, 2, kAttnPlain, LOOSE>(p, s);
+  return attn_launch<TI, KT, W, 3, kAttnPlain, LOOSE>(p, s);
+}
+
+// Waves of a workgroup: four where that many units share q and k, else two.
+// Rows that are not whole packs always go by two (fewer kernels; the packs'
+// masks cost more than the sharing gives), and fp32 rows of 256 leave LDS for
+// one wave's values only.
+inline int attn_waves(bool f32, int Kd, int Cd, int64_t units) {
+  if (f32 && Kd > 128) return 1;
+  if (Kd % kPack != 0 || Cd % kPack != 0) return 2;
+  return units >= 3 ? 4 : 2;
 }
 
 template <typename TI, int KT>
-int attn_launch_waves(const AttnParams& p, int waves, bool state, bool exact, hipStream_t s) {
-  // fp32 rows of 256 leave LDS for one wave's values
-  constexpr bool kNarrow = sizeof(TI) == 4 && KT == 8;
-  if constexpr (!kNarrow) {
-    if (waves == 4) return attn_launch_kind<TI, KT, 4>(p, state, exact, s);
-    if (waves == 2) return attn_launch_kind<TI, KT, 2>(p, state, exact, s);
+int attn_launch_waves(const AttnParams& p, bool state, bool exact, hipStream_t s) {
+  const int64_t units = (int64_t)p.qshare * p.ctiles;
+  const bool loose = p.Kd % kPack != 0 || p.Cd % kPack != 0;
+  if constexpr (sizeof(TI) == 4 && KT == 8) {
+    return loose ? attn_launch_kind<TI, KT, 1, true>(p, state, exact, s)
+                 : attn_launch_kind<TI, KT, 1, false>(p, state, exact, s);
+  } else {
+    if (loose) return attn_launch_kind<TI, KT, 2, true>(p, state, exact, s);
+    if (attn_waves(sizeof(TI) == 4, p.Kd, p.Cd, units) == 4)
+      return attn_launch_kind<TI, KT, 4, false>(p, state, exact, s);
+    return attn_launch_kind<TI, KT, 2, false>(p, state, exact, s);
   }
-  return attn_launch_kind<TI, KT, 1>(p, state, exact, s);
 }
 
 // One per dtype and padded row size.
 #define SWIMBA_ATTN_DECL(name) \
-  int name(const AttnParams& p, int waves, bool state, bool exact, hipStream_t s);
+  int name(const AttnParams& p, bool state, bool exact, hipStream_t s);
 SWIMBA_ATTN_DECL(attn_bf16_32)
 SWIMBA_ATTN_DECL(attn_bf16_64)
 SWIMBA_ATTN_DECL(attn_bf16_128)

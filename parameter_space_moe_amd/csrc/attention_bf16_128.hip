@@ -2,7 +2,7 @@
 #include "attention.hpp"
 
 namespace swimba {
-int attn_bf16_128(const AttnParams& p, int waves, bool state, bool exact, hipStream_t s) {
-  return attn_launch_waves<bf16_t, 4>(p, waves, state, exact, s);
+int attn_bf16_128(const AttnParams& p, bool state, bool exact, hipStream_t s) {
+  return attn_launch_waves<bf16_t, 4>(p, state, exact, s);
 }
 }  // namespace swimba

@@ -2,7 +2,7 @@
 #include "attention.hpp"
 
 namespace swimba {
-int attn_f32_64(const AttnParams& p, int waves, bool state, bool exact, hipStream_t s) {
-  return attn_launch_waves<float, 2>(p, waves, state, exact, s);
+int attn_f32_64(const AttnParams& p, bool state, bool exact, hipStream_t s) {
+  return attn_launch_waves<float, 2>(p, state, exact, s);
 }
 }  // namespace swimba
