@@ -507,8 +507,9 @@ typedef struct {
  * bf16 inputs multiply exactly and sum in fp32; states are fp32.  Non-finite
  * inputs reach every later output of their sequence and head, also across a
  * cleared state, and the outputs up to 63 tokens before them.
- * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256
- * (SWIMBA_EUNSUPPORTED above).  L == 0 writes h_final = h0 (or zeros).
+ * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256, H * P and
+ * G * N < 2^23 (SWIMBA_EUNSUPPORTED above).  L == 0 writes h_final = h0 (or
+ * zeros).
  */
 size_t swimba_linear_attention_workspace_size(const swimba_linear_attention_args* a);
 int swimba_linear_attention(const swimba_linear_attention_args* a, void* ws, size_t ws_bytes,

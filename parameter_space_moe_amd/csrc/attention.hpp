@@ -130,9 +130,13 @@ struct AttnShape {
   static constexpr int kQStride = kRows + (kF32 ? 4 : 8);
   static constexpr int kKStride = kRows + (kF32 ? 4 : 16);
   static constexpr int kValStride = 32 + (kF32 ? 4 : 16);
-  static constexpr size_t kBytes =
-      (size_t)(kChunk * (kQStride + kKStride) + W * kChunk * kValStride) * sizeof(TI) +
-      (size_t)(kChunk * kScoreStride + kChunk + W * 4 * kChunk) * sizeof(float);
+  static constexpr int kGates = 4 * kChunk;  // floats per wave
+  // K rows, values and factors; and the Q rows and scores that the state pass
+  // does without
+  static constexpr size_t kStateBytes = (size_t)(kChunk * kKStride + W * kChunk * kValStride) *
+                                            sizeof(TI) + (size_t)W * kGates * sizeof(float);
+  static constexpr size_t kBytes = kStateBytes + (size_t)kChunk * kQStride * sizeof(TI) +
+                                   (size_t)kChunk * kScoreStride * sizeof(float);
 };
 
 typedef uint32_t u4x __attribute__((ext_vector_type(4)));
@@ -172,11 +176,16 @@ struct RowStage {
   __device__ __forceinline__ void load(int round) {
     const int c = column();
     if constexpr (!LOOSE) {
-      const T* chunk = base + first;
+      // a chunk's rows lie within 2^31 bytes (checked on the host): a wave-uniform
+      // base and 32-bit offsets
+      const char* chunk = reinterpret_cast<const char*>(base + first);
+      const uint32_t step = (uint32_t)stride * (uint32_t)sizeof(T);
+      const uint32_t mine = (uint32_t)(tid / kPer) * step + (uint32_t)(c * (int)sizeof(T));
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
-        const int r = row(round * kRound + i);
-        fetch(i, chunk + (inside(r) ? r * stride + c : 0));
+        const int n = round * kRound + i;
+        const uint32_t off = inside(row(n)) ? mine + (uint32_t)(n * kStep) * step : 0u;
+        fetch(i, reinterpret_cast<const T*>(chunk + off));
       }
     } else if (total >= kPack) {
 #pragma unroll
@@ -324,17 +333,18 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   constexpr bool kF32 = Sh::kF32, STATE = MODE == kAttnState, SUMS = MODE == kAttnSums;
   constexpr int QS = Sh::kQStride, KS = Sh::kKStride, VS = Sh::kValStride;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
-  TI* sQ = reinterpret_cast<TI*>(smem_raw);
-  TI* sK = sQ + kChunk * QS;
+  TI* sK = reinterpret_cast<TI*>(smem_raw);
   TI* sVall = sK + kChunk * KS;
-  float* sS = reinterpret_cast<float*>(sVall + W * kChunk * VS);
-  float* sD = sS + kChunk * kScoreStride;  // the scores' diagonal (SUMS)
-  float* sGall = sD + kChunk;
+  float* sGall = reinterpret_cast<float*>(sVall + W * kChunk * VS);
+  float* sS = sGall + W * Sh::kGates;
+  TI* sQ = reinterpret_cast<TI*>(sS + kChunk * kScoreStride);
+  // the scores' diagonal (SUMS), in the score rows' part above it that nobody reads
+  auto diagonal = [&](int t) -> float& { return sS[(t & 31) * kScoreStride + 32 + (t >> 5)]; };
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
   TI* sV = sVall + wave * kChunk * VS;
-  float* gHi = sGall + wave * 4 * kChunk;  // high and low parts of G
+  float* gHi = sGall + wave * Sh::kGates;  // high and low parts of G
   float *gLo = gHi + kChunk;
   float *gRead = gLo + kChunk, *gWrite = gRead + kChunk;  // factors of y_t and of v_s
 
@@ -400,7 +410,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   using Rows = RowStage<TI, 32 * KT, 64 * W, LOOSE>;
   using Vals = RowStage<TI, 32, 64, LOOSE>;
   // the next chunk's rows travel while this one is worked on, where registers hold them
-  constexpr bool kAhead = false && !kF32 && W == 4 && KT <= 4 && !SUMS;
+  constexpr bool kAhead = !kF32 && KT <= 4 && !SUMS;
   Rows rk, rq;
   Vals rv;
   float g = 0.f;
@@ -524,7 +534,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int r = tile_row(i, half);
-          if (SUMS && lead == 0 && r == col) sD[32 * tt + r] = a[i];
+          if (SUMS && lead == 0 && r == col) diagonal(32 * tt + r) = a[i];
           const bool seen = SUMS ? col < r + lead : col <= r + lead;
           sS[(32 * tt + r) * kScoreStride + 32 * ss + col] = seen ? a[i] : 0.f;
         }
@@ -565,16 +575,19 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
             for (int i = 0; i < 8; ++i) x[i] = h[kt][8 * k2 + i];
             bf8x t[S];
             split_terms<S>(x, t);
+            bf8x a[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
               const TI* r = sQ + (32 * tt + col) * QS + 32 * kt + 16 * k2 + 4 * half;
               struct { uint2 a, b; } qa;
               qa.a = *reinterpret_cast<const uint2*>(r);
               qa.b = *reinterpret_cast<const uint2*>(r + 8);
-              const bf8x a = __builtin_bit_cast(bf8x, qa);
-#pragma unroll
-              for (int s = S - 1; s >= 0; --s) ys[tt] = mma(a, t[s], ys[tt]);
+              a[tt] = __builtin_bit_cast(bf8x, qa);
             }
+#pragma unroll
+            for (int s = S - 1; s >= 0; --s)
+#pragma unroll
+              for (int tt = 0; tt < 2; ++tt) ys[tt] = mma(a[tt], t[s], ys[tt]);
           }
         }
         __builtin_amdgcn_sched_barrier(0);  // keep the operands of few steps in registers
@@ -706,7 +719,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int t = 32 * tt + tile_row(i, half);
-          vd[i] = sD[t] * to_f32(sV[t * VS + col]);  // the diagonal
+          vd[i] = diagonal(t) * to_f32(sV[t * VS + col]);  // the diagonal
         }
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -762,7 +775,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
             const int un = k * 64 + lane, r = un >> 2, cc = (un & 3) * kPack, t = 32 * tt + r0 + r;
             const Pack<TO> v = *reinterpret_cast<const Pack<TO>*>(so + r * OS + cc);
             if (t < len && cc < cols)
-              store_pack(out + yfirst + token(t) * ystride + cc, v, cols - cc);
+              store_pack(out + yfirst + token(t) * ystride + cc, v, LOOSE ? cols - cc : kPack);
           }
           __builtin_amdgcn_wave_barrier();
         }
@@ -808,7 +821,8 @@ int attn_launch(const AttnParams& p, hipStream_t s) {
   const int64_t grid = (int64_t)p.B * groups * (MODE == kAttnState ? p.nseg - 1 : p.nseg) *
                        ((units + W - 1) / W);
   if (grid > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
-  constexpr size_t lds = AttnShape<TI, KT, W>::kBytes;
+  using Sh = AttnShape<TI, KT, W>;
+  constexpr size_t lds = MODE == kAttnState ? Sh::kStateBytes : Sh::kBytes;
   static_assert(lds <= 160 * 1024, "a CU's LDS");
   allow_dynamic_lds(attn_kernel<TI, KT, W, S, MODE, LOOSE>, lds);
   hipLaunchKernelGGL((attn_kernel<TI, KT, W, S, MODE, LOOSE>), dim3((unsigned)grid), dim3(64 * W),

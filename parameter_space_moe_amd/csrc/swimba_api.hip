@@ -446,6 +446,8 @@ int validate_attention(int B, int L, int H, int G, int N, int P, swimba_dtype in
   if (N > 256) return SWIMBA_EUNSUPPORTED;
   // workgroups are counted in 31 bits
   if ((int64_t)B * H * ((P + 15) / 16) > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
+  // 64 rows of a token's heads within 2^31 bytes
+  if ((int64_t)H * P >= (1 << 23) || (int64_t)G * N >= (1 << 23)) return SWIMBA_EUNSUPPORTED;
   return SWIMBA_OK;
 }
 
