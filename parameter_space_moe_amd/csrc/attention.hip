@@ -296,9 +296,12 @@ WalkPlan plan_walk(bool f32, int B, int L, int H, int share, int Kd, int Cd, int
   w.waves = attn_waves(f32, Kd, Cd, units);
   const int64_t nc = (L + kChunk - 1) / kChunk;
   const int64_t base = (int64_t)B * (H / share) * ((units + w.waves - 1) / w.waves);
-  // eight waves per CU from the independent walks, or from segments of them
-  // (whose first states cost a pass over k and v) of four chunks or more
-  int64_t want = 8LL * device_cus(dev) / (base * w.waves > 0 ? base * w.waves : 1);
+  // as many workgroups as the device holds at once, from the independent walks
+  // or from segments of them (whose first states cost a pass over k and v) of
+  // four chunks or more
+  const int64_t hold = (int64_t)device_cus(dev) *
+                       (f32 ? attn_resident<float>(Kd, w.waves) : attn_resident<bf16_t>(Kd, w.waves));
+  int64_t want = base > 0 ? hold / base : 1;
   if (want > nc / 4) want = nc / 4;
   if (want < 2) want = 1;
   w.seg_chunks = (int)((nc + want - 1) / want);

@@ -141,13 +141,12 @@ struct AttnShape {
 
 typedef uint32_t u4x __attribute__((ext_vector_type(4)));
 
-// Rows of one operand of a chunk on their way to LDS, up to eight packs per
-// thread at a time: load() issues the loads of a round, store() writes them,
-// zero beyond `len` rows and `cols` columns.  The packs stay whole registers and
-// no load waits for another: without branches between them where rows are whole
-// packs; LOOSE rows take one load per pack inside the tensor, moved back from
-// its end where it would pass it.  Memory is walked in rising order; a chunk
-// walked backwards is turned round in LDS.
+// Rows of one operand of a chunk, up to eight packs per thread at a time: load()
+// issues the loads of a round, pack() has them with zeros beyond `len` rows and
+// `cols` columns, store() writes those to LDS.  The packs stay whole registers
+// and no load waits for another: without branches between them where rows are
+// whole packs; LOOSE rows take one load per pack inside the tensor, moved back
+// from its end where it would pass it.
 template <typename T, int PAD, int THREADS, bool LOOSE>
 struct RowStage {
   static constexpr int kPer = PAD / kPack, kN = kChunk * kPer / THREADS;
@@ -161,11 +160,15 @@ struct RowStage {
   int64_t first;    // element of the chunk's lowest token, column 0
   int64_t stride;   // between tokens
   int cols, len, tid;
+  bool down;        // row 0 is the highest token
   u4x v[kRound][kQuads];
 
   __device__ __forceinline__ int row(int i) const { return i * kStep + tid / kPer; }
   __device__ __forceinline__ int column() const { return tid % kPer * kPack; }
   __device__ __forceinline__ bool inside(int r) const { return r < len && column() < cols; }
+  __device__ __forceinline__ int64_t element(int r) const {
+    return first + (down ? len - 1 - r : r) * stride + column();
+  }
 
   __device__ __forceinline__ void fetch(int i, const T* at) {
     const Loose l = *reinterpret_cast<const Loose*>(at);
@@ -174,49 +177,46 @@ struct RowStage {
   }
 
   __device__ __forceinline__ void load(int round) {
-    const int c = column();
     if constexpr (!LOOSE) {
       // a chunk's rows lie within 2^31 bytes (checked on the host): a wave-uniform
       // base and 32-bit offsets
       const char* chunk = reinterpret_cast<const char*>(base + first);
-      const uint32_t step = (uint32_t)stride * (uint32_t)sizeof(T);
-      const uint32_t mine = (uint32_t)(tid / kPer) * step + (uint32_t)(c * (int)sizeof(T));
+      const uint32_t bytes = (uint32_t)stride * (uint32_t)sizeof(T);
+      const uint32_t step = (down ? 0u - bytes : bytes) * (uint32_t)kStep;
+      const uint32_t mine = (uint32_t)(down ? len - 1 - tid / kPer : tid / kPer) * bytes +
+                            (uint32_t)(column() * (int)sizeof(T));
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
         const int n = round * kRound + i;
-        const uint32_t off = inside(row(n)) ? mine + (uint32_t)(n * kStep) * step : 0u;
+        const uint32_t off = inside(row(n)) ? mine + (uint32_t)n * step : 0u;
         fetch(i, reinterpret_cast<const T*>(chunk + off));
       }
     } else if (total >= kPack) {
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
         const int r = row(round * kRound + i);
-        const int64_t e = inside(r) ? first + r * stride + c : 0;
+        const int64_t e = inside(r) ? element(r) : 0;
         fetch(i, base + (e + kPack <= total ? e : total - kPack));
       }
     } else {  // a tensor of less than a pack
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
-        const int r = row(round * kRound + i);
-        const Pack<T> p = inside(r) ? load_pack(base + first + r * stride + c,
-                                                cols - c < 7 ? cols - c : 7)
-                                    : Pack<T>{};
+        const int r = row(round * kRound + i), n = cols - column();
+        const Pack<T> p = inside(r) ? load_pack(base + element(r), n < 7 ? n : 7) : Pack<T>{};
         __builtin_memcpy(v[i], &p, sizeof(p));
       }
     }
   }
 
-  // The pack i of this round and the chunk row it is (walk order).
-  __device__ __forceinline__ void pack(int round, int i, bool down, int* at, u4x* out) const {
-    const int r = row(round * kRound + i), c = column();
-    *at = down && r < len ? len - 1 - r : r;
+  __device__ __forceinline__ void pack(int round, int i, u4x* out) const {
+    const int r = row(round * kRound + i);
     const bool in = inside(r);
 #pragma unroll
     for (int q = 0; q < kQuads; ++q) out[q] = in ? v[i][q] : u4x{0, 0, 0, 0};
     if constexpr (LOOSE) {
       uint32_t w[kWords];
       __builtin_memcpy(w, out, sizeof(w));
-      const int64_t e = first + r * stride + c;
+      const int64_t e = element(r);
       const int shift = in && total >= kPack && e + kPack > total ? (int)(e + kPack - total) : 0;
       if (__ballot(shift != 0)) {  // the tensor's last elements
         T m[kPack], o[kPack];
@@ -229,7 +229,7 @@ struct RowStage {
         }
         __builtin_memcpy(w, o, sizeof(o));
       }
-      const int n = cols - c;  // columns of this pack
+      const int n = cols - column();  // columns of this pack
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int k = 0; k < kWords; ++k)
@@ -242,15 +242,23 @@ struct RowStage {
     }
   }
 
-  __device__ __forceinline__ void store(int round, T* dst, int dst_stride, bool down) const {
+  __device__ __forceinline__ void store(int round, T* dst, int dst_stride) const {
+    T* d = dst + row(round * kRound) * dst_stride + column();
+    if (!LOOSE && len == kChunk && cols >= PAD) {  // nothing to leave out
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < kRound; ++i)
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+          reinterpret_cast<u4x*>(d + i * kStep * dst_stride)[q] = v[i][q];
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kRound; ++i) {
-      int r;
       u4x p[kQuads];
-      pack(round, i, down, &r, p);
-      u4x* d = reinterpret_cast<u4x*>(dst + r * dst_stride + column());
+      pack(round, i, p);
 #pragma unroll
-      for (int q = 0; q < kQuads; ++q) d[q] = p[q];
+      for (int q = 0; q < kQuads; ++q) reinterpret_cast<u4x*>(d + i * kStep * dst_stride)[q] = p[q];
     }
   }
 };
@@ -277,30 +285,6 @@ __device__ __forceinline__ double last_lane(double v) {
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63);
   const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
   return __longlong_as_double(((uint64_t)hi << 32) | lo);
-}
-
-// Sums of 16 registers, each over the 32 lanes of its half: lane l of a half
-// returns that of register (l >> 1).
-__device__ __forceinline__ float half_sums(const float* v, int lane) {
-  float a[8], b[4], c[2];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool up = lane & 16;
-    a[i] = (up ? v[i + 8] : v[i]) + xor_lane<16>(up ? v[i] : v[i + 8], lane);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool up = lane & 8;
-    b[i] = (up ? a[i + 4] : a[i]) + xor_lane<8>(up ? a[i] : a[i + 4], lane);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const bool up = lane & 4;
-    c[i] = (up ? b[i + 2] : b[i]) + xor_lane<4>(up ? b[i] : b[i + 2], lane);
-  }
-  const bool up = lane & 2;
-  float s = (up ? c[1] : c[0]) + xor_lane<2>(up ? c[0] : c[1], lane);
-  return s + xor_lane<1>(s, lane);
 }
 
 // Row of register i of a 32 x 32 accumulator tile.
@@ -426,6 +410,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     rk.cols = p.Kd;
     rk.len = len;
     rk.tid = tid;
+    rk.down = down;
     rv.base = static_cast<const TI*>(p.v);
     rv.total = vtotal;
     rv.first = vfirst + t0 * vstride;
@@ -433,6 +418,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     rv.cols = cols;
     rv.len = len;
     rv.tid = lane;
+    rv.down = down;
     if (!p.token_decay) {
       g = lane < len && !(down && t0 + len - 1 - lane + 1 >= p.L) ? gb[0] : 0.f;
     } else {
@@ -451,6 +437,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       rq.cols = rk.cols;
       rq.len = rk.len;
       rq.tid = rk.tid;
+      rq.down = down;
       if (Rows::kRounds == 1) rq.load(0);
     }
   };
@@ -474,6 +461,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     // h is scaled.
     const bool split = __ballot(!(hi >= kLeastSum && hi <= kMostSum)) == 0;
     if (!split || c < kLeastScale || c > kMostScale) {
+      __builtin_amdgcn_sched_barrier(0);  // rare: a branch, not a product with one
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -487,18 +475,18 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     gLo[lane] = (float)(sum - (double)hi);
     gRead[lane] = read;
     gWrite[lane] = write;
-    rv.store(0, sV, VS, down);
-    rk.store(0, sK, KS, down);
+    rv.store(0, sV, VS);
+    rk.store(0, sK, KS);
 #pragma unroll
     for (int r = 1; r < Rows::kRounds; ++r) {
       rk.load(r);
-      rk.store(r, sK, KS, down);
+      rk.store(r, sK, KS);
     }
     if (!STATE) {
 #pragma unroll
       for (int r = 0; r < Rows::kRounds; ++r) {
         if (!(Rows::kRounds == 1)) rq.load(r);
-        rq.store(r, sQ, QS, down);
+        rq.store(r, sQ, QS);
       }
     }
     __syncthreads();
@@ -607,6 +595,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
         }
     };
     if (!split) {
+      __builtin_amdgcn_sched_barrier(0);
       if (!STATE) scale_rows(ys);
       const float carry = exp2_sum(end);
 #pragma unroll
@@ -694,12 +683,18 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       continue;
     }
     if (split) {
+      __builtin_amdgcn_sched_barrier(0);
       scale_rows(ys);
       if (SUMS) scale_rows(yi);
     }
 
-    Vals rz;
-    if (SUMS) {
+    const int64_t ystride = (int64_t)p.H * p.Cd;
+    const int64_t yfirst = (int64_t)b * p.L * ystride + (int64_t)head * p.Cd + c0;
+    if constexpr (SUMS) {
+      // 16 rows at a time the two parts pass through the wave's V slab (free once
+      // the rows for the diagonal are out) to eight columns per lane, four lanes
+      // per row, where z comes from memory and the sums stay short.
+      Vals rz;
       rz.base = static_cast<const TI*>(p.z);
       rz.total = vtotal;
       rz.first = vfirst + t0 * vstride;
@@ -707,82 +702,102 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       rz.cols = cols;
       rz.len = len;
       rz.tid = lane;
+      rz.down = down;
       rz.load(0);
-    }
-    // The wave's V slab is free row by row now: z comes in through it and the
-    // results leave through it, 32 rows at a time, as whole packs.
+      Pack<TI> vd[Vals::kN];
 #pragma unroll
-    for (int tt = 0; tt < 2; ++tt) {
-      f16x o = y[tt];
-      if constexpr (SUMS) {
-        float m[16], vd[16];
+      for (int k = 0; k < Vals::kN; ++k)
+        vd[k] = *reinterpret_cast<const Pack<TI>*>(sV + rz.row(k) * VS + rz.column());
+      __builtin_amdgcn_wave_barrier();
+      constexpr int OS = 36;
+      float* part = reinterpret_cast<float*>(sV);  // [2][16][OS]
+      static_assert(2 * 16 * OS * sizeof(float) <= kChunk * VS * sizeof(TI), "the slab");
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = 32 * tt + tile_row(i, half);
-          vd[i] = diagonal(t) * to_f32(sV[t * VS + col]);  // the diagonal
+      for (int k = 0; k < Vals::kN; ++k) {
+        const int tt = k >> 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = tile_row(i, half) * OS + col;
+          part[r] = yi[tt][8 * (k & 1) + i];
+          part[16 * OS + r] = ys[tt][8 * (k & 1) + i];
         }
         __builtin_amdgcn_wave_barrier();
+        const int t = rz.row(k), cc = rz.column();
+        float in[kPack], st[kPack];
 #pragma unroll
-        for (int k = 0; k < Vals::kN; ++k) {
-          int r;
-          u4x zp[Vals::kQuads];
-          rz.pack(0, k, down, &r, zp);
-          if ((r >> 5) == tt) {
+        for (int i = 0; i < kPack; i += 4) {
+          const float* r = part + (lane >> 2) * OS + cc + i;
+          *reinterpret_cast<float4*>(in + i) = *reinterpret_cast<const float4*>(r);
+          *reinterpret_cast<float4*>(st + i) = *reinterpret_cast<const float4*>(r + 16 * OS);
+        }
+        u4x zq[Vals::kQuads];
+        rz.pack(0, k, zq);
+        Pack<TI> z;
+        __builtin_memcpy(&z, zq, sizeof(z));
+        float zin = 0.f, zst = 0.f;
+        const float dg = diagonal(t);
 #pragma unroll
-            for (int q = 0; q < Vals::kQuads; ++q)
-              reinterpret_cast<u4x*>(sV + r * VS + rz.column())[q] = zp[q];
+        for (int i = 0; i < kPack; ++i) {
+          zin = fmaf(to_f32(z.v[i]), in[i], zin);
+          zst = fmaf(to_f32(z.v[i]), st[i], zst);
+          in[i] = fmaf(dg, to_f32(vd[k].v[i]), in[i]) + st[i];
+        }
+        zin += xor_lane<1>(zin, lane);
+        zst += xor_lane<1>(zst, lane);
+        zin += xor_lane<2>(zin, lane);
+        zst += xor_lane<2>(zst, lane);
+        if (t < len && cc < cols) {
+          const int64_t at = yfirst + token(t) * ystride + cc;
+          if (p.y_bf16) {
+            Pack<bf16_t> o;
+#pragma unroll
+            for (int i = 0; i < kPack; ++i) o.v[i] = from_f32<bf16_t>(in[i]);
+            store_pack(static_cast<bf16_t*>(p.y) + at, o, LOOSE ? cols - cc : kPack);
+          } else {
+            Pack<float> o;
+#pragma unroll
+            for (int i = 0; i < kPack; ++i) o.v[i] = in[i];
+            store_pack(static_cast<float*>(p.y) + at, o, LOOSE ? cols - cc : kPack);
           }
         }
-        __builtin_amdgcn_wave_barrier();
-        float z[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          z[i] = to_f32(sV[(32 * tt + tile_row(i, half)) * VS + col]);
-          m[i] = z[i] * o[i];
-        }
-        const float zin = half_sums(m, lane);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) m[i] = z[i] * ys[tt][i];
-        const float zst = half_sums(m, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        const int t = 32 * tt + tile_row(col >> 1, half);
-        if (active && (lane & 1) == 0 && t < len) {
+        if (active && (lane & 3) == 0 && t < len) {
           float* zs = p.zsum + (((int64_t)b * p.H + head) * p.ctiles + u % p.ctiles) * 2 * p.L;
           zs[token(t)] = zin;
           zs[p.L + token(t)] = zst;
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = (o[i] + vd[i]) + ys[tt][i];
         __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const int64_t ystride = (int64_t)p.H * p.Cd;
-      const int64_t yfirst = (int64_t)b * p.L * ystride + (int64_t)head * p.Cd + c0;
+    } else {
+      // The results leave through the wave's V slab, 32 rows at a time (16 where
+      // they are wider), as whole packs.
       auto leave = [&](auto* out) {
         using TO = std::remove_pointer_t<decltype(out)>;
         constexpr int OS = 32 + 16 / (int)sizeof(TO);
-        // rows at a time that fit the slab's 32 rows
         constexpr int kOut = sizeof(TO) > sizeof(TI) ? 16 : 32;
-        TO* so = reinterpret_cast<TO*>(sV + 32 * tt * VS);
+        TO* so = reinterpret_cast<TO*>(sV);
+        static_assert(kOut * OS * sizeof(TO) <= kChunk * VS * sizeof(TI), "the slab");
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += kOut) {
+        for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-          for (int i = r0 / 2; i < (r0 + kOut) / 2; ++i)
-            so[(tile_row(i, half) - r0) * OS + col] = from_f32<TO>(o[i]);
-          __builtin_amdgcn_wave_barrier();
+          for (int r0 = 0; r0 < 32; r0 += kOut) {
 #pragma unroll
-          for (int k = 0; k < kOut / 16; ++k) {
-            const int un = k * 64 + lane, r = un >> 2, cc = (un & 3) * kPack, t = 32 * tt + r0 + r;
-            const Pack<TO> v = *reinterpret_cast<const Pack<TO>*>(so + r * OS + cc);
-            if (t < len && cc < cols)
-              store_pack(out + yfirst + token(t) * ystride + cc, v, LOOSE ? cols - cc : kPack);
+            for (int i = r0 / 2; i < (r0 + kOut) / 2; ++i)
+              so[(tile_row(i, half) - r0) * OS + col] = from_f32<TO>(ys[tt][i]);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int k = 0; k < kOut / 16; ++k) {
+              const int un = k * 64 + lane, r = un >> 2, cc = (un & 3) * kPack;
+              const int t = 32 * tt + r0 + r;
+              const Pack<TO> v = *reinterpret_cast<const Pack<TO>*>(so + r * OS + cc);
+              if (t < len && cc < cols)
+                store_pack(out + yfirst + token(t) * ystride + cc, v, LOOSE ? cols - cc : kPack);
+            }
+            __builtin_amdgcn_wave_barrier();
           }
-          __builtin_amdgcn_wave_barrier();
-        }
       };
       if (p.y_bf16) leave(static_cast<bf16_t*>(p.y));
       else leave(static_cast<float*>(p.y));
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -847,6 +862,25 @@ inline int attn_waves(bool f32, int Kd, int Cd, int64_t units) {
   if (f32 && Kd > 128) return 1;
   if (Kd % kPack != 0 || Cd % kPack != 0) return 2;
   return units >= 3 ? 4 : 2;
+}
+
+// Workgroups of a walk that a CU holds at once: by its LDS, and two waves per
+// SIMD by the registers (one with rows of more than 128).
+template <typename TI, int KT>
+int attn_resident_rows(int waves) {
+  size_t lds = 0;
+  if (waves == 4) lds = AttnShape<TI, KT, 4>::kBytes;
+  else if (waves == 2) lds = AttnShape<TI, KT, 2>::kBytes;
+  else lds = AttnShape<TI, KT, 1>::kBytes;
+  const int by_lds = (int)(160 * 1024 / lds), by_regs = (KT > 4 ? 4 : 8) / waves;
+  return by_lds < by_regs ? by_lds : by_regs;
+}
+template <typename TI>
+int attn_resident(int Kd, int waves) {
+  if (Kd <= 32) return attn_resident_rows<TI, 1>(waves);
+  if (Kd <= 64) return attn_resident_rows<TI, 2>(waves);
+  if (Kd <= 128) return attn_resident_rows<TI, 4>(waves);
+  return attn_resident_rows<TI, 8>(waves);
 }
 
 template <typename TI, int KT>
