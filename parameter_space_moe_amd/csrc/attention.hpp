@@ -527,7 +527,6 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           sS[(32 * tt + r) * kScoreStride + 32 * ss + col] = seen ? a[i] : 0.f;
         }
       }
-      __syncthreads();
     }
 
     f16x ys[2];  // from the state
@@ -580,6 +579,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
         }
         __builtin_amdgcn_sched_barrier(0);  // keep the operands of few steps in registers
       }
+      __syncthreads();  // the scores are there (the state's part did not need them)
     }
     // y_t's factor, from the state's part before the sums or on all of it after
     auto scale_rows = [&](f16x(&v)[2]) {
@@ -669,12 +669,13 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       } else {
         bf8x wt[3];
         split_terms<3>(vf, wt);
+        bf8x a[KT];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-          const bf8x a = column8(sK, KS, s0, 32 * kt, lane);
+        for (int kt = 0; kt < KT; ++kt) a[kt] = column8(sK, KS, s0, 32 * kt, lane);
 #pragma unroll
-          for (int s = 2; s >= 0; --s) h[kt] = mma(a, wt[s], h[kt]);
-        }
+        for (int s = 2; s >= 0; --s)
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) h[kt] = mma(a[kt], wt[s], h[kt]);
       }
     }
     if (split) c *= exp2_sum(end);
