@@ -33,20 +33,36 @@ struct RouteGradParams {
   int64_t T;
   int D, E, k;
   int64_t per;  // tokens per split
+  int two;      // LDS holds two slope tables
 };
 
+// Four channels of one token as they are in memory.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, int n, float* v) {
-  struct __attribute__((packed, aligned(sizeof(T)))) Loose { T e[4]; };
-  if (n >= 4) {
-    const Loose l = *reinterpret_cast<const Loose*>(p);
+struct Quad {
+  struct __attribute__((packed, aligned(sizeof(T)))) Loose { uint32_t w[sizeof(T)]; };
+  uint32_t w[sizeof(T)];
+
+  // n elements of the row are left (WHOLE: four or none); none: anything inside x
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if (WHOLE || n >= 4) {
+      const Loose l = *reinterpret_cast<const Loose*>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = to_f32(l.e[i]);
-  } else {
+      for (int i = 0; i < (int)sizeof(T); ++i) w[i] = l.w[i];
+    } else {
+      T e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+      for (int i = 0; i < 4; ++i) e[i] = i < n ? p[i] : T(0);
+      __builtin_memcpy(w, e, sizeof(w));
+    }
   }
-}
+  __device__ __forceinline__ void floats(float* v, bool on) const {
+    T e[4];
+    __builtin_memcpy(e, w, sizeof(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = on ? to_f32(e[i]) : 0.f;
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(T* p, int n, const float* v) {
@@ -63,16 +79,31 @@ __device__ __forceinline__ void store4(T* p, int n, const float* v) {
   }
 }
 
-// ET: expert tiles of 16.
-template <typename TI, typename TO, int ET>
-__global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradParams p) {
-  constexpr int kDense = ET * 16 + 1;
+// LDS of one tile's slopes: dense by expert, and by slot.
+template <int ET>
+struct Slopes {
+  static constexpr int kDense = ET * 16 + 1;
+  float* dense;   // [kTile][kDense]
+  float* slot;    // [kTile][k]
+  int32_t* expert;  // [kTile][k], -1 without
+  int32_t* any;     // [kTile] tokens with an expert
+  static constexpr size_t words(int k) { return kTile * (kDense + 1 + 2 * (size_t)k); }
+  __device__ __forceinline__ Slopes(float* at, int k)
+      : dense(at),
+        slot(at + kTile * kDense),
+        expert(reinterpret_cast<int32_t*>(slot + kTile * k)),
+        any(expert + kTile * k) {}
+};
+
+// ET: expert tiles of 16; K: slots per token (0: any number, from p.k); WHOLE:
+// rows are whole groups of four channels.
+template <typename TI, typename TO, int ET, int K, bool WHOLE>
+__global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void route_grad_kernel(RouteGradParams p) {
+  using Table = Slopes<ET>;
+  constexpr int kDense = Table::kDense;
   extern __shared__ __attribute__((aligned(16))) float smem[];
-  float* sW = smem;                               // [E][kSlabStride]
-  float* sS = sW + p.E * kSlabStride;             // [kTile][kDense] slopes
-  float* sV = sS + kTile * kDense;                // [kTile][k] slopes of the slots
-  int32_t* sE = reinterpret_cast<int32_t*>(sV + kTile * p.k);  // [kTile][k] experts
-  int32_t* sOk = sE + kTile * p.k;                // [kTile] tokens with an expert
+  const int k = K > 0 ? K : p.k;
+  float* sW = smem;  // [E][kSlabStride]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int q = lane >> 4, c = lane & 15;
   const int d0 = blockIdx.x * kSlab, dl = wave * 64 + 4 * c, d = d0 + dl;
@@ -94,65 +125,107 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradParams p)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[e][j] = f4{0.f, 0.f, 0.f, 0.f};
 
-  for (int64_t t0 = tb; t0 < te; t0 += kTile) {
-    const int len = te - t0 < kTile ? (int)(te - t0) : kTile;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTile * kDense; i += kThreads) sS[i] = 0.f;
-    __syncthreads();
-    if ((int)threadIdx.x < len) {
-      const int64_t s = (t0 + threadIdx.x) * p.k;
-      float mean = 0.f;
-      int32_t any = 0;
-      for (int j = 0; j < p.k; ++j) mean = fmaf(p.gate[s + j], p.dgate[s + j], mean);
-      for (int j = 0; j < p.k; ++j) {
-        const int e = p.idx[s + j];
-        const bool in = e >= 0 && e < p.E;
-        const float v = p.gate[s + j] * (p.dgate[s + j] - mean);
-        sV[threadIdx.x * p.k + j] = v;
-        sE[threadIdx.x * p.k + j] = in ? e : -1;
-        any |= in;
-        if (in) sS[threadIdx.x * kDense + e] += v;  // an expert listed twice adds twice
-      }
-      sOk[threadIdx.x] = any;
-    } else if (threadIdx.x < kTile) {
-      sOk[threadIdx.x] = 0;
+  // 32 rows of x are in flight while the 32 before are worked on
+  constexpr int kSteps = 8;
+  Quad<TI> xr[kSteps];
+  auto fetch = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int64_t t = t0 + 4 * i + q;
+      const bool in = t < te && left > 0;  // others: the first channels of x
+      xr[i].template load<WHOLE>(x + (in ? t * p.D + d : 0), in ? left : p.D);
     }
-    __syncthreads();
+  };
+  if (tb < te) fetch(tb);  // without tokens x may be null
+
+  int buf = 0;
+  for (int64_t t0 = tb; t0 < te; t0 += kTile, buf ^= p.two) {
+    if (!p.two) __syncthreads();  // one table only: everyone is done with it
+    const int len = te - t0 < kTile ? (int)(te - t0) : kTile;
+    const Table tab(smem + p.E * kSlabStride + buf * Table::words(k), k);
+    // one wave after the other makes a tile's table: a lane per token
+    if (wave == (int)((t0 - tb) / kTile & 3)) {
+      float* row = tab.dense + lane * kDense;
+      for (int e = 0; e < ET * 16; ++e) row[e] = 0.f;
+      int32_t any = 0;
+      if (lane < len) {
+        const int64_t s = (t0 + lane) * k;
+        if constexpr (K > 0) {
+          float g[K], dg[K];
+          int32_t ex[K];
 #pragma unroll
-    for (int st = 0; st < kTile / 16; ++st) {
-      if (st * 16 >= len) break;
-      float xv[4][4];
+          for (int j = 0; j < K; ++j) {
+            g[j] = p.gate[s + j];
+            dg[j] = p.dgate[s + j];
+            ex[j] = p.idx[s + j];
+          }
+          float mean = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = st * 16 + 4 * i + q;
-        // a token without an expert may hold anything: not read
-        load4(x + (t0 + t) * p.D + d, sOk[t] ? left : 0, xv[i]);
+          for (int j = 0; j < K; ++j) mean = fmaf(g[j], dg[j], mean);
+#pragma unroll
+          for (int j = 0; j < K; ++j) {
+            const bool in = ex[j] >= 0 && ex[j] < p.E;
+            const float v = g[j] * (dg[j] - mean);
+            tab.slot[lane * K + j] = v;
+            tab.expert[lane * K + j] = in ? ex[j] : -1;
+            any |= in;
+            if (in) row[ex[j]] += v;  // an expert listed twice adds twice
+          }
+        } else {
+          float mean = 0.f;
+          for (int j = 0; j < k; ++j) mean = fmaf(p.gate[s + j], p.dgate[s + j], mean);
+          for (int j = 0; j < k; ++j) {
+            const int e = p.idx[s + j];
+            const bool in = e >= 0 && e < p.E;
+            const float v = p.gate[s + j] * (p.dgate[s + j] - mean);
+            tab.slot[lane * k + j] = v;
+            tab.expert[lane * k + j] = in ? e : -1;
+            any |= in;
+            if (in) row[e] += v;
+          }
+        }
       }
+      tab.any[lane] = any;
+    }
+    // with two tables the one barrier per tile: the table of two tiles before, in
+    // this place, has been read by everyone who passed the last one
+    __syncthreads();
+#pragma unroll 1
+    for (int hb = 0; hb < kTile; hb += 4 * kSteps) {
+      if (hb >= len) break;
+      Quad<TI> xc[kSteps];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = st * 16 + 4 * i + q;
+      for (int i = 0; i < kSteps; ++i) xc[i] = xr[i];
+      fetch(t0 + hb + 4 * kSteps);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int t = hb + 4 * i + q;
+        float xv[4];
+        // a token without an expert may hold anything: left out
+        xc[i].floats(xv, tab.any[t] != 0);
         float a[ET];
 #pragma unroll
-        for (int e = 0; e < ET; ++e) a[e] = sS[t * kDense + e * 16 + c];
+        for (int e = 0; e < ET; ++e) a[e] = tab.dense[t * kDense + e * 16 + c];
 #pragma unroll
         for (int e = 0; e < ET; ++e)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            acc[e][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], xv[i][j], acc[e][j], 0, 0, 0);
-        if (t < len && left > 0) {
-          float o[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int j = 0; j < p.k; ++j) {
-            const int e = sE[t * p.k + j];
-            if (e < 0) continue;
-            const float v = sV[t * p.k + j];
-            const float4 w = *reinterpret_cast<const float4*>(sW + e * kSlabStride + dl);
-            o[0] = fmaf(v, w.x, o[0]);
-            o[1] = fmaf(v, w.y, o[1]);
-            o[2] = fmaf(v, w.z, o[2]);
-            o[3] = fmaf(v, w.w, o[3]);
-          }
-          store4(dx + (t0 + t) * p.D + d, left, o);
+            acc[e][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], xv[j], acc[e][j], 0, 0, 0);
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        const int ts = t < len ? t : 0;
+        // (a loop of K, unrolled, where K is known)
+        for (int j = 0; j < k; ++j) {
+          const int e = tab.expert[ts * k + j];
+          const float v = tab.slot[ts * k + j];
+          const float4 w =
+              *reinterpret_cast<const float4*>(sW + (e < 0 ? 0 : e) * kSlabStride + dl);
+          o[0] = e < 0 ? o[0] : fmaf(v, w.x, o[0]);
+          o[1] = e < 0 ? o[1] : fmaf(v, w.y, o[1]);
+          o[2] = e < 0 ? o[2] : fmaf(v, w.z, o[2]);
+          o[3] = e < 0 ? o[3] : fmaf(v, w.w, o[3]);
         }
+        if (t < len && left > 0) store4(dx + (t0 + t) * p.D + d, WHOLE ? 4 : left, o);
+        if (i & 1) __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -194,14 +267,16 @@ struct RouteGradPlan {
   size_t bytes = 0;
 };
 
-// Four workgroups per CU (the LDS of 16 experts allows more), splits of whole
-// 64-token tiles.
-RouteGradPlan plan(int64_t T, int D, int E, int dev) {
+// Four workgroups per CU, splits of whole 64-token tiles, and no more of them
+// than keeps the partial sums (8 E bytes per channel and split, out and in) at
+// half the stream of x and dx.
+RouteGradPlan plan(int64_t T, int D, int E, int elem, int dev) {
   RouteGradPlan r;
   r.slabs = (D + kSlab - 1) / kSlab;
   const int64_t tiles = (T + kTile - 1) / kTile;
   int64_t want = (4LL * device_cus(dev) + r.slabs - 1) / r.slabs;
-  if (want > tiles) want = tiles;
+  const int64_t least = (16LL * E / (2 * elem) + kTile - 1) / kTile;  // tiles per split
+  if (want > tiles / least) want = tiles / least;
   if (want < 1) want = 1;
   const int64_t per = (tiles + want - 1) / want;
   r.per = per * kTile;
@@ -210,13 +285,16 @@ RouteGradPlan plan(int64_t T, int D, int E, int dev) {
   return r;
 }
 
-template <typename TI, typename TO, int ET>
-int launch(const RouteGradParams& p, const RouteGradPlan& r, hipStream_t s) {
-  const size_t lds = ((size_t)p.E * kSlabStride + kTile * (ET * 16 + 2) + 2 * (size_t)kTile * p.k) *
-                     sizeof(float);
-  allow_dynamic_lds(route_grad_kernel<TI, TO, ET>, lds);
-  hipLaunchKernelGGL((route_grad_kernel<TI, TO, ET>), dim3(r.slabs, r.splits), dim3(kThreads), lds,
-                     s, p);
+template <typename TI, typename TO, int ET, int K, bool WHOLE>
+int launch(const RouteGradParams& a, const RouteGradPlan& r, hipStream_t s) {
+  RouteGradParams p = a;
+  const size_t fixed = (size_t)p.E * kSlabStride * sizeof(float);
+  const size_t table = Slopes<ET>::words(p.k) * sizeof(float);
+  p.two = fixed + 2 * table <= 160 * 1024;  // one table where nearly every expert is selected
+  const size_t lds = fixed + (p.two ? 2 : 1) * table;
+  allow_dynamic_lds(route_grad_kernel<TI, TO, ET, K, WHOLE>, lds);
+  hipLaunchKernelGGL((route_grad_kernel<TI, TO, ET, K, WHOLE>), dim3(r.slabs, r.splits),
+                     dim3(kThreads), lds, s, p);
   if (hipGetLastError() != hipSuccess) return SWIMBA_EHIP;
   if (r.splits > 1) {
     const int64_t n = (int64_t)p.D * p.E;
@@ -226,22 +304,34 @@ int launch(const RouteGradParams& p, const RouteGradPlan& r, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
+template <typename TI, typename TO, int ET>
+int launch_slots(const RouteGradParams& p, const RouteGradPlan& r, hipStream_t s) {
+  const bool whole = p.D % 4 == 0;
+  if (p.k == 2)
+    return whole ? launch<TI, TO, ET, 2, true>(p, r, s) : launch<TI, TO, ET, 2, false>(p, r, s);
+  return whole ? launch<TI, TO, ET, 0, true>(p, r, s) : launch<TI, TO, ET, 0, false>(p, r, s);
+}
+
 template <typename TI, typename TO>
 int launch_types(const RouteGradParams& p, const RouteGradPlan& r, hipStream_t s) {
-  if (p.E <= 16) return launch<TI, TO, 1>(p, r, s);
-  if (p.E <= 32) return launch<TI, TO, 2>(p, r, s);
-  return launch<TI, TO, 4>(p, r, s);
+  if (p.E <= 16) return launch_slots<TI, TO, 1>(p, r, s);
+  if (p.E <= 32) return launch_slots<TI, TO, 2>(p, r, s);
+  return launch_slots<TI, TO, 4>(p, r, s);
 }
 
 }  // namespace
 
-size_t route_backward_bytes(int64_t T, int D, int E, int dev) { return plan(T, D, E, dev).bytes; }
+size_t route_backward_bytes(int64_t T, int D, int E, int dev) {
+  // whatever the types are
+  const size_t a = plan(T, D, E, 2, dev).bytes, b = plan(T, D, E, 4, dev).bytes;
+  return a > b ? a : b;
+}
 
 int launch_route_backward(const void* x, swimba_dtype xd, const float* Wr, const int32_t* idx,
                           const float* gate, const float* dgate, int64_t T, int D, int E, int k,
                           void* dx, swimba_dtype dxd, float* dWr, void* ws, int dev,
                           hipStream_t s) {
-  const RouteGradPlan r = plan(T, D, E, dev);
+  const RouteGradPlan r = plan(T, D, E, xd == SWIMBA_BF16 ? 2 : 4, dev);
   RouteGradParams p;
   p.x = x;
   p.Wr = Wr;

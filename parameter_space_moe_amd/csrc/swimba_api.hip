@@ -637,7 +637,7 @@ int swimba_combine_tokens_backward(const void* rows, swimba_dtype rows_dtype, co
       !aligned_as(drows, drows_dtype))
     return SWIMBA_EINVAL;
   return launch_combine_tokens_backward(rows, rows_dtype, pos, gate, dy, dy_dtype, T, D, k, drows,
-                                        drows_dtype, dgate, stream);
+                                        drows_dtype, dgate, stream_device(stream), stream);
 }
 
 size_t swimba_route_backward_workspace_size(int64_t T, int D, int E) {

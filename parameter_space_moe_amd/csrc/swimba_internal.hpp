@@ -89,7 +89,7 @@ int launch_combine_tokens(const void* rows, swimba_dtype rd, const int32_t* pos,
 int launch_combine_tokens_backward(const void* rows, swimba_dtype rd, const int32_t* pos,
                                    const float* gate, const void* dy, swimba_dtype dyd, int64_t T,
                                    int D, int k, void* drows, swimba_dtype drd, float* dgate,
-                                   hipStream_t s);
+                                   int dev, hipStream_t s);
 size_t route_backward_bytes(int64_t T, int D, int E, int dev);
 int launch_route_backward(const void* x, swimba_dtype xd, const float* Wr, const int32_t* idx,
                           const float* gate, const float* dgate, int64_t T, int D, int E, int k,

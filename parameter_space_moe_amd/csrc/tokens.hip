@@ -158,57 +158,103 @@ struct MoveParams {
   int D, k, ppr;     // row width, slots, packs per row
 };
 
-// f(token, first element) for the packs of this thread.  Work is laid out over
-// packs, not rows, so that every row width fills the workgroups alike.
-template <typename F>
-__device__ __forceinline__ void each_pack(const MoveParams& p, F f) {
+// The packs of a thread: token and first element of each, `on` where there is
+// one.  Work is laid out over packs, not rows, so that every row width fills
+// the workgroups alike; all of a thread's packs are loaded before any is used
+// (the loads of one pack after the other left the copy out at 3.6 TB/s).
+struct Packs {
+  int64_t t[kMovePacks];
+  int c[kMovePacks];
+  bool on[kMovePacks];
+};
+
+__device__ __forceinline__ Packs packs_of(const MoveParams& p) {
   const int64_t base = (int64_t)blockIdx.x * (kMoveThreads * kMovePacks);
   const int64_t t0 = base / p.ppr;  // uniform
   const uint32_t r0 = (uint32_t)(base - t0 * p.ppr);
+  Packs m;
 #pragma unroll
   for (int i = 0; i < kMovePacks; ++i) {
     const uint32_t r = r0 + i * kMoveThreads + threadIdx.x;
     const uint32_t dt = r / (uint32_t)p.ppr;
-    const int64_t t = t0 + dt;
-    if (t < p.T) f(t, (int)(r - dt * p.ppr) * kPack);
+    m.t[i] = t0 + dt;
+    m.c[i] = (int)(r - dt * p.ppr) * kPack;
+    m.on[i] = m.t[i] < p.T;
+    if (!m.on[i]) {  // reads then take the first row
+      m.t[i] = 0;
+      m.c[i] = 0;
+    }
   }
+  return m;
 }
 
-template <typename T>
+// The pack at p of a row with n elements left; WHOLE rows are whole packs.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ Pack<T> row_pack(const T* p, int n) {
+  return load_pack(p, WHOLE ? kPack : n);
+}
+
+template <typename T, bool WHOLE>
 __global__ __launch_bounds__(kMoveThreads) void dispatch_kernel(MoveParams p) {
   const T* x = static_cast<const T*>(p.src);
   T* rows = static_cast<T*>(p.dst);
   const int64_t n = p.T * p.k;
-  each_pack(p, [&](int64_t t, int c) {
-    const Pack<T> v = load_pack(x + t * p.D + c, p.D - c);
-    for (int j = 0; j < p.k; ++j) {
-      const int32_t at = p.pos[t * p.k + j];
-      if (is_row(at, n)) store_pack(rows + (int64_t)at * p.D + c, v, p.D - c);
-    }
-  });
+  const Packs m = packs_of(p);
+  Pack<T> v[kMovePacks];
+#pragma unroll
+  for (int i = 0; i < kMovePacks; ++i)
+    v[i] = row_pack<WHOLE>(x + m.t[i] * p.D + m.c[i], p.D - m.c[i]);
+  for (int j = 0; j < p.k; ++j) {
+    int32_t at[kMovePacks];
+#pragma unroll
+    for (int i = 0; i < kMovePacks; ++i) at[i] = p.pos[m.t[i] * p.k + j];
+#pragma unroll
+    for (int i = 0; i < kMovePacks; ++i)
+      if (m.on[i] && is_row(at[i], n))
+        store_pack(rows + (int64_t)at[i] * p.D + m.c[i], v[i], WHOLE ? kPack : p.D - m.c[i]);
+  }
 }
 
 // y_t = sum_j gate_j rows[pos_j], in slot order in fp32 (gate null: ones).
-template <typename TI, typename TO>
+// A slot without a row reads row 0 and leaves it out.
+template <typename TI, typename TO, bool WHOLE>
 __global__ __launch_bounds__(kMoveThreads) void combine_kernel(MoveParams p) {
   const TI* rows = static_cast<const TI*>(p.src);
   TO* y = static_cast<TO*>(p.dst);
   const int64_t n = p.T * p.k;
-  each_pack(p, [&](int64_t t, int c) {
-    float acc[kPack] = {};
-    for (int j = 0; j < p.k; ++j) {
-      const int32_t at = p.pos[t * p.k + j];
-      if (!is_row(at, n)) continue;
-      const float g = p.gate != nullptr ? p.gate[t * p.k + j] : 1.f;
-      const Pack<TI> v = load_pack(rows + (int64_t)at * p.D + c, p.D - c);
+  const Packs m = packs_of(p);
+  float acc[kMovePacks][kPack] = {};
+  for (int j = 0; j < p.k; ++j) {
+    int32_t at[kMovePacks];
+    float g[kMovePacks];
+    Pack<TI> v[kMovePacks];
 #pragma unroll
-      for (int i = 0; i < kPack; ++i) acc[i] = fmaf(g, to_f32(v.v[i]), acc[i]);
+    for (int i = 0; i < kMovePacks; ++i) {
+      at[i] = p.pos[m.t[i] * p.k + j];
+      g[i] = p.gate != nullptr ? p.gate[m.t[i] * p.k + j] : 1.f;
     }
+#pragma unroll
+    for (int i = 0; i < kMovePacks; ++i)
+      v[i] = row_pack<WHOLE>(rows + (is_row(at[i], n) ? (int64_t)at[i] * p.D : 0) + m.c[i],
+                             p.D - m.c[i]);
+#pragma unroll
+    for (int i = 0; i < kMovePacks; ++i) {
+      const bool in = is_row(at[i], n);
+#pragma unroll
+      for (int e = 0; e < kPack; ++e) {
+        const float s = fmaf(g[i], to_f32(v[i].v[e]), acc[i][e]);
+        acc[i][e] = in ? s : acc[i][e];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kMovePacks; ++i) {
     Pack<TO> o;
 #pragma unroll
-    for (int i = 0; i < kPack; ++i) o.v[i] = from_f32<TO>(acc[i]);
-    store_pack(y + t * p.D + c, o, p.D - c);
-  });
+    for (int e = 0; e < kPack; ++e) o.v[e] = from_f32<TO>(acc[i][e]);
+    if (m.on[i])
+      store_pack(y + m.t[i] * p.D + m.c[i], o, WHOLE ? kPack : p.D - m.c[i]);
+  }
 }
 
 struct CombineGradParams {
@@ -221,44 +267,77 @@ struct CombineGradParams {
   int D, k;
 };
 
-// drows[pos_j] = gate_j dy_t and dgate_j = <dy_t, rows[pos_j]>: a workgroup of
-// WAVES waves per token and slot pass, sums across its threads.
-template <typename TI, typename TY, typename TO, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void combine_grad_kernel(CombineGradParams p) {
-  __shared__ float part[WAVES];
-  const int64_t t = blockIdx.x;
+// drows[pos_j] = gate_j dy_t and dgate_j = <dy_t, rows[pos_j]>, two slots at a
+// time: a token per wave (PER = 1), or per workgroup of four where the tokens
+// alone would leave most of the device idle (PER = 4).
+template <typename TI, typename TY, typename TO, int PER, bool WHOLE>
+__global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradParams p) {
+  __shared__ float part[4][2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = PER == 4 ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+  if (t >= p.T) return;  // whole waves, and no barrier follows where PER is 1
   const TY* dy = static_cast<const TY*>(p.dy) + t * p.D;
+  const TI* rows = static_cast<const TI*>(p.rows);
+  TO* drows = static_cast<TO*>(p.drows);
   const int64_t n = p.T * p.k;
-  for (int j = 0; j < p.k; ++j) {
-    const int32_t at = p.pos[t * p.k + j];  // uniform
-    float s = 0.f;
-    if (is_row(at, n)) {
-      const float g = p.gate[t * p.k + j];
-      const TI* row = static_cast<const TI*>(p.rows) + (int64_t)at * p.D;
-      TO* drow = static_cast<TO*>(p.drows) + (int64_t)at * p.D;
-      for (int c = threadIdx.x * kPack; c < p.D; c += WAVES * 64 * kPack) {
-        const Pack<TY> d = load_pack(dy + c, p.D - c);
-        const Pack<TI> r = load_pack(row + c, p.D - c);
-        Pack<TO> o;
+  const int first = (PER == 4 ? threadIdx.x : lane) * kPack;
+  constexpr int kStride = PER * 64 * kPack;
+  for (int j0 = 0; j0 < p.k; j0 += 2) {
+    bool in[2];
+    float g[2], s[2] = {0.f, 0.f};
+    int64_t row[2];
 #pragma unroll
-        for (int i = 0; i < kPack; ++i) {
-          const float v = to_f32(d.v[i]);
-          s = fmaf(v, to_f32(r.v[i]), s);
-          o.v[i] = from_f32<TO>(g * v);
-        }
-        store_pack(drow + c, o, p.D - c);
+    for (int j = 0; j < 2; ++j) {
+      const int32_t at = j0 + j < p.k ? uniform(p.pos[t * p.k + j0 + j]) : -1;
+      in[j] = is_row(at, n);
+      row[j] = in[j] ? (int64_t)at * p.D : 0;
+      g[j] = in[j] ? p.gate[t * p.k + j0 + j] : 0.f;
+    }
+    auto pass = [&](auto* dst, int j, const Pack<TY>& d, const Pack<TI>& r, int c) {
+      Pack<TO> o;
+#pragma unroll
+      for (int i = 0; i < kPack; ++i) {
+        const float v = to_f32(d.v[i]);
+        s[j] = fmaf(v, to_f32(r.v[i]), s[j]);
+        o.v[i] = from_f32<TO>(g[j] * v);
+      }
+      store_pack(dst + row[j] + c, o, WHOLE ? kPack : p.D - c);
+    };
+    if (in[0] && in[1]) {
+#pragma unroll 2
+      for (int c = first; c < p.D; c += kStride) {
+        const Pack<TY> d = row_pack<WHOLE>(dy + c, p.D - c);
+        const Pack<TI> a = row_pack<WHOLE>(rows + row[0] + c, p.D - c);
+        const Pack<TI> b = row_pack<WHOLE>(rows + row[1] + c, p.D - c);
+        pass(drows, 0, d, a, c);
+        pass(drows, 1, d, b, c);
+      }
+    } else if (in[0] || in[1]) {
+      const int j = in[0] ? 0 : 1;
+      for (int c = first; c < p.D; c += kStride) {
+        const Pack<TY> d = row_pack<WHOLE>(dy + c, p.D - c);
+        const Pack<TI> a = row_pack<WHOLE>(rows + row[j] + c, p.D - c);
+        if (j == 0) pass(drows, 0, d, a, c);
+        else pass(drows, 1, d, a, c);
       }
     }
-    s = wave_sum64(s);
-    if (WAVES > 1) {
-      if (lane == 0) part[wave] = s;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) s[j] = wave_sum64(s[j]);
+    if (PER == 4) {
+      if (lane == 0) {
+        part[wave][0] = s[0];
+        part[wave][1] = s[1];
+      }
       __syncthreads();
-      s = 0.f;
-      for (int w = 0; w < WAVES; ++w) s += part[w];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        s[j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
       __syncthreads();
     }
-    if (threadIdx.x == 0) p.dgate[t * p.k + j] = s;
+    if ((PER == 4 ? (int)threadIdx.x : lane) == 0) {
+      p.dgate[t * p.k + j0] = s[0];
+      if (j0 + 1 < p.k) p.dgate[t * p.k + j0 + 1] = s[1];
+    }
   }
 }
 
@@ -288,9 +367,37 @@ bool move_grid(const MoveParams& p, dim3* grid) {
 }
 
 template <typename TI, typename TY, typename TO>
-int launch_combine_grad(const CombineGradParams& p, hipStream_t s) {
+int launch_combine_grad(const CombineGradParams& p, int dev, hipStream_t s) {
   if (p.T > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
-  hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 4>), dim3((unsigned)p.T), dim3(256), 0, s, p);
+  const bool few = p.T < 16LL * device_cus(dev);  // waves for every SIMD four times over
+  const dim3 grid((unsigned)(few ? p.T : (p.T + 3) / 4)), th(256);
+  const bool whole = p.D % kPack == 0;
+  if (few && whole)
+    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 4, true>), grid, th, 0, s, p);
+  else if (few)
+    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 4, false>), grid, th, 0, s, p);
+  else if (whole)
+    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 1, true>), grid, th, 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 1, false>), grid, th, 0, s, p);
+  return checked();
+}
+
+template <typename T>
+int launch_dispatch(const MoveParams& p, dim3 grid, hipStream_t s) {
+  if (p.D % kPack == 0)
+    hipLaunchKernelGGL((dispatch_kernel<T, true>), grid, dim3(kMoveThreads), 0, s, p);
+  else
+    hipLaunchKernelGGL((dispatch_kernel<T, false>), grid, dim3(kMoveThreads), 0, s, p);
+  return checked();
+}
+
+template <typename TI, typename TO>
+int launch_combine(const MoveParams& p, dim3 grid, hipStream_t s) {
+  if (p.D % kPack == 0)
+    hipLaunchKernelGGL((combine_kernel<TI, TO, true>), grid, dim3(kMoveThreads), 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_kernel<TI, TO, false>), grid, dim3(kMoveThreads), 0, s, p);
   return checked();
 }
 
@@ -328,11 +435,7 @@ int launch_dispatch_tokens(const void* x, swimba_dtype xd, const int32_t* pos, i
   const MoveParams p = move_params(x, rows, pos, nullptr, T, D, k);
   dim3 grid;
   if (!move_grid(p, &grid)) return SWIMBA_EUNSUPPORTED;
-  if (xd == SWIMBA_BF16)
-    hipLaunchKernelGGL((dispatch_kernel<bf16_t>), grid, dim3(kMoveThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL((dispatch_kernel<float>), grid, dim3(kMoveThreads), 0, s, p);
-  return checked();
+  return xd == SWIMBA_BF16 ? launch_dispatch<bf16_t>(p, grid, s) : launch_dispatch<float>(p, grid, s);
 }
 
 int launch_combine_tokens(const void* rows, swimba_dtype rd, const int32_t* pos, const float* gate,
@@ -340,22 +443,16 @@ int launch_combine_tokens(const void* rows, swimba_dtype rd, const int32_t* pos,
   const MoveParams p = move_params(rows, y, pos, gate, T, D, k);
   dim3 grid;
   if (!move_grid(p, &grid)) return SWIMBA_EUNSUPPORTED;
-  const dim3 th(kMoveThreads);
-  if (rd == SWIMBA_BF16 && yd == SWIMBA_BF16)
-    hipLaunchKernelGGL((combine_kernel<bf16_t, bf16_t>), grid, th, 0, s, p);
-  else if (rd == SWIMBA_BF16)
-    hipLaunchKernelGGL((combine_kernel<bf16_t, float>), grid, th, 0, s, p);
-  else if (yd == SWIMBA_BF16)
-    hipLaunchKernelGGL((combine_kernel<float, bf16_t>), grid, th, 0, s, p);
-  else
-    hipLaunchKernelGGL((combine_kernel<float, float>), grid, th, 0, s, p);
-  return checked();
+  const bool r = rd == SWIMBA_BF16, o = yd == SWIMBA_BF16;
+  if (r && o) return launch_combine<bf16_t, bf16_t>(p, grid, s);
+  if (r) return launch_combine<bf16_t, float>(p, grid, s);
+  return o ? launch_combine<float, bf16_t>(p, grid, s) : launch_combine<float, float>(p, grid, s);
 }
 
 int launch_combine_tokens_backward(const void* rows, swimba_dtype rd, const int32_t* pos,
                                    const float* gate, const void* dy, swimba_dtype dyd, int64_t T,
                                    int D, int k, void* drows, swimba_dtype drd, float* dgate,
-                                   hipStream_t s) {
+                                   int dev, hipStream_t s) {
   CombineGradParams p;
   p.rows = rows;
   p.dy = dy;
@@ -367,14 +464,14 @@ int launch_combine_tokens_backward(const void* rows, swimba_dtype rd, const int3
   p.D = D;
   p.k = k;
   const bool r = rd == SWIMBA_BF16, y = dyd == SWIMBA_BF16, o = drd == SWIMBA_BF16;
-  if (r && y && o) return launch_combine_grad<bf16_t, bf16_t, bf16_t>(p, s);
-  if (r && y) return launch_combine_grad<bf16_t, bf16_t, float>(p, s);
-  if (r && o) return launch_combine_grad<bf16_t, float, bf16_t>(p, s);
-  if (r) return launch_combine_grad<bf16_t, float, float>(p, s);
-  if (y && o) return launch_combine_grad<float, bf16_t, bf16_t>(p, s);
-  if (y) return launch_combine_grad<float, bf16_t, float>(p, s);
-  if (o) return launch_combine_grad<float, float, bf16_t>(p, s);
-  return launch_combine_grad<float, float, float>(p, s);
+  if (r && y && o) return launch_combine_grad<bf16_t, bf16_t, bf16_t>(p, dev, s);
+  if (r && y) return launch_combine_grad<bf16_t, bf16_t, float>(p, dev, s);
+  if (r && o) return launch_combine_grad<bf16_t, float, bf16_t>(p, dev, s);
+  if (r) return launch_combine_grad<bf16_t, float, float>(p, dev, s);
+  if (y && o) return launch_combine_grad<float, bf16_t, bf16_t>(p, dev, s);
+  if (y) return launch_combine_grad<float, bf16_t, float>(p, dev, s);
+  if (o) return launch_combine_grad<float, float, bf16_t>(p, dev, s);
+  return launch_combine_grad<float, float, float>(p, dev, s);
 }
 
 }  // namespace swimba
