@@ -35,15 +35,27 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(AttnParams p) {
 }
 
 // out[b, h] = <a, b> over a state, in 64 bits.
-__global__ __launch_bounds__(256) void attn_dot_kernel(const float* a, const float* b, double* out,
-                                                       int64_t n) {
-  __shared__ double part[256];
+constexpr int kDotThreads = 1024;
+__global__ __launch_bounds__(kDotThreads) void attn_dot_kernel(const float* a, const float* b,
+                                                               double* out, int64_t n) {
+  __shared__ double part[kDotThreads];
   const int64_t at = (int64_t)blockIdx.x * n;
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 256) s += (double)a[at + i] * (double)b[at + i];
+  for (int64_t i = threadIdx.x; i < n; i += 8 * kDotThreads) {
+    float x[8], y[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t e = i + u * kDotThreads;
+      x[u] = a[at + (e < n ? e : 0)];
+      y[u] = e < n ? b[at + e] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + u * kDotThreads < n) s += (double)x[u] * (double)y[u];
+  }
   part[threadIdx.x] = s;
   __syncthreads();
-  for (int w = 128; w > 0; w >>= 1) {
+  for (int w = kDotThreads / 2; w > 0; w >>= 1) {
     if ((int)threadIdx.x < w) part[threadIdx.x] += part[threadIdx.x + w];
     __syncthreads();
   }
@@ -297,13 +309,12 @@ WalkPlan plan_walk(bool f32, int B, int L, int H, int share, int Kd, int Cd, int
   const int64_t nc = (L + kChunk - 1) / kChunk;
   const int64_t base = (int64_t)B * (H / share) * ((units + w.waves - 1) / w.waves);
   // as many workgroups as the device holds at once, from the independent walks
-  // or from segments of them (whose first states cost a pass over k and v) of
-  // four chunks or more
+  // or from segments of them (whose first states cost a pass over k and v)
   const int64_t hold = (int64_t)device_cus(dev) *
                        (f32 ? attn_resident<float>(Kd, w.waves) : attn_resident<bf16_t>(Kd, w.waves));
   int64_t want = base > 0 ? hold / base : 1;
-  if (want > nc / 4) want = nc / 4;
-  if (want < 2) want = 1;
+  if (want > nc) want = nc;
+  if (want < 2 || nc < 4) want = 1;
   w.seg_chunks = (int)((nc + want - 1) / want);
   if (w.seg_chunks < 1) w.seg_chunks = 1;
   w.nseg = nc > 0 ? (int)((nc + w.seg_chunks - 1) / w.seg_chunks) : 1;
@@ -532,7 +543,7 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   d.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
   if (g->dh_final != nullptr) {
     double* x = at<double>(ws, r.off_x);
-    hipLaunchKernelGGL(attn_dot_kernel, dim3(a->B * a->H), dim3(256), 0, s, end, g->dh_final, x,
+    hipLaunchKernelGGL(attn_dot_kernel, dim3(a->B * a->H), dim3(kDotThreads), 0, s, end, g->dh_final, x,
                        (int64_t)a->N * a->P);
     d.x_end = x;
   }

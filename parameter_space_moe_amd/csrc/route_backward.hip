@@ -95,8 +95,8 @@ struct Slopes {
         any(expert + kTile * k) {}
 };
 
-// ET: expert tiles of 16; K: slots per token (0: any number, from p.k); WHOLE:
-// rows are whole groups of four channels.
+// ET: expert tiles of 16; K: most slots per token that are held in registers
+// (0: any number of slots); WHOLE: rows are whole groups of four channels.
 template <typename TI, typename TO, int ET, int K, bool WHOLE>
 __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void route_grad_kernel(RouteGradParams p) {
   using Table = Slopes<ET>;
@@ -114,9 +114,19 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
   TO* dx = static_cast<TO*>(p.dx);
 
   const int slab = p.D - d0 < kSlab ? p.D - d0 : kSlab;
-  for (int i = threadIdx.x; i < slab * p.E; i += kThreads) {
-    const int r = i / p.E;
-    sW[(i - r * p.E) * kSlabStride + r] = p.Wr[(int64_t)d0 * p.E + i];
+  // Wr's rows of the slab lie one behind the other; eight loads at a time
+  for (int i0 = threadIdx.x; i0 < slab * p.E; i0 += 8 * kThreads) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * kThreads;
+      v[u] = p.Wr[(int64_t)d0 * p.E + (i < slab * p.E ? i : 0)];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * kThreads, r = i / p.E;
+      if (i < slab * p.E) sW[(i - r * p.E) * kSlabStride + r] = v[u];
+    }
   }
 
   f4 acc[ET][4];
@@ -138,58 +148,69 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
   };
   if (tb < te) fetch(tb);  // without tokens x may be null
 
-  int buf = 0;
-  for (int64_t t0 = tb; t0 < te; t0 += kTile, buf ^= p.two) {
-    if (!p.two) __syncthreads();  // one table only: everyone is done with it
-    const int len = te - t0 < kTile ? (int)(te - t0) : kTile;
-    const Table tab(smem + p.E * kSlabStride + buf * Table::words(k), k);
-    // one wave after the other makes a tile's table: a lane per token
-    if (wave == (int)((t0 - tb) / kTile & 3)) {
-      float* row = tab.dense + lane * kDense;
-      for (int e = 0; e < ET * 16; ++e) row[e] = 0.f;
-      int32_t any = 0;
-      if (lane < len) {
-        const int64_t s = (t0 + lane) * k;
-        if constexpr (K > 0) {
-          float g[K], dg[K];
-          int32_t ex[K];
+  // A tile's table is made by one wave, a lane per token, each wave in its turn:
+  // from values loaded before the tile ahead of it is worked on.
+  constexpr int kHold = K > 0 ? K : 1;
+  float pg[kHold], pd[kHold];
+  int32_t pe[kHold];
+  auto values = [&](int64_t t0) {
+    if constexpr (K > 0) {
+      const int64_t t = t0 + lane, s = (t < te ? t : tb) * p.k;
 #pragma unroll
-          for (int j = 0; j < K; ++j) {
-            g[j] = p.gate[s + j];
-            dg[j] = p.dgate[s + j];
-            ex[j] = p.idx[s + j];
-          }
-          float mean = 0.f;
-#pragma unroll
-          for (int j = 0; j < K; ++j) mean = fmaf(g[j], dg[j], mean);
-#pragma unroll
-          for (int j = 0; j < K; ++j) {
-            const bool in = ex[j] >= 0 && ex[j] < p.E;
-            const float v = g[j] * (dg[j] - mean);
-            tab.slot[lane * K + j] = v;
-            tab.expert[lane * K + j] = in ? ex[j] : -1;
-            any |= in;
-            if (in) row[ex[j]] += v;  // an expert listed twice adds twice
-          }
-        } else {
-          float mean = 0.f;
-          for (int j = 0; j < k; ++j) mean = fmaf(p.gate[s + j], p.dgate[s + j], mean);
-          for (int j = 0; j < k; ++j) {
-            const int e = p.idx[s + j];
-            const bool in = e >= 0 && e < p.E;
-            const float v = p.gate[s + j] * (p.dgate[s + j] - mean);
-            tab.slot[lane * k + j] = v;
-            tab.expert[lane * k + j] = in ? e : -1;
-            any |= in;
-            if (in) row[e] += v;
-          }
-        }
+      for (int j = 0; j < K; ++j) {
+        const int64_t at = s + (j < p.k ? j : 0);
+        pg[j] = p.gate[at];
+        pd[j] = p.dgate[at];
+        pe[j] = p.idx[at];
       }
-      tab.any[lane] = any;
     }
-    // with two tables the one barrier per tile: the table of two tiles before, in
-    // this place, has been read by everyone who passed the last one
-    __syncthreads();
+  };
+  auto make = [&](int64_t t0, const Table& tab) {
+    float* row = tab.dense + lane * kDense;
+    for (int e = 0; e < ET * 16; ++e) row[e] = 0.f;
+    int32_t any = 0;
+    if (t0 + lane < te) {
+      float mean = 0.f;
+      if constexpr (K > 0) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (j < p.k) mean = fmaf(pg[j], pd[j], mean);
+      } else {
+        const int64_t s = (t0 + lane) * k;
+        for (int j = 0; j < k; ++j) mean = fmaf(p.gate[s + j], p.dgate[s + j], mean);
+      }
+      auto slot = [&](int j, float g, float dg, int e, bool has) {
+        const bool in = has && e >= 0 && e < p.E;
+        const float v = g * (dg - mean);
+        tab.slot[lane * k + j] = v;
+        tab.expert[lane * k + j] = in ? e : -1;
+        any |= in;
+        if (in) row[e] += v;  // an expert listed twice adds twice
+      };
+      if constexpr (K > 0) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) slot(j, pg[j], pd[j], pe[j], j < p.k);
+      } else {
+        const int64_t s = (t0 + lane) * k;
+        for (int j = 0; j < k; ++j) slot(j, p.gate[s + j], p.dgate[s + j], p.idx[s + j], true);
+      }
+    }
+    tab.any[lane] = any;
+  };
+  const Table tab0(smem + p.E * kSlabStride, k);
+  const Table tab1(smem + p.E * kSlabStride + (p.two ? Table::words(k) : 0), k);
+  if (wave == 0 && tb < te) {
+    values(tb);
+    make(tb, tab0);
+  }
+
+  for (int64_t t0 = tb; t0 < te; t0 += kTile) {
+    const int turn = (int)((t0 - tb) / kTile);
+    const int len = te - t0 < kTile ? (int)(te - t0) : kTile;
+    const Table& tab = turn & 1 ? tab1 : tab0;
+    const bool maker = wave == ((turn + 1) & 3) && t0 + kTile < te;
+    __syncthreads();  // this tile's table is made, the one before is done with
+    if (maker) values(t0 + kTile);
 #pragma unroll 1
     for (int hb = 0; hb < kTile; hb += 4 * kSteps) {
       if (hb >= len) break;
@@ -228,6 +249,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
         if (i & 1) __builtin_amdgcn_sched_barrier(0);
       }
     }
+    if (!p.two) __syncthreads();  // one table only: everyone has to be done with it
+    if (maker) make(t0 + kTile, turn & 1 ? tab0 : tab1);
   }
 
   // acc[e][j][i]: expert 16 e + 4 q + i, channel d + j
@@ -267,14 +290,17 @@ struct RouteGradPlan {
   size_t bytes = 0;
 };
 
-// Four workgroups per CU, splits of whole 64-token tiles, and no more of them
-// than keeps the partial sums (8 E bytes per channel and split, out and in) at
-// half the stream of x and dx.
+// As many workgroups as the device holds at once (by registers and LDS three
+// per CU up to 16 experts with bf16 x, two up to 32 and with fp32 x, one
+// beyond), splits of whole 64-token tiles, and no more of them than keeps the
+// partial sums (8 E bytes per channel and split, out and in) at half the stream
+// of x and dx.
 RouteGradPlan plan(int64_t T, int D, int E, int elem, int dev) {
   RouteGradPlan r;
   r.slabs = (D + kSlab - 1) / kSlab;
   const int64_t tiles = (T + kTile - 1) / kTile;
-  int64_t want = (4LL * device_cus(dev) + r.slabs - 1) / r.slabs;
+  const int per_cu = E > 32 ? 1 : (E > 16 || elem == 4 ? 2 : 3);
+  int64_t want = (int64_t)per_cu * device_cus(dev) / r.slabs;
   const int64_t least = (16LL * E / (2 * elem) + kTile - 1) / kTile;  // tiles per split
   if (want > tiles / least) want = tiles / least;
   if (want < 1) want = 1;
@@ -289,7 +315,7 @@ template <typename TI, typename TO, int ET, int K, bool WHOLE>
 int launch(const RouteGradParams& a, const RouteGradPlan& r, hipStream_t s) {
   RouteGradParams p = a;
   const size_t fixed = (size_t)p.E * kSlabStride * sizeof(float);
-  const size_t table = Slopes<ET>::words(p.k) * sizeof(float);
+  const size_t table = Slopes<ET>::words(K > 0 ? K : p.k) * sizeof(float);
   p.two = fixed + 2 * table <= 160 * 1024;  // one table where nearly every expert is selected
   const size_t lds = fixed + (p.two ? 2 : 1) * table;
   allow_dynamic_lds(route_grad_kernel<TI, TO, ET, K, WHOLE>, lds);
@@ -309,6 +335,8 @@ int launch_slots(const RouteGradParams& p, const RouteGradPlan& r, hipStream_t s
   const bool whole = p.D % 4 == 0;
   if (p.k == 2)
     return whole ? launch<TI, TO, ET, 2, true>(p, r, s) : launch<TI, TO, ET, 2, false>(p, r, s);
+  if (p.k <= 4)
+    return whole ? launch<TI, TO, ET, 4, true>(p, r, s) : launch<TI, TO, ET, 4, false>(p, r, s);
   return whole ? launch<TI, TO, ET, 0, true>(p, r, s) : launch<TI, TO, ET, 0, false>(p, r, s);
 }
 

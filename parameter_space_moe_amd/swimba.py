@@ -689,11 +689,23 @@ class PreparedStep:
         return self.y
 
 
+def _fits(t, name, shape, dtype, dev):
+    """_need for calls where latency counts: one expression when all is well."""
+    if not (isinstance(t, torch.Tensor) and t.device == dev and t.shape == shape
+            and (dtype is None or t.dtype == dtype) and t.is_contiguous()):
+        _need(t, name, shape, dtype, dev)
+
+
+def _current(dev):
+    """The handle of `dev`'s current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _new(t, name, shape, dtype, dev):
     """The caller's output buffer, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, shape, dtype, dev)
+    _fits(t, name, shape, dtype, dev)
     return t
 
 
@@ -718,7 +730,7 @@ def _placed(fn):
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            return fn(first, *args, **kw)  # refused by its own checks
+            raise ValueError("%s: the first argument must be a device tensor" % fn.__name__)
         dev = first.device
         if stream is not None:
             if stream.device != dev:
@@ -752,17 +764,18 @@ def sort_tokens(idx, E, order=None, pos=None, offsets=None, workspace=None):
     lib = load()
     ws, wp, wn = _workspace(workspace, lib.swimba_sort_tokens_workspace_size(T, E, k), dev)
     rc = lib.swimba_sort_tokens(_ptr(idx), T, E, k, _ptr(order), _ptr(pos), _ptr(offsets), wp, wn,
-                                _stream(None))
+                                _current(dev))
     _check("swimba_sort_tokens", rc)
     return order, pos, offsets
 
 
-def _pos_shape(pos, dev=None):
-    _need(pos, "pos", None, torch.int32, dev)
-    if pos.dim() < 1 or pos.shape[-1] < 1:
-        raise ValueError("pos must be [..., k]")
-    k = pos.shape[-1]
-    return tuple(pos.shape[:-1]), pos.numel() // k, k
+def _pos_shape(pos, dev):
+    if not isinstance(pos, torch.Tensor) or pos.dim() < 1 or pos.shape[-1] < 1:
+        raise ValueError("pos must be a tensor [..., k]")
+    shape = pos.shape
+    _fits(pos, "pos", shape, torch.int32, dev)
+    k = shape[-1]
+    return tuple(shape[:-1]), pos.numel() // k, k
 
 
 @_placed
@@ -770,13 +783,13 @@ def dispatch_tokens(x, pos, rows=None):
     """rows[pos[t, j]] = x[t] (include/swimba.h: swimba_dispatch_tokens).  x
     [..., D], pos [..., k] from sort_tokens; returns rows [T*k, D].  Rows that no
     slot has are left as they were (unwritten memory where `rows` is not given)."""
-    _need(x, "x")
-    lead, T, k = _pos_shape(pos, x.device)
+    dev = x.device
+    lead, T, k = _pos_shape(pos, dev)
     D = x.shape[-1] if x.dim() else 0
-    _need(x, "x", lead + (D,))
-    rows = _new(rows, "rows", (T * k, D), x.dtype, x.device)
+    _fits(x, "x", lead + (D,), None, dev)
+    rows = _new(rows, "rows", (T * k, D), x.dtype, dev)
     rc = load().swimba_dispatch_tokens(_ptr(x), _dt(x), _ptr(pos), T, D, k, _ptr(rows),
-                                       _stream(None))
+                                       _current(dev))
     _check("swimba_dispatch_tokens", rc)
     return rows
 
@@ -786,17 +799,18 @@ def combine_tokens(rows, pos, gate=None, y=None, y_dtype=None):
     """y[t] = sum_j gate[t, j] rows[pos[t, j]] (include/swimba.h:
     swimba_combine_tokens).  rows [T*k, D], pos and gate [..., k]; gate None: ones.
     Returns y [..., D]."""
-    _need(rows, "rows")
-    lead, T, k = _pos_shape(pos, rows.device)
+    dev = rows.device
+    lead, T, k = _pos_shape(pos, dev)
     D = rows.shape[-1] if rows.dim() else 0
-    _need(rows, "rows", (T * k, D))
+    _fits(rows, "rows", (T * k, D), None, dev)
     if gate is not None:
-        _need(gate, "gate", lead + (k,), torch.float32, rows.device)
+        _fits(gate, "gate", lead + (k,), torch.float32, dev)
     if y is None:
-        y = torch.empty(lead + (D,), dtype=y_dtype or rows.dtype, device=rows.device)
-    _need(y, "y", lead + (D,), None, rows.device)
+        y = torch.empty(lead + (D,), dtype=y_dtype or rows.dtype, device=dev)
+    else:
+        _fits(y, "y", lead + (D,), None, dev)
     rc = load().swimba_combine_tokens(_ptr(rows), _dt(rows), _ptr(pos), _ptr(gate), T, D, k,
-                                      _ptr(y), _dt(y), _stream(None))
+                                      _ptr(y), _dt(y), _current(dev))
     _check("swimba_combine_tokens", rc)
     return y
 
@@ -815,20 +829,19 @@ def combine_tokens_backward(rows, pos, gate, dy, drows=None, dgate=None, grad_dt
     swimba_combine_tokens_backward).  Returns (drows [T*k, D], by default of rows'
     dtype, and dgate [..., k] f32).  Rows of drows that no slot has are left as
     they were (unwritten memory where it is not given)."""
-    _need(rows, "rows")
     dev = rows.device
     lead, T, k = _pos_shape(pos, dev)
     D = rows.shape[-1] if rows.dim() else 0
-    _need(rows, "rows", (T * k, D))
-    _need(gate, "gate", lead + (k,), torch.float32, dev)
-    _need(dy, "dy", lead + (D,), None, dev)
+    _fits(rows, "rows", (T * k, D), None, dev)
+    _fits(gate, "gate", lead + (k,), torch.float32, dev)
+    _fits(dy, "dy", lead + (D,), None, dev)
     if drows is None:
         drows = torch.empty((T * k, D), dtype=grad_dtype or rows.dtype, device=dev)
-    _need(drows, "drows", (T * k, D), None, dev)
+    _fits(drows, "drows", (T * k, D), None, dev)
     dgate = _new(dgate, "dgate", lead + (k,), torch.float32, dev)
     rc = load().swimba_combine_tokens_backward(
         _ptr(rows), _dt(rows), _ptr(pos), _ptr(gate), _ptr(dy), _dt(dy), T, D, k, _ptr(drows),
-        _dt(drows), _ptr(dgate), _stream(None))
+        _dt(drows), _ptr(dgate), _current(dev))
     _check("swimba_combine_tokens_backward", rc)
     return drows, dgate
 
@@ -857,7 +870,7 @@ def route_backward(x, Wr, idx, gate, dgate, dx=None, dWr=None, grad_dtype=torch.
     ws, wp, wn = _workspace(workspace, need, dev)
     rc = lib.swimba_route_backward(_ptr(x), _dt(x), _ptr(Wr), _ptr(idx), _ptr(gate), _ptr(dgate),
                                    T, D, E, k, _ptr(dx), _dt(dx), _ptr(dWr), wp, wn,
-                                   _stream(None))
+                                   _current(dev))
     _check("swimba_route_backward", rc)
     return dx, dWr
 
@@ -878,17 +891,17 @@ def _linear_attention_args(q, k, v, log_decay, h0, y, h_final, need_y=True):
         raise ValueError("q must be [B, L, G, N]")
     G, N = q.shape[2:]
     _need(q, "q", (B, L, G, N))
-    _need(k, "k", (B, L, G, N), v.dtype, dev)
+    _fits(k, "k", (B, L, G, N), v.dtype, dev)
     a = LinearAttentionArgs()
     a.decay_form = DECAY_HEAD if log_decay.dim() == 1 else DECAY_TOKEN
     _need(log_decay, "log_decay", (H,) if a.decay_form == DECAY_HEAD else (B, L, H),
           torch.float32, dev)
     if h0 is not None:
-        _need(h0, "h0", (B, H, N, P), torch.float32, dev)
+        _fits(h0, "h0", (B, H, N, P), torch.float32, dev)
     if need_y:
-        _need(y, "y", (B, L, H, P), None, dev)
+        _fits(y, "y", (B, L, H, P), None, dev)
     if h_final is not None:
-        _need(h_final, "h_final", (B, H, N, P), torch.float32, dev)
+        _fits(h_final, "h_final", (B, H, N, P), torch.float32, dev)
     a.B, a.L, a.H, a.G, a.N, a.P = B, L, H, G, N, P
     a.in_dtype = _dt(v)
     a.y_dtype = _dt(y) if y is not None else a.in_dtype
@@ -913,7 +926,7 @@ def linear_attention(q, k, v, log_decay, h0=None, y=None, h_final=None, y_dtype=
     lib, ref = load(), ctypes.byref(a)
     need = lib.swimba_linear_attention_workspace_size(ref) if workspace is None else 0
     ws, wp, wn = _workspace(workspace, need, v.device)
-    _check("swimba_linear_attention", lib.swimba_linear_attention(ref, wp, wn, _stream(None)))
+    _check("swimba_linear_attention", lib.swimba_linear_attention(ref, wp, wn, _current(v.device)))
     return y, h_final
 
 
@@ -954,7 +967,7 @@ def linear_attention_backward(q, k, v, log_decay, dy, h0=None, dh_final=None, wa
     need = lib.swimba_linear_attention_backward_workspace_size(ref) if workspace is None else 0
     ws, wp, wn = _workspace(workspace, need, dev)
     _check("swimba_linear_attention_backward",
-           lib.swimba_linear_attention_backward(ref, wp, wn, _stream(None)))
+           lib.swimba_linear_attention_backward(ref, wp, wn, _current(dev)))
     return res
 
 
@@ -969,15 +982,15 @@ def _linear_attention_step_args(q, k, v, log_decay, state, state_out, y, y_dtype
         raise ValueError("q must be [B, G, N]")
     G, N = q.shape[1:]
     _need(q, "q", (B, G, N))
-    _need(k, "k", (B, G, N), v.dtype, dev)
+    _fits(k, "k", (B, G, N), v.dtype, dev)
     form = DECAY_HEAD if log_decay.dim() == 1 else DECAY_TOKEN
     _need(log_decay, "log_decay", (H,) if form == DECAY_HEAD else (B, H), torch.float32, dev)
-    _need(state, "state", (B, H, N, P), torch.float32, dev)
+    _fits(state, "state", (B, H, N, P), torch.float32, dev)
     if state_out is not None:
-        _need(state_out, "state_out", (B, H, N, P), torch.float32, dev)
+        _fits(state_out, "state_out", (B, H, N, P), torch.float32, dev)
     if y is None:
         y = torch.empty((B, H, P), dtype=y_dtype or v.dtype, device=dev)
-    _need(y, "y", (B, H, P), None, dev)
+    _fits(y, "y", (B, H, P), None, dev)
     a = LinearAttentionStepArgs()
     a.B, a.H, a.G, a.N, a.P = B, H, G, N, P
     a.in_dtype, a.y_dtype, a.decay_form = _dt(v), _dt(y), form
@@ -994,7 +1007,7 @@ def linear_attention_step(q, k, v, log_decay, state, state_out=None, y=None, y_d
     Returns y [B,H,P]."""
     a, y = _linear_attention_step_args(q, k, v, log_decay, state, state_out, y, y_dtype)
     _check("swimba_linear_attention_step",
-           load().swimba_linear_attention_step(ctypes.byref(a), _stream(None)))
+           load().swimba_linear_attention_step(ctypes.byref(a), _current(v.device)))
     return y
 
 
