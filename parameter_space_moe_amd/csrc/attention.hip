@@ -294,6 +294,28 @@ int copy_or_zero(const float* in, float* out, int64_t n, hipStream_t s) {
   return checked();
 }
 
+// The walks load whole packs inside a tensor.  One of fewer elements than a pack
+// (a token of a few features) is first copied to a slot of the workspace.
+constexpr size_t kTinySlot = 256;
+template <typename T>
+__global__ __launch_bounds__(64) void attn_tiny_kernel(const T* in, T* out, int n) {
+  if (threadIdx.x < kPack) out[threadIdx.x] = (int)threadIdx.x < n ? in[threadIdx.x] : T(0);
+}
+bool is_tiny(int64_t n) { return n < kPack; }
+// The rows to read: `rows` itself or its copy at `slot`.
+const void* whole_packs(const void* rows, int64_t n, bool f32, unsigned char* slot, hipStream_t s,
+                        int* rc) {
+  if (!is_tiny(n) || *rc != SWIMBA_OK) return rows;
+  if (f32)
+    hipLaunchKernelGGL(attn_tiny_kernel<float>, dim3(1), dim3(64), 0, s,
+                       static_cast<const float*>(rows), reinterpret_cast<float*>(slot), (int)n);
+  else
+    hipLaunchKernelGGL(attn_tiny_kernel<bf16_t>, dim3(1), dim3(64), 0, s,
+                       static_cast<const bf16_t*>(rows), reinterpret_cast<bf16_t*>(slot), (int)n);
+  *rc = checked();
+  return slot;
+}
+
 // How one walk is laid out over the device.
 struct WalkPlan {
   int waves = 1, nseg = 1, seg_chunks = 1;
@@ -367,9 +389,21 @@ AttnParams base_params(const swimba_linear_attention_args* a) {
   return p;
 }
 
+int64_t key_elements(const swimba_linear_attention_args* a) {
+  return (int64_t)a->B * a->L * a->G * a->N;
+}
+int64_t value_elements(const swimba_linear_attention_args* a) {
+  return (int64_t)a->B * a->L * a->H * a->P;
+}
+// Slots behind the rest of the workspace for `slots` operands.
+size_t tiny_bytes(const swimba_linear_attention_args* a, int slots) {
+  return is_tiny(key_elements(a)) || is_tiny(value_elements(a)) ? slots * kTinySlot : 0;
+}
+
 struct GradPlan {
   WalkPlan q, v;  // dq and dk walk (states [P][N]), dv walk (states [N][P])
   size_t off_zq = 0, off_zk = 0, off_diff = 0, off_part = 0, off_x = 0, off_end = 0, off_rows = 0;
+  size_t off_tiny = 0;
   size_t bytes = 0;
   int nc = 0, ntiles = 0;
 };
@@ -397,6 +431,7 @@ GradPlan plan_grad(const swimba_linear_attention_grad_args* g, int dev) {
   r.off_end = take(g->dh_final != nullptr ? bh * a->N * a->P * sizeof(float) : 0);
   // per-head rows of dq, then of dk, where heads share them
   r.off_rows = take(a->H != a->G ? bh * a->L * a->N * sizeof(float) : 0);
+  r.off_tiny = take(tiny_bytes(a, 4));
   r.bytes = o;
   return r;
 }
@@ -424,8 +459,9 @@ int share_sum(const float* rows, void* out, swimba_dtype d, const swimba_linear_
 
 size_t attention_bytes(const swimba_linear_attention_args* a, int dev) {
   if (a->B == 0 || a->L == 0) return 0;
-  return plan_walk(a->in_dtype == SWIMBA_F32, a->B, a->L, a->H, a->H / a->G, a->N, a->P, dev)
-      .bytes();
+  const size_t walk =
+      plan_walk(a->in_dtype == SWIMBA_F32, a->B, a->L, a->H, a->H / a->G, a->N, a->P, dev).bytes();
+  return walk + tiny_bytes(a, 3);
 }
 
 int launch_attention(const swimba_linear_attention_args* a, void* ws, int dev, hipStream_t s) {
@@ -435,9 +471,12 @@ int launch_attention(const swimba_linear_attention_args* a, void* ws, int dev, h
   const bool f32 = a->in_dtype == SWIMBA_F32;
   const WalkPlan w = plan_walk(f32, a->B, a->L, a->H, a->H / a->G, a->N, a->P, dev);
   AttnParams p = base_params(a);
-  p.q = a->q;
-  p.k = a->k;
-  p.v = a->v;
+  unsigned char* slot = static_cast<unsigned char*>(ws) + w.bytes();
+  int rc = SWIMBA_OK;
+  p.q = whole_packs(a->q, key_elements(a), f32, slot, s, &rc);
+  p.k = whole_packs(a->k, key_elements(a), f32, slot + kTinySlot, s, &rc);
+  p.v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
+  if (rc != SWIMBA_OK) return rc;
   p.y = a->y;
   p.qshare = a->H / a->G;
   p.vshare = 1;
@@ -473,11 +512,19 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   float *zq = at<float>(ws, r.off_zq), *zk = at<float>(ws, r.off_zk);
   float *rows = at<float>(ws, r.off_rows), *end = at<float>(ws, r.off_end);
 
+  unsigned char* slot = at<unsigned char>(ws, r.off_tiny);
+  int rc = SWIMBA_OK;
+  const void* q = whole_packs(a->q, key_elements(a), f32, slot, s, &rc);
+  const void* k = whole_packs(a->k, key_elements(a), f32, slot + kTinySlot, s, &rc);
+  const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
+  const void* dy = whole_packs(g->dy, value_elements(a), f32, slot + 3 * kTinySlot, s, &rc);
+  if (rc != SWIMBA_OK) return rc;
+
   // dq = walk(dY, V, K)
   AttnParams p = base_params(a);
-  p.q = g->dy;
-  p.k = a->v;
-  p.v = a->k;
+  p.q = dy;
+  p.k = v;
+  p.v = k;
   p.qshare = 1;
   p.vshare = a->H / a->G;
   p.Kd = a->P;
@@ -486,22 +533,22 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   p.sc = a->P;
   p.s0 = a->h0;
   p.s_final = g->dh_final != nullptr ? end : nullptr;
-  p.z = a->q;
+  p.z = q;
   p.zsum = zq;
   p.y = shared ? static_cast<void*>(rows) : g->dq;
   p.y_bf16 = !shared && g->grad_dtype == SWIMBA_BF16;
-  int rc = walk(p, r.q, f32, true, seg, s);
+  rc = walk(p, r.q, f32, true, seg, s);
   if (rc == SWIMBA_OK && shared) rc = share_sum(rows, g->dq, g->grad_dtype, a, s);
   if (rc != SWIMBA_OK) return rc;
 
   // dk = backward walk(V, dY, Q)
-  p.q = a->v;
-  p.k = g->dy;
-  p.v = a->q;
+  p.q = v;
+  p.k = dy;
+  p.v = q;
   p.reverse = 1;
   p.s0 = g->dh_final;
   p.s_final = nullptr;
-  p.z = a->k;
+  p.z = k;
   p.zsum = zk;
   p.y = shared ? static_cast<void*>(rows) : g->dk;
   rc = walk(p, r.q, f32, true, seg, s);
@@ -510,9 +557,9 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
 
   // dv = backward walk(K, Q, dY), whose last state is dh0
   p = base_params(a);
-  p.q = a->k;
-  p.k = a->q;
-  p.v = g->dy;
+  p.q = k;
+  p.k = q;
+  p.v = dy;
   p.qshare = a->H / a->G;
   p.vshare = 1;
   p.Kd = a->N;

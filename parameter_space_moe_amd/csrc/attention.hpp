@@ -156,7 +156,7 @@ struct RowStage {
   static constexpr int kWords = 4 * kQuads;
   struct __attribute__((packed, aligned(sizeof(T)))) Loose { u4x q[kQuads]; };
   const T* base;
-  int64_t total;    // elements of the tensor
+  int64_t total;    // elements of the tensor, a pack at least
   int64_t first;    // element of the chunk's lowest token, column 0
   int64_t stride;   // between tokens
   int cols, len, tid;
@@ -191,19 +191,12 @@ struct RowStage {
         const uint32_t off = inside(row(n)) ? mine + (uint32_t)n * step : 0u;
         fetch(i, reinterpret_cast<const T*>(chunk + off));
       }
-    } else if (total >= kPack) {
+    } else {
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
         const int r = row(round * kRound + i);
         const int64_t e = inside(r) ? element(r) : 0;
         fetch(i, base + (e + kPack <= total ? e : total - kPack));
-      }
-    } else {  // a tensor of less than a pack
-#pragma unroll
-      for (int i = 0; i < kRound; ++i) {
-        const int r = row(round * kRound + i), n = cols - column();
-        const Pack<T> p = inside(r) ? load_pack(base + element(r), n < 7 ? n : 7) : Pack<T>{};
-        __builtin_memcpy(v[i], &p, sizeof(p));
       }
     }
   }
@@ -217,7 +210,7 @@ struct RowStage {
       uint32_t w[kWords];
       __builtin_memcpy(w, out, sizeof(w));
       const int64_t e = element(r);
-      const int shift = in && total >= kPack && e + kPack > total ? (int)(e + kPack - total) : 0;
+      const int shift = in && e + kPack > total ? (int)(e + kPack - total) : 0;
       if (__ballot(shift != 0)) {  // the tensor's last elements
         T m[kPack], o[kPack];
         __builtin_memcpy(m, w, sizeof(m));
@@ -354,7 +347,9 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 
   const int hv = p.H / p.vshare;
   const int64_t qstride = (int64_t)groups * p.Kd, vstride = (int64_t)hv * p.Cd;
-  const int64_t qtotal = (int64_t)p.B * p.L * qstride, vtotal = (int64_t)p.B * p.L * vstride;
+  // (smaller tensors were copied to whole packs)
+  const int64_t qall = (int64_t)p.B * p.L * qstride, vall = (int64_t)p.B * p.L * vstride;
+  const int64_t qtotal = qall < kPack ? kPack : qall, vtotal = vall < kPack ? kPack : vall;
   const int64_t qfirst = (int64_t)b * p.L * qstride + (int64_t)grp * p.Kd;
   const int64_t vfirst = (int64_t)b * p.L * vstride + (int64_t)(head / p.vshare) * p.Cd + c0;
   const float* gb = p.g + (p.token_decay ? (int64_t)b * p.L * p.H : 0) + head;

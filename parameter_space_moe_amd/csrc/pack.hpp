@@ -46,4 +46,59 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T>& r, int n) {
   }
 }
 
+// How the rows of a tensor lie for loads of N elements: whole groups, any width,
+// or a tensor of fewer than N elements in all.
+enum Rows { kLoose = 0, kWhole = 1, kTiny = 2 };
+
+// N elements of a row on their way: one whole load that stays inside the tensor
+// whatever the row width, so that a run of them is issued without branches
+// between.  Where the tensor's last row ends inside it the load starts `back`
+// elements (back_of) earlier; get() moves the elements up again and clears
+// those from `left`, the elements left in the row, on.
+template <typename T, int N>
+struct Loose {
+  static constexpr int kWords = N * (int)sizeof(T) / 4;
+  typedef uint32_t raw_t __attribute__((ext_vector_type(kWords > 4 ? 4 : kWords)));
+  static constexpr int kRaw = kWords > 4 ? kWords / 4 : 1;
+  struct __attribute__((packed, aligned(sizeof(T)))) Mem { raw_t r[kRaw]; };
+  raw_t r[kRaw];
+
+  __device__ __forceinline__ void whole(const T* p) {
+    const Mem m = *reinterpret_cast<const Mem*>(p);
+#pragma unroll
+    for (int i = 0; i < kRaw; ++i) r[i] = m.r[i];
+  }
+  // a tensor of fewer than N elements
+  __device__ __forceinline__ void few(const T* p, int left) {
+    T v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < left ? p[i] : T(0);
+    __builtin_memcpy(r, v, sizeof(v));
+  }
+  __device__ __forceinline__ void get(int back, int left, T* out) const {
+    T m[N];
+    __builtin_memcpy(m, r, sizeof(m));
+    if (__ballot(back != 0)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        T v = m[i];
+#pragma unroll
+        for (int j = i + 1; j < N; ++j) v = back == j - i ? m[j] : v;
+        out[i] = v;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) out[i] = m[i];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = i < left ? out[i] : T(0);
+  }
+};
+
+// How far a load of N elements, `left` of them in the row, has to be moved back.
+template <int N>
+__device__ __forceinline__ int back_of(bool last_row, int left) {
+  return last_row && left > 0 && left < N ? N - left : 0;
+}
+
 }  // namespace swimba

@@ -36,34 +36,6 @@ struct RouteGradParams {
   int two;      // LDS holds two slope tables
 };
 
-// Four channels of one token as they are in memory.
-template <typename T>
-struct Quad {
-  struct __attribute__((packed, aligned(sizeof(T)))) Loose { uint32_t w[sizeof(T)]; };
-  uint32_t w[sizeof(T)];
-
-  // n elements of the row are left (WHOLE: four or none); none: anything inside x
-  template <bool WHOLE>
-  __device__ __forceinline__ void load(const T* p, int n) {
-    if (WHOLE || n >= 4) {
-      const Loose l = *reinterpret_cast<const Loose*>(p);
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(T); ++i) w[i] = l.w[i];
-    } else {
-      T e[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = i < n ? p[i] : T(0);
-      __builtin_memcpy(w, e, sizeof(w));
-    }
-  }
-  __device__ __forceinline__ void floats(float* v, bool on) const {
-    T e[4];
-    __builtin_memcpy(e, w, sizeof(w));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = on ? to_f32(e[i]) : 0.f;
-  }
-};
-
 template <typename T>
 __device__ __forceinline__ void store4(T* p, int n, const float* v) {
   struct __attribute__((packed, aligned(sizeof(T)))) Loose { T e[4]; };
@@ -79,31 +51,32 @@ __device__ __forceinline__ void store4(T* p, int n, const float* v) {
   }
 }
 
-// LDS of one tile's slopes: dense by expert, and by slot.
+// LDS of one tile's slopes: by slot (with the place of the expert's row of Wr^T
+// in LDS: the row of zeros behind the last one without an expert), and dense by
+// expert.
 template <int ET>
 struct Slopes {
   static constexpr int kDense = ET * 16 + 1;
+  float2* slot;   // [kTile][k] slope, row (an int's bits)
   float* dense;   // [kTile][kDense]
-  float* slot;    // [kTile][k]
-  int32_t* expert;  // [kTile][k], -1 without
-  int32_t* any;     // [kTile] tokens with an expert
+  int32_t* any;   // [kTile] tokens with an expert
   static constexpr size_t words(int k) { return kTile * (kDense + 1 + 2 * (size_t)k); }
   __device__ __forceinline__ Slopes(float* at, int k)
-      : dense(at),
-        slot(at + kTile * kDense),
-        expert(reinterpret_cast<int32_t*>(slot + kTile * k)),
-        any(expert + kTile * k) {}
+      : slot(reinterpret_cast<float2*>(at)),
+        dense(at + 2 * kTile * k),
+        any(reinterpret_cast<int32_t*>(dense + kTile * kDense)) {}
 };
 
 // ET: expert tiles of 16; K: most slots per token that are held in registers
-// (0: any number of slots); WHOLE: rows are whole groups of four channels.
-template <typename TI, typename TO, int ET, int K, bool WHOLE>
+// (0: any number of slots); ROWS: kLoose, kWhole or kTiny.
+template <typename TI, typename TO, int ET, int K, int ROWS>
 __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void route_grad_kernel(RouteGradParams p) {
   using Table = Slopes<ET>;
+  constexpr bool WHOLE = ROWS == kWhole;
   constexpr int kDense = Table::kDense;
   extern __shared__ __attribute__((aligned(16))) float smem[];
   const int k = K > 0 ? K : p.k;
-  float* sW = smem;  // [E][kSlabStride]
+  float* sW = smem;  // [E + 1][kSlabStride]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int q = lane >> 4, c = lane & 15;
   const int d0 = blockIdx.x * kSlab, dl = wave * 64 + 4 * c, d = d0 + dl;
@@ -129,6 +102,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
     }
   }
 
+  sW[p.E * kSlabStride + threadIdx.x] = 0.f;
+
   f4 acc[ET][4];
 #pragma unroll
   for (int e = 0; e < ET; ++e)
@@ -137,13 +112,18 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
 
   // 32 rows of x are in flight while the 32 before are worked on
   constexpr int kSteps = 8;
-  Quad<TI> xr[kSteps];
+  Loose<TI, 4> xr[kSteps];
+  auto back = [&](int64_t t) {
+    return ROWS == kLoose ? back_of<4>(t == p.T - 1, left) : 0;
+  };
   auto fetch = [&](int64_t t0) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int64_t t = t0 + 4 * i + q;
       const bool in = t < te && left > 0;  // others: the first channels of x
-      xr[i].template load<WHOLE>(x + (in ? t * p.D + d : 0), in ? left : p.D);
+      const TI* at = x + (in ? t * p.D + d - back(t) : 0);
+      if constexpr (ROWS == kTiny) xr[i].few(at, in ? left : 0);
+      else xr[i].whole(at);
     }
   };
   if (tb < te) fetch(tb);  // without tokens x may be null
@@ -182,8 +162,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
       auto slot = [&](int j, float g, float dg, int e, bool has) {
         const bool in = has && e >= 0 && e < p.E;
         const float v = g * (dg - mean);
-        tab.slot[lane * k + j] = v;
-        tab.expert[lane * k + j] = in ? e : -1;
+        tab.slot[lane * k + j] = make_float2(in ? v : 0.f, __int_as_float((in ? e : p.E) * kSlabStride));
         any |= in;
         if (in) row[e] += v;  // an expert listed twice adds twice
       };
@@ -197,8 +176,8 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
     }
     tab.any[lane] = any;
   };
-  const Table tab0(smem + p.E * kSlabStride, k);
-  const Table tab1(smem + p.E * kSlabStride + (p.two ? Table::words(k) : 0), k);
+  const Table tab0(smem + (p.E + 1) * kSlabStride, k);
+  const Table tab1(smem + (p.E + 1) * kSlabStride + (p.two ? Table::words(k) : 0), k);
   if (wave == 0 && tb < te) {
     values(tb);
     make(tb, tab0);
@@ -214,7 +193,7 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
 #pragma unroll 1
     for (int hb = 0; hb < kTile; hb += 4 * kSteps) {
       if (hb >= len) break;
-      Quad<TI> xc[kSteps];
+      Loose<TI, 4> xc[kSteps];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) xc[i] = xr[i];
       fetch(t0 + hb + 4 * kSteps);
@@ -223,7 +202,13 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
         const int t = hb + 4 * i + q;
         float xv[4];
         // a token without an expert may hold anything: left out
-        xc[i].floats(xv, tab.any[t] != 0);
+        {
+          const int n = t < len && tab.any[t] ? (WHOLE && left > 0 ? 4 : left) : 0;
+          TI e[4];
+          xc[i].get(back(t0 + t), n, e);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) xv[j] = to_f32(e[j]);
+        }
         float a[ET];
 #pragma unroll
         for (int e = 0; e < ET; ++e) a[e] = tab.dense[t * kDense + e * 16 + c];
@@ -236,17 +221,16 @@ __global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void
         const int ts = t < len ? t : 0;
         // (a loop of K, unrolled, where K is known)
         for (int j = 0; j < k; ++j) {
-          const int e = tab.expert[ts * k + j];
-          const float v = tab.slot[ts * k + j];
-          const float4 w =
-              *reinterpret_cast<const float4*>(sW + (e < 0 ? 0 : e) * kSlabStride + dl);
-          o[0] = e < 0 ? o[0] : fmaf(v, w.x, o[0]);
-          o[1] = e < 0 ? o[1] : fmaf(v, w.y, o[1]);
-          o[2] = e < 0 ? o[2] : fmaf(v, w.z, o[2]);
-          o[3] = e < 0 ? o[3] : fmaf(v, w.w, o[3]);
+          const float2 v = tab.slot[ts * k + j];
+          const float4 w = *reinterpret_cast<const float4*>(sW + __float_as_int(v.y) + dl);
+          o[0] = fmaf(v.x, w.x, o[0]);
+          o[1] = fmaf(v.x, w.y, o[1]);
+          o[2] = fmaf(v.x, w.z, o[2]);
+          o[3] = fmaf(v.x, w.w, o[3]);
         }
-        if (t < len && left > 0) store4(dx + (t0 + t) * p.D + d, WHOLE ? 4 : left, o);
-        if (i & 1) __builtin_amdgcn_sched_barrier(0);
+        if (t < len && left > 0)
+          store4(dx + t0 * p.D + ((int64_t)t * p.D + d), WHOLE ? 4 : left, o);
+        __builtin_amdgcn_sched_barrier(0);  // else every step's operands are held at once
       }
     }
     if (!p.two) __syncthreads();  // one table only: everyone has to be done with it
@@ -311,15 +295,15 @@ RouteGradPlan plan(int64_t T, int D, int E, int elem, int dev) {
   return r;
 }
 
-template <typename TI, typename TO, int ET, int K, bool WHOLE>
+template <typename TI, typename TO, int ET, int K, int ROWS>
 int launch(const RouteGradParams& a, const RouteGradPlan& r, hipStream_t s) {
   RouteGradParams p = a;
-  const size_t fixed = (size_t)p.E * kSlabStride * sizeof(float);
+  const size_t fixed = (size_t)(p.E + 1) * kSlabStride * sizeof(float);
   const size_t table = Slopes<ET>::words(K > 0 ? K : p.k) * sizeof(float);
   p.two = fixed + 2 * table <= 160 * 1024;  // one table where nearly every expert is selected
   const size_t lds = fixed + (p.two ? 2 : 1) * table;
-  allow_dynamic_lds(route_grad_kernel<TI, TO, ET, K, WHOLE>, lds);
-  hipLaunchKernelGGL((route_grad_kernel<TI, TO, ET, K, WHOLE>), dim3(r.slabs, r.splits),
+  allow_dynamic_lds(route_grad_kernel<TI, TO, ET, K, ROWS>, lds);
+  hipLaunchKernelGGL((route_grad_kernel<TI, TO, ET, K, ROWS>), dim3(r.slabs, r.splits),
                      dim3(kThreads), lds, s, p);
   if (hipGetLastError() != hipSuccess) return SWIMBA_EHIP;
   if (r.splits > 1) {
@@ -334,14 +318,15 @@ template <typename TI, typename TO, int ET>
 int launch_slots(const RouteGradParams& p, const RouteGradPlan& r, hipStream_t s) {
   const bool whole = p.D % 4 == 0;
   if (p.k == 2)
-    return whole ? launch<TI, TO, ET, 2, true>(p, r, s) : launch<TI, TO, ET, 2, false>(p, r, s);
+    return whole ? launch<TI, TO, ET, 2, kWhole>(p, r, s) : launch<TI, TO, ET, 2, kLoose>(p, r, s);
   if (p.k <= 4)
-    return whole ? launch<TI, TO, ET, 4, true>(p, r, s) : launch<TI, TO, ET, 4, false>(p, r, s);
-  return whole ? launch<TI, TO, ET, 0, true>(p, r, s) : launch<TI, TO, ET, 0, false>(p, r, s);
+    return whole ? launch<TI, TO, ET, 4, kWhole>(p, r, s) : launch<TI, TO, ET, 4, kLoose>(p, r, s);
+  return whole ? launch<TI, TO, ET, 0, kWhole>(p, r, s) : launch<TI, TO, ET, 0, kLoose>(p, r, s);
 }
 
 template <typename TI, typename TO>
 int launch_types(const RouteGradParams& p, const RouteGradPlan& r, hipStream_t s) {
+  if (p.D % 4 != 0 && p.T * p.D < 4) return launch<TI, TO, 4, 0, kTiny>(p, r, s);
   if (p.E <= 16) return launch_slots<TI, TO, 1>(p, r, s);
   if (p.E <= 32) return launch_slots<TI, TO, 2>(p, r, s);
   return launch_slots<TI, TO, 4>(p, r, s);

@@ -188,22 +188,37 @@ __device__ __forceinline__ Packs packs_of(const MoveParams& p) {
   return m;
 }
 
-// The pack at p of a row with n elements left; WHOLE rows are whole packs.
-template <bool WHOLE, typename T>
-__device__ __forceinline__ Pack<T> row_pack(const T* p, int n) {
-  return load_pack(p, WHOLE ? kPack : n);
-}
+// A pack of row `row` (of `rows`, D wide) from column c on.
+template <typename T, int ROWS>
+struct RowPack {
+  Loose<T, kPack> v;
+  __device__ __forceinline__ void load(const T* base, int64_t row, int64_t rows, int D, int c) {
+    const T* p = base + row * D + c;
+    if constexpr (ROWS == kWhole) v.whole(p);
+    else if constexpr (ROWS == kLoose) v.whole(p - back_of<kPack>(row == rows - 1, D - c));
+    else v.few(p, D - c);
+  }
+  __device__ __forceinline__ Pack<T> get(int64_t row, int64_t rows, int D, int c) const {
+    Pack<T> p;
+    if constexpr (ROWS == kWhole) v.get(0, kPack, p.v);
+    else v.get(ROWS == kLoose ? back_of<kPack>(row == rows - 1, D - c) : 0, D - c, p.v);
+    return p;
+  }
+};
 
-template <typename T, bool WHOLE>
+template <typename T, int ROWS>
 __global__ __launch_bounds__(kMoveThreads) void dispatch_kernel(MoveParams p) {
   const T* x = static_cast<const T*>(p.src);
   T* rows = static_cast<T*>(p.dst);
   const int64_t n = p.T * p.k;
   const Packs m = packs_of(p);
+  RowPack<T, ROWS> in[kMovePacks];
   Pack<T> v[kMovePacks];
 #pragma unroll
+  for (int i = 0; i < kMovePacks; ++i) in[i].load(x, m.t[i], p.T, p.D, m.c[i]);
+#pragma unroll
   for (int i = 0; i < kMovePacks; ++i)
-    v[i] = row_pack<WHOLE>(x + m.t[i] * p.D + m.c[i], p.D - m.c[i]);
+    v[i] = in[i].get(m.t[i], p.T, p.D, m.c[i]);
   for (int j = 0; j < p.k; ++j) {
     int32_t at[kMovePacks];
 #pragma unroll
@@ -211,13 +226,13 @@ __global__ __launch_bounds__(kMoveThreads) void dispatch_kernel(MoveParams p) {
 #pragma unroll
     for (int i = 0; i < kMovePacks; ++i)
       if (m.on[i] && is_row(at[i], n))
-        store_pack(rows + (int64_t)at[i] * p.D + m.c[i], v[i], WHOLE ? kPack : p.D - m.c[i]);
+        store_pack(rows + (int64_t)at[i] * p.D + m.c[i], v[i], ROWS == kWhole ? kPack : p.D - m.c[i]);
   }
 }
 
 // y_t = sum_j gate_j rows[pos_j], in slot order in fp32 (gate null: ones).
 // A slot without a row reads row 0 and leaves it out.
-template <typename TI, typename TO, bool WHOLE>
+template <typename TI, typename TO, int ROWS>
 __global__ __launch_bounds__(kMoveThreads) void combine_kernel(MoveParams p) {
   const TI* rows = static_cast<const TI*>(p.src);
   TO* y = static_cast<TO*>(p.dst);
@@ -227,23 +242,26 @@ __global__ __launch_bounds__(kMoveThreads) void combine_kernel(MoveParams p) {
   for (int j = 0; j < p.k; ++j) {
     int32_t at[kMovePacks];
     float g[kMovePacks];
-    Pack<TI> v[kMovePacks];
+    RowPack<TI, ROWS> v[kMovePacks];
+    int64_t row[kMovePacks];
 #pragma unroll
     for (int i = 0; i < kMovePacks; ++i) {
       at[i] = p.pos[m.t[i] * p.k + j];
       g[i] = p.gate != nullptr ? p.gate[m.t[i] * p.k + j] : 1.f;
     }
 #pragma unroll
-    for (int i = 0; i < kMovePacks; ++i)
-      v[i] = row_pack<WHOLE>(rows + (is_row(at[i], n) ? (int64_t)at[i] * p.D : 0) + m.c[i],
-                             p.D - m.c[i]);
+    for (int i = 0; i < kMovePacks; ++i) {
+      row[i] = is_row(at[i], n) ? at[i] : 0;
+      v[i].load(rows, row[i], n, p.D, m.c[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kMovePacks; ++i) {
       const bool in = is_row(at[i], n);
+      const Pack<TI> r = v[i].get(row[i], n, p.D, m.c[i]);
 #pragma unroll
-      for (int e = 0; e < kPack; ++e) {
-        const float s = fmaf(g[i], to_f32(v[i].v[e]), acc[i][e]);
-        acc[i][e] = in ? s : acc[i][e];
+      for (int u = 0; u < kPack; ++u) {
+        const float s = fmaf(g[i], to_f32(r.v[u]), acc[i][u]);
+        acc[i][u] = in ? s : acc[i][u];
       }
     }
   }
@@ -253,7 +271,7 @@ __global__ __launch_bounds__(kMoveThreads) void combine_kernel(MoveParams p) {
 #pragma unroll
     for (int e = 0; e < kPack; ++e) o.v[e] = from_f32<TO>(acc[i][e]);
     if (m.on[i])
-      store_pack(y + m.t[i] * p.D + m.c[i], o, WHOLE ? kPack : p.D - m.c[i]);
+      store_pack(y + m.t[i] * p.D + m.c[i], o, ROWS == kWhole ? kPack : p.D - m.c[i]);
   }
 }
 
@@ -270,13 +288,13 @@ struct CombineGradParams {
 // drows[pos_j] = gate_j dy_t and dgate_j = <dy_t, rows[pos_j]>, two slots at a
 // time: a token per wave (PER = 1), or per workgroup of four where the tokens
 // alone would leave most of the device idle (PER = 4).
-template <typename TI, typename TY, typename TO, int PER, bool WHOLE>
+template <typename TI, typename TY, typename TO, int PER, int ROWS>
 __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradParams p) {
   __shared__ float part[4][2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = PER == 4 ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
   if (t >= p.T) return;  // whole waves, and no barrier follows where PER is 1
-  const TY* dy = static_cast<const TY*>(p.dy) + t * p.D;
+  const TY* dyb = static_cast<const TY*>(p.dy);
   const TI* rows = static_cast<const TI*>(p.rows);
   TO* drows = static_cast<TO*>(p.drows);
   const int64_t n = p.T * p.k;
@@ -290,7 +308,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradParams p) 
     for (int j = 0; j < 2; ++j) {
       const int32_t at = j0 + j < p.k ? uniform(p.pos[t * p.k + j0 + j]) : -1;
       in[j] = is_row(at, n);
-      row[j] = in[j] ? (int64_t)at * p.D : 0;
+      row[j] = in[j] ? at : 0;
       g[j] = in[j] ? p.gate[t * p.k + j0 + j] : 0.f;
     }
     auto pass = [&](auto* dst, int j, const Pack<TY>& d, const Pack<TI>& r, int c) {
@@ -301,24 +319,31 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradParams p) 
         s[j] = fmaf(v, to_f32(r.v[i]), s[j]);
         o.v[i] = from_f32<TO>(g[j] * v);
       }
-      store_pack(dst + row[j] + c, o, WHOLE ? kPack : p.D - c);
+      store_pack(dst + row[j] * p.D + c, o, ROWS == kWhole ? kPack : p.D - c);
     };
     if (in[0] && in[1]) {
 #pragma unroll 2
       for (int c = first; c < p.D; c += kStride) {
-        const Pack<TY> d = row_pack<WHOLE>(dy + c, p.D - c);
-        const Pack<TI> a = row_pack<WHOLE>(rows + row[0] + c, p.D - c);
-        const Pack<TI> b = row_pack<WHOLE>(rows + row[1] + c, p.D - c);
-        pass(drows, 0, d, a, c);
-        pass(drows, 1, d, b, c);
+        RowPack<TY, ROWS> d;
+        RowPack<TI, ROWS> a, b;
+        d.load(dyb, t, p.T, p.D, c);
+        a.load(rows, row[0], n, p.D, c);
+        b.load(rows, row[1], n, p.D, c);
+        const Pack<TY> dp = d.get(t, p.T, p.D, c);
+        pass(drows, 0, dp, a.get(row[0], n, p.D, c), c);
+        pass(drows, 1, dp, b.get(row[1], n, p.D, c), c);
       }
     } else if (in[0] || in[1]) {
-      const int j = in[0] ? 0 : 1;
+      const int64_t r = in[0] ? row[0] : row[1];
       for (int c = first; c < p.D; c += kStride) {
-        const Pack<TY> d = row_pack<WHOLE>(dy + c, p.D - c);
-        const Pack<TI> a = row_pack<WHOLE>(rows + row[j] + c, p.D - c);
-        if (j == 0) pass(drows, 0, d, a, c);
-        else pass(drows, 1, d, a, c);
+        RowPack<TY, ROWS> d;
+        RowPack<TI, ROWS> a;
+        d.load(dyb, t, p.T, p.D, c);
+        a.load(rows, r, n, p.D, c);
+        const Pack<TY> dp = d.get(t, p.T, p.D, c);
+        const Pack<TI> ap = a.get(r, n, p.D, c);
+        if (in[0]) pass(drows, 0, dp, ap, c);
+        else pass(drows, 1, dp, ap, c);
       }
     }
 #pragma unroll
@@ -366,38 +391,49 @@ bool move_grid(const MoveParams& p, dim3* grid) {
   return true;
 }
 
+// How rows of width D lie, in the smallest of the tensors read (`least` rows).
+int rows_kind(int D, int64_t least) {
+  if (D % kPack == 0) return kWhole;
+  return least * D >= kPack ? kLoose : kTiny;
+}
+
+template <typename TI, typename TY, typename TO, int PER>
+int launch_combine_grad_rows(const CombineGradParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)((p.T + 4 / PER - 1) / (4 / PER))), th(256);
+  const int kind = rows_kind(p.D, p.T);
+  if (kind == kWhole)
+    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, PER, kWhole>), grid, th, 0, s, p);
+  else if (kind == kLoose)
+    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, PER, kLoose>), grid, th, 0, s, p);
+  else
+    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, PER, kTiny>), grid, th, 0, s, p);
+  return checked();
+}
+
 template <typename TI, typename TY, typename TO>
 int launch_combine_grad(const CombineGradParams& p, int dev, hipStream_t s) {
-  if (p.T > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
-  const bool few = p.T < 16LL * device_cus(dev);  // waves for every SIMD four times over
-  const dim3 grid((unsigned)(few ? p.T : (p.T + 3) / 4)), th(256);
-  const bool whole = p.D % kPack == 0;
-  if (few && whole)
-    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 4, true>), grid, th, 0, s, p);
-  else if (few)
-    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 4, false>), grid, th, 0, s, p);
-  else if (whole)
-    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 1, true>), grid, th, 0, s, p);
-  else
-    hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, 1, false>), grid, th, 0, s, p);
-  return checked();
+  // a workgroup per token where waves alone do not fill every SIMD four times
+  return p.T < 16LL * device_cus(dev) ? launch_combine_grad_rows<TI, TY, TO, 4>(p, s)
+                                      : launch_combine_grad_rows<TI, TY, TO, 1>(p, s);
 }
 
 template <typename T>
 int launch_dispatch(const MoveParams& p, dim3 grid, hipStream_t s) {
-  if (p.D % kPack == 0)
-    hipLaunchKernelGGL((dispatch_kernel<T, true>), grid, dim3(kMoveThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL((dispatch_kernel<T, false>), grid, dim3(kMoveThreads), 0, s, p);
+  const dim3 th(kMoveThreads);
+  const int kind = rows_kind(p.D, p.T);
+  if (kind == kWhole) hipLaunchKernelGGL((dispatch_kernel<T, kWhole>), grid, th, 0, s, p);
+  else if (kind == kLoose) hipLaunchKernelGGL((dispatch_kernel<T, kLoose>), grid, th, 0, s, p);
+  else hipLaunchKernelGGL((dispatch_kernel<T, kTiny>), grid, th, 0, s, p);
   return checked();
 }
 
 template <typename TI, typename TO>
 int launch_combine(const MoveParams& p, dim3 grid, hipStream_t s) {
-  if (p.D % kPack == 0)
-    hipLaunchKernelGGL((combine_kernel<TI, TO, true>), grid, dim3(kMoveThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL((combine_kernel<TI, TO, false>), grid, dim3(kMoveThreads), 0, s, p);
+  const dim3 th(kMoveThreads);
+  const int kind = rows_kind(p.D, p.T);
+  if (kind == kWhole) hipLaunchKernelGGL((combine_kernel<TI, TO, kWhole>), grid, th, 0, s, p);
+  else if (kind == kLoose) hipLaunchKernelGGL((combine_kernel<TI, TO, kLoose>), grid, th, 0, s, p);
+  else hipLaunchKernelGGL((combine_kernel<TI, TO, kTiny>), grid, th, 0, s, p);
   return checked();
 }
 
@@ -435,7 +471,8 @@ int launch_dispatch_tokens(const void* x, swimba_dtype xd, const int32_t* pos, i
   const MoveParams p = move_params(x, rows, pos, nullptr, T, D, k);
   dim3 grid;
   if (!move_grid(p, &grid)) return SWIMBA_EUNSUPPORTED;
-  return xd == SWIMBA_BF16 ? launch_dispatch<bf16_t>(p, grid, s) : launch_dispatch<float>(p, grid, s);
+  if (xd == SWIMBA_BF16) return launch_dispatch<bf16_t>(p, grid, s);
+  return launch_dispatch<float>(p, grid, s);
 }
 
 int launch_combine_tokens(const void* rows, swimba_dtype rd, const int32_t* pos, const float* gate,
@@ -446,7 +483,8 @@ int launch_combine_tokens(const void* rows, swimba_dtype rd, const int32_t* pos,
   const bool r = rd == SWIMBA_BF16, o = yd == SWIMBA_BF16;
   if (r && o) return launch_combine<bf16_t, bf16_t>(p, grid, s);
   if (r) return launch_combine<bf16_t, float>(p, grid, s);
-  return o ? launch_combine<float, bf16_t>(p, grid, s) : launch_combine<float, float>(p, grid, s);
+  if (o) return launch_combine<float, bf16_t>(p, grid, s);
+  return launch_combine<float, float>(p, grid, s);
 }
 
 int launch_combine_tokens_backward(const void* rows, swimba_dtype rd, const int32_t* pos,

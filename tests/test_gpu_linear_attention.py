@@ -317,3 +317,15 @@ def test_wrong_arguments():
         swimba.linear_attention(q.half(), k.half(), v.half(), g)
     with pytest.raises(ValueError):
         swimba.linear_attention_backward(q, k, v, g, torch.zeros(1, 8, 4, 16, device=DEV))
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 3, 200), (1, 1, 1, 1, 256, 2), (1, 2, 1, 1, 3, 2), (1, 1, 3, 1, 5, 1)], ids=str)
+def test_operands_of_less_than_a_pack(shape):
+    B, L, H, G, N, P = shape
+    for dtype in ("bf16", "f32"):
+        dev, ref = make(*shape, dtype=dtype, grad=True, seed=41)
+        y, h = forward(dev, y_dtype=torch.float32)
+        want, size = refs.attention(*args(ref)), refs.attention_sizes(*args(ref))
+        close(y, want["y"], size["y"], refs.roundings(N, P, L), "y")
+        close(h, want["h_final"], size["h_final"], refs.roundings(N, P, L), "h")
+        check_backward(dev, ref, shape, "f32")

@@ -305,3 +305,26 @@ def test_binding_refuses():
         swimba.sort_tokens(pos.t(), 4)
     with pytest.raises(swimba.SwimbaError):
         swimba.sort_tokens(pos, 1)  # k > E
+
+
+@pytest.mark.parametrize("T,D", [(1, 1), (2, 3), (1, 7), (3, 1), (1, 3)])
+def test_tensors_of_less_than_a_pack(T, D):
+    idx = torch.zeros((T, 1), dtype=torch.int32, device=DEV)
+    for dt in (torch.bfloat16, torch.float32):
+        x = torch.randn(T, D, device=DEV).to(dt)
+        _, pos, _ = swimba.sort_tokens(idx, 2)
+        rows = swimba.dispatch_tokens(x, pos)
+        assert torch.equal(rows.cpu(), x.cpu())
+        gate = torch.full((T, 1), 0.5, device=DEV)
+        assert torch.equal(swimba.combine_tokens(rows, pos, gate).cpu(), (0.5 * x.float()).to(dt).cpu())
+        drows, dgate = swimba.combine_tokens_backward(rows, pos, gate, x)
+        assert torch.equal(drows.cpu(), (0.5 * x.float()).to(dt).cpu())
+        want = (up(x) ** 2).sum(1, keepdims=True)
+        assert (np.abs(up(dgate) - want) <= (D + 8) * refs.U32 * want).all()
+        two = torch.tensor([[0, 1]] * T, dtype=torch.int32, device=DEV)
+        g2, dg2 = torch.full((T, 2), 0.5, device=DEV), torch.tensor([[1.0, -1.0]] * T, device=DEV)
+        W = torch.randn(D, 2, device=DEV)
+        dx, dW = swimba.route_backward(x, W, two, g2, dg2)
+        wx, wW, sx, sW = refs.route_backward(up(x), up(W), two.cpu().numpy(), up(g2), up(dg2))
+        assert (np.abs(up(dx) - wx) <= 10 * refs.U32 * sx).all()
+        assert (np.abs(up(dW) - wW) <= (T + 10) * refs.U32 * sW).all()
