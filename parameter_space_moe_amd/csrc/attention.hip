@@ -34,20 +34,29 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(AttnParams p) {
   }
 }
 
+// X (below) where segments meet, from both walks' first states: the state
+// before the boundary and the adjoint behind it, joined by the decay of the
+// first token behind it.
+struct AnchorParams {
+  const float *h, *adj;  // [B, H, nseg, n] first states of the dq and of the dk walk
+  const float* g;
+  double* out;           // [B, H, nseg - 1]
+  int64_t n;
+  int H, L, nseg, seg_chunks, token_decay;
+};
+
 // out[b, h] = <a, b> over a state, in 64 bits.
 constexpr int kDotThreads = 1024;
-__global__ __launch_bounds__(kDotThreads) void attn_dot_kernel(const float* a, const float* b,
-                                                               double* out, int64_t n) {
-  __shared__ double part[kDotThreads];
-  const int64_t at = (int64_t)blockIdx.x * n;
+__device__ __forceinline__ double block_dot(const float* a, const float* b, int64_t n,
+                                            double* part) {
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += 8 * kDotThreads) {
     float x[8], y[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int64_t e = i + u * kDotThreads;
-      x[u] = a[at + (e < n ? e : 0)];
-      y[u] = e < n ? b[at + e] : 0.f;
+      x[u] = a[e < n ? e : 0];
+      y[u] = b[e < n ? e : 0];
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
@@ -59,7 +68,29 @@ __global__ __launch_bounds__(kDotThreads) void attn_dot_kernel(const float* a, c
     if ((int)threadIdx.x < w) part[threadIdx.x] += part[threadIdx.x + w];
     __syncthreads();
   }
-  if (threadIdx.x == 0) out[blockIdx.x] = part[0];
+  return part[0];
+}
+
+__global__ __launch_bounds__(kDotThreads) void attn_dot_kernel(const float* a, const float* b,
+                                                               double* out, int64_t n) {
+  __shared__ double part[kDotThreads];
+  const int64_t at = (int64_t)blockIdx.x * n;
+  const double s = block_dot(a + at, b + at, n, part);
+  if (threadIdx.x == 0) out[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kDotThreads) void attn_anchor_kernel(AnchorParams p) {
+  __shared__ double part[kDotThreads];
+  const int64_t bh = blockIdx.y;
+  const int i = blockIdx.x + 1;  // the boundary before segment i
+  const int64_t f = (bh * p.nseg + i) * p.n, r = (bh * p.nseg + p.nseg - i) * p.n;
+  const double s = block_dot(p.h + f, p.adj + r, p.n, part);
+  if (threadIdx.x == 0) {
+    const int64_t t = (int64_t)i * p.seg_chunks * kChunk, b = bh / p.H, h = bh % p.H;
+    const double d = (double)p.g[p.token_decay ? (b * p.L + t) * p.H + h : h] * 1.4426950408889634;
+    p.out[bh * (p.nseg - 1) + blockIdx.x] =
+        s * (double)exp2_sum(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
+  }
 }
 
 // Gradients of the log decays.  In a chunk, with row_r and col_s the sums of
@@ -69,10 +100,14 @@ __global__ __launch_bounds__(kDotThreads) void attn_dot_kernel(const float* a, c
 //   dg_t = sum_{r >= t} (row_r - col_r + a_r) + sum_{s < t} b_s + through
 // where `through` is what later chunks read of the first state: with X the
 // product of state and adjoint at a chunk's end, through = X - sum b, and X at
-// its beginning is through + sum a.  The cancelling sums stay inside a chunk.
+// its beginning is through + sum a.  X is known behind the last chunk and where
+// segments meet, and chained over the chunks between.  The cancelling sums stay
+// inside a chunk.
 struct DecayGradParams {
   const float *zq, *zk;   // [B, H, ctiles, 2, L] of the dq and dk walks
   const double* x_end;    // [B, H] X behind the last chunk, or null for zero
+  const double* anchor;   // [B, H, segments - 1] X where segments meet, or null
+  int seg_chunks, nseg;
   double* diff;           // [B, H, chunks] sum a - sum b
   double* part;           // [B, H, chunks] sums of dg (a decay per head), or null
   const float* g;
@@ -121,8 +156,18 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(DecayGradParams p)
   const int64_t bh = w / p.nc;
   const int c = (int)(w - bh * p.nc), h = (int)(bh % p.H), t = c * kChunk + lane;
   double x = 0.0;
-  for (int i = c + 1 + lane; i < p.nc; i += 64) x += p.diff[bh * p.nc + i];
-  x = wave_sum(x) + (p.x_end != nullptr ? p.x_end[bh] : 0.0);
+  // up to the next segment's first chunk, or the end
+  int stop = p.nc;
+  double known = p.x_end != nullptr ? p.x_end[bh] : 0.0;
+  if (p.anchor != nullptr) {
+    const int next = c / p.seg_chunks + 1;
+    if (next < p.nseg) {
+      stop = next * p.seg_chunks;
+      known = p.anchor[bh * (p.nseg - 1) + next - 1];
+    }
+  }
+  for (int i = c + 1 + lane; i < stop; i += 64) x += p.diff[bh * p.nc + i];
+  x = wave_sum(x) + known;
   const DecayTerms r = decay_terms(p, bh, t);
   double after = r.inside + r.a, before = r.b;
 #pragma unroll
@@ -336,7 +381,10 @@ WalkPlan plan_walk(bool f32, int B, int L, int H, int share, int Kd, int Cd, int
                        (f32 ? attn_resident<float>(Kd, w.waves) : attn_resident<bf16_t>(Kd, w.waves));
   int64_t want = base > 0 ? hold / base : 1;
   if (want > nc) want = nc;
-  if (want < 2 || nc < 4) want = 1;
+  // A chunk takes a lone workgroup of a CU two thirds of the time it takes two
+  // at once: halves of walks that fill the CUs once would only add the pass
+  // (1.4B-like prompts: 416 us in halves, 375 us whole).
+  if (want < 3 || nc < 4) want = 1;
   w.seg_chunks = (int)((nc + want - 1) / want);
   if (w.seg_chunks < 1) w.seg_chunks = 1;
   w.nseg = nc > 0 ? (int)((nc + w.seg_chunks - 1) / w.seg_chunks) : 1;
@@ -403,7 +451,7 @@ size_t tiny_bytes(const swimba_linear_attention_args* a, int slots) {
 struct GradPlan {
   WalkPlan q, v;  // dq and dk walk (states [P][N]), dv walk (states [N][P])
   size_t off_zq = 0, off_zk = 0, off_diff = 0, off_part = 0, off_x = 0, off_end = 0, off_rows = 0;
-  size_t off_tiny = 0;
+  size_t off_tiny = 0, off_adj = 0, off_v = 0, off_anchor = 0;
   size_t bytes = 0;
   int nc = 0, ntiles = 0;
 };
@@ -416,13 +464,18 @@ GradPlan plan_grad(const swimba_linear_attention_grad_args* g, int dev) {
   r.v = plan_walk(f32, a->B, a->L, a->H, a->H / a->G, a->N, a->P, dev);
   r.nc = (a->L + kChunk - 1) / kChunk;
   r.ntiles = (a->N + 31) / 32;
-  size_t o = r.q.bytes() > r.v.bytes() ? r.q.bytes() : r.v.bytes();  // one walk after the other
+  // segment states of the dq and dk walks (the decays' gradient meets both) and
+  // of the dv walk
+  size_t o = r.q.bytes();
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o += align256(bytes);
     return at;
   };
   const size_t bh = (size_t)a->B * a->H;
+  r.off_adj = take(r.q.bytes());
+  r.off_v = take(r.v.bytes());
+  r.off_anchor = take(r.q.nseg > 1 ? bh * (r.q.nseg - 1) * sizeof(double) : 0);
   r.off_zq = take(bh * r.ntiles * 2 * a->L * sizeof(float));
   r.off_zk = take(bh * r.ntiles * 2 * a->L * sizeof(float));
   r.off_diff = take(bh * r.nc * sizeof(double));
@@ -551,7 +604,7 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   p.z = k;
   p.zsum = zk;
   p.y = shared ? static_cast<void*>(rows) : g->dk;
-  rc = walk(p, r.q, f32, true, seg, s);
+  rc = walk(p, r.q, f32, true, at<unsigned char>(ws, r.off_adj), s);
   if (rc == SWIMBA_OK && shared) rc = share_sum(rows, g->dk, g->grad_dtype, a, s);
   if (rc != SWIMBA_OK) return rc;
 
@@ -571,13 +624,16 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   p.s_final = g->dh0;
   p.y = g->dv;
   p.y_bf16 = g->grad_dtype == SWIMBA_BF16;
-  rc = walk(p, r.v, f32, g->grad_dtype == SWIMBA_F32, seg, s);
+  rc = walk(p, r.v, f32, g->grad_dtype == SWIMBA_F32, at<unsigned char>(ws, r.off_v), s);
   if (rc != SWIMBA_OK) return rc;
 
   DecayGradParams d;
   d.zq = zq;
   d.zk = zk;
   d.x_end = nullptr;
+  d.anchor = nullptr;
+  d.seg_chunks = r.q.seg_chunks;
+  d.nseg = r.q.nseg;
   d.diff = at<double>(ws, r.off_diff);
   d.part = a->decay_form == SWIMBA_DECAY_HEAD ? at<double>(ws, r.off_part) : nullptr;
   d.g = a->log_decay;
@@ -593,6 +649,22 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
     hipLaunchKernelGGL(attn_dot_kernel, dim3(a->B * a->H), dim3(kDotThreads), 0, s, end, g->dh_final, x,
                        (int64_t)a->N * a->P);
     d.x_end = x;
+  }
+  if (r.q.nseg > 1) {
+    AnchorParams x;
+    x.h = reinterpret_cast<const float*>(seg);
+    x.adj = at<float>(ws, r.off_adj);
+    x.g = a->log_decay;
+    x.out = at<double>(ws, r.off_anchor);
+    x.n = (int64_t)a->N * a->P;
+    x.H = a->H;
+    x.L = a->L;
+    x.nseg = r.q.nseg;
+    x.seg_chunks = r.q.seg_chunks;
+    x.token_decay = d.token_decay;
+    hipLaunchKernelGGL(attn_anchor_kernel, dim3(r.q.nseg - 1, (unsigned)(a->B * a->H)),
+                       dim3(kDotThreads), 0, s, x);
+    d.anchor = x.out;
   }
   const unsigned wg = (unsigned)(((int64_t)a->B * a->H * r.nc + 3) / 4);
   hipLaunchKernelGGL(attn_decay_diff_kernel, dim3(wg), dim3(256), 0, s, d);

@@ -394,7 +394,10 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   Vals rv;
   float g = 0.f;
   const int nc = (p.L + kChunk - 1) / kChunk;
-  const int j1 = (seg + 1) * p.seg_chunks < nc ? (seg + 1) * p.seg_chunks : nc;
+  // segments are the same chunks in either direction
+  const int low = (down ? p.nseg - 1 - seg : seg) * p.seg_chunks;
+  const int high = low + p.seg_chunks < nc ? low + p.seg_chunks : nc;
+  const int j0 = down ? nc - high : low, j1 = down ? nc - low : high;
   auto chunk_first = [&](int j) { return (down ? nc - 1 - j : j) * kChunk; };
   auto fetch = [&](int j) {
     const int t0 = chunk_first(j), len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
@@ -436,9 +439,9 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       if (Rows::kRounds == 1) rq.load(0);
     }
   };
-  if (kAhead) fetch(seg * p.seg_chunks);
+  if (kAhead) fetch(j0);
 
-  for (int j = seg * p.seg_chunks; j < j1; ++j) {
+  for (int j = j0; j < j1; ++j) {
     const int t0 = chunk_first(j), len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
     auto token = [&](int r) { return (int64_t)(down ? t0 + len - 1 - r : t0 + r); };
     if (!kAhead) fetch(j);
@@ -524,6 +527,8 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       }
     }
 
+    // a wave at its products goes before one that stages rows (2 to 5 % of a walk)
+    __builtin_amdgcn_s_setprio(1);
     f16x ys[2];  // from the state
     f16x yi[2];  // from the chunk (SUMS: apart)
     f16x(&y)[2] = SUMS ? yi : ys;
@@ -673,6 +678,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           for (int kt = 0; kt < KT; ++kt) h[kt] = mma(a[kt], wt[s], h[kt]);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     if (split) c *= exp2_sum(end);
     if (STATE) {
       whole += end;
