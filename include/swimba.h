@@ -504,11 +504,15 @@ typedef struct {
  *   swimba_linear_attention_workspace_size(a) bytes, 256-byte aligned; needed where a
  *   long sequence is walked in segments.  Planned for the current device by
  *   the query and for the device of `stream` by the call.
- * bf16 inputs multiply exactly and sum in fp32; states are fp32.  Non-finite
- * inputs reach every later output of their sequence and head, also across a
- * cleared state, and the outputs up to 63 tokens before them.
- * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256, H * P and
- * G * N < 2^23 (SWIMBA_EUNSUPPORTED above).  L == 0 writes h_final = h0 (or
+ * bf16 inputs multiply exactly and sum in fp32; states are fp32.  An infinity
+ * or a NaN of q reaches its token's outputs, one of k, v or a decay the outputs
+ * of its token and all later ones of its sequence and head (one of v as NaN, in
+ * its own and up to 31 columns next to it), also across a cleared state, and
+ * never an earlier token.
+ * Finite products |q| |k| |v| have to stay below 1e18 (partial sums carry
+ * factors of up to 2^64).
+ * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256, L <= 2^30, H * P
+ * and G * N < 2^23 (SWIMBA_EUNSUPPORTED above).  L == 0 writes h_final = h0 (or
  * zeros).
  */
 size_t swimba_linear_attention_workspace_size(const swimba_linear_attention_args* a);

@@ -150,7 +150,8 @@ typedef uint32_t u4x __attribute__((ext_vector_type(4)));
 template <typename T, int PAD, int THREADS, bool LOOSE>
 struct RowStage {
   static constexpr int kPer = PAD / kPack, kN = kChunk * kPer / THREADS;
-  static constexpr int kRound = kN < 8 ? kN : 8, kRounds = kN / kRound;
+  static constexpr int kMost = sizeof(T) == 4 ? 4 : 8;  // 32 registers
+  static constexpr int kRound = kN < kMost ? kN : kMost, kRounds = kN / kRound;
   static constexpr int kStep = THREADS / kPer;      // rows between a thread's packs
   static constexpr int kQuads = sizeof(T) / 2;      // 16-byte registers per pack
   static constexpr int kWords = 4 * kQuads;
@@ -232,6 +233,32 @@ struct RowStage {
         for (int k = 0; k < kWords; ++k) w[k] = n > k ? w[k] : 0u;
       }
       __builtin_memcpy(out, w, sizeof(w));
+    }
+  }
+
+  // An infinity or a NaN among the packs of a round (or in rows left out).
+  __device__ __forceinline__ bool wild() const {
+    if constexpr (sizeof(T) == 2) {
+      typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+      us2 m = {0, 0};
+#pragma unroll
+      for (int i = 0; i < kRound; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          m = __builtin_elementwise_max(m, __builtin_bit_cast(us2, v[i][0][k] & 0x7fff7fffu));
+      return m.x >= 0x7f80 || m.y >= 0x7f80;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kRound; ++i)
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w = v[i][q][k] & 0x7fffffffu;
+            m = m > w ? m : w;
+          }
+      return m >= 0x7f800000u;
     }
   }
 
@@ -468,12 +495,40 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     }
     const float read = exp2_sum(sum) * c;
     const float write = split ? exp2_sum(-sum) / c : exp2_sum(end - sum);
+    float poison = 1.f;
     __syncthreads();  // everyone is done with the last chunk
     gHi[lane] = hi;
     gLo[lane] = (float)(sum - (double)hi);
     gRead[lane] = read;
     gWrite[lane] = write;
+    const bool wild = __ballot(rv.wild()) != 0;
     rv.store(0, sV, VS);
+    if (wild) {
+      // An infinity or a NaN in v_s may reach y_t for t >= s only, and a product of
+      // the matrix units with a zero score would spread it.  It is taken out of
+      // the slab, and the factors of the results from the first one on (all 32
+      // columns) and the state's scale become NaN instead.
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_wave_barrier();
+      int bad = kChunk;
+#pragma unroll 1
+      for (int r = 31; r >= 0; --r) {
+        TI* at = sV + (32 * half + r) * VS + col;
+        if (!(fabsf(to_f32(*at)) < __builtin_inff())) {
+          bad = 32 * half + r;
+          *at = TI(0);
+        }
+      }
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) {
+        const int o = __shfl_xor(bad, m);
+        bad = o < bad ? o : bad;
+      }
+      if (lane >= bad) gRead[lane] = __builtin_nanf("");
+      poison = bad < kChunk ? __builtin_nanf("") : 1.f;
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    }
     rk.store(0, sK, KS);
 #pragma unroll
     for (int r = 1; r < Rows::kRounds; ++r) {
@@ -680,6 +735,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     }
     __builtin_amdgcn_s_setprio(0);
     if (split) c *= exp2_sum(end);
+    c *= poison;
     if (STATE) {
       whole += end;
       continue;

@@ -443,7 +443,7 @@ int validate_attention(int B, int L, int H, int G, int N, int P, swimba_dtype in
   if (B < 0 || L < 0 || H < 1 || G < 1 || N < 1 || P < 1 || H % G != 0) return SWIMBA_EINVAL;
   if (!dtype_ok(in) || !dtype_ok(out)) return SWIMBA_EINVAL;
   if (form != SWIMBA_DECAY_HEAD && form != SWIMBA_DECAY_TOKEN) return SWIMBA_EINVAL;
-  if (N > 256) return SWIMBA_EUNSUPPORTED;
+  if (N > 256 || L > (1 << 30)) return SWIMBA_EUNSUPPORTED;
   // workgroups are counted in 31 bits
   if ((int64_t)B * H * ((P + 15) / 16) > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
   // 64 rows of a token's heads within 2^31 bytes

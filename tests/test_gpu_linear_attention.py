@@ -329,3 +329,76 @@ def test_operands_of_less_than_a_pack(shape):
         close(y, want["y"], size["y"], refs.roundings(N, P, L), "y")
         close(h, want["h_final"], size["h_final"], refs.roundings(N, P, L), "h")
         check_backward(dev, ref, shape, "f32")
+
+
+@pytest.mark.parametrize("dtype,N,P", [("bf16", 64, 64), ("f32", 33, 20), ("bf16", 128, 96)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_non_finite_values_never_reach_earlier_tokens(dtype, N, P, bad):
+    # a padded batch may hold anything behind its last token, and the token before
+    # it lies in the same chunk
+    L, s = 150, 77
+    dev, ref = make(1, L, 2, 1, N, P, dtype=dtype, form="token", h0=True, seed=51)
+    y, h = forward(dev)
+    want, size = refs.attention(*args(ref)), refs.attention_sizes(*args(ref))
+    for name in ("q", "k", "v", "log_decay"):
+        if name == "log_decay" and bad < 0:
+            continue  # clears the state
+        d = {n: x.clone() for n, x in dev.items() if x is not None}
+        d[name][0, s].view(-1)[1] = bad  # key 1, value (head 0, column 1) or head 1
+        y2, h2 = forward(d)
+        if name == "log_decay":
+            # that chunk of that head takes the decays pair by pair instead of as two
+            # factors: other roundings, each result within the same bound of the exact
+            # one as any output
+            close(y2[:, :s], want["y"][:, :s], size["y"][:, :s], refs.roundings(N, P, L, dtype == "f32"), name)
+        else:
+            assert torch.equal(y2[:, :s], y[:, :s]), name
+        if name == "q":
+            keep = torch.arange(L, device=DEV) != s
+            assert torch.equal(y2[:, keep], y[:, keep]) and torch.equal(h2, h)
+            assert not torch.isfinite(y2[:, s]).any()
+        elif name == "v":
+            assert not torch.isfinite(y2[0, s:, 0, 1]).any() and not torch.isfinite(h2[0, 0, :, 1]).any()
+            # the columns next to it go with it, 32 together; others and other heads do not
+            assert torch.equal(y2[0, :, 0, 32:], y[0, :, 0, 32:]) and torch.equal(y2[0, :, 1], y[0, :, 1])
+            assert torch.equal(h2[0, 0, :, 32:], h[0, 0, :, 32:]) and torch.equal(h2[0, 1], h[0, 1])
+        elif name == "k":
+            assert not torch.isfinite(y2[:, s:]).any() and not torch.isfinite(h2[0, :, 1]).any()
+        else:
+            assert not torch.isfinite(y2[0, s:, 1]).any() and torch.equal(y2[0, :, 0], y[0, :, 0])
+
+
+def test_non_finite_gradients_stay_behind():
+    # dy of a token with rubbish reaches dq of that token and what came before it,
+    # not dq of other tokens; dk and dv of later tokens stay as they are
+    L, s = 100, 41
+    dev, _ = make(1, L, 2, 2, 32, 32, dtype="bf16", grad=True, seed=52)
+    a = [dev[n] for n in ("q", "k", "v", "log_decay")]
+    g = swimba.linear_attention_backward(*a, dev["dy"], h0=dev["h0"], dh_final=dev["dh"])
+    dy = dev["dy"].clone()
+    dy[0, s, 0, 3] = float("nan")
+    b = swimba.linear_attention_backward(*a, dy, h0=dev["h0"], dh_final=dev["dh"])
+    keep = torch.arange(L, device=DEV) != s
+    assert torch.equal(g["dq"][:, keep], b["dq"][:, keep]) and not torch.isfinite(b["dq"][0, s, 0]).any()
+    for n in ("dk", "dv"):
+        assert torch.equal(g[n][:, s + 1:], b[n][:, s + 1:]) and torch.equal(g[n][:, :, 1], b[n][:, :, 1]), n
+
+
+def test_fp32_inputs_bf16_results():
+    dev, ref = make(2, 90, 4, 2, 40, 24, dtype="f32", seed=61)
+    y, h = forward(dev, y_dtype=torch.bfloat16)
+    want, size = refs.attention(*args(ref)), refs.attention_sizes(*args(ref))
+    close(y, want["y"], size["y"], refs.roundings(40, 24, 90, False), "y")
+
+
+def test_large_and_small_magnitudes():
+    for scale in (1e5, 1e-6):
+        dev, ref = make(1, 140, 2, 1, 32, 32, dtype="f32", seed=71)
+        for n in ("q", "k", "v", "h0"):
+            f = scale * scale if n == "h0" else scale
+            dev[n] = dev[n] * f
+            ref[n] = dev[n].double().cpu().numpy()
+        y, h = forward(dev)
+        want, size = refs.attention(*args(ref)), refs.attention_sizes(*args(ref))
+        close(y, want["y"], size["y"], refs.roundings(32, 32, 140), "y")
+        close(h, want["h_final"], size["h_final"], refs.roundings(32, 32, 140), "h")
