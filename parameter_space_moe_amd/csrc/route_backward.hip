@@ -67,10 +67,17 @@ struct Slopes {
         any(reinterpret_cast<int32_t*>(dense + kTile * kDense)) {}
 };
 
+// Waves per SIMD that the registers have to leave room for: what the LDS of the
+// expert count allows, and fewer where a step would spill (its reloads wait for
+// the rows on their way).
+constexpr int least_waves(size_t elem, int et, int rows) {
+  return et == 4 ? 1 : (elem == 4 || et == 2 || rows != kWhole ? 2 : 3);
+}
+
 // ET: expert tiles of 16; K: most slots per token that are held in registers
 // (0: any number of slots); ROWS: kLoose, kWhole or kTiny.
 template <typename TI, typename TO, int ET, int K, int ROWS>
-__global__ __launch_bounds__(kThreads, (sizeof(TI) == 4 || ET > 1) ? 2 : 3) void route_grad_kernel(RouteGradParams p) {
+__global__ __launch_bounds__(kThreads, least_waves(sizeof(TI), ET, ROWS)) void route_grad_kernel(RouteGradParams p) {
   using Table = Slopes<ET>;
   constexpr bool WHOLE = ROWS == kWhole;
   constexpr int kDense = Table::kDense;
@@ -277,15 +284,16 @@ struct RouteGradPlan {
 // As many workgroups as the device holds at once (by registers and LDS three
 // per CU up to 16 experts with bf16 x, two up to 32 and with fp32 x, one
 // beyond), splits of whole 64-token tiles, and no more of them than keeps the
-// partial sums (8 E bytes per channel and split, out and in) at half the stream
-// of x and dx.
+// partial sums (8 E bytes per channel and split, out and in) within the stream of
+// x and dx: a tile of 64 experts takes a workgroup 7 us, as long as the sums of
+// 30 MB.
 RouteGradPlan plan(int64_t T, int D, int E, int elem, int dev) {
   RouteGradPlan r;
   r.slabs = (D + kSlab - 1) / kSlab;
   const int64_t tiles = (T + kTile - 1) / kTile;
-  const int per_cu = E > 32 ? 1 : (E > 16 || elem == 4 ? 2 : 3);
+  const int per_cu = E > 32 ? 1 : (E > 16 || elem == 4 || D % 4 != 0 ? 2 : 3);
   int64_t want = (int64_t)per_cu * device_cus(dev) / r.slabs;
-  const int64_t least = (16LL * E / (2 * elem) + kTile - 1) / kTile;  // tiles per split
+  const int64_t least = (8LL * E / (2 * elem) + kTile - 1) / kTile;  // tiles per split
   if (want > tiles / least) want = tiles / least;
   if (want < 1) want = 1;
   const int64_t per = (tiles + want - 1) / want;
