@@ -35,6 +35,10 @@
  *            streams arrive per routing slot; the injection
  *            Delta sum_j g_j B_j X_j and the readout vector sum_j g_j C_j
  *            are mixed ([SW] "Kernmechanisme van Swimba").
+ *   tokens:  slots sorted by expert, rows copied to them and brought back
+ *            weighted by the gates, and the gradients; the router's backward.
+ *   linear attention: one scalar decay per head, a state of N keys by P
+ *            values, on the matrix units; its backward and decode step.
  *
  * Conventions (all entry points):
  *   - Every tensor argument is a DEVICE pointer owned by the caller, dense and
@@ -542,8 +546,8 @@ typedef struct {
  */
 size_t swimba_linear_attention_backward_workspace_size(
     const swimba_linear_attention_grad_args* g);
-int swimba_linear_attention_backward(const swimba_linear_attention_grad_args* g, void* ws, size_t ws_bytes,
-                              hipStream_t stream);
+int swimba_linear_attention_backward(const swimba_linear_attention_grad_args* g, void* ws,
+                                     size_t ws_bytes, hipStream_t stream);
 
 typedef struct {
   int B, H, G, N, P;

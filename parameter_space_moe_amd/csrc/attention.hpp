@@ -21,6 +21,18 @@
 // token enters on the value side (w * V), which a wave reads for itself, so
 // that K stays as it came.
 //
+// What bounds it (MI355X, bf16, N = 128; 1280-column 64K-token prompt, 41 chunks
+// by each of 500 workgroups, two per CU): 8.6 us per chunk and CU, of which the
+// matrix units are busy 29 % (98 instructions of 32 cycles per wave and chunk)
+// and the VALU 41 % (1110 instructions, most of them the splits below); the two
+// hardly overlap with two waves per SIMD, the registers' limit (64 of state, 32
+// of results, 48 of rows on their way).  Memory would allow a third of the time.
+// Measured on the way: loads issued under per-pack branches waited for each
+// other (34 us per chunk); one workgroup per CU, when the LDS passed 80 KB by
+// half a KB, cost 1.6 x; an exponential per pair instead of two factors per
+// token 1.2 x; a full unroll of the token steps, or the order of matrix and vector
+// instructions fixed by hand, 0.95 to 1 x.
+//
 // Roundings.  bf16 inputs multiply exactly.  What is computed in fp32 and
 // enters a product (decayed scores, state, decayed values) is split into two
 // or three bf16 terms that sum to it within 2^-16 or 2^-24 of its size, two
@@ -110,7 +122,8 @@ __device__ __forceinline__ f16x mma(float a, float b, f16x c) {
 // Eight rows (half the lanes four each, twice) of one column from a row-major
 // LDS tile: the transposing read hands lane i of 16 the column i of a block of
 // 4 rows x 16 columns of which it points at row i / 4, columns 4 (i % 4)..
-__device__ __forceinline__ bf8x column8(const bf16_t* tile, int stride, int row, int col, int lane) {
+__device__ __forceinline__ bf8x column8(const bf16_t* tile, int stride, int row, int col,
+                                        int lane) {
   typedef __attribute__((address_space(3))) s4x* lds_s4;
   const bf16_t* p = tile + (row + 8 * (lane >> 5) + ((lane & 15) >> 2)) * stride + col +
                     16 * ((lane >> 4) & 1) + 4 * (lane & 3);
@@ -289,7 +302,8 @@ template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp_add(double v) {
   const uint64_t b = __double_as_longlong(v);
   const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  const uint32_t hi =
+      __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
   return v + __longlong_as_double(((uint64_t)hi << 32) | lo);
 }
 __device__ __forceinline__ double wave_prefix(double v) {
@@ -602,8 +616,8 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           for (int a = 0; a < 4; ++a)
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-              const float4 x = *reinterpret_cast<const float4*>(sQ + (32 * tt + col) * QS + 32 * kt +
-                                                                8 * a + 4 * half);
+              const float4 x = *reinterpret_cast<const float4*>(sQ + (32 * tt + col) * QS +
+                                                                32 * kt + 8 * a + 4 * half);
               ys[tt] = mma(x.x, h[kt][4 * a], ys[tt]);
               ys[tt] = mma(x.y, h[kt][4 * a + 1], ys[tt]);
               ys[tt] = mma(x.z, h[kt][4 * a + 2], ys[tt]);

@@ -684,8 +684,8 @@ size_t swimba_linear_attention_backward_workspace_size(
   return validate_attention_grad(g) == SWIMBA_OK ? attention_backward_bytes(g, -1) : 0;
 }
 
-int swimba_linear_attention_backward(const swimba_linear_attention_grad_args* g, void* ws, size_t ws_bytes,
-                              hipStream_t stream) {
+int swimba_linear_attention_backward(const swimba_linear_attention_grad_args* g, void* ws,
+                                     size_t ws_bytes, hipStream_t stream) {
   int rc = validate_attention_grad(g);
   if (rc != SWIMBA_OK) return rc;
   rc = validate_attention_inputs(&g->fwd);

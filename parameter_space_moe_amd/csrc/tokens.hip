@@ -161,7 +161,7 @@ struct MoveParams {
 // The packs of a thread: token and first element of each, `on` where there is
 // one.  Work is laid out over packs, not rows, so that every row width fills
 // the workgroups alike; all of a thread's packs are loaded before any is used
-// (the loads of one pack after the other left the copy out at 3.6 TB/s).
+// (one pack after the other, the copy out ran at 3.6 TB/s).
 struct Packs {
   int64_t t[kMovePacks];
   int c[kMovePacks];
@@ -226,7 +226,8 @@ __global__ __launch_bounds__(kMoveThreads) void dispatch_kernel(MoveParams p) {
 #pragma unroll
     for (int i = 0; i < kMovePacks; ++i)
       if (m.on[i] && is_row(at[i], n))
-        store_pack(rows + (int64_t)at[i] * p.D + m.c[i], v[i], ROWS == kWhole ? kPack : p.D - m.c[i]);
+        store_pack(rows + (int64_t)at[i] * p.D + m.c[i], v[i],
+                   ROWS == kWhole ? kPack : p.D - m.c[i]);
   }
 }
 
