@@ -52,7 +52,7 @@ enum Rows { kLoose = 0, kWhole = 1, kTiny = 2 };
 
 // N elements of a row on their way: one whole load that stays inside the tensor
 // whatever the row width, so that a run of them is issued without branches
-// between.  Where the tensor's last row ends inside it the load starts `back`
+// between.  Where the tensor ends inside it the load starts `back`
 // elements (back_of) earlier; get() moves the elements up again and clears
 // those from `left`, the elements left in the row, on.
 template <typename T, int N>
@@ -95,10 +95,14 @@ struct Loose {
   }
 };
 
-// How far a load of N elements, `left` of them in the row, has to be moved back.
+// How far a load of N elements has to be moved back to stay inside a tensor of at
+// least N: `left` (above 0) elements of the row and `behind` rows of `width`
+// follow.  Rows narrower than N may need it before the last one.
 template <int N>
-__device__ __forceinline__ int back_of(bool last_row, int left) {
-  return last_row && left > 0 && left < N ? N - left : 0;
+__host__ __device__ __forceinline__ int back_of(int64_t behind, int width, int left) {
+  const int rows = behind < N ? (int)behind : N, w = width < N ? width : N;
+  const int rest = rows * w + (left < N ? left : N);
+  return left > 0 && rest < N ? N - rest : 0;
 }
 
 }  // namespace swimba

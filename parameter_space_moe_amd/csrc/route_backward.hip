@@ -127,7 +127,7 @@ void route_grad_kernel(RouteGradParams p) {
   constexpr int kSteps = 8;
   Loose<TI, 4> xr[kSteps];
   auto back = [&](int64_t t) {
-    return ROWS == kLoose ? back_of<4>(t == p.T - 1, left) : 0;
+    return ROWS == kLoose ? back_of<4>(p.T - 1 - t, p.D, left) : 0;
   };
   auto fetch = [&](int64_t t0) {
 #pragma unroll

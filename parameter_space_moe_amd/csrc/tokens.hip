@@ -195,13 +195,13 @@ struct RowPack {
   __device__ __forceinline__ void load(const T* base, int64_t row, int64_t rows, int D, int c) {
     const T* p = base + row * D + c;
     if constexpr (ROWS == kWhole) v.whole(p);
-    else if constexpr (ROWS == kLoose) v.whole(p - back_of<kPack>(row == rows - 1, D - c));
+    else if constexpr (ROWS == kLoose) v.whole(p - back_of<kPack>(rows - 1 - row, D, D - c));
     else v.few(p, D - c);
   }
   __device__ __forceinline__ Pack<T> get(int64_t row, int64_t rows, int D, int c) const {
     Pack<T> p;
     if constexpr (ROWS == kWhole) v.get(0, kPack, p.v);
-    else v.get(ROWS == kLoose ? back_of<kPack>(row == rows - 1, D - c) : 0, D - c, p.v);
+    else v.get(ROWS == kLoose ? back_of<kPack>(rows - 1 - row, D, D - c) : 0, D - c, p.v);
     return p;
   }
 };

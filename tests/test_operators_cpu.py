@@ -235,3 +235,41 @@ def test_route_and_combine_reference_gradients_are_differences():
     d, e = rng.standard_normal(rows.shape), rng.standard_normal(gate.shape)  # bilinear: exact
     assert abs((drows * d).sum() - (dy * refs.combine(d, pos, gate)).sum()) < 1e-12
     assert abs((dg * e).sum() - (dy * refs.combine(rows, pos, e)).sum()) < 1e-12
+
+
+PACKS = r'''
+#include <cstdio>
+#include "pack.hpp"
+using namespace swimba;
+// Every whole load of every row has to lie inside the tensor, and to hold the
+// row's elements from its `back`-th on.
+template <int N>
+int check() {
+  int bad = 0;
+  for (int rows = 1; rows <= 24; ++rows)
+    for (int width = 1; width <= 2 * N + 3; ++width) {
+      if (rows * width < N) continue;  // taken element by element
+      for (int r = 0; r < rows; ++r)
+        for (int c = 0; c < width; c += N) {
+          const int left = width - c, back = back_of<N>(rows - 1 - r, width, left);
+          const int first = r * width + c - back, used = left < N ? left : N;
+          if (back < 0 || first < 0 || first + N > rows * width || back + used > N) {
+            if (bad++ < 5) std::printf("%d: %d x %d, row %d column %d\n", N, rows, width, r, c);
+          }
+        }
+    }
+  return bad;
+}
+int main() { return check<4>() + check<8>() != 0; }
+'''
+
+
+def test_whole_loads_stay_inside_the_tensor(tmp_path):
+    f = tmp_path / "packs.hip"
+    f.write_text(PACKS)
+    exe = tmp_path / "packs"
+    subprocess.run(["/opt/rocm/bin/hipcc", "--offload-host-only", "-std=c++17",
+                    "-I" + os.path.join(ROOT, "parameter_space_moe_amd", "csrc"), str(f), "-o",
+                    str(exe)], check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
