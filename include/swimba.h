@@ -425,7 +425,8 @@ int swimba_sort_tokens(const int32_t* idx, int64_t T, int E, int k, int32_t* ord
  *   pos   [T, k]  rows of the slots, each used once; a value outside
  *                 [0, T * k) is a slot without a row
  * Rows that no slot has are left as they were.  Its gradient is
- * swimba_combine_tokens of the rows' gradients without gates.
+ * swimba_combine_tokens of the rows' gradients without gates.  rows must not
+ * overlap x.
  */
 int swimba_dispatch_tokens(const void* x, swimba_dtype x_dtype, const int32_t* pos, int64_t T,
                            int D, int k, void* rows, hipStream_t stream);
@@ -433,7 +434,8 @@ int swimba_dispatch_tokens(const void* x, swimba_dtype x_dtype, const int32_t* p
 /*
  * swimba_combine_tokens -- y[t, :] = sum_j gate[t, j] rows[pos[t, j], :], over
  * the slots that have a row, in slot order, in fp32 (zero without any).
- *   gate  [T, k] fp32, or NULL for ones;  y [T, D] out, dtype y_dtype
+ *   gate  [T, k] fp32, or NULL for ones;  y [T, D] out, dtype y_dtype; it must
+ *         not overlap rows
  */
 int swimba_combine_tokens(const void* rows, swimba_dtype rows_dtype, const int32_t* pos,
                           const float* gate, int64_t T, int D, int k, void* y,
@@ -466,6 +468,7 @@ int swimba_combine_tokens_backward(const void* rows, swimba_dtype rows_dtype, co
  * the gate is constant and both gradients are zero.  Sums are fp32 in a fixed
  * order (deterministic).  Values of x must be finite: an infinity or a NaN in
  * a token that has an expert makes its channel of dWr NaN for every expert.
+ * dx must not overlap x.
  * Constraints: those of swimba_route.  T == 0 writes dWr = 0.
  */
 size_t swimba_route_backward_workspace_size(int64_t T, int D, int E);
@@ -515,9 +518,11 @@ typedef struct {
  * never an earlier token.
  * Finite products |q| |k| |v| have to stay below 1e18 (partial sums carry
  * factors of up to 2^64).
+ * h_final may be h0 itself; otherwise no output overlaps an input or another
+ * output.
  * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256, L <= 2^30, H * P
- * and G * N < 2^23 (SWIMBA_EUNSUPPORTED above).  L == 0 writes h_final = h0 (or
- * zeros).
+ * and G * N < 2^23, B * H * ceil(P / 32) < 2^24 (SWIMBA_EUNSUPPORTED above).
+ * L == 0 writes h_final = h0 (or zeros).
  */
 size_t swimba_linear_attention_workspace_size(const swimba_linear_attention_args* a);
 int swimba_linear_attention(const swimba_linear_attention_args* a, void* ws, size_t ws_bytes,
@@ -541,8 +546,12 @@ typedef struct {
  * swimba_linear_attention_backward -- gradients of swimba_linear_attention, from its inputs
  * (nothing of the forward pass is kept).  Workspace as there, sized by
  * swimba_linear_attention_backward_workspace_size(g).  Every output is deterministic.
- * Constraints: those of swimba_linear_attention, and P <= 256.  L == 0 or B == 0
- * writes dh0 = dh_final (or zeros) and a zero dlog_decay [H].
+ * dh0 may be dh_final itself; otherwise no output overlaps an input or another
+ * output.
+ * Constraints: those of swimba_linear_attention, and P <= 256, B * H < 2^22,
+ * B * H * ceil(N / 32) < 2^24, B * H * (L + 64) and B * L * G * ceil(N / 8) below
+ * 2^32 - 256.  L == 0 or B == 0 writes dh0 = dh_final (or zeros) and a zero
+ * dlog_decay [H].
  */
 size_t swimba_linear_attention_backward_workspace_size(
     const swimba_linear_attention_grad_args* g);

@@ -330,14 +330,14 @@ __global__ __launch_bounds__(256) void attn_step_kernel(AttnStepParams p) {
 }
 
 __global__ __launch_bounds__(256) void attn_copy_kernel(const float* in, float* out, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) out[i] = in != nullptr ? in[i] : 0.f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    out[i] = in != nullptr ? in[i] : 0.f;
 }
 
 int copy_or_zero(const float* in, float* out, int64_t n, hipStream_t s) {
   if (n <= 0) return SWIMBA_OK;
-  hipLaunchKernelGGL(attn_copy_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, in, out,
-                     n);
+  const int64_t wg = (n + 255) / 256 < (1 << 20) ? (n + 255) / 256 : 1 << 20;
+  hipLaunchKernelGGL(attn_copy_kernel, dim3((unsigned)wg), dim3(256), 0, s, in, out, n);
   return checked();
 }
 
@@ -611,6 +611,15 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   if (rc == SWIMBA_OK && shared) rc = share_sum(rows, g->dk, g->grad_dtype, a, s);
   if (rc != SWIMBA_OK) return rc;
 
+  // <h, dL/dh> behind the last token, before dh0 is written (it may be dh_final)
+  double* x_end = nullptr;
+  if (g->dh_final != nullptr) {
+    x_end = at<double>(ws, r.off_x);
+    hipLaunchKernelGGL(attn_dot_kernel, dim3(a->B * a->H), dim3(kDotThreads), 0, s, end,
+                       g->dh_final, x_end, (int64_t)a->N * a->P);
+    if (checked() != SWIMBA_OK) return SWIMBA_EHIP;
+  }
+
   // dv = backward walk(K, Q, dY), whose last state is dh0
   p = base_params(a);
   p.q = k;
@@ -633,7 +642,7 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   DecayGradParams d;
   d.zq = zq;
   d.zk = zk;
-  d.x_end = nullptr;
+  d.x_end = x_end;
   d.anchor = nullptr;
   d.seg_chunks = r.q.seg_chunks;
   d.nseg = r.q.nseg;
@@ -647,12 +656,6 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   d.ctiles = r.ntiles;
   d.nc = r.nc;
   d.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
-  if (g->dh_final != nullptr) {
-    double* x = at<double>(ws, r.off_x);
-    hipLaunchKernelGGL(attn_dot_kernel, dim3(a->B * a->H), dim3(kDotThreads), 0, s, end,
-                       g->dh_final, x, (int64_t)a->N * a->P);
-    d.x_end = x;
-  }
   if (r.q.nseg > 1) {
     AnchorParams x;
     x.h = reinterpret_cast<const float*>(seg);
@@ -705,7 +708,6 @@ int launch_attention_step(const swimba_linear_attention_step_args* a, int dev, h
   p.slices = (a->P + p.slice - 1) / p.slice;
   p.cg = (p.slice + V - 1) / V;
   const int64_t grid = heads * p.slices;
-  if (grid > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
   const dim3 g((unsigned)grid), t(256);
   const bool bf = a->in_dtype == SWIMBA_BF16;
   if (vec && bf) hipLaunchKernelGGL((attn_step_kernel<bf16_t, 4>), g, t, 0, s, p);

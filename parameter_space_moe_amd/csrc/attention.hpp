@@ -907,7 +907,6 @@ int attn_launch(const AttnParams& p, hipStream_t s) {
   const int groups = p.H / p.qshare, units = p.qshare * p.ctiles;
   const int64_t grid = (int64_t)p.B * groups * (MODE == kAttnState ? p.nseg - 1 : p.nseg) *
                        ((units + W - 1) / W);
-  if (grid > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
   using Sh = AttnShape<TI, KT, W>;
   constexpr size_t lds = MODE == kAttnState ? Sh::kStateBytes : Sh::kBytes;
   static_assert(lds <= 160 * 1024, "a CU's LDS");

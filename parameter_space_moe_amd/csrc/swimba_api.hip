@@ -444,8 +444,9 @@ int validate_attention(int B, int L, int H, int G, int N, int P, swimba_dtype in
   if (!dtype_ok(in) || !dtype_ok(out)) return SWIMBA_EINVAL;
   if (form != SWIMBA_DECAY_HEAD && form != SWIMBA_DECAY_TOKEN) return SWIMBA_EINVAL;
   if (N > 256 || L > (1 << 30)) return SWIMBA_EUNSUPPORTED;
-  // workgroups are counted in 31 bits
-  if ((int64_t)B * H * ((P + 15) / 16) > 0x7fffffff) return SWIMBA_EUNSUPPORTED;
+  // a launch counts threads in 32 bits: at most 256 for 32 columns of a head's state
+  if ((int64_t)B * H >= (1 << 24) || (int64_t)B * H * ((P + 31LL) / 32) >= (1 << 24))
+    return SWIMBA_EUNSUPPORTED;
   // 64 rows of a token's heads within 2^31 bytes
   if ((int64_t)H * P >= (1 << 23) || (int64_t)G * N >= (1 << 23)) return SWIMBA_EUNSUPPORTED;
   return SWIMBA_OK;
@@ -473,7 +474,15 @@ int validate_attention_grad(const swimba_linear_attention_grad_args* g) {
   if (rc != SWIMBA_OK) return rc;
   if (!dtype_ok(g->grad_dtype)) return SWIMBA_EINVAL;
   // the values are rows of the dq and dk walks
-  return g->fwd.P > 256 ? SWIMBA_EUNSUPPORTED : SWIMBA_OK;
+  const swimba_linear_attention_args& a = g->fwd;
+  if (a.P > 256) return SWIMBA_EUNSUPPORTED;
+  // threads of a launch, as above: of the dq and dk walks, of X behind the last
+  // token, of the decays' gradients and of the heads' sums
+  const int64_t bh = (int64_t)a.B * a.H, limit = int64_t(1) << 32;
+  if (bh * ((a.N + 31) / 32) >= (1 << 24) || bh * 1024 >= limit || bh * (a.L + 64LL) >= limit ||
+      (int64_t)a.B * a.L * a.G * ((a.N + 7) / 8) >= limit - 256)
+    return SWIMBA_EUNSUPPORTED;
+  return SWIMBA_OK;
 }
 
 }  // namespace

@@ -293,7 +293,8 @@ template <typename TI, typename TY, typename TO, int PER, int ROWS>
 __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradParams p) {
   __shared__ float part[4][2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = PER == 4 ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+  const int64_t wg = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t t = PER == 4 ? wg : wg * 4 + wave;
   if (t >= p.T) return;  // whole waves, and no barrier follows where PER is 1
   const TY* dyb = static_cast<const TY*>(p.dy);
   const TI* rows = static_cast<const TI*>(p.rows);
@@ -387,7 +388,7 @@ MoveParams move_params(const void* src, void* dst, const int32_t* pos, const flo
 bool move_grid(const MoveParams& p, dim3* grid) {
   const int64_t per = kMoveThreads * kMovePacks;
   const int64_t b = (p.packs + per - 1) / per;
-  if (b > 0x7fffffff) return false;
+  if (b >= (1 << 24)) return false;  // threads are counted in 32 bits: 2^37 elements
   *grid = dim3((unsigned)b);
   return true;
 }
@@ -400,7 +401,9 @@ int rows_kind(int D, int64_t least) {
 
 template <typename TI, typename TY, typename TO, int PER>
 int launch_combine_grad_rows(const CombineGradParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)((p.T + 4 / PER - 1) / (4 / PER))), th(256);
+  // threads of a grid's row are counted in 32 bits
+  const int64_t wg = (p.T + 4 / PER - 1) / (4 / PER), row = wg < (1 << 22) ? wg : 1 << 22;
+  const dim3 grid((unsigned)row, (unsigned)((wg + row - 1) / row)), th(256);
   const int kind = rows_kind(p.D, p.T);
   if (kind == kWhole)
     hipLaunchKernelGGL((combine_grad_kernel<TI, TY, TO, PER, kWhole>), grid, th, 0, s, p);

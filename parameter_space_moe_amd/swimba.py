@@ -917,6 +917,8 @@ def linear_attention(q, k, v, log_decay, h0=None, y=None, h_final=None, y_dtype=
     swimba_linear_attention).  q, k [B,L,G,N], v [B,L,H,P] (f32 or bf16, H a multiple
     of G); log_decay [H] or [B,L,H] f32; h0 [B,H,N,P] f32.  Returns (y [B,L,H,P],
     h_final [B,H,N,P] f32 or None)."""
+    if not (isinstance(v, torch.Tensor) and v.dim() == 4 and q.dim() == 4):
+        raise ValueError("q must be [B, L, G, N] and v [B, L, H, P]")
     if y is None:
         y = torch.empty(v.shape, dtype=y_dtype or v.dtype, device=v.device)
     if h_final is None and want_state:

@@ -402,3 +402,18 @@ def test_large_and_small_magnitudes():
         want, size = refs.attention(*args(ref)), refs.attention_sizes(*args(ref))
         close(y, want["y"], size["y"], refs.roundings(32, 32, 140), "y")
         close(h, want["h_final"], size["h_final"], refs.roundings(32, 32, 140), "h")
+
+
+@pytest.mark.parametrize("L", [100, 1500])  # whole walks and segments
+def test_states_in_place(L):
+    dev, _ = make(1, L, 4, 2, 64, 64, grad=True, seed=21)
+    grads = dict(h0=dev["h0"], dh_final=dev["dh"])
+    ops = [dev[n] for n in ("q", "k", "v", "log_decay")]
+    y, h = forward(dev)
+    want = swimba.linear_attention_backward(*ops, dev["dy"], **grads)
+    st = dev["h0"].clone()
+    y2, h2 = swimba.linear_attention(*ops, h0=st, h_final=st)
+    assert torch.equal(y, y2) and torch.equal(h, h2) and h2 is st
+    adj = dev["dh"].clone()
+    got = swimba.linear_attention_backward(*ops, dev["dy"], h0=dev["h0"], dh_final=adj, out={"dh0": adj})
+    assert all(torch.equal(want[n], got[n]) for n in want)

@@ -328,3 +328,46 @@ def test_tensors_of_less_than_a_pack(T, D):
         wx, wW, sx, sW = refs.route_backward(up(x), up(W), two.cpu().numpy(), up(g2), up(dg2))
         assert (np.abs(up(dx) - wx) <= 10 * refs.U32 * sx).all()
         assert (np.abs(up(dW) - wW) <= (T + 10) * refs.U32 * sW).all()
+
+
+@pytest.mark.parametrize("D", [1, 2, 3, 5, 9])
+@pytest.mark.parametrize("T", [9, 300])
+def test_rows_narrower_than_a_pack(T, D):
+    gen = torch.Generator().manual_seed(T + D)
+    idx = torch.from_numpy(make_idx(T, 4, 2, 0.1, seed=D)).to(DEV)
+    for dt in (torch.bfloat16, torch.float32):
+        x = torch.randn(T, D, generator=gen).to(dt).to(DEV)
+        order, pos, off = swimba.sort_tokens(idx, 4)
+        n = int(off[-1])
+        rows = swimba.dispatch_tokens(x, pos)
+        assert torch.equal(rows[:n], x[order[:n].long() // 2])
+        rows[n:] = 0
+        gate = torch.rand(T, 2, generator=gen).to(DEV)
+        y = swimba.combine_tokens(rows, pos, gate, y_dtype=torch.float32)
+        g = torch.where(pos >= 0, gate, torch.zeros_like(gate)).double()
+        want = g.sum(1, keepdim=True) * x.double()
+        size = want.abs() + 1e-30
+        assert ((y.double() - want).abs() <= 4 * refs.U32 * size).all()
+        drows, dgate = swimba.combine_tokens_backward(rows, pos, gate, x, grad_dtype=torch.float32)
+        want = gate.flatten()[order[:n].long()][:, None].double() * x[order[:n].long() // 2].double()
+        assert ((drows[:n].double() - want).abs() <= 2 * refs.U32 * want.abs()).all()
+        want = torch.where(pos >= 0, (x.double() ** 2).sum(1, keepdim=True), 0.0)
+        assert ((dgate.double() - want).abs() <= (D + 8) * refs.U32 * want).all()
+        W, dg = torch.randn(D, 4, generator=gen).to(DEV), torch.randn(T, 2, generator=gen).to(DEV)
+        dx, dW = swimba.route_backward(x, W, idx, gate, dg)
+        wx, wW, sx, sW = refs.route_backward(up(x), up(W), idx.cpu().numpy(), up(gate), up(dg))
+        assert (np.abs(up(dx) - wx) <= 12 * refs.U32 * sx).all()
+        assert (np.abs(up(dW) - wW) <= (T + 12) * refs.U32 * sW).all()
+
+
+def test_combine_backward_of_more_tokens_than_a_grid_row():
+    T, D = (1 << 24) + 5, 3
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    rows = torch.randn(T, D, generator=gen, device=DEV)
+    dy = torch.randn(T, D, generator=gen, device=DEV)
+    gate = torch.rand(T, 1, generator=gen, device=DEV)
+    pos = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV)[:, None]
+    drows, dgate = swimba.combine_tokens_backward(rows, pos, gate, dy)
+    assert torch.equal(drows, (gate * dy).flip(0))  # one product, rounded once
+    terms = dy.double() * rows.flip(0).double()
+    assert ((dgate[:, 0].double() - terms.sum(1)).abs() <= (D + 8) * refs.U32 * terms.abs().sum(1)).all()

@@ -237,6 +237,30 @@ def test_route_and_combine_reference_gradients_are_differences():
     assert abs((dg * e).sum() - (dy * refs.combine(rows, pos, e)).sum()) < 1e-12
 
 
+def test_refuses_more_than_a_launch_counts(lib):
+    """Threads of a launch are counted in 32 bits."""
+    many = {"B": 1 << 24, "L": 1, "H": 1, "G": 1, "N": 1, "P": 1}
+    wide = {"B": 1 << 20, "L": 1, "H": 1, "G": 1, "N": 1, "P": 512}
+    for kw in (many, wide, dict(many, L=0)):
+        a = attention_args(**kw)
+        assert lib.swimba_linear_attention(ctypes.byref(a), FAKE, 1 << 40, None) == sw.EUNSUPPORTED
+        assert lib.swimba_linear_attention_workspace_size(ctypes.byref(a)) == 0
+    for kw in (many, dict(many, B=1 << 22), dict(many, B=1 << 21, N=256),
+               dict(many, B=16, L=(1 << 28) - 64), dict(many, B=1 << 10, L=1 << 18, H=2, G=1, N=128)):
+        g = sw.LinearAttentionGradArgs()
+        g.fwd = attention_args(**kw)
+        g.grad_dtype = sw.BF16
+        for f in ("dy", "dq", "dk", "dv", "dlog_decay"):
+            setattr(g, f, FAKE)
+        assert lib.swimba_linear_attention_backward(ctypes.byref(g), FAKE, 1 << 40, None) == sw.EUNSUPPORTED
+    st = sw.LinearAttentionStepArgs()
+    st.B, st.H, st.G, st.N, st.P = 1 << 14, 1 << 10, 1, 1, 1
+    assert lib.swimba_linear_attention_step(ctypes.byref(st), None) == sw.EUNSUPPORTED
+    assert lib.swimba_dispatch_tokens(FAKE, sw.F32, FAKE, 1 << 30, 128, 1, FAKE, None) == sw.EUNSUPPORTED
+    assert lib.swimba_combine_tokens(FAKE, sw.F32, FAKE, None, 1 << 30, 128, 1, FAKE, sw.F32,
+                                     None) == sw.EUNSUPPORTED
+
+
 PACKS = r'''
 #include <cstdio>
 #include "pack.hpp"
