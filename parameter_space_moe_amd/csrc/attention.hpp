@@ -37,7 +37,7 @@
 // enters a product (decayed scores, state, decayed values) is split into two
 // or three bf16 terms that sum to it within 2^-16 or 2^-24 of its size, two
 // where the result is rounded to bf16 anyway, three where it is kept in fp32:
-// a single bf16 term would leave 2^-9, as much as the output's own rounding,
+// a single bf16 term would leave 2^-8, as much as the output's own rounding,
 // and in the state it would stay for the rest of the sequence.  fp32 inputs go
 // through the fp32 matrix instruction.  Sums of log decays are taken in 64
 // bits and handed on as a high and a low fp32 part: differences of large sums
