@@ -412,12 +412,18 @@ int dispatch(const AttnParams& p, bool f32, bool state, bool exact, hipStream_t 
   return attn_bf16_256(p, state, exact, s);
 }
 
-// One walk; ws holds the plan's segment states.
-int walk(AttnParams p, const WalkPlan& w, bool f32, bool exact, unsigned char* ws, hipStream_t s) {
+// One walk; ws holds the plan's segment states, or `turned` the transposed first
+// states of the same segments from another walk.
+int walk(AttnParams p, const WalkPlan& w, bool f32, bool exact, unsigned char* ws, hipStream_t s,
+         float* turned = nullptr) {
   p.nseg = w.nseg;
   p.seg_chunks = w.seg_chunks;
   p.ctiles = (p.Cd + 31) / 32;
-  if (w.nseg > 1) {
+  p.fk = turned != nullptr ? 1 : p.Cd;
+  p.fc = turned != nullptr ? p.Kd : 1;
+  if (turned != nullptr) {
+    p.seg_state = turned;
+  } else if (w.nseg > 1) {
     p.seg_state = reinterpret_cast<float*>(ws);
     p.seg_decay = reinterpret_cast<float*>(ws + w.state_bytes);
     const int rc = dispatch(p, f32, true, true, s);
@@ -453,6 +459,10 @@ size_t tiny_bytes(const swimba_linear_attention_args* a, int slots) {
 
 struct GradPlan {
   WalkPlan q, v;  // dq and dk walk (states [P][N]), dv walk (states [N][P])
+  // The dk and the dv walk have the same states, transposed: cut into the same
+  // segments, the second takes the first's (24 heads of 64 x 64: 26 us less of
+  // 273; 32 heads of 128 x 128: 50 of 726).
+  bool turned = false;
   size_t off_zq = 0, off_zk = 0, off_diff = 0, off_part = 0, off_x = 0, off_end = 0, off_rows = 0;
   size_t off_tiny = 0, off_adj = 0, off_v = 0, off_anchor = 0;
   size_t bytes = 0;
@@ -467,8 +477,8 @@ GradPlan plan_grad(const swimba_linear_attention_grad_args* g, int dev) {
   r.v = plan_walk(f32, a->B, a->L, a->H, a->H / a->G, a->N, a->P, dev);
   r.nc = (a->L + kChunk - 1) / kChunk;
   r.ntiles = (a->N + 31) / 32;
-  // segment states of the dq and dk walks (the decays' gradient meets both) and
-  // of the dv walk
+  // segment states of the dq and dk walks (the decays' gradient meets both) and,
+  // where they are not the dk walk's, of the dv walk
   size_t o = r.q.bytes();
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -477,7 +487,8 @@ GradPlan plan_grad(const swimba_linear_attention_grad_args* g, int dev) {
   };
   const size_t bh = (size_t)a->B * a->H;
   r.off_adj = take(r.q.bytes());
-  r.off_v = take(r.v.bytes());
+  r.turned = r.q.nseg > 1 && r.v.nseg == r.q.nseg && r.v.seg_chunks == r.q.seg_chunks;
+  r.off_v = take(r.turned ? 0 : r.v.bytes());
   r.off_anchor = take(r.q.nseg > 1 ? bh * (r.q.nseg - 1) * sizeof(double) : 0);
   r.off_zq = take(bh * r.ntiles * 2 * a->L * sizeof(float));
   r.off_zk = take(bh * r.ntiles * 2 * a->L * sizeof(float));
@@ -636,7 +647,8 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   p.s_final = g->dh0;
   p.y = g->dv;
   p.y_bf16 = g->grad_dtype == SWIMBA_BF16;
-  rc = walk(p, r.v, f32, g->grad_dtype == SWIMBA_F32, at<unsigned char>(ws, r.off_v), s);
+  rc = walk(p, r.v, f32, g->grad_dtype == SWIMBA_F32, at<unsigned char>(ws, r.off_v), s,
+            r.turned ? at<float>(ws, r.off_adj) : nullptr);
   if (rc != SWIMBA_OK) return rc;
 
   DecayGradParams d;

@@ -66,7 +66,8 @@ struct AttnParams {
   float* s_final;         // or null; the same layout
   int64_t sk, sc;
   int nseg, seg_chunks;   // segments of the walk, chunks in each
-  float* seg_state;       // [B, H, nseg, Kd, Cd]: end states out (state pass), first states in
+  float* seg_state;       // [B, H, nseg, Kd, Cd]: end states out (state pass), first states in,
+  int64_t fk, fc;         // whose entry (n, c) is at n * fk + c * fc
   float* seg_decay;       // [B, H, nseg] out of the state pass
   const void* z;          // null, or rows (B, L, H / vshare, Cd) for the sums below
   float* zsum;            // [B, H, ctiles, 2, L]: <z_t, y_t> inside the chunk, and from the state
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   const float* from = STATE ? nullptr : walked ? p.seg_state + sstate : p.s0;
   if (from != nullptr) {
     if (!walked) from += state;
-    const int64_t fk = walked ? p.Cd : p.sk, fc = walked ? 1 : p.sc;
+    const int64_t fk = walked ? p.fk : p.sk, fc = walked ? p.fc : p.sc;
     const int64_t at = (c0 + col) * fc;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
