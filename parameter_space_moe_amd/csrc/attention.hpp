@@ -367,6 +367,14 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   float *gLo = gHi + kChunk;
   float *gRead = gLo + kChunk, *gWrite = gRead + kChunk;  // factors of y_t and of v_s
 
+  // Row tiles of the state that hold rows: tiles past the middle may not.  An fp32
+  // product takes 16 times the cycles of a bf16 one, so there a tile without rows
+  // is branched round (8192 tokens of 16 heads: 122 -> 110 us with 96 rows, 1270 ->
+  // 1015 us with 160, 1270 -> 1353 us where all eight are used; 16384 bf16 tokens:
+  // 140 -> 138 us with 160 rows, 155 -> 162 us with 256, not taken).
+  constexpr bool kSkip = kF32;
+  auto used = [&](int kt) { return !kSkip || kt <= KT / 2 || 32 * kt < p.Kd; };
+
   // workgroup -> (sequence, group of heads sharing q and k, segment, W units),
   // neighbours (which read the same q and k) on one XCD: workgroups go to the
   // eight of them in turn
@@ -571,8 +579,9 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
         const TI* qr = sQ + (32 * tt + col) * QS;
         const TI* kr = sK + (32 * ss + col) * KS;
         if constexpr (kF32) {
+          const int rows = (p.Kd + 31) & ~31;
 #pragma unroll 4
-          for (int n = 0; n < 32 * KT; n += 8) {
+          for (int n = 0; n < rows; n += 8) {
             const float4 x = *reinterpret_cast<const float4*>(qr + n + 4 * half);
             const float4 y = *reinterpret_cast<const float4*>(kr + n + 4 * half);
             a = mma(x.x, y.x, a);
@@ -612,6 +621,7 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
         }
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
+        if (!used(kt)) continue;
         if constexpr (kF32) {
 #pragma unroll
           for (int a = 0; a < 4; ++a)
@@ -733,9 +743,11 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       for (int i = 0; i < kV; ++i) vf[i] *= ws[i];
       if constexpr (kF32) {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT; ++kt) {
+          if (!used(kt)) continue;
 #pragma unroll
           for (int i = 0; i < kV; ++i) h[kt] = mma(sK[(sl + i) * KS + 32 * kt + col], vf[i], h[kt]);
+        }
       } else {
         bf8x wt[3];
         split_terms<3>(vf, wt);
@@ -745,7 +757,8 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
 #pragma unroll
         for (int s = 2; s >= 0; --s)
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt) h[kt] = mma(a[kt], wt[s], h[kt]);
+          for (int kt = 0; kt < KT; ++kt)
+            if (used(kt)) h[kt] = mma(a[kt], wt[s], h[kt]);
       }
     }
     __builtin_amdgcn_s_setprio(0);
@@ -926,7 +939,9 @@ int attn_launch_kind(const AttnParams& p, bool state, bool exact, hipStream_t s)
   return attn_launch<TI, KT, W, 3, kAttnPlain, LOOSE>(p, s);
 }
 
-// Waves of a workgroup: four where that many units share q and k, else two.
+// Waves of a workgroup: four where that many units share q and k, else two (two
+// everywhere: 1152 against 533 us for the 64K-token prompt, 781 against 388 us for
+// the 1.4B-like prompts, whose rows then do not fit the registers).
 // Rows that are not whole packs always go by two (fewer kernels; the packs'
 // masks cost more than the sharing gives), and fp32 rows of 256 leave LDS for
 // one wave's values only.
