@@ -35,9 +35,9 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(AttnParams p) {
   }
 }
 
-// X (below) where segments meet, from both walks' first states: the state
-// before the boundary and the adjoint behind it, joined by the decay of the
-// first token behind it.
+// The log decays' gradient (below) where segments meet, from both walks' first
+// states: the state before the boundary and the adjoint behind it, joined by the
+// decay of the first token behind it.
 struct AnchorParams {
   const float *h, *adj;  // [B, H, nseg, n] first states of the dq and of the dk walk
   const float* g;
@@ -89,27 +89,31 @@ __global__ __launch_bounds__(kDotThreads) void attn_anchor_kernel(AnchorParams p
   if (threadIdx.x == 0) {
     const int64_t t = (int64_t)i * p.seg_chunks * kChunk, b = bh / p.H, h = bh % p.H;
     const double d = (double)p.g[p.token_decay ? (b * p.L + t) * p.H + h : h] * 1.4426950408889634;
-    p.out[bh * (p.nseg - 1) + blockIdx.x] =
-        s * (double)exp2_sum(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
+    const float e = exp2_sum(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
+    p.out[bh * (p.nseg - 1) + blockIdx.x] = e == 0.f ? 0.0 : s * (double)e;
   }
 }
 
 // Gradients of the log decays.  In a chunk, with row_r and col_s the sums of
 // (q_r . k_s)(dy_r . v_s) D[r][s] over the pairs s <= r of the chunk (the walks'
 // <q, dq> and <k, dk> inside the chunk), a_r what r reads of the chunk's first
-// state and b_s what later chunks read of s:
-//   dg_t = sum_{r >= t} (row_r - col_r + a_r) + sum_{s < t} b_s + through
-// where `through` is what later chunks read of the first state: with X the
-// product of state and adjoint at a chunk's end, through = X - sum b, and X at
-// its beginning is through + sum a.  X is known behind the last chunk and where
-// segments meet, and chained over the chunks between.  The cancelling sums stay
-// inside a chunk.
+// state and b_s what later chunks read of s, the slopes of neighbours differ by
+//   dg_t - dg_{t+1} = u_t = row_t - col_t + a_t - b_t,
+// and over a whole chunk the pairs' part of that sum is zero.  dg is known behind
+// the last token (the product of state and adjoint there), where segments meet,
+// and where a state is cleared: zero.  Every other token's is summed up from the
+// nearest of these behind it, so that the rounding of what cancels stays inside
+// a document and inside a segment (a whole walk is one segment).
 struct DecayGradParams {
   const float *zq, *zk;   // [B, H, ctiles, 2, L] of the dq and dk walks
-  const double* x_end;    // [B, H] X behind the last chunk, or null for zero
-  const double* anchor;   // [B, H, segments - 1] X where segments meet, or null
+  const double* x_end;    // [B, H] dg behind the last token, or null for zero
+  const double* anchor;   // [B, H, segments - 1] dg where segments meet, or null
   int seg_chunks, nseg;
-  double* diff;           // [B, H, chunks] sum a - sum b
+  struct Chunk {          // the slopes' difference over a chunk
+    double back;          // from its first token to its end, or to the first cleared state
+    int32_t cleared;      // whether there is one
+  };
+  Chunk* chunk;           // [B, H, chunks]
   double* part;           // [B, H, chunks] sums of dg (a decay per head), or null
   const float* g;
   float* dg;              // [B, L, H] or [H]
@@ -139,15 +143,31 @@ __device__ __forceinline__ DecayTerms decay_terms(const DecayGradParams& p, int6
   return r;
 }
 
+// Whether token t clears the state: nothing passes, whatever g is near by.
+__device__ __forceinline__ bool clears(const DecayGradParams& p, int64_t bh, int t) {
+  if (t >= p.L) return false;
+  const int h = (int)(bh % p.H);
+  return hw_exp2((p.token_decay ? p.g[(bh / p.H * p.L + t) * p.H + h] : p.g[h]) * kLog2e) == 0.f;
+}
+
+// First lane of a mask, 64 for none.
+__device__ __forceinline__ int first_lane(uint64_t mask) {
+  return mask != 0 ? __ffsll((unsigned long long)mask) - 1 : 64;
+}
+
 __global__ __launch_bounds__(256) void attn_decay_diff_kernel(DecayGradParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (w >= (int64_t)p.B * p.H * p.nc) return;
   const int64_t bh = w / p.nc;
-  const int c = (int)(w - bh * p.nc);
-  const DecayTerms r = decay_terms(p, bh, c * kChunk + lane);
-  const double d = wave_sum(r.a - r.b);
-  if (lane == 0) p.diff[w] = d;
+  const int t = (int)(w - bh * p.nc) * kChunk + lane;
+  const DecayTerms r = decay_terms(p, bh, t);
+  const uint64_t mask = __ballot(clears(p, bh, t));
+  const double back = wave_sum(lane < first_lane(mask) ? r.a - r.b : 0.0);
+  if (lane == 0) {
+    p.chunk[w].back = back;
+    p.chunk[w].cleared = mask != 0;
+  }
 }
 
 __global__ __launch_bounds__(256) void attn_decay_grad_kernel(DecayGradParams p) {
@@ -156,8 +176,7 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(DecayGradParams p)
   if (w >= (int64_t)p.B * p.H * p.nc) return;
   const int64_t bh = w / p.nc;
   const int c = (int)(w - bh * p.nc), h = (int)(bh % p.H), t = c * kChunk + lane;
-  double x = 0.0;
-  // up to the next segment's first chunk, or the end
+  // up to the next segment's first chunk, or the end, or a chunk that clears
   int stop = p.nc;
   double known = p.x_end != nullptr ? p.x_end[bh] : 0.0;
   if (p.anchor != nullptr) {
@@ -167,26 +186,32 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(DecayGradParams p)
       known = p.anchor[bh * (p.nseg - 1) + next - 1];
     }
   }
-  for (int i = c + 1 + lane; i < stop; i += 64) x += p.diff[bh * p.nc + i];
+  double x = 0.0;
+  for (int i = c + 1; i < stop; i += 64) {
+    DecayGradParams::Chunk n = {0.0, 0};
+    if (i + lane < stop) n = p.chunk[bh * p.nc + i + lane];
+    const int first = first_lane(__ballot(n.cleared != 0));
+    if (lane <= first) x += n.back;
+    if (first < 64) {
+      known = 0.0;
+      break;
+    }
+  }
   x = wave_sum(x) + known;
   const DecayTerms r = decay_terms(p, bh, t);
-  double after = r.inside + r.a, before = r.b;
+  const bool clear = clears(p, bh, t);
+  const uint64_t mask = __ballot(clear);
+  // the next token that clears, behind this one
+  const int next = first_lane(lane < 63 ? mask & (~0ull << (lane + 1)) : 0);
+  double dg = r.inside + r.a - r.b;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
-    const double o = __shfl_down(after, m), q = __shfl_up(before, m);
-    if (lane + m < 64) after += o;
-    if (lane >= m) before += q;
+    const double o = __shfl_down(dg, m);
+    if (lane + m < next) dg += o;
   }
-  // x - (all b) + (earlier b): minus this and the later ones
-  const double later = __shfl(before, 63) - (before - r.b);
-  double dg = after + (x - later);
-  if (t < p.L) {
-    const float g = p.token_decay ? p.g[(bh / p.H * p.L + t) * p.H + h] : p.g[h];
-    if (hw_exp2(g * kLog2e) == 0.f) dg = 0.0;  // nothing passes, whatever g is near by
-    if (p.token_decay) p.dg[(bh / p.H * p.L + t) * p.H + h] = (float)dg;
-  } else {
-    dg = 0.0;
-  }
+  if (next == 64) dg += x;
+  if (clear || t >= p.L) dg = 0.0;
+  if (t < p.L && p.token_decay) p.dg[(bh / p.H * p.L + t) * p.H + h] = (float)dg;
   if (p.part != nullptr) {
     dg = wave_sum(dg);
     if (lane == 0) p.part[w] = dg;
@@ -465,7 +490,7 @@ struct GradPlan {
   // rows of a column per load made walks of 128 rows spill (1.4B-like prompts 388 ->
   // 537 us).
   bool turned = false;
-  size_t off_zq = 0, off_zk = 0, off_diff = 0, off_part = 0, off_x = 0, off_end = 0, off_rows = 0;
+  size_t off_zq = 0, off_zk = 0, off_chunk = 0, off_part = 0, off_x = 0, off_end = 0, off_rows = 0;
   size_t off_tiny = 0, off_adj = 0, off_v = 0, off_anchor = 0;
   size_t bytes = 0;
   int nc = 0, ntiles = 0;
@@ -494,7 +519,7 @@ GradPlan plan_grad(const swimba_linear_attention_grad_args* g, int dev) {
   r.off_anchor = take(r.q.nseg > 1 ? bh * (r.q.nseg - 1) * sizeof(double) : 0);
   r.off_zq = take(bh * r.ntiles * 2 * a->L * sizeof(float));
   r.off_zk = take(bh * r.ntiles * 2 * a->L * sizeof(float));
-  r.off_diff = take(bh * r.nc * sizeof(double));
+  r.off_chunk = take(bh * r.nc * sizeof(DecayGradParams::Chunk));
   r.off_part = take(a->decay_form == SWIMBA_DECAY_HEAD ? bh * r.nc * sizeof(double) : 0);
   r.off_x = take(bh * sizeof(double));
   r.off_end = take(g->dh_final != nullptr ? bh * a->N * a->P * sizeof(float) : 0);
@@ -660,7 +685,7 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   d.anchor = nullptr;
   d.seg_chunks = r.q.seg_chunks;
   d.nseg = r.q.nseg;
-  d.diff = at<double>(ws, r.off_diff);
+  d.chunk = at<DecayGradParams::Chunk>(ws, r.off_chunk);
   d.part = a->decay_form == SWIMBA_DECAY_HEAD ? at<double>(ws, r.off_part) : nullptr;
   d.g = a->log_decay;
   d.dg = g->dlog_decay;

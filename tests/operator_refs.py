@@ -5,6 +5,7 @@ shared with the library."""
 from __future__ import annotations
 
 import numpy as np
+import torch
 
 U32 = 2.0 ** -24   # half a step of fp32
 U16 = 2.0 ** -8    # half a step of bf16
@@ -66,6 +67,70 @@ def attention_sizes(q, k, v, log_decay, h0=None, dy=None, dh=None):
         later = later + (ab[5] * out["h_final"]).sum((-1, -2))[:, None, :]
     out["dlog_decay"] = later.sum((0, 1)) if np.asarray(log_decay).ndim == 1 else later
     return out
+
+
+def attention_on_device(q, k, v, log_decay, h0=None, dy=None, dh=None):
+    """attention() for long sequences and many heads: the same recurrence on torch
+    tensors, in 64 bits, where they are.  Returns (values, sizes); the size of the
+    decays' gradient sums over the later tokens of the same document only (up to
+    the next decay below 2^-126, which no fp32 number passes)."""
+    B, L, H, P = v.shape
+    G, N = q.shape[2:]
+    share = H // G
+    g = log_decay.double().expand(B, L, H)
+    e = g.exp()
+
+    def walk(q, k, v, h0, dy, dh):
+        q, k = (t.double().repeat_interleave(share, dim=2) for t in (q, k))
+        v = v.double()
+        h = torch.zeros(B, H, N, P, dtype=torch.float64, device=v.device)
+        if h0 is not None:
+            h = h0.double()
+        states, y = [h], torch.empty(B, L, H, P, dtype=torch.float64, device=v.device)
+        for t in range(L):
+            h = e[:, t, :, None, None] * h + k[:, t, :, :, None] * v[:, t, :, None, :]
+            y[:, t] = (q[:, t, :, :, None] * h).sum(2)
+            states.append(h)
+        out = {"y": y, "h_final": h}
+        if dy is None:
+            return out
+        dy = dy.double()
+        a = torch.zeros_like(h) if dh is None else dh.double()
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dg = torch.empty(B, L, H, dtype=torch.float64, device=v.device)
+        for t in range(L - 1, -1, -1):
+            dq[:, t] = (states[t + 1] * dy[:, t, :, None, :]).sum(3)
+            a = a + q[:, t, :, :, None] * dy[:, t, :, None, :]
+            dk[:, t] = (a * v[:, t, :, None, :]).sum(3)
+            dv[:, t] = (a * k[:, t, :, :, None]).sum(2)
+            a = e[:, t, :, None, None] * a
+            dg[:, t] = (a * states[t]).sum((-1, -2))
+        out["dq"], out["dk"] = (t.reshape(B, L, G, share, N).sum(3) for t in (dq, dk))
+        out["dv"], out["dh0"] = dv, a
+        out["dlog_decay"] = dg
+        out["terms"] = (q * dq + k * dk).sum(-1)
+        return out
+
+    def size(t):
+        return None if t is None else t.abs()
+
+    want = walk(q, k, v, h0, dy, dh)
+    most = walk(size(q), size(k), size(v), size(h0), size(dy), size(dh))
+    if dy is not None:
+        later = torch.zeros(B, H, dtype=torch.float64, device=v.device)
+        if dh is not None:
+            later = (dh.double().abs() * most["h_final"]).sum((-1, -2))
+        sums = torch.empty_like(g)
+        passes = g * 1.4426950408889634 >= -126
+        for t in range(L - 1, -1, -1):
+            later = later + most["terms"][:, t]
+            sums[:, t] = later
+            later = torch.where(passes[:, t], later, torch.zeros_like(later))
+        most["dlog_decay"] = sums
+        want["dlog_decay"] = torch.where(passes, want["dlog_decay"], torch.zeros_like(g))
+        if log_decay.dim() == 1:
+            want["dlog_decay"], most["dlog_decay"] = (d["dlog_decay"].sum((0, 1)) for d in (want, most))
+    return want, most
 
 
 def roundings(N, P, L, terms3=True):
