@@ -546,6 +546,10 @@ typedef struct {
  * swimba_linear_attention_backward -- gradients of swimba_linear_attention, from its inputs
  * (nothing of the forward pass is kept).  Workspace as there, sized by
  * swimba_linear_attention_backward_workspace_size(g).  Every output is deterministic.
+ * An infinity or a NaN of k or v reaches dq and dlog_decay of later tokens only,
+ * besides its own token's dq, dk and dv; one of q or dy dk, dv and dlog_decay of
+ * its token and earlier ones, dh0, and its own token's dq.  (A q or dy before such
+ * a k or v in one sequence and head: also dlog_decay between the two.)
  * dh0 may be dh_final itself; otherwise no output overlaps an input or another
  * output.
  * Constraints: those of swimba_linear_attention, and P <= 256, B * H < 2^22,

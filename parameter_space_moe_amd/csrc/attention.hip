@@ -37,13 +37,16 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(AttnParams p) {
 
 // The log decays' gradient (below) where segments meet, from both walks' first
 // states: the state before the boundary and the adjoint behind it, joined by the
-// decay of the first token behind it.
+// decay of the first token behind it.  And before the first token: <h0, dL/dh0>.
 struct AnchorParams {
   const float *h, *adj;  // [B, H, nseg, n] first states of the dq and of the dk walk
+  const float *h0, *dh0; // null: a first state of zero
   const float* g;
   double* out;           // [B, H, nseg - 1]
+  double* begin;         // [B, H]
   int64_t n;
   int H, L, nseg, seg_chunks, token_decay;
+  int known;             // values per sequence and head: nseg - 1, and one with h0
 };
 
 // out[b, h] = <a, b> over a state, in 64 bits.
@@ -82,15 +85,21 @@ __global__ __launch_bounds__(kDotThreads) void attn_dot_kernel(const float* a, c
 
 __global__ __launch_bounds__(kDotThreads) void attn_anchor_kernel(AnchorParams p) {
   __shared__ double part[kDotThreads];
-  const int64_t bh = blockIdx.y;
-  const int i = blockIdx.x + 1;  // the boundary before segment i
+  const int64_t bh = blockIdx.x / p.known;
+  // the boundary before segment i, or last the sequence's start
+  const int i = (int)(blockIdx.x % p.known) + 1;
+  if (i == p.nseg) {
+    const double s = block_dot(p.h0 + bh * p.n, p.dh0 + bh * p.n, p.n, part);
+    if (threadIdx.x == 0) p.begin[bh] = s;
+    return;
+  }
   const int64_t f = (bh * p.nseg + i) * p.n, r = (bh * p.nseg + p.nseg - i) * p.n;
   const double s = block_dot(p.h + f, p.adj + r, p.n, part);
   if (threadIdx.x == 0) {
     const int64_t t = (int64_t)i * p.seg_chunks * kChunk, b = bh / p.H, h = bh % p.H;
     const double d = (double)p.g[p.token_decay ? (b * p.L + t) * p.H + h : h] * 1.4426950408889634;
     const float e = exp2_sum(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
-    p.out[bh * (p.nseg - 1) + blockIdx.x] = e == 0.f ? 0.0 : s * (double)e;
+    p.out[bh * (p.nseg - 1) + i - 1] = e == 0.f ? 0.0 : s * (double)e;
   }
 }
 
@@ -104,13 +113,20 @@ __global__ __launch_bounds__(kDotThreads) void attn_anchor_kernel(AnchorParams p
 // and where a state is cleared: zero.  Every other token's is summed up from the
 // nearest of these behind it, so that the rounding of what cancels stays inside
 // a document and inside a segment (a whole walk is one segment).
+// u of a token with an infinity or a NaN in k or v, and of the later ones, is not
+// finite, and neither is that sum for the tokens before it, whose gradients do
+// not depend on that k or v.  Where it is not, the sum from the nearest known
+// value in front (the product of the first state and its gradient at the start)
+// is taken if it is finite.
 struct DecayGradParams {
   const float *zq, *zk;   // [B, H, ctiles, 2, L] of the dq and dk walks
   const double* x_end;    // [B, H] dg behind the last token, or null for zero
+  const double* begin;    // [B, H] dg before the first token, or null for zero
   const double* anchor;   // [B, H, segments - 1] dg where segments meet, or null
   int seg_chunks, nseg;
   struct Chunk {          // the slopes' difference over a chunk
     double back;          // from its first token to its end, or to the first cleared state
+    double fore;          // from its first token, or from the last cleared state, to its end
     int32_t cleared;      // whether there is one
   };
   Chunk* chunk;           // [B, H, chunks]
@@ -150,9 +166,12 @@ __device__ __forceinline__ bool clears(const DecayGradParams& p, int64_t bh, int
   return hw_exp2((p.token_decay ? p.g[(bh / p.H * p.L + t) * p.H + h] : p.g[h]) * kLog2e) == 0.f;
 }
 
-// First lane of a mask, 64 for none.
+// First lane of a mask, 64 for none; last lane, -1 for none.
 __device__ __forceinline__ int first_lane(uint64_t mask) {
   return mask != 0 ? __ffsll((unsigned long long)mask) - 1 : 64;
+}
+__device__ __forceinline__ int last_lane_of(uint64_t mask) {
+  return 63 - __clzll((long long)mask);
 }
 
 __global__ __launch_bounds__(256) void attn_decay_diff_kernel(DecayGradParams p) {
@@ -164,11 +183,15 @@ __global__ __launch_bounds__(256) void attn_decay_diff_kernel(DecayGradParams p)
   const DecayTerms r = decay_terms(p, bh, t);
   const uint64_t mask = __ballot(clears(p, bh, t));
   const double back = wave_sum(lane < first_lane(mask) ? r.a - r.b : 0.0);
+  const double fore = wave_sum(lane >= last_lane_of(mask) ? r.a - r.b : 0.0);
   if (lane == 0) {
     p.chunk[w].back = back;
+    p.chunk[w].fore = fore;
     p.chunk[w].cleared = mask != 0;
   }
 }
+
+__device__ __forceinline__ bool finite(double v) { return fabs(v) < (double)__builtin_inff(); }
 
 __global__ __launch_bounds__(256) void attn_decay_grad_kernel(DecayGradParams p) {
   const int lane = threadIdx.x & 63;
@@ -188,7 +211,7 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(DecayGradParams p)
   }
   double x = 0.0;
   for (int i = c + 1; i < stop; i += 64) {
-    DecayGradParams::Chunk n = {0.0, 0};
+    DecayGradParams::Chunk n = {0.0, 0.0, 0};
     if (i + lane < stop) n = p.chunk[bh * p.nc + i + lane];
     const int first = first_lane(__ballot(n.cleared != 0));
     if (lane <= first) x += n.back;
@@ -203,13 +226,42 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(DecayGradParams p)
   const uint64_t mask = __ballot(clear);
   // the next token that clears, behind this one
   const int next = first_lane(lane < 63 ? mask & (~0ull << (lane + 1)) : 0);
-  double dg = r.inside + r.a - r.b;
+  const double u = r.inside + r.a - r.b;
+  double dg = u;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
     const double o = __shfl_down(dg, m);
     if (lane + m < next) dg += o;
   }
   if (next == 64) dg += x;
+  const bool lost = t < p.L && !clear && !finite(dg);
+  if (__ballot(lost)) {
+    const int seg = p.anchor != nullptr ? c / p.seg_chunks : 0;
+    double in_front = seg > 0 ? p.anchor[bh * (p.nseg - 1) + seg - 1]
+                              : (p.begin != nullptr ? p.begin[bh] : 0.0);
+    double y = 0.0;
+    for (int i = c - 1; i >= seg * p.seg_chunks; i -= 64) {
+      DecayGradParams::Chunk n = {0.0, 0.0, 0};
+      if (i - lane >= seg * p.seg_chunks) n = p.chunk[bh * p.nc + i - lane];
+      const int first = first_lane(__ballot(n.cleared != 0));
+      if (lane <= first) y -= n.fore;
+      if (first < 64) {
+        in_front = 0.0;
+        break;
+      }
+    }
+    y = wave_sum(y) + in_front;
+    const int from = last_lane_of(mask & (~0ull >> (63 - lane)));  // this token's document
+    double before = u;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const double o = __shfl_up(before, m);
+      if (lane - m >= (from < 0 ? 0 : from)) before += o;
+    }
+    before = __shfl_up(before, 1);  // without this token's own
+    const double fore = (from < 0 ? y : 0.0) - (lane > 0 ? before : 0.0);
+    if (lost && finite(fore)) dg = fore;
+  }
   if (clear || t >= p.L) dg = 0.0;
   if (t < p.L && p.token_decay) p.dg[(bh / p.H * p.L + t) * p.H + h] = (float)dg;
   if (p.part != nullptr) {
@@ -490,7 +542,7 @@ struct GradPlan {
   // rows of a column per load made walks of 128 rows spill (1.4B-like prompts 388 ->
   // 537 us).
   bool turned = false;
-  size_t off_zq = 0, off_zk = 0, off_chunk = 0, off_part = 0, off_x = 0, off_end = 0, off_rows = 0;
+  size_t off_zq = 0, off_zk = 0, off_chunk = 0, off_part = 0, off_x = 0, off_begin = 0, off_end = 0, off_dh0 = 0, off_rows = 0;
   size_t off_tiny = 0, off_adj = 0, off_v = 0, off_anchor = 0;
   size_t bytes = 0;
   int nc = 0, ntiles = 0;
@@ -522,6 +574,8 @@ GradPlan plan_grad(const swimba_linear_attention_grad_args* g, int dev) {
   r.off_chunk = take(bh * r.nc * sizeof(DecayGradParams::Chunk));
   r.off_part = take(a->decay_form == SWIMBA_DECAY_HEAD ? bh * r.nc * sizeof(double) : 0);
   r.off_x = take(bh * sizeof(double));
+  r.off_begin = take(a->h0 != nullptr ? bh * sizeof(double) : 0);
+  r.off_dh0 = take(a->h0 != nullptr && g->dh0 == nullptr ? bh * a->N * a->P * sizeof(float) : 0);
   r.off_end = take(g->dh_final != nullptr ? bh * a->N * a->P * sizeof(float) : 0);
   // per-head rows of dq, then of dk, where heads share them
   r.off_rows = take(a->H != a->G ? bh * a->L * a->N * sizeof(float) : 0);
@@ -671,7 +725,8 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   p.sc = 1;
   p.reverse = 1;
   p.s0 = g->dh_final;
-  p.s_final = g->dh0;
+  float* dh0 = g->dh0 == nullptr && a->h0 != nullptr ? at<float>(ws, r.off_dh0) : g->dh0;
+  p.s_final = dh0;
   p.y = g->dv;
   p.y_bf16 = g->grad_dtype == SWIMBA_BF16;
   rc = walk(p, r.v, f32, g->grad_dtype == SWIMBA_F32, at<unsigned char>(ws, r.off_v), s,
@@ -683,6 +738,7 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   d.zk = zk;
   d.x_end = x_end;
   d.anchor = nullptr;
+  d.begin = nullptr;
   d.seg_chunks = r.q.seg_chunks;
   d.nseg = r.q.nseg;
   d.chunk = at<DecayGradParams::Chunk>(ws, r.off_chunk);
@@ -695,21 +751,26 @@ int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* 
   d.ctiles = r.ntiles;
   d.nc = r.nc;
   d.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
-  if (r.q.nseg > 1) {
-    AnchorParams x;
+  AnchorParams x;
+  x.known = r.q.nseg - 1 + (a->h0 != nullptr ? 1 : 0);
+  if (x.known > 0) {
     x.h = reinterpret_cast<const float*>(seg);
     x.adj = at<float>(ws, r.off_adj);
+    x.h0 = a->h0;
+    x.dh0 = dh0;
     x.g = a->log_decay;
     x.out = at<double>(ws, r.off_anchor);
+    x.begin = at<double>(ws, r.off_begin);
     x.n = (int64_t)a->N * a->P;
     x.H = a->H;
     x.L = a->L;
     x.nseg = r.q.nseg;
     x.seg_chunks = r.q.seg_chunks;
     x.token_decay = d.token_decay;
-    hipLaunchKernelGGL(attn_anchor_kernel, dim3(r.q.nseg - 1, (unsigned)(a->B * a->H)),
+    hipLaunchKernelGGL(attn_anchor_kernel, dim3((unsigned)(a->B * a->H * x.known)),
                        dim3(kDotThreads), 0, s, x);
-    d.anchor = x.out;
+    if (r.q.nseg > 1) d.anchor = x.out;
+    if (a->h0 != nullptr) d.begin = x.begin;
   }
   const unsigned wg = (unsigned)(((int64_t)a->B * a->H * r.nc + 3) / 4);
   hipLaunchKernelGGL(attn_decay_diff_kernel, dim3(wg), dim3(256), 0, s, d);

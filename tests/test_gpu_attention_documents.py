@@ -45,3 +45,35 @@ def test_decay_gradients_stay_inside_documents(B, H, L, starts):
     off = (got - want).abs() / allow
     assert bool((off <= 1).all()), "worst %.3g times the bound, at token %d" % (
         float(off.max()), int(off.amax((0, 2)).argmax()))
+
+
+# as above, and with a first state whose gradient is not asked for
+@pytest.mark.parametrize("B,H,L,h0", [(4, 80, 300, "given"), (2, 130, 300, "kept"), (1, 1, 200, None),
+                                      (2, 40, 700, "kept"), (1, 2, 900, "given")])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_decay_gradients_before_non_finite_keys_and_values(B, H, L, h0, dtype, bad):
+    # a padded batch: rubbish in k and v behind the last token, zeros in dy.  No
+    # gradient of the last token's decay and of earlier ones depends on that rubbish
+    N, P = 16, 24
+    t = inputs(B, L, H, N, P, [], seed=L)
+    for n in ("q", "k", "v", "dy"):
+        t[n] = t[n].to(dtype)
+    s = L - 70
+    t["dy"][:, s:] = 0
+    t["k"][:, s], t["v"][:, s] = 0, 0
+    if h0 is None:
+        t["h0"] = t["dh"] = None
+    want, size = refs.attention_on_device(**t)
+    allow = refs.roundings(N, P, L) * size["dlog_decay"][:, :1]  # a sum from either end
+    allow = allow + refs.U32 * want["dlog_decay"].abs() + 1e-30
+    for name in ("k", "v", "both"):
+        r = dict(t)
+        for n in ("k", "v"):
+            if name in (n, "both"):
+                r[n] = t[n].clone()
+                r[n][:, s, :, 3] = bad
+                r[n][0, s + 9] = float("nan")
+        got = backward(r, want_dh0=h0 == "given")["dlog_decay"].double()
+        off = ((got - want["dlog_decay"]).abs() / allow)[:, :s + 1]
+        assert bool((off <= 1).all()), (name, float(off.max()))
