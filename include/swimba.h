@@ -516,8 +516,9 @@ typedef struct {
  * of its token and all later ones of its sequence and head (one of v as NaN, in
  * its own and up to 31 columns next to it), also across a cleared state, and
  * never an earlier token.
- * Finite products |q| |k| |v| have to stay below 1e18 (partial sums carry
- * factors of up to 2^64).
+ * Magnitudes: |v|, |q| |k| summed over the keys of a head, and every state and
+ * result as the sum of its terms' magnitudes have to stay below 1e26 (scaled
+ * partial sums are up to 2^40 times larger).
  * h_final may be h0 itself; otherwise no output overlaps an input or another
  * output.
  * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256, L <= 2^30, H * P
@@ -550,6 +551,8 @@ typedef struct {
  * besides its own token's dq, dk and dv; one of q or dy dk, dv and dlog_decay of
  * its token and earlier ones, dh0, and its own token's dq.  (A q or dy before such
  * a k or v in one sequence and head: also dlog_decay between the two.)
+ * Magnitudes: as there, for every operand, state and gradient, and |v| |dy| summed
+ * over the values; |q| |dq| and |k| |dk| below 1e38.
  * dh0 may be dh_final itself; otherwise no output overlaps an input or another
  * output.
  * Constraints: those of swimba_linear_attention, and P <= 256, B * H < 2^22,

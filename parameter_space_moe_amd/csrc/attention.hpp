@@ -341,9 +341,11 @@ __device__ __forceinline__ float exp2_sum(double x) {
 }
 
 // Sums of log2 decays inside a chunk that keep e^{G_t} and e^{-G_s} apart, and
-// the scale a state may carry on top.
+// the product of e^{G_t} and the scale that the state carries on top.  Scaled
+// partial sums are at most 1 / kLeastScale times what they stand for: fp32 holds
+// them up to 2^127 kLeastScale.
 constexpr float kLeastSum = -40.f, kMostSum = 16.f;
-constexpr float kLeastScale = 0x1p-24f, kMostScale = 0x1p24f;
+constexpr float kLeastScale = 0x1p-40f, kMostScale = 0x1p40f;
 
 // S: bf16 terms of what is computed (2 or 3).
 template <typename TI, int KT, int W, int S, int MODE, bool LOOSE>
@@ -508,15 +510,16 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     // Elsewhere (a cleared state, a NaN) every pair has its own exponential and
     // h is scaled.
     const bool split = __ballot(!(hi >= kLeastSum && hi <= kMostSum)) == 0;
-    if (!split || c < kLeastScale || c > kMostScale) {
+    float read = exp2_sum(sum) * c;
+    if (!split || __ballot(!(read >= kLeastScale && read <= kMostScale))) {
       __builtin_amdgcn_sched_barrier(0);  // rare: a branch, not a product with one
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) h[kt][i] *= c;
       c = 1.f;
+      read = exp2_sum(sum);
     }
-    const float read = exp2_sum(sum) * c;
     const float write = split ? exp2_sum(-sum) / c : exp2_sum(end - sum);
     float poison = 1.f;
     __syncthreads();  // everyone is done with the last chunk
