@@ -513,9 +513,8 @@ typedef struct {
  *   the query and for the device of `stream` by the call.
  * bf16 inputs multiply exactly and sum in fp32; states are fp32.  An infinity
  * or a NaN of q reaches its token's outputs, one of k, v or a decay the outputs
- * of its token and all later ones of its sequence and head (one of v as NaN, in
- * its own and up to 31 columns next to it), also across a cleared state, and
- * never an earlier token.
+ * of its token and all later ones of its sequence and head (one of v in its own
+ * column only, as NaN), also across a cleared state, and never an earlier token.
  * Magnitudes: |v|, |q| |k| summed over the keys of a head, and every state and
  * result as the sum of its terms' magnitudes have to stay below 1e26 (scaled
  * partial sums are up to 2^40 times larger).
@@ -583,7 +582,8 @@ typedef struct {
 /*
  * swimba_linear_attention_step -- one decoding step of swimba_linear_attention on a
  * persistent state: the same as a sequence of one token with h0 = state and
- * h_final = state_out (or state).  Constraints: those of swimba_linear_attention.
+ * h_final = state_out (or state), but that an infinity of v enters the sums as
+ * such.  Constraints: those of swimba_linear_attention.
  */
 int swimba_linear_attention_step(const swimba_linear_attention_step_args* a, hipStream_t stream);
 

@@ -327,6 +327,13 @@ __device__ __forceinline__ int tile_row(int i, int half) {
   return 8 * (i >> 2) + 4 * half + (i & 3);
 }
 
+// A rare branch computes its addresses from these for itself: hoisted out of it
+// they would cost registers everywhere.
+__device__ __forceinline__ int apart(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 enum AttnMode {
   kAttnState = 0,  // only the segment's end state from zero, and its decay
   kAttnPlain = 1,
@@ -376,6 +383,18 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
   // 140 -> 138 us with 160 rows, 155 -> 162 us with 256, not taken).
   constexpr bool kSkip = kF32;
   auto used = [&](int kt) { return !kSkip || kt <= KT / 2 || 32 * kt < p.Kd; };
+
+  // This column's first token with an infinity or a NaN in v: in a row's padding.
+  auto bad_at = [&]() -> void* {
+    const int at = apart(col);
+    return STATE ? static_cast<void*>(sV + at * VS + 32) : sS + at * kScoreStride + kChunk + wave;
+  };
+  static_assert(W <= kScoreStride - kChunk, "a place per wave");
+  auto first_bad = [&] {
+    int t;
+    __builtin_memcpy(&t, bad_at(), sizeof(t));
+    return t;
+  };
 
   // workgroup -> (sequence, group of heads sharing q and k, segment, W units),
   // neighbours (which read the same q and k) on one XCD: workgroups go to the
@@ -521,7 +540,6 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       read = exp2_sum(sum);
     }
     const float write = split ? exp2_sum(-sum) / c : exp2_sum(end - sum);
-    float poison = 1.f;
     __syncthreads();  // everyone is done with the last chunk
     gHi[lane] = hi;
     gLo[lane] = (float)(sum - (double)hi);
@@ -532,8 +550,9 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     if (wild) {
       // An infinity or a NaN in v_s may reach y_t for t >= s only, and a product of
       // the matrix units with a zero score would spread it.  It is taken out of
-      // the slab, and the factors of the results from the first one on (all 32
-      // columns) and the state's scale become NaN instead.
+      // the slab, and the column's state and its results from it on become NaN
+      // behind the products (the results in memory: branches round their registers
+      // cost 25 of them, and in LDS on their way out 3 % of a walk).
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_wave_barrier();
       int bad = kChunk;
@@ -545,13 +564,9 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
           *at = TI(0);
         }
       }
-#pragma unroll
-      for (int m = 1; m < 64; m <<= 1) {
-        const int o = __shfl_xor(bad, m);
-        bad = o < bad ? o : bad;
-      }
-      if (lane >= bad) gRead[lane] = __builtin_nanf("");
-      poison = bad < kChunk ? __builtin_nanf("") : 1.f;
+      const int o = __shfl_xor(bad, 32);
+      bad = o < bad ? o : bad;
+      __builtin_memcpy(bad_at(), &bad, sizeof(bad));
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -766,7 +781,14 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
     }
     __builtin_amdgcn_s_setprio(0);
     if (split) c *= exp2_sum(end);
-    c *= poison;
+    if (wild) {
+      __builtin_amdgcn_sched_barrier(0);
+      const bool lost = first_bad() < kChunk;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[kt][i] = lost ? __builtin_nanf("") : h[kt][i];
+    }
     if (STATE) {
       whole += end;
       continue;
@@ -887,6 +909,29 @@ __global__ __launch_bounds__(64 * W, KT > 4 ? 1 : 2) void attn_kernel(AttnParams
       };
       if (p.y_bf16) leave(static_cast<bf16_t*>(p.y));
       else leave(static_cast<float*>(p.y));
+    }
+    if (wild) {  // over what has left
+      __builtin_amdgcn_sched_barrier(0);
+      __threadfence();
+      const int at = apart(col);
+      int bad = first_bad();
+#pragma unroll 1
+      for (int t = bad + (apart(lane) >> 5); t < len; t += 2) {
+        const int64_t to = yfirst + token(t) * ystride + at;
+        if (at >= cols) break;
+        if (p.y_bf16) static_cast<bf16_t*>(p.y)[to] = from_f32<bf16_t>(__builtin_nanf(""));
+        else static_cast<float*>(p.y)[to] = __builtin_nanf("");
+      }
+      if (SUMS) {
+#pragma unroll 1
+        for (int m = 1; m < 32; m <<= 1) {
+          const int o = __shfl_xor(bad, m);
+          bad = o < bad ? o : bad;
+        }
+        float* zs = p.zsum + (((int64_t)b * p.H + head) * p.ctiles + u % p.ctiles) * 2 * p.L;
+        const int t = bad + apart(lane);
+        if (active && t < len) zs[p.L + token(t)] = __builtin_nanf("");
+      }
     }
   }
 

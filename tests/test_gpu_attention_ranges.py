@@ -46,3 +46,38 @@ def test_states_up_to_the_limit(H, dtype, decay):
         assert max(float(t.max()) for n, t in size.items() if n != "terms") < 1e26
         for name, t in dict(got, y=y, h_final=h).items():
             assert off(t, want[name], size[name], refs.roundings(N, P, L)) <= 1, (swap, name)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("H,L,N,P", [(320, 150, 16, 40), (2, 700, 40, 33), (2, 200, 128, 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_columns_of_non_finite_values_are_apart(H, L, N, P, dtype, bad):
+    # one value of one head: its column is lost from that token on, and nothing else
+    gen = torch.Generator(device=DEV).manual_seed(L)
+    q, k, v = (torch.randn(1, L, H, n, generator=gen, device=DEV).to(dtype) for n in (N, N, P))
+    g = -0.1 * torch.rand(1, L, H, generator=gen, device=DEV)
+    g[:, 100] = -float("inf")
+    h0 = torch.randn(1, H, N, P, generator=gen, device=DEV)
+    dy = torch.randn(1, L, H, P, generator=gen, device=DEV).to(dtype)
+    s, last, col = 77, L - 2, 5
+    y, h = swimba.linear_attention(q, k, v, g, h0=h0)
+    grads = swimba.linear_attention_backward(q, k, v, g, dy, h0=h0)
+    w = v.clone()
+    w[0, s, 1, col] = bad
+    w[0, last, 0, P - 1] = bad
+    y2, h2 = swimba.linear_attention(q, k, w, g, h0=h0)
+    lost = torch.zeros_like(y, dtype=torch.bool)
+    lost[0, s:, 1, col] = lost[0, last:, 0, P - 1] = True
+    assert not torch.isfinite(y2[lost]).any() and torch.equal(y2[~lost], y[~lost])
+    gone = torch.zeros_like(h, dtype=torch.bool)
+    gone[0, 1, :, col] = gone[0, 0, :, P - 1] = True
+    assert not torch.isfinite(h2[gone]).any() and torch.equal(h2[~gone], h[~gone])
+    # the backward's values are k (for dq) and q (for dk, from the last token back)
+    for name, n in (("k", "dq"), ("q", "dk")):
+        ops = {"q": q, "k": k}
+        ops[name] = ops[name].clone()
+        ops[name][0, s, 1, col] = bad
+        got = swimba.linear_attention_backward(ops["q"], ops["k"], v, g, dy, h0=h0)[n]
+        lost = torch.zeros_like(got, dtype=torch.bool)
+        lost[0, (slice(s, None) if n == "dq" else slice(0, s + 1)), 1, col] = True
+        assert not torch.isfinite(got[lost]).any() and torch.equal(got[~lost], grads[n][~lost]), n
