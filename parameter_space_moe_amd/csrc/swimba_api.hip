@@ -699,7 +699,10 @@ int swimba_linear_attention_backward(const swimba_linear_attention_grad_args* g,
   if (rc != SWIMBA_OK) return rc;
   rc = validate_attention_inputs(&g->fwd);
   if (rc != SWIMBA_OK) return rc;
-  if (g->dlog_decay == nullptr) return SWIMBA_EINVAL;
+  // without tokens a gradient per token has no elements
+  if (g->dlog_decay == nullptr &&
+      (g->fwd.decay_form == SWIMBA_DECAY_HEAD || (g->fwd.B > 0 && g->fwd.L > 0)))
+    return SWIMBA_EINVAL;
   if (g->fwd.B > 0 && g->fwd.L > 0) {
     if (g->dy == nullptr || g->dq == nullptr || g->dk == nullptr || g->dv == nullptr ||
         !aligned_as(g->dy, g->fwd.in_dtype) || !aligned_as(g->dq, g->grad_dtype) ||

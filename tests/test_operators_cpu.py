@@ -297,3 +297,15 @@ def test_whole_loads_stay_inside_the_tensor(tmp_path):
                     str(exe)], check=True, capture_output=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+@pytest.mark.parametrize("B,L", [(2, 0), (0, 5)])
+def test_backward_without_tokens_takes_empty_gradients(lib, B, L):
+    """An empty tensor has no address: the decays' gradient per token may be null there,
+    the one per head may not."""
+    g = sw.LinearAttentionGradArgs()
+    g.fwd = attention_args(B=B, L=L, q=None, k=None, v=None, log_decay=None, y=None)
+    g.grad_dtype = sw.BF16
+    assert lib.swimba_linear_attention_backward(ctypes.byref(g), None, 0, None) == sw.OK
+    g.fwd.decay_form = sw.DECAY_HEAD
+    assert lib.swimba_linear_attention_backward(ctypes.byref(g), None, 0, None) == sw.EINVAL
