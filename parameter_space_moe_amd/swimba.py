@@ -727,20 +727,23 @@ def _placed(fn):
     results on another stream waits for s there and records them, as for any
     tensor made on a side stream)."""
 
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("%s: the first argument must be a device tensor" % fn.__name__)
+            raise ValueError("%s: %s must be a device tensor" % (fn.__name__, name))
         dev = first.device
         if stream is not None:
             if stream.device != dev:
                 raise ValueError("stream is on %s, the tensors on %s" % (stream.device, dev))
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         if dev.index != torch.cuda.current_device():
             with torch.cuda.device(dev):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
+                return fn(*args, **kw)
+        return fn(*args, **kw)
 
     return call
 

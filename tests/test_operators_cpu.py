@@ -309,3 +309,13 @@ def test_backward_without_tokens_takes_empty_gradients(lib, B, L):
     assert lib.swimba_linear_attention_backward(ctypes.byref(g), None, 0, None) == sw.OK
     g.fwd.decay_form = sw.DECAY_HEAD
     assert lib.swimba_linear_attention_backward(ctypes.byref(g), None, 0, None) == sw.EINVAL
+
+
+def test_binding_takes_the_first_argument_by_keyword():
+    t = torch.zeros(1, 4, 2, 8)
+    with pytest.raises(ValueError):
+        sw.linear_attention(q=t, k=t, v=t, log_decay=torch.zeros(2))
+    with pytest.raises(ValueError):
+        sw.sort_tokens(idx=torch.zeros(4, 2, dtype=torch.int32), E=4)
+    with pytest.raises(ValueError):
+        sw.sort_tokens(E=4)
