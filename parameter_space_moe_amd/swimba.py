@@ -1018,7 +1018,8 @@ def linear_attention_step(q, k, v, log_decay, state, state_out=None, y=None, y_d
 
 class PreparedLinearAttentionStep:
     """swimba_linear_attention_step marshalled once for fixed tensors (see
-    PreparedStep)."""
+    PreparedStep).  Each call goes to the device's current stream (a capturing one
+    records it), or to `stream` if that is given."""
 
     def __init__(self, q, k, v, log_decay, state, state_out=None, y=None, y_dtype=None,
                  stream=None):
@@ -1030,14 +1031,17 @@ class PreparedLinearAttentionStep:
         self._dev = v.device.index
         if stream is not None and stream.device != v.device:
             raise ValueError("stream is on %s, the tensors on %s" % (stream.device, v.device))
-        self.stream = (stream or torch.cuda.current_stream(v.device)).cuda_stream
+        self.stream = None if stream is None else stream.cuda_stream
 
     def __call__(self):
+        stream = self.stream
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(self._dev)
         if self._dev != torch.cuda.current_device():
             with torch.cuda.device(self._dev):
-                rc = self._fn(self._ref, self.stream)
+                rc = self._fn(self._ref, stream)
         else:
-            rc = self._fn(self._ref, self.stream)
+            rc = self._fn(self._ref, stream)
         if rc != OK:
             raise SwimbaError("swimba_linear_attention_step", rc)
         return self.y

@@ -42,3 +42,72 @@ def test_arguments_by_keyword():
     W = torch.randn(32, 4, device=DEV)
     d = swimba.route_backward(x=x, Wr=W, idx=idx, gate=gate, dgate=c[1])
     assert all(torch.equal(m, n) for m, n in zip(d, swimba.route_backward(x, W, idx, gate, c[1])))
+
+
+def step_inputs(B=3, H=4, G=2, N=64, P=32, seed=0):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device=DEV)
+
+    return [normal(B, G, N), normal(B, G, N), normal(B, H, P), -normal(B, H).abs()], normal(B, H, N, P)
+
+
+@pytest.mark.parametrize("prepared", [False, True])
+def test_step_on_another_stream(prepared):
+    # the state is there only behind a wait on that stream
+    ops, st = step_inputs()
+    y = swimba.linear_attention_step(*ops, st, state_out=(out := torch.empty_like(st)))
+    late, got = torch.zeros_like(st), torch.empty_like(st)
+    call = swimba.PreparedLinearAttentionStep(*ops, late, state_out=got)
+    assert torch.isfinite(call()).all()  # also after a call on the stream that it was made on
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(st)
+        y2 = call() if prepared else swimba.linear_attention_step(*ops, late, state_out=got)
+    side.synchronize()
+    assert torch.equal(y2, y) and torch.equal(got, out)
+    # a stream of the caller's
+    late.zero_()
+    torch.cuda.synchronize()
+    if prepared:
+        call = swimba.PreparedLinearAttentionStep(*ops, late, state_out=got, stream=side)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(st)
+    y2 = call() if prepared else swimba.linear_attention_step(*ops, late, state_out=got, stream=side)
+    side.synchronize()
+    assert torch.equal(y2, y) and torch.equal(got, out)
+
+
+@pytest.mark.parametrize("prepared", [False, True])
+def test_step_captured(prepared):
+    # a decode loop: the state in place, a token per replay
+    ops, first = step_inputs(seed=1)
+    tokens = [step_inputs(seed=2 + i)[0] for i in range(4)]
+    want, st = [], first.clone()
+    for t in tokens:
+        want.append(swimba.linear_attention_step(*t, st))
+    held, y = first.clone(), torch.empty_like(want[0])
+    call = swimba.PreparedLinearAttentionStep(*ops, held, y=y)
+    if not prepared:
+        def call():
+            return swimba.linear_attention_step(*ops, held, y=y)
+    call()  # warm-up
+    held.copy_(first)
+    y.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    assert torch.equal(held, first) and not y.any()  # recorded, not run
+    for t, w in zip(tokens, want):
+        for dst, src in zip(ops, t):
+            dst.copy_(src)
+        graph.replay()
+        other = swimba.linear_attention_step(*t, first.clone())  # eager work between the replays
+        torch.cuda.synchronize()
+        assert torch.equal(y, w) and torch.isfinite(other).all()
+    assert torch.equal(held, st)
