@@ -312,13 +312,13 @@ def _run_own(st, op):
                                                         dh_final=st["dh"], grad_dtype=st["v"].dtype))
         return out
     if op == "la_step":
-        # a decode loop marshals its call once and keeps the buffers
-        call = st.get("call")
-        if call is None:
-            st["state_out"] = torch.empty_like(st["h0"])
-            call = st["call"] = swimba.PreparedLinearAttentionStep(st["q"], st["k"], st["v"], st["g"], st["h0"],
-                                                                   state_out=st["state_out"])
-        return {"y": call(), "state": st["state_out"]}
+        # a decode loop marshals its call once for its buffers (which the call holds); others get a call of their own
+        ops = (st["q"], st["k"], st["v"], st["g"], st["h0"])
+        made = st.get("made")
+        if made is None or made[0] != list(map(id, ops)):
+            out = torch.empty_like(st["h0"])
+            made = st["made"] = (list(map(id, ops)), out, swimba.PreparedLinearAttentionStep(*ops, state_out=out))
+        return {"y": made[2](), "state": made[1]}
     if op == "route_grad":
         dx, dWr = swimba.route_backward(st["x"], st["Wr"], st["idx"], st["gate"], st["dgate"], grad_dtype=st["x"].dtype)
         return {"dx": dx, "dWr": dWr}
