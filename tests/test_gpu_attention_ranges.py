@@ -81,3 +81,64 @@ def test_columns_of_non_finite_values_are_apart(H, L, N, P, dtype, bad):
         lost = torch.zeros_like(got, dtype=torch.bool)
         lost[0, (slice(s, None) if n == "dq" else slice(0, s + 1)), 1, col] = True
         assert not torch.isfinite(got[lost]).any() and torch.equal(got[~lost], grads[n][~lost]), n
+
+
+def segments(q, v, g):
+    """Segments of the forward walk, from the workspace that holds their states."""
+    B, L, H, P = v.shape
+    state = B * H * q.shape[-1] * P * 4
+    return max(1, swimba.linear_attention_workspace_bytes(q, q, v, g) // state)
+
+
+def check(shape, dtype, form, gdt, h0=True, reset=0, seed=0):
+    B, L, H, G, N, P = shape
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device=DEV)
+
+    q, k = (normal(B, L, G, N) * N ** -0.25 for _ in range(2))
+    v, dy = normal(B, L, H, P), normal(B, L, H, P)
+    if form == "head":  # from 1 - 1/4 to 1 - 1/1024
+        g = torch.log1p(-torch.exp2(-torch.linspace(2, 10, H, device=DEV)))
+    else:
+        g = -0.2 * normal(B, L, H).abs() * torch.rand(H, generator=gen, device=DEV)
+        if reset:
+            g[torch.rand(B, L, generator=gen, device=DEV) < 1 / reset] = -float("inf")
+    q, k, v, dy = (t.to(dtype) for t in (q, k, v, dy))
+    st, dh = (normal(B, H, N, P), normal(B, H, N, P)) if h0 else (None, None)
+    y, h = swimba.linear_attention(q, k, v, g, h0=st, y_dtype=gdt)
+    got = swimba.linear_attention_backward(q, k, v, g, dy, h0=st, dh_final=dh, grad_dtype=gdt)
+    want, size = refs.attention_on_device(q, k, v, g, st, dy, dh)
+    for name, t in dict(got, y=y, h_final=h).items():
+        b = refs.roundings(N, P, L, gdt == torch.float32 or name not in ("y", "dv")) + H // G * refs.U32
+        worst = off(t, want[name], size[name], b)
+        assert worst <= 1, (name, worst)
+    return segments(q, v, g), -(-L // 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("form", ["head", "token", "documents"])
+@pytest.mark.parametrize("shape", [(4, 1300, 80, 80, 16, 16), (3, 1000, 120, 30, 24, 40)], ids=str)
+def test_whole_walks_of_many_chunks(shape, form, dtype):
+    nseg, chunks = check(shape, dtype, form, torch.float32, h0=form != "head", reset=300 * (form == "documents"))
+    assert nseg == 1 and chunks >= 16
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("form", ["head", "token", "documents"])
+@pytest.mark.parametrize("shape", [(2, 1400, 40, 40, 16, 16), (4, 1500, 32, 8, 128, 128), (4, 1100, 24, 24, 64, 64),
+                                   (2, 900, 30, 10, 33, 50), (2, 1100, 20, 20, 40, 256)], ids=str)
+def test_segments_of_several_chunks(shape, form, dtype):
+    gdt = dtype if form == "head" else torch.float32
+    nseg, chunks = check(shape, dtype, form, gdt, h0=form != "head", reset=250 * (form == "documents"), seed=1)
+    # fp32 rows of 128 leave one workgroup per CU: whole walks of 24 chunks there
+    assert chunks > nseg and (nseg > 1) == (dtype == torch.bfloat16 or shape[4] < 128)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("shape", [(1, 200, 2, 1, 96, 256), (1, 130, 1, 1, 40, 200), (2, 70, 3, 3, 256, 256),
+                                   (1, 1100, 2, 2, 256, 256), (1, 65, 2, 1, 7, 131), (1, 700, 4, 2, 200, 136)], ids=str)
+def test_rows_of_more_than_128(shape, dtype):
+    for form, gdt in (("head", torch.float32), ("token", dtype)):
+        check(shape, dtype, form, gdt, reset=100 * (form == "token"), seed=2)
