@@ -545,7 +545,9 @@ typedef struct {
 /*
  * swimba_linear_attention_backward -- gradients of swimba_linear_attention, from its inputs
  * (nothing of the forward pass is kept).  Workspace as there, sized by
- * swimba_linear_attention_backward_workspace_size(g).  Every output is deterministic.
+ * swimba_linear_attention_backward_workspace_size(g) for the same arguments: 16 B H L
+ * ceil(N / 32) bytes of sums, 4 B H L N of rows per head where heads share q and k,
+ * and up to three sets of segments' states.  Every output is deterministic.
  * An infinity or a NaN of k or v reaches dq and dlog_decay of later tokens only,
  * besides its own token's dq, dk and dv; one of q or dy dk, dv and dlog_decay of
  * its token and earlier ones, dh0, and its own token's dq.  (A q or dy before such

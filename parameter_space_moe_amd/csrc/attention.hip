@@ -461,9 +461,11 @@ WalkPlan plan_walk(bool f32, int B, int L, int H, int share, int Kd, int Cd, int
                             : attn_resident<bf16_t>(Kd, w.waves));
   int64_t want = base > 0 ? hold / base : 1;
   if (want > nc) want = nc;
-  // A chunk takes a lone workgroup of a CU two thirds of the time it takes two
-  // at once: halves of walks that fill the CUs once would only add the pass
-  // (1.4B-like prompts: 416 us in halves, 375 us whole).
+  // Four waves of a lone workgroup take every SIMD of a CU: halves of such walks
+  // would only add the pass (8 x 4096 tokens, 32 heads of 128 x 128, both on one
+  // card: 410 us in halves, 387 us whole).  Two waves leave SIMDs idle, and halves
+  // would gain there (4 x 8192, 64 heads of 128 x 64: 1049 us against 1268 us as it
+  // is; 3 x 3000, 100 heads of 64 x 64: 214 us against 263 us): not taken yet.
   if (want < 3 || nc < 4) want = 1;
   w.seg_chunks = (int)((nc + want - 1) / want);
   if (w.seg_chunks < 1) w.seg_chunks = 1;

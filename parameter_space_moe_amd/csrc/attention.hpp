@@ -21,12 +21,14 @@
 // token enters on the value side (w * V), which a wave reads for itself, so
 // that K stays as it came.
 //
-// What bounds it (MI355X, bf16, N = 128; 1280-column 64K-token prompt, 41 chunks
-// by each of 500 workgroups, two per CU): 8.6 us per chunk and CU, of which the
-// matrix units are busy 29 % (98 instructions of 32 cycles per wave and chunk)
-// and the VALU 41 % (1110 instructions, most of them the splits below); the two
-// hardly overlap with two waves per SIMD, the registers' limit (64 of state, 32
-// of results, 48 of rows on their way).  Memory would allow a third of the time.
+// What bounds it (MI355X, bf16, N = 128; 2560-column 64K-token prompt, 41 chunks
+// by each of 500 workgroups, two per CU): 9.0 us per chunk and CU.  Of a CU's busy
+// cycles the matrix units take 35 % (98 instructions of 32 cycles per wave and
+// chunk) and vector issue 50 % (1115 instructions, most of them the splits
+// below; each wave splits the shared scores for itself), and 13 % see a conflict
+// of LDS banks; the two hardly overlap with two waves per SIMD, the registers'
+// limit (64 of state, 32 of results, 48 of rows on their way).  Memory would
+// allow a third of the time.
 // Measured on the way: loads issued under per-pack branches waited for each
 // other (34 us per chunk); one workgroup per CU, when the LDS passed 80 KB by
 // half a KB, cost 1.6 x; an exponential per pair instead of two factors per
