@@ -584,8 +584,9 @@ typedef struct {
 /*
  * swimba_linear_attention_step -- one decoding step of swimba_linear_attention on a
  * persistent state: the same as a sequence of one token with h0 = state and
- * h_final = state_out (or state), but that an infinity of v enters the sums as
- * such.  Constraints: those of swimba_linear_attention.
+ * h_final = state_out (or state), but that infinities enter the sums as such
+ * (the sequence may give NaN for them).  Constraints: those of
+ * swimba_linear_attention.
  */
 int swimba_linear_attention_step(const swimba_linear_attention_step_args* a, hipStream_t stream);
 
