@@ -590,6 +590,182 @@ typedef struct {
  */
 int swimba_linear_attention_step(const swimba_linear_attention_step_args* a, hipStream_t stream);
 
+/*
+ * The gated delta rule: linear attention whose write first takes out of the state
+ * what it holds under the token's key ([SW] Spanish summary "Arquitectura de Swimba"
+ * and [MB] "SSMs" give the recurrence h_t = A h_{t-1} + B x_t; here A_t =
+ * e^{g_t} (I - beta_t k_t k_t^T)):
+ *   h~  = exp(log_decay_t) h_{t-1},   u_t = beta_t (v_t - h~^T k_t),
+ *   h_t = h~ + k_t u_t^T,             y_t = h_t^T q_t.
+ * It is stable where beta_t |k_t|^2 <= 2 (keys of unit length and beta in [0, 2]:
+ * swimba_norm_rotate); longer keys are taken as they are.
+ */
+typedef struct {
+  int B, L, H, G, N, P;         /* as in swimba_linear_attention_args                      */
+  swimba_dtype in_dtype;        /* dtype of q, k, v                                       */
+  swimba_dtype y_dtype;         /* dtype of y                                             */
+  swimba_decay_form decay_form; /* log_decay is [H] (HEAD) or [B, L, H] (TOKEN)           */
+  const void* q;                /* [B, L, G, N]                                           */
+  const void* k;                /* [B, L, G, N]                                           */
+  const void* v;                /* [B, L, H, P]                                           */
+  const float* log_decay;       /* natural logarithm of the decay, <= 0; -INFINITY clears
+                                   the state (the first token of a packed document).
+                                   Values above 0 are taken as they are                   */
+  const float* beta;            /* [B, L, H]  how much of the write is done               */
+  const float* h0;              /* NULL = zeros; [B, H, N, P]                             */
+  void* y;                      /* [B, L, H, P]  out                                      */
+  float* h_final;               /* NULL = not written; [B, H, N, P]                       */
+} swimba_delta_rule_args;
+
+/*
+ * swimba_delta_rule -- the whole sequence, 64 tokens at a time on the matrix units.
+ *   ws, ws_bytes: device workspace of at least
+ *   swimba_delta_rule_workspace_size(a) bytes, 256-byte aligned.
+ * bf16 inputs multiply exactly; what is computed and fp32 inputs enter products as
+ * three bf16 terms (within 2^-27 of their size; two, 2^-18, for what only reaches a
+ * bf16 y); sums and states are fp32.  An infinity or
+ * a NaN of q reaches its token's outputs, one of k, beta or a decay the outputs of
+ * its token and all later ones of its sequence and head as NaN (one of v in its own
+ * column only), also across a cleared state, and never an earlier token.
+ * h_final may be h0 itself; otherwise no output overlaps an input or another
+ * output.
+ * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256 (128 with fp32
+ * inputs), L <= 2^30, H * P and G * N < 2^23, B * H * max(ceil(P / 32), ceil(L / 64)) < 2^24 (SWIMBA_EUNSUPPORTED
+ * above).  L == 0 writes h_final = h0 (or zeros).
+ */
+size_t swimba_delta_rule_workspace_size(const swimba_delta_rule_args* a);
+int swimba_delta_rule(const swimba_delta_rule_args* a, void* ws, size_t ws_bytes,
+                      hipStream_t stream);
+
+typedef struct {
+  swimba_delta_rule_args fwd;   /* the forward call's arguments; its y and h_final are not
+                                   used                                                    */
+  const void* dy;               /* [B, L, H, P]  dL/dy, dtype in_dtype                     */
+  const float* dh_final;        /* [B, H, N, P]  dL/dh_final, or NULL for zero             */
+  swimba_dtype grad_dtype;      /* dtype of dq, dk, dv                                     */
+  void* dq;                     /* [B, L, G, N]  out, summed over the heads that share it  */
+  void* dk;                     /* [B, L, G, N]  out, summed over the heads that share it  */
+  void* dv;                     /* [B, L, H, P]  out                                       */
+  float* dlog_decay;            /* [H] (summed over batch and tokens) or [B, L, H]  out; 0
+                                   where exp(log_decay) is 0                               */
+  float* dbeta;                 /* [B, L, H]     out                                       */
+  float* dh0;                   /* [B, H, N, P]  out, or NULL                              */
+} swimba_delta_rule_grad_args;
+
+/*
+ * swimba_delta_rule_backward -- gradients of swimba_delta_rule, from its inputs (nothing
+ * of the forward pass is kept).  Workspace as there, sized by
+ * swimba_delta_rule_backward_workspace_size(g) for the same arguments: per 64 tokens
+ * and head two states of (N rounded up to a power of two) x (P to a multiple of 64)
+ * floats, two sets of 64 rows of P and 55 KB; 8 B H L N bytes of rows per head where heads
+ * share q and k.  Every output is deterministic.  All inputs must be finite (log_decay
+ * may be -INFINITY): an infinity or a NaN leaves the gradients of its sequence and
+ * head, and of the heads that share its q and k, without meaning.
+ * dh0 may be dh_final itself; otherwise no output overlaps an input or another
+ * output.
+ * Constraints: those of swimba_delta_rule, and B * L * G * ceil(N / 8) below
+ * 2^32 - 256.  L == 0 or B == 0 writes dh0 = dh_final (or zeros) and a zero
+ * dlog_decay [H].
+ */
+size_t swimba_delta_rule_backward_workspace_size(const swimba_delta_rule_grad_args* g);
+int swimba_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+
+typedef struct {
+  int B, H, G, N, P;
+  swimba_dtype in_dtype, y_dtype;
+  swimba_decay_form decay_form; /* log_decay is [H] (HEAD) or [B, H] (TOKEN)               */
+  const void* q;                /* [B, G, N]                                               */
+  const void* k;                /* [B, G, N]                                               */
+  const void* v;                /* [B, H, P]                                               */
+  const float* log_decay;
+  const float* beta;            /* [B, H]                                                  */
+  float* state;                 /* [B, H, N, P] fp32, read; updated in place unless
+                                   state_out is given                                      */
+  float* state_out;             /* NULL, or [B, H, N, P] out: `state` itself or a buffer
+                                   that does not overlap it                                */
+  void* y;                      /* [B, H, P] out                                           */
+} swimba_delta_rule_step_args;
+
+/*
+ * swimba_delta_rule_step -- one decoding step of swimba_delta_rule on a persistent state:
+ * the same as a sequence of one token with h0 = state and h_final = state_out (or
+ * state), in fp32 throughout, but that infinities enter the sums as such.
+ * Constraints: those of swimba_delta_rule (N <= 256 for either dtype), and B * H *
+ * ceil(P / 16) < 2^24.
+ */
+int swimba_delta_rule_step(const swimba_delta_rule_step_args* a, hipStream_t stream);
+
+/*
+ * Norms of queries and keys for each head, with the rotation of their positions in the
+ * same pass: what stands before swimba_linear_attention and swimba_delta_rule.  Of each
+ * row x of N elements (a token's q or k of one head),
+ *   n = x / sqrt(c <x, x> + eps),  c = 1 / N (RMS) or 1 (L2)
+ *   y = scale Rot(n * w),          scale = q_scale for queries, 1 for keys,
+ * where Rot turns the pair i < R / 2 of the first R elements, (i, i + R / 2) for
+ * HALVES or (2 i, 2 i + 1) for NEIGHBOURS, by the angle positions[t] * rates[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin).
+ */
+typedef enum { SWIMBA_NORM_RMS = 0, SWIMBA_NORM_L2 = 1 } swimba_norm;
+typedef enum { SWIMBA_PAIRS_HALVES = 0, SWIMBA_PAIRS_NEIGHBOURS = 1 } swimba_pairs;
+
+typedef struct {
+  int64_t T;                    /* tokens                                                 */
+  int Hq, Hk, N, R;             /* heads of q and of k, their size, elements turned (even) */
+  swimba_dtype in_dtype;        /* dtype of q and k                                       */
+  swimba_dtype out_dtype;       /* dtype of q_out and k_out                               */
+  swimba_norm norm;
+  swimba_pairs pairs;
+  float eps;                    /* > 0                                                    */
+  float q_scale;
+  const void* q;                /* [T, Hq, N], tokens q_stride elements apart             */
+  const void* k;                /* [T, Hk, N], tokens k_stride elements apart             */
+  int64_t q_stride, k_stride;   /* 0 = Hq * N, Hk * N (q and k may be parts of one
+                                   projection's rows)                                     */
+  const float* wq;              /* [N], or NULL for ones                                  */
+  const float* wk;              /* [N], or NULL for ones                                  */
+  const int32_t* positions;     /* [T]; not read with R == 0                              */
+  const float* rates;           /* [R / 2] radians per position; not read with R == 0     */
+  void* q_out;                  /* [T, Hq, N] out                                         */
+  void* k_out;                  /* [T, Hk, N] out                                         */
+} swimba_norm_rotate_args;
+
+/*
+ * swimba_norm_rotate -- sums of squares and everything else in fp32, angles in 64 bits
+ * less their whole turns.  Rows are independent: what is not finite stays in its row.
+ * q_out may be q itself (of the same dtype, dense rows), and k_out k; otherwise no
+ * output overlaps an input or another output.
+ * Constraints: T >= 0; Hq, Hk, N >= 1; 0 <= R <= N, even; eps a normal number above 0;
+ * strides of a token at least its heads' elements (SWIMBA_EINVAL); N <= 512, Hq + Hk <=
+ * 2^16, T * (Hq + Hk) <= 2^40, T <= 2^31 (SWIMBA_EUNSUPPORTED above).
+ */
+int swimba_norm_rotate(const swimba_norm_rotate_args* a, hipStream_t stream);
+
+typedef struct {
+  swimba_norm_rotate_args fwd;  /* the forward call's arguments; its q_out, k_out and
+                                   out_dtype are not used                                  */
+  const void* dq_out;           /* [T, Hq, N]  dL/dq_out, dtype in_dtype, dense            */
+  const void* dk_out;           /* [T, Hk, N]  dL/dk_out                                   */
+  swimba_dtype grad_dtype;      /* dtype of dq and dk                                      */
+  void* dq;                     /* [T, Hq, N]  out                                         */
+  void* dk;                     /* [T, Hk, N]  out                                         */
+  float* dwq;                   /* [N] out, summed over tokens and heads, or NULL          */
+  float* dwk;                   /* [N] out, or NULL                                        */
+} swimba_norm_rotate_grad_args;
+
+/*
+ * swimba_norm_rotate_backward -- gradients of swimba_norm_rotate, from its inputs.  dwq and dwk
+ * may be asked for without wq and wk (the gradient at ones).
+ *   ws, ws_bytes: device workspace of at least
+ *   swimba_norm_rotate_backward_workspace_size(g) bytes, 256-byte aligned; 0 without
+ *   dwq and dwk.
+ * Deterministic.  dq may be dq_out itself (of the same dtype), and dk dk_out; otherwise no
+ * output overlaps an input or another output.  T == 0 writes zero dwq and dwk.
+ */
+size_t swimba_norm_rotate_backward_workspace_size(const swimba_norm_rotate_grad_args* g);
+int swimba_norm_rotate_backward(const swimba_norm_rotate_grad_args* g, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
 /* Static string for a status code. */
 const char* swimba_status_string(int status);
 

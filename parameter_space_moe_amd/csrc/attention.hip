@@ -411,34 +411,13 @@ __global__ __launch_bounds__(256) void attn_copy_kernel(const float* in, float* 
     out[i] = in != nullptr ? in[i] : 0.f;
 }
 
-int copy_or_zero(const float* in, float* out, int64_t n, hipStream_t s) {
-  if (n <= 0) return SWIMBA_OK;
-  const int64_t wg = (n + 255) / 256 < (1 << 20) ? (n + 255) / 256 : 1 << 20;
-  hipLaunchKernelGGL(attn_copy_kernel, dim3((unsigned)wg), dim3(256), 0, s, in, out, n);
-  return checked();
-}
-
 // The walks load whole packs inside a tensor.  One of fewer elements than a pack
 // (a token of a few features) is first copied to a slot of the workspace.
-constexpr size_t kTinySlot = 256;
 template <typename T>
 __global__ __launch_bounds__(64) void attn_tiny_kernel(const T* in, T* out, int n) {
   if (threadIdx.x < kPack) out[threadIdx.x] = (int)threadIdx.x < n ? in[threadIdx.x] : T(0);
 }
 bool is_tiny(int64_t n) { return n < kPack; }
-// The rows to read: `rows` itself or its copy at `slot`.
-const void* whole_packs(const void* rows, int64_t n, bool f32, unsigned char* slot, hipStream_t s,
-                        int* rc) {
-  if (!is_tiny(n) || *rc != SWIMBA_OK) return rows;
-  if (f32)
-    hipLaunchKernelGGL(attn_tiny_kernel<float>, dim3(1), dim3(64), 0, s,
-                       static_cast<const float*>(rows), reinterpret_cast<float*>(slot), (int)n);
-  else
-    hipLaunchKernelGGL(attn_tiny_kernel<bf16_t>, dim3(1), dim3(64), 0, s,
-                       static_cast<const bf16_t*>(rows), reinterpret_cast<bf16_t*>(slot), (int)n);
-  *rc = checked();
-  return slot;
-}
 
 // How one walk is laid out over the device.
 struct WalkPlan {
@@ -593,19 +572,48 @@ T* at(void* ws, size_t off) {
 
 int share_sum(const float* rows, void* out, swimba_dtype d, const swimba_linear_attention_args* a,
               hipStream_t s) {
-  const int64_t r = (int64_t)a->B * a->L * a->G;
-  const int64_t packs = r * ((a->N + kPack - 1) / kPack);
-  const dim3 grid((unsigned)((packs + 255) / 256));
-  if (d == SWIMBA_BF16)
-    hipLaunchKernelGGL((attn_share_sum_kernel<bf16_t>), grid, dim3(256), 0, s, rows,
-                       static_cast<bf16_t*>(out), r, a->H / a->G, a->N);
-  else
-    hipLaunchKernelGGL((attn_share_sum_kernel<float>), grid, dim3(256), 0, s, rows,
-                       static_cast<float*>(out), r, a->H / a->G, a->N);
-  return checked();
+  return sum_shared_heads(rows, out, d, (int64_t)a->B * a->L * a->G, a->H / a->G, a->N, s);
 }
 
 }  // namespace
+
+int copy_or_zero(const float* in, float* out, int64_t n, hipStream_t s) {
+  if (n <= 0) return SWIMBA_OK;
+  const int64_t wg = (n + 255) / 256 < (1 << 20) ? (n + 255) / 256 : 1 << 20;
+  hipLaunchKernelGGL(attn_copy_kernel, dim3((unsigned)wg), dim3(256), 0, s, in, out, n);
+  return checked();
+}
+
+const void* whole_packs(const void* rows, int64_t n, bool f32, unsigned char* slot, hipStream_t s,
+                        int* rc) {
+  if (!is_tiny(n) || *rc != SWIMBA_OK) return rows;
+  if (f32)
+    hipLaunchKernelGGL(attn_tiny_kernel<float>, dim3(1), dim3(64), 0, s,
+                       static_cast<const float*>(rows), reinterpret_cast<float*>(slot), (int)n);
+  else
+    hipLaunchKernelGGL(attn_tiny_kernel<bf16_t>, dim3(1), dim3(64), 0, s,
+                       static_cast<const bf16_t*>(rows), reinterpret_cast<bf16_t*>(slot), (int)n);
+  *rc = checked();
+  return slot;
+}
+
+int sum_shared_heads(const float* rows, void* out, swimba_dtype d, int64_t n, int share, int N,
+                     hipStream_t s) {
+  const int64_t packs = n * ((N + kPack - 1) / kPack);
+  const dim3 grid((unsigned)((packs + 255) / 256));
+  if (d == SWIMBA_BF16)
+    hipLaunchKernelGGL((attn_share_sum_kernel<bf16_t>), grid, dim3(256), 0, s, rows,
+                       static_cast<bf16_t*>(out), n, share, N);
+  else
+    hipLaunchKernelGGL((attn_share_sum_kernel<float>), grid, dim3(256), 0, s, rows,
+                       static_cast<float*>(out), n, share, N);
+  return checked();
+}
+
+int sum_decay_parts(const double* part, float* dg, int B, int H, int nc, hipStream_t s) {
+  hipLaunchKernelGGL(attn_decay_sum_kernel, dim3(H), dim3(256), 0, s, part, dg, B, H, nc);
+  return checked();
+}
 
 size_t attention_bytes(const swimba_linear_attention_args* a, int dev) {
   if (a->B == 0 || a->L == 0) return 0;

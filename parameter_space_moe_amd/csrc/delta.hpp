@@ -1,0 +1,1224 @@
+// The gated delta rule, in chunks on the matrix units.
+//
+//   h~ = e^{g_t} h_{t-1},  u_t = beta_t (v_t - h~^T k_t),  h_t = h~ + k_t u_t^T,  y_t = h_t^T q_t.
+// With h the state before a chunk of 64 tokens, G_t the running sum of g inside it,
+// D[t][s] = e^{G_t - G_s}, w_s = e^{G_end - G_s} and o_t = u_t / beta_t:
+//   (I + A diag(beta)) O = V - e^G K h,   A[t][s] = D[t][s] k_t . k_s  for s < t
+//   y  = e^G Q h + ((Q K^T) * D) (beta O),   h' = e^{G_end} h + K^T (w beta O).
+// The 64 x 64 inverse T = (I + A diag(beta))^-1 and the decayed scores
+// S = (Q K^T) * D depend on no state: delta_prep_kernel makes them for every
+// chunk and head at once.  delta_walk_kernel carries the state through them.
+// Backwards, with a = dL/dh' and dU = dL/d(beta O):
+//   dU = S^T dY + w K a,   dV = T^T (beta dU),
+//   a0 = e^{G_end} a + Q^T (e^G dY) - K^T (e^G dV),
+// the same walk with operands exchanged; delta_grad_kernel makes the other
+// gradients from each chunk's h, a, O and dV, every chunk for itself.
+//
+// Mapping of a walk.  A wave owns 16 columns of the state (its 16 x 16 accumulator
+// tiles hold h[n][c] in fp32 for the whole walk).  Register for register the
+// accumulator layout of two tiles is the layout of the other operand of a product
+// over their 32 rows when these run in the order n = 4 g + j, 16 + 4 g + j
+// (g = lane / 16, j < 4): state, O and U go from one product to the next without
+// leaving their lane.  K and Q rows lie in LDS in that order.
+//
+// Roundings.  bf16 inputs multiply exactly.  What is computed in fp32 and enters a
+// product, and fp32 inputs, are three bf16 terms, which hold them within 2^-27 of their
+// size (2^-9 for each of three round-to-nearests); of a product of two such operands
+// the pairs of 2^-27 and below are left out.  Two terms (2^-18) take part in a y that is
+// rounded to bf16 anyway; with two in the states and gradients as well these were off by
+// 3 to 7e-6 in the 2-norm, a decay's gradient that cancels over the tokens by 1e-4.
+// Sums, states and inverses are fp32; sums of log decays are in 64 bits.
+#pragma once
+#include "attention.hpp"
+
+namespace swimba {
+
+typedef float f4x __attribute__((ext_vector_type(4)));
+
+constexpr int kDeltaBlocks = 6;               // 16 x 32 blocks of a triangle of 64 x 64
+constexpr int kDeltaTri = kDeltaBlocks * 512; // values of one term of a triangle
+constexpr int kDeltaTerms = 3;
+constexpr int kDeltaGates = 4 * kChunk;       // floats: e^G, w, beta; e^{G_end}, first bad token
+
+struct DeltaParams {
+  const void *q, *k, *v, *dy;
+  void* out;              // y, or dv
+  const float *g, *beta;  // [H] or [B, L, H]; [B, L, H]
+  int B, L, H, G, N, P;
+  int token_decay, out_bf16;
+  int nc;                 // chunks
+  int ctiles;             // columns / 64, rounded up
+  int score_terms;        // 2 where y is bf16
+  // workspace, per (b, h, chunk)
+  bf16_t *tri, *tri_t;    // [3][kDeltaTri] T in operand order; its transpose (backward)
+  bf16_t* score;          // [3][kDeltaTri] S, or its transpose (backward)
+  float* gates;           // [kDeltaGates]
+  const float* s0;        // first state or null, [B, H, N, P]
+  float* s_final;         // or null
+  float* states;          // [N', P'] the state before (behind: walking back) the chunk
+  float* rows;            // [64, P'] O, or dV
+  int Pp;                 // P' = P rounded up to 64
+};
+
+__device__ __forceinline__ f4x mma16(bf8x a, bf8x b, f4x c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4x mma16(float a, float b, f4x c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// c += a b of operands in terms, smallest products first; pairs of terms beyond the finer
+// operand's last one are left out.
+template <int NA, int NB>
+__device__ __forceinline__ f4x mma_terms(const bf8x* a, const bf8x* b, f4x c) {
+  constexpr int kLast = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+  for (int n = kLast; n >= 0; --n)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (n - i >= 0 && n - i < NB) c = mma16(a[i], b[n - i], c);
+  return c;
+}
+
+// Two accumulator tiles as one operand in S terms.
+template <int S>
+__device__ __forceinline__ void split_tiles(f4x lo, f4x hi, bf8x* out) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = lo[i];
+    x[4 + i] = hi[i];
+  }
+  split_terms<S>(x, out);
+}
+
+// Place of column `col` (a multiple of four) of a row in operand order.
+__device__ __forceinline__ int operand_place(int col) {
+  const int c = col & 31;
+  return (col & ~31) + (c < 16 ? 2 * c : 2 * (c - 16) + 4);
+}
+
+// First block of row tile rt of a triangle (tiles 0, 1: one block of 32, tiles 2, 3:
+// two), and of its transpose (tiles 0, 1: two blocks, tiles 2, 3: the second).
+__device__ __forceinline__ constexpr int tri_block(int rt, int b) {
+  return rt < 2 ? rt : 2 * rt - 2 + b;
+}
+__device__ __forceinline__ constexpr int tri_block_t(int rt, int b) {
+  return rt < 2 ? 2 * rt + b : 2 + rt;
+}
+
+template <typename TI, int KT>
+struct DeltaShape {
+  static constexpr bool kF32 = sizeof(TI) == 4;
+  static constexpr int kTerms = kF32 ? kDeltaTerms : 1;
+  static constexpr int kRows = 32 * KT;
+  static constexpr int kStride = kRows + 8;
+  static constexpr int kTile = kChunk * kStride;  // values of one term
+};
+
+constexpr int kDeltaThreads = 256, kDeltaWaves = 4;
+
+// The staged rows of a chunk into LDS, in operand order and in terms; rows from `len` on
+// are zero.
+template <typename TI, int KT, bool LOOSE>
+struct DeltaRows {
+  using Stage = RowStage<TI, 32 * KT, kDeltaThreads, LOOSE>;
+  using Sh = DeltaShape<TI, KT>;
+  static __device__ __forceinline__ void put(const Stage& st, int round, bf16_t* dst) {
+#pragma unroll
+    for (int i = 0; i < Stage::kRound; ++i) {
+      u4x w[Stage::kQuads];
+      st.pack(round, i, w);
+      bf16_t* d = dst + st.row(round * Stage::kRound + i) * Sh::kStride +
+                  operand_place(st.column());
+      if constexpr (Sh::kF32) {
+        float x[8];
+        __builtin_memcpy(x, w, sizeof(x));
+        bf8x t[Sh::kTerms];
+        split_terms<Sh::kTerms>(x, t);
+#pragma unroll
+        for (int s = 0; s < Sh::kTerms; ++s) {
+          struct { uint2 a, b; } o = __builtin_bit_cast(decltype(o), t[s]);
+          *reinterpret_cast<uint2*>(d + s * Sh::kTile) = o.a;
+          *reinterpret_cast<uint2*>(d + s * Sh::kTile + 8) = o.b;
+        }
+      } else {
+        *reinterpret_cast<uint2*>(d) = make_uint2(w[0][0], w[0][1]);
+        *reinterpret_cast<uint2*>(d + 8) = make_uint2(w[0][2], w[0][3]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void all(Stage& st, bf16_t* dst) {
+#pragma unroll
+    for (int r = 0; r < Stage::kRounds; ++r) {
+      if (r > 0) st.load(r);
+      put(st, r, dst);
+    }
+  }
+  static __device__ __forceinline__ void place(Stage& st, const void* base, const DeltaParams& p,
+                                               int b, int grp, int t0, int len, int tid) {
+    const int64_t stride = (int64_t)p.G * p.N, all = (int64_t)p.B * p.L * stride;
+    st.base = static_cast<const TI*>(base);
+    st.total = all < kPack ? kPack : all;  // (smaller tensors were copied to whole packs)
+    st.first = ((int64_t)b * p.L + t0) * stride + (int64_t)grp * p.N;
+    st.stride = stride;
+    st.cols = p.N;
+    st.len = len;
+    st.tid = tid;
+    st.down = false;
+  }
+};
+
+// Operand of 16 rows (from `row`) by 32 columns (block b) of staged rows.
+template <typename Sh>
+__device__ __forceinline__ void row_operand(const bf16_t* tile, int row, int b, int lane,
+                                            bf8x* out) {
+#pragma unroll
+  for (int s = 0; s < Sh::kTerms; ++s)
+    out[s] = *reinterpret_cast<const bf8x*>(tile + s * Sh::kTile +
+                                            (row + (lane & 15)) * Sh::kStride + 32 * b +
+                                            8 * (lane >> 4));
+}
+
+// Operand of 16 columns (tile nt) by 32 rows (block b) of staged rows: the transposing
+// read hands lane i of 16 the column i of four rows, of which it points at row
+// i / 4, columns 4 (i % 4)..
+template <typename Sh>
+__device__ __forceinline__ void column_operand(const bf16_t* tile, int nt, int b, int lane,
+                                               bf8x* out) {
+  typedef __attribute__((address_space(3))) s4x* lds_s4;
+  const int i = lane & 15;
+  const bf16_t* p = tile + (32 * b + 4 * (lane >> 4) + (i >> 2)) * Sh::kStride + 32 * (nt >> 1) +
+                    8 * (i & 3) + 4 * (nt & 1);
+#pragma unroll
+  for (int s = 0; s < Sh::kTerms; ++s) {
+    struct { s4x a, b; } r;
+    r.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + s * Sh::kTile));
+    r.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + s * Sh::kTile + 16 * Sh::kStride));
+    out[s] = __builtin_bit_cast(bf8x, r);
+  }
+}
+
+// ---- what depends on no state -------------------------------------------------
+
+constexpr int kTriStride = kChunk + 4;
+
+// (I + A)^-1 of the strictly lower triangular 64 x 64 matrix in `a` (rows kTriStride
+// apart), into `t`, in fp32: the four 16 x 16 blocks on the diagonal by substitution, a lane per
+// column, then the blocks below them a block column per wave,
+//   T_ij = -T_ii sum_k A_ik T_kj,
+// where a product's result is register for register the next one's right operand.
+// Called by the workgroup; ends with a barrier.
+__device__ __forceinline__ void unit_inverse(const float* a, float* t, int lane, int wave) {
+  const int g = lane >> 4, col = lane & 15;
+  if (wave == 0) {
+    const float* d = a + 16 * g * kTriStride + 16 * g;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == col ? 1.f : 0.f;
+#pragma unroll
+      for (int k = 0; k < i; k += 4) {
+        const float4 r = *reinterpret_cast<const float4*>(d + i * kTriStride + k);
+        s = fmaf(-r.x, x[k], s);
+        if (k + 1 < i) s = fmaf(-r.y, x[k + 1], s);
+        if (k + 2 < i) s = fmaf(-r.z, x[k + 2], s);
+        if (k + 3 < i) s = fmaf(-r.w, x[k + 3], s);
+      }
+      x[i] = s;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[(16 * g + i) * kTriStride + 16 * g + col] = x[i];
+  }
+  __syncthreads();
+  if (wave < 3) {
+    f4x tk[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      tk[0][r] = t[(16 * wave + 4 * g + r) * kTriStride + 16 * wave + col];
+#pragma unroll
+    for (int n = 1; n < 4; ++n) {  // block row wave + n
+      if (wave + n > 3) break;
+      const int i = wave + n;
+      f4x s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < n; ++k) {
+        const float4 r = *reinterpret_cast<const float4*>(a + (16 * i + col) * kTriStride +
+                                                          16 * (wave + k) + 4 * g);
+        s = mma16(r.x, tk[k][0], s);
+        s = mma16(r.y, tk[k][1], s);
+        s = mma16(r.z, tk[k][2], s);
+        s = mma16(r.w, tk[k][3], s);
+      }
+      const float4 r =
+          *reinterpret_cast<const float4*>(t + (16 * i + col) * kTriStride + 16 * i + 4 * g);
+      f4x o = {0.f, 0.f, 0.f, 0.f};
+      o = mma16(-r.x, s[0], o);
+      o = mma16(-r.y, s[1], o);
+      o = mma16(-r.z, s[2], o);
+      o = mma16(-r.w, s[3], o);
+      tk[n] = o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        t[(16 * i + 4 * g + e) * kTriStride + 16 * wave + col] = o[e];
+    }
+  }
+  // blocks above the diagonal that share a 32-block with one below
+  for (int e = threadIdx.x; e < 2 * 256; e += kDeltaThreads) {
+    const int r = (e >> 8) * 32 + ((e >> 4) & 15), c = (e >> 8) * 32 + 16 + (e & 15);
+    t[r * kTriStride + c] = 0.f;
+  }
+  __syncthreads();
+}
+
+// A lower triangle in LDS to the operand order of a product with it, or with its
+// transpose, in two or three terms.  The triangle's 32-blocks are whole (zeros above).
+template <bool TRANSPOSED>
+__device__ __forceinline__ void put_triangle(const float* m, bf16_t* out, int terms, int tid) {
+  for (int e = tid; e < kDeltaBlocks * 64; e += kDeltaThreads) {
+    const int blk = e >> 6, lane = e & 63, g = lane >> 4;
+    int rt, b;
+    if (TRANSPOSED) {
+      rt = blk < 4 ? blk >> 1 : blk - 2;
+      b = blk < 4 ? blk & 1 : 1;
+    } else {
+      rt = blk < 2 ? blk : 2 + ((blk - 2) >> 1);
+      b = blk < 2 ? 0 : (blk - 2) & 1;
+    }
+    const int row = 16 * rt + (lane & 15);
+    float x[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = 32 * b + 16 * h + 4 * g;
+      if (TRANSPOSED) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * h + i] = m[(c + i) * kTriStride + row];
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(m + row * kTriStride + c);
+        x[4 * h] = v.x;
+        x[4 * h + 1] = v.y;
+        x[4 * h + 2] = v.z;
+        x[4 * h + 3] = v.w;
+      }
+    }
+    bf8x t[kDeltaTerms];
+    split_terms<kDeltaTerms>(x, t);
+#pragma unroll
+    for (int s = 0; s < kDeltaTerms; ++s)
+      if (s < terms) *reinterpret_cast<bf8x*>(out + s * kDeltaTri + blk * 512 + lane * 8) = t[s];
+  }
+}
+
+// First token of a chunk whose k, beta or decay is not finite, kChunk without one: it and
+// those behind it leave the products, and the walk makes what it reaches NaN.
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < __builtin_inff()); }
+
+template <typename TI, int KT>
+constexpr size_t delta_prep_lds() {
+  using Sh = DeltaShape<TI, KT>;
+  const size_t rows = 2 * (size_t)Sh::kTerms * Sh::kTile * sizeof(bf16_t);
+  const size_t tris = 2 * (size_t)kChunk * kTriStride * sizeof(float);
+  return (rows > tris ? rows : tris) + (size_t)kChunk * kTriStride * sizeof(float) +
+         4 * kChunk * sizeof(float);
+}
+
+// One workgroup per chunk and head.  BACK: for the gradients.
+template <typename TI, int KT, bool LOOSE, bool BACK>
+__global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p) {
+  using Sh = DeltaShape<TI, KT>;
+  using Rows = DeltaRows<TI, KT, LOOSE>;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
+  float* sA = reinterpret_cast<float*>(smem_raw);
+  float* sG = sA + kChunk * kTriStride;  // high and low parts of G, beta
+  bf16_t* sK = reinterpret_cast<bf16_t*>(sG + 4 * kChunk);
+  bf16_t* sQ = sK + Sh::kTerms * Sh::kTile;
+  float* sT = reinterpret_cast<float*>(sK);  // once the rows are done with
+  float* sP = sT + kChunk * kTriStride;
+  int* bad = reinterpret_cast<int*>(sG + 3 * kChunk);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int g = lane >> 4, col = lane & 15;
+  const int64_t unit = blockIdx.x;
+  const int c = (int)(unit % p.nc);
+  const int64_t bh = unit / p.nc;
+  const int b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
+  const int t0 = c * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
+
+  typename Rows::Stage rk, rq;
+  Rows::place(rk, p.k, p, b, h / (p.H / p.G), t0, len, tid);
+  Rows::place(rq, p.q, p, b, h / (p.H / p.G), t0, len, tid);
+  rk.load(0);
+  if (tid == 0) *bad = kChunk;
+  __syncthreads();
+  if (wave == 0) {
+    const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
+    float gt = 0.f, bt = 0.f;
+    if (lane < len) {
+      gt = p.token_decay ? p.g[at] : p.g[h];
+      bt = p.beta[at];
+    }
+    if (not_finite(bt) || !(gt < __builtin_inff())) atomicMin(bad, lane);
+    if (!(gt < __builtin_inff())) gt = 0.f;
+    const double d = (double)gt * 1.4426950408889634;
+    const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
+    const double end = last_lane(sum);
+    const float hi = (float)sum;
+    sG[lane] = hi;
+    sG[kChunk + lane] = (float)(sum - (double)hi);
+    sG[2 * kChunk + lane] = not_finite(bt) ? 0.f : bt;
+    float* gates = p.gates + unit * kDeltaGates;
+    gates[lane] = exp2_sum(sum);
+    gates[kChunk + lane] = exp2_sum(end - sum);
+    gates[2 * kChunk + lane] = not_finite(bt) ? 0.f : bt;
+    if (lane == 0) gates[3 * kChunk] = exp2_sum(end);
+  }
+#pragma unroll
+  for (int r = 0; r < Rows::Stage::kRounds; ++r) {
+    if (r > 0) rk.load(r);
+    if (rk.wild()) {
+      for (int i = 0; i < Rows::Stage::kRound; ++i) {
+        u4x w[Rows::Stage::kQuads];
+        rk.pack(r, i, w);
+        TI e[kPack];
+        __builtin_memcpy(e, w, sizeof(e));
+        bool wild = false;
+#pragma unroll
+        for (int n = 0; n < kPack; ++n) wild |= not_finite(to_f32(e[n]));
+        if (wild) atomicMin(bad, rk.row(r * Rows::Stage::kRound + i));
+      }
+    }
+    Rows::put(rk, r, sK);
+  }
+  rq.load(0);
+  Rows::all(rq, sQ);
+  __syncthreads();
+  const int first_bad = *bad;
+  if (first_bad < kChunk) {
+    for (int e = tid; e < (kChunk - first_bad) * Sh::kStride; e += kDeltaThreads) {
+#pragma unroll
+      for (int s = 0; s < Sh::kTerms; ++s)
+        sK[s * Sh::kTile + first_bad * Sh::kStride + e] = 0;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) p.gates[unit * kDeltaGates + 3 * kChunk + 1] = __int_as_float(first_bad);
+
+  // wave w: rows of tile w against the keys before them, and queries of tile 3 - w
+  f4x kk[4], qk[4];
+  const int rk_t = wave, rq_t = 3 - wave;
+#pragma unroll
+  for (int ct = 0; ct < 4; ++ct) {
+    kk[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+    qk[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+  }
+#pragma unroll
+  for (int n = 0; n < KT; ++n) {
+    bf8x ak[Sh::kTerms], aq[Sh::kTerms];
+    row_operand<Sh>(sK, 16 * rk_t, n, lane, ak);
+    row_operand<Sh>(sQ, 16 * rq_t, n, lane, aq);
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      if (ct > rk_t && ct > rq_t) continue;
+      bf8x bk[Sh::kTerms];
+      row_operand<Sh>(sK, 16 * ct, n, lane, bk);
+      if (ct <= rk_t) kk[ct] = mma_terms<Sh::kTerms, Sh::kTerms>(ak, bk, kk[ct]);
+      if (ct <= rq_t) qk[ct] = mma_terms<Sh::kTerms, Sh::kTerms>(aq, bk, qk[ct]);
+    }
+  }
+  auto decay = [&](int t, int s) {
+    return hw_exp2((sG[t] - sG[s]) + (sG[kChunk + t] - sG[kChunk + s]));
+  };
+#pragma unroll
+  for (int ct = 0; ct < 4; ++ct) {
+    const int s = 16 * ct + col;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tk = 16 * rk_t + 4 * g + r, tq = 16 * rq_t + 4 * g + r;
+      kk[ct][r] = s < tk ? kk[ct][r] * decay(tk, s) * sG[2 * kChunk + s] : 0.f;
+      qk[ct][r] = s <= tq ? qk[ct][r] * decay(tq, s) : 0.f;
+    }
+  }
+  __syncthreads();  // the rows are done with
+#pragma unroll
+  for (int ct = 0; ct < 4; ++ct)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      sA[(16 * rk_t + 4 * g + r) * kTriStride + 16 * ct + col] = kk[ct][r];
+      sP[(16 * rq_t + 4 * g + r) * kTriStride + 16 * ct + col] = qk[ct][r];
+    }
+  __syncthreads();
+  unit_inverse(sA, sT, lane, wave);
+  const int64_t to = unit * kDeltaTerms * kDeltaTri;
+  put_triangle<false>(sT, p.tri + to, kDeltaTerms, tid);
+  if (BACK) put_triangle<true>(sT, p.tri_t + to, kDeltaTerms, tid);
+  put_triangle<BACK>(sP, p.score + to, p.score_terms, tid);
+}
+
+// ---- the walk -------------------------------------------------------------------
+
+enum DeltaMode {
+  kDeltaOut = 0,    // y, in bf16
+  kDeltaOutF32 = 1, // y, in fp32
+  kDeltaKeep = 2,   // each chunk's first state, and O
+  kDeltaBack = 3    // dv, each chunk's last adjoint and dV, backwards
+};
+
+template <typename TI, int KT, int MODE>
+struct DeltaLds {
+  using Sh = DeltaShape<TI, KT>;
+  static constexpr bool kQ = MODE != kDeltaKeep;
+  static constexpr size_t kRows = (size_t)(kQ ? 2 : 1) * Sh::kTerms * Sh::kTile;
+  static constexpr int kScoreTerms = MODE == kDeltaOut ? 2 : kQ ? kDeltaTerms : 0;
+  static constexpr size_t kTris = (size_t)(kDeltaTerms + kScoreTerms) * kDeltaTri;
+  static constexpr size_t kBytes =
+      (kRows + kTris) * sizeof(bf16_t) + kDeltaGates * sizeof(float);
+};
+
+template <typename TI, int KT, bool LOOSE, int MODE>
+__global__ __launch_bounds__(kDeltaThreads, 1) void delta_walk_kernel(DeltaParams p) {
+  using Sh = DeltaShape<TI, KT>;
+  using Rows = DeltaRows<TI, KT, LOOSE>;
+  using Lds = DeltaLds<TI, KT, MODE>;
+  constexpr int NT = Sh::kTerms, HT = 2 * KT;  // terms of inputs; 16-row tiles
+  constexpr bool BACK = MODE == kDeltaBack, QUERY = Lds::kQ;
+  constexpr bool OUT = MODE == kDeltaOut || MODE == kDeltaOutF32;
+  constexpr int S = kDeltaTerms, YT = MODE == kDeltaOut ? 2 : S, QT = NT < YT ? NT : YT;
+  // 16-byte loads of the triangles' terms
+  constexpr int kTriPacks = S * kDeltaTri / 8, kScorePacks = Lds::kScoreTerms * kDeltaTri / 8;
+  constexpr int kTriLoads = (kTriPacks + kDeltaThreads - 1) / kDeltaThreads;
+  constexpr int kScoreLoads = (kScorePacks + kDeltaThreads - 1) / kDeltaThreads;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
+  bf16_t* sK = reinterpret_cast<bf16_t*>(smem_raw);
+  bf16_t* sQ = sK + NT * Sh::kTile;  // (QUERY)
+  bf16_t* sT = sK + Lds::kRows;
+  bf16_t* sP = sT + S * kDeltaTri;   // (QUERY)
+  float* sG = reinterpret_cast<float*>(sT + Lds::kTris);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int g = lane >> 4;
+  // neighbours (which read the same rows) on one XCD: workgroups go to the eight in turn
+  int blk = blockIdx.x;
+  {
+    const int n = gridDim.x, x = blk & 7, per = n >> 3, more = n & 7;
+    blk = x * per + (x < more ? x : more) + (blk >> 3);
+  }
+  const int ct = blk % p.ctiles;
+  const int bh = blk / p.ctiles, b = bh / p.H, h = bh - b * p.H;
+  const int c = 64 * ct + 16 * wave + (lane & 15);  // this lane's column
+  const bool inside = c < p.P;
+  const int grp = h / (p.H / p.G);
+  const int64_t vstride = (int64_t)p.H * p.P;
+  const int64_t vfirst = (int64_t)b * p.L * vstride + (int64_t)h * p.P + (inside ? c : 0);
+  const int64_t state = (int64_t)bh * p.N * p.P;
+
+  f4x st[HT];
+#pragma unroll
+  for (int i = 0; i < HT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int n = 16 * i + 4 * g + r;
+      st[i][r] = p.s0 != nullptr && inside && n < p.N ? p.s0[state + (int64_t)n * p.P + c] : 0.f;
+    }
+
+  constexpr bool kAhead = Rows::Stage::kRounds == 1;
+  typename Rows::Stage rk, rq;
+  u4x tri[kTriLoads], score[kScoreLoads + 1];
+  float gate = 0.f;
+  int next_bad = kChunk;
+  TI val[16];
+  auto chunk_of = [&](int j) { return BACK ? p.nc - 1 - j : j; };
+  auto fetch = [&](int j) {
+    const int cc = chunk_of(j), t0 = cc * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
+    const int64_t unit = (int64_t)bh * p.nc + cc;
+    Rows::place(rk, p.k, p, b, grp, t0, len, tid);
+    rk.load(0);
+    if (QUERY) {
+      Rows::place(rq, p.q, p, b, grp, t0, len, tid);
+      if (kAhead) rq.load(0);
+    }
+    const u4x* ts = reinterpret_cast<const u4x*>((BACK ? p.tri_t : p.tri) + unit * S * kDeltaTri);
+    const u4x* ps = reinterpret_cast<const u4x*>(p.score + unit * S * kDeltaTri);
+#pragma unroll
+    for (int i = 0; i < kTriLoads; ++i) {
+      const int e = i * kDeltaThreads + tid;
+      tri[i] = ts[e < kTriPacks ? e : tid];
+    }
+#pragma unroll
+    for (int i = 0; i < kScoreLoads; ++i) {
+      const int e = i * kDeltaThreads + tid;
+      score[i] = ps[e < kScorePacks ? e : tid];
+    }
+    gate = p.gates[unit * kDeltaGates + tid];
+    next_bad = __float_as_int(p.gates[unit * kDeltaGates + 3 * kChunk + 1]);
+    const TI* v = static_cast<const TI*>(BACK ? p.dy : p.v) + vfirst + t0 * vstride;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int t = 16 * (i >> 2) + 4 * g + (i & 3);
+      val[i] = v[(t < len ? t : 0) * vstride];
+    }
+  };
+  fetch(0);
+
+  for (int j = 0; j < p.nc; ++j) {
+    const int cc = chunk_of(j), t0 = cc * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
+    const int64_t unit = (int64_t)bh * p.nc + cc;
+    if (j > 0 && !kAhead) fetch(j);
+    __syncthreads();  // everyone is done with the last chunk
+    // tokens from the first bad one on leave the products
+    const int bad = next_bad;
+    const int used = bad < len ? bad : len;
+    rk.len = used;
+    Rows::all(rk, sK);
+    if (QUERY) {
+      if (!kAhead) rq.load(0);
+      Rows::all(rq, sQ);
+    }
+#pragma unroll
+    for (int i = 0; i < kTriLoads; ++i) {
+      const int e = i * kDeltaThreads + tid;
+      if (e < kTriPacks) reinterpret_cast<u4x*>(sT)[e] = tri[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kScoreLoads; ++i) {
+      const int e = i * kDeltaThreads + tid;
+      if (e < kScorePacks) reinterpret_cast<u4x*>(sP)[e] = score[i];
+    }
+    sG[tid] = gate;
+    f4x vv[4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int t = 16 * (i >> 2) + 4 * g + (i & 3);
+      vv[i >> 2][i & 3] = inside && t < used ? to_f32(val[i]) : 0.f;
+    }
+    // an infinity or a NaN of v reaches its own column from its token on
+    int limit = bad;
+    if constexpr (!BACK) {
+      bool wild = false;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) wild |= not_finite(vv[i >> 2][i & 3]);
+      if (__ballot(wild)) {
+        __builtin_amdgcn_sched_barrier(0);
+        int first = kChunk;
+#pragma unroll
+        for (int i = 15; i >= 0; --i)
+          if (not_finite(vv[i >> 2][i & 3])) first = 16 * (i >> 2) + 4 * g + (i & 3);
+        int o = __shfl_xor(first, 16);
+        first = o < first ? o : first;
+        o = __shfl_xor(first, 32);
+        first = o < first ? o : first;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (16 * (i >> 2) + 4 * g + (i & 3) >= first) vv[i >> 2][i & 3] = 0.f;
+        limit = first < limit ? first : limit;
+      }
+    }
+    __syncthreads();
+    if (kAhead && j + 1 < p.nc) fetch(j + 1);
+
+    if (!OUT) {
+      float* to = p.states + unit * (32 * KT) * p.Pp + c;
+#pragma unroll
+      for (int i = 0; i < HT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[(int64_t)(16 * i + 4 * g + r) * p.Pp] = st[i][r];
+    }
+
+    // K h, and Q h
+    f4x z[4], y[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      z[t] = f4x{0.f, 0.f, 0.f, 0.f};
+      y[t] = f4x{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int n = 0; n < KT; ++n) {
+      bf8x hb[S];
+      split_tiles<S>(st[2 * n], st[2 * n + 1], hb);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        bf8x a[NT];
+        row_operand<Sh>(sK, 16 * t, n, lane, a);
+        z[t] = mma_terms<NT, S>(a, hb, z[t]);
+        if (OUT) {
+          row_operand<Sh>(sQ, 16 * t, n, lane, a);
+          y[t] = mma_terms<QT, YT>(a, hb, y[t]);
+        }
+      }
+    }
+    auto gates = [&](int which, int t) {
+      return *reinterpret_cast<const f4x*>(sG + which * kChunk + 16 * t + 4 * g);
+    };
+    auto triangle = [&](const bf16_t* m, int blk2, int terms, bf8x* out) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s < terms)
+          out[s] = *reinterpret_cast<const bf8x*>(m + s * kDeltaTri + blk2 * 512 + lane * 8);
+    };
+    const float carry = sG[3 * kChunk];
+    f4x o[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) o[t] = f4x{0.f, 0.f, 0.f, 0.f};
+    if constexpr (!BACK) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) vv[t] -= gates(0, t) * z[t];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        bf8x rb[S];
+        split_tiles<S>(vv[2 * m], vv[2 * m + 1], rb);
+#pragma unroll
+        for (int t = 2 * m; t < 4; ++t) {
+          bf8x a[S];
+          triangle(sT, tri_block(t, m), S, a);
+          o[t] = mma_terms<S, S>(a, rb, o[t]);
+        }
+      }
+      f4x u[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = gates(2, t) * o[t];
+      if (OUT) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) y[t] *= gates(0, t);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          bf8x ub[YT];
+          split_tiles<YT>(u[2 * m], u[2 * m + 1], ub);
+#pragma unroll
+          for (int t = 2 * m; t < 4; ++t) {
+            bf8x a[S];
+            triangle(sP, tri_block(t, m), YT, a);
+            y[t] = mma_terms<YT, YT>(a, ub, y[t]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < HT; ++i) st[i] *= carry;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        bf8x ub[S];
+        split_tiles<S>(u[2 * m] * gates(1, 2 * m), u[2 * m + 1] * gates(1, 2 * m + 1), ub);
+#pragma unroll
+        for (int i = 0; i < HT; ++i) {
+          bf8x a[NT];
+          column_operand<Sh>(sK, i, m, lane, a);
+          st[i] = mma_terms<NT, S>(a, ub, st[i]);
+        }
+      }
+      if (limit < len) {
+#pragma unroll
+        for (int i = 0; i < HT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) st[i][r] = __builtin_nanf("");
+      }
+      if (OUT) {
+        const int64_t to = vfirst + t0 * vstride;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int t = 16 * (i >> 2) + 4 * g + (i & 3);
+          const float v = t < limit ? y[i >> 2][i & 3] : __builtin_nanf("");
+          if (inside && t < len) {
+            if (p.out_bf16) static_cast<bf16_t*>(p.out)[to + t * vstride] = from_f32<bf16_t>(v);
+            else static_cast<float*>(p.out)[to + t * vstride] = v;
+          }
+        }
+      } else {
+        float* to = p.rows + unit * kChunk * p.Pp + c;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          to[(16 * (i >> 2) + 4 * g + (i & 3)) * p.Pp] = o[i >> 2][i & 3];
+      }
+    } else {
+      // dU = w K a + S^T dY, dV = T^T (beta dU)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) z[t] *= gates(1, t);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        bf8x db[NT];
+        split_tiles<NT>(vv[2 * m], vv[2 * m + 1], db);
+#pragma unroll
+        for (int t = 0; t < 2 * m + 2; ++t) {
+          bf8x a[S];
+          triangle(sP, tri_block_t(t, m), S, a);
+          z[t] = mma_terms<S, NT>(a, db, z[t]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) z[t] *= gates(2, t);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        bf8x ub[S];
+        split_tiles<S>(z[2 * m], z[2 * m + 1], ub);
+#pragma unroll
+        for (int t = 0; t < 2 * m + 2; ++t) {
+          bf8x a[S];
+          triangle(sT, tri_block_t(t, m), S, a);
+          o[t] = mma_terms<S, S>(a, ub, o[t]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < HT; ++i) st[i] *= carry;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        bf8x yb[S], vb[S];
+        split_tiles<S>(vv[2 * m] * gates(0, 2 * m), vv[2 * m + 1] * gates(0, 2 * m + 1), yb);
+        split_tiles<S>(o[2 * m] * -gates(0, 2 * m), o[2 * m + 1] * -gates(0, 2 * m + 1), vb);
+#pragma unroll
+        for (int i = 0; i < HT; ++i) {
+          bf8x a[NT];
+          column_operand<Sh>(sQ, i, m, lane, a);
+          st[i] = mma_terms<NT, S>(a, yb, st[i]);
+          column_operand<Sh>(sK, i, m, lane, a);
+          st[i] = mma_terms<NT, S>(a, vb, st[i]);
+        }
+      }
+      const int64_t to = vfirst + t0 * vstride;
+      float* keep = p.rows + unit * kChunk * p.Pp + c;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int t = 16 * (i >> 2) + 4 * g + (i & 3);
+        const float v = o[i >> 2][i & 3];
+        keep[t * p.Pp] = v;
+        if (inside && t < len) {
+          if (p.out_bf16) static_cast<bf16_t*>(p.out)[to + t * vstride] = from_f32<bf16_t>(v);
+          else static_cast<float*>(p.out)[to + t * vstride] = v;
+        }
+      }
+    }
+  }
+  if (p.s_final != nullptr) {
+#pragma unroll
+    for (int i = 0; i < HT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = 16 * i + 4 * g + r;
+        if (inside && n < p.N) p.s_final[state + (int64_t)n * p.P + c] = st[i][r];
+      }
+  }
+}
+
+// ---- the other gradients, every chunk for itself --------------------------------
+
+struct DeltaGradParams {
+  const void *q, *k, *dy;
+  const float *g, *beta;
+  int B, L, H, G, N, P, Pp;
+  int token_decay, nc;
+  const float *states, *adjoints;  // [32 KT, P'] before and behind each chunk
+  const float *o, *dv;             // [64, P']
+  void *dq, *dk;                   // [B, L, H, N] rows per head
+  int grad_bf16;
+  float* dg;                       // [B, L, H], or null
+  double* part;                    // sums of dg per chunk (a decay per head), or null
+  float* dbeta;                    // [B, L, H]
+};
+
+constexpr int kDeltaGradVectors = 16;  // of 64 floats
+
+template <typename TI, int KT>
+constexpr size_t delta_grad_lds() {
+  using Sh = DeltaShape<TI, KT>;
+  return 2 * (size_t)Sh::kTerms * Sh::kTile * sizeof(bf16_t) +
+         ((size_t)kChunk * kTriStride + kDeltaGradVectors * kChunk) * sizeof(float);
+}
+
+// Sum over the 16 lanes of a row, on each of them.
+__device__ __forceinline__ float row_sum(float v) {
+  v += xor_lane<1>(v, 0);
+  v += xor_lane<2>(v, 0);
+  v += xor_lane<4>(v, 0);
+  return v + xor_lane<8>(v, 0);
+}
+// Sum over the four lanes of a column.
+__device__ __forceinline__ float column_sum(float v) {
+  v = xchg_add<32>(v, v);
+  return xchg_add<16>(v, v);
+}
+
+// With F = dY O^T and E = dV O^T (pairs s <= t and s < t):
+//   dQ = e^G dY h^T + (F D beta) K
+//   dK = beta w O a^T - e^G dV h^T + (F D beta)^T Q - (E D beta) K - (E D beta)^T K
+//   dbeta_s = sum_t (q_t . k_s) D F - (k_t . k_s) D E + w_s k_s . (O a^T)_s
+// and dg_t is the sum of everything that spans t: the pairs s < t <= r of
+// beta_s D (q_r . k_s F - k_r . k_s E), what tokens r >= t read of h, what later
+// chunks read of tokens s < t, and e^{G_end} <h, a>.  The pairs' sum is taken up from its
+// differences between neighbours (column sum less row sum) from the chunk's start or the
+// last cleared state, in 64 bits.
+// One workgroup per chunk and head; wave w takes the 16 tokens of tile w.
+template <typename TI, int KT, bool LOOSE>
+__global__ __launch_bounds__(kDeltaThreads, 1) void delta_grad_kernel(DeltaGradParams p) {
+  using Sh = DeltaShape<TI, KT>;
+  using Rows = DeltaRows<TI, KT, LOOSE>;
+  constexpr int NT = Sh::kTerms, HT = 2 * KT, S = kDeltaTerms;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
+  bf16_t* sK = reinterpret_cast<bf16_t*>(smem_raw);
+  bf16_t* sQ = sK + NT * Sh::kTile;
+  // F D beta on and below the diagonal, (E D beta)^T above it
+  float* sM = reinterpret_cast<float*>(sQ + NT * Sh::kTile);
+  float* vec = sM + kChunk * kTriStride;
+  float *gHi = vec, *gLo = vec + 64, *gRead = vec + 128, *gWrite = vec + 192, *gBeta = vec + 256;
+  float *rowF = vec + 320, *rowE = vec + 384, *diag = vec + 448;
+  float *seen = vec + 512, *wrote = vec + 576, *thru = vec + 640;  // thru: 4 per wave
+  float* cols = vec + 704;  // [4 tiles][64]
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int g = lane >> 4, col = lane & 15;
+  const int64_t unit = blockIdx.x;
+  const int c = (int)(unit % p.nc);
+  const int64_t bh = unit / p.nc;
+  const int b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
+  const int t0 = c * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
+
+  DeltaParams rp = {};
+  rp.G = p.G;
+  rp.N = p.N;
+  rp.B = p.B;
+  rp.L = p.L;
+  typename Rows::Stage rk, rq;
+  Rows::place(rk, p.k, rp, b, h / (p.H / p.G), t0, len, tid);
+  Rows::place(rq, p.q, rp, b, h / (p.H / p.G), t0, len, tid);
+  rk.load(0);
+  rq.load(0);
+  float gt = 0.f, bt = 0.f;
+  if (wave == 0) {
+    const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
+    if (lane < len) {
+      gt = p.token_decay ? p.g[at] : p.g[h];
+      bt = p.beta[at];
+    }
+    const double d = (double)gt * 1.4426950408889634;
+    const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
+    const double end = last_lane(sum);
+    const float hi = (float)sum;
+    gHi[lane] = hi;
+    gLo[lane] = (float)(sum - (double)hi);
+    gRead[lane] = exp2_sum(sum);
+    gWrite[lane] = exp2_sum(end - sum);
+    gBeta[lane] = bt;
+  }
+  Rows::all(rk, sK);
+  Rows::all(rq, sQ);
+  __syncthreads();
+
+  // This wave's rows along the values: slots 8 g.. of a block of 32, in their own order.
+  const int64_t vstride = (int64_t)p.H * p.P;
+  const TI* dy = static_cast<const TI*>(p.dy) + ((int64_t)b * p.L + t0) * vstride +
+                 (int64_t)h * p.P;
+  const float* o = p.o + unit * kChunk * p.Pp;
+  const float* dv = p.dv + unit * kChunk * p.Pp;
+  auto split_row = [&](const float* at, bf8x* out) {
+    float x[8];
+    *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(at);
+    *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(at + 4);
+    split_terms<S>(x, out);
+  };
+  auto dy_operand = [&](int rt, int m, bf8x* out) {
+    const int t = 16 * rt + col, cc = 32 * m + 8 * g, n = t < len ? p.P - cc : 0;
+    const Pack<TI> v = load_pack(dy + (n > 0 ? t * vstride + cc : 0), n);
+    if constexpr (Sh::kF32) split_terms<S>(v.v, out);
+    else out[0] = __builtin_bit_cast(bf8x, v);
+  };
+  const int blocks = (p.P + 31) / 32;
+
+  // F of tile w and E of tile 3 - w
+  const int tf = wave, te = 3 - wave;
+  f4x f[4], e[4];
+#pragma unroll
+  for (int ct = 0; ct < 4; ++ct) {
+    f[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+    e[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+  }
+  for (int m = 0; m < blocks; ++m) {
+    bf8x ay[NT], av[S];
+    dy_operand(tf, m, ay);
+    split_row(dv + (int64_t)(16 * te + col) * p.Pp + 32 * m + 8 * g, av);
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      if (ct > tf && ct > te) continue;
+      bf8x bo[S];
+      split_row(o + (int64_t)(16 * ct + col) * p.Pp + 32 * m + 8 * g, bo);
+      if (ct <= tf) f[ct] = mma_terms<NT, S>(ay, bo, f[ct]);
+      if (ct <= te) e[ct] = mma_terms<S, S>(av, bo, e[ct]);
+    }
+  }
+  // the scores that go with them
+  {
+    f4x qk[4], kk[4];
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      qk[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+      kk[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int n = 0; n < KT; ++n) {
+      bf8x ak[NT], aq[NT];
+      row_operand<Sh>(sK, 16 * te, n, lane, ak);
+      row_operand<Sh>(sQ, 16 * tf, n, lane, aq);
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) {
+        if (ct > tf && ct > te) continue;
+        bf8x bk[NT];
+        row_operand<Sh>(sK, 16 * ct, n, lane, bk);
+        if (ct <= tf) qk[ct] = mma_terms<NT, NT>(aq, bk, qk[ct]);
+        if (ct <= te) kk[ct] = mma_terms<NT, NT>(ak, bk, kk[ct]);
+      }
+    }
+    float rf[4] = {}, re[4] = {};
+    float cf[4], ce[4];
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      const int s = 16 * ct + col;
+      const float bs = gBeta[s];
+      cf[ct] = ce[ct] = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * tf + 4 * g + r, u = 16 * te + 4 * g + r;
+        const float d = hw_exp2((gHi[t] - gHi[s]) + (gLo[t] - gLo[s]));
+        const float fd = s <= t ? f[ct][r] * d : 0.f;
+        const float fq = fd * qk[ct][r];
+        if (s <= t) sM[t * kTriStride + s] = fd * bs;
+        if (s == t) diag[t] = fq;
+        else {
+          cf[ct] += fq;
+          rf[r] = fmaf(fq, bs, rf[r]);
+        }
+        const float ed =
+            s < u ? e[ct][r] * hw_exp2((gHi[u] - gHi[s]) + (gLo[u] - gLo[s])) : 0.f;
+        const float ek = ed * kk[ct][r];
+        if (s < u) sM[s * kTriStride + u] = ed * bs;
+        ce[ct] += ek;
+        re[r] = fmaf(ek, bs, re[r]);
+      }
+      cf[ct] = column_sum(cf[ct]);
+      ce[ct] = column_sum(ce[ct]);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      rf[r] = row_sum(rf[r]);
+      re[r] = row_sum(re[r]);
+      if (col == 0) {
+        rowF[16 * tf + 4 * g + r] = rf[r];
+        rowE[16 * te + 4 * g + r] = re[r];
+      }
+    }
+    if (g == 0) {
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) cols[tf * 64 + 16 * ct + col] = cf[ct];
+    }
+    __syncthreads();  // tiles tf and te are two waves' columns
+    if (g == 0) {
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) cols[te * 64 + 16 * ct + col] -= ce[ct];
+    }
+  }
+  __syncthreads();
+
+  // what this wave's tokens read of h, erase of it and write into a
+  f4x reads[HT], erased[HT], written[HT];
+#pragma unroll
+  for (int i = 0; i < HT; ++i) {
+    reads[i] = f4x{0.f, 0.f, 0.f, 0.f};
+    erased[i] = f4x{0.f, 0.f, 0.f, 0.f};
+    written[i] = f4x{0.f, 0.f, 0.f, 0.f};
+  }
+  const float* hs = p.states + unit * (32 * KT) * p.Pp;
+  const float* as = p.adjoints + unit * (32 * KT) * p.Pp;
+  float through = 0.f;
+  for (int m = 0; m < blocks; ++m) {
+    bf8x ay[NT], av[S], ao[S];
+    const int64_t at = (int64_t)(16 * wave + col) * p.Pp + 32 * m + 8 * g;
+    dy_operand(wave, m, ay);
+    split_row(dv + at, av);
+    split_row(o + at, ao);
+#pragma unroll
+    for (int i = 0; i < HT; ++i) {
+      const int64_t n = (int64_t)(16 * i + col) * p.Pp + 32 * m + 8 * g;
+      float x[8], y[8];
+      bf8x hb[S], ab[S];
+      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(hs + n);
+      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(hs + n + 4);
+      *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(as + n);
+      *reinterpret_cast<float4*>(y + 4) = *reinterpret_cast<const float4*>(as + n + 4);
+      if ((i & 3) == wave) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) through = fmaf(x[k], y[k], through);
+      }
+      split_terms<S>(x, hb);
+      split_terms<S>(y, ab);
+      reads[i] = mma_terms<NT, S>(ay, hb, reads[i]);
+      erased[i] = mma_terms<S, S>(av, hb, erased[i]);
+      written[i] = mma_terms<S, S>(ao, ab, written[i]);
+    }
+  }
+  through = wave_sum64(through);
+  if (lane == 0) thru[wave] = through;
+  auto element = [&](const bf16_t* tile, int t, int n) {
+    const bf16_t* at = tile + t * Sh::kStride + operand_place(n & ~3) + (n & 3);
+    float v = to_f32(at[0]);
+#pragma unroll
+    for (int s = 1; s < NT; ++s) v += to_f32(at[s * Sh::kTile]);
+    return v;
+  };
+  const f4x er = *reinterpret_cast<const f4x*>(gRead + 16 * wave + 4 * g);
+  const f4x ew = *reinterpret_cast<const f4x*>(gWrite + 16 * wave + 4 * g);
+  const f4x eb = *reinterpret_cast<const f4x*>(gBeta + 16 * wave + 4 * g);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int t = 16 * wave + 4 * g + r;
+    float s = 0.f, w = 0.f;
+#pragma unroll
+    for (int i = 0; i < HT; ++i) {
+      const float kn = element(sK, t, 16 * i + col), qn = element(sQ, t, 16 * i + col);
+      s += qn * reads[i][r] - kn * erased[i][r];
+      w = fmaf(kn, written[i][r], w);
+    }
+    s = row_sum(s) * er[r];
+    w = row_sum(w) * ew[r];
+    if (col == 0) {
+      seen[t] = s;
+      wrote[t] = w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < HT; ++i) {
+    reads[i] *= er;
+    written[i] = written[i] * (ew * eb) - erased[i] * er;
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const int t = 16 * wave + col;
+    float fd[8], both[8], ft[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = 32 * m + 16 * (i >> 2) + 4 * g + (i & 3);
+      const float row = sM[t * kTriStride + s], down = sM[s * kTriStride + t];
+      fd[i] = s <= t ? row : 0.f;
+      ft[i] = s >= t ? down : 0.f;
+      both[i] = s == t ? 0.f : s < t ? -down : -row;
+    }
+    bf8x af[S], ae[S], at[S];
+    split_terms<S>(fd, af);
+    split_terms<S>(both, ae);
+    split_terms<S>(ft, at);
+#pragma unroll
+    for (int i = 0; i < HT; ++i) {
+      bf8x bk[NT], bq[NT];
+      column_operand<Sh>(sK, i, m, lane, bk);
+      column_operand<Sh>(sQ, i, m, lane, bq);
+      reads[i] = mma_terms<S, NT>(af, bk, reads[i]);
+      written[i] = mma_terms<S, NT>(ae, bk, written[i]);
+      written[i] = mma_terms<S, NT>(at, bq, written[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < HT; ++i) {
+    const int n = 16 * i + col;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * wave + 4 * g + r;
+      if (t < len && n < p.N) {
+        const int64_t to = (((int64_t)b * p.L + t0 + t) * p.H + h) * p.N + n;
+        if (p.grad_bf16) {
+          static_cast<bf16_t*>(p.dq)[to] = from_f32<bf16_t>(reads[i][r]);
+          static_cast<bf16_t*>(p.dk)[to] = from_f32<bf16_t>(written[i][r]);
+        } else {
+          static_cast<float*>(p.dq)[to] = reads[i][r];
+          static_cast<float*>(p.dk)[to] = written[i][r];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  const float down = cols[lane] + cols[64 + lane] + cols[128 + lane] + cols[192 + lane];
+  const float wr = wrote[lane];
+  if (lane < len) p.dbeta[((int64_t)b * p.L + t0 + lane) * p.H + h] = down + diag[lane] + wr;
+  const bool clear = lane < len && hw_exp2(gt * kLog2e) == 0.f;
+  const double slope = (double)bt * down - ((double)rowF[lane] - (double)rowE[lane]);
+  const double upto = wave_prefix(slope) - slope;  // of the tokens before
+  const uint64_t mask = __ballot(clear) & (~0ull >> (63 - lane));
+  const int from = mask != 0 ? 63 - __clzll((long long)mask) : 0;
+  const double base = __shfl(upto, from);
+  const double sn = seen[lane], wb = (double)bt * wr;
+  const double all_seen = wave_prefix(sn), all_wrote = wave_prefix(wb);
+  double dg = (upto - base) + (last_lane(all_seen) - all_seen + sn) + (all_wrote - wb) +
+              (double)exp2_sum((double)gHi[63] + (double)gLo[63]) *
+                  ((double)thru[0] + thru[1] + thru[2] + thru[3]);
+  if (clear || lane >= len) dg = 0.0;
+  if (p.dg != nullptr && lane < len) p.dg[((int64_t)b * p.L + t0 + lane) * p.H + h] = (float)dg;
+  if (p.part != nullptr) {
+    dg = wave_prefix(dg);
+    if (lane == 63) p.part[unit] = dg;
+  }
+}
+
+// ---- launches -------------------------------------------------------------------
+
+template <typename TI, int KT, bool LOOSE, bool BACK>
+int delta_prep(const DeltaParams& p, hipStream_t s) {
+  constexpr size_t lds = delta_prep_lds<TI, KT>();
+  static_assert(lds <= 160 * 1024, "a CU's LDS");
+  allow_dynamic_lds(delta_prep_kernel<TI, KT, LOOSE, BACK>, lds);
+  hipLaunchKernelGGL((delta_prep_kernel<TI, KT, LOOSE, BACK>),
+                     dim3((unsigned)((int64_t)p.B * p.H * p.nc)), dim3(kDeltaThreads), lds, s, p);
+  return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
+}
+
+template <typename TI, int KT, bool LOOSE, int MODE>
+int delta_walk(const DeltaParams& p, hipStream_t s) {
+  constexpr size_t lds = DeltaLds<TI, KT, MODE>::kBytes;
+  static_assert(lds <= 160 * 1024, "a CU's LDS");
+  allow_dynamic_lds(delta_walk_kernel<TI, KT, LOOSE, MODE>, lds);
+  hipLaunchKernelGGL((delta_walk_kernel<TI, KT, LOOSE, MODE>),
+                     dim3((unsigned)((int64_t)p.B * p.H * p.ctiles)), dim3(kDeltaThreads), lds, s,
+                     p);
+  return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
+}
+
+template <typename TI, int KT, bool LOOSE>
+int delta_grad(const DeltaGradParams& p, hipStream_t s) {
+  constexpr size_t lds = delta_grad_lds<TI, KT>();
+  static_assert(lds <= 160 * 1024, "a CU's LDS");
+  allow_dynamic_lds(delta_grad_kernel<TI, KT, LOOSE>, lds);
+  hipLaunchKernelGGL((delta_grad_kernel<TI, KT, LOOSE>),
+                     dim3((unsigned)((int64_t)p.B * p.H * p.nc)), dim3(kDeltaThreads), lds, s, p);
+  return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
+}
+
+enum DeltaPhase { kPhasePrep, kPhasePrepBack, kPhaseOut, kPhaseKeep, kPhaseBack };
+
+template <typename TI, int KT, bool LOOSE>
+int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
+  switch (phase) {
+    case kPhasePrep: return delta_prep<TI, KT, LOOSE, false>(p, s);
+    case kPhasePrepBack: return delta_prep<TI, KT, LOOSE, true>(p, s);
+    case kPhaseOut:
+      return p.out_bf16 ? delta_walk<TI, KT, LOOSE, kDeltaOut>(p, s)
+                        : delta_walk<TI, KT, LOOSE, kDeltaOutF32>(p, s);
+    case kPhaseKeep: return delta_walk<TI, KT, LOOSE, kDeltaKeep>(p, s);
+    default: return delta_walk<TI, KT, LOOSE, kDeltaBack>(p, s);
+  }
+}
+
+// One pair per dtype and padded row size.
+#define SWIMBA_DELTA_DECL(name)                                       \
+  int name(const DeltaParams& p, int phase, hipStream_t s);           \
+  int name##_grad(const DeltaGradParams& p, hipStream_t s);
+SWIMBA_DELTA_DECL(delta_bf16_32)
+SWIMBA_DELTA_DECL(delta_bf16_64)
+SWIMBA_DELTA_DECL(delta_bf16_128)
+SWIMBA_DELTA_DECL(delta_bf16_256)
+SWIMBA_DELTA_DECL(delta_f32_32)
+SWIMBA_DELTA_DECL(delta_f32_64)
+SWIMBA_DELTA_DECL(delta_f32_128)
+#undef SWIMBA_DELTA_DECL
+
+#define SWIMBA_DELTA_DEFINE(name, TI, KT)                                           \
+  int name(const DeltaParams& p, int phase, hipStream_t s) {                        \
+    return p.N % kPack != 0 ? delta_phase<TI, KT, true>(p, phase, s)                \
+                            : delta_phase<TI, KT, false>(p, phase, s);              \
+  }                                                                                 \
+  int name##_grad(const DeltaGradParams& p, hipStream_t s) {                        \
+    return p.N % kPack != 0 ? delta_grad<TI, KT, true>(p, s)                        \
+                            : delta_grad<TI, KT, false>(p, s);                      \
+  }
+
+}  // namespace swimba

@@ -485,6 +485,71 @@ int validate_attention_grad(const swimba_linear_attention_grad_args* g) {
   return SWIMBA_OK;
 }
 
+int validate_delta(int B, int L, int H, int G, int N, int P, swimba_dtype in, swimba_dtype out,
+                   swimba_decay_form form) {
+  const int rc = validate_attention(B, L, H, G, N, P, in, out, form);
+  if (rc != SWIMBA_OK) return rc;
+  if (in == SWIMBA_F32 && L > 1 && N > 128) return SWIMBA_EUNSUPPORTED;  // a CU's LDS
+  // a launch of 256 threads per chunk and head
+  if ((int64_t)B * H * ((L + 63LL) / 64) >= (1 << 24)) return SWIMBA_EUNSUPPORTED;
+  return SWIMBA_OK;
+}
+
+int validate_delta(const swimba_delta_rule_args* a) {
+  if (a == nullptr) return SWIMBA_EINVAL;
+  return validate_delta(a->B, a->L, a->H, a->G, a->N, a->P, a->in_dtype, a->y_dtype,
+                        a->decay_form);
+}
+
+int validate_delta_inputs(const swimba_delta_rule_args* a) {
+  if (a->B == 0 || a->L == 0) return SWIMBA_OK;
+  if (a->q == nullptr || a->k == nullptr || a->v == nullptr || a->log_decay == nullptr ||
+      a->beta == nullptr)
+    return SWIMBA_EINVAL;
+  if (!aligned_as(a->q, a->in_dtype) || !aligned_as(a->k, a->in_dtype) ||
+      !aligned_as(a->v, a->in_dtype))
+    return SWIMBA_EINVAL;
+  return SWIMBA_OK;
+}
+
+int validate_delta_grad(const swimba_delta_rule_grad_args* g) {
+  if (g == nullptr) return SWIMBA_EINVAL;
+  const int rc = validate_delta(&g->fwd);
+  if (rc != SWIMBA_OK) return rc;
+  if (!dtype_ok(g->grad_dtype)) return SWIMBA_EINVAL;
+  const swimba_delta_rule_args& a = g->fwd;
+  // threads of the launch that sums up the heads' rows
+  if ((int64_t)a.B * a.L * a.G * ((a.N + 7) / 8) >= (int64_t(1) << 32) - 256)
+    return SWIMBA_EUNSUPPORTED;
+  return SWIMBA_OK;
+}
+
+int validate_norm(const swimba_norm_rotate_args* a) {
+  if (a == nullptr) return SWIMBA_EINVAL;
+  if (a->T < 0 || a->Hq < 1 || a->Hk < 1 || a->N < 1 || a->R < 0 || a->R > a->N || a->R % 2 != 0)
+    return SWIMBA_EINVAL;
+  if (!dtype_ok(a->in_dtype) || !dtype_ok(a->out_dtype)) return SWIMBA_EINVAL;
+  if (a->norm != SWIMBA_NORM_RMS && a->norm != SWIMBA_NORM_L2) return SWIMBA_EINVAL;
+  if (a->pairs != SWIMBA_PAIRS_HALVES && a->pairs != SWIMBA_PAIRS_NEIGHBOURS) return SWIMBA_EINVAL;
+  if (!(a->eps >= 1.17549435e-38f && a->eps <= 3.4e38f)) return SWIMBA_EINVAL;
+  if ((a->q_stride != 0 && a->q_stride < (int64_t)a->Hq * a->N) ||
+      (a->k_stride != 0 && a->k_stride < (int64_t)a->Hk * a->N))
+    return SWIMBA_EINVAL;
+  if (a->N > 512 || (int64_t)a->Hq + a->Hk > (1 << 16) || a->T > (int64_t(1) << 31))
+    return SWIMBA_EUNSUPPORTED;
+  if (a->T * ((int64_t)a->Hq + a->Hk) > (int64_t(1) << 40)) return SWIMBA_EUNSUPPORTED;
+  return SWIMBA_OK;
+}
+
+int validate_norm_inputs(const swimba_norm_rotate_args* a) {
+  if (a->T == 0) return SWIMBA_OK;
+  if (a->q == nullptr || a->k == nullptr || !aligned_as(a->q, a->in_dtype) ||
+      !aligned_as(a->k, a->in_dtype))
+    return SWIMBA_EINVAL;
+  if (a->R > 0 && (a->positions == nullptr || a->rates == nullptr)) return SWIMBA_EINVAL;
+  return SWIMBA_OK;
+}
+
 }  // namespace
 }  // namespace swimba
 
@@ -726,6 +791,95 @@ int swimba_linear_attention_step(const swimba_linear_attention_step_args* a, hip
       !aligned_as(a->y, a->y_dtype))
     return SWIMBA_EINVAL;
   return launch_attention_step(a, stream_device(stream), stream);
+}
+
+size_t swimba_delta_rule_workspace_size(const swimba_delta_rule_args* a) {
+  return validate_delta(a) == SWIMBA_OK ? delta_rule_bytes(a) : 0;
+}
+
+int swimba_delta_rule(const swimba_delta_rule_args* a, void* ws, size_t ws_bytes,
+                      hipStream_t stream) {
+  int rc = validate_delta(a);
+  if (rc != SWIMBA_OK) return rc;
+  rc = validate_delta_inputs(a);
+  if (rc != SWIMBA_OK) return rc;
+  if (a->B > 0 && a->L > 0 && (a->y == nullptr || !aligned_as(a->y, a->y_dtype)))
+    return SWIMBA_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, delta_rule_bytes(a))) return SWIMBA_EWORKSPACE;
+  return launch_delta_rule(a, ws, stream);
+}
+
+size_t swimba_delta_rule_backward_workspace_size(const swimba_delta_rule_grad_args* g) {
+  return validate_delta_grad(g) == SWIMBA_OK ? delta_rule_backward_bytes(g) : 0;
+}
+
+int swimba_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, size_t ws_bytes,
+                               hipStream_t stream) {
+  int rc = validate_delta_grad(g);
+  if (rc != SWIMBA_OK) return rc;
+  rc = validate_delta_inputs(&g->fwd);
+  if (rc != SWIMBA_OK) return rc;
+  const bool any = g->fwd.B > 0 && g->fwd.L > 0;
+  // without tokens a gradient per token has no elements
+  if (g->dlog_decay == nullptr && (g->fwd.decay_form == SWIMBA_DECAY_HEAD || any))
+    return SWIMBA_EINVAL;
+  if (any && (g->dy == nullptr || g->dq == nullptr || g->dk == nullptr || g->dv == nullptr ||
+              g->dbeta == nullptr || !aligned_as(g->dy, g->fwd.in_dtype) ||
+              !aligned_as(g->dq, g->grad_dtype) || !aligned_as(g->dk, g->grad_dtype) ||
+              !aligned_as(g->dv, g->grad_dtype)))
+    return SWIMBA_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, delta_rule_backward_bytes(g))) return SWIMBA_EWORKSPACE;
+  return launch_delta_rule_backward(g, ws, stream);
+}
+
+int swimba_delta_rule_step(const swimba_delta_rule_step_args* a, hipStream_t stream) {
+  if (a == nullptr) return SWIMBA_EINVAL;
+  const int rc = validate_delta(a->B, 1, a->H, a->G, a->N, a->P, a->in_dtype, a->y_dtype,
+                                a->decay_form);
+  if (rc != SWIMBA_OK) return rc;
+  // a workgroup of 256 threads for 16 columns at least
+  if ((int64_t)a->B * a->H * ((a->P + 15LL) / 16) >= (1 << 24)) return SWIMBA_EUNSUPPORTED;
+  if (a->B == 0) return SWIMBA_OK;
+  if (a->q == nullptr || a->k == nullptr || a->v == nullptr || a->log_decay == nullptr ||
+      a->beta == nullptr || a->state == nullptr || a->y == nullptr ||
+      !aligned_as(a->q, a->in_dtype) || !aligned_as(a->k, a->in_dtype) ||
+      !aligned_as(a->v, a->in_dtype) || !aligned_as(a->y, a->y_dtype))
+    return SWIMBA_EINVAL;
+  return launch_delta_rule_step(a, stream_device(stream), stream);
+}
+
+int swimba_norm_rotate(const swimba_norm_rotate_args* a, hipStream_t stream) {
+  int rc = validate_norm(a);
+  if (rc != SWIMBA_OK) return rc;
+  rc = validate_norm_inputs(a);
+  if (rc != SWIMBA_OK) return rc;
+  if (a->T > 0 && (a->q_out == nullptr || a->k_out == nullptr ||
+                   !aligned_as(a->q_out, a->out_dtype) || !aligned_as(a->k_out, a->out_dtype)))
+    return SWIMBA_EINVAL;
+  return launch_norm_rotate(a, stream_device(stream), stream);
+}
+
+size_t swimba_norm_rotate_backward_workspace_size(const swimba_norm_rotate_grad_args* g) {
+  if (g == nullptr || validate_norm(&g->fwd) != SWIMBA_OK) return 0;
+  return norm_rotate_backward_bytes(g, -1);
+}
+
+int swimba_norm_rotate_backward(const swimba_norm_rotate_grad_args* g, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+  if (g == nullptr) return SWIMBA_EINVAL;
+  int rc = validate_norm(&g->fwd);
+  if (rc != SWIMBA_OK) return rc;
+  if (!dtype_ok(g->grad_dtype)) return SWIMBA_EINVAL;
+  rc = validate_norm_inputs(&g->fwd);
+  if (rc != SWIMBA_OK) return rc;
+  if (g->fwd.T > 0 &&
+      (g->dq_out == nullptr || g->dk_out == nullptr || g->dq == nullptr || g->dk == nullptr ||
+       !aligned_as(g->dq_out, g->fwd.in_dtype) || !aligned_as(g->dk_out, g->fwd.in_dtype) ||
+       !aligned_as(g->dq, g->grad_dtype) || !aligned_as(g->dk, g->grad_dtype)))
+    return SWIMBA_EINVAL;
+  const int dev = stream_device(stream);
+  if (!workspace_ok(ws, ws_bytes, norm_rotate_backward_bytes(g, dev))) return SWIMBA_EWORKSPACE;
+  return launch_norm_rotate_backward(g, ws, dev, stream);
 }
 
 const char* swimba_status_string(int status) {

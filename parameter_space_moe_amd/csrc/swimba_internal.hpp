@@ -102,6 +102,27 @@ size_t attention_backward_bytes(const swimba_linear_attention_grad_args* g, int 
 int launch_attention_backward(const swimba_linear_attention_grad_args* g, void* ws, int dev,
                               hipStream_t s);
 int launch_attention_step(const swimba_linear_attention_step_args* a, int dev, hipStream_t s);
+// Pieces of it that the delta rule shares.  out = in (null: zeros); the rows to read
+// where loads take whole packs of eight: `rows` itself, or, of a tensor of fewer
+// elements, its copy at `slot`; out[t, g, :] = the sum over the `share` heads of group
+// g of in; dg[h] = the sum of part [B, H, nc].
+constexpr size_t kTinySlot = 256;
+int copy_or_zero(const float* in, float* out, int64_t n, hipStream_t s);
+const void* whole_packs(const void* rows, int64_t n, bool f32, unsigned char* slot, hipStream_t s,
+                        int* rc);
+int sum_shared_heads(const float* rows, void* out, swimba_dtype d, int64_t n, int share, int N,
+                     hipStream_t s);
+int sum_decay_parts(const double* part, float* dg, int B, int H, int nc, hipStream_t s);
+// Delta rule (delta.hip) and norms of queries and keys (norm_rotate.hip).
+size_t delta_rule_bytes(const swimba_delta_rule_args* a);
+int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, hipStream_t s);
+size_t delta_rule_backward_bytes(const swimba_delta_rule_grad_args* g);
+int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, hipStream_t s);
+int launch_delta_rule_step(const swimba_delta_rule_step_args* a, int dev, hipStream_t s);
+int launch_norm_rotate(const swimba_norm_rotate_args* a, int dev, hipStream_t s);
+size_t norm_rotate_backward_bytes(const swimba_norm_rotate_grad_args* g, int dev);
+int launch_norm_rotate_backward(const swimba_norm_rotate_grad_args* g, void* ws, int dev,
+                                hipStream_t s);
 // Pass 2 of the chunked scans: carried-in state per chunk (rows = 16, or 16 per
 // trajectory: E * 16 per expert, k * 16 per routing slot, with E passed as the
 // trajectory count).

@@ -81,6 +81,40 @@ class LinearAttentionStepArgs(ctypes.Structure):
                 ("state_out", _vp), ("y", _vp)]
 
 
+class DeltaRuleArgs(ctypes.Structure):
+    _fields_ = [("B", _ci), ("L", _ci), ("H", _ci), ("G", _ci), ("N", _ci), ("P", _ci),
+                ("in_dtype", _ci), ("y_dtype", _ci), ("decay_form", _ci),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("log_decay", _vp), ("beta", _vp),
+                ("h0", _vp), ("y", _vp), ("h_final", _vp)]
+
+
+class DeltaRuleGradArgs(ctypes.Structure):
+    _fields_ = [("fwd", DeltaRuleArgs), ("dy", _vp), ("dh_final", _vp), ("grad_dtype", _ci),
+                ("dq", _vp), ("dk", _vp), ("dv", _vp), ("dlog_decay", _vp), ("dbeta", _vp),
+                ("dh0", _vp)]
+
+
+class DeltaRuleStepArgs(ctypes.Structure):
+    _fields_ = [("B", _ci), ("H", _ci), ("G", _ci), ("N", _ci), ("P", _ci),
+                ("in_dtype", _ci), ("y_dtype", _ci), ("decay_form", _ci),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("log_decay", _vp), ("beta", _vp),
+                ("state", _vp), ("state_out", _vp), ("y", _vp)]
+
+
+class NormRotateArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("Hq", _ci), ("Hk", _ci), ("N", _ci), ("R", _ci),
+                ("in_dtype", _ci), ("out_dtype", _ci), ("norm", _ci), ("pairs", _ci),
+                ("eps", ctypes.c_float), ("q_scale", ctypes.c_float),
+                ("q", _vp), ("k", _vp), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("wq", _vp), ("wk", _vp), ("positions", _vp),
+                ("rates", _vp), ("q_out", _vp), ("k_out", _vp)]
+
+
+class NormRotateGradArgs(ctypes.Structure):
+    _fields_ = [("fwd", NormRotateArgs), ("dq_out", _vp), ("dk_out", _vp), ("grad_dtype", _ci),
+                ("dq", _vp), ("dk", _vp), ("dwq", _vp), ("dwk", _vp)]
+
+
 class SwimbaError(RuntimeError):
     def __init__(self, fn, status):
         super().__init__("%s failed: %s (%d)" % (fn, status_string(status), status))
@@ -144,16 +178,25 @@ def load(path: str | None = None):
                                           _ci, _vp, _vp, _sz, _vp]
     lib.swimba_route_backward.restype = _ci
     for fn, args in ((lib.swimba_linear_attention, LinearAttentionArgs),
-                     (lib.swimba_linear_attention_backward, LinearAttentionGradArgs)):
+                     (lib.swimba_linear_attention_backward, LinearAttentionGradArgs),
+                     (lib.swimba_delta_rule, DeltaRuleArgs),
+                     (lib.swimba_delta_rule_backward, DeltaRuleGradArgs),
+                     (lib.swimba_norm_rotate_backward, NormRotateGradArgs)):
         fn.argtypes = [ctypes.POINTER(args), _vp, _sz, _vp]
         fn.restype = _ci
     for fn, args in ((lib.swimba_linear_attention_workspace_size, LinearAttentionArgs),
                      (lib.swimba_linear_attention_backward_workspace_size,
-                      LinearAttentionGradArgs)):
+                      LinearAttentionGradArgs),
+                     (lib.swimba_delta_rule_workspace_size, DeltaRuleArgs),
+                     (lib.swimba_delta_rule_backward_workspace_size, DeltaRuleGradArgs),
+                     (lib.swimba_norm_rotate_backward_workspace_size, NormRotateGradArgs)):
         fn.argtypes = [ctypes.POINTER(args)]
         fn.restype = _sz
-    lib.swimba_linear_attention_step.argtypes = [ctypes.POINTER(LinearAttentionStepArgs), _vp]
-    lib.swimba_linear_attention_step.restype = _ci
+    for fn, args in ((lib.swimba_linear_attention_step, LinearAttentionStepArgs),
+                     (lib.swimba_delta_rule_step, DeltaRuleStepArgs),
+                     (lib.swimba_norm_rotate, NormRotateArgs)):
+        fn.argtypes = [ctypes.POINTER(args), _vp]
+        fn.restype = _ci
     lib.swimba_status_string.argtypes = [_ci]
     lib.swimba_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -1021,16 +1064,21 @@ class PreparedLinearAttentionStep:
     PreparedStep).  Each call goes to the device's current stream (a capturing one
     records it), or to `stream` if that is given."""
 
+    _name = "swimba_linear_attention_step"
+
     def __init__(self, q, k, v, log_decay, state, state_out=None, y=None, y_dtype=None,
                  stream=None):
         self.args, self.y = _linear_attention_step_args(q, k, v, log_decay, state, state_out, y,
                                                         y_dtype)
-        self._keep = (q, k, v, log_decay, state, state_out)
+        self._prepare((q, k, v, log_decay, state, state_out), v.device, stream)
+
+    def _prepare(self, keep, dev, stream):
+        self._keep = keep
         self._ref = ctypes.byref(self.args)
-        self._fn = load().swimba_linear_attention_step
-        self._dev = v.device.index
-        if stream is not None and stream.device != v.device:
-            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, v.device))
+        self._fn = getattr(load(), self._name)
+        self._dev = dev.index
+        if stream is not None and stream.device != dev:
+            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, dev))
         self.stream = None if stream is None else stream.cuda_stream
 
     def __call__(self):
@@ -1043,5 +1091,227 @@ class PreparedLinearAttentionStep:
         else:
             rc = self._fn(self._ref, stream)
         if rc != OK:
-            raise SwimbaError("swimba_linear_attention_step", rc)
+            raise SwimbaError(self._name, rc)
         return self.y
+
+
+# ---- the gated delta rule ----
+
+
+def _delta_rule_args(q, k, v, log_decay, beta, h0, y, h_final, need_y=True):
+    la = _linear_attention_args(q, k, v, log_decay, h0, y, h_final, need_y)
+    _fits(beta, "beta", (la.B, la.L, la.H), torch.float32, v.device)
+    a = DeltaRuleArgs()
+    for name, _ in LinearAttentionArgs._fields_:
+        setattr(a, name, getattr(la, name))
+    a.beta = _ptr(beta)
+    return a
+
+
+@_placed
+def delta_rule(q, k, v, log_decay, beta, h0=None, y=None, h_final=None, y_dtype=None,
+               want_state=True, workspace=None):
+    """The gated delta rule (include/swimba.h: swimba_delta_rule).  q, k [B,L,G,N], v
+    [B,L,H,P] (f32 or bf16, H a multiple of G); log_decay [H] or [B,L,H] f32; beta
+    [B,L,H] f32; h0 [B,H,N,P] f32.  Returns (y [B,L,H,P], h_final [B,H,N,P] f32 or
+    None)."""
+    if not (isinstance(v, torch.Tensor) and v.dim() == 4 and q.dim() == 4):
+        raise ValueError("q must be [B, L, G, N] and v [B, L, H, P]")
+    if y is None:
+        y = torch.empty(v.shape, dtype=y_dtype or v.dtype, device=v.device)
+    if h_final is None and want_state:
+        h_final = torch.empty((v.shape[0], v.shape[2], q.shape[-1], v.shape[3]),
+                              dtype=torch.float32, device=v.device)
+    a = _delta_rule_args(q, k, v, log_decay, beta, h0, y, h_final)
+    lib, ref = load(), ctypes.byref(a)
+    need = lib.swimba_delta_rule_workspace_size(ref) if workspace is None else 0
+    ws, wp, wn = _workspace(workspace, need, v.device)
+    _check("swimba_delta_rule", lib.swimba_delta_rule(ref, wp, wn, _current(v.device)))
+    return y, h_final
+
+
+def delta_rule_workspace_bytes(q, k, v, log_decay, beta):
+    """Workspace bytes delta_rule needs for these shapes."""
+    a = _delta_rule_args(q, k, v, log_decay, beta, None, None, None, need_y=False)
+    with torch.cuda.device(v.device):
+        return int(load().swimba_delta_rule_workspace_size(ctypes.byref(a)))
+
+
+@_placed
+def delta_rule_backward(q, k, v, log_decay, beta, dy, h0=None, dh_final=None, want_dh0=True,
+                        grad_dtype=torch.float32, out=None, workspace=None):
+    """Gradients of delta_rule (include/swimba.h: swimba_delta_rule_backward) for dL/dy
+    = dy (of v's dtype) and dL/dh_final.  Returns a dict: dq, dk [B,L,G,N], dv
+    [B,L,H,P] of grad_dtype; dlog_decay like log_decay, dbeta [B,L,H] and dh0
+    [B,H,N,P] (when want_dh0), f32."""
+    a = _delta_rule_args(q, k, v, log_decay, beta, h0, None, None, need_y=False)
+    dev = v.device
+    _need(dy, "dy", tuple(v.shape), v.dtype, dev)
+    state = (a.B, a.H, a.N, a.P)
+    if dh_final is not None:
+        _need(dh_final, "dh_final", state, torch.float32, dev)
+    out = dict(out or {})
+    shapes = {"dq": q.shape, "dk": k.shape, "dv": v.shape, "dlog_decay": log_decay.shape,
+              "dbeta": beta.shape}
+    if want_dh0:
+        shapes["dh0"] = state
+    res = {}
+    for name, shape in shapes.items():
+        dt = grad_dtype if name in ("dq", "dk", "dv") else torch.float32
+        res[name] = _new(out.get(name), name, tuple(shape), dt, dev)
+    g = DeltaRuleGradArgs()
+    g.fwd = a
+    g.dy, g.dh_final, g.grad_dtype = _ptr(dy), _ptr(dh_final), _dt(res["dq"])
+    for name in res:
+        setattr(g, name, _ptr(res[name]))
+    lib, ref = load(), ctypes.byref(g)
+    need = lib.swimba_delta_rule_backward_workspace_size(ref) if workspace is None else 0
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _check("swimba_delta_rule_backward",
+           lib.swimba_delta_rule_backward(ref, wp, wn, _current(dev)))
+    return res
+
+
+def _delta_rule_step_args(q, k, v, log_decay, beta, state, state_out, y, y_dtype):
+    la, y = _linear_attention_step_args(q, k, v, log_decay, state, state_out, y, y_dtype)
+    _fits(beta, "beta", (la.B, la.H), torch.float32, v.device)
+    a = DeltaRuleStepArgs()
+    for name, _ in LinearAttentionStepArgs._fields_:
+        setattr(a, name, getattr(la, name))
+    a.beta = _ptr(beta)
+    return a, y
+
+
+@_placed
+def delta_rule_step(q, k, v, log_decay, beta, state, state_out=None, y=None, y_dtype=None):
+    """One decode step of delta_rule (include/swimba.h: swimba_delta_rule_step).  q, k
+    [B,G,N], v [B,H,P]; log_decay [H] or [B,H] f32; beta [B,H] f32; state [B,H,N,P]
+    f32, updated in place unless state_out is given.  Returns y [B,H,P]."""
+    a, y = _delta_rule_step_args(q, k, v, log_decay, beta, state, state_out, y, y_dtype)
+    _check("swimba_delta_rule_step",
+           load().swimba_delta_rule_step(ctypes.byref(a), _current(v.device)))
+    return y
+
+
+class PreparedDeltaRuleStep(PreparedLinearAttentionStep):
+    """swimba_delta_rule_step marshalled once for fixed tensors (see
+    PreparedLinearAttentionStep)."""
+
+    _name = "swimba_delta_rule_step"
+
+    def __init__(self, q, k, v, log_decay, beta, state, state_out=None, y=None, y_dtype=None,
+                 stream=None):
+        self.args, self.y = _delta_rule_step_args(q, k, v, log_decay, beta, state, state_out, y,
+                                                  y_dtype)
+        self._prepare((q, k, v, log_decay, beta, state, state_out), v.device, stream)
+
+
+# ---- norms of queries and keys, with their rotation ----
+
+NORM = {"rms": 0, "l2": 1}
+PAIRS = {"halves": 0, "neighbours": 1}
+
+
+def _token_rows(t, name):
+    """(tokens, heads, N, stride of a token) of a tensor [..., heads, N] whose tokens are
+    equally far apart, each dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dim() < 2:
+        raise ValueError("%s must be [..., heads, N]" % name)
+    heads, N = t.shape[-2:]
+    lead, strides = t.shape[:-2], t.stride()
+    T = 1
+    for n in lead:
+        T *= n
+    if T * heads * N == 0:
+        return T, heads, N, heads * N
+    if (N > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != N):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    stride = far = None
+    for n, step in zip(reversed(lead), reversed(strides[:-2])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride, far = step, step * n
+        elif step == far:
+            far *= n
+        else:
+            raise ValueError("%s: tokens must be equally far apart" % name)
+    stride = heads * N if stride is None else stride
+    if stride < heads * N:
+        raise ValueError("%s: tokens overlap" % name)
+    return T, heads, N, stride
+
+
+def _norm_rotate_args(q, k, wq, wk, positions, rates, norm, pairs, eps, q_scale):
+    a = NormRotateArgs()
+    a.T, a.Hq, a.N, a.q_stride = _token_rows(q, "q")
+    T, a.Hk, N, a.k_stride = _token_rows(k, "k")
+    dev, lead = q.device, tuple(q.shape[:-2])
+    if tuple(k.shape[:-2]) != lead or N != a.N or k.dtype != q.dtype or k.device != dev:
+        raise ValueError("k must have the tokens, the head size, the dtype and the device of q")
+    for name, t in (("wq", wq), ("wk", wk)):
+        if t is not None:
+            _fits(t, name, (N,), torch.float32, dev)
+    if (positions is None) != (rates is None):
+        raise ValueError("positions and rates belong together")
+    if positions is not None:
+        _need(rates, "rates", None, torch.float32, dev)
+        if rates.dim() != 1:
+            raise ValueError("rates must be [R / 2]")
+        _fits(positions, "positions", lead, torch.int32, dev)
+        a.R = 2 * rates.numel()
+    if norm not in NORM or pairs not in PAIRS:
+        raise ValueError("norm is one of %s, pairs of %s" % (sorted(NORM), sorted(PAIRS)))
+    a.in_dtype = a.out_dtype = _dt(q)
+    a.norm, a.pairs, a.eps, a.q_scale = NORM[norm], PAIRS[pairs], eps, q_scale
+    a.q, a.k, a.wq, a.wk = _ptr(q), _ptr(k), _ptr(wq), _ptr(wk)
+    a.positions, a.rates = _ptr(positions), _ptr(rates)
+    return a
+
+
+@_placed
+def norm_rotate(q, k, wq=None, wk=None, positions=None, rates=None, norm="rms", pairs="halves",
+                eps=1e-6, q_scale=1.0, q_out=None, k_out=None, out_dtype=None):
+    """Norms of queries and keys for each head with the rotation of their positions
+    (include/swimba.h: swimba_norm_rotate).  q [..., Hq, N], k [..., Hk, N] (f32 or
+    bf16; tokens may lie apart, as parts of one projection's rows); wq, wk [N] f32;
+    positions [...] int32 with rates [R/2] f32, or neither (no rotation).  norm:
+    "rms" or "l2"; pairs: "halves" or "neighbours".  Returns (q_out, k_out), dense."""
+    a = _norm_rotate_args(q, k, wq, wk, positions, rates, norm, pairs, eps, q_scale)
+    dt = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
+    q_out = _new(q_out, "q_out", tuple(q.shape), dt, q.device)
+    k_out = _new(k_out, "k_out", tuple(k.shape), dt, q.device)
+    a.out_dtype, a.q_out, a.k_out = _dt(q_out), _ptr(q_out), _ptr(k_out)
+    _check("swimba_norm_rotate", load().swimba_norm_rotate(ctypes.byref(a), _current(q.device)))
+    return q_out, k_out
+
+
+@_placed
+def norm_rotate_backward(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, rates=None,
+                         norm="rms", pairs="halves", eps=1e-6, q_scale=1.0,
+                         grad_dtype=torch.float32, out=None, workspace=None):
+    """Gradients of norm_rotate (include/swimba.h: swimba_norm_rotate_backward) for dL/dq_out
+    and dL/dk_out (dense, of q's dtype).  Returns a dict: dq, dk like q and k, of
+    grad_dtype; dwq and dwk [N] f32, None where that weight is not given."""
+    a = _norm_rotate_args(q, k, wq, wk, positions, rates, norm, pairs, eps, q_scale)
+    dev = q.device
+    _need(dq_out, "dq_out", tuple(q.shape), q.dtype, dev)
+    _need(dk_out, "dk_out", tuple(k.shape), k.dtype, dev)
+    out = dict(out or {})
+    res = {"dq": _new(out.get("dq"), "dq", tuple(q.shape), grad_dtype, dev),
+           "dk": _new(out.get("dk"), "dk", tuple(k.shape), grad_dtype, dev)}
+    for name, w in (("dwq", wq), ("dwk", wk)):
+        res[name] = None if w is None else _new(out.get(name), name, (a.N,), torch.float32, dev)
+    g = NormRotateGradArgs()
+    g.fwd = a
+    g.dq_out, g.dk_out, g.grad_dtype = _ptr(dq_out), _ptr(dk_out), _dt(res["dq"])
+    for name in res:
+        setattr(g, name, _ptr(res[name]))
+    lib, ref = load(), ctypes.byref(g)
+    need = lib.swimba_norm_rotate_backward_workspace_size(ref) if workspace is None else 0
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _check("swimba_norm_rotate_backward",
+           lib.swimba_norm_rotate_backward(ref, wp, wn, _current(dev)))
+    return res
