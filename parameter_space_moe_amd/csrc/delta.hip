@@ -39,13 +39,20 @@ int grads(const DeltaGradParams& p, bool f32, hipStream_t s) {
 
 int padded_rows(int N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 
-constexpr size_t kTriBytes = kDeltaTerms * kDeltaTri * sizeof(bf16_t);
+constexpr size_t kTriBytes = kDeltaTri * sizeof(float);
 constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
 
 int64_t chunks_of(const swimba_delta_rule_args* a) { return (a->L + kChunk - 1) / kChunk; }
 
 int64_t key_elements(const swimba_delta_rule_args* a) {
   return (int64_t)a->B * a->L * a->G * a->N;
+}
+int64_t value_elements(const swimba_delta_rule_args* a) {
+  return (int64_t)a->B * a->L * a->H * a->P;
+}
+// Slots for copies of operands of less than a pack.
+size_t tiny_bytes(const swimba_delta_rule_args* a) {
+  return key_elements(a) < kPack || value_elements(a) < kPack ? 4 * kTinySlot : 0;
 }
 
 // Workspace of a forward call: per chunk and head the inverse, the scores and the gates.
@@ -65,7 +72,7 @@ DeltaPlan plan_delta(const swimba_delta_rule_args* a) {
   r.off_tri = take(units * kTriBytes);
   r.off_score = take(units * kTriBytes);
   r.off_gates = take(units * kGateBytes);
-  r.off_tiny = take(key_elements(a) < kPack ? 2 * kTinySlot : 0);
+  r.off_tiny = take(tiny_bytes(a));
   r.bytes = o;
   return r;
 }
@@ -79,7 +86,7 @@ struct DeltaGradPlan {
 DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g) {
   const swimba_delta_rule_args* a = &g->fwd;
   DeltaGradPlan r;
-  const size_t units = (size_t)a->B * a->H * chunks_of(a), Pp = (size_t)(a->P + 63) / 64 * 64;
+  const size_t units = (size_t)a->B * a->H * chunks_of(a), Pp = (size_t)(a->P + kWalkCols - 1) / kWalkCols * kWalkCols;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -99,16 +106,17 @@ DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g) {
   r.off_dq = take(rows);
   r.off_dk = take(rows);
   r.off_part = take(a->decay_form == SWIMBA_DECAY_HEAD ? units * sizeof(double) : 0);
-  r.off_tiny = take(key_elements(a) < kPack ? 2 * kTinySlot : 0);
+  r.off_tiny = take(tiny_bytes(a));
   r.bytes = o;
   return r;
 }
 
-DeltaParams base_params(const swimba_delta_rule_args* a, const void* q, const void* k) {
+DeltaParams base_params(const swimba_delta_rule_args* a, const void* q, const void* k,
+                        const void* v) {
   DeltaParams p = {};
   p.q = q;
   p.k = k;
-  p.v = a->v;
+  p.v = v;
   p.g = a->log_decay;
   p.beta = a->beta;
   p.B = a->B;
@@ -119,9 +127,10 @@ DeltaParams base_params(const swimba_delta_rule_args* a, const void* q, const vo
   p.P = a->P;
   p.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
   p.nc = (int)chunks_of(a);
-  p.ctiles = (a->P + 63) / 64;
-  p.score_terms = kDeltaTerms;
-  p.Pp = 64 * p.ctiles;
+  p.ctiles = (a->P + kWalkCols - 1) / kWalkCols;
+  p.nseg = 1;
+  p.seg_chunks = p.nc;
+  p.Pp = kWalkCols * p.ctiles;
   return p;
 }
 
@@ -261,13 +270,13 @@ int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, hipStream_t s) 
   int rc = SWIMBA_OK;
   const void* q = whole_packs(a->q, key_elements(a), f32, slot, s, &rc);
   const void* k = whole_packs(a->k, key_elements(a), f32, slot + kTinySlot, s, &rc);
-  DeltaParams p = base_params(a, q, k);
-  p.tri = at<bf16_t>(ws, r.off_tri);
-  p.score = at<bf16_t>(ws, r.off_score);
+  const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
+  DeltaParams p = base_params(a, q, k, v);
+  p.tri = at<float>(ws, r.off_tri);
+  p.score = at<float>(ws, r.off_score);
   p.gates = at<float>(ws, r.off_gates);
   p.out = a->y;
   p.out_bf16 = a->y_dtype == SWIMBA_BF16;
-  if (p.out_bf16) p.score_terms = 2;
   p.s0 = a->h0;
   p.s_final = a->h_final;
   if (rc == SWIMBA_OK) rc = phase(p, f32, kPhasePrep, s);
@@ -295,11 +304,12 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, h
   int rc = SWIMBA_OK;
   const void* q = whole_packs(a->q, key_elements(a), f32, slot, s, &rc);
   const void* k = whole_packs(a->k, key_elements(a), f32, slot + kTinySlot, s, &rc);
-  DeltaParams p = base_params(a, q, k);
-  p.dy = g->dy;
-  p.tri = at<bf16_t>(ws, r.off_tri);
-  p.tri_t = at<bf16_t>(ws, r.off_tri_t);
-  p.score = at<bf16_t>(ws, r.off_score);
+  const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
+  DeltaParams p = base_params(a, q, k, v);
+  p.dy = whole_packs(g->dy, value_elements(a), f32, slot + 3 * kTinySlot, s, &rc);
+  p.tri = at<float>(ws, r.off_tri);
+  p.tri_t = at<float>(ws, r.off_tri_t);
+  p.score = at<float>(ws, r.off_score);
   p.gates = at<float>(ws, r.off_gates);
   p.out = g->dv;
   p.out_bf16 = g->grad_dtype == SWIMBA_BF16;

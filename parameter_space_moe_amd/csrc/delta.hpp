@@ -36,7 +36,7 @@ namespace swimba {
 typedef float f4x __attribute__((ext_vector_type(4)));
 
 constexpr int kDeltaBlocks = 6;               // 16 x 32 blocks of a triangle of 64 x 64
-constexpr int kDeltaTri = kDeltaBlocks * 512; // values of one term of a triangle
+constexpr int kDeltaTri = kDeltaBlocks * 512; // values of a triangle
 constexpr int kDeltaTerms = 3;
 constexpr int kDeltaGates = 4 * kChunk;       // floats: e^G, w, beta; e^{G_end}, first bad token
 
@@ -47,11 +47,13 @@ struct DeltaParams {
   int B, L, H, G, N, P;
   int token_decay, out_bf16;
   int nc;                 // chunks
-  int ctiles;             // columns / 64, rounded up
-  int score_terms;        // 2 where y is bf16
+  int ctiles;             // workgroups for the columns of a state
+  int nseg, seg_chunks;   // segments of the walk, chunks in each
+  float* seg_state;       // [B, H, nseg, N', P'] end states out (state pass), first states in
+  float* seg_carry;       // [B, H, nseg, N', N'] the segments' transitions (state pass)
   // workspace, per (b, h, chunk)
-  bf16_t *tri, *tri_t;    // [3][kDeltaTri] T in operand order; its transpose (backward)
-  bf16_t* score;          // [3][kDeltaTri] S, or its transpose (backward)
+  float *tri, *tri_t;     // [kDeltaTri] T in operand order; its transpose (backward)
+  float* score;           // [kDeltaTri] S, or its transpose (backward)
   float* gates;           // [kDeltaGates]
   const float* s0;        // first state or null, [B, H, N, P]
   float* s_final;         // or null
@@ -80,6 +82,50 @@ __device__ __forceinline__ f4x mma_terms(const bf8x* a, const bf8x* b, f4x c) {
   return c;
 }
 
+// The same for M accumulators that share one operand: products of one pair of terms next to
+// each other, as none of them waits for another.
+template <int NA, int NB, int M>
+__device__ __forceinline__ void mma_tiles(const bf8x (*a)[NA], const bf8x* b, f4x* c) {
+  constexpr int kLast = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+  for (int n = kLast; n >= 0; --n)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        if (n - i >= 0 && n - i < NB) c[m] = mma16(a[m][i], b[n - i], c[m]);
+}
+
+// x (8 values) as S bf16 terms, as split_terms() makes them.  What a pair of terms leaves is
+// one two-element product each, x - 1 * term + 0 * the other, which is exact: seven
+// instructions for a pair's three terms instead of eleven.  The factors come from
+// registers: as constants in the instruction they are read as fp32 numbers.
+template <int S>
+__device__ __forceinline__ void split_values(const float* x, bf8x* out) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  uint32_t first = 0x0000bf80u, second = 0xbf800000u;  // (-1, 0) and (0, -1)
+  asm("" : "+s"(first), "+s"(second));
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    Bits8 b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b.w[i] = bf16_pair(r[2 * i], r[2 * i + 1]);
+    out[s] = __builtin_bit_cast(bf8x, b);
+    if (s + 1 < S) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const b2 t = __builtin_bit_cast(b2, b.w[i]);
+        r[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(t, __builtin_bit_cast(b2, first), r[2 * i], false);
+        r[2 * i + 1] =
+            __builtin_amdgcn_fdot2_f32_bf16(t, __builtin_bit_cast(b2, second), r[2 * i + 1], false);
+      }
+    }
+  }
+}
+
 // Two accumulator tiles as one operand in S terms.
 template <int S>
 __device__ __forceinline__ void split_tiles(f4x lo, f4x hi, bf8x* out) {
@@ -89,7 +135,7 @@ __device__ __forceinline__ void split_tiles(f4x lo, f4x hi, bf8x* out) {
     x[i] = lo[i];
     x[4 + i] = hi[i];
   }
-  split_terms<S>(x, out);
+  split_values<S>(x, out);
 }
 
 // Place of column `col` (a multiple of four) of a row in operand order.
@@ -120,22 +166,32 @@ constexpr int kDeltaThreads = 256, kDeltaWaves = 4;
 
 // The staged rows of a chunk into LDS, in operand order and in terms; rows from `len` on
 // are zero.
-template <typename TI, int KT, bool LOOSE>
+template <typename TI, int KT, bool LOOSE, int THREADS = kDeltaThreads>
 struct DeltaRows {
-  using Stage = RowStage<TI, 32 * KT, kDeltaThreads, LOOSE>;
+  using Stage = RowStage<TI, 32 * KT, THREADS, LOOSE>;
   using Sh = DeltaShape<TI, KT>;
   static __device__ __forceinline__ void put(const Stage& st, int round, bf16_t* dst) {
+    if (!LOOSE && st.len == kChunk && st.cols >= Sh::kRows) put_as<true>(st, round, dst);
+    else put_as<false>(st, round, dst);
+  }
+  template <bool FULL>  // nothing to leave out
+  static __device__ __forceinline__ void put_as(const Stage& st, int round, bf16_t* dst) {
 #pragma unroll
     for (int i = 0; i < Stage::kRound; ++i) {
       u4x w[Stage::kQuads];
-      st.pack(round, i, w);
+      if constexpr (FULL) {
+#pragma unroll
+        for (int q = 0; q < Stage::kQuads; ++q) w[q] = st.v[i][q];
+      } else {
+        st.pack(round, i, w);
+      }
       bf16_t* d = dst + st.row(round * Stage::kRound + i) * Sh::kStride +
                   operand_place(st.column());
       if constexpr (Sh::kF32) {
         float x[8];
         __builtin_memcpy(x, w, sizeof(x));
         bf8x t[Sh::kTerms];
-        split_terms<Sh::kTerms>(x, t);
+        split_values<Sh::kTerms>(x, t);
 #pragma unroll
         for (int s = 0; s < Sh::kTerms; ++s) {
           struct { uint2 a, b; } o = __builtin_bit_cast(decltype(o), t[s]);
@@ -272,9 +328,9 @@ __device__ __forceinline__ void unit_inverse(const float* a, float* t, int lane,
 }
 
 // A lower triangle in LDS to the operand order of a product with it, or with its
-// transpose, in two or three terms.  The triangle's 32-blocks are whole (zeros above).
+// transpose.  The triangle's 32-blocks are whole (zeros above).
 template <bool TRANSPOSED>
-__device__ __forceinline__ void put_triangle(const float* m, bf16_t* out, int terms, int tid) {
+__device__ __forceinline__ void put_triangle(const float* m, float* out, int tid) {
   for (int e = tid; e < kDeltaBlocks * 64; e += kDeltaThreads) {
     const int blk = e >> 6, lane = e & 63, g = lane >> 4;
     int rt, b;
@@ -301,11 +357,9 @@ __device__ __forceinline__ void put_triangle(const float* m, bf16_t* out, int te
         x[4 * h + 3] = v.w;
       }
     }
-    bf8x t[kDeltaTerms];
-    split_terms<kDeltaTerms>(x, t);
-#pragma unroll
-    for (int s = 0; s < kDeltaTerms; ++s)
-      if (s < terms) *reinterpret_cast<bf8x*>(out + s * kDeltaTri + blk * 512 + lane * 8) = t[s];
+    float4* to = reinterpret_cast<float4*>(out + e * 8);
+    to[0] = make_float4(x[0], x[1], x[2], x[3]);
+    to[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
 }
 
@@ -448,10 +502,10 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
     }
   __syncthreads();
   unit_inverse(sA, sT, lane, wave);
-  const int64_t to = unit * kDeltaTerms * kDeltaTri;
-  put_triangle<false>(sT, p.tri + to, kDeltaTerms, tid);
-  if (BACK) put_triangle<true>(sT, p.tri_t + to, kDeltaTerms, tid);
-  put_triangle<BACK>(sP, p.score + to, p.score_terms, tid);
+  const int64_t to = unit * kDeltaTri;
+  put_triangle<false>(sT, p.tri + to, tid);
+  if (BACK) put_triangle<true>(sT, p.tri_t + to, tid);
+  put_triangle<BACK>(sP, p.score + to, tid);
 }
 
 // ---- the walk -------------------------------------------------------------------
@@ -460,39 +514,96 @@ enum DeltaMode {
   kDeltaOut = 0,    // y, in bf16
   kDeltaOutF32 = 1, // y, in fp32
   kDeltaKeep = 2,   // each chunk's first state, and O
-  kDeltaBack = 3    // dv, each chunk's last adjoint and dV, backwards
+  kDeltaBack = 3,   // dv, each chunk's last adjoint and dV, backwards
+  kDeltaSeg = 4,    // only a segment's end state from zero, and its transition
+  kDeltaSegBack = 5,// only a segment's adjoint before it from zero
+  kDeltaSegOut = 6  // kDeltaSeg for kDeltaOut
 };
 
-template <typename TI, int KT, int MODE>
+// Terms of what is computed: two where inputs and y are bf16.
+template <typename TI, int MODE>
+constexpr int delta_terms() {
+  return sizeof(TI) == 2 && (MODE == kDeltaOut || MODE == kDeltaSegOut) ? 2 : 3;
+}
+
+template <typename TI, int KT, int MODE, int COLS>
 struct DeltaLds {
   using Sh = DeltaShape<TI, KT>;
-  static constexpr bool kQ = MODE != kDeltaKeep;
+  static constexpr bool kQ = MODE != kDeltaKeep && MODE != kDeltaSeg && MODE != kDeltaSegOut;
+  static constexpr int kTerms = delta_terms<TI, MODE>();
   static constexpr size_t kRows = (size_t)(kQ ? 2 : 1) * Sh::kTerms * Sh::kTile;
-  static constexpr int kScoreTerms = MODE == kDeltaOut ? 2 : kQ ? kDeltaTerms : 0;
-  static constexpr size_t kTris = (size_t)(kDeltaTerms + kScoreTerms) * kDeltaTri;
+  static constexpr int kScoreTerms = MODE == kDeltaOut ? 2 : kQ ? kTerms : 0;
+  static constexpr size_t kTris = (size_t)(kTerms + kScoreTerms) * kDeltaTri;
+  // values: strides that spread the transposing reads over the banks
+  static constexpr int kValStride = COLS + (Sh::kF32 ? 4 : 8);
+  static constexpr size_t kVals = (size_t)kChunk * kValStride * (Sh::kF32 ? 4 : 2);
   static constexpr size_t kBytes =
-      (kRows + kTris) * sizeof(bf16_t) + kDeltaGates * sizeof(float);
+      (kRows + kTris) * sizeof(bf16_t) + kVals + kDeltaGates * sizeof(float);
 };
 
-template <typename TI, int KT, bool LOOSE, int MODE>
-__global__ __launch_bounds__(kDeltaThreads, 1) void delta_walk_kernel(DeltaParams p) {
+// Element `i` of a wave-uniform base and a byte offset per lane.
+template <typename T>
+__device__ __forceinline__ T& lane_at(T* base, int64_t i, uint32_t off) {
+  return *reinterpret_cast<T*>(reinterpret_cast<char*>(base + i) + off);
+}
+
+// A triangle's values on their way to LDS, where they lie in terms.
+template <int TERMS, int THREADS>
+struct TriStage {
+  static constexpr int kAll = kDeltaTri / 8, kN = (kAll + THREADS - 1) / THREADS;
+  f4x v[kN][2];
+  __device__ __forceinline__ void load(const float* from, int tid) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = i * THREADS + tid;
+      const f4x* at = reinterpret_cast<const f4x*>(from) + 2 * (e < kAll ? e : tid);
+      v[i][0] = at[0];
+      v[i][1] = at[1];
+    }
+  }
+  __device__ __forceinline__ void store(bf16_t* to, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = i * THREADS + tid;
+      bf8x t[TERMS];
+      split_tiles<TERMS>(v[i][0], v[i][1], t);
+      if (kAll % THREADS == 0 || e < kAll) {
+#pragma unroll
+        for (int s = 0; s < TERMS; ++s)
+          *reinterpret_cast<bf8x*>(to + s * kDeltaTri + e * 8) = t[s];
+      }
+    }
+  }
+};
+
+// Two workgroups of four waves share a CU where LDS and 256 registers suffice.
+template <typename TI, int KT>
+constexpr int delta_waves_per_simd() {
+  return sizeof(TI) == 2 && KT <= 4 ? 2 : 1;
+}
+
+template <typename TI, int KT, bool LOOSE, int MODE, int W, int CT>
+__global__ __launch_bounds__(64 * W) __attribute__((
+    amdgpu_waves_per_eu(delta_waves_per_simd<TI, KT>(), delta_waves_per_simd<TI, KT>())))
+void delta_walk_kernel(DeltaParams p) {
+  constexpr int THREADS = 64 * W, COLS = 16 * W * CT;
   using Sh = DeltaShape<TI, KT>;
-  using Rows = DeltaRows<TI, KT, LOOSE>;
-  using Lds = DeltaLds<TI, KT, MODE>;
+  using Rows = DeltaRows<TI, KT, LOOSE, THREADS>;
+  using Lds = DeltaLds<TI, KT, MODE, COLS>;
   constexpr int NT = Sh::kTerms, HT = 2 * KT;  // terms of inputs; 16-row tiles
-  constexpr bool BACK = MODE == kDeltaBack, QUERY = Lds::kQ;
+  constexpr bool BACK = MODE == kDeltaBack || MODE == kDeltaSegBack, QUERY = Lds::kQ;
   constexpr bool OUT = MODE == kDeltaOut || MODE == kDeltaOutF32;
-  constexpr int S = kDeltaTerms, YT = MODE == kDeltaOut ? 2 : S, QT = NT < YT ? NT : YT;
-  // 16-byte loads of the triangles' terms
-  constexpr int kTriPacks = S * kDeltaTri / 8, kScorePacks = Lds::kScoreTerms * kDeltaTri / 8;
-  constexpr int kTriLoads = (kTriPacks + kDeltaThreads - 1) / kDeltaThreads;
-  constexpr int kScoreLoads = (kScorePacks + kDeltaThreads - 1) / kDeltaThreads;
+  constexpr bool CARRY = MODE == kDeltaSeg || MODE == kDeltaSegOut;  // transitions too
+  constexpr bool SEG = CARRY || MODE == kDeltaSegBack;
+  constexpr bool KEEP = MODE == kDeltaKeep || MODE == kDeltaBack;
+  constexpr int S = Lds::kTerms, YT = MODE == kDeltaOut ? 2 : S, QT = NT < YT ? NT : YT;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
   bf16_t* sK = reinterpret_cast<bf16_t*>(smem_raw);
   bf16_t* sQ = sK + NT * Sh::kTile;  // (QUERY)
   bf16_t* sT = sK + Lds::kRows;
   bf16_t* sP = sT + S * kDeltaTri;   // (QUERY)
-  float* sG = reinterpret_cast<float*>(sT + Lds::kTris);
+  TI* sV = reinterpret_cast<TI*>(sT + Lds::kTris);
+  float* sG = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(sV) + Lds::kVals);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int g = lane >> 4;
@@ -502,31 +613,55 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_walk_kernel(DeltaParam
     const int n = gridDim.x, x = blk & 7, per = n >> 3, more = n & 7;
     blk = x * per + (x < more ? x : more) + (blk >> 3);
   }
-  const int ct = blk % p.ctiles;
-  const int bh = blk / p.ctiles, b = bh / p.H, h = bh - b * p.H;
-  const int c = 64 * ct + 16 * wave + (lane & 15);  // this lane's column
-  const bool inside = c < p.P;
+  // the state pass has columns of the transition behind those of the state
+  const int all_tiles = CARRY ? p.ctiles + (32 * KT + COLS - 1) / COLS : p.ctiles;
+  const int tile = blk % all_tiles;
+  blk /= all_tiles;
+  const int segs = SEG ? p.nseg - 1 : p.nseg;  // the last one's end is not carried on
+  const int seg = blk % segs;
+  const int bh = blk / segs, b = bh / p.H, h = bh - b * p.H;
+  const bool unit_state = CARRY && tile >= p.ctiles;
+  const int c0 = COLS * (unit_state ? tile - p.ctiles : tile);
+  const int cw = 16 * CT * wave + (lane & 15);  // this lane's first column in the workgroup
+  const int width = unit_state ? 0 : p.P - c0;  // columns with values
   const int grp = h / (p.H / p.G);
   const int64_t vstride = (int64_t)p.H * p.P;
-  const int64_t vfirst = (int64_t)b * p.L * vstride + (int64_t)h * p.P + (inside ? c : 0);
+  const int64_t vfirst = (int64_t)b * p.L * vstride + (int64_t)h * p.P + (unit_state ? 0 : c0);
   const int64_t state = (int64_t)bh * p.N * p.P;
+  // chunks of this segment; segments are the same either way, counted from where the walk starts
+  const int low = (BACK ? p.nseg - 1 - seg : seg) * p.seg_chunks;
+  const int high = low + p.seg_chunks < p.nc ? low + p.seg_chunks : p.nc;
+  const int nj = high - low;
+  auto chunk_of = [&](int j) { return BACK ? high - 1 - j : low + j; };
 
-  f4x st[HT];
+  f4x st[CT][HT];
 #pragma unroll
-  for (int i = 0; i < HT; ++i)
+  for (int k = 0; k < CT; ++k)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int n = 16 * i + 4 * g + r;
-      st[i][r] = p.s0 != nullptr && inside && n < p.N ? p.s0[state + (int64_t)n * p.P + c] : 0.f;
-    }
+    for (int i = 0; i < HT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = 16 * i + 4 * g + r, cc = cw + 16 * k;
+        float v = 0.f;
+        if constexpr (SEG) {
+          v = unit_state && n == c0 + cc ? 1.f : 0.f;
+        } else if (p.nseg > 1) {
+          v = p.seg_state[(((int64_t)bh * p.nseg + seg) * (32 * KT) + n) * p.Pp + c0 + cc];
+        } else if (p.s0 != nullptr) {
+          if (cc < width && n < p.N) v = p.s0[state + (int64_t)n * p.P + c0 + cc];
+        }
+        st[k][i][r] = v;
+      }
 
   constexpr bool kAhead = Rows::Stage::kRounds == 1;
   typename Rows::Stage rk, rq;
-  u4x tri[kTriLoads], score[kScoreLoads + 1];
-  float gate = 0.f;
+  TriStage<S, THREADS> tri;
+  TriStage<MODE == kDeltaOut ? 2 : S, THREADS> score;
+  using Vals = RowStage<TI, COLS, THREADS, LOOSE>;
+  static_assert(Vals::kRounds == 1, "values in one round");
+  Vals rv;
+  float gate[kDeltaGates / THREADS];
   int next_bad = kChunk;
-  TI val[16];
-  auto chunk_of = [&](int j) { return BACK ? p.nc - 1 - j : j; };
   auto fetch = [&](int j) {
     const int cc = chunk_of(j), t0 = cc * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
     const int64_t unit = (int64_t)bh * p.nc + cc;
@@ -536,30 +671,67 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_walk_kernel(DeltaParam
       Rows::place(rq, p.q, p, b, grp, t0, len, tid);
       if (kAhead) rq.load(0);
     }
-    const u4x* ts = reinterpret_cast<const u4x*>((BACK ? p.tri_t : p.tri) + unit * S * kDeltaTri);
-    const u4x* ps = reinterpret_cast<const u4x*>(p.score + unit * S * kDeltaTri);
+    tri.load((BACK ? p.tri_t : p.tri) + unit * kDeltaTri, tid);
+    if (QUERY) score.load(p.score + unit * kDeltaTri, tid);
 #pragma unroll
-    for (int i = 0; i < kTriLoads; ++i) {
-      const int e = i * kDeltaThreads + tid;
-      tri[i] = ts[e < kTriPacks ? e : tid];
-    }
-#pragma unroll
-    for (int i = 0; i < kScoreLoads; ++i) {
-      const int e = i * kDeltaThreads + tid;
-      score[i] = ps[e < kScorePacks ? e : tid];
-    }
-    gate = p.gates[unit * kDeltaGates + tid];
+    for (int i = 0; i < kDeltaGates / THREADS; ++i)
+      gate[i] = p.gates[unit * kDeltaGates + i * THREADS + tid];
     next_bad = __float_as_int(p.gates[unit * kDeltaGates + 3 * kChunk + 1]);
-    const TI* v = static_cast<const TI*>(BACK ? p.dy : p.v) + vfirst + t0 * vstride;
+    const int64_t all = (int64_t)p.B * p.L * vstride;
+    rv.base = static_cast<const TI*>(BACK ? p.dy : p.v);
+    rv.total = all < kPack ? kPack : all;
+    rv.first = vfirst + t0 * vstride;
+    rv.stride = vstride;
+    rv.cols = width;
+    rv.len = len;
+    rv.tid = tid;
+    rv.down = false;
+    rv.load(0);
+  };
+  // A chunk's results, stored while the next one is worked on.
+  f4x late[CT][4];
+  const uint32_t state_off = (uint32_t)(4 * g * p.Pp + c0 + cw) * 4u;  // of the workspace's rows
+  auto leave_as = [&](auto* out, int64_t first, int len) {
+    using TO = std::remove_pointer_t<decltype(out)>;
+    const uint32_t off = (uint32_t)(4 * g * (uint32_t)vstride + (uint32_t)cw) * (uint32_t)sizeof(TO);
+    out += first;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int t = 16 * (i >> 2) + 4 * g + (i & 3);
-      val[i] = v[(t < len ? t : 0) * vstride];
+    for (int k = 0; k < CT; ++k) {
+      if (cw + 16 * k >= width) continue;
+      if (len == kChunk) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          lane_at(out, (16 * (i >> 2) + (i & 3)) * vstride + 16 * k, off) =
+              from_f32<TO>(late[k][i >> 2][i & 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (16 * (i >> 2) + 4 * g + (i & 3) < len)
+            lane_at(out, (16 * (i >> 2) + (i & 3)) * vstride + 16 * k, off) =
+                from_f32<TO>(late[k][i >> 2][i & 3]);
+      }
     }
+  };
+  auto leave = [&](int cc) {
+    const int t0 = cc * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
+    if (KEEP) {
+      float* to = p.rows + ((int64_t)bh * p.nc + cc) * kChunk * p.Pp;
+#pragma unroll
+      for (int k = 0; k < CT; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          lane_at(to, (16 * (i >> 2) + (i & 3)) * p.Pp + 16 * k, state_off) =
+              late[k][i >> 2][i & 3];
+    }
+    const int64_t first = vfirst + t0 * vstride;
+    if (MODE == kDeltaOut) leave_as(static_cast<bf16_t*>(p.out), first, len);
+    else if (MODE == kDeltaOutF32) leave_as(static_cast<float*>(p.out), first, len);
+    else if (MODE == kDeltaBack && p.out_bf16) leave_as(static_cast<bf16_t*>(p.out), first, len);
+    else if (MODE == kDeltaBack) leave_as(static_cast<float*>(p.out), first, len);
   };
   fetch(0);
 
-  for (int j = 0; j < p.nc; ++j) {
+  for (int j = 0; j < nj; ++j) {
     const int cc = chunk_of(j), t0 = cc * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
     const int64_t unit = (int64_t)bh * p.nc + cc;
     if (j > 0 && !kAhead) fetch(j);
@@ -573,225 +745,285 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_walk_kernel(DeltaParam
       if (!kAhead) rq.load(0);
       Rows::all(rq, sQ);
     }
+    tri.store(sT, tid);
+    if (QUERY) score.store(sP, tid);
 #pragma unroll
-    for (int i = 0; i < kTriLoads; ++i) {
-      const int e = i * kDeltaThreads + tid;
-      if (e < kTriPacks) reinterpret_cast<u4x*>(sT)[e] = tri[i];
-    }
-#pragma unroll
-    for (int i = 0; i < kScoreLoads; ++i) {
-      const int e = i * kDeltaThreads + tid;
-      if (e < kScorePacks) reinterpret_cast<u4x*>(sP)[e] = score[i];
-    }
-    sG[tid] = gate;
-    f4x vv[4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int t = 16 * (i >> 2) + 4 * g + (i & 3);
-      vv[i >> 2][i & 3] = inside && t < used ? to_f32(val[i]) : 0.f;
-    }
-    // an infinity or a NaN of v reaches its own column from its token on
-    int limit = bad;
-    if constexpr (!BACK) {
-      bool wild = false;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) wild |= not_finite(vv[i >> 2][i & 3]);
-      if (__ballot(wild)) {
-        __builtin_amdgcn_sched_barrier(0);
-        int first = kChunk;
-#pragma unroll
-        for (int i = 15; i >= 0; --i)
-          if (not_finite(vv[i >> 2][i & 3])) first = 16 * (i >> 2) + 4 * g + (i & 3);
-        int o = __shfl_xor(first, 16);
-        first = o < first ? o : first;
-        o = __shfl_xor(first, 32);
-        first = o < first ? o : first;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (16 * (i >> 2) + 4 * g + (i & 3) >= first) vv[i >> 2][i & 3] = 0.f;
-        limit = first < limit ? first : limit;
-      }
-    }
+    for (int i = 0; i < kDeltaGates / THREADS; ++i) sG[i * THREADS + tid] = gate[i];
+    rv.len = used;
+    rv.store(0, sV, Lds::kValStride);
     __syncthreads();
-    if (kAhead && j + 1 < p.nc) fetch(j + 1);
-
-    if (!OUT) {
-      float* to = p.states + unit * (32 * KT) * p.Pp + c;
+    // stores before the loads that the next chunk waits for, not behind them
+    if (j > 0 && !SEG) leave(chunk_of(j - 1));
+    if (KEEP) {
+      float* to = p.states + unit * (32 * KT) * p.Pp;
 #pragma unroll
-      for (int i = 0; i < HT; ++i)
+      for (int k = 0; k < CT; ++k)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) to[(int64_t)(16 * i + 4 * g + r) * p.Pp] = st[i][r];
+        for (int i = 0; i < HT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            lane_at(to, (16 * i + r) * p.Pp + 16 * k, state_off) = st[k][i][r];
     }
+    if (kAhead && j + 1 < nj) fetch(j + 1);
 
-    // K h, and Q h
-    f4x z[4], y[4];
+    // K h, and Q h, the next rows on their way
+    f4x z[CT][4], y[CT][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      z[t] = f4x{0.f, 0.f, 0.f, 0.f};
-      y[t] = f4x{0.f, 0.f, 0.f, 0.f};
-    }
-#pragma unroll
-    for (int n = 0; n < KT; ++n) {
-      bf8x hb[S];
-      split_tiles<S>(st[2 * n], st[2 * n + 1], hb);
+    for (int k = 0; k < CT; ++k)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        bf8x a[NT];
-        row_operand<Sh>(sK, 16 * t, n, lane, a);
-        z[t] = mma_terms<NT, S>(a, hb, z[t]);
-        if (OUT) {
-          row_operand<Sh>(sQ, 16 * t, n, lane, a);
-          y[t] = mma_terms<QT, YT>(a, hb, y[t]);
+        z[k][t] = f4x{0.f, 0.f, 0.f, 0.f};
+        y[k][t] = f4x{0.f, 0.f, 0.f, 0.f};
+      }
+    {
+      bf8x ak[2][4][NT], aq[2][4][QT];
+      auto rows = [&](int n) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          row_operand<Sh>(sK, 16 * t, n, lane, ak[n & 1][t]);
+          if (OUT) {
+            bf8x a[NT];
+            row_operand<Sh>(sQ, 16 * t, n, lane, a);
+#pragma unroll
+            for (int i = 0; i < QT; ++i) aq[n & 1][t][i] = a[i];
+          }
+        }
+      };
+      rows(0);
+#pragma unroll
+      for (int n = 0; n < KT; ++n) {
+        bf8x hb[CT][S];
+#pragma unroll
+        for (int k = 0; k < CT; ++k) split_tiles<S>(st[k][2 * n], st[k][2 * n + 1], hb[k]);
+        if (n + 1 < KT) rows(n + 1);
+#pragma unroll
+        for (int k = 0; k < CT; ++k) {
+          mma_tiles<NT, S, 4>(ak[n & 1], hb[k], z[k]);
+          if (OUT) mma_tiles<QT, YT, 4>(aq[n & 1], hb[k], y[k]);
+        }
+      }
+    }
+    // this lane's columns of the values; an infinity or a NaN of v reaches its own column from
+    // its token on
+    f4x vv[CT][4];
+    int limit[CT];
+#pragma unroll
+    for (int k = 0; k < CT; ++k) {
+      float odd = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if constexpr (Sh::kF32) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            vv[k][t][r] = sV[(16 * t + 4 * g + r) * Lds::kValStride + cw + 16 * k];
+        } else {
+          typedef __attribute__((address_space(3))) s4x* lds_s4;
+          const int i = lane & 15;
+          const s4x q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s4)(sV + (16 * t + 4 * g + (i >> 2)) * Lds::kValStride + 16 * CT * wave +
+                       16 * k + 4 * (i & 3)));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) vv[k][t][r] = to_f32((bf16_t)q[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) odd = fmaf(vv[k][t][r], 0.f, odd);
+      }
+      limit[k] = bad;
+      if constexpr (!BACK) {
+        if (__ballot(!(odd == 0.f))) {
+          __builtin_amdgcn_sched_barrier(0);
+          int first = kChunk;
+#pragma unroll
+          for (int i = 15; i >= 0; --i)
+            if (not_finite(vv[k][i >> 2][i & 3])) first = 16 * (i >> 2) + 4 * g + (i & 3);
+          int o = __shfl_xor(first, 16);
+          first = o < first ? o : first;
+          o = __shfl_xor(first, 32);
+          first = o < first ? o : first;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (16 * (i >> 2) + 4 * g + (i & 3) >= first) vv[k][i >> 2][i & 3] = 0.f;
+          limit[k] = first < bad ? first : bad;
         }
       }
     }
     auto gates = [&](int which, int t) {
       return *reinterpret_cast<const f4x*>(sG + which * kChunk + 16 * t + 4 * g);
     };
-    auto triangle = [&](const bf16_t* m, int blk2, int terms, bf8x* out) {
+    // c += the triangle's (or its transpose's) product with values in terms
+    auto triangle = [&](auto nt, auto nb, const bf16_t* tri_in, int m, auto& v, f4x (*acc)[4]) {
+      constexpr int NA = decltype(nt)::value, NB = decltype(nb)::value;
+      bf8x a[4][NA];
 #pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (s < terms)
-          out[s] = *reinterpret_cast<const bf8x*>(m + s * kDeltaTri + blk2 * 512 + lane * 8);
+      for (int t = 0; t < 4; ++t) {
+        if (BACK ? t >= 2 * m + 2 : t < 2 * m) continue;
+        const int blk2 = BACK ? tri_block_t(t, m) : tri_block(t, m);
+#pragma unroll
+        for (int s = 0; s < NA; ++s)
+          a[t][s] = *reinterpret_cast<const bf8x*>(tri_in + s * kDeltaTri + blk2 * 512 + lane * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < CT; ++k) {
+        if (BACK ? m == 1 : m == 0) mma_tiles<NA, NB, 4>(a, v[k], acc[k]);
+        else if (BACK) mma_tiles<NA, NB, 2>(a, v[k], acc[k]);
+        else mma_tiles<NA, NB, 2>(a + 2, v[k], acc[k] + 2);
+      }
+    };
+    using Three = std::integral_constant<int, S>;
+    using OfY = std::integral_constant<int, YT>;
+    using OfInput = std::integral_constant<int, NT>;
+    // state += columns of staged rows times values in terms
+    auto update = [&](const bf16_t* tile_in, int m, auto& v) {
+      constexpr int kAtOnce = NT == 1 ? (HT < 8 ? HT : 8) : 2;
+#pragma unroll
+      for (int i0 = 0; i0 < HT; i0 += kAtOnce) {
+        bf8x a[kAtOnce][NT];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) column_operand<Sh>(tile_in, i0 + i, m, lane, a[i]);
+#pragma unroll
+        for (int k = 0; k < CT; ++k) mma_tiles<NT, S, kAtOnce>(a, v[k], st[k] + i0);
+      }
     };
     const float carry = sG[3 * kChunk];
-    f4x o[4];
+    f4x o[CT][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) o[t] = f4x{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < CT; ++k)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[k][t] = f4x{0.f, 0.f, 0.f, 0.f};
     if constexpr (!BACK) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) vv[t] -= gates(0, t) * z[t];
+      for (int t = 0; t < 4; ++t) {
+        const f4x e = gates(0, t);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        bf8x rb[S];
-        split_tiles<S>(vv[2 * m], vv[2 * m + 1], rb);
-#pragma unroll
-        for (int t = 2 * m; t < 4; ++t) {
-          bf8x a[S];
-          triangle(sT, tri_block(t, m), S, a);
-          o[t] = mma_terms<S, S>(a, rb, o[t]);
+        for (int k = 0; k < CT; ++k) {
+          vv[k][t] -= e * z[k][t];
+          if (OUT) y[k][t] *= e;
         }
       }
-      f4x u[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) u[t] = gates(2, t) * o[t];
+      for (int m = 0; m < 2; ++m) {
+        bf8x rb[CT][S];
+#pragma unroll
+        for (int k = 0; k < CT; ++k) split_tiles<S>(vv[k][2 * m], vv[k][2 * m + 1], rb[k]);
+        triangle(Three(), Three(), sT, m, rb, o);
+      }
+      f4x u[CT][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f4x e = gates(2, t);
+#pragma unroll
+        for (int k = 0; k < CT; ++k) u[k][t] = e * o[k][t];
+      }
       if (OUT) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) y[t] *= gates(0, t);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          bf8x ub[YT];
-          split_tiles<YT>(u[2 * m], u[2 * m + 1], ub);
+          bf8x ub[CT][YT];
 #pragma unroll
-          for (int t = 2 * m; t < 4; ++t) {
-            bf8x a[S];
-            triangle(sP, tri_block(t, m), YT, a);
-            y[t] = mma_terms<YT, YT>(a, ub, y[t]);
-          }
+          for (int k = 0; k < CT; ++k) split_tiles<YT>(u[k][2 * m], u[k][2 * m + 1], ub[k]);
+          triangle(OfY(), OfY(), sP, m, ub, y);
         }
       }
 #pragma unroll
-      for (int i = 0; i < HT; ++i) st[i] *= carry;
+      for (int k = 0; k < CT; ++k)
+#pragma unroll
+        for (int i = 0; i < HT; ++i) st[k][i] *= carry;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x ub[S];
-        split_tiles<S>(u[2 * m] * gates(1, 2 * m), u[2 * m + 1] * gates(1, 2 * m + 1), ub);
+        bf8x ub[CT][S];
+        const f4x e0 = gates(1, 2 * m), e1 = gates(1, 2 * m + 1);
 #pragma unroll
-        for (int i = 0; i < HT; ++i) {
-          bf8x a[NT];
-          column_operand<Sh>(sK, i, m, lane, a);
-          st[i] = mma_terms<NT, S>(a, ub, st[i]);
-        }
+        for (int k = 0; k < CT; ++k) split_tiles<S>(u[k][2 * m] * e0, u[k][2 * m + 1] * e1, ub[k]);
+        update(sK, m, ub);
       }
-      if (limit < len) {
 #pragma unroll
-        for (int i = 0; i < HT; ++i)
+      for (int k = 0; k < CT; ++k) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) st[i][r] = __builtin_nanf("");
-      }
-      if (OUT) {
-        const int64_t to = vfirst + t0 * vstride;
+        for (int t = 0; t < 4; ++t) late[k][t] = OUT ? y[k][t] : o[k][t];
+        if (limit[k] < len) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = 16 * (i >> 2) + 4 * g + (i & 3);
-          const float v = t < limit ? y[i >> 2][i & 3] : __builtin_nanf("");
-          if (inside && t < len) {
-            if (p.out_bf16) static_cast<bf16_t*>(p.out)[to + t * vstride] = from_f32<bf16_t>(v);
-            else static_cast<float*>(p.out)[to + t * vstride] = v;
-          }
+          for (int i = 0; i < HT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st[k][i][r] = __builtin_nanf("");
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (16 * (i >> 2) + 4 * g + (i & 3) >= limit[k])
+              late[k][i >> 2][i & 3] = __builtin_nanf("");
         }
-      } else {
-        float* to = p.rows + unit * kChunk * p.Pp + c;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          to[(16 * (i >> 2) + 4 * g + (i & 3)) * p.Pp] = o[i >> 2][i & 3];
       }
     } else {
       // dU = w K a + S^T dY, dV = T^T (beta dU)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) z[t] *= gates(1, t);
+      for (int t = 0; t < 4; ++t) {
+        const f4x e = gates(1, t);
+#pragma unroll
+        for (int k = 0; k < CT; ++k) z[k][t] *= e;
+      }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x db[NT];
-        split_tiles<NT>(vv[2 * m], vv[2 * m + 1], db);
+        bf8x db[CT][NT];
 #pragma unroll
-        for (int t = 0; t < 2 * m + 2; ++t) {
-          bf8x a[S];
-          triangle(sP, tri_block_t(t, m), S, a);
-          z[t] = mma_terms<S, NT>(a, db, z[t]);
-        }
+        for (int k = 0; k < CT; ++k) split_tiles<NT>(vv[k][2 * m], vv[k][2 * m + 1], db[k]);
+        triangle(Three(), OfInput(), sP, m, db, z);
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) z[t] *= gates(2, t);
+      for (int t = 0; t < 4; ++t) {
+        const f4x e = gates(2, t);
+#pragma unroll
+        for (int k = 0; k < CT; ++k) z[k][t] *= e;
+      }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x ub[S];
-        split_tiles<S>(z[2 * m], z[2 * m + 1], ub);
+        bf8x ub[CT][S];
 #pragma unroll
-        for (int t = 0; t < 2 * m + 2; ++t) {
-          bf8x a[S];
-          triangle(sT, tri_block_t(t, m), S, a);
-          o[t] = mma_terms<S, S>(a, ub, o[t]);
-        }
+        for (int k = 0; k < CT; ++k) split_tiles<S>(z[k][2 * m], z[k][2 * m + 1], ub[k]);
+        triangle(Three(), Three(), sT, m, ub, o);
       }
 #pragma unroll
-      for (int i = 0; i < HT; ++i) st[i] *= carry;
+      for (int k = 0; k < CT; ++k)
+#pragma unroll
+        for (int i = 0; i < HT; ++i) st[k][i] *= carry;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x yb[S], vb[S];
-        split_tiles<S>(vv[2 * m] * gates(0, 2 * m), vv[2 * m + 1] * gates(0, 2 * m + 1), yb);
-        split_tiles<S>(o[2 * m] * -gates(0, 2 * m), o[2 * m + 1] * -gates(0, 2 * m + 1), vb);
+        bf8x yb[CT][S], vb[CT][S];
+        const f4x e0 = gates(0, 2 * m), e1 = gates(0, 2 * m + 1);
 #pragma unroll
-        for (int i = 0; i < HT; ++i) {
-          bf8x a[NT];
-          column_operand<Sh>(sQ, i, m, lane, a);
-          st[i] = mma_terms<NT, S>(a, yb, st[i]);
-          column_operand<Sh>(sK, i, m, lane, a);
-          st[i] = mma_terms<NT, S>(a, vb, st[i]);
+        for (int k = 0; k < CT; ++k) {
+          split_tiles<S>(vv[k][2 * m] * e0, vv[k][2 * m + 1] * e1, yb[k]);
+          split_tiles<S>(o[k][2 * m] * -e0, o[k][2 * m + 1] * -e1, vb[k]);
         }
+        update(sQ, m, yb);
+        update(sK, m, vb);
       }
-      const int64_t to = vfirst + t0 * vstride;
-      float* keep = p.rows + unit * kChunk * p.Pp + c;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int t = 16 * (i >> 2) + 4 * g + (i & 3);
-        const float v = o[i >> 2][i & 3];
-        keep[t * p.Pp] = v;
-        if (inside && t < len) {
-          if (p.out_bf16) static_cast<bf16_t*>(p.out)[to + t * vstride] = from_f32<bf16_t>(v);
-          else static_cast<float*>(p.out)[to + t * vstride] = v;
-        }
-      }
+      for (int k = 0; k < CT; ++k)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) late[k][t] = o[k][t];
     }
   }
-  if (p.s_final != nullptr) {
+  if (!SEG) leave(chunk_of(nj - 1));
+  if constexpr (SEG) {
+    const int64_t at = (int64_t)bh * p.nseg + seg;
+    const int ld = unit_state ? 32 * KT : p.Pp;
+    float* to = unit_state ? p.seg_carry + at * (32 * KT) * (32 * KT) : p.seg_state + at * (32 * KT) * p.Pp;
 #pragma unroll
-    for (int i = 0; i < HT; ++i)
+    for (int k = 0; k < CT; ++k) {
+      if (c0 + cw + 16 * k >= ld) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int n = 16 * i + 4 * g + r;
-        if (inside && n < p.N) p.s_final[state + (int64_t)n * p.P + c] = st[i][r];
-      }
+      for (int i = 0; i < HT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          to[(int64_t)(16 * i + 4 * g + r) * ld + c0 + cw + 16 * k] = st[k][i][r];
+    }
+  } else if (p.s_final != nullptr && seg == p.nseg - 1) {
+#pragma unroll
+    for (int k = 0; k < CT; ++k)
+#pragma unroll
+      for (int i = 0; i < HT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int n = 16 * i + 4 * g + r, cc = cw + 16 * k;
+          if (cc < width && n < p.N) p.s_final[state + (int64_t)n * p.P + c0 + cc] = st[k][i][r];
+        }
   }
 }
 
@@ -908,12 +1140,12 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_grad_kernel(DeltaGradP
     float x[8];
     *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(at);
     *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(at + 4);
-    split_terms<S>(x, out);
+    split_values<S>(x, out);
   };
   auto dy_operand = [&](int rt, int m, bf8x* out) {
     const int t = 16 * rt + col, cc = 32 * m + 8 * g, n = t < len ? p.P - cc : 0;
     const Pack<TI> v = load_pack(dy + (n > 0 ? t * vstride + cc : 0), n);
-    if constexpr (Sh::kF32) split_terms<S>(v.v, out);
+    if constexpr (Sh::kF32) split_values<S>(v.v, out);
     else out[0] = __builtin_bit_cast(bf8x, v);
   };
   const int blocks = (p.P + 31) / 32;
@@ -1041,8 +1273,8 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_grad_kernel(DeltaGradP
 #pragma unroll
         for (int k = 0; k < 8; ++k) through = fmaf(x[k], y[k], through);
       }
-      split_terms<S>(x, hb);
-      split_terms<S>(y, ab);
+      split_values<S>(x, hb);
+      split_values<S>(y, ab);
       reads[i] = mma_terms<NT, S>(ay, hb, reads[i]);
       erased[i] = mma_terms<S, S>(av, hb, erased[i]);
       written[i] = mma_terms<S, S>(ao, ab, written[i]);
@@ -1095,9 +1327,9 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_grad_kernel(DeltaGradP
       both[i] = s == t ? 0.f : s < t ? -down : -row;
     }
     bf8x af[S], ae[S], at[S];
-    split_terms<S>(fd, af);
-    split_terms<S>(both, ae);
-    split_terms<S>(ft, at);
+    split_values<S>(fd, af);
+    split_values<S>(both, ae);
+    split_values<S>(ft, at);
 #pragma unroll
     for (int i = 0; i < HT; ++i) {
       bf8x bk[NT], bq[NT];
@@ -1162,14 +1394,19 @@ int delta_prep(const DeltaParams& p, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
+// Waves of a walk's workgroup and 16-column tiles of a wave.
+constexpr int kWalkWaves = 4, kWalkTiles = 1, kWalkCols = 16 * kWalkWaves * kWalkTiles;
+
 template <typename TI, int KT, bool LOOSE, int MODE>
 int delta_walk(const DeltaParams& p, hipStream_t s) {
-  constexpr size_t lds = DeltaLds<TI, KT, MODE>::kBytes;
+  constexpr int W = kWalkWaves, CT = kWalkTiles;
+  constexpr size_t lds = DeltaLds<TI, KT, MODE, kWalkCols>::kBytes;
   static_assert(lds <= 160 * 1024, "a CU's LDS");
-  allow_dynamic_lds(delta_walk_kernel<TI, KT, LOOSE, MODE>, lds);
-  hipLaunchKernelGGL((delta_walk_kernel<TI, KT, LOOSE, MODE>),
-                     dim3((unsigned)((int64_t)p.B * p.H * p.ctiles)), dim3(kDeltaThreads), lds, s,
-                     p);
+  const int tiles = p.ctiles + (MODE == kDeltaSeg || MODE == kDeltaSegOut ? (32 * KT + kWalkCols - 1) / kWalkCols : 0);
+  const int segs = MODE >= kDeltaSeg ? p.nseg - 1 : p.nseg;
+  allow_dynamic_lds(delta_walk_kernel<TI, KT, LOOSE, MODE, W, CT>, lds);
+  hipLaunchKernelGGL((delta_walk_kernel<TI, KT, LOOSE, MODE, W, CT>),
+                     dim3((unsigned)((int64_t)p.B * p.H * segs * tiles)), dim3(64 * W), lds, s, p);
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
@@ -1183,7 +1420,10 @@ int delta_grad(const DeltaGradParams& p, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
-enum DeltaPhase { kPhasePrep, kPhasePrepBack, kPhaseOut, kPhaseKeep, kPhaseBack };
+enum DeltaPhase {
+  kPhasePrep, kPhasePrepBack, kPhaseOut, kPhaseKeep, kPhaseBack, kPhaseSeg, kPhaseSegOut,
+  kPhaseSegBack
+};
 
 template <typename TI, int KT, bool LOOSE>
 int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
@@ -1194,7 +1434,10 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
       return p.out_bf16 ? delta_walk<TI, KT, LOOSE, kDeltaOut>(p, s)
                         : delta_walk<TI, KT, LOOSE, kDeltaOutF32>(p, s);
     case kPhaseKeep: return delta_walk<TI, KT, LOOSE, kDeltaKeep>(p, s);
-    default: return delta_walk<TI, KT, LOOSE, kDeltaBack>(p, s);
+    case kPhaseBack: return delta_walk<TI, KT, LOOSE, kDeltaBack>(p, s);
+    case kPhaseSeg: return delta_walk<TI, KT, LOOSE, kDeltaSeg>(p, s);
+    case kPhaseSegOut: return delta_walk<TI, KT, LOOSE, kDeltaSegOut>(p, s);
+    default: return delta_walk<TI, KT, LOOSE, kDeltaSegBack>(p, s);
   }
 }
 
@@ -1213,7 +1456,7 @@ SWIMBA_DELTA_DECL(delta_f32_128)
 
 #define SWIMBA_DELTA_DEFINE(name, TI, KT)                                           \
   int name(const DeltaParams& p, int phase, hipStream_t s) {                        \
-    return p.N % kPack != 0 ? delta_phase<TI, KT, true>(p, phase, s)                \
+    return p.N % kPack != 0 || p.P % kPack != 0 ? delta_phase<TI, KT, true>(p, phase, s) \
                             : delta_phase<TI, KT, false>(p, phase, s);              \
   }                                                                                 \
   int name##_grad(const DeltaGradParams& p, hipStream_t s) {                        \
