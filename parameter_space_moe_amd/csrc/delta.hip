@@ -37,10 +37,59 @@ int grads(const DeltaGradParams& p, bool f32, hipStream_t s) {
   return delta_bf16_256_grad(p, s);
 }
 
+int carry(const DeltaParams& p, bool back, hipStream_t s) {
+  if (p.N <= 32) return back ? delta_carry<1, true>(p, s) : delta_carry<1, false>(p, s);
+  if (p.N <= 64) return back ? delta_carry<2, true>(p, s) : delta_carry<2, false>(p, s);
+  if (p.N <= 128) return back ? delta_carry<4, true>(p, s) : delta_carry<4, false>(p, s);
+  return back ? delta_carry<8, true>(p, s) : delta_carry<8, false>(p, s);
+}
+
 int padded_rows(int N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 
-constexpr size_t kTriBytes = kDeltaTri * sizeof(float);
+constexpr size_t kTriBytes = kDeltaTri * sizeof(bf16_t);  // of a term
+// Terms of what a call computes: two where inputs and y are bf16.
+int terms_of(const swimba_delta_rule_args* a) {
+  return a->in_dtype == SWIMBA_BF16 && a->y_dtype == SWIMBA_BF16 ? 2 : kDeltaTerms;
+}
 constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
+
+// Segments of the walks.  A walk's chunks follow each other; where the independent ones leave
+// CUs idle, they are cut into segments, whose transitions and ends are made first (a state
+// pass over the state's columns and as many more as it has rows) and joined.  The
+// number is the one of the least time, in steps of a chunk: `slots` workgroups run at once, and
+// one that has a CU for itself takes 0.6 of the time of one that shares it (4.1 us against
+// 6.8 us per chunk of 128 keys); a state pass's step takes 0.6 of a walk's (no queries,
+// scores and results); a join takes half a step per segment.
+struct SegPlan {
+  int nseg = 1, seg_chunks = 1;
+};
+
+SegPlan plan_segments(int64_t walks, int64_t state_walks, int passes, int64_t nc, bool shared_cu,
+                      int dev) {
+  SegPlan best;
+  best.seg_chunks = (int)nc;
+  const double cus = device_cus(dev);
+  auto steps = [&](double wgs) {
+    if (wgs <= cus) return 0.6;
+    const double slots = shared_cu ? 2 * cus : cus, rounds = wgs / slots;
+    return (shared_cu ? 1.0 : 0.6) * (rounds < 1 ? 1.0 : (double)(int64_t)(rounds + 0.999));
+  };
+  double least = passes * nc * steps((double)walks);
+  for (int64_t n = 2; n <= 256 && 2 * n <= nc; ++n) {
+    const int64_t len = (nc + n - 1) / n;
+    if ((nc + len - 1) / len != n) continue;
+    const double t = passes * len * steps((double)(walks * n)) +
+                     0.6 * len * steps((double)(state_walks * (n - 1))) +
+                     (passes - 1) * 0.6 * len * steps((double)(walks * (n - 1))) +
+                     passes * (0.5 * n + 2.0);
+    if (t < least) {
+      least = t;
+      best.nseg = (int)n;
+      best.seg_chunks = (int)len;
+    }
+  }
+  return best;
+}
 
 int64_t chunks_of(const swimba_delta_rule_args* a) { return (a->L + kChunk - 1) / kChunk; }
 
@@ -57,11 +106,29 @@ size_t tiny_bytes(const swimba_delta_rule_args* a) {
 
 // Workspace of a forward call: per chunk and head the inverse, the scores and the gates.
 struct DeltaPlan {
-  size_t off_tri = 0, off_score = 0, off_gates = 0, off_tiny = 0, bytes = 0;
+  SegPlan seg;
+  size_t off_tri = 0, off_score = 0, off_gates = 0, off_tiny = 0, off_seg = 0, off_carry = 0,
+         bytes = 0;
 };
 
-DeltaPlan plan_delta(const swimba_delta_rule_args* a) {
+// A walk's workgroups, and those of a state pass with transitions.
+int64_t walks_of(const swimba_delta_rule_args* a) {
+  return (int64_t)a->B * a->H * ((a->P + kWalkCols - 1) / kWalkCols);
+}
+int64_t state_walks_of(const swimba_delta_rule_args* a) {
+  return (int64_t)a->B * a->H * ((a->P + kWalkCols - 1) / kWalkCols +
+                                 (padded_rows(a->N) + kWalkCols - 1) / kWalkCols);
+}
+size_t padded_columns(const swimba_delta_rule_args* a) {
+  return (size_t)(a->P + kWalkCols - 1) / kWalkCols * kWalkCols;
+}
+bool shares_cu(const swimba_delta_rule_args* a) {
+  return a->in_dtype == SWIMBA_BF16 && a->N <= 128;
+}
+
+DeltaPlan plan_delta(const swimba_delta_rule_args* a, int dev) {
   DeltaPlan r;
+  r.seg = plan_segments(walks_of(a), state_walks_of(a), 1, chunks_of(a), shares_cu(a), dev);
   const size_t units = (size_t)a->B * a->H * chunks_of(a);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -69,33 +136,39 @@ DeltaPlan plan_delta(const swimba_delta_rule_args* a) {
     o += align256(bytes);
     return at;
   };
-  r.off_tri = take(units * kTriBytes);
-  r.off_score = take(units * kTriBytes);
+  r.off_tri = take(units * terms_of(a) * kTriBytes);
+  r.off_score = take(units * terms_of(a) * kTriBytes);
   r.off_gates = take(units * kGateBytes);
   r.off_tiny = take(tiny_bytes(a));
+  const size_t N = padded_rows(a->N), segs = (size_t)a->B * a->H * (r.seg.nseg > 1 ? r.seg.nseg : 0);
+  r.off_seg = take(segs * N * padded_columns(a) * sizeof(float));
+  r.off_carry = take(segs * N * N * sizeof(float));
   r.bytes = o;
   return r;
 }
 
 // And of a backward call.
 struct DeltaGradPlan {
+  SegPlan seg;
+  size_t off_seg = 0, off_carry = 0;
   size_t off_tri = 0, off_tri_t = 0, off_score = 0, off_gates = 0, off_states = 0, off_adj = 0,
          off_o = 0, off_dv = 0, off_dq = 0, off_dk = 0, off_part = 0, off_tiny = 0, bytes = 0;
 };
 
-DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g) {
+DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g, int dev) {
   const swimba_delta_rule_args* a = &g->fwd;
   DeltaGradPlan r;
-  const size_t units = (size_t)a->B * a->H * chunks_of(a), Pp = (size_t)(a->P + kWalkCols - 1) / kWalkCols * kWalkCols;
+  r.seg = plan_segments(walks_of(a), state_walks_of(a), 2, chunks_of(a), shares_cu(a), dev);
+  const size_t units = (size_t)a->B * a->H * chunks_of(a), Pp = padded_columns(a);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o += align256(bytes);
     return at;
   };
-  r.off_tri = take(units * kTriBytes);
-  r.off_tri_t = take(units * kTriBytes);
-  r.off_score = take(units * kTriBytes);
+  r.off_tri = take(units * kDeltaTerms * kTriBytes);
+  r.off_tri_t = take(units * kDeltaTerms * kTriBytes);
+  r.off_score = take(units * kDeltaTerms * kTriBytes);
   r.off_gates = take(units * kGateBytes);
   r.off_states = take(units * padded_rows(a->N) * Pp * sizeof(float));
   r.off_adj = take(units * padded_rows(a->N) * Pp * sizeof(float));
@@ -107,6 +180,9 @@ DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g) {
   r.off_dk = take(rows);
   r.off_part = take(a->decay_form == SWIMBA_DECAY_HEAD ? units * sizeof(double) : 0);
   r.off_tiny = take(tiny_bytes(a));
+  const size_t N = padded_rows(a->N), segs = (size_t)a->B * a->H * (r.seg.nseg > 1 ? r.seg.nseg : 0);
+  r.off_seg = take(segs * N * Pp * sizeof(float));
+  r.off_carry = take(segs * N * N * sizeof(float));
   r.bytes = o;
   return r;
 }
@@ -128,6 +204,7 @@ DeltaParams base_params(const swimba_delta_rule_args* a, const void* q, const vo
   p.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
   p.nc = (int)chunks_of(a);
   p.ctiles = (a->P + kWalkCols - 1) / kWalkCols;
+  p.terms = kDeltaTerms;
   p.nseg = 1;
   p.seg_chunks = p.nc;
   p.Pp = kWalkCols * p.ctiles;
@@ -256,39 +333,58 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
 
 }  // namespace
 
-size_t delta_rule_bytes(const swimba_delta_rule_args* a) {
-  return a->B == 0 || a->L == 0 ? 0 : plan_delta(a).bytes;
+size_t delta_rule_bytes(const swimba_delta_rule_args* a, int dev) {
+  return a->B == 0 || a->L == 0 ? 0 : plan_delta(a, dev).bytes;
 }
 
-int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, hipStream_t s) {
+// A walk, from the first states of its segments if it has some: the state pass `pass`, the
+// join and the walk.
+int walk(const DeltaParams& p, bool f32, int pass, int which, bool back, hipStream_t s) {
+  int rc = SWIMBA_OK;
+  if (p.nseg > 1) {
+    rc = phase(p, f32, pass, s);
+    if (rc == SWIMBA_OK) rc = carry(p, back, s);
+  }
+  return rc == SWIMBA_OK ? phase(p, f32, which, s) : rc;
+}
+
+int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, int dev, hipStream_t s) {
   const int64_t states = (int64_t)a->B * a->H * a->N * a->P;
   if (a->B == 0 || a->L == 0)
     return a->h_final != nullptr ? copy_or_zero(a->h0, a->h_final, states, s) : SWIMBA_OK;
   const bool f32 = a->in_dtype == SWIMBA_F32;
-  const DeltaPlan r = plan_delta(a);
+  const DeltaPlan r = plan_delta(a, dev);
   unsigned char* slot = at<unsigned char>(ws, r.off_tiny);
   int rc = SWIMBA_OK;
   const void* q = whole_packs(a->q, key_elements(a), f32, slot, s, &rc);
   const void* k = whole_packs(a->k, key_elements(a), f32, slot + kTinySlot, s, &rc);
   const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
   DeltaParams p = base_params(a, q, k, v);
-  p.tri = at<float>(ws, r.off_tri);
-  p.score = at<float>(ws, r.off_score);
+  p.tri = at<bf16_t>(ws, r.off_tri);
+  p.score = at<bf16_t>(ws, r.off_score);
   p.gates = at<float>(ws, r.off_gates);
   p.out = a->y;
   p.out_bf16 = a->y_dtype == SWIMBA_BF16;
+  p.terms = terms_of(a);
   p.s0 = a->h0;
   p.s_final = a->h_final;
+  p.nseg = r.seg.nseg;
+  p.state_segs = p.nseg - 1;  // the last one's end is not carried on
+  p.seg_chunks = r.seg.seg_chunks;
+  p.seg_state = at<float>(ws, r.off_seg);
+  p.seg_carry = at<float>(ws, r.off_carry);
   if (rc == SWIMBA_OK) rc = phase(p, f32, kPhasePrep, s);
-  if (rc == SWIMBA_OK) rc = phase(p, f32, kPhaseOut, s);
+  if (rc == SWIMBA_OK)
+    rc = walk(p, f32, p.terms == 2 ? kPhaseSegOut : kPhaseSeg, kPhaseOut, false, s);
   return rc;
 }
 
-size_t delta_rule_backward_bytes(const swimba_delta_rule_grad_args* g) {
-  return g->fwd.B == 0 || g->fwd.L == 0 ? 0 : plan_delta_grad(g).bytes;
+size_t delta_rule_backward_bytes(const swimba_delta_rule_grad_args* g, int dev) {
+  return g->fwd.B == 0 || g->fwd.L == 0 ? 0 : plan_delta_grad(g, dev).bytes;
 }
 
-int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, hipStream_t s) {
+int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, int dev,
+                               hipStream_t s) {
   const swimba_delta_rule_args* a = &g->fwd;
   const int64_t states = (int64_t)a->B * a->H * a->N * a->P;
   if (a->B == 0 || a->L == 0) {
@@ -299,7 +395,7 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, h
     return rc;
   }
   const bool f32 = a->in_dtype == SWIMBA_F32, shared = a->H != a->G;
-  const DeltaGradPlan r = plan_delta_grad(g);
+  const DeltaGradPlan r = plan_delta_grad(g, dev);
   unsigned char* slot = at<unsigned char>(ws, r.off_tiny);
   int rc = SWIMBA_OK;
   const void* q = whole_packs(a->q, key_elements(a), f32, slot, s, &rc);
@@ -307,22 +403,29 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, h
   const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
   DeltaParams p = base_params(a, q, k, v);
   p.dy = whole_packs(g->dy, value_elements(a), f32, slot + 3 * kTinySlot, s, &rc);
-  p.tri = at<float>(ws, r.off_tri);
-  p.tri_t = at<float>(ws, r.off_tri_t);
-  p.score = at<float>(ws, r.off_score);
+  p.tri = at<bf16_t>(ws, r.off_tri);
+  p.tri_t = at<bf16_t>(ws, r.off_tri_t);
+  p.score = at<bf16_t>(ws, r.off_score);
   p.gates = at<float>(ws, r.off_gates);
   p.out = g->dv;
   p.out_bf16 = g->grad_dtype == SWIMBA_BF16;
   p.s0 = a->h0;
   p.states = at<float>(ws, r.off_states);
   p.rows = at<float>(ws, r.off_o);
+  p.nseg = r.seg.nseg;
+  p.state_segs = p.nseg - 1;  // the last one's end is not carried on
+  p.seg_chunks = r.seg.seg_chunks;
+  p.seg_state = at<float>(ws, r.off_seg);
+  p.seg_carry = at<float>(ws, r.off_carry);
+  p.state_segs = p.nseg;  // walking back, the last one's transition is the first to be passed
   if (rc == SWIMBA_OK) rc = phase(p, f32, kPhasePrepBack, s);
-  if (rc == SWIMBA_OK) rc = phase(p, f32, kPhaseKeep, s);
+  if (rc == SWIMBA_OK) rc = walk(p, f32, kPhaseSeg, kPhaseKeep, false, s);
   p.s0 = g->dh_final;
   p.s_final = g->dh0;
   p.states = at<float>(ws, r.off_adj);
   p.rows = at<float>(ws, r.off_dv);
-  if (rc == SWIMBA_OK) rc = phase(p, f32, kPhaseBack, s);
+  p.state_segs = p.nseg - 1;
+  if (rc == SWIMBA_OK) rc = walk(p, f32, kPhaseSegBack, kPhaseBack, true, s);
   if (rc != SWIMBA_OK) return rc;
 
   DeltaGradParams d = {};

@@ -49,11 +49,13 @@ struct DeltaParams {
   int nc;                 // chunks
   int ctiles;             // workgroups for the columns of a state
   int nseg, seg_chunks;   // segments of the walk, chunks in each
+  int state_segs;         // segments of a state pass
   float* seg_state;       // [B, H, nseg, N', P'] end states out (state pass), first states in
   float* seg_carry;       // [B, H, nseg, N', N'] the segments' transitions (state pass)
   // workspace, per (b, h, chunk)
-  float *tri, *tri_t;     // [kDeltaTri] T in operand order; its transpose (backward)
-  float* score;           // [kDeltaTri] S, or its transpose (backward)
+  bf16_t *tri, *tri_t;    // [terms, kDeltaTri] T in operand order; its transpose (backward)
+  bf16_t* score;          // [terms, kDeltaTri] S, or its transpose (backward)
+  int terms;
   float* gates;           // [kDeltaGates]
   const float* s0;        // first state or null, [B, H, N, P]
   float* s_final;         // or null
@@ -138,12 +140,6 @@ __device__ __forceinline__ void split_tiles(f4x lo, f4x hi, bf8x* out) {
   split_values<S>(x, out);
 }
 
-// Place of column `col` (a multiple of four) of a row in operand order.
-__device__ __forceinline__ int operand_place(int col) {
-  const int c = col & 31;
-  return (col & ~31) + (c < 16 ? 2 * c : 2 * (c - 16) + 4);
-}
-
 // First block of row tile rt of a triangle (tiles 0, 1: one block of 32, tiles 2, 3:
 // two), and of its transpose (tiles 0, 1: two blocks, tiles 2, 3: the second).
 __device__ __forceinline__ constexpr int tri_block(int rt, int b) {
@@ -158,8 +154,23 @@ struct DeltaShape {
   static constexpr bool kF32 = sizeof(TI) == 4;
   static constexpr int kTerms = kF32 ? kDeltaTerms : 1;
   static constexpr int kRows = 32 * KT;
-  static constexpr int kStride = kRows + 8;
+  static constexpr int kStride = kRows;
   static constexpr int kTile = kChunk * kStride;  // values of one term
+
+  // Where a row's values lie.  Slots of eight hold what a lane takes of a block of 32
+  // columns (4 g.. and 16 + 4 g..), and a row's slots are exchanged by an exclusive or
+  // with mix(row): 16 rows at one slot, and the 4 rows by 4 slots of a transposing read,
+  // are then 16 different slots of the 64 banks.
+  static __device__ __forceinline__ int mix(int row) {
+    if constexpr (KT >= 4) return ((row & 3) << 2) | ((row >> 2) & 3);
+    else if constexpr (KT == 2) return ((row & 2) << 1) | ((row >> 2) & 3);
+    else return (row >> 2) & 3;
+  }
+  static __device__ __forceinline__ int slot(int row, int n) { return 8 * (n ^ mix(row)); }
+  // Place of column `col` (a multiple of four).
+  static __device__ __forceinline__ int place(int row, int col) {
+    return row * kStride + slot(row, 4 * (col >> 5) + ((col & 15) >> 2)) + (col & 16) / 4;
+  }
 };
 
 constexpr int kDeltaThreads = 256, kDeltaWaves = 4;
@@ -171,22 +182,16 @@ struct DeltaRows {
   using Stage = RowStage<TI, 32 * KT, THREADS, LOOSE>;
   using Sh = DeltaShape<TI, KT>;
   static __device__ __forceinline__ void put(const Stage& st, int round, bf16_t* dst) {
-    if (!LOOSE && st.len == kChunk && st.cols >= Sh::kRows) put_as<true>(st, round, dst);
-    else put_as<false>(st, round, dst);
+#pragma unroll
+    for (int i = 0; i < Stage::kRound; ++i) put_one(st, round, i, dst);
   }
-  template <bool FULL>  // nothing to leave out
-  static __device__ __forceinline__ void put_as(const Stage& st, int round, bf16_t* dst) {
-#pragma unroll
-    for (int i = 0; i < Stage::kRound; ++i) {
+  static __device__ __forceinline__ void put_one(const Stage& st, int round, int i, bf16_t* dst) {
+    {
       u4x w[Stage::kQuads];
-      if constexpr (FULL) {
-#pragma unroll
-        for (int q = 0; q < Stage::kQuads; ++q) w[q] = st.v[i][q];
-      } else {
-        st.pack(round, i, w);
-      }
-      bf16_t* d = dst + st.row(round * Stage::kRound + i) * Sh::kStride +
-                  operand_place(st.column());
+      st.pack(round, i, w);
+      const int row = st.row(round * Stage::kRound + i);
+      bf16_t* d = dst + Sh::place(row, st.column());
+      bf16_t* d4 = dst + Sh::place(row, st.column() + 4);
       if constexpr (Sh::kF32) {
         float x[8];
         __builtin_memcpy(x, w, sizeof(x));
@@ -196,11 +201,11 @@ struct DeltaRows {
         for (int s = 0; s < Sh::kTerms; ++s) {
           struct { uint2 a, b; } o = __builtin_bit_cast(decltype(o), t[s]);
           *reinterpret_cast<uint2*>(d + s * Sh::kTile) = o.a;
-          *reinterpret_cast<uint2*>(d + s * Sh::kTile + 8) = o.b;
+          *reinterpret_cast<uint2*>(d4 + s * Sh::kTile) = o.b;
         }
       } else {
         *reinterpret_cast<uint2*>(d) = make_uint2(w[0][0], w[0][1]);
-        *reinterpret_cast<uint2*>(d + 8) = make_uint2(w[0][2], w[0][3]);
+        *reinterpret_cast<uint2*>(d4) = make_uint2(w[0][2], w[0][3]);
       }
     }
   }
@@ -232,8 +237,8 @@ __device__ __forceinline__ void row_operand(const bf16_t* tile, int row, int b, 
 #pragma unroll
   for (int s = 0; s < Sh::kTerms; ++s)
     out[s] = *reinterpret_cast<const bf8x*>(tile + s * Sh::kTile +
-                                            (row + (lane & 15)) * Sh::kStride + 32 * b +
-                                            8 * (lane >> 4));
+                                            (row + (lane & 15)) * Sh::kStride +
+                                            Sh::slot(lane & 15, 4 * b + (lane >> 4)));
 }
 
 // Operand of 16 columns (tile nt) by 32 rows (block b) of staged rows: the transposing
@@ -243,9 +248,9 @@ template <typename Sh>
 __device__ __forceinline__ void column_operand(const bf16_t* tile, int nt, int b, int lane,
                                                bf8x* out) {
   typedef __attribute__((address_space(3))) s4x* lds_s4;
-  const int i = lane & 15;
-  const bf16_t* p = tile + (32 * b + 4 * (lane >> 4) + (i >> 2)) * Sh::kStride + 32 * (nt >> 1) +
-                    8 * (i & 3) + 4 * (nt & 1);
+  const int i = lane & 15, row = 4 * (lane >> 4) + (i >> 2);
+  const bf16_t* p = tile + (32 * b + row) * Sh::kStride + Sh::slot(row, 4 * (nt >> 1) + (i & 3)) +
+                    4 * (nt & 1);
 #pragma unroll
   for (int s = 0; s < Sh::kTerms; ++s) {
     struct { s4x a, b; } r;
@@ -328,9 +333,9 @@ __device__ __forceinline__ void unit_inverse(const float* a, float* t, int lane,
 }
 
 // A lower triangle in LDS to the operand order of a product with it, or with its
-// transpose.  The triangle's 32-blocks are whole (zeros above).
+// transpose, in terms.  The triangle's 32-blocks are whole (zeros above).
 template <bool TRANSPOSED>
-__device__ __forceinline__ void put_triangle(const float* m, float* out, int tid) {
+__device__ __forceinline__ void put_triangle(const float* m, bf16_t* out, int terms, int tid) {
   for (int e = tid; e < kDeltaBlocks * 64; e += kDeltaThreads) {
     const int blk = e >> 6, lane = e & 63, g = lane >> 4;
     int rt, b;
@@ -357,9 +362,11 @@ __device__ __forceinline__ void put_triangle(const float* m, float* out, int tid
         x[4 * h + 3] = v.w;
       }
     }
-    float4* to = reinterpret_cast<float4*>(out + e * 8);
-    to[0] = make_float4(x[0], x[1], x[2], x[3]);
-    to[1] = make_float4(x[4], x[5], x[6], x[7]);
+    bf8x t[kDeltaTerms];
+    split_values<kDeltaTerms>(x, t);
+#pragma unroll
+    for (int s = 0; s < kDeltaTerms; ++s)
+      if (s < terms) *reinterpret_cast<bf8x*>(out + s * kDeltaTri + e * 8) = t[s];
   }
 }
 
@@ -502,10 +509,10 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
     }
   __syncthreads();
   unit_inverse(sA, sT, lane, wave);
-  const int64_t to = unit * kDeltaTri;
-  put_triangle<false>(sT, p.tri + to, tid);
-  if (BACK) put_triangle<true>(sT, p.tri_t + to, tid);
-  put_triangle<BACK>(sP, p.score + to, tid);
+  const int64_t to = unit * p.terms * kDeltaTri;
+  put_triangle<false>(sT, p.tri + to, p.terms, tid);
+  if (BACK) put_triangle<true>(sT, p.tri_t + to, p.terms, tid);
+  put_triangle<BACK>(sP, p.score + to, p.terms, tid);
 }
 
 // ---- the walk -------------------------------------------------------------------
@@ -547,31 +554,23 @@ __device__ __forceinline__ T& lane_at(T* base, int64_t i, uint32_t off) {
   return *reinterpret_cast<T*>(reinterpret_cast<char*>(base + i) + off);
 }
 
-// A triangle's values on their way to LDS, where they lie in terms.
+// The first TERMS terms of a triangle on their way to LDS.
 template <int TERMS, int THREADS>
 struct TriStage {
-  static constexpr int kAll = kDeltaTri / 8, kN = (kAll + THREADS - 1) / THREADS;
-  f4x v[kN][2];
-  __device__ __forceinline__ void load(const float* from, int tid) {
+  static constexpr int kAll = TERMS * kDeltaTri / 8, kN = (kAll + THREADS - 1) / THREADS;
+  u4x v[kN];
+  __device__ __forceinline__ void load(const bf16_t* from, int tid) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int e = i * THREADS + tid;
-      const f4x* at = reinterpret_cast<const f4x*>(from) + 2 * (e < kAll ? e : tid);
-      v[i][0] = at[0];
-      v[i][1] = at[1];
+      v[i] = reinterpret_cast<const u4x*>(from)[e < kAll ? e : tid];
     }
   }
   __device__ __forceinline__ void store(bf16_t* to, int tid) const {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int e = i * THREADS + tid;
-      bf8x t[TERMS];
-      split_tiles<TERMS>(v[i][0], v[i][1], t);
-      if (kAll % THREADS == 0 || e < kAll) {
-#pragma unroll
-        for (int s = 0; s < TERMS; ++s)
-          *reinterpret_cast<bf8x*>(to + s * kDeltaTri + e * 8) = t[s];
-      }
+      if (kAll % THREADS == 0 || e < kAll) reinterpret_cast<u4x*>(to)[e] = v[i];
     }
   }
 };
@@ -601,7 +600,7 @@ void delta_walk_kernel(DeltaParams p) {
   bf16_t* sK = reinterpret_cast<bf16_t*>(smem_raw);
   bf16_t* sQ = sK + NT * Sh::kTile;  // (QUERY)
   bf16_t* sT = sK + Lds::kRows;
-  bf16_t* sP = sT + S * kDeltaTri;   // (QUERY)
+  bf16_t* sS = sT + S * kDeltaTri;   // (QUERY)
   TI* sV = reinterpret_cast<TI*>(sT + Lds::kTris);
   float* sG = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(sV) + Lds::kVals);
 
@@ -617,7 +616,7 @@ void delta_walk_kernel(DeltaParams p) {
   const int all_tiles = CARRY ? p.ctiles + (32 * KT + COLS - 1) / COLS : p.ctiles;
   const int tile = blk % all_tiles;
   blk /= all_tiles;
-  const int segs = SEG ? p.nseg - 1 : p.nseg;  // the last one's end is not carried on
+  const int segs = SEG ? p.state_segs : p.nseg;
   const int seg = blk % segs;
   const int bh = blk / segs, b = bh / p.H, h = bh - b * p.H;
   const bool unit_state = CARRY && tile >= p.ctiles;
@@ -653,7 +652,7 @@ void delta_walk_kernel(DeltaParams p) {
         st[k][i][r] = v;
       }
 
-  constexpr bool kAhead = Rows::Stage::kRounds == 1;
+  static_assert(Rows::Stage::kRounds == 1, "rows in one round");
   typename Rows::Stage rk, rq;
   TriStage<S, THREADS> tri;
   TriStage<MODE == kDeltaOut ? 2 : S, THREADS> score;
@@ -669,10 +668,11 @@ void delta_walk_kernel(DeltaParams p) {
     rk.load(0);
     if (QUERY) {
       Rows::place(rq, p.q, p, b, grp, t0, len, tid);
-      if (kAhead) rq.load(0);
+      rq.load(0);
     }
-    tri.load((BACK ? p.tri_t : p.tri) + unit * kDeltaTri, tid);
-    if (QUERY) score.load(p.score + unit * kDeltaTri, tid);
+    const int64_t tris = unit * S * kDeltaTri;
+    tri.load((BACK ? p.tri_t : p.tri) + tris, tid);
+    if (QUERY) score.load(p.score + tris, tid);
 #pragma unroll
     for (int i = 0; i < kDeltaGates / THREADS; ++i)
       gate[i] = p.gates[unit * kDeltaGates + i * THREADS + tid];
@@ -734,22 +734,16 @@ void delta_walk_kernel(DeltaParams p) {
   for (int j = 0; j < nj; ++j) {
     const int cc = chunk_of(j), t0 = cc * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
     const int64_t unit = (int64_t)bh * p.nc + cc;
-    if (j > 0 && !kAhead) fetch(j);
     __syncthreads();  // everyone is done with the last chunk
     // tokens from the first bad one on leave the products
     const int bad = next_bad;
-    const int used = bad < len ? bad : len;
-    rk.len = used;
+    rk.len = rv.len = bad < len ? bad : len;
     Rows::all(rk, sK);
-    if (QUERY) {
-      if (!kAhead) rq.load(0);
-      Rows::all(rq, sQ);
-    }
+    if (QUERY) Rows::all(rq, sQ);
     tri.store(sT, tid);
-    if (QUERY) score.store(sP, tid);
+    if (QUERY) score.store(sS, tid);
 #pragma unroll
     for (int i = 0; i < kDeltaGates / THREADS; ++i) sG[i * THREADS + tid] = gate[i];
-    rv.len = used;
     rv.store(0, sV, Lds::kValStride);
     __syncthreads();
     // stores before the loads that the next chunk waits for, not behind them
@@ -764,7 +758,7 @@ void delta_walk_kernel(DeltaParams p) {
           for (int r = 0; r < 4; ++r)
             lane_at(to, (16 * i + r) * p.Pp + 16 * k, state_off) = st[k][i][r];
     }
-    if (kAhead && j + 1 < nj) fetch(j + 1);
+    if (j + 1 < nj) fetch(j + 1);
 
     // K h, and Q h, the next rows on their way
     f4x z[CT][4], y[CT][4];
@@ -920,7 +914,7 @@ void delta_walk_kernel(DeltaParams p) {
           bf8x ub[CT][YT];
 #pragma unroll
           for (int k = 0; k < CT; ++k) split_tiles<YT>(u[k][2 * m], u[k][2 * m + 1], ub[k]);
-          triangle(OfY(), OfY(), sP, m, ub, y);
+          triangle(OfY(), OfY(), sS, m, ub, y);
         }
       }
 #pragma unroll
@@ -963,7 +957,7 @@ void delta_walk_kernel(DeltaParams p) {
         bf8x db[CT][NT];
 #pragma unroll
         for (int k = 0; k < CT; ++k) split_tiles<NT>(vv[k][2 * m], vv[k][2 * m + 1], db[k]);
-        triangle(Three(), OfInput(), sP, m, db, z);
+        triangle(Three(), OfInput(), sS, m, db, z);
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -1283,7 +1277,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_grad_kernel(DeltaGradP
   through = wave_sum64(through);
   if (lane == 0) thru[wave] = through;
   auto element = [&](const bf16_t* tile, int t, int n) {
-    const bf16_t* at = tile + t * Sh::kStride + operand_place(n & ~3) + (n & 3);
+    const bf16_t* at = tile + Sh::place(t, n & ~3) + (n & 3);
     float v = to_f32(at[0]);
 #pragma unroll
     for (int s = 1; s < NT; ++s) v += to_f32(at[s * Sh::kTile]);
@@ -1403,7 +1397,7 @@ int delta_walk(const DeltaParams& p, hipStream_t s) {
   constexpr size_t lds = DeltaLds<TI, KT, MODE, kWalkCols>::kBytes;
   static_assert(lds <= 160 * 1024, "a CU's LDS");
   const int tiles = p.ctiles + (MODE == kDeltaSeg || MODE == kDeltaSegOut ? (32 * KT + kWalkCols - 1) / kWalkCols : 0);
-  const int segs = MODE >= kDeltaSeg ? p.nseg - 1 : p.nseg;
+  const int segs = MODE >= kDeltaSeg ? p.state_segs : p.nseg;
   allow_dynamic_lds(delta_walk_kernel<TI, KT, LOOSE, MODE, W, CT>, lds);
   hipLaunchKernelGGL((delta_walk_kernel<TI, KT, LOOSE, MODE, W, CT>),
                      dim3((unsigned)((int64_t)p.B * p.H * segs * tiles)), dim3(64 * W), lds, s, p);
@@ -1442,6 +1436,96 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
 }
 
 // One pair per dtype and padded row size.
+// First states of the segments, h(i + 1) = M_i h(i) + end(i), from the state pass's
+// transitions M (walking back: their transposes) and ends, in place.  Four waves take the
+// rows of 16 columns of one state in turn of 16-row tiles, in fp32 on the matrix units.
+template <int KT, bool BACK>
+__global__ __launch_bounds__(kDeltaThreads) void delta_carry_kernel(DeltaParams p) {
+  constexpr int N = 32 * KT, HT = 2 * KT, kMine = (HT + 3) / 4, kStride = N + 4;
+  __shared__ __attribute__((aligned(16))) float sH[2][16 * kStride];  // [column][row]
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int g = lane >> 4, col = lane & 15;
+  const int tiles = p.Pp / 16;
+  const int64_t bh = blockIdx.x / tiles;
+  const int c = (int)(blockIdx.x % tiles) * 16 + col;
+  auto put = [&](float* h, int i, f4x v) {
+    *reinterpret_cast<f4x*>(h + col * kStride + 16 * i + 4 * g) = v;
+  };
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int i = wave + 4 * k;
+    if (i >= HT) break;
+    f4x v = {0.f, 0.f, 0.f, 0.f};
+    if (p.s0 != nullptr) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = 16 * i + 4 * g + r;
+        if (c < p.P && n < p.N) v[r] = p.s0[(bh * p.N + n) * p.P + c];
+      }
+    }
+    put(sH[0], i, v);
+  }
+  for (int s = 0; s < p.nseg; ++s) {
+    const int64_t at = bh * p.nseg + s;
+    // the transition over the same tokens, made by the forward state pass
+    const float* m = p.seg_carry + (BACK ? bh * p.nseg + p.nseg - 1 - s : at) * N * N;
+    float* st = p.seg_state + at * N * p.Pp + c;
+    const float* h = sH[s & 1];
+    f4x end[kMine], a[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = wave + 4 * k;
+      if (i >= HT) break;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        end[k][r] = s + 1 < p.nseg ? st[(int64_t)(16 * i + 4 * g + r) * p.Pp] : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = wave + 4 * k;
+      if (i >= HT) break;
+      const f4x v = *reinterpret_cast<const f4x*>(h + col * kStride + 16 * i + 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) st[(int64_t)(16 * i + 4 * g + r) * p.Pp] = v[r];
+      a[k] = end[k];
+    }
+    if (s + 1 == p.nseg) break;
+#pragma unroll 4
+    for (int n = 0; n < HT; ++n) {
+      const f4x b = *reinterpret_cast<const f4x*>(h + col * kStride + 16 * n + 4 * g);
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        const int i = wave + 4 * k;
+        if (i >= HT) break;
+        f4x x;
+        if (BACK) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[r] = m[(16 * n + 4 * g + r) * N + 16 * i + col];
+        } else {
+          x = *reinterpret_cast<const f4x*>(m + (16 * i + col) * N + 16 * n + 4 * g);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[k] = mma16(x[r], b[r], a[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = wave + 4 * k;
+      if (i >= HT) break;
+      put(sH[(s + 1) & 1], i, a[k]);
+    }
+  }
+}
+
+template <int KT, bool BACK>
+int delta_carry(const DeltaParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((delta_carry_kernel<KT, BACK>),
+                     dim3((unsigned)((int64_t)p.B * p.H * (p.Pp / 16))), dim3(kDeltaThreads), 0, s,
+                     p);
+  return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
+}
+
 #define SWIMBA_DELTA_DECL(name)                                       \
   int name(const DeltaParams& p, int phase, hipStream_t s);           \
   int name##_grad(const DeltaGradParams& p, hipStream_t s);

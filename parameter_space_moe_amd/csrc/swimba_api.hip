@@ -794,7 +794,7 @@ int swimba_linear_attention_step(const swimba_linear_attention_step_args* a, hip
 }
 
 size_t swimba_delta_rule_workspace_size(const swimba_delta_rule_args* a) {
-  return validate_delta(a) == SWIMBA_OK ? delta_rule_bytes(a) : 0;
+  return validate_delta(a) == SWIMBA_OK ? delta_rule_bytes(a, -1) : 0;
 }
 
 int swimba_delta_rule(const swimba_delta_rule_args* a, void* ws, size_t ws_bytes,
@@ -805,12 +805,13 @@ int swimba_delta_rule(const swimba_delta_rule_args* a, void* ws, size_t ws_bytes
   if (rc != SWIMBA_OK) return rc;
   if (a->B > 0 && a->L > 0 && (a->y == nullptr || !aligned_as(a->y, a->y_dtype)))
     return SWIMBA_EINVAL;
-  if (!workspace_ok(ws, ws_bytes, delta_rule_bytes(a))) return SWIMBA_EWORKSPACE;
-  return launch_delta_rule(a, ws, stream);
+  const int dev = stream_device(stream);
+  if (!workspace_ok(ws, ws_bytes, delta_rule_bytes(a, dev))) return SWIMBA_EWORKSPACE;
+  return launch_delta_rule(a, ws, dev, stream);
 }
 
 size_t swimba_delta_rule_backward_workspace_size(const swimba_delta_rule_grad_args* g) {
-  return validate_delta_grad(g) == SWIMBA_OK ? delta_rule_backward_bytes(g) : 0;
+  return validate_delta_grad(g) == SWIMBA_OK ? delta_rule_backward_bytes(g, -1) : 0;
 }
 
 int swimba_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, size_t ws_bytes,
@@ -828,8 +829,9 @@ int swimba_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, s
               !aligned_as(g->dq, g->grad_dtype) || !aligned_as(g->dk, g->grad_dtype) ||
               !aligned_as(g->dv, g->grad_dtype)))
     return SWIMBA_EINVAL;
-  if (!workspace_ok(ws, ws_bytes, delta_rule_backward_bytes(g))) return SWIMBA_EWORKSPACE;
-  return launch_delta_rule_backward(g, ws, stream);
+  const int dev = stream_device(stream);
+  if (!workspace_ok(ws, ws_bytes, delta_rule_backward_bytes(g, dev))) return SWIMBA_EWORKSPACE;
+  return launch_delta_rule_backward(g, ws, dev, stream);
 }
 
 int swimba_delta_rule_step(const swimba_delta_rule_step_args* a, hipStream_t stream) {

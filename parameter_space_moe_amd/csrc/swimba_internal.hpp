@@ -114,10 +114,11 @@ int sum_shared_heads(const float* rows, void* out, swimba_dtype d, int64_t n, in
                      hipStream_t s);
 int sum_decay_parts(const double* part, float* dg, int B, int H, int nc, hipStream_t s);
 // Delta rule (delta.hip) and norms of queries and keys (norm_rotate.hip).
-size_t delta_rule_bytes(const swimba_delta_rule_args* a);
-int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, hipStream_t s);
-size_t delta_rule_backward_bytes(const swimba_delta_rule_grad_args* g);
-int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, hipStream_t s);
+size_t delta_rule_bytes(const swimba_delta_rule_args* a, int dev);
+int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, int dev, hipStream_t s);
+size_t delta_rule_backward_bytes(const swimba_delta_rule_grad_args* g, int dev);
+int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, int dev,
+                               hipStream_t s);
 int launch_delta_rule_step(const swimba_delta_rule_step_args* a, int dev, hipStream_t s);
 int launch_norm_rotate(const swimba_norm_rotate_args* a, int dev, hipStream_t s);
 size_t norm_rotate_backward_bytes(const swimba_norm_rotate_grad_args* g, int dev);
