@@ -204,7 +204,6 @@ DeltaParams base_params(const swimba_delta_rule_args* a, const void* q, const vo
   p.token_decay = a->decay_form == SWIMBA_DECAY_TOKEN;
   p.nc = (int)chunks_of(a);
   p.ctiles = (a->P + kWalkCols - 1) / kWalkCols;
-  p.terms = kDeltaTerms;
   p.nseg = 1;
   p.seg_chunks = p.nc;
   p.Pp = kWalkCols * p.ctiles;
@@ -365,7 +364,6 @@ int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, int dev, hipStr
   p.gates = at<float>(ws, r.off_gates);
   p.out = a->y;
   p.out_bf16 = a->y_dtype == SWIMBA_BF16;
-  p.terms = terms_of(a);
   p.s0 = a->h0;
   p.s_final = a->h_final;
   p.nseg = r.seg.nseg;
@@ -375,7 +373,7 @@ int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, int dev, hipStr
   p.seg_carry = at<float>(ws, r.off_carry);
   if (rc == SWIMBA_OK) rc = phase(p, f32, kPhasePrep, s);
   if (rc == SWIMBA_OK)
-    rc = walk(p, f32, p.terms == 2 ? kPhaseSegOut : kPhaseSeg, kPhaseOut, false, s);
+    rc = walk(p, f32, terms_of(a) == 2 ? kPhaseSegOut : kPhaseSeg, kPhaseOut, false, s);
   return rc;
 }
 

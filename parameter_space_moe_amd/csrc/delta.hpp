@@ -55,7 +55,6 @@ struct DeltaParams {
   // workspace, per (b, h, chunk)
   bf16_t *tri, *tri_t;    // [terms, kDeltaTri] T in operand order; its transpose (backward)
   bf16_t* score;          // [terms, kDeltaTri] S, or its transpose (backward)
-  int terms;
   float* gates;           // [kDeltaGates]
   const float* s0;        // first state or null, [B, H, N, P]
   float* s_final;         // or null
@@ -264,255 +263,251 @@ __device__ __forceinline__ void column_operand(const bf16_t* tile, int nt, int b
 
 constexpr int kTriStride = kChunk + 4;
 
-// (I + A)^-1 of the strictly lower triangular 64 x 64 matrix in `a` (rows kTriStride
-// apart), into `t`, in fp32: the four 16 x 16 blocks on the diagonal by substitution, a lane per
-// column, then the blocks below them a block column per wave,
-//   T_ij = -T_ii sum_k A_ik T_kj,
-// where a product's result is register for register the next one's right operand.
-// Called by the workgroup; ends with a barrier.
-__device__ __forceinline__ void unit_inverse(const float* a, float* t, int lane, int wave) {
-  const int g = lane >> 4, col = lane & 15;
-  if (wave == 0) {
-    const float* d = a + 16 * g * kTriStride + 16 * g;
-    float x[16];
+// Blocks of a triangle whose row tile `rt` a wave holds, tile by tile (zero beyond the diagonal),
+// in operand order and in TERMS terms.
+template <int TERMS, bool TRANSPOSED>
+__device__ __forceinline__ void put_tiles(const f4x* tiles, int rt, bf16_t* out, int lane) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float s = i == col ? 1.f : 0.f;
+  for (int b = 0; b < 2; ++b) {
+    if (TRANSPOSED ? b < rt / 2 : b > rt / 2) continue;
+    bf8x t[TERMS];
+    split_tiles<TERMS>(tiles[2 * b], tiles[2 * b + 1], t);
+    const int blk = TRANSPOSED ? tri_block_t(rt, b) : tri_block(rt, b);
 #pragma unroll
-      for (int k = 0; k < i; k += 4) {
-        const float4 r = *reinterpret_cast<const float4*>(d + i * kTriStride + k);
-        s = fmaf(-r.x, x[k], s);
-        if (k + 1 < i) s = fmaf(-r.y, x[k + 1], s);
-        if (k + 2 < i) s = fmaf(-r.z, x[k + 2], s);
-        if (k + 3 < i) s = fmaf(-r.w, x[k + 3], s);
-      }
-      x[i] = s;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t[(16 * g + i) * kTriStride + 16 * g + col] = x[i];
+    for (int s = 0; s < TERMS; ++s)
+      *reinterpret_cast<bf8x*>(out + s * kDeltaTri + (blk * 64 + lane) * 8) = t[s];
   }
-  __syncthreads();
-  if (wave < 3) {
-    f4x tk[4];
+}
+
+constexpr int kDiagStride = 20;
+
+// T = (I + A)^-1 of a strictly lower triangular A of 64 x 64, in fp32; `at` holds A^T, its rows
+// kTriStride apart.  The four blocks of 16 x 16 on the diagonal by substitution in one
+// wave, a lane per row of T: T[i][k] = [i = k] - sum_{m > k} T[i][m] A[m][k], transposed
+// into `diag`.
+__device__ __forceinline__ void unit_blocks(const float* at, float* diag, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  const float* a = at + 16 * g * kTriStride + 16 * g;
+  float x[16];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      tk[0][r] = t[(16 * wave + 4 * g + r) * kTriStride + 16 * wave + col];
+  for (int k = 15; k >= 0; --k) {
+    float s = i == k ? 1.f : 0.f;
 #pragma unroll
-    for (int n = 1; n < 4; ++n) {  // block row wave + n
-      if (wave + n > 3) break;
-      const int i = wave + n;
+    for (int m = k / 4 * 4; m < 16; m += 4) {
+      const float4 r = *reinterpret_cast<const float4*>(a + k * kTriStride + m);
+      if (m > k) s = fmaf(-r.x, x[m], s);
+      if (m + 1 > k) s = fmaf(-r.y, x[m + 1], s);
+      if (m + 2 > k) s = fmaf(-r.z, x[m + 2], s);
+      if (m + 3 > k) s = fmaf(-r.w, x[m + 3], s);
+    }
+    x[k] = s;
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) diag[(16 * g + k) * kDiagStride + i] = x[k];
+}
+
+// The tiles of block row `row` of T, transposed: x[j] = T_row,j^T, by
+//   T_ij = -(sum_{j < k <= i} T_ik A_kj) T_jj,
+// where a product's result is register for register the next one's right operand.
+__device__ __forceinline__ void unit_row(const float* at, const float* diag, int row, int lane,
+                                         f4x* x) {
+  const int g = lane >> 4, col = lane & 15;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = f4x{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i != row) continue;  // (uniform)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[i][r] = diag[(16 * i + 4 * g + r) * kDiagStride + col];
+#pragma unroll
+    for (int j = 2; j >= 0; --j) {
+      if (j >= i) continue;
       f4x s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < n; ++k) {
-        const float4 r = *reinterpret_cast<const float4*>(a + (16 * i + col) * kTriStride +
-                                                          16 * (wave + k) + 4 * g);
-        s = mma16(r.x, tk[k][0], s);
-        s = mma16(r.y, tk[k][1], s);
-        s = mma16(r.z, tk[k][2], s);
-        s = mma16(r.w, tk[k][3], s);
+      for (int k = 3; k >= 1; --k) {
+        if (k > i || k <= j) continue;
+        const f4x a = *reinterpret_cast<const f4x*>(at + (16 * j + col) * kTriStride + 16 * k +
+                                                    4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s = mma16(a[r], x[k][r], s);
       }
-      const float4 r =
-          *reinterpret_cast<const float4*>(t + (16 * i + col) * kTriStride + 16 * i + 4 * g);
-      f4x o = {0.f, 0.f, 0.f, 0.f};
-      o = mma16(-r.x, s[0], o);
-      o = mma16(-r.y, s[1], o);
-      o = mma16(-r.z, s[2], o);
-      o = mma16(-r.w, s[3], o);
-      tk[n] = o;
+      const f4x d = *reinterpret_cast<const f4x*>(diag + (16 * j + col) * kDiagStride + 4 * g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        t[(16 * i + 4 * g + e) * kTriStride + 16 * wave + col] = o[e];
+      for (int r = 0; r < 4; ++r) x[j] = mma16(-d[r], s[r], x[j]);
     }
-  }
-  // blocks above the diagonal that share a 32-block with one below
-  for (int e = threadIdx.x; e < 2 * 256; e += kDeltaThreads) {
-    const int r = (e >> 8) * 32 + ((e >> 4) & 15), c = (e >> 8) * 32 + 16 + (e & 15);
-    t[r * kTriStride + c] = 0.f;
-  }
-  __syncthreads();
-}
-
-// A lower triangle in LDS to the operand order of a product with it, or with its
-// transpose, in terms.  The triangle's 32-blocks are whole (zeros above).
-template <bool TRANSPOSED>
-__device__ __forceinline__ void put_triangle(const float* m, bf16_t* out, int terms, int tid) {
-  for (int e = tid; e < kDeltaBlocks * 64; e += kDeltaThreads) {
-    const int blk = e >> 6, lane = e & 63, g = lane >> 4;
-    int rt, b;
-    if (TRANSPOSED) {
-      rt = blk < 4 ? blk >> 1 : blk - 2;
-      b = blk < 4 ? blk & 1 : 1;
-    } else {
-      rt = blk < 2 ? blk : 2 + ((blk - 2) >> 1);
-      b = blk < 2 ? 0 : (blk - 2) & 1;
-    }
-    const int row = 16 * rt + (lane & 15);
-    float x[8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = 32 * b + 16 * h + 4 * g;
-      if (TRANSPOSED) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 * h + i] = m[(c + i) * kTriStride + row];
-      } else {
-        const float4 v = *reinterpret_cast<const float4*>(m + row * kTriStride + c);
-        x[4 * h] = v.x;
-        x[4 * h + 1] = v.y;
-        x[4 * h + 2] = v.z;
-        x[4 * h + 3] = v.w;
-      }
-    }
-    bf8x t[kDeltaTerms];
-    split_values<kDeltaTerms>(x, t);
-#pragma unroll
-    for (int s = 0; s < kDeltaTerms; ++s)
-      if (s < terms) *reinterpret_cast<bf8x*>(out + s * kDeltaTri + e * 8) = t[s];
   }
 }
 
-// First token of a chunk whose k, beta or decay is not finite, kChunk without one: it and
-// those behind it leave the products, and the walk makes what it reaches NaN.
 __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < __builtin_inff()); }
 
 template <typename TI, int KT>
-constexpr size_t delta_prep_lds() {
+constexpr size_t delta_prep_lds(bool back) {
   using Sh = DeltaShape<TI, KT>;
   const size_t rows = 2 * (size_t)Sh::kTerms * Sh::kTile * sizeof(bf16_t);
-  const size_t tris = 2 * (size_t)kChunk * kTriStride * sizeof(float);
-  return (rows > tris ? rows : tris) + (size_t)kChunk * kTriStride * sizeof(float) +
-         4 * kChunk * sizeof(float);
+  const size_t tris = ((back ? 2 : 1) * (size_t)kChunk * kTriStride + kChunk * kDiagStride) *
+                      sizeof(float);
+  return (rows > tris ? rows : tris) + 4 * kChunk * sizeof(float);
 }
 
-// One workgroup per chunk and head.  BACK: for the gradients.
-template <typename TI, int KT, bool LOOSE, bool BACK>
+// One workgroup per chunk and head.  Tokens from the first one on whose k, beta or decay is not
+// finite leave the products, and the walk makes what it reaches NaN.  Wave w holds column
+// tile w of the scores K K^T, which go to LDS for the inverse, and of K Q^T (BACK: Q K^T),
+// whose accumulators are the triangle's operand register for register; while wave 0 inverts
+// the blocks on the diagonal the others write theirs.  BACK: for the gradients, S
+// transposed and T both ways.
+template <typename TI, int KT, bool LOOSE, bool BACK, int TERMS>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p) {
   using Sh = DeltaShape<TI, KT>;
   using Rows = DeltaRows<TI, KT, LOOSE>;
+  constexpr int NT = Sh::kTerms;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
-  float* sA = reinterpret_cast<float*>(smem_raw);
-  float* sG = sA + kChunk * kTriStride;  // high and low parts of G, beta
-  bf16_t* sK = reinterpret_cast<bf16_t*>(sG + 4 * kChunk);
-  bf16_t* sQ = sK + Sh::kTerms * Sh::kTile;
-  float* sT = reinterpret_cast<float*>(sK);  // once the rows are done with
-  float* sP = sT + kChunk * kTriStride;
+  float* sG = reinterpret_cast<float*>(smem_raw);  // high and low parts of G, beta
   int* bad = reinterpret_cast<int*>(sG + 3 * kChunk);
+  bf16_t* sK = reinterpret_cast<bf16_t*>(sG + 4 * kChunk);
+  bf16_t* sQ = sK + NT * Sh::kTile;
+  float* sA = reinterpret_cast<float*>(sK);  // once the rows are done with: A^T
+  float* sD = sA + kChunk * kTriStride;
+  float* sT = sD + kChunk * kDiagStride;     // (BACK) T^T
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int g = lane >> 4, col = lane & 15;
   const int64_t unit = blockIdx.x;
-  const int c = (int)(unit % p.nc);
-  const int64_t bh = unit / p.nc;
-  const int b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
+  const int bh = (int)blockIdx.x / p.nc, c = (int)blockIdx.x - bh * p.nc;
+  const int b = bh / p.H, h = bh - b * p.H;
   const int t0 = c * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
 
   typename Rows::Stage rk, rq;
   Rows::place(rk, p.k, p, b, h / (p.H / p.G), t0, len, tid);
   Rows::place(rq, p.q, p, b, h / (p.H / p.G), t0, len, tid);
   rk.load(0);
+  rq.load(0);
   if (tid == 0) *bad = kChunk;
+  float gt = 0.f, bt = 0.f;
+  if (wave == 0 && lane < len) {
+    const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
+    gt = p.token_decay ? p.g[at] : p.g[h];
+    bt = p.beta[at];
+  }
   __syncthreads();
   if (wave == 0) {
-    const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
-    float gt = 0.f, bt = 0.f;
-    if (lane < len) {
-      gt = p.token_decay ? p.g[at] : p.g[h];
-      bt = p.beta[at];
-    }
     if (not_finite(bt) || !(gt < __builtin_inff())) atomicMin(bad, lane);
     if (!(gt < __builtin_inff())) gt = 0.f;
     const double d = (double)gt * 1.4426950408889634;
     const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
     const double end = last_lane(sum);
     const float hi = (float)sum;
+    bt = not_finite(bt) ? 0.f : bt;
     sG[lane] = hi;
     sG[kChunk + lane] = (float)(sum - (double)hi);
-    sG[2 * kChunk + lane] = not_finite(bt) ? 0.f : bt;
+    sG[2 * kChunk + lane] = bt;
     float* gates = p.gates + unit * kDeltaGates;
     gates[lane] = exp2_sum(sum);
     gates[kChunk + lane] = exp2_sum(end - sum);
-    gates[2 * kChunk + lane] = not_finite(bt) ? 0.f : bt;
+    gates[2 * kChunk + lane] = bt;
     if (lane == 0) gates[3 * kChunk] = exp2_sum(end);
   }
+  static_assert(Rows::Stage::kRounds == 1, "rows in one round");
+  if (rk.wild()) {
+    for (int i = 0; i < Rows::Stage::kRound; ++i) {
+      u4x w[Rows::Stage::kQuads];
+      rk.pack(0, i, w);
+      TI e[kPack];
+      __builtin_memcpy(e, w, sizeof(e));
+      bool wild = false;
 #pragma unroll
-  for (int r = 0; r < Rows::Stage::kRounds; ++r) {
-    if (r > 0) rk.load(r);
-    if (rk.wild()) {
-      for (int i = 0; i < Rows::Stage::kRound; ++i) {
-        u4x w[Rows::Stage::kQuads];
-        rk.pack(r, i, w);
-        TI e[kPack];
-        __builtin_memcpy(e, w, sizeof(e));
-        bool wild = false;
-#pragma unroll
-        for (int n = 0; n < kPack; ++n) wild |= not_finite(to_f32(e[n]));
-        if (wild) atomicMin(bad, rk.row(r * Rows::Stage::kRound + i));
-      }
+      for (int n = 0; n < kPack; ++n) wild |= not_finite(to_f32(e[n]));
+      if (wild) atomicMin(bad, rk.row(i));
     }
-    Rows::put(rk, r, sK);
   }
-  rq.load(0);
+  Rows::all(rk, sK);
   Rows::all(rq, sQ);
   __syncthreads();
   const int first_bad = *bad;
   if (first_bad < kChunk) {
     for (int e = tid; e < (kChunk - first_bad) * Sh::kStride; e += kDeltaThreads) {
 #pragma unroll
-      for (int s = 0; s < Sh::kTerms; ++s)
-        sK[s * Sh::kTile + first_bad * Sh::kStride + e] = 0;
+      for (int s = 0; s < NT; ++s) sK[s * Sh::kTile + first_bad * Sh::kStride + e] = 0;
     }
     __syncthreads();
   }
   if (tid == 0) p.gates[unit * kDeltaGates + 3 * kChunk + 1] = __int_as_float(first_bad);
 
-  // wave w: rows of tile w against the keys before them, and queries of tile 3 - w
   f4x kk[4], qk[4];
-  const int rk_t = wave, rq_t = 3 - wave;
 #pragma unroll
-  for (int ct = 0; ct < 4; ++ct) {
-    kk[ct] = f4x{0.f, 0.f, 0.f, 0.f};
-    qk[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+  for (int rt = 0; rt < 4; ++rt) {
+    kk[rt] = f4x{0.f, 0.f, 0.f, 0.f};
+    qk[rt] = f4x{0.f, 0.f, 0.f, 0.f};
   }
 #pragma unroll
   for (int n = 0; n < KT; ++n) {
-    bf8x ak[Sh::kTerms], aq[Sh::kTerms];
-    row_operand<Sh>(sK, 16 * rk_t, n, lane, ak);
-    row_operand<Sh>(sQ, 16 * rq_t, n, lane, aq);
+    bf8x bk[NT], bq[NT];
+    row_operand<Sh>(sK, 16 * wave, n, lane, bk);
+    if (!BACK) row_operand<Sh>(sQ, 16 * wave, n, lane, bq);
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-      if (ct > rk_t && ct > rq_t) continue;
-      bf8x bk[Sh::kTerms];
-      row_operand<Sh>(sK, 16 * ct, n, lane, bk);
-      if (ct <= rk_t) kk[ct] = mma_terms<Sh::kTerms, Sh::kTerms>(ak, bk, kk[ct]);
-      if (ct <= rq_t) qk[ct] = mma_terms<Sh::kTerms, Sh::kTerms>(aq, bk, qk[ct]);
+    for (int rt = 0; rt < 4; ++rt) {
+      bf8x a[NT];
+      if (rt <= wave) {
+        row_operand<Sh>(sK, 16 * rt, n, lane, a);
+        kk[rt] = mma_terms<NT, NT>(a, bk, kk[rt]);
+        if (!BACK) qk[rt] = mma_terms<NT, NT>(a, bq, qk[rt]);
+      }
+      if (BACK && rt >= wave) {
+        row_operand<Sh>(sQ, 16 * rt, n, lane, a);
+        qk[rt] = mma_terms<NT, NT>(a, bk, qk[rt]);
+      }
     }
   }
-  auto decay = [&](int t, int s) {
-    return hw_exp2((sG[t] - sG[s]) + (sG[kChunk + t] - sG[kChunk + s]));
-  };
+  // decays: this lane's column, and four rows per tile
+  const int mine = 16 * wave + col;
+  const float hi = sG[mine], lo = sG[kChunk + mine];
 #pragma unroll
-  for (int ct = 0; ct < 4; ++ct) {
-    const int s = 16 * ct + col;
+  for (int rt = 0; rt < 4; ++rt) {
+    const int row = 16 * rt + 4 * g;
+    const f4x rh = *reinterpret_cast<const f4x*>(sG + row);
+    const f4x rl = *reinterpret_cast<const f4x*>(sG + kChunk + row);
+    const f4x rb = *reinterpret_cast<const f4x*>(sG + 2 * kChunk + row);
+    if (rt <= wave) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int tk = 16 * rk_t + 4 * g + r, tq = 16 * rq_t + 4 * g + r;
-      kk[ct][r] = s < tk ? kk[ct][r] * decay(tk, s) * sG[2 * kChunk + s] : 0.f;
-      qk[ct][r] = s <= tq ? qk[ct][r] * decay(tq, s) : 0.f;
+      for (int r = 0; r < 4; ++r) {
+        const float d = hw_exp2((hi - rh[r]) + (lo - rl[r]));
+        kk[rt][r] = row + r < mine ? kk[rt][r] * d * rb[r] : 0.f;
+        if (!BACK) qk[rt][r] = row + r <= mine ? qk[rt][r] * d : 0.f;
+      }
+    }
+    if (BACK && rt >= wave) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        qk[rt][r] = row + r >= mine ? qk[rt][r] * hw_exp2((rh[r] - hi) + (rl[r] - lo)) : 0.f;
     }
   }
   __syncthreads();  // the rows are done with
 #pragma unroll
-  for (int ct = 0; ct < 4; ++ct)
+  for (int rt = 0; rt < 4; ++rt) {
+    if (rt > wave) continue;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      sA[(16 * rk_t + 4 * g + r) * kTriStride + 16 * ct + col] = kk[ct][r];
-      sP[(16 * rq_t + 4 * g + r) * kTriStride + 16 * ct + col] = qk[ct][r];
-    }
+    for (int r = 0; r < 4; ++r) sA[(16 * rt + 4 * g + r) * kTriStride + mine] = kk[rt][r];
+  }
   __syncthreads();
-  unit_inverse(sA, sT, lane, wave);
-  const int64_t to = unit * p.terms * kDeltaTri;
-  put_triangle<false>(sT, p.tri + to, p.terms, tid);
-  if (BACK) put_triangle<true>(sT, p.tri_t + to, p.terms, tid);
-  put_triangle<BACK>(sP, p.score + to, p.terms, tid);
+  const int64_t to = unit * TERMS * kDeltaTri;
+  if (wave == 0) unit_blocks(sA, sD, lane);
+  put_tiles<TERMS, BACK>(qk, wave, p.score + to, lane);
+  __syncthreads();
+  f4x x[4];
+  unit_row(sA, sD, wave, lane, x);
+  put_tiles<TERMS, false>(x, wave, p.tri + to, lane);
+  if constexpr (BACK) {
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sT[(16 * rt + 4 * g + r) * kTriStride + mine] = x[rt][r];
+    __syncthreads();
+    // rows of T^T: tile `wave`, columns 32 b + 4 g.., + 16
+    f4x t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      t[i] = *reinterpret_cast<const f4x*>(sT + mine * kTriStride + 16 * i + 4 * g);
+    put_tiles<TERMS, true>(t, wave, p.tri_t + to, lane);
+  }
 }
 
 // ---- the walk -------------------------------------------------------------------
@@ -576,14 +571,15 @@ struct TriStage {
 };
 
 // Two workgroups of four waves share a CU where LDS and 256 registers suffice.
-template <typename TI, int KT>
+template <typename TI, int KT, int MODE>
 constexpr int delta_waves_per_simd() {
-  return sizeof(TI) == 2 && KT <= 4 ? 2 : 1;
+  if (sizeof(TI) == 4 || KT > 4) return 1;
+  return MODE == kDeltaSegOut ? 3 : 2;
 }
 
 template <typename TI, int KT, bool LOOSE, int MODE, int W, int CT>
 __global__ __launch_bounds__(64 * W) __attribute__((
-    amdgpu_waves_per_eu(delta_waves_per_simd<TI, KT>(), delta_waves_per_simd<TI, KT>())))
+    amdgpu_waves_per_eu(delta_waves_per_simd<TI, KT, MODE>(), delta_waves_per_simd<TI, KT, MODE>())))
 void delta_walk_kernel(DeltaParams p) {
   constexpr int THREADS = 64 * W, COLS = 16 * W * CT;
   using Sh = DeltaShape<TI, KT>;
@@ -770,30 +766,32 @@ void delta_walk_kernel(DeltaParams p) {
         y[k][t] = f4x{0.f, 0.f, 0.f, 0.f};
       }
     {
-      bf8x ak[2][4][NT], aq[2][4][QT];
+      constexpr int kSets = CARRY ? 1 : 2;  // a state pass has three waves to wait for each other
+      bf8x ak[kSets][4][NT], aq[kSets][4][QT];
       auto rows = [&](int n) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          row_operand<Sh>(sK, 16 * t, n, lane, ak[n & 1][t]);
+          row_operand<Sh>(sK, 16 * t, n, lane, ak[n % kSets][t]);
           if (OUT) {
             bf8x a[NT];
             row_operand<Sh>(sQ, 16 * t, n, lane, a);
 #pragma unroll
-            for (int i = 0; i < QT; ++i) aq[n & 1][t][i] = a[i];
+            for (int i = 0; i < QT; ++i) aq[n % kSets][t][i] = a[i];
           }
         }
       };
-      rows(0);
+      if (kSets == 2) rows(0);
 #pragma unroll
       for (int n = 0; n < KT; ++n) {
         bf8x hb[CT][S];
 #pragma unroll
         for (int k = 0; k < CT; ++k) split_tiles<S>(st[k][2 * n], st[k][2 * n + 1], hb[k]);
-        if (n + 1 < KT) rows(n + 1);
+        if (kSets == 1) rows(n);
+        else if (n + 1 < KT) rows(n + 1);
 #pragma unroll
         for (int k = 0; k < CT; ++k) {
-          mma_tiles<NT, S, 4>(ak[n & 1], hb[k], z[k]);
-          if (OUT) mma_tiles<QT, YT, 4>(aq[n & 1], hb[k], y[k]);
+          mma_tiles<NT, S, 4>(ak[n % kSets], hb[k], z[k]);
+          if (OUT) mma_tiles<QT, YT, 4>(aq[n % kSets], hb[k], y[k]);
         }
       }
     }
@@ -855,7 +853,13 @@ void delta_walk_kernel(DeltaParams p) {
 #pragma unroll
         for (int s = 0; s < NA; ++s)
           a[t][s] = *reinterpret_cast<const bf8x*>(tri_in + s * kDeltaTri + blk2 * 512 + lane * 8);
+        if constexpr (CARRY) {
+#pragma unroll
+          for (int k = 0; k < CT; ++k) mma_tiles<NA, NB, 1>(a + t, v[k], acc[k] + t);
+          if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // operands of two tiles at a time
+        }
       }
+      if constexpr (CARRY) return;
 #pragma unroll
       for (int k = 0; k < CT; ++k) {
         if (BACK ? m == 1 : m == 0) mma_tiles<NA, NB, 4>(a, v[k], acc[k]);
@@ -868,7 +872,7 @@ void delta_walk_kernel(DeltaParams p) {
     using OfInput = std::integral_constant<int, NT>;
     // state += columns of staged rows times values in terms
     auto update = [&](const bf16_t* tile_in, int m, auto& v) {
-      constexpr int kAtOnce = NT == 1 ? (HT < 8 ? HT : 8) : 2;
+      constexpr int kMost = CARRY ? 4 : 8, kAtOnce = NT == 1 ? (HT < kMost ? HT : kMost) : 2;
 #pragma unroll
       for (int i0 = 0; i0 < HT; i0 += kAtOnce) {
         bf8x a[kAtOnce][NT];
@@ -932,7 +936,8 @@ void delta_walk_kernel(DeltaParams p) {
 #pragma unroll
       for (int k = 0; k < CT; ++k) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) late[k][t] = OUT ? y[k][t] : o[k][t];
+        for (int t = 0; t < 4; ++t)
+          if (!SEG) late[k][t] = OUT ? y[k][t] : o[k][t];
         if (limit[k] < len) {
 #pragma unroll
           for (int i = 0; i < HT; ++i)
@@ -1378,12 +1383,12 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_grad_kernel(DeltaGradP
 
 // ---- launches -------------------------------------------------------------------
 
-template <typename TI, int KT, bool LOOSE, bool BACK>
+template <typename TI, int KT, bool LOOSE, bool BACK, int TERMS>
 int delta_prep(const DeltaParams& p, hipStream_t s) {
-  constexpr size_t lds = delta_prep_lds<TI, KT>();
+  constexpr size_t lds = delta_prep_lds<TI, KT>(BACK);
   static_assert(lds <= 160 * 1024, "a CU's LDS");
-  allow_dynamic_lds(delta_prep_kernel<TI, KT, LOOSE, BACK>, lds);
-  hipLaunchKernelGGL((delta_prep_kernel<TI, KT, LOOSE, BACK>),
+  allow_dynamic_lds(delta_prep_kernel<TI, KT, LOOSE, BACK, TERMS>, lds);
+  hipLaunchKernelGGL((delta_prep_kernel<TI, KT, LOOSE, BACK, TERMS>),
                      dim3((unsigned)((int64_t)p.B * p.H * p.nc)), dim3(kDeltaThreads), lds, s, p);
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
@@ -1422,8 +1427,11 @@ enum DeltaPhase {
 template <typename TI, int KT, bool LOOSE>
 int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
   switch (phase) {
-    case kPhasePrep: return delta_prep<TI, KT, LOOSE, false>(p, s);
-    case kPhasePrepBack: return delta_prep<TI, KT, LOOSE, true>(p, s);
+    case kPhasePrep:  // in the terms of the walk
+      if (p.out_bf16)
+        return delta_prep<TI, KT, LOOSE, false, delta_terms<TI, kDeltaOut>()>(p, s);
+      return delta_prep<TI, KT, LOOSE, false, kDeltaTerms>(p, s);
+    case kPhasePrepBack: return delta_prep<TI, KT, LOOSE, true, kDeltaTerms>(p, s);
     case kPhaseOut:
       return p.out_bf16 ? delta_walk<TI, KT, LOOSE, kDeltaOut>(p, s)
                         : delta_walk<TI, KT, LOOSE, kDeltaOutF32>(p, s);
@@ -1438,82 +1446,95 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
 // One pair per dtype and padded row size.
 // First states of the segments, h(i + 1) = M_i h(i) + end(i), from the state pass's
 // transitions M (walking back: their transposes) and ends, in place.  Four waves take the
-// rows of 16 columns of one state in turn of 16-row tiles, in fp32 on the matrix units.
+// rows of 16 columns of one state in turn of 16-row tiles, in fp32 on the matrix units; the next
+// transition is on its way while one is applied.
 template <int KT, bool BACK>
-__global__ __launch_bounds__(kDeltaThreads) void delta_carry_kernel(DeltaParams p) {
+__global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaParams p) {
   constexpr int N = 32 * KT, HT = 2 * KT, kMine = (HT + 3) / 4, kStride = N + 4;
+  constexpr int kPart = KT > 4 ? HT / 2 : HT;  // tiles of a row on their way at once
   __shared__ __attribute__((aligned(16))) float sH[2][16 * kStride];  // [column][row]
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int g = lane >> 4, col = lane & 15;
   const int tiles = p.Pp / 16;
   const int64_t bh = blockIdx.x / tiles;
   const int c = (int)(blockIdx.x % tiles) * 16 + col;
-  auto put = [&](float* h, int i, f4x v) {
-    *reinterpret_cast<f4x*>(h + col * kStride + 16 * i + 4 * g) = v;
+  // (waves without a tile do the work of tile 0 again and keep nothing)
+  auto tile = [&](int k) { return wave + 4 * k < HT ? wave + 4 * k : 0; };
+  auto mine = [&](int k) { return wave + 4 * k < HT; };
+  f4x h[kMine], end[kMine], m[kMine][kPart];
+  auto load_end = [&](int s) {
+    const float* st = p.seg_state + (bh * p.nseg + s) * N * p.Pp + c;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) end[k][r] = st[(int64_t)(16 * tile(k) + 4 * g + r) * p.Pp];
+  };
+  auto load_part = [&](int s, int part) {
+    // the transition over the same tokens, made by the forward state pass
+    const float* from = p.seg_carry + (bh * p.nseg + (BACK ? p.nseg - 1 - s : s)) * N * N;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+#pragma unroll
+      for (int n = 0; n < kPart; ++n) {
+        const int nn = 16 * (part * kPart + n) + 4 * g;
+        if (BACK) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) m[k][n][r] = from[(nn + r) * N + 16 * tile(k) + col];
+        } else {
+          m[k][n] = *reinterpret_cast<const f4x*>(from + (16 * tile(k) + col) * N + nn);
+        }
+      }
   };
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
-    const int i = wave + 4 * k;
-    if (i >= HT) break;
-    f4x v = {0.f, 0.f, 0.f, 0.f};
+    h[k] = f4x{0.f, 0.f, 0.f, 0.f};
     if (p.s0 != nullptr) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int n = 16 * i + 4 * g + r;
-        if (c < p.P && n < p.N) v[r] = p.s0[(bh * p.N + n) * p.P + c];
+        const int n = 16 * tile(k) + 4 * g + r;
+        if (c < p.P && n < p.N) h[k][r] = p.s0[(bh * p.N + n) * p.P + c];
       }
     }
-    put(sH[0], i, v);
+  }
+  if (p.nseg > 1) {
+    load_end(0);
+    load_part(0, 0);
   }
   for (int s = 0; s < p.nseg; ++s) {
-    const int64_t at = bh * p.nseg + s;
-    // the transition over the same tokens, made by the forward state pass
-    const float* m = p.seg_carry + (BACK ? bh * p.nseg + p.nseg - 1 - s : at) * N * N;
-    float* st = p.seg_state + at * N * p.Pp + c;
-    const float* h = sH[s & 1];
-    f4x end[kMine], a[kMine];
+    float* st = p.seg_state + (bh * p.nseg + s) * N * p.Pp + c;
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
-      const int i = wave + 4 * k;
-      if (i >= HT) break;
+      if (!mine(k)) continue;
+      *reinterpret_cast<f4x*>(sH[s & 1] + col * kStride + 16 * tile(k) + 4 * g) = h[k];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        end[k][r] = s + 1 < p.nseg ? st[(int64_t)(16 * i + 4 * g + r) * p.Pp] : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int i = wave + 4 * k;
-      if (i >= HT) break;
-      const f4x v = *reinterpret_cast<const f4x*>(h + col * kStride + 16 * i + 4 * g);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) st[(int64_t)(16 * i + 4 * g + r) * p.Pp] = v[r];
-      a[k] = end[k];
+      for (int r = 0; r < 4; ++r) st[(int64_t)(16 * tile(k) + 4 * g + r) * p.Pp] = h[k][r];
     }
     if (s + 1 == p.nseg) break;
-#pragma unroll 4
-    for (int n = 0; n < HT; ++n) {
-      const f4x b = *reinterpret_cast<const f4x*>(h + col * kStride + 16 * n + 4 * g);
+    __syncthreads();
+    f4x a[kMine][kPart];
 #pragma unroll
-      for (int k = 0; k < kMine; ++k) {
-        const int i = wave + 4 * k;
-        if (i >= HT) break;
-        f4x x;
-        if (BACK) {
+    for (int k = 0; k < kMine; ++k) h[k] = end[k];
+    const bool more = s + 2 < p.nseg;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) x[r] = m[(16 * n + 4 * g + r) * N + 16 * i + col];
-        } else {
-          x = *reinterpret_cast<const f4x*>(m + (16 * i + col) * N + 16 * n + 4 * g);
-        }
+    for (int part = 0; part < HT / kPart; ++part) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[k] = mma16(x[r], b[r], a[k]);
+      for (int k = 0; k < kMine; ++k)
+#pragma unroll
+        for (int n = 0; n < kPart; ++n) a[k][n] = m[k][n];
+      if (part + 1 < HT / kPart) load_part(s, part + 1);
+      else if (more) {
+        load_end(s + 1);
+        load_part(s + 1, 0);
       }
-    }
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int i = wave + 4 * k;
-      if (i >= HT) break;
-      put(sH[(s + 1) & 1], i, a[k]);
+      for (int n = 0; n < kPart; ++n) {
+        const f4x b = *reinterpret_cast<const f4x*>(sH[s & 1] + col * kStride +
+                                                    16 * (part * kPart + n) + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int k = 0; k < kMine; ++k) h[k] = mma16(a[k][n][r], b[r], h[k]);
+      }
     }
   }
 }
