@@ -47,41 +47,60 @@ int carry(const DeltaParams& p, bool back, hipStream_t s) {
 int padded_rows(int N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 
 constexpr size_t kTriBytes = kDeltaTri * sizeof(bf16_t);  // of a term
+constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
+
 // Terms of what a call computes: two where inputs and y are bf16.
 int terms_of(const swimba_delta_rule_args* a) {
   return a->in_dtype == SWIMBA_BF16 && a->y_dtype == SWIMBA_BF16 ? 2 : kDeltaTerms;
 }
-constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
 
 // Segments of the walks.  A walk's chunks follow each other; where the independent ones leave
 // CUs idle, they are cut into segments, whose transitions and ends are made first (a state
-// pass over the state's columns and as many more as it has rows) and joined.  The
-// number is the one of the least time, in steps of a chunk: `slots` workgroups run at once, and
-// one that has a CU for itself takes 0.6 of the time of one that shares it (4.1 us against
-// 6.8 us per chunk of 128 keys); a state pass's step takes 0.6 of a walk's (no queries,
-// scores and results); a join takes half a step per segment.
+// pass over the state's columns and as many more as it has rows) and joined.  Taken is the
+// number of the least time, in units of a chunk's walk by a workgroup that shares its CU
+// (6.7 us with 128 keys; 4.1 us for one that has it alone).  Measured, whole against cut: 8 heads
+// of 64 x 64 over 32768 tokens 1346 / 168 us in 32 segments, one head of 128 x 128 over
+// 65536 tokens 3494 / 312 us in 48, 40 heads of 128 x 64 over 65536 tokens 4118 / 1754 us in
+// 12, 256 x 128 x 128 over 4096 tokens 596 / 898 us in 2.
 struct SegPlan {
   int nseg = 1, seg_chunks = 1;
 };
 
-SegPlan plan_segments(int64_t walks, int64_t state_walks, int passes, int64_t nc, bool shared_cu,
-                      int dev) {
+// A step of `wgs` workgroups of which a CU holds up to `most`: `alone`, or `full` when it does.
+double step_time(double wgs, double alone, double full, int most, double cus) {
+  if (wgs <= cus) return alone;
+  const double each = wgs / cus;
+  if (most == 1) return alone * (each + 0.1);
+  if (each <= most) return alone + (full - alone) * (each < 2 ? 1.0 : each - 1) / (most - 1);
+  return full * (each / most + 0.1);
+}
+
+SegPlan plan_segments(const swimba_delta_rule_args* a, bool back, int dev) {
+  const int64_t tiles = (a->P + kWalkCols - 1) / kWalkCols, bh = (int64_t)a->B * a->H;
+  const int64_t more = (padded_rows(a->N) + kWalkCols - 1) / kWalkCols;
+  const int64_t nc = (a->L + kChunk - 1) / kChunk;
+  const double cus = device_cus(dev), join = 0.45;
+  const bool one = a->in_dtype == SWIMBA_F32 || a->N > 128;  // a CU's LDS
+  const bool out = !back && terms_of(a) == 2;
+  auto time = [&](int64_t n) {
+    const double len = (double)((nc + n - 1) / n), w = (double)(bh * tiles * n);
+    const double walk = step_time(w, 0.6, 1.0, one ? 1 : 2, cus);
+    double t = walk * (back ? 2.2 : 1.0);
+    if (n > 1) {
+      const double states = (double)(bh * (tiles + more) * (back ? n : n - 1));
+      t += out && !one ? step_time(states, 0.4, 0.8, 3, cus)
+                       : step_time(states, 0.45, 0.7, one ? 1 : 2, cus);
+      if (back) t += 0.9 * step_time(w * (double)(n - 1) / (double)n, 0.6, 1.0, one ? 1 : 2, cus);
+    }
+    return len * t + (n > 1 ? (double)n * join * (back ? 2 : 1) + 2.0 : 0.0);
+  };
   SegPlan best;
   best.seg_chunks = (int)nc;
-  const double cus = device_cus(dev);
-  auto steps = [&](double wgs) {
-    if (wgs <= cus) return 0.6;
-    const double slots = shared_cu ? 2 * cus : cus, rounds = wgs / slots;
-    return (shared_cu ? 1.0 : 0.6) * (rounds < 1 ? 1.0 : (double)(int64_t)(rounds + 0.999));
-  };
-  double least = passes * nc * steps((double)walks);
-  for (int64_t n = 2; n <= 256 && 2 * n <= nc; ++n) {
+  double least = time(1);
+  for (int64_t n = 2; n <= 128 && 2 * n <= nc; ++n) {
     const int64_t len = (nc + n - 1) / n;
     if ((nc + len - 1) / len != n) continue;
-    const double t = passes * len * steps((double)(walks * n)) +
-                     0.6 * len * steps((double)(state_walks * (n - 1))) +
-                     (passes - 1) * 0.6 * len * steps((double)(walks * (n - 1))) +
-                     passes * (0.5 * n + 2.0);
+    const double t = time(n);
     if (t < least) {
       least = t;
       best.nseg = (int)n;
@@ -111,24 +130,12 @@ struct DeltaPlan {
          bytes = 0;
 };
 
-// A walk's workgroups, and those of a state pass with transitions.
-int64_t walks_of(const swimba_delta_rule_args* a) {
-  return (int64_t)a->B * a->H * ((a->P + kWalkCols - 1) / kWalkCols);
-}
-int64_t state_walks_of(const swimba_delta_rule_args* a) {
-  return (int64_t)a->B * a->H * ((a->P + kWalkCols - 1) / kWalkCols +
-                                 (padded_rows(a->N) + kWalkCols - 1) / kWalkCols);
-}
 size_t padded_columns(const swimba_delta_rule_args* a) {
   return (size_t)(a->P + kWalkCols - 1) / kWalkCols * kWalkCols;
 }
-bool shares_cu(const swimba_delta_rule_args* a) {
-  return a->in_dtype == SWIMBA_BF16 && a->N <= 128;
-}
-
 DeltaPlan plan_delta(const swimba_delta_rule_args* a, int dev) {
   DeltaPlan r;
-  r.seg = plan_segments(walks_of(a), state_walks_of(a), 1, chunks_of(a), shares_cu(a), dev);
+  r.seg = plan_segments(a, false, dev);
   const size_t units = (size_t)a->B * a->H * chunks_of(a);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -150,15 +157,26 @@ DeltaPlan plan_delta(const swimba_delta_rule_args* a, int dev) {
 // And of a backward call.
 struct DeltaGradPlan {
   SegPlan seg;
+  int parts = 1;
   size_t off_seg = 0, off_carry = 0;
   size_t off_tri = 0, off_tri_t = 0, off_score = 0, off_gates = 0, off_states = 0, off_adj = 0,
          off_o = 0, off_dv = 0, off_dq = 0, off_dk = 0, off_part = 0, off_tiny = 0, bytes = 0;
 };
 
+// Workgroups of a group of heads that share q and k in the gradients' kernel: one, which adds
+// their gradients up in registers, unless that leaves CUs idle.
+int grad_parts(const swimba_delta_rule_args* a, int dev) {
+  const int share = a->H / a->G;
+  const int64_t units = (int64_t)a->B * a->G * chunks_of(a), want = 2LL * device_cus(dev);
+  int n = 1;
+  while (n < share && (units * n < want || share % n != 0)) ++n;
+  return n;
+}
+
 DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g, int dev) {
   const swimba_delta_rule_args* a = &g->fwd;
   DeltaGradPlan r;
-  r.seg = plan_segments(walks_of(a), state_walks_of(a), 2, chunks_of(a), shares_cu(a), dev);
+  r.seg = plan_segments(a, true, dev);
   const size_t units = (size_t)a->B * a->H * chunks_of(a), Pp = padded_columns(a);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -174,8 +192,9 @@ DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g, int dev) {
   r.off_adj = take(units * padded_rows(a->N) * Pp * sizeof(float));
   r.off_o = take(units * kChunk * Pp * sizeof(float));
   r.off_dv = take(units * kChunk * Pp * sizeof(float));
-  // per-head rows of dq and dk where heads share them
-  const size_t rows = a->H != a->G ? (size_t)a->B * a->L * a->H * a->N * sizeof(float) : 0;
+  // rows of dq and dk of the parts of a group of heads
+  r.parts = grad_parts(a, dev);
+  const size_t rows = r.parts > 1 ? (size_t)a->B * a->L * a->G * r.parts * a->N * sizeof(float) : 0;
   r.off_dq = take(rows);
   r.off_dk = take(rows);
   r.off_part = take(a->decay_form == SWIMBA_DECAY_HEAD ? units * sizeof(double) : 0);
@@ -392,10 +411,11 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, i
       rc = copy_or_zero(nullptr, g->dlog_decay, a->H, s);
     return rc;
   }
-  const bool f32 = a->in_dtype == SWIMBA_F32, shared = a->H != a->G;
+  const bool f32 = a->in_dtype == SWIMBA_F32;
   const DeltaGradPlan r = plan_delta_grad(g, dev);
   unsigned char* slot = at<unsigned char>(ws, r.off_tiny);
   int rc = SWIMBA_OK;
+  const bool shared = r.parts > 1;
   const void* q = whole_packs(a->q, key_elements(a), f32, slot, s, &rc);
   const void* k = whole_packs(a->k, key_elements(a), f32, slot + kTinySlot, s, &rc);
   const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
@@ -429,7 +449,7 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, i
   DeltaGradParams d = {};
   d.q = q;
   d.k = k;
-  d.dy = g->dy;
+  d.dy = p.dy;
   d.g = a->log_decay;
   d.beta = a->beta;
   d.B = a->B;
@@ -441,6 +461,8 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, i
   d.Pp = p.Pp;
   d.token_decay = p.token_decay;
   d.nc = p.nc;
+  d.parts = r.parts;
+  d.heads = a->H / a->G / r.parts;
   d.states = at<float>(ws, r.off_states);
   d.adjoints = at<float>(ws, r.off_adj);
   d.o = at<float>(ws, r.off_o);
@@ -454,10 +476,9 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, i
   rc = grads(d, f32, s);
   if (rc == SWIMBA_OK && shared) {
     const int64_t rows = (int64_t)a->B * a->L * a->G;
-    rc = sum_shared_heads(at<float>(ws, r.off_dq), g->dq, g->grad_dtype, rows, a->H / a->G, a->N, s);
+    rc = sum_shared_heads(at<float>(ws, r.off_dq), g->dq, g->grad_dtype, rows, r.parts, a->N, s);
     if (rc == SWIMBA_OK)
-      rc = sum_shared_heads(at<float>(ws, r.off_dk), g->dk, g->grad_dtype, rows, a->H / a->G, a->N,
-                            s);
+      rc = sum_shared_heads(at<float>(ws, r.off_dk), g->dk, g->grad_dtype, rows, r.parts, a->N, s);
   }
   if (rc == SWIMBA_OK && d.part != nullptr)
     rc = sum_decay_parts(d.part, g->dlog_decay, a->B, a->H, p.nc, s);

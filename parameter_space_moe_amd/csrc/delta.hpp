@@ -158,10 +158,11 @@ struct DeltaShape {
 
   // Where a row's values lie.  Slots of eight hold what a lane takes of a block of 32
   // columns (4 g.. and 16 + 4 g..), and a row's slots are exchanged by an exclusive or
-  // with mix(row): 16 rows at one slot, and the 4 rows by 4 slots of a transposing read,
-  // are then 16 different slots of the 64 banks.
+  // with mix(row): 16 rows at one slot, the 4 rows by 4 slots of a transposing read, and
+  // the even or odd slots of four rows that a store has, are then different slots of the
+  // 64 banks.
   static __device__ __forceinline__ int mix(int row) {
-    if constexpr (KT >= 4) return ((row & 3) << 2) | ((row >> 2) & 3);
+    if constexpr (KT >= 4) return ((row & 3) << 2) | (((row >> 2) + row) & 3);
     else if constexpr (KT == 2) return ((row & 2) << 1) | ((row >> 2) & 3);
     else return (row >> 2) & 3;
   }
@@ -1033,23 +1034,15 @@ struct DeltaGradParams {
   const float *g, *beta;
   int B, L, H, G, N, P, Pp;
   int token_decay, nc;
-  const float *states, *adjoints;  // [32 KT, P'] before and behind each chunk
+  int parts, heads;                // workgroups of a group of heads that share q and k, heads each
+  const float *states, *adjoints;  // [N', P'] before and behind each chunk
   const float *o, *dv;             // [64, P']
-  void *dq, *dk;                   // [B, L, H, N] rows per head
+  void *dq, *dk;                   // [B, L, G, parts, N]
   int grad_bf16;
   float* dg;                       // [B, L, H], or null
   double* part;                    // sums of dg per chunk (a decay per head), or null
   float* dbeta;                    // [B, L, H]
 };
-
-constexpr int kDeltaGradVectors = 16;  // of 64 floats
-
-template <typename TI, int KT>
-constexpr size_t delta_grad_lds() {
-  using Sh = DeltaShape<TI, KT>;
-  return 2 * (size_t)Sh::kTerms * Sh::kTile * sizeof(bf16_t) +
-         ((size_t)kChunk * kTriStride + kDeltaGradVectors * kChunk) * sizeof(float);
-}
 
 // Sum over the 16 lanes of a row, on each of them.
 __device__ __forceinline__ float row_sum(float v) {
@@ -1064,6 +1057,26 @@ __device__ __forceinline__ float column_sum(float v) {
   return xchg_add<16>(v, v);
 }
 
+constexpr int kGradThreads = 512;
+
+// LDS of the gradients' kernel: K and Q; 32 columns of dY, O, dV, h and a in terms (h and a in
+// turn where they do not fit together), later the slopes of the scores; vectors.
+template <typename TI, int KT>
+struct GradLds {
+  using Sh = DeltaShape<TI, KT>;
+  static constexpr int S = kDeltaTerms;
+  static constexpr size_t kRows = 2 * (size_t)Sh::kTerms * Sh::kTile * sizeof(bf16_t);
+  static constexpr size_t kToken = (size_t)kChunk * 32 * sizeof(bf16_t);  // of a term
+  static constexpr size_t kState = (size_t)Sh::kRows * 32 * sizeof(bf16_t);
+  static constexpr size_t kTokens = (Sh::kTerms + 2 * S) * kToken;
+  static constexpr size_t kVectors = 16 * kChunk * sizeof(float);
+  static constexpr bool kTogether =
+      kRows + kTokens + 2 * S * kState + kVectors <= 160 * 1024;
+  static constexpr size_t kStage = kTokens + (kTogether ? 2 : 1) * S * kState;
+  static constexpr size_t kSlopes = (size_t)kChunk * kTriStride * sizeof(float);
+  static constexpr size_t kBytes = kRows + (kStage > kSlopes ? kStage : kSlopes) + kVectors;
+};
+
 // With F = dY O^T and E = dV O^T (pairs s <= t and s < t):
 //   dQ = e^G dY h^T + (F D beta) K
 //   dK = beta w O a^T - e^G dV h^T + (F D beta)^T Q - (E D beta) K - (E D beta)^T K
@@ -1073,311 +1086,426 @@ __device__ __forceinline__ float column_sum(float v) {
 // chunks read of tokens s < t, and e^{G_end} <h, a>.  The pairs' sum is taken up from its
 // differences between neighbours (column sum less row sum) from the chunk's start or the
 // last cleared state, in 64 bits.
-// One workgroup per chunk and head; wave w takes the 16 tokens of tile w.
+//
+// One workgroup per chunk and `heads` heads that share its q and k, whose gradients stay in
+// registers from head to head.  Wave (rt, half) takes the 16 tokens of tile rt by half
+// of the keys; waves of half 0 also take row tile rt of F, of half 1 of E.  dY, O, dV, h
+// and a pass through LDS 32 columns at a time, split into terms once for all waves, the next
+// ones on their way in registers.
 template <typename TI, int KT, bool LOOSE>
-__global__ __launch_bounds__(kDeltaThreads, 1) void delta_grad_kernel(DeltaGradParams p) {
+__global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParams p) {
   using Sh = DeltaShape<TI, KT>;
-  using Rows = DeltaRows<TI, KT, LOOSE>;
-  constexpr int NT = Sh::kTerms, HT = 2 * KT, S = kDeltaTerms;
+  using Lds = GradLds<TI, KT>;
+  using Rows = DeltaRows<TI, KT, LOOSE, kGradThreads / 2>;
+  constexpr int NT = Sh::kTerms, S = kDeltaTerms, N = Sh::kRows;
+  constexpr int kTokenTerm = kChunk * 32, kStateTerm = N * 32;  // values of a term
+  constexpr int kStatePacks = (N * 4 + kGradThreads - 1) / kGradThreads;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
   bf16_t* sK = reinterpret_cast<bf16_t*>(smem_raw);
   bf16_t* sQ = sK + NT * Sh::kTile;
+  bf16_t* sY = sQ + NT * Sh::kTile;
+  bf16_t* sO = sY + NT * kTokenTerm;
+  bf16_t* sV = sO + S * kTokenTerm;
+  bf16_t* sH = sV + S * kTokenTerm;
+  bf16_t* sB = Lds::kTogether ? sH + S * kStateTerm : sH;
   // F D beta on and below the diagonal, (E D beta)^T above it
-  float* sM = reinterpret_cast<float*>(sQ + NT * Sh::kTile);
-  float* vec = sM + kChunk * kTriStride;
+  float* sM = reinterpret_cast<float*>(sY);
+  float* vec = reinterpret_cast<float*>(smem_raw + Lds::kBytes - Lds::kVectors);
   float *gHi = vec, *gLo = vec + 64, *gRead = vec + 128, *gWrite = vec + 192, *gBeta = vec + 256;
-  float *rowF = vec + 320, *rowE = vec + 384, *diag = vec + 448;
-  float *seen = vec + 512, *wrote = vec + 576, *thru = vec + 640;  // thru: 4 per wave
-  float* cols = vec + 704;  // [4 tiles][64]
+  float *row = vec + 320, *diag = vec + 384;
+  float *seen = vec + 448, *wrote = vec + 576;  // [2][64]: halves of the keys
+  float* cols = vec + 704;                      // [4][64]: row tiles
+  float* thru = vec + 960;                      // [8]: waves
+  static_assert(Lds::kVectors >= 968 * sizeof(float), "the vectors");
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int g = lane >> 4, col = lane & 15;
-  const int64_t unit = blockIdx.x;
-  const int c = (int)(unit % p.nc);
-  const int64_t bh = unit / p.nc;
-  const int b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
+  const int rt = wave & 3, half = wave >> 2;
+  int blk = (int)blockIdx.x;
+  const int part = blk % p.parts;
+  blk /= p.parts;
+  const int c = blk % p.nc;
+  blk /= p.nc;
+  const int grp = blk % p.G, b = blk / p.G;
   const int t0 = c * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
-
-  DeltaParams rp = {};
-  rp.G = p.G;
-  rp.N = p.N;
-  rp.B = p.B;
-  rp.L = p.L;
-  typename Rows::Stage rk, rq;
-  Rows::place(rk, p.k, rp, b, h / (p.H / p.G), t0, len, tid);
-  Rows::place(rq, p.q, rp, b, h / (p.H / p.G), t0, len, tid);
-  rk.load(0);
-  rq.load(0);
-  float gt = 0.f, bt = 0.f;
-  if (wave == 0) {
-    const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
-    if (lane < len) {
-      gt = p.token_decay ? p.g[at] : p.g[h];
-      bt = p.beta[at];
-    }
-    const double d = (double)gt * 1.4426950408889634;
-    const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
-    const double end = last_lane(sum);
-    const float hi = (float)sum;
-    gHi[lane] = hi;
-    gLo[lane] = (float)(sum - (double)hi);
-    gRead[lane] = exp2_sum(sum);
-    gWrite[lane] = exp2_sum(end - sum);
-    gBeta[lane] = bt;
-  }
-  Rows::all(rk, sK);
-  Rows::all(rq, sQ);
-  __syncthreads();
-
-  // This wave's rows along the values: slots 8 g.. of a block of 32, in their own order.
-  const int64_t vstride = (int64_t)p.H * p.P;
-  const TI* dy = static_cast<const TI*>(p.dy) + ((int64_t)b * p.L + t0) * vstride +
-                 (int64_t)h * p.P;
-  const float* o = p.o + unit * kChunk * p.Pp;
-  const float* dv = p.dv + unit * kChunk * p.Pp;
-  auto split_row = [&](const float* at, bf8x* out) {
-    float x[8];
-    *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(at);
-    *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(at + 4);
-    split_values<S>(x, out);
-  };
-  auto dy_operand = [&](int rt, int m, bf8x* out) {
-    const int t = 16 * rt + col, cc = 32 * m + 8 * g, n = t < len ? p.P - cc : 0;
-    const Pack<TI> v = load_pack(dy + (n > 0 ? t * vstride + cc : 0), n);
-    if constexpr (Sh::kF32) split_values<S>(v.v, out);
-    else out[0] = __builtin_bit_cast(bf8x, v);
-  };
+  const int h0 = grp * (p.H / p.G) + part * p.heads;
   const int blocks = (p.P + 31) / 32;
 
-  // F of tile w and E of tile 3 - w
-  const int tf = wave, te = 3 - wave;
-  f4x f[4], e[4];
-#pragma unroll
-  for (int ct = 0; ct < 4; ++ct) {
-    f[ct] = f4x{0.f, 0.f, 0.f, 0.f};
-    e[ct] = f4x{0.f, 0.f, 0.f, 0.f};
-  }
-  for (int m = 0; m < blocks; ++m) {
-    bf8x ay[NT], av[S];
-    dy_operand(tf, m, ay);
-    split_row(dv + (int64_t)(16 * te + col) * p.Pp + 32 * m + 8 * g, av);
-#pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-      if (ct > tf && ct > te) continue;
-      bf8x bo[S];
-      split_row(o + (int64_t)(16 * ct + col) * p.Pp + 32 * m + 8 * g, bo);
-      if (ct <= tf) f[ct] = mma_terms<NT, S>(ay, bo, f[ct]);
-      if (ct <= te) e[ct] = mma_terms<S, S>(av, bo, e[ct]);
-    }
-  }
-  // the scores that go with them
+  // K and Q, by half of the threads each
   {
-    f4x qk[4], kk[4];
-#pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-      qk[ct] = f4x{0.f, 0.f, 0.f, 0.f};
-      kk[ct] = f4x{0.f, 0.f, 0.f, 0.f};
-    }
-#pragma unroll
-    for (int n = 0; n < KT; ++n) {
-      bf8x ak[NT], aq[NT];
-      row_operand<Sh>(sK, 16 * te, n, lane, ak);
-      row_operand<Sh>(sQ, 16 * tf, n, lane, aq);
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) {
-        if (ct > tf && ct > te) continue;
-        bf8x bk[NT];
-        row_operand<Sh>(sK, 16 * ct, n, lane, bk);
-        if (ct <= tf) qk[ct] = mma_terms<NT, NT>(aq, bk, qk[ct]);
-        if (ct <= te) kk[ct] = mma_terms<NT, NT>(ak, bk, kk[ct]);
-      }
-    }
-    float rf[4] = {}, re[4] = {};
-    float cf[4], ce[4];
-#pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-      const int s = 16 * ct + col;
-      const float bs = gBeta[s];
-      cf[ct] = ce[ct] = 0.f;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * tf + 4 * g + r, u = 16 * te + 4 * g + r;
-        const float d = hw_exp2((gHi[t] - gHi[s]) + (gLo[t] - gLo[s]));
-        const float fd = s <= t ? f[ct][r] * d : 0.f;
-        const float fq = fd * qk[ct][r];
-        if (s <= t) sM[t * kTriStride + s] = fd * bs;
-        if (s == t) diag[t] = fq;
-        else {
-          cf[ct] += fq;
-          rf[r] = fmaf(fq, bs, rf[r]);
-        }
-        const float ed =
-            s < u ? e[ct][r] * hw_exp2((gHi[u] - gHi[s]) + (gLo[u] - gLo[s])) : 0.f;
-        const float ek = ed * kk[ct][r];
-        if (s < u) sM[s * kTriStride + u] = ed * bs;
-        ce[ct] += ek;
-        re[r] = fmaf(ek, bs, re[r]);
-      }
-      cf[ct] = column_sum(cf[ct]);
-      ce[ct] = column_sum(ce[ct]);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      rf[r] = row_sum(rf[r]);
-      re[r] = row_sum(re[r]);
-      if (col == 0) {
-        rowF[16 * tf + 4 * g + r] = rf[r];
-        rowE[16 * te + 4 * g + r] = re[r];
-      }
-    }
-    if (g == 0) {
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) cols[tf * 64 + 16 * ct + col] = cf[ct];
-    }
-    __syncthreads();  // tiles tf and te are two waves' columns
-    if (g == 0) {
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) cols[te * 64 + 16 * ct + col] -= ce[ct];
-    }
+    DeltaParams rp = {};
+    rp.G = p.G;
+    rp.N = p.N;
+    rp.B = p.B;
+    rp.L = p.L;
+    typename Rows::Stage st;
+    Rows::place(st, half ? p.q : p.k, rp, b, grp, t0, len, tid & (kGradThreads / 2 - 1));
+    st.load(0);
+    Rows::all(st, half ? sQ : sK);
   }
-  __syncthreads();
 
-  // what this wave's tokens read of h, erase of it and write into a
-  f4x reads[HT], erased[HT], written[HT];
-#pragma unroll
-  for (int i = 0; i < HT; ++i) {
-    reads[i] = f4x{0.f, 0.f, 0.f, 0.f};
-    erased[i] = f4x{0.f, 0.f, 0.f, 0.f};
-    written[i] = f4x{0.f, 0.f, 0.f, 0.f};
-  }
-  const float* hs = p.states + unit * (32 * KT) * p.Pp;
-  const float* as = p.adjoints + unit * (32 * KT) * p.Pp;
-  float through = 0.f;
-  for (int m = 0; m < blocks; ++m) {
-    bf8x ay[NT], av[S], ao[S];
-    const int64_t at = (int64_t)(16 * wave + col) * p.Pp + 32 * m + 8 * g;
-    dy_operand(wave, m, ay);
-    split_row(dv + at, av);
-    split_row(o + at, ao);
-#pragma unroll
-    for (int i = 0; i < HT; ++i) {
-      const int64_t n = (int64_t)(16 * i + col) * p.Pp + 32 * m + 8 * g;
-      float x[8], y[8];
-      bf8x hb[S], ab[S];
-      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(hs + n);
-      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(hs + n + 4);
-      *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(as + n);
-      *reinterpret_cast<float4*>(y + 4) = *reinterpret_cast<const float4*>(as + n + 4);
-      if ((i & 3) == wave) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) through = fmaf(x[k], y[k], through);
-      }
-      split_values<S>(x, hb);
-      split_values<S>(y, ab);
-      reads[i] = mma_terms<NT, S>(ay, hb, reads[i]);
-      erased[i] = mma_terms<S, S>(av, hb, erased[i]);
-      written[i] = mma_terms<S, S>(ao, ab, written[i]);
-    }
-  }
-  through = wave_sum64(through);
-  if (lane == 0) thru[wave] = through;
-  auto element = [&](const bf16_t* tile, int t, int n) {
-    const bf16_t* at = tile + Sh::place(t, n & ~3) + (n & 3);
-    float v = to_f32(at[0]);
-#pragma unroll
-    for (int s = 1; s < NT; ++s) v += to_f32(at[s * Sh::kTile]);
+  // The next 32 columns: a pack of eight of O or dV and of dY per thread, and of h and a.
+  struct Pack8 {
+    f4x a, b;
+  };
+  const int tok = tid & 255, trow = tok >> 2, tslot = tok & 3;
+  const int64_t vstride = (int64_t)p.H * p.P;
+  Pack8 ro, rh[kStatePacks], ra[kStatePacks];
+  Pack<TI> ry;
+  float gt = 0.f, bt = 0.f, next_g = 0.f, next_b = 0.f;
+  auto load8 = [](const float* at) {
+    Pack8 v;
+    v.a = *reinterpret_cast<const f4x*>(at);
+    v.b = *reinterpret_cast<const f4x*>(at + 4);
     return v;
   };
-  const f4x er = *reinterpret_cast<const f4x*>(gRead + 16 * wave + 4 * g);
-  const f4x ew = *reinterpret_cast<const f4x*>(gWrite + 16 * wave + 4 * g);
-  const f4x eb = *reinterpret_cast<const f4x*>(gBeta + 16 * wave + 4 * g);
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int t = 16 * wave + 4 * g + r;
-    float s = 0.f, w = 0.f;
-#pragma unroll
-    for (int i = 0; i < HT; ++i) {
-      const float kn = element(sK, t, 16 * i + col), qn = element(sQ, t, 16 * i + col);
-      s += qn * reads[i][r] - kn * erased[i][r];
-      w = fmaf(kn, written[i][r], w);
+  auto fetch = [&](int i, int m) {
+    const int64_t bh = (int64_t)b * p.H + h0 + i, unit = bh * p.nc + c;
+    const int cc = 32 * m + 8 * tslot;
+    ro = load8((half ? p.dv : p.o) + (unit * kChunk + trow) * p.Pp + cc);
+    if (half == 0) {
+      const TI* dy = static_cast<const TI*>(p.dy) + ((int64_t)b * p.L + t0) * vstride +
+                     (int64_t)(h0 + i) * p.P;
+      const int n = trow < len ? p.P - cc : 0;
+      if (LOOSE) ry = load_pack(dy + (n > 0 ? trow * vstride + cc : 0), n);
+      else ry = load_pack(dy + (n > 0 ? trow * vstride + cc : 0), kPack);
     }
-    s = row_sum(s) * er[r];
-    w = row_sum(w) * ew[r];
-    if (col == 0) {
-      seen[t] = s;
-      wrote[t] = w;
+#pragma unroll
+    for (int k = 0; k < kStatePacks; ++k) {
+      const int e = k * kGradThreads + tid;
+      const int64_t at = (unit * N + (e < N * 4 ? e >> 2 : 0)) * p.Pp + 32 * m + 8 * (e & 3);
+      rh[k] = load8(p.states + at);
+      ra[k] = load8(p.adjoints + at);
+    }
+    if (m == 0 && wave == 0 && lane < len) {
+      const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h0 + i;
+      next_g = p.token_decay ? p.g[at] : p.g[h0 + i];
+      next_b = p.beta[at];
+    }
+  };
+  auto place = [](int r, int slot) { return ((r >> 4) * 64 + slot * 16 + (r & 15)) * 8; };
+  auto put = [&](const Pack8& v, bf16_t* to, int term) {
+    bf8x t[S];
+    split_tiles<S>(v.a, v.b, t);
+#pragma unroll
+    for (int s = 0; s < S; ++s) *reinterpret_cast<bf8x*>(to + s * term) = t[s];
+  };
+  auto put_states = [&](const Pack8* v, bf16_t* to) {
+#pragma unroll
+    for (int k = 0; k < kStatePacks; ++k) {
+      const int e = k * kGradThreads + tid;
+      if (N * 4 % kGradThreads == 0 || e < N * 4) put(v[k], to + place(e >> 2, e & 3), kStateTerm);
+    }
+  };
+  auto operand = [&](const bf16_t* from, int tile, int term, int s) {
+    return *reinterpret_cast<const bf8x*>(from + s * term + (tile * 64 + lane) * 8);
+  };
+
+  f4x dq[KT], dk[KT];
+#pragma unroll
+  for (int k = 0; k < KT; ++k) {
+    dq[k] = f4x{0.f, 0.f, 0.f, 0.f};
+    dk[k] = f4x{0.f, 0.f, 0.f, 0.f};
+  }
+  fetch(0, 0);
+  __syncthreads();
+  // scores of row tile rt, before the decays: Q K^T, or (half 1) K K^T
+  f4x sc[4];
+#pragma unroll
+  for (int ct = 0; ct < 4; ++ct) sc[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < KT; ++n) {
+    bf8x a[NT];
+    row_operand<Sh>(half ? sK : sQ, 16 * rt, n, lane, a);
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      if (ct > rt) continue;
+      bf8x bk[NT];
+      row_operand<Sh>(sK, 16 * ct, n, lane, bk);
+      sc[ct] = mma_terms<NT, NT>(a, bk, sc[ct]);
     }
   }
+
+  for (int i = 0; i < p.heads; ++i) {
+    const int h = h0 + i;
+    const int64_t bh = (int64_t)b * p.H + h, unit = bh * p.nc + c;
+    // what this wave's tokens read of h, erase of it and write into a; F or E
+    f4x reads[KT], erased[KT], written[KT], fe[4];
 #pragma unroll
-  for (int i = 0; i < HT; ++i) {
-    reads[i] *= er;
-    written[i] = written[i] * (ew * eb) - erased[i] * er;
-  }
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const int t = 16 * wave + col;
-    float fd[8], both[8], ft[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int s = 32 * m + 16 * (i >> 2) + 4 * g + (i & 3);
-      const float row = sM[t * kTriStride + s], down = sM[s * kTriStride + t];
-      fd[i] = s <= t ? row : 0.f;
-      ft[i] = s >= t ? down : 0.f;
-      both[i] = s == t ? 0.f : s < t ? -down : -row;
+    for (int k = 0; k < KT; ++k) {
+      reads[k] = f4x{0.f, 0.f, 0.f, 0.f};
+      erased[k] = f4x{0.f, 0.f, 0.f, 0.f};
+      written[k] = f4x{0.f, 0.f, 0.f, 0.f};
     }
-    bf8x af[S], ae[S], at[S];
-    split_values<S>(fd, af);
-    split_values<S>(both, ae);
-    split_values<S>(ft, at);
 #pragma unroll
-    for (int i = 0; i < HT; ++i) {
-      bf8x bk[NT], bq[NT];
-      column_operand<Sh>(sK, i, m, lane, bk);
-      column_operand<Sh>(sQ, i, m, lane, bq);
-      reads[i] = mma_terms<S, NT>(af, bk, reads[i]);
-      written[i] = mma_terms<S, NT>(ae, bk, written[i]);
-      written[i] = mma_terms<S, NT>(at, bq, written[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < HT; ++i) {
-    const int n = 16 * i + col;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * wave + 4 * g + r;
-      if (t < len && n < p.N) {
-        const int64_t to = (((int64_t)b * p.L + t0 + t) * p.H + h) * p.N + n;
-        if (p.grad_bf16) {
-          static_cast<bf16_t*>(p.dq)[to] = from_f32<bf16_t>(reads[i][r]);
-          static_cast<bf16_t*>(p.dk)[to] = from_f32<bf16_t>(written[i][r]);
+    for (int ct = 0; ct < 4; ++ct) fe[ct] = f4x{0.f, 0.f, 0.f, 0.f};
+    float through = 0.f;
+    for (int m = 0; m < blocks; ++m) {
+      __syncthreads();  // everyone is done with the last ones
+      if (m == 0) {
+        gt = next_g;
+        bt = next_b;
+        if (wave == 0) {
+          const double d = (double)gt * 1.4426950408889634;
+          const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
+          const double end = last_lane(sum);
+          const float hi = (float)sum;
+          gHi[lane] = hi;
+          gLo[lane] = (float)(sum - (double)hi);
+          gRead[lane] = exp2_sum(sum);
+          gWrite[lane] = exp2_sum(end - sum);
+          gBeta[lane] = bt;
+        }
+      }
+      put(ro, (half ? sV : sO) + place(trow, tslot), kTokenTerm);
+      if (half == 0) {
+        const bool in = LOOSE || (trow < len && 32 * m + 8 * tslot < p.P);
+        if constexpr (Sh::kF32) {
+          Pack8 v;
+          __builtin_memcpy(&v, &ry, sizeof(v));
+          if (!in) v.a = v.b = f4x{0.f, 0.f, 0.f, 0.f};
+          put(v, sY + place(trow, tslot), kTokenTerm);
         } else {
-          static_cast<float*>(p.dq)[to] = reads[i][r];
-          static_cast<float*>(p.dk)[to] = written[i][r];
+          u4x v = __builtin_bit_cast(u4x, ry);
+          if (!in) v = u4x{0, 0, 0, 0};
+          *reinterpret_cast<u4x*>(sY + place(trow, tslot)) = v;
+        }
+      }
+      put_states(rh, sH);
+      if (Lds::kTogether) put_states(ra, sB);
+#pragma unroll
+      for (int k = 0; k < kStatePacks; ++k) {
+        if (N * 4 % kGradThreads != 0 && k * kGradThreads + tid >= N * 4) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          through = fmaf(rh[k].a[e], ra[k].a[e], fmaf(rh[k].b[e], ra[k].b[e], through));
+      }
+      __syncthreads();
+      const bool more = m + 1 < blocks || i + 1 < p.heads;
+      auto ahead = [&] {
+        if (more) fetch(m + 1 < blocks ? i : i + 1, m + 1 < blocks ? m + 1 : 0);
+      };
+      if (Lds::kTogether) ahead();
+
+      bf8x ay[NT], av[S], ao[S];
+#pragma unroll
+      for (int s = 0; s < NT; ++s) ay[s] = operand(sY, rt, kTokenTerm, s);
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        av[s] = operand(sV, rt, kTokenTerm, s);
+        ao[s] = operand(sO, rt, kTokenTerm, s);
+      }
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) {
+        if (ct > rt) continue;
+        bf8x bo[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) bo[s] = operand(sO, ct, kTokenTerm, s);
+        if (half) fe[ct] = mma_terms<S, S>(av, bo, fe[ct]);
+        else fe[ct] = mma_terms<NT, S>(ay, bo, fe[ct]);
+      }
+      // two tiles of keys at a time (four spill), a pair of terms for both in turn
+      constexpr int kAtOnce = KT < 2 ? KT : 2;
+      auto tiles = [&](auto na, const bf8x* a, const bf8x (*v)[S], f4x* acc) {
+        constexpr int NA = decltype(na)::value;
+#pragma unroll
+        for (int n = S - 1; n >= 0; --n)
+#pragma unroll
+          for (int x = 0; x < NA; ++x)
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+              if (n - x >= 0) acc[k] = mma16(a[x], v[k][n - x], acc[k]);
+      };
+      using Three = std::integral_constant<int, S>;
+      using OfInput = std::integral_constant<int, NT>;
+#pragma unroll
+      for (int k0 = 0; k0 < KT; k0 += kAtOnce) {
+        bf8x v[kAtOnce][S];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+          for (int s = 0; s < S; ++s) v[k][s] = operand(sH, half * KT + k0 + k, kStateTerm, s);
+        tiles(OfInput(), ay, v, reads + k0);
+        tiles(Three(), av, v, erased + k0);
+      }
+      if (!Lds::kTogether) {
+        __syncthreads();
+        put_states(ra, sB);
+        ahead();
+        __syncthreads();
+      }
+#pragma unroll
+      for (int k0 = 0; k0 < KT; k0 += kAtOnce) {
+        bf8x v[kAtOnce][S];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+          for (int s = 0; s < S; ++s) v[k][s] = operand(sB, half * KT + k0 + k, kStateTerm, s);
+        tiles(Three(), ao, v, written + k0);
+      }
+    }
+    through = wave_sum64(through);
+    if (lane == 0) thru[wave] = through;
+    __syncthreads();  // the columns are done with: slopes in their place
+
+    // (addresses from here on are made anew for each head: kept over the loop they spill, and
+    // a load of a spilled one waits for the next head's columns on their way)
+    {
+    const int lane_now = apart(lane), g = lane_now >> 4, col = lane_now & 15;
+
+    {
+      float rs[4] = {}, cs[4];
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) {
+        cs[ct] = 0.f;
+        if (ct > rt) continue;
+        const int s = 16 * ct + col;
+        const float bs = gBeta[s], hs = gHi[s], ls = gLo[s];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * rt + 4 * g + r;
+          const float d = fe[ct][r] * hw_exp2((gHi[t] - hs) + (gLo[t] - ls));
+          const float x = s < t ? d * sc[ct][r] : 0.f;
+          if (half) {
+            if (s < t) sM[s * kTriStride + t] = d * bs;
+          } else {
+            if (s <= t) sM[t * kTriStride + s] = d * bs;
+            if (s == t) diag[t] = d * sc[ct][r];
+          }
+          cs[ct] += x;
+          rs[r] = fmaf(x, bs, rs[r]);
+        }
+        cs[ct] = column_sum(cs[ct]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rs[r] = row_sum(rs[r]);
+      if (half == 0) {
+        if (g == 0) {
+#pragma unroll
+          for (int ct = 0; ct < 4; ++ct) cols[rt * 64 + 16 * ct + col] = cs[ct];
+        }
+        if (col == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) row[16 * rt + 4 * g + r] = rs[r];
+        }
+      }
+      __syncthreads();
+      if (half) {  // less those of E
+        if (g == 0) {
+#pragma unroll
+          for (int ct = 0; ct < 4; ++ct) cols[rt * 64 + 16 * ct + col] -= cs[ct];
+        }
+        if (col == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) row[16 * rt + 4 * g + r] -= rs[r];
         }
       }
     }
+    auto element = [&](const bf16_t* tile, int t, int n) {
+      const bf16_t* at = tile + Sh::place(t, n & ~3) + (n & 3);
+      float v = to_f32(at[0]);
+#pragma unroll
+      for (int s = 1; s < NT; ++s) v += to_f32(at[s * Sh::kTile]);
+      return v;
+    };
+    const f4x er = *reinterpret_cast<const f4x*>(gRead + 16 * rt + 4 * g);
+    const f4x ew = *reinterpret_cast<const f4x*>(gWrite + 16 * rt + 4 * g);
+    const f4x eb = *reinterpret_cast<const f4x*>(gBeta + 16 * rt + 4 * g);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * rt + 4 * g + r;
+      float x = 0.f, w = 0.f;
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const int n = 16 * (half * KT + k) + col;
+        const float kn = element(sK, t, n), qn = element(sQ, t, n);
+        x += qn * reads[k][r] - kn * erased[k][r];
+        w = fmaf(kn, written[k][r], w);
+      }
+      x = row_sum(x) * er[r];
+      w = row_sum(w) * ew[r];
+      if (col == 0) {
+        seen[half * 64 + t] = x;
+        wrote[half * 64 + t] = w;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      dq[k] += reads[k] * er;
+      dk[k] += written[k] * (ew * eb) - erased[k] * er;
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int t = 16 * rt + col;
+      float fd[8], both[8], ft[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int s = 32 * m + 16 * (e >> 2) + 4 * g + (e & 3);
+        const float across = sM[t * kTriStride + s], down = sM[s * kTriStride + t];
+        fd[e] = s <= t ? across : 0.f;
+        ft[e] = s >= t ? down : 0.f;
+        both[e] = s == t ? 0.f : s < t ? -down : -across;
+      }
+      bf8x af[S], ae[S], at[S];
+      split_values<S>(fd, af);
+      split_values<S>(both, ae);
+      split_values<S>(ft, at);
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        bf8x bk[NT], bq[NT];
+        column_operand<Sh>(sK, half * KT + k, m, lane_now, bk);
+        column_operand<Sh>(sQ, half * KT + k, m, lane_now, bq);
+        dq[k] = mma_terms<S, NT>(af, bk, dq[k]);
+        dk[k] = mma_terms<S, NT>(ae, bk, dk[k]);
+        dk[k] = mma_terms<S, NT>(at, bq, dk[k]);
+      }
+    }
+    __syncthreads();
+    if (wave == 0) {
+      const float down = cols[lane] + cols[64 + lane] + cols[128 + lane] + cols[192 + lane];
+      const float wr = wrote[lane] + wrote[64 + lane];
+      const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
+      if (lane < len) p.dbeta[at] = down + diag[lane] + wr;
+      const bool clear = lane < len && hw_exp2(gt * kLog2e) == 0.f;
+      const double slope = (double)bt * down - (double)row[lane];
+      const double upto = wave_prefix(slope) - slope;  // of the tokens before
+      const uint64_t mask = __ballot(clear) & (~0ull >> (63 - lane));
+      const int from = mask != 0 ? 63 - __clzll((long long)mask) : 0;
+      const double base = __shfl(upto, from);
+      const double sn = (double)seen[lane] + seen[64 + lane], wb = (double)bt * wr;
+      const double all_seen = wave_prefix(sn), all_wrote = wave_prefix(wb);
+      double ha = 0.0;
+#pragma unroll
+      for (int w = 0; w < kGradThreads / 64; ++w) ha += thru[w];
+      double dg = (upto - base) + (last_lane(all_seen) - all_seen + sn) + (all_wrote - wb) +
+                  (double)exp2_sum((double)gHi[63] + (double)gLo[63]) * ha;
+      if (clear || lane >= len) dg = 0.0;
+      if (p.dg != nullptr && lane < len) p.dg[at] = (float)dg;
+      if (p.part != nullptr) {
+        dg = wave_prefix(dg);
+        if (lane == 63) p.part[unit] = dg;
+      }
+    }
+      }
   }
-  __syncthreads();
-  if (wave != 0) return;
-  const float down = cols[lane] + cols[64 + lane] + cols[128 + lane] + cols[192 + lane];
-  const float wr = wrote[lane];
-  if (lane < len) p.dbeta[((int64_t)b * p.L + t0 + lane) * p.H + h] = down + diag[lane] + wr;
-  const bool clear = lane < len && hw_exp2(gt * kLog2e) == 0.f;
-  const double slope = (double)bt * down - ((double)rowF[lane] - (double)rowE[lane]);
-  const double upto = wave_prefix(slope) - slope;  // of the tokens before
-  const uint64_t mask = __ballot(clear) & (~0ull >> (63 - lane));
-  const int from = mask != 0 ? 63 - __clzll((long long)mask) : 0;
-  const double base = __shfl(upto, from);
-  const double sn = seen[lane], wb = (double)bt * wr;
-  const double all_seen = wave_prefix(sn), all_wrote = wave_prefix(wb);
-  double dg = (upto - base) + (last_lane(all_seen) - all_seen + sn) + (all_wrote - wb) +
-              (double)exp2_sum((double)gHi[63] + (double)gLo[63]) *
-                  ((double)thru[0] + thru[1] + thru[2] + thru[3]);
-  if (clear || lane >= len) dg = 0.0;
-  if (p.dg != nullptr && lane < len) p.dg[((int64_t)b * p.L + t0 + lane) * p.H + h] = (float)dg;
-  if (p.part != nullptr) {
-    dg = wave_prefix(dg);
-    if (lane == 63) p.part[unit] = dg;
+#pragma unroll
+  for (int k = 0; k < KT; ++k) {
+    const int n = 16 * (half * KT + k) + col;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * rt + 4 * g + r;
+      if (t < len && n < p.N) {
+        const int64_t to =
+            ((((int64_t)b * p.L + t0 + t) * p.G + grp) * p.parts + part) * p.N + n;
+        if (p.grad_bf16) {
+          static_cast<bf16_t*>(p.dq)[to] = from_f32<bf16_t>(dq[k][r]);
+          static_cast<bf16_t*>(p.dk)[to] = from_f32<bf16_t>(dk[k][r]);
+        } else {
+          static_cast<float*>(p.dq)[to] = dq[k][r];
+          static_cast<float*>(p.dk)[to] = dk[k][r];
+        }
+      }
+    }
   }
 }
 
@@ -1411,11 +1539,12 @@ int delta_walk(const DeltaParams& p, hipStream_t s) {
 
 template <typename TI, int KT, bool LOOSE>
 int delta_grad(const DeltaGradParams& p, hipStream_t s) {
-  constexpr size_t lds = delta_grad_lds<TI, KT>();
+  constexpr size_t lds = GradLds<TI, KT>::kBytes;
   static_assert(lds <= 160 * 1024, "a CU's LDS");
   allow_dynamic_lds(delta_grad_kernel<TI, KT, LOOSE>, lds);
   hipLaunchKernelGGL((delta_grad_kernel<TI, KT, LOOSE>),
-                     dim3((unsigned)((int64_t)p.B * p.H * p.nc)), dim3(kDeltaThreads), lds, s, p);
+                     dim3((unsigned)((int64_t)p.B * p.G * p.nc * p.parts)), dim3(kGradThreads), lds,
+                     s, p);
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
@@ -1565,8 +1694,8 @@ SWIMBA_DELTA_DECL(delta_f32_128)
                             : delta_phase<TI, KT, false>(p, phase, s);              \
   }                                                                                 \
   int name##_grad(const DeltaGradParams& p, hipStream_t s) {                        \
-    return p.N % kPack != 0 ? delta_grad<TI, KT, true>(p, s)                        \
-                            : delta_grad<TI, KT, false>(p, s);                      \
+    return p.N % kPack != 0 || p.P % kPack != 0 ? delta_grad<TI, KT, true>(p, s)    \
+                                                : delta_grad<TI, KT, false>(p, s);  \
   }
 
 }  // namespace swimba
