@@ -1355,28 +1355,33 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
 
     {
       float rs[4] = {}, cs[4];
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) {
-        cs[ct] = 0.f;
-        if (ct > rt) continue;
+      const int t = 16 * rt + 4 * g;
+      const f4x ht = *reinterpret_cast<const f4x*>(gHi + t);
+      const f4x lt = *reinterpret_cast<const f4x*>(gLo + t);
+      // pairs in tiles below the diagonal are all seen
+      auto slopes = [&](int ct, auto whole) {
+        constexpr bool ALL = decltype(whole)::value;
         const int s = 16 * ct + col;
         const float bs = gBeta[s], hs = gHi[s], ls = gLo[s];
+        float sum = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int t = 16 * rt + 4 * g + r;
-          const float d = fe[ct][r] * hw_exp2((gHi[t] - hs) + (gLo[t] - ls));
-          const float x = s < t ? d * sc[ct][r] : 0.f;
-          if (half) {
-            if (s < t) sM[s * kTriStride + t] = d * bs;
-          } else {
-            if (s <= t) sM[t * kTriStride + s] = d * bs;
-            if (s == t) diag[t] = d * sc[ct][r];
-          }
-          cs[ct] += x;
+          const float d = fe[ct][r] * hw_exp2((ht[r] - hs) + (lt[r] - ls));
+          const float y = d * sc[ct][r];
+          const float x = ALL || s < t + r ? y : 0.f;
+          // the other triangle's places of the diagonal's tile are the other half's
+          float* to = half ? sM + s * kTriStride + t + r : sM + (t + r) * kTriStride + s;
+          if (ALL || s < t + r || (half == 0 && s == t + r)) *to = d * bs;
+          if (!ALL && half == 0 && s == t + r) diag[s] = y;
+          sum += x;
           rs[r] = fmaf(x, bs, rs[r]);
         }
-        cs[ct] = column_sum(cs[ct]);
-      }
+        return column_sum(sum);
+      };
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct)
+        cs[ct] = ct < rt ? slopes(ct, std::true_type())
+                         : ct == rt ? slopes(ct, std::false_type()) : 0.f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) rs[r] = row_sum(rs[r]);
       if (half == 0) {
