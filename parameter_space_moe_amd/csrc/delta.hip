@@ -123,10 +123,10 @@ size_t tiny_bytes(const swimba_delta_rule_args* a) {
   return key_elements(a) < kPack || value_elements(a) < kPack ? 4 * kTinySlot : 0;
 }
 
-// Workspace of a forward call: per chunk and head the inverse, the scores and the gates.
+// Workspace of a forward call: per chunk and head the inverse and the gates.
 struct DeltaPlan {
   SegPlan seg;
-  size_t off_tri = 0, off_score = 0, off_gates = 0, off_tiny = 0, off_seg = 0, off_carry = 0,
+  size_t off_tri = 0, off_gates = 0, off_tiny = 0, off_seg = 0, off_carry = 0,
          bytes = 0;
 };
 
@@ -144,7 +144,6 @@ DeltaPlan plan_delta(const swimba_delta_rule_args* a, int dev) {
     return at;
   };
   r.off_tri = take(units * terms_of(a) * kTriBytes);
-  r.off_score = take(units * terms_of(a) * kTriBytes);
   r.off_gates = take(units * kGateBytes);
   r.off_tiny = take(tiny_bytes(a));
   const size_t N = padded_rows(a->N), segs = (size_t)a->B * a->H * (r.seg.nseg > 1 ? r.seg.nseg : 0);
@@ -159,7 +158,7 @@ struct DeltaGradPlan {
   SegPlan seg;
   int parts = 1;
   size_t off_seg = 0, off_carry = 0;
-  size_t off_tri = 0, off_tri_t = 0, off_score = 0, off_gates = 0, off_states = 0, off_adj = 0,
+  size_t off_tri = 0, off_tri_t = 0, off_gates = 0, off_states = 0, off_adj = 0,
          off_o = 0, off_dv = 0, off_dq = 0, off_dk = 0, off_part = 0, off_tiny = 0, bytes = 0;
 };
 
@@ -186,7 +185,6 @@ DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g, int dev) {
   };
   r.off_tri = take(units * kDeltaTerms * kTriBytes);
   r.off_tri_t = take(units * kDeltaTerms * kTriBytes);
-  r.off_score = take(units * kDeltaTerms * kTriBytes);
   r.off_gates = take(units * kGateBytes);
   r.off_states = take(units * padded_rows(a->N) * Pp * sizeof(float));
   r.off_adj = take(units * padded_rows(a->N) * Pp * sizeof(float));
@@ -379,7 +377,6 @@ int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, int dev, hipStr
   const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
   DeltaParams p = base_params(a, q, k, v);
   p.tri = at<bf16_t>(ws, r.off_tri);
-  p.score = at<bf16_t>(ws, r.off_score);
   p.gates = at<float>(ws, r.off_gates);
   p.out = a->y;
   p.out_bf16 = a->y_dtype == SWIMBA_BF16;
@@ -423,7 +420,6 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, i
   p.dy = whole_packs(g->dy, value_elements(a), f32, slot + 3 * kTinySlot, s, &rc);
   p.tri = at<bf16_t>(ws, r.off_tri);
   p.tri_t = at<bf16_t>(ws, r.off_tri_t);
-  p.score = at<bf16_t>(ws, r.off_score);
   p.gates = at<float>(ws, r.off_gates);
   p.out = g->dv;
   p.out_bf16 = g->grad_dtype == SWIMBA_BF16;

@@ -5,9 +5,10 @@
 // D[t][s] = e^{G_t - G_s}, w_s = e^{G_end - G_s} and o_t = u_t / beta_t:
 //   (I + A diag(beta)) O = V - e^G K h,   A[t][s] = D[t][s] k_t . k_s  for s < t
 //   y  = e^G Q h + ((Q K^T) * D) (beta O),   h' = e^{G_end} h + K^T (w beta O).
-// The 64 x 64 inverse T = (I + A diag(beta))^-1 and the decayed scores
-// S = (Q K^T) * D depend on no state: delta_prep_kernel makes them for every
-// chunk and head at once.  delta_walk_kernel carries the state through them.
+// The 64 x 64 inverse T = (I + A diag(beta))^-1 depends on no state: delta_prep_kernel
+// makes it for every chunk and head at once.  delta_walk_kernel carries the state through
+// them, with the decayed scores S = (Q K^T) * D, which it makes for itself (written out
+// by the preparation they cost as much memory traffic as T).
 // Backwards, with a = dL/dh' and dU = dL/d(beta O):
 //   dU = S^T dY + w K a,   dV = T^T (beta dU),
 //   a0 = e^{G_end} a + Q^T (e^G dY) - K^T (e^G dV),
@@ -38,7 +39,9 @@ typedef float f4x __attribute__((ext_vector_type(4)));
 constexpr int kDeltaBlocks = 6;               // 16 x 32 blocks of a triangle of 64 x 64
 constexpr int kDeltaTri = kDeltaBlocks * 512; // values of a triangle
 constexpr int kDeltaTerms = 3;
-constexpr int kDeltaGates = 4 * kChunk;       // floats: e^G, w, beta; e^{G_end}, first bad token
+// Of a chunk and head, 64 floats each: e^G, w, beta, (e^{G_end}, first bad token), and
+// G / ln 2 in a high and a low part.
+constexpr int kDeltaGates = 6 * kChunk;
 
 struct DeltaParams {
   const void *q, *k, *v, *dy;
@@ -54,7 +57,6 @@ struct DeltaParams {
   float* seg_carry;       // [B, H, nseg, N', N'] the segments' transitions (state pass)
   // workspace, per (b, h, chunk)
   bf16_t *tri, *tri_t;    // [terms, kDeltaTri] T in operand order; its transpose (backward)
-  bf16_t* score;          // [terms, kDeltaTri] S, or its transpose (backward)
   float* gates;           // [kDeltaGates]
   const float* s0;        // first state or null, [B, H, N, P]
   float* s_final;         // or null
@@ -344,7 +346,7 @@ __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) < __buil
 template <typename TI, int KT>
 constexpr size_t delta_prep_lds(bool back) {
   using Sh = DeltaShape<TI, KT>;
-  const size_t rows = 2 * (size_t)Sh::kTerms * Sh::kTile * sizeof(bf16_t);
+  const size_t rows = (size_t)Sh::kTerms * Sh::kTile * sizeof(bf16_t);
   const size_t tris = ((back ? 2 : 1) * (size_t)kChunk * kTriStride + kChunk * kDiagStride) *
                       sizeof(float);
   return (rows > tris ? rows : tris) + 4 * kChunk * sizeof(float);
@@ -352,10 +354,9 @@ constexpr size_t delta_prep_lds(bool back) {
 
 // One workgroup per chunk and head.  Tokens from the first one on whose k, beta or decay is not
 // finite leave the products, and the walk makes what it reaches NaN.  Wave w holds column
-// tile w of the scores K K^T, which go to LDS for the inverse, and of K Q^T (BACK: Q K^T),
-// whose accumulators are the triangle's operand register for register; while wave 0 inverts
-// the blocks on the diagonal the others write theirs.  BACK: for the gradients, S
-// transposed and T both ways.
+// tile w of the scores K K^T, which go to LDS for the inverse, and then block row w of T,
+// transposed, whose accumulators are the triangle's operand register for register.  BACK:
+// for the gradients, T both ways.
 template <typename TI, int KT, bool LOOSE, bool BACK, int TERMS>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p) {
   using Sh = DeltaShape<TI, KT>;
@@ -365,7 +366,6 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
   float* sG = reinterpret_cast<float*>(smem_raw);  // high and low parts of G, beta
   int* bad = reinterpret_cast<int*>(sG + 3 * kChunk);
   bf16_t* sK = reinterpret_cast<bf16_t*>(sG + 4 * kChunk);
-  bf16_t* sQ = sK + NT * Sh::kTile;
   float* sA = reinterpret_cast<float*>(sK);  // once the rows are done with: A^T
   float* sD = sA + kChunk * kTriStride;
   float* sT = sD + kChunk * kDiagStride;     // (BACK) T^T
@@ -377,11 +377,9 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
   const int b = bh / p.H, h = bh - b * p.H;
   const int t0 = c * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
 
-  typename Rows::Stage rk, rq;
+  typename Rows::Stage rk;
   Rows::place(rk, p.k, p, b, h / (p.H / p.G), t0, len, tid);
-  Rows::place(rq, p.q, p, b, h / (p.H / p.G), t0, len, tid);
   rk.load(0);
-  rq.load(0);
   if (tid == 0) *bad = kChunk;
   float gt = 0.f, bt = 0.f;
   if (wave == 0 && lane < len) {
@@ -406,6 +404,8 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
     gates[kChunk + lane] = exp2_sum(end - sum);
     gates[2 * kChunk + lane] = bt;
     if (lane == 0) gates[3 * kChunk] = exp2_sum(end);
+    gates[4 * kChunk + lane] = hi;
+    gates[5 * kChunk + lane] = (float)(sum - (double)hi);
   }
   static_assert(Rows::Stage::kRounds == 1, "rows in one round");
   if (rk.wild()) {
@@ -421,7 +421,6 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
     }
   }
   Rows::all(rk, sK);
-  Rows::all(rq, sQ);
   __syncthreads();
   const int first_bad = *bad;
   if (first_bad < kChunk) {
@@ -433,29 +432,19 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
   }
   if (tid == 0) p.gates[unit * kDeltaGates + 3 * kChunk + 1] = __int_as_float(first_bad);
 
-  f4x kk[4], qk[4];
+  f4x kk[4];
 #pragma unroll
-  for (int rt = 0; rt < 4; ++rt) {
-    kk[rt] = f4x{0.f, 0.f, 0.f, 0.f};
-    qk[rt] = f4x{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int rt = 0; rt < 4; ++rt) kk[rt] = f4x{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int n = 0; n < KT; ++n) {
-    bf8x bk[NT], bq[NT];
+    bf8x bk[NT];
     row_operand<Sh>(sK, 16 * wave, n, lane, bk);
-    if (!BACK) row_operand<Sh>(sQ, 16 * wave, n, lane, bq);
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
+      if (rt > wave) continue;
       bf8x a[NT];
-      if (rt <= wave) {
-        row_operand<Sh>(sK, 16 * rt, n, lane, a);
-        kk[rt] = mma_terms<NT, NT>(a, bk, kk[rt]);
-        if (!BACK) qk[rt] = mma_terms<NT, NT>(a, bq, qk[rt]);
-      }
-      if (BACK && rt >= wave) {
-        row_operand<Sh>(sQ, 16 * rt, n, lane, a);
-        qk[rt] = mma_terms<NT, NT>(a, bk, qk[rt]);
-      }
+      row_operand<Sh>(sK, 16 * rt, n, lane, a);
+      kk[rt] = mma_terms<NT, NT>(a, bk, kk[rt]);
     }
   }
   // decays: this lane's column, and four rows per tile
@@ -463,22 +452,15 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
   const float hi = sG[mine], lo = sG[kChunk + mine];
 #pragma unroll
   for (int rt = 0; rt < 4; ++rt) {
+    if (rt > wave) continue;
     const int row = 16 * rt + 4 * g;
     const f4x rh = *reinterpret_cast<const f4x*>(sG + row);
     const f4x rl = *reinterpret_cast<const f4x*>(sG + kChunk + row);
     const f4x rb = *reinterpret_cast<const f4x*>(sG + 2 * kChunk + row);
-    if (rt <= wave) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float d = hw_exp2((hi - rh[r]) + (lo - rl[r]));
-        kk[rt][r] = row + r < mine ? kk[rt][r] * d * rb[r] : 0.f;
-        if (!BACK) qk[rt][r] = row + r <= mine ? qk[rt][r] * d : 0.f;
-      }
-    }
-    if (BACK && rt >= wave) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        qk[rt][r] = row + r >= mine ? qk[rt][r] * hw_exp2((rh[r] - hi) + (rl[r] - lo)) : 0.f;
+    for (int r = 0; r < 4; ++r) {
+      const float d = hw_exp2((hi - rh[r]) + (lo - rl[r]));
+      kk[rt][r] = row + r < mine ? kk[rt][r] * d * rb[r] : 0.f;
     }
   }
   __syncthreads();  // the rows are done with
@@ -491,7 +473,6 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
   __syncthreads();
   const int64_t to = unit * TERMS * kDeltaTri;
   if (wave == 0) unit_blocks(sA, sD, lane);
-  put_tiles<TERMS, BACK>(qk, wave, p.score + to, lane);
   __syncthreads();
   f4x x[4];
   unit_row(sA, sD, wave, lane, x);
@@ -652,11 +633,11 @@ void delta_walk_kernel(DeltaParams p) {
   static_assert(Rows::Stage::kRounds == 1, "rows in one round");
   typename Rows::Stage rk, rq;
   TriStage<S, THREADS> tri;
-  TriStage<MODE == kDeltaOut ? 2 : S, THREADS> score;
   using Vals = RowStage<TI, COLS, THREADS, LOOSE>;
   static_assert(Vals::kRounds == 1, "values in one round");
   Vals rv;
-  float gate[kDeltaGates / THREADS];
+  constexpr int kGateLoads = (kDeltaGates + THREADS - 1) / THREADS;
+  float gate[kGateLoads];
   int next_bad = kChunk;
   auto fetch = [&](int j) {
     const int cc = chunk_of(j), t0 = cc * kChunk, len = p.L - t0 < kChunk ? p.L - t0 : kChunk;
@@ -667,12 +648,12 @@ void delta_walk_kernel(DeltaParams p) {
       Rows::place(rq, p.q, p, b, grp, t0, len, tid);
       rq.load(0);
     }
-    const int64_t tris = unit * S * kDeltaTri;
-    tri.load((BACK ? p.tri_t : p.tri) + tris, tid);
-    if (QUERY) score.load(p.score + tris, tid);
+    tri.load((BACK ? p.tri_t : p.tri) + unit * S * kDeltaTri, tid);
 #pragma unroll
-    for (int i = 0; i < kDeltaGates / THREADS; ++i)
-      gate[i] = p.gates[unit * kDeltaGates + i * THREADS + tid];
+    for (int i = 0; i < kGateLoads; ++i) {
+      const int e = i * THREADS + tid;
+      gate[i] = p.gates[unit * kDeltaGates + (e < kDeltaGates ? e : tid)];
+    }
     next_bad = __float_as_int(p.gates[unit * kDeltaGates + 3 * kChunk + 1]);
     const int64_t all = (int64_t)p.B * p.L * vstride;
     rv.base = static_cast<const TI*>(BACK ? p.dy : p.v);
@@ -738,9 +719,9 @@ void delta_walk_kernel(DeltaParams p) {
     Rows::all(rk, sK);
     if (QUERY) Rows::all(rq, sQ);
     tri.store(sT, tid);
-    if (QUERY) score.store(sS, tid);
 #pragma unroll
-    for (int i = 0; i < kDeltaGates / THREADS; ++i) sG[i * THREADS + tid] = gate[i];
+    for (int i = 0; i < kGateLoads; ++i)
+      if (i * THREADS + tid < kDeltaGates) sG[i * THREADS + tid] = gate[i];
     rv.store(0, sV, Lds::kValStride);
     __syncthreads();
     // stores before the loads that the next chunk waits for, not behind them
@@ -756,6 +737,62 @@ void delta_walk_kernel(DeltaParams p) {
             lane_at(to, (16 * i + r) * p.Pp + 16 * k, state_off) = st[k][i][r];
     }
     if (j + 1 < nj) fetch(j + 1);
+
+    // The decayed scores of K Q^T (walking back: of Q K^T), whose accumulators are the triangle's
+    // operand register for register: its six blocks of two tiles, two or three tiles per wave.
+    if constexpr (QUERY) {
+      static_assert(W == 4, "blocks by wave");
+      const int lane_now = apart(lane), col = lane_now & 15, g4 = 4 * (lane_now >> 4);
+      auto block = [&](int rt, int b) {  // operand row tile, 32-block
+        f4x sc[2];
+        sc[0] = sc[1] = f4x{0.f, 0.f, 0.f, 0.f};
+        const int mine = 16 * rt + col;
+        const float hi = sG[4 * kChunk + mine], lo = sG[5 * kChunk + mine];
+#pragma unroll
+        for (int n = 0; n < KT; ++n) {
+          bf8x bm[NT];
+          row_operand<Sh>(BACK ? sK : sQ, 16 * rt, n, lane_now, bm);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int t = 2 * b + x;
+            if (BACK ? t < rt : t > rt) continue;
+            bf8x a[NT];
+            row_operand<Sh>(BACK ? sQ : sK, 16 * t, n, lane_now, a);
+            sc[x] = mma_terms<NT, NT>(a, bm, sc[x]);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int t = 2 * b + x;
+          if (BACK ? t < rt : t > rt) continue;
+          const f4x rh = *reinterpret_cast<const f4x*>(sG + 4 * kChunk + 16 * t + g4);
+          const f4x rl = *reinterpret_cast<const f4x*>(sG + 5 * kChunk + 16 * t + g4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float e = BACK ? (rh[r] - hi) + (rl[r] - lo) : (hi - rh[r]) + (lo - rl[r]);
+            sc[x][r] *= hw_exp2(e);
+            if (t == rt && (BACK ? g4 + r < col : g4 + r > col)) sc[x][r] = 0.f;
+          }
+        }
+        bf8x v[YT];
+        split_tiles<YT>(sc[0], sc[1], v);
+        const int blk2 = BACK ? tri_block_t(rt, b) : tri_block(rt, b);
+#pragma unroll
+        for (int x = 0; x < YT; ++x)
+          *reinterpret_cast<bf8x*>(sS + x * kDeltaTri + (blk2 * 64 + lane_now) * 8) = v[x];
+      };
+      if constexpr (BACK) {
+        if (wave == 0) block(0, 0);
+        else if (wave == 1) { block(0, 1); block(3, 1); }
+        else if (wave == 2) { block(1, 0); block(1, 1); }
+        else block(2, 1);
+      } else {
+        if (wave == 0) block(3, 0);
+        else if (wave == 1) { block(3, 1); block(0, 0); }
+        else if (wave == 2) { block(2, 0); block(2, 1); }
+        else block(1, 0);
+      }
+    }
 
     // K h, and Q h, the next rows on their way
     f4x z[CT][4], y[CT][4];
@@ -796,6 +833,8 @@ void delta_walk_kernel(DeltaParams p) {
         }
       }
     }
+    if (QUERY) __syncthreads();  // the scores are there
+
     // this lane's columns of the values; an infinity or a NaN of v reaches its own column from
     // its token on
     f4x vv[CT][4];
@@ -823,7 +862,7 @@ void delta_walk_kernel(DeltaParams p) {
       }
       limit[k] = bad;
       if constexpr (!BACK) {
-        if (__ballot(!(odd == 0.f))) {
+        if (!unit_state && __ballot(!(odd == 0.f))) {
           __builtin_amdgcn_sched_barrier(0);
           int first = kChunk;
 #pragma unroll
