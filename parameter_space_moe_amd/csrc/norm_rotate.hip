@@ -273,21 +273,38 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   }
 }
 
-// dw[n] = sum over the workgroups' parts, in order, in 64 bits.  Four columns apart per row of
-// 64 threads.
-__global__ __launch_bounds__(256) void norm_weights_kernel(const float* part, float* dwq,
-                                                           float* dwk, int64_t blocks, int N) {
-  __shared__ double s[4][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), row = threadIdx.x >> 6;
+// dw[n] = sum over the workgroups' parts, in order, in 64 bits: 16 columns per workgroup, 64
+// threads in turn of each, eight parts of a thread on their way at once.
+constexpr int kSumRows = 64, kSumCols = 16;
+__global__ __launch_bounds__(kSumRows * kSumCols) void norm_weights_kernel(const float* part,
+                                                                          float* dwq, float* dwk,
+                                                                          int64_t blocks, int N) {
+  __shared__ double s[kSumRows][kSumCols];
+  const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;
+  const int c = blockIdx.x * kSumCols + col;
   double v = 0.0;
-  if (c < 2 * N)
-    for (int64_t i = row; i < blocks; i += 4) v += part[i * 2 * N + c];
-  s[row][threadIdx.x & 63] = v;
+  if (c < 2 * N) {
+    for (int64_t i = row; i < blocks; i += 8 * kSumRows) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int64_t at = i + u * kSumRows;
+        x[u] = part[(at < blocks ? at : 0) * 2 * N + c];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i + u * kSumRows < blocks) v += x[u];
+    }
+  }
+  s[row][col] = v;
   __syncthreads();
+  for (int w = kSumRows / 2; w > 0; w >>= 1) {
+    if (row < w) s[row][col] += s[row + w][col];
+    __syncthreads();
+  }
   if (row == 0 && c < 2 * N) {
-    v = (s[0][threadIdx.x] + s[1][threadIdx.x]) + (s[2][threadIdx.x] + s[3][threadIdx.x]);
     float* out = c < N ? dwq : dwk;
-    if (out != nullptr) out[c < N ? c : c - N] = (float)v;
+    if (out != nullptr) out[c < N ? c : c - N] = (float)s[0][col];
   }
 }
 
@@ -428,8 +445,10 @@ int launch_norm_rotate_backward(const swimba_norm_rotate_grad_args* g, void* ws,
     if (rc != SWIMBA_OK) return rc;
   }
   if (!weights) return SWIMBA_OK;
-  hipLaunchKernelGGL(norm_weights_kernel, dim3((unsigned)((2 * a->N + 63) / 64)), dim3(256), 0, s,
-                     part, g->dwq, g->dwk, a->T > 0 ? n.blocks * n.ysize : 0, a->N);
+  hipLaunchKernelGGL(norm_weights_kernel,
+                     dim3((unsigned)((2 * a->N + kSumCols - 1) / kSumCols)),
+                     dim3(kSumRows * kSumCols), 0, s, part, g->dwq, g->dwk,
+                     a->T > 0 ? n.blocks * n.ysize : 0, a->N);
   return checked();
 }
 

@@ -1220,6 +1220,8 @@ def _token_rows(t, name):
     if t.dim() < 2:
         raise ValueError("%s must be [..., heads, N]" % name)
     heads, N = t.shape[-2:]
+    if t.is_contiguous() and heads * N:
+        return t.numel() // (heads * N), heads, N, heads * N
     lead, strides = t.shape[:-2], t.stride()
     T = 1
     for n in lead:
@@ -1248,8 +1250,8 @@ def _norm_rotate_args(q, k, wq, wk, positions, rates, norm, pairs, eps, q_scale)
     a = NormRotateArgs()
     a.T, a.Hq, a.N, a.q_stride = _token_rows(q, "q")
     T, a.Hk, N, a.k_stride = _token_rows(k, "k")
-    dev, lead = q.device, tuple(q.shape[:-2])
-    if tuple(k.shape[:-2]) != lead or N != a.N or k.dtype != q.dtype or k.device != dev:
+    dev, lead = q.device, q.shape[:-2]
+    if k.shape[:-2] != lead or N != a.N or k.dtype != q.dtype or k.device != dev:
         raise ValueError("k must have the tokens, the head size, the dtype and the device of q")
     for name, t in (("wq", wq), ("wk", wk)):
         if t is not None:
@@ -1281,8 +1283,8 @@ def norm_rotate(q, k, wq=None, wk=None, positions=None, rates=None, norm="rms", 
     "rms" or "l2"; pairs: "halves" or "neighbours".  Returns (q_out, k_out), dense."""
     a = _norm_rotate_args(q, k, wq, wk, positions, rates, norm, pairs, eps, q_scale)
     dt = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
-    q_out = _new(q_out, "q_out", tuple(q.shape), dt, q.device)
-    k_out = _new(k_out, "k_out", tuple(k.shape), dt, q.device)
+    q_out = _new(q_out, "q_out", q.shape, dt, q.device)
+    k_out = _new(k_out, "k_out", k.shape, dt, q.device)
     a.out_dtype, a.q_out, a.k_out = _dt(q_out), _ptr(q_out), _ptr(k_out)
     _check("swimba_norm_rotate", load().swimba_norm_rotate(ctypes.byref(a), _current(q.device)))
     return q_out, k_out
