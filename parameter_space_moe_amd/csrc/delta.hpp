@@ -184,13 +184,20 @@ struct DeltaRows {
   using Stage = RowStage<TI, 32 * KT, THREADS, LOOSE>;
   using Sh = DeltaShape<TI, KT>;
   static __device__ __forceinline__ void put(const Stage& st, int round, bf16_t* dst) {
-#pragma unroll
-    for (int i = 0; i < Stage::kRound; ++i) put_one(st, round, i, dst);
+    if (!LOOSE && st.len == kChunk && st.cols >= Sh::kRows) put_as<true>(st, round, dst);
+    else put_as<false>(st, round, dst);
   }
-  static __device__ __forceinline__ void put_one(const Stage& st, int round, int i, bf16_t* dst) {
-    {
+  template <bool FULL>  // nothing to leave out
+  static __device__ __forceinline__ void put_as(const Stage& st, int round, bf16_t* dst) {
+#pragma unroll
+    for (int i = 0; i < Stage::kRound; ++i) {
       u4x w[Stage::kQuads];
-      st.pack(round, i, w);
+      if constexpr (FULL) {
+#pragma unroll
+        for (int q = 0; q < Stage::kQuads; ++q) w[q] = st.v[i][q];
+      } else {
+        st.pack(round, i, w);
+      }
       const int row = st.row(round * Stage::kRound + i);
       bf16_t* d = dst + Sh::place(row, st.column());
       bf16_t* d4 = dst + Sh::place(row, st.column() + 4);
