@@ -49,11 +49,6 @@ int padded_rows(int N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 2
 constexpr size_t kTriBytes = kDeltaTri * sizeof(bf16_t);  // of a term
 constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
 
-// Terms of what a call computes: two where inputs and y are bf16.
-int terms_of(const swimba_delta_rule_args* a) {
-  return a->in_dtype == SWIMBA_BF16 && a->y_dtype == SWIMBA_BF16 ? 2 : kDeltaTerms;
-}
-
 // Segments of the walks.  A walk's chunks follow each other; where the independent ones leave
 // CUs idle, they are cut into segments, whose transitions and ends are made first (a state
 // pass over the state's columns and as many more as it has rows) and joined.  Taken is the
@@ -81,15 +76,13 @@ SegPlan plan_segments(const swimba_delta_rule_args* a, bool back, int dev) {
   const int64_t nc = (a->L + kChunk - 1) / kChunk;
   const double cus = device_cus(dev), join = 0.45;
   const bool one = a->in_dtype == SWIMBA_F32 || a->N > 128;  // a CU's LDS
-  const bool out = !back && terms_of(a) == 2;
   auto time = [&](int64_t n) {
     const double len = (double)((nc + n - 1) / n), w = (double)(bh * tiles * n);
     const double walk = step_time(w, 0.6, 1.0, one ? 1 : 2, cus);
     double t = walk * (back ? 2.2 : 1.0);
     if (n > 1) {
       const double states = (double)(bh * (tiles + more) * (back ? n : n - 1));
-      t += out && !one ? step_time(states, 0.4, 0.8, 3, cus)
-                       : step_time(states, 0.45, 0.7, one ? 1 : 2, cus);
+      t += step_time(states, 0.45, 0.7, one ? 1 : 2, cus);
       if (back) t += 0.9 * step_time(w * (double)(n - 1) / (double)n, 0.6, 1.0, one ? 1 : 2, cus);
     }
     return len * t + (n > 1 ? (double)n * join * (back ? 2 : 1) + 2.0 : 0.0);
@@ -143,7 +136,7 @@ DeltaPlan plan_delta(const swimba_delta_rule_args* a, int dev) {
     o += align256(bytes);
     return at;
   };
-  r.off_tri = take(units * terms_of(a) * kTriBytes);
+  r.off_tri = take(units * kDeltaTerms * kTriBytes);
   r.off_gates = take(units * kGateBytes);
   r.off_tiny = take(tiny_bytes(a));
   const size_t N = padded_rows(a->N), segs = (size_t)a->B * a->H * (r.seg.nseg > 1 ? r.seg.nseg : 0);
@@ -389,7 +382,7 @@ int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, int dev, hipStr
   p.seg_carry = at<float>(ws, r.off_carry);
   if (rc == SWIMBA_OK) rc = phase(p, f32, kPhasePrep, s);
   if (rc == SWIMBA_OK)
-    rc = walk(p, f32, terms_of(a) == 2 ? kPhaseSegOut : kPhaseSeg, kPhaseOut, false, s);
+    rc = walk(p, f32, kPhaseSeg, kPhaseOut, false, s);
   return rc;
 }
 

@@ -26,8 +26,9 @@
 // product, and fp32 inputs, are three bf16 terms, which hold them within 2^-27 of their
 // size (2^-9 for each of three round-to-nearests); of a product of two such operands
 // the pairs of 2^-27 and below are left out.  Two terms (2^-18) take part in a y that is
-// rounded to bf16 anyway; with two in the states and gradients as well these were off by
-// 3 to 7e-6 in the 2-norm, a decay's gradient that cancels over the tokens by 1e-4.
+// rounded to bf16 anyway; with two in the states as well (1626 us for the 64K-token prompt
+// of 40 heads of 128 x 64 instead of 2015) these were off by 3e-6 in the 2-norm, gradients
+// by 7e-6, a decay's that cancels over the tokens by 1e-4: not taken.
 // Sums, states and inverses are fp32; sums of log decays are in 64 bits.
 #pragma once
 #include "attention.hpp"
@@ -56,7 +57,7 @@ struct DeltaParams {
   float* seg_state;       // [B, H, nseg, N', P'] end states out (state pass), first states in
   float* seg_carry;       // [B, H, nseg, N', N'] the segments' transitions (state pass)
   // workspace, per (b, h, chunk)
-  bf16_t *tri, *tri_t;    // [terms, kDeltaTri] T in operand order; its transpose (backward)
+  bf16_t *tri, *tri_t;    // [3, kDeltaTri] T in operand order; its transpose (backward)
   float* gates;           // [kDeltaGates]
   const float* s0;        // first state or null, [B, H, N, P]
   float* s_final;         // or null
@@ -364,7 +365,7 @@ constexpr size_t delta_prep_lds(bool back) {
 // tile w of the scores K K^T, which go to LDS for the inverse, and then block row w of T,
 // transposed, whose accumulators are the triangle's operand register for register.  BACK:
 // for the gradients, T both ways.
-template <typename TI, int KT, bool LOOSE, bool BACK, int TERMS>
+template <typename TI, int KT, bool LOOSE, bool BACK>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p) {
   using Sh = DeltaShape<TI, KT>;
   using Rows = DeltaRows<TI, KT, LOOSE>;
@@ -478,12 +479,12 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
     for (int r = 0; r < 4; ++r) sA[(16 * rt + 4 * g + r) * kTriStride + mine] = kk[rt][r];
   }
   __syncthreads();
-  const int64_t to = unit * TERMS * kDeltaTri;
+  const int64_t to = unit * kDeltaTerms * kDeltaTri;
   if (wave == 0) unit_blocks(sA, sD, lane);
   __syncthreads();
   f4x x[4];
   unit_row(sA, sD, wave, lane, x);
-  put_tiles<TERMS, false>(x, wave, p.tri + to, lane);
+  put_tiles<kDeltaTerms, false>(x, wave, p.tri + to, lane);
   if constexpr (BACK) {
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt)
@@ -495,7 +496,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       t[i] = *reinterpret_cast<const f4x*>(sT + mine * kTriStride + 16 * i + 4 * g);
-    put_tiles<TERMS, true>(t, wave, p.tri_t + to, lane);
+    put_tiles<kDeltaTerms, true>(t, wave, p.tri_t + to, lane);
   }
 }
 
@@ -507,24 +508,16 @@ enum DeltaMode {
   kDeltaKeep = 2,   // each chunk's first state, and O
   kDeltaBack = 3,   // dv, each chunk's last adjoint and dV, backwards
   kDeltaSeg = 4,    // only a segment's end state from zero, and its transition
-  kDeltaSegBack = 5,// only a segment's adjoint before it from zero
-  kDeltaSegOut = 6  // kDeltaSeg for kDeltaOut
+  kDeltaSegBack = 5 // only a segment's adjoint before it from zero
 };
-
-// Terms of what is computed: two where inputs and y are bf16.
-template <typename TI, int MODE>
-constexpr int delta_terms() {
-  return sizeof(TI) == 2 && (MODE == kDeltaOut || MODE == kDeltaSegOut) ? 2 : 3;
-}
 
 template <typename TI, int KT, int MODE, int COLS>
 struct DeltaLds {
   using Sh = DeltaShape<TI, KT>;
-  static constexpr bool kQ = MODE != kDeltaKeep && MODE != kDeltaSeg && MODE != kDeltaSegOut;
-  static constexpr int kTerms = delta_terms<TI, MODE>();
+  static constexpr bool kQ = MODE != kDeltaKeep && MODE != kDeltaSeg;
   static constexpr size_t kRows = (size_t)(kQ ? 2 : 1) * Sh::kTerms * Sh::kTile;
-  static constexpr int kScoreTerms = MODE == kDeltaOut ? 2 : kQ ? kTerms : 0;
-  static constexpr size_t kTris = (size_t)(kTerms + kScoreTerms) * kDeltaTri;
+  static constexpr int kScoreTerms = MODE == kDeltaOut ? 2 : kQ ? kDeltaTerms : 0;
+  static constexpr size_t kTris = (size_t)(kDeltaTerms + kScoreTerms) * kDeltaTri;
   // values: strides that spread the transposing reads over the banks
   static constexpr int kValStride = COLS + (Sh::kF32 ? 4 : 8);
   static constexpr size_t kVals = (size_t)kChunk * kValStride * (Sh::kF32 ? 4 : 2);
@@ -563,7 +556,7 @@ struct TriStage {
 template <typename TI, int KT, int MODE>
 constexpr int delta_waves_per_simd() {
   if (sizeof(TI) == 4 || KT > 4) return 1;
-  return MODE == kDeltaSegOut ? 3 : 2;
+  return 2;
 }
 
 template <typename TI, int KT, bool LOOSE, int MODE, int W, int CT>
@@ -577,10 +570,10 @@ void delta_walk_kernel(DeltaParams p) {
   constexpr int NT = Sh::kTerms, HT = 2 * KT;  // terms of inputs; 16-row tiles
   constexpr bool BACK = MODE == kDeltaBack || MODE == kDeltaSegBack, QUERY = Lds::kQ;
   constexpr bool OUT = MODE == kDeltaOut || MODE == kDeltaOutF32;
-  constexpr bool CARRY = MODE == kDeltaSeg || MODE == kDeltaSegOut;  // transitions too
+  constexpr bool CARRY = MODE == kDeltaSeg;  // transitions too
   constexpr bool SEG = CARRY || MODE == kDeltaSegBack;
   constexpr bool KEEP = MODE == kDeltaKeep || MODE == kDeltaBack;
-  constexpr int S = Lds::kTerms, YT = MODE == kDeltaOut ? 2 : S, QT = NT < YT ? NT : YT;
+  constexpr int S = kDeltaTerms, YT = MODE == kDeltaOut ? 2 : S, QT = NT < YT ? NT : YT;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
   bf16_t* sK = reinterpret_cast<bf16_t*>(smem_raw);
   bf16_t* sQ = sK + NT * Sh::kTile;  // (QUERY)
@@ -811,7 +804,9 @@ void delta_walk_kernel(DeltaParams p) {
         y[k][t] = f4x{0.f, 0.f, 0.f, 0.f};
       }
     {
-      constexpr int kSets = CARRY ? 1 : 2;  // a state pass has three waves to wait for each other
+      // two sets of operands where the registers allow it (with queries they spill: 64K-token
+      // prompt's walk 833 us, with one set 732 us)
+      constexpr int kSets = KEEP ? 2 : 1;
       bf8x ak[kSets][4][NT], aq[kSets][4][QT];
       auto rows = [&](int n) {
 #pragma unroll
@@ -892,26 +887,20 @@ void delta_walk_kernel(DeltaParams p) {
     // c += the triangle's (or its transpose's) product with values in terms
     auto triangle = [&](auto nt, auto nb, const bf16_t* tri_in, int m, auto& v, f4x (*acc)[4]) {
       constexpr int NA = decltype(nt)::value, NB = decltype(nb)::value;
-      bf8x a[4][NA];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (BACK ? t >= 2 * m + 2 : t < 2 * m) continue;
-        const int blk2 = BACK ? tri_block_t(t, m) : tri_block(t, m);
+      for (int t0 = 0; t0 < 4; t0 += 2) {  // operands of two tiles at a time
+        if (BACK ? t0 >= 2 * m + 2 : t0 < 2 * m) continue;
+        bf8x a[2][NA];
 #pragma unroll
-        for (int s = 0; s < NA; ++s)
-          a[t][s] = *reinterpret_cast<const bf8x*>(tri_in + s * kDeltaTri + blk2 * 512 + lane * 8);
-        if constexpr (CARRY) {
+        for (int t = 0; t < 2; ++t) {
+          const int blk2 = BACK ? tri_block_t(t0 + t, m) : tri_block(t0 + t, m);
 #pragma unroll
-          for (int k = 0; k < CT; ++k) mma_tiles<NA, NB, 1>(a + t, v[k], acc[k] + t);
-          if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // operands of two tiles at a time
+          for (int s = 0; s < NA; ++s)
+            a[t][s] =
+                *reinterpret_cast<const bf8x*>(tri_in + s * kDeltaTri + blk2 * 512 + lane * 8);
         }
-      }
-      if constexpr (CARRY) return;
 #pragma unroll
-      for (int k = 0; k < CT; ++k) {
-        if (BACK ? m == 1 : m == 0) mma_tiles<NA, NB, 4>(a, v[k], acc[k]);
-        else if (BACK) mma_tiles<NA, NB, 2>(a, v[k], acc[k]);
-        else mma_tiles<NA, NB, 2>(a + 2, v[k], acc[k] + 2);
+        for (int k = 0; k < CT; ++k) mma_tiles<NA, NB, 2>(a, v[k], acc[k] + t0);
       }
     };
     using Three = std::integral_constant<int, S>;
@@ -919,7 +908,7 @@ void delta_walk_kernel(DeltaParams p) {
     using OfInput = std::integral_constant<int, NT>;
     // state += columns of staged rows times values in terms
     auto update = [&](const bf16_t* tile_in, int m, auto& v) {
-      constexpr int kMost = CARRY ? 4 : 8, kAtOnce = NT == 1 ? (HT < kMost ? HT : kMost) : 2;
+      constexpr int kMost = 4, kAtOnce = NT == 1 ? (HT < kMost ? HT : kMost) : 2;
 #pragma unroll
       for (int i0 = 0; i0 < HT; i0 += kAtOnce) {
         bf8x a[kAtOnce][NT];
@@ -1562,12 +1551,12 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
 
 // ---- launches -------------------------------------------------------------------
 
-template <typename TI, int KT, bool LOOSE, bool BACK, int TERMS>
+template <typename TI, int KT, bool LOOSE, bool BACK>
 int delta_prep(const DeltaParams& p, hipStream_t s) {
   constexpr size_t lds = delta_prep_lds<TI, KT>(BACK);
   static_assert(lds <= 160 * 1024, "a CU's LDS");
-  allow_dynamic_lds(delta_prep_kernel<TI, KT, LOOSE, BACK, TERMS>, lds);
-  hipLaunchKernelGGL((delta_prep_kernel<TI, KT, LOOSE, BACK, TERMS>),
+  allow_dynamic_lds(delta_prep_kernel<TI, KT, LOOSE, BACK>, lds);
+  hipLaunchKernelGGL((delta_prep_kernel<TI, KT, LOOSE, BACK>),
                      dim3((unsigned)((int64_t)p.B * p.H * p.nc)), dim3(kDeltaThreads), lds, s, p);
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
@@ -1580,7 +1569,7 @@ int delta_walk(const DeltaParams& p, hipStream_t s) {
   constexpr int W = kWalkWaves, CT = kWalkTiles;
   constexpr size_t lds = DeltaLds<TI, KT, MODE, kWalkCols>::kBytes;
   static_assert(lds <= 160 * 1024, "a CU's LDS");
-  const int tiles = p.ctiles + (MODE == kDeltaSeg || MODE == kDeltaSegOut ? (32 * KT + kWalkCols - 1) / kWalkCols : 0);
+  const int tiles = p.ctiles + (MODE == kDeltaSeg ? (32 * KT + kWalkCols - 1) / kWalkCols : 0);
   const int segs = MODE >= kDeltaSeg ? p.state_segs : p.nseg;
   allow_dynamic_lds(delta_walk_kernel<TI, KT, LOOSE, MODE, W, CT>, lds);
   hipLaunchKernelGGL((delta_walk_kernel<TI, KT, LOOSE, MODE, W, CT>),
@@ -1600,25 +1589,20 @@ int delta_grad(const DeltaGradParams& p, hipStream_t s) {
 }
 
 enum DeltaPhase {
-  kPhasePrep, kPhasePrepBack, kPhaseOut, kPhaseKeep, kPhaseBack, kPhaseSeg, kPhaseSegOut,
-  kPhaseSegBack
+  kPhasePrep, kPhasePrepBack, kPhaseOut, kPhaseKeep, kPhaseBack, kPhaseSeg, kPhaseSegBack
 };
 
 template <typename TI, int KT, bool LOOSE>
 int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
   switch (phase) {
-    case kPhasePrep:  // in the terms of the walk
-      if (p.out_bf16)
-        return delta_prep<TI, KT, LOOSE, false, delta_terms<TI, kDeltaOut>()>(p, s);
-      return delta_prep<TI, KT, LOOSE, false, kDeltaTerms>(p, s);
-    case kPhasePrepBack: return delta_prep<TI, KT, LOOSE, true, kDeltaTerms>(p, s);
+    case kPhasePrep: return delta_prep<TI, KT, LOOSE, false>(p, s);
+    case kPhasePrepBack: return delta_prep<TI, KT, LOOSE, true>(p, s);
     case kPhaseOut:
       return p.out_bf16 ? delta_walk<TI, KT, LOOSE, kDeltaOut>(p, s)
                         : delta_walk<TI, KT, LOOSE, kDeltaOutF32>(p, s);
     case kPhaseKeep: return delta_walk<TI, KT, LOOSE, kDeltaKeep>(p, s);
     case kPhaseBack: return delta_walk<TI, KT, LOOSE, kDeltaBack>(p, s);
     case kPhaseSeg: return delta_walk<TI, KT, LOOSE, kDeltaSeg>(p, s);
-    case kPhaseSegOut: return delta_walk<TI, KT, LOOSE, kDeltaSegOut>(p, s);
     default: return delta_walk<TI, KT, LOOSE, kDeltaSegBack>(p, s);
   }
 }
