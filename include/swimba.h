@@ -620,18 +620,23 @@ typedef struct {
 /*
  * swimba_delta_rule -- the whole sequence, 64 tokens at a time on the matrix units.
  *   ws, ws_bytes: device workspace of at least
- *   swimba_delta_rule_workspace_size(a) bytes, 256-byte aligned.
+ *   swimba_delta_rule_workspace_size(a) bytes, 256-byte aligned: per 64 tokens and head
+ *   20 KB, and where a long sequence is walked in segments their states and
+ *   transitions.  Planned for the current device by the query and for the device of
+ *   `stream` by the call.
  * bf16 inputs multiply exactly; what is computed and fp32 inputs enter products as
  * three bf16 terms (within 2^-27 of their size; two, 2^-18, for what only reaches a
- * bf16 y); sums and states are fp32.  An infinity or
- * a NaN of q reaches its token's outputs, one of k, beta or a decay the outputs of
- * its token and all later ones of its sequence and head as NaN (one of v in its own
- * column only), also across a cleared state, and never an earlier token.
+ * bf16 y); sums and states are fp32.  An infinity or a NaN of q reaches its token's
+ * outputs, one of k, beta or a decay the outputs of its token and all later ones of
+ * its sequence and head as NaN (one of v in its own column only), also across a
+ * cleared state, and never an earlier token.
+ * Magnitudes: products of decays over up to 64 tokens (where log_decay is above 0),
+ * states, and the sums that make them and the results, below 1e38.
  * h_final may be h0 itself; otherwise no output overlaps an input or another
  * output.
  * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256 (128 with fp32
- * inputs), L <= 2^30, H * P and G * N < 2^23, B * H * max(ceil(P / 32), ceil(L / 64)) < 2^24 (SWIMBA_EUNSUPPORTED
- * above).  L == 0 writes h_final = h0 (or zeros).
+ * inputs), L <= 2^30, H * P and G * N < 2^23, B * H * max(ceil(P / 32), ceil(L / 64)) <
+ * 2^24 (SWIMBA_EUNSUPPORTED above).  L == 0 writes h_final = h0 (or zeros).
  */
 size_t swimba_delta_rule_workspace_size(const swimba_delta_rule_args* a);
 int swimba_delta_rule(const swimba_delta_rule_args* a, void* ws, size_t ws_bytes,
@@ -657,8 +662,9 @@ typedef struct {
  * of the forward pass is kept).  Workspace as there, sized by
  * swimba_delta_rule_backward_workspace_size(g) for the same arguments: per 64 tokens
  * and head two states of (N rounded up to a power of two) x (P to a multiple of 64)
- * floats, two sets of 64 rows of P and 55 KB; 8 B H L N bytes of rows per head where heads
- * share q and k.  Every output is deterministic.  All inputs must be finite (log_decay
+ * floats, two sets of 64 rows of P and 38 KB; and where heads share q and k and the
+ * sequences are short, rows of dq and dk for parts of the heads.  Every output is
+ * deterministic.  All inputs must be finite (log_decay
  * may be -INFINITY): an infinity or a NaN leaves the gradients of its sequence and
  * head, and of the heads that share its q and k, without meaning.
  * dh0 may be dh_final itself; otherwise no output overlaps an input or another

@@ -698,7 +698,7 @@ void delta_walk_kernel(DeltaParams p) {
       for (int k = 0; k < CT; ++k)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          lane_at(to, (16 * (i >> 2) + (i & 3)) * p.Pp + 16 * k, state_off) =
+          lane_at(to, (int64_t)(16 * (i >> 2) + (i & 3)) * p.Pp + 16 * k, state_off) =
               late[k][i >> 2][i & 3];
     }
     const int64_t first = vfirst + t0 * vstride;
@@ -734,7 +734,7 @@ void delta_walk_kernel(DeltaParams p) {
         for (int i = 0; i < HT; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            lane_at(to, (16 * i + r) * p.Pp + 16 * k, state_off) = st[k][i][r];
+            lane_at(to, (int64_t)(16 * i + r) * p.Pp + 16 * k, state_off) = st[k][i][r];
     }
     if (j + 1 < nj) fetch(j + 1);
 

@@ -128,6 +128,24 @@ def test_long(dtype, shape):
     check_backward(make(*shape, dtype=dtype, form="head", seed=8), dtype, "f32")
 
 
+@pytest.mark.parametrize("B,L,H,G", [(5, 3900, 4, 1), (8, 4200, 6, 2)])  # two heads, three heads at a time
+def test_heads_that_share_keys_are_summed(B, L, H, G):
+    check_backward(make(B, L, H, G, 16, 16, seed=9, reset=900), "bf16", "f32")
+
+
+def test_wide_keys_in_segments():
+    t = make(1, 900, 1, 1, 200, 20, seed=10, reset=500)
+    check_forward(t, "bf16", "f32")
+    check_backward(t, "bf16", "f32")
+
+
+def test_many_segments():
+    # and a last one that is shorter
+    t = make(1, 64 * 75 + 13, 1, 1, 32, 16, form="head", seed=16)
+    check_forward(t, "bf16", "f32")
+    check_backward(t, "bf16", "bf16")
+
+
 def test_a_document_is_its_own():
     # behind a cleared state nothing of the first document is left, whatever its size
     t = make(1, 100, 2, 1, 32, 32, dtype="f32", seed=13)
