@@ -52,11 +52,11 @@ constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
 // Segments of the walks.  A walk's chunks follow each other; where the independent ones leave
 // CUs idle, they are cut into segments, whose transitions and ends are made first (a state
 // pass over the state's columns and as many more as it has rows) and joined.  Taken is the
-// number of the least time, in units of a chunk's walk by a workgroup that shares its CU
-// (6.7 us with 128 keys; 4.1 us for one that has it alone).  Measured, whole against cut: 8 heads
-// of 64 x 64 over 32768 tokens 1346 / 168 us in 32 segments, one head of 128 x 128 over
-// 65536 tokens 3494 / 312 us in 48, 40 heads of 128 x 64 over 65536 tokens 4118 / 1754 us in
-// 12, 256 x 128 x 128 over 4096 tokens 596 / 898 us in 2.
+// number of the least time, in units of a chunk's walk by a workgroup that shares its CU.
+// Measured, whole against cut: 8 heads of 64 x 64 over 32768 tokens 1858 / 194 us in 32
+// segments, one head of 128 x 128 over 65536 tokens 4905 / 341 us in 48, 40 heads of 128 x 64
+// over 65536 tokens 5390 / 2039 us in 12, 256 heads of 128 x 128 over 4096 tokens 668 / 998 us
+// in 2.
 struct SegPlan {
   int nseg = 1, seg_chunks = 1;
 };
@@ -420,7 +420,6 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, i
   p.states = at<float>(ws, r.off_states);
   p.rows = at<float>(ws, r.off_o);
   p.nseg = r.seg.nseg;
-  p.state_segs = p.nseg - 1;  // the last one's end is not carried on
   p.seg_chunks = r.seg.seg_chunks;
   p.seg_state = at<float>(ws, r.off_seg);
   p.seg_carry = at<float>(ws, r.off_carry);

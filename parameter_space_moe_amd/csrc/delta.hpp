@@ -27,7 +27,7 @@
 // size (2^-9 for each of three round-to-nearests); of a product of two such operands
 // the pairs of 2^-27 and below are left out.  Two terms (2^-18) take part in a y that is
 // rounded to bf16 anyway; with two in the states as well (1626 us for the 64K-token prompt
-// of 40 heads of 128 x 64 instead of 2015) these were off by 3e-6 in the 2-norm, gradients
+// of 40 heads of 128 x 64 instead of 2039) these were off by 3e-6 in the 2-norm, gradients
 // by 7e-6, a decay's that cancels over the tokens by 1e-4: not taken.
 // Sums, states and inverses are fp32; sums of log decays are in 64 bits.
 #pragma once
@@ -1386,147 +1386,147 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
     // (addresses from here on are made anew for each head: kept over the loop they spill, and
     // a load of a spilled one waits for the next head's columns on their way)
     {
-    const int lane_now = apart(lane), g = lane_now >> 4, col = lane_now & 15;
+      const int lane_now = apart(lane), g = lane_now >> 4, col = lane_now & 15;
 
-    {
-      float rs[4] = {}, cs[4];
-      const int t = 16 * rt + 4 * g;
-      const f4x ht = *reinterpret_cast<const f4x*>(gHi + t);
-      const f4x lt = *reinterpret_cast<const f4x*>(gLo + t);
-      // pairs in tiles below the diagonal are all seen
-      auto slopes = [&](int ct, auto whole) {
-        constexpr bool ALL = decltype(whole)::value;
-        const int s = 16 * ct + col;
-        const float bs = gBeta[s], hs = gHi[s], ls = gLo[s];
-        float sum = 0.f;
+      {
+        float rs[4] = {}, cs[4];
+        const int t = 16 * rt + 4 * g;
+        const f4x ht = *reinterpret_cast<const f4x*>(gHi + t);
+        const f4x lt = *reinterpret_cast<const f4x*>(gLo + t);
+        // pairs in tiles below the diagonal are all seen
+        auto slopes = [&](int ct, auto whole) {
+          constexpr bool ALL = decltype(whole)::value;
+          const int s = 16 * ct + col;
+          const float bs = gBeta[s], hs = gHi[s], ls = gLo[s];
+          float sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float d = fe[ct][r] * hw_exp2((ht[r] - hs) + (lt[r] - ls));
-          const float y = d * sc[ct][r];
-          const float x = ALL || s < t + r ? y : 0.f;
-          // the other triangle's places of the diagonal's tile are the other half's
-          float* to = half ? sM + s * kTriStride + t + r : sM + (t + r) * kTriStride + s;
-          if (ALL || s < t + r || (half == 0 && s == t + r)) *to = d * bs;
-          if (!ALL && half == 0 && s == t + r) diag[s] = y;
-          sum += x;
-          rs[r] = fmaf(x, bs, rs[r]);
+          for (int r = 0; r < 4; ++r) {
+            const float d = fe[ct][r] * hw_exp2((ht[r] - hs) + (lt[r] - ls));
+            const float y = d * sc[ct][r];
+            const float x = ALL || s < t + r ? y : 0.f;
+            // the other triangle's places of the diagonal's tile are the other half's
+            float* to = half ? sM + s * kTriStride + t + r : sM + (t + r) * kTriStride + s;
+            if (ALL || s < t + r || (half == 0 && s == t + r)) *to = d * bs;
+            if (!ALL && half == 0 && s == t + r) diag[s] = y;
+            sum += x;
+            rs[r] = fmaf(x, bs, rs[r]);
+          }
+          return column_sum(sum);
+        };
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct)
+          cs[ct] = ct < rt ? slopes(ct, std::true_type())
+                           : ct == rt ? slopes(ct, std::false_type()) : 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rs[r] = row_sum(rs[r]);
+        if (half == 0) {
+          if (g == 0) {
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct) cols[rt * 64 + 16 * ct + col] = cs[ct];
+          }
+          if (col == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) row[16 * rt + 4 * g + r] = rs[r];
+          }
         }
-        return column_sum(sum);
+        __syncthreads();
+        if (half) {  // less those of E
+          if (g == 0) {
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct) cols[rt * 64 + 16 * ct + col] -= cs[ct];
+          }
+          if (col == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) row[16 * rt + 4 * g + r] -= rs[r];
+          }
+        }
+      }
+      auto element = [&](const bf16_t* tile, int t, int n) {
+        const bf16_t* at = tile + Sh::place(t, n & ~3) + (n & 3);
+        float v = to_f32(at[0]);
+#pragma unroll
+        for (int s = 1; s < NT; ++s) v += to_f32(at[s * Sh::kTile]);
+        return v;
       };
+      const f4x er = *reinterpret_cast<const f4x*>(gRead + 16 * rt + 4 * g);
+      const f4x ew = *reinterpret_cast<const f4x*>(gWrite + 16 * rt + 4 * g);
+      const f4x eb = *reinterpret_cast<const f4x*>(gBeta + 16 * rt + 4 * g);
 #pragma unroll
-      for (int ct = 0; ct < 4; ++ct)
-        cs[ct] = ct < rt ? slopes(ct, std::true_type())
-                         : ct == rt ? slopes(ct, std::false_type()) : 0.f;
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * rt + 4 * g + r;
+        float x = 0.f, w = 0.f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) rs[r] = row_sum(rs[r]);
-      if (half == 0) {
-        if (g == 0) {
-#pragma unroll
-          for (int ct = 0; ct < 4; ++ct) cols[rt * 64 + 16 * ct + col] = cs[ct];
+        for (int k = 0; k < KT; ++k) {
+          const int n = 16 * (half * KT + k) + col;
+          const float kn = element(sK, t, n), qn = element(sQ, t, n);
+          x += qn * reads[k][r] - kn * erased[k][r];
+          w = fmaf(kn, written[k][r], w);
         }
+        x = row_sum(x) * er[r];
+        w = row_sum(w) * ew[r];
         if (col == 0) {
+          seen[half * 64 + t] = x;
+          wrote[half * 64 + t] = w;
+        }
+      }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) row[16 * rt + 4 * g + r] = rs[r];
+      for (int k = 0; k < KT; ++k) {
+        dq[k] += reads[k] * er;
+        dk[k] += written[k] * (ew * eb) - erased[k] * er;
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int t = 16 * rt + col;
+        float fd[8], both[8], ft[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int s = 32 * m + 16 * (e >> 2) + 4 * g + (e & 3);
+          const float across = sM[t * kTriStride + s], down = sM[s * kTriStride + t];
+          fd[e] = s <= t ? across : 0.f;
+          ft[e] = s >= t ? down : 0.f;
+          both[e] = s == t ? 0.f : s < t ? -down : -across;
+        }
+        bf8x af[S], ae[S], at[S];
+        split_values<S>(fd, af);
+        split_values<S>(both, ae);
+        split_values<S>(ft, at);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          bf8x bk[NT], bq[NT];
+          column_operand<Sh>(sK, half * KT + k, m, lane_now, bk);
+          column_operand<Sh>(sQ, half * KT + k, m, lane_now, bq);
+          dq[k] = mma_terms<S, NT>(af, bk, dq[k]);
+          dk[k] = mma_terms<S, NT>(ae, bk, dk[k]);
+          dk[k] = mma_terms<S, NT>(at, bq, dk[k]);
         }
       }
       __syncthreads();
-      if (half) {  // less those of E
-        if (g == 0) {
+      if (wave == 0) {
+        const float down = cols[lane] + cols[64 + lane] + cols[128 + lane] + cols[192 + lane];
+        const float wr = wrote[lane] + wrote[64 + lane];
+        const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
+        if (lane < len) p.dbeta[at] = down + diag[lane] + wr;
+        const bool clear = lane < len && hw_exp2(gt * kLog2e) == 0.f;
+        const double slope = (double)bt * down - (double)row[lane];
+        const double upto = wave_prefix(slope) - slope;  // of the tokens before
+        const uint64_t mask = __ballot(clear) & (~0ull >> (63 - lane));
+        const int from = mask != 0 ? 63 - __clzll((long long)mask) : 0;
+        const double base = __shfl(upto, from);
+        const double sn = (double)seen[lane] + seen[64 + lane], wb = (double)bt * wr;
+        const double all_seen = wave_prefix(sn), all_wrote = wave_prefix(wb);
+        double ha = 0.0;
 #pragma unroll
-          for (int ct = 0; ct < 4; ++ct) cols[rt * 64 + 16 * ct + col] -= cs[ct];
+        for (int w = 0; w < kGradThreads / 64; ++w) ha += thru[w];
+        double dg = (upto - base) + (last_lane(all_seen) - all_seen + sn) + (all_wrote - wb) +
+                    (double)exp2_sum((double)gHi[63] + (double)gLo[63]) * ha;
+        if (clear || lane >= len) dg = 0.0;
+        if (p.dg != nullptr && lane < len) p.dg[at] = (float)dg;
+        if (p.part != nullptr) {
+          dg = wave_prefix(dg);
+          if (lane == 63) p.part[unit] = dg;
         }
-        if (col == 0) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) row[16 * rt + 4 * g + r] -= rs[r];
-        }
       }
     }
-    auto element = [&](const bf16_t* tile, int t, int n) {
-      const bf16_t* at = tile + Sh::place(t, n & ~3) + (n & 3);
-      float v = to_f32(at[0]);
-#pragma unroll
-      for (int s = 1; s < NT; ++s) v += to_f32(at[s * Sh::kTile]);
-      return v;
-    };
-    const f4x er = *reinterpret_cast<const f4x*>(gRead + 16 * rt + 4 * g);
-    const f4x ew = *reinterpret_cast<const f4x*>(gWrite + 16 * rt + 4 * g);
-    const f4x eb = *reinterpret_cast<const f4x*>(gBeta + 16 * rt + 4 * g);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * rt + 4 * g + r;
-      float x = 0.f, w = 0.f;
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        const int n = 16 * (half * KT + k) + col;
-        const float kn = element(sK, t, n), qn = element(sQ, t, n);
-        x += qn * reads[k][r] - kn * erased[k][r];
-        w = fmaf(kn, written[k][r], w);
-      }
-      x = row_sum(x) * er[r];
-      w = row_sum(w) * ew[r];
-      if (col == 0) {
-        seen[half * 64 + t] = x;
-        wrote[half * 64 + t] = w;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      dq[k] += reads[k] * er;
-      dk[k] += written[k] * (ew * eb) - erased[k] * er;
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int t = 16 * rt + col;
-      float fd[8], both[8], ft[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int s = 32 * m + 16 * (e >> 2) + 4 * g + (e & 3);
-        const float across = sM[t * kTriStride + s], down = sM[s * kTriStride + t];
-        fd[e] = s <= t ? across : 0.f;
-        ft[e] = s >= t ? down : 0.f;
-        both[e] = s == t ? 0.f : s < t ? -down : -across;
-      }
-      bf8x af[S], ae[S], at[S];
-      split_values<S>(fd, af);
-      split_values<S>(both, ae);
-      split_values<S>(ft, at);
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        bf8x bk[NT], bq[NT];
-        column_operand<Sh>(sK, half * KT + k, m, lane_now, bk);
-        column_operand<Sh>(sQ, half * KT + k, m, lane_now, bq);
-        dq[k] = mma_terms<S, NT>(af, bk, dq[k]);
-        dk[k] = mma_terms<S, NT>(ae, bk, dk[k]);
-        dk[k] = mma_terms<S, NT>(at, bq, dk[k]);
-      }
-    }
-    __syncthreads();
-    if (wave == 0) {
-      const float down = cols[lane] + cols[64 + lane] + cols[128 + lane] + cols[192 + lane];
-      const float wr = wrote[lane] + wrote[64 + lane];
-      const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
-      if (lane < len) p.dbeta[at] = down + diag[lane] + wr;
-      const bool clear = lane < len && hw_exp2(gt * kLog2e) == 0.f;
-      const double slope = (double)bt * down - (double)row[lane];
-      const double upto = wave_prefix(slope) - slope;  // of the tokens before
-      const uint64_t mask = __ballot(clear) & (~0ull >> (63 - lane));
-      const int from = mask != 0 ? 63 - __clzll((long long)mask) : 0;
-      const double base = __shfl(upto, from);
-      const double sn = (double)seen[lane] + seen[64 + lane], wb = (double)bt * wr;
-      const double all_seen = wave_prefix(sn), all_wrote = wave_prefix(wb);
-      double ha = 0.0;
-#pragma unroll
-      for (int w = 0; w < kGradThreads / 64; ++w) ha += thru[w];
-      double dg = (upto - base) + (last_lane(all_seen) - all_seen + sn) + (all_wrote - wb) +
-                  (double)exp2_sum((double)gHi[63] + (double)gLo[63]) * ha;
-      if (clear || lane >= len) dg = 0.0;
-      if (p.dg != nullptr && lane < len) p.dg[at] = (float)dg;
-      if (p.part != nullptr) {
-        dg = wave_prefix(dg);
-        if (lane == 63) p.part[unit] = dg;
-      }
-    }
-      }
   }
 #pragma unroll
   for (int k = 0; k < KT; ++k) {
