@@ -365,6 +365,8 @@ constexpr size_t delta_prep_lds(bool back) {
 // tile w of the scores K K^T, which go to LDS for the inverse, and then block row w of T,
 // transposed, whose accumulators are the triangle's operand register for register.  BACK:
 // for the gradients, T both ways.
+// 40960 chunks and heads of 128 keys in 300-310 us: 0.82 GB of T and gates written, and the
+// substitution in one wave while three wait, which other workgroups fill.
 template <typename TI, int KT, bool LOOSE, bool BACK>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p) {
   using Sh = DeltaShape<TI, KT>;
@@ -552,7 +554,12 @@ struct TriStage {
   }
 };
 
-// Two workgroups of four waves share a CU where LDS and 256 registers suffice.
+// Two workgroups of four waves share a CU where LDS and 256 registers suffice: the stages of a
+// chunk (rows to LDS, K h, T R, U, the state's update) follow each other, and one workgroup's
+// products run while the other waits.  A chunk of 128 keys and 64 columns takes 5.5 us alone
+// and 4.2 us as one of two; its matrix instructions are 1.3 us of that, vector issue and LDS
+// as much again each.  Eight waves on 128 columns share rows, T and scores, but their barriers
+// stop the whole CU: 256 heads of 128 x 128 over 4096 tokens 546 us, two workgroups 505.
 template <typename TI, int KT, int MODE>
 constexpr int delta_waves_per_simd() {
   if (sizeof(TI) == 4 || KT > 4) return 1;
@@ -1127,6 +1134,11 @@ struct GradLds {
 // of the keys; waves of half 0 also take row tile rt of F, of half 1 of E.  dY, O, dV, h
 // and a pass through LDS 32 columns at a time, split into terms once for all waves, the next
 // ones on their way in registers.
+// 2 x 4096 tokens, 32 heads of 128 x 128 over 4 key heads: 330-355 us, of which a head's four
+// column blocks are 60 % (the three-term products, one workgroup per CU for want of LDS and
+// registers), slopes 10 %, their products with K and Q 10 % and the sums behind them, in one
+// wave, 20 %.  Two workgroups per CU (128 registers) spill: 4 x 2048 tokens, 24 heads of
+// 64 x 64 in 270 us instead of 170.
 template <typename TI, int KT, bool LOOSE>
 __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParams p) {
   using Sh = DeltaShape<TI, KT>;
@@ -1607,11 +1619,11 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
   }
 }
 
-// One pair per dtype and padded row size.
 // First states of the segments, h(i + 1) = M_i h(i) + end(i), from the state pass's
 // transitions M (walking back: their transposes) and ends, in place.  Four waves take the
 // rows of 16 columns of one state in turn of 16-row tiles, in fp32 on the matrix units; the next
-// transition is on its way while one is applied.
+// transition is on its way while one is applied.  Bound by its chain: 3.7 us per segment of
+// 128 x 128 (12 segments of 40 heads in 42-45 us).
 template <int KT, bool BACK>
 __global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaParams p) {
   constexpr int N = 32 * KT, HT = 2 * KT, kMine = (HT + 3) / 4, kStride = N + 4;
@@ -1711,6 +1723,7 @@ int delta_carry(const DeltaParams& p, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
+// One pair per dtype and padded row size.
 #define SWIMBA_DELTA_DECL(name)                                       \
   int name(const DeltaParams& p, int phase, hipStream_t s);           \
   int name##_grad(const DeltaGradParams& p, hipStream_t s);

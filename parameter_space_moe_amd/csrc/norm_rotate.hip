@@ -10,6 +10,9 @@
 // heads of a few tokens and makes these tokens' cosines and sines once, in LDS: the
 // angle is a product in 64 bits, whose whole turns are taken off before it is rounded (at
 // position 10^6 an fp32 angle would be off by 0.06).  Everything else is fp32.
+// 65536 tokens of 48 heads of 64, bf16, all turned: 166 us, 4.85 TB/s (a copy: 5.3).  32768
+// tokens of 36 heads of 128: forward 113 us, 5.3 TB/s; backward 217 us, 4.2 TB/s.  256 tokens of
+// 80 heads of 128, not turned: 5.0 us.
 #include "pack.hpp"
 #include "swimba_internal.hpp"
 
@@ -274,7 +277,8 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
 }
 
 // dw[n] = sum over the workgroups' parts, in order, in 64 bits: 16 columns per workgroup, 64
-// threads in turn of each, eight parts of a thread on their way at once.
+// threads in turn of each, eight parts of a thread on their way at once.  1024 parts of 2 x 128
+// in 5 us (four threads per column: 67).
 constexpr int kSumRows = 64, kSumCols = 16;
 __global__ __launch_bounds__(kSumRows * kSumCols) void norm_weights_kernel(const float* part,
                                                                           float* dwq, float* dwk,
