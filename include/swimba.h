@@ -669,8 +669,8 @@ typedef struct {
  * head, and of the heads that share its q and k, without meaning.
  * dh0 may be dh_final itself; otherwise no output overlaps an input or another
  * output.
- * Constraints: those of swimba_delta_rule, and B * L * G * ceil(N / 8) below
- * 2^32 - 256.  L == 0 or B == 0 writes dh0 = dh_final (or zeros) and a zero
+ * Constraints: those of swimba_delta_rule, B * H * ceil(L / 64) < 2^23, and
+ * B * L * G * ceil(N / 8) below 2^32 - 256.  L == 0 or B == 0 writes dh0 = dh_final (or zeros) and a zero
  * dlog_decay [H].
  */
 size_t swimba_delta_rule_backward_workspace_size(const swimba_delta_rule_grad_args* g);
@@ -739,6 +739,7 @@ typedef struct {
 /*
  * swimba_norm_rotate -- sums of squares and everything else in fp32, angles in 64 bits
  * less their whole turns.  Rows are independent: what is not finite stays in its row.
+ * <x, x> is meant to stay below 3e38 (a row beyond it comes out as zeros).
  * q_out may be q itself (of the same dtype, dense rows), and k_out k; otherwise no
  * output overlaps an input or another output.
  * Constraints: T >= 0; Hq, Hk, N >= 1; 0 <= R <= N, even; eps a normal number above 0;

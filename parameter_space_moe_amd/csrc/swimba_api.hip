@@ -489,7 +489,6 @@ int validate_delta(int B, int L, int H, int G, int N, int P, swimba_dtype in, sw
                    swimba_decay_form form) {
   const int rc = validate_attention(B, L, H, G, N, P, in, out, form);
   if (rc != SWIMBA_OK) return rc;
-  if (in == SWIMBA_F32 && L > 1 && N > 128) return SWIMBA_EUNSUPPORTED;  // a CU's LDS
   // a launch of 256 threads per chunk and head
   if ((int64_t)B * H * ((L + 63LL) / 64) >= (1 << 24)) return SWIMBA_EUNSUPPORTED;
   return SWIMBA_OK;
@@ -497,8 +496,11 @@ int validate_delta(int B, int L, int H, int G, int N, int P, swimba_dtype in, sw
 
 int validate_delta(const swimba_delta_rule_args* a) {
   if (a == nullptr) return SWIMBA_EINVAL;
-  return validate_delta(a->B, a->L, a->H, a->G, a->N, a->P, a->in_dtype, a->y_dtype,
-                        a->decay_form);
+  const int rc = validate_delta(a->B, a->L, a->H, a->G, a->N, a->P, a->in_dtype, a->y_dtype,
+                                a->decay_form);
+  if (rc != SWIMBA_OK) return rc;
+  if (a->in_dtype == SWIMBA_F32 && a->N > 128) return SWIMBA_EUNSUPPORTED;  // a CU's LDS
+  return SWIMBA_OK;
 }
 
 int validate_delta_inputs(const swimba_delta_rule_args* a) {
@@ -518,6 +520,8 @@ int validate_delta_grad(const swimba_delta_rule_grad_args* g) {
   if (rc != SWIMBA_OK) return rc;
   if (!dtype_ok(g->grad_dtype)) return SWIMBA_EINVAL;
   const swimba_delta_rule_args& a = g->fwd;
+  // a launch of 512 threads per chunk and head
+  if ((int64_t)a.B * a.H * ((a.L + 63LL) / 64) >= (1 << 23)) return SWIMBA_EUNSUPPORTED;
   // threads of the launch that sums up the heads' rows
   if ((int64_t)a.B * a.L * a.G * ((a.N + 7) / 8) >= (int64_t(1) << 32) - 256)
     return SWIMBA_EUNSUPPORTED;

@@ -94,6 +94,27 @@ def test_delta_rule_refuses_wide_fp32_keys(lib):
         assert (lib.swimba_delta_rule_workspace_size(ctypes.byref(a)) > 0) == ok
 
 
+@pytest.mark.parametrize("L", (0, 1, 2, 64, 65))
+def test_delta_rule_refuses_wide_fp32_keys_at_any_length(lib, L):
+    for N, ok in ((128, True), (129, False), (256, False)):
+        a = delta_args(in_dtype=sw.F32, N=N, L=L)
+        want = (sw.OK if L == 0 else sw.EWORKSPACE) if ok else sw.EUNSUPPORTED
+        assert lib.swimba_delta_rule(ctypes.byref(a), None, 0, None) == want, N
+        if ok and L == 0:
+            continue  # (writes a zero dlog_decay where there is one per head)
+        g = grad_args({"in_dtype": sw.F32, "N": N, "L": L})
+        assert lib.swimba_delta_rule_backward(ctypes.byref(g), None, 0, None) == want, N
+
+
+def test_delta_rule_backward_refuses_more_chunks_than_a_launch_holds(lib):
+    """512 threads per chunk and head: the forward takes twice as many."""
+    for B, ok in (((1 << 22) - 1, True), (1 << 22, False)):
+        fwd = {"B": B, "L": 64, "H": 2, "N": 8, "P": 8}
+        assert lib.swimba_delta_rule(ctypes.byref(delta_args(**fwd)), None, 0, None) == sw.EWORKSPACE
+        want = sw.EWORKSPACE if ok else sw.EUNSUPPORTED
+        assert lib.swimba_delta_rule_backward(ctypes.byref(grad_args(fwd)), None, 0, None) == want, B
+
+
 def test_delta_rule_refuses_workspace(lib):
     a = delta_args()
     need = lib.swimba_delta_rule_workspace_size(ctypes.byref(a))
