@@ -628,7 +628,7 @@ typedef struct {
  * three bf16 terms (within 2^-27 of their size; two, 2^-18, for what only reaches a
  * bf16 y); sums and states are fp32.  An infinity or a NaN of q reaches its token's
  * outputs, one of k, beta or a decay the outputs of its token and all later ones of
- * its sequence and head as NaN (one of v in its own column only), also across a
+ * its sequence and head as NaN (one of v or h0 in its own column only), also across a
  * cleared state, and never an earlier token.
  * Magnitudes: products of decays over up to 64 tokens (where log_decay is above 0),
  * states, and the sums that make them and the results, below 1e38.

@@ -24,6 +24,7 @@ int checked() { return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP
 constexpr int kThreads = 256;
 constexpr int kPairs = 8;         // per lane
 constexpr int kTable = 2048;      // cosines and sines of a workgroup
+constexpr int kWeightStride = 2 * kPairs + 4;  // eight lanes' packs in different banks
 
 struct NormParams {
   const void *q, *k;              // x
@@ -146,6 +147,7 @@ __device__ __forceinline__ float lanes_sum(float v, int lane) {
 template <typename TI, typename TO, int LANES, bool WHOLE, bool NEIGHBOURS, bool BACK>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   __shared__ float2 table[kTable];
+  __shared__ __attribute__((aligned(16))) float weights[2 * LANES * kWeightStride];
   __shared__ float sums[BACK ? 4 * 2 * 2 * kPairs * LANES : 1];
   constexpr int kRowsAtOnce = kThreads / LANES;
   const int lane = threadIdx.x & (LANES - 1), r0 = threadIdx.x / LANES;
@@ -154,11 +156,17 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   const int h0 = (int)blockIdx.y * p.heads;
   const int heads = p.Hq + p.Hk - h0 < p.heads ? p.Hq + p.Hk - h0 : p.heads;
 
-  float wq[2 * kPairs], wk[2 * kPairs];
+  // the weights as the lanes take them, in LDS for the registers' sake
+  if (threadIdx.x < 2 * LANES) {
+    const float* w = threadIdx.x < LANES ? p.wq : p.wk;
+    float x[2 * kPairs];
 #pragma unroll
-  for (int i = 0; i < 2 * kPairs; ++i) wq[i] = wk[i] = 1.f;
-  if (p.wq != nullptr) mine.load(p.wq, wq, wq + kPairs);
-  if (p.wk != nullptr) mine.load(p.wk, wk, wk + kPairs);
+    for (int i = 0; i < 2 * kPairs; ++i) x[i] = 1.f;
+    if (w != nullptr) mine.load(w, x, x + kPairs);
+#pragma unroll
+    for (int i = 0; i < 2 * kPairs; ++i) weights[threadIdx.x * kWeightStride + i] = x[i];
+  }
+  __syncthreads();
   float dwq[2 * kPairs] = {}, dwk[2 * kPairs] = {};
 
   for (int64_t grp = blockIdx.x; grp < p.groups; grp += gridDim.x) {
@@ -192,12 +200,22 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
       sq = lanes_sum<LANES>(sq, (int)threadIdx.x & 63);
       const float r = __builtin_amdgcn_rsqf(fmaf(sq, p.c, p.eps));
       const float scale = isq ? p.q_scale : 1.f;
+      float w[2 * kPairs];
+#pragma unroll
+      for (int i = 0; i < 2 * kPairs; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(
+            weights + ((isq ? 0 : LANES) + lane) * kWeightStride + i);
+        w[i] = f.x;
+        w[i + 1] = f.y;
+        w[i + 2] = f.z;
+        w[i + 3] = f.w;
+      }
       if constexpr (!BACK) {
         const float f = r * scale;
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          a[i] *= f * (isq ? wq[i] : wk[i]);
-          b[i] *= f * (isq ? wq[kPairs + i] : wk[kPairs + i]);
+          a[i] *= f * w[i];
+          b[i] *= f * w[kPairs + i];
           const int pi = mine.pair(i);
           if (pi < half) {
             const float2 cs = table[t * half + pi];
@@ -226,8 +244,8 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
           dwk[i] += isq ? 0.f : da;
           dwq[kPairs + i] += isq ? db : 0.f;
           dwk[kPairs + i] += isq ? 0.f : db;
-          ga[i] *= isq ? wq[i] : wk[i];
-          gb[i] *= isq ? wq[kPairs + i] : wk[kPairs + i];
+          ga[i] *= w[i];
+          gb[i] *= w[kPairs + i];
           dot = fmaf(ga[i], a[i], fmaf(gb[i], b[i], dot));
         }
         dot = lanes_sum<LANES>(dot, (int)threadIdx.x & 63) * p.c;
