@@ -10,9 +10,9 @@
 // heads of a few tokens and makes these tokens' cosines and sines once, in LDS: the
 // angle is a product in 64 bits, whose whole turns are taken off before it is rounded (at
 // position 10^6 an fp32 angle would be off by 0.06).  Everything else is fp32.
-// 65536 tokens of 48 heads of 64, bf16, all turned: 166 us, 4.85 TB/s (a copy: 5.3).  32768
-// tokens of 36 heads of 128: forward 113 us, 5.3 TB/s; backward 217 us, 4.2 TB/s.  256 tokens of
-// 80 heads of 128, not turned: 5.0 us.
+// 65536 tokens of 48 heads of 64, bf16, all turned: 148 us, 5.4 TB/s (a copy: 5.3).  32768
+// tokens of 36 heads of 128: forward 102 us, 5.9 TB/s (a part of it from the caches); backward
+// 175 us, 5.2 TB/s.  256 tokens of 80 heads of 128, not turned: 5.0 us.
 #include "pack.hpp"
 #include "swimba_internal.hpp"
 
@@ -156,7 +156,8 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   const int h0 = (int)blockIdx.y * p.heads;
   const int heads = p.Hq + p.Hk - h0 < p.heads ? p.Hq + p.Hk - h0 : p.heads;
 
-  // the weights as the lanes take them, in LDS for the registers' sake
+  // the weights as the lanes take them, in LDS: in registers they cost the backward pass a
+  // wave per SIMD (145 instead of 121 registers; 217 us instead of 189)
   if (threadIdx.x < 2 * LANES) {
     const float* w = threadIdx.x < LANES ? p.wq : p.wk;
     float x[2 * kPairs];
@@ -353,8 +354,10 @@ NormGrid plan_norm(int64_t T, int H, int N, int R, bool back, int dev) {
   g.heads = H;
   while (g.heads > rows && T * ((H + g.heads - 1) / g.heads) < target) g.heads = (g.heads + 1) / 2;
   g.ysize = (H + g.heads - 1) / g.heads;
-  // rounds of rows that make the table worth while, if the tokens suffice
-  int64_t tokens = (8 * rows + g.heads - 1) / g.heads;
+  // Two rounds of rows, if the tokens suffice: fewer repeat the wait for the table, with more
+  // the workgroups' streams lie further apart (65536 tokens of 48 heads of 64: 168 us with one
+  // token, 148 with 3, 167 with 11, 184 with 32).
+  int64_t tokens = (2 * rows + g.heads - 1) / g.heads;
   if (tokens > T * g.ysize / target) tokens = T * g.ysize / target;
   if (half > 0 && tokens > kTable / half) tokens = kTable / half;
   g.tokens = tokens < 1 ? 1 : (int)tokens;
