@@ -621,7 +621,7 @@ typedef struct {
  * swimba_delta_rule -- the whole sequence, 64 tokens at a time on the matrix units.
  *   ws, ws_bytes: device workspace of at least
  *   swimba_delta_rule_workspace_size(a) bytes, 256-byte aligned: per 64 tokens and head
- *   20 KB, and where a long sequence is walked in segments their states and
+ *   14 KB, and where a long sequence is walked in segments their states and
  *   transitions.  Planned for the current device by the query and for the device of
  *   `stream` by the call.
  * bf16 inputs multiply exactly; what is computed and fp32 inputs enter products as
@@ -662,7 +662,7 @@ typedef struct {
  * of the forward pass is kept).  Workspace as there, sized by
  * swimba_delta_rule_backward_workspace_size(g) for the same arguments: per 64 tokens
  * and head two states of (N rounded up to a power of two) x (P to a multiple of 64)
- * floats, two sets of 64 rows of P and 38 KB; and where heads share q and k and the
+ * floats, two sets of 64 rows of P and 26 KB; and where heads share q and k and the
  * sequences are short, rows of dq and dk for parts of the heads.  Every output is
  * deterministic.  All inputs must be finite (log_decay
  * may be -INFINITY): an infinity or a NaN leaves the gradients of its sequence and

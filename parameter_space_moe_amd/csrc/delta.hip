@@ -46,7 +46,7 @@ int carry(const DeltaParams& p, bool back, hipStream_t s) {
 
 int padded_rows(int N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 
-constexpr size_t kTriBytes = kDeltaTri * sizeof(bf16_t);  // of a term
+constexpr size_t kTriBytes = kDeltaTri * sizeof(float);
 constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
 
 // Segments of the walks.  A walk's chunks follow each other; where the independent ones leave
@@ -55,7 +55,7 @@ constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
 // number of the least time, in units of a chunk's walk by a workgroup that shares its CU.
 // Measured, whole against cut: 8 heads of 64 x 64 over 32768 tokens 1858 / 194 us in 32
 // segments, one head of 128 x 128 over 65536 tokens 4905 / 341 us in 48, 40 heads of 128 x 64
-// over 65536 tokens 5390 / 2039 us in 12, 256 heads of 128 x 128 over 4096 tokens 668 / 998 us
+// over 65536 tokens 5390 / 2000 us in 12, 256 heads of 128 x 128 over 4096 tokens 625 / 998 us
 // in 2.
 struct SegPlan {
   int nseg = 1, seg_chunks = 1;
@@ -136,7 +136,7 @@ DeltaPlan plan_delta(const swimba_delta_rule_args* a, int dev) {
     o += align256(bytes);
     return at;
   };
-  r.off_tri = take(units * kDeltaTerms * kTriBytes);
+  r.off_tri = take(units * kTriBytes);
   r.off_gates = take(units * kGateBytes);
   r.off_tiny = take(tiny_bytes(a));
   const size_t N = padded_rows(a->N), segs = (size_t)a->B * a->H * (r.seg.nseg > 1 ? r.seg.nseg : 0);
@@ -176,8 +176,8 @@ DeltaGradPlan plan_delta_grad(const swimba_delta_rule_grad_args* g, int dev) {
     o += align256(bytes);
     return at;
   };
-  r.off_tri = take(units * kDeltaTerms * kTriBytes);
-  r.off_tri_t = take(units * kDeltaTerms * kTriBytes);
+  r.off_tri = take(units * kTriBytes);
+  r.off_tri_t = take(units * kTriBytes);
   r.off_gates = take(units * kGateBytes);
   r.off_states = take(units * padded_rows(a->N) * Pp * sizeof(float));
   r.off_adj = take(units * padded_rows(a->N) * Pp * sizeof(float));
@@ -370,7 +370,7 @@ int launch_delta_rule(const swimba_delta_rule_args* a, void* ws, int dev, hipStr
   const void* k = whole_packs(a->k, key_elements(a), f32, slot + kTinySlot, s, &rc);
   const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
   DeltaParams p = base_params(a, q, k, v);
-  p.tri = at<bf16_t>(ws, r.off_tri);
+  p.tri = at<float>(ws, r.off_tri);
   p.gates = at<float>(ws, r.off_gates);
   p.out = a->y;
   p.out_bf16 = a->y_dtype == SWIMBA_BF16;
@@ -412,8 +412,8 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, i
   const void* v = whole_packs(a->v, value_elements(a), f32, slot + 2 * kTinySlot, s, &rc);
   DeltaParams p = base_params(a, q, k, v);
   p.dy = whole_packs(g->dy, value_elements(a), f32, slot + 3 * kTinySlot, s, &rc);
-  p.tri = at<bf16_t>(ws, r.off_tri);
-  p.tri_t = at<bf16_t>(ws, r.off_tri_t);
+  p.tri = at<float>(ws, r.off_tri);
+  p.tri_t = at<float>(ws, r.off_tri_t);
   p.gates = at<float>(ws, r.off_gates);
   p.out = g->dv;
   p.out_bf16 = g->grad_dtype == SWIMBA_BF16;

@@ -27,7 +27,7 @@
 // size (2^-9 for each of three round-to-nearests); of a product of two such operands
 // the pairs of 2^-27 and below are left out.  Two terms (2^-18) take part in a y that is
 // rounded to bf16 anyway; with two in the states as well (1626 us for the 64K-token prompt
-// of 40 heads of 128 x 64 instead of 2039) these were off by 3e-6 in the 2-norm, gradients
+// of 40 heads of 128 x 64 instead of 2000) these were off by 3e-6 in the 2-norm, gradients
 // by 7e-6, a decay's that cancels over the tokens by 1e-4: not taken.
 // Sums, states and inverses are fp32; sums of log decays are in 64 bits.
 #pragma once
@@ -57,7 +57,7 @@ struct DeltaParams {
   float* seg_state;       // [B, H, nseg, N', P'] end states out (state pass), first states in
   float* seg_carry;       // [B, H, nseg, N', N'] the segments' transitions (state pass)
   // workspace, per (b, h, chunk)
-  bf16_t *tri, *tri_t;    // [3, kDeltaTri] T in operand order; its transpose (backward)
+  float *tri, *tri_t;     // [kDeltaTri] T in operand order; its transpose (backward)
   float* gates;           // [kDeltaGates]
   const float* s0;        // first state or null, [B, H, N, P]
   float* s_final;         // or null
@@ -100,34 +100,40 @@ __device__ __forceinline__ void mma_tiles(const bf8x (*a)[NA], const bf8x* b, f4
         if (n - i >= 0 && n - i < NB) c[m] = mma16(a[m][i], b[n - i], c[m]);
 }
 
-// x (8 values) as S bf16 terms, as split_terms() makes them.  What a pair of terms leaves is
-// one two-element product each, x - 1 * term + 0 * the other, which is exact: seven
+// x (V values, even) as S bf16 terms, as split_terms() makes them.  What a pair of terms leaves
+// is one two-element product each, x - 1 * term + 0 * the other, which is exact: seven
 // instructions for a pair's three terms instead of eleven.  The factors come from
 // registers: as constants in the instruction they are read as fp32 numbers.
-template <int S>
-__device__ __forceinline__ void split_values(const float* x, bf8x* out) {
+template <int S, int V>
+__device__ __forceinline__ void split_pairs(const float* x, uint32_t (*out)[V / 2]) {
   typedef __bf16 b2 __attribute__((ext_vector_type(2)));
   uint32_t first = 0x0000bf80u, second = 0xbf800000u;  // (-1, 0) and (0, -1)
   asm("" : "+s"(first), "+s"(second));
-  float r[8];
+  float r[V];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = x[i];
+  for (int i = 0; i < V; ++i) r[i] = x[i];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    Bits8 b;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b.w[i] = bf16_pair(r[2 * i], r[2 * i + 1]);
-    out[s] = __builtin_bit_cast(bf8x, b);
+    for (int i = 0; i < V / 2; ++i) out[s][i] = bf16_pair(r[2 * i], r[2 * i + 1]);
     if (s + 1 < S) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const b2 t = __builtin_bit_cast(b2, b.w[i]);
+      for (int i = 0; i < V / 2; ++i) {
+        const b2 t = __builtin_bit_cast(b2, out[s][i]);
         r[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(t, __builtin_bit_cast(b2, first), r[2 * i], false);
         r[2 * i + 1] =
             __builtin_amdgcn_fdot2_f32_bf16(t, __builtin_bit_cast(b2, second), r[2 * i + 1], false);
       }
     }
   }
+}
+
+template <int S>
+__device__ __forceinline__ void split_values(const float* x, bf8x* out) {
+  uint32_t w[S][4];
+  split_pairs<S, 8>(x, w);
+#pragma unroll
+  for (int s = 0; s < S; ++s) out[s] = __builtin_bit_cast(bf8x, u4x{w[s][0], w[s][1], w[s][2], w[s][3]});
 }
 
 // Two accumulator tiles as one operand in S terms.
@@ -275,18 +281,16 @@ __device__ __forceinline__ void column_operand(const bf16_t* tile, int nt, int b
 constexpr int kTriStride = kChunk + 4;
 
 // Blocks of a triangle whose row tile `rt` a wave holds, tile by tile (zero beyond the diagonal),
-// in operand order and in TERMS terms.
-template <int TERMS, bool TRANSPOSED>
-__device__ __forceinline__ void put_tiles(const f4x* tiles, int rt, bf16_t* out, int lane) {
+// in operand order.
+template <bool TRANSPOSED>
+__device__ __forceinline__ void put_tiles(const f4x* tiles, int rt, float* out, int lane) {
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     if (TRANSPOSED ? b < rt / 2 : b > rt / 2) continue;
-    bf8x t[TERMS];
-    split_tiles<TERMS>(tiles[2 * b], tiles[2 * b + 1], t);
     const int blk = TRANSPOSED ? tri_block_t(rt, b) : tri_block(rt, b);
-#pragma unroll
-    for (int s = 0; s < TERMS; ++s)
-      *reinterpret_cast<bf8x*>(out + s * kDeltaTri + (blk * 64 + lane) * 8) = t[s];
+    f4x* to = reinterpret_cast<f4x*>(out + (blk * 64 + lane) * 8);
+    to[0] = tiles[2 * b];
+    to[1] = tiles[2 * b + 1];
   }
 }
 
@@ -365,8 +369,9 @@ constexpr size_t delta_prep_lds(bool back) {
 // tile w of the scores K K^T, which go to LDS for the inverse, and then block row w of T,
 // transposed, whose accumulators are the triangle's operand register for register.  BACK:
 // for the gradients, T both ways.
-// 40960 chunks and heads of 128 keys in 300-310 us: 0.82 GB of T and gates written, and the
-// substitution in one wave while three wait, which other workgroups fill.
+// 40960 chunks and heads of 128 keys in 260-270 us: 0.57 GB of T and gates written, and the
+// substitution in one wave while three wait, which other workgroups fill.  (T written in
+// three terms was 0.82 GB and 310 us; the walks split it, which costs them 2 %.)
 template <typename TI, int KT, bool LOOSE, bool BACK>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p) {
   using Sh = DeltaShape<TI, KT>;
@@ -481,12 +486,12 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
     for (int r = 0; r < 4; ++r) sA[(16 * rt + 4 * g + r) * kTriStride + mine] = kk[rt][r];
   }
   __syncthreads();
-  const int64_t to = unit * kDeltaTerms * kDeltaTri;
+  const int64_t to = unit * kDeltaTri;
   if (wave == 0) unit_blocks(sA, sD, lane);
   __syncthreads();
   f4x x[4];
   unit_row(sA, sD, wave, lane, x);
-  put_tiles<kDeltaTerms, false>(x, wave, p.tri + to, lane);
+  put_tiles<false>(x, wave, p.tri + to, lane);
   if constexpr (BACK) {
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt)
@@ -498,7 +503,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       t[i] = *reinterpret_cast<const f4x*>(sT + mine * kTriStride + 16 * i + 4 * g);
-    put_tiles<kDeltaTerms, true>(t, wave, p.tri_t + to, lane);
+    put_tiles<true>(t, wave, p.tri_t + to, lane);
   }
 }
 
@@ -533,23 +538,26 @@ __device__ __forceinline__ T& lane_at(T* base, int64_t i, uint32_t off) {
   return *reinterpret_cast<T*>(reinterpret_cast<char*>(base + i) + off);
 }
 
-// The first TERMS terms of a triangle on their way to LDS.
-template <int TERMS, int THREADS>
+// A triangle on its way to LDS, where it lies in terms.
+template <int THREADS>
 struct TriStage {
-  static constexpr int kAll = TERMS * kDeltaTri / 8, kN = (kAll + THREADS - 1) / THREADS;
-  u4x v[kN];
-  __device__ __forceinline__ void load(const bf16_t* from, int tid) {
+  static constexpr int kN = kDeltaTri / 4 / THREADS;
+  static_assert(kN * 4 * THREADS == kDeltaTri, "whole rounds");
+  f4x v[kN];
+  __device__ __forceinline__ void load(const float* from, int tid) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = i * THREADS + tid;
-      v[i] = reinterpret_cast<const u4x*>(from)[e < kAll ? e : tid];
-    }
+    for (int i = 0; i < kN; ++i) v[i] = reinterpret_cast<const f4x*>(from)[i * THREADS + tid];
   }
   __device__ __forceinline__ void store(bf16_t* to, int tid) const {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int e = i * THREADS + tid;
-      if (kAll % THREADS == 0 || e < kAll) reinterpret_cast<u4x*>(to)[e] = v[i];
+      const float x[4] = {v[i][0], v[i][1], v[i][2], v[i][3]};
+      uint32_t w[kDeltaTerms][2];
+      split_pairs<kDeltaTerms, 4>(x, w);
+#pragma unroll
+      for (int s = 0; s < kDeltaTerms; ++s)
+        *reinterpret_cast<uint2*>(to + s * kDeltaTri + (i * THREADS + tid) * 4) =
+            make_uint2(w[s][0], w[s][1]);
     }
   }
 };
@@ -639,7 +647,7 @@ void delta_walk_kernel(DeltaParams p) {
 
   static_assert(Rows::Stage::kRounds == 1, "rows in one round");
   typename Rows::Stage rk, rq;
-  TriStage<S, THREADS> tri;
+  TriStage<THREADS> tri;
   using Vals = RowStage<TI, COLS, THREADS, LOOSE>;
   static_assert(Vals::kRounds == 1, "values in one round");
   Vals rv;
@@ -655,7 +663,7 @@ void delta_walk_kernel(DeltaParams p) {
       Rows::place(rq, p.q, p, b, grp, t0, len, tid);
       rq.load(0);
     }
-    tri.load((BACK ? p.tri_t : p.tri) + unit * S * kDeltaTri, tid);
+    tri.load((BACK ? p.tri_t : p.tri) + unit * kDeltaTri, tid);
 #pragma unroll
     for (int i = 0; i < kGateLoads; ++i) {
       const int e = i * THREADS + tid;
