@@ -625,8 +625,7 @@ typedef struct {
  *   transitions.  Planned for the current device by the query and for the device of
  *   `stream` by the call.
  * bf16 inputs multiply exactly; what is computed and fp32 inputs enter products as
- * three bf16 terms (within 2^-27 of their size; two, 2^-18, for what only reaches a
- * bf16 y); sums and states are fp32.  An infinity or a NaN of q reaches its token's
+ * three bf16 terms (within 2^-27 of their size); sums and states are fp32.  An infinity or a NaN of q reaches its token's
  * outputs, one of k, beta or a decay the outputs of its token and all later ones of
  * its sequence and head as NaN (one of v or h0 in its own column only), also across a
  * cleared state, and never an earlier token.

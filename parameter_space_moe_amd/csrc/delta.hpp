@@ -25,10 +25,12 @@
 // Roundings.  bf16 inputs multiply exactly.  What is computed in fp32 and enters a
 // product, and fp32 inputs, are three bf16 terms, which hold them within 2^-27 of their
 // size (2^-9 for each of three round-to-nearests); of a product of two such operands
-// the pairs of 2^-27 and below are left out.  Two terms (2^-18) take part in a y that is
-// rounded to bf16 anyway; with two in the states as well (1626 us for the 64K-token prompt
-// of 40 heads of 128 x 64 instead of 2000) these were off by 3e-6 in the 2-norm, gradients
-// by 7e-6, a decay's that cancels over the tokens by 1e-4: not taken.
+// the pairs of 2^-27 and below are left out.  Two terms (2^-18) leave 3e-6 of the states in
+// the 2-norm, 7e-6 of gradients, 1e-4 of a decay's that cancels over the tokens.  For a y in
+// bf16 they would do where it does not cancel, but one in 300 of its values is another
+// one then, and of sums |q| |h| that cancel to 2^-10 of them bits are lost: three there as well
+// (8 x 4096 tokens of 32 heads of 128 x 128: 680 us instead of 630; 64K tokens of 40 heads
+// of 128 x 64: 2053 instead of 1995).
 // Sums, states and inverses are fp32; sums of log decays are in 64 bits.
 #pragma once
 #include "attention.hpp"
@@ -510,12 +512,11 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prep_kernel(DeltaParams p
 // ---- the walk -------------------------------------------------------------------
 
 enum DeltaMode {
-  kDeltaOut = 0,    // y, in bf16
-  kDeltaOutF32 = 1, // y, in fp32
-  kDeltaKeep = 2,   // each chunk's first state, and O
-  kDeltaBack = 3,   // dv, each chunk's last adjoint and dV, backwards
-  kDeltaSeg = 4,    // only a segment's end state from zero, and its transition
-  kDeltaSegBack = 5 // only a segment's adjoint before it from zero
+  kDeltaOut = 0,    // y
+  kDeltaKeep = 1,   // each chunk's first state, and O
+  kDeltaBack = 2,   // dv, each chunk's last adjoint and dV, backwards
+  kDeltaSeg = 3,    // only a segment's end state from zero, and its transition
+  kDeltaSegBack = 4 // only a segment's adjoint before it from zero
 };
 
 template <typename TI, int KT, int MODE, int COLS>
@@ -523,8 +524,7 @@ struct DeltaLds {
   using Sh = DeltaShape<TI, KT>;
   static constexpr bool kQ = MODE != kDeltaKeep && MODE != kDeltaSeg;
   static constexpr size_t kRows = (size_t)(kQ ? 2 : 1) * Sh::kTerms * Sh::kTile;
-  static constexpr int kScoreTerms = MODE == kDeltaOut ? 2 : kQ ? kDeltaTerms : 0;
-  static constexpr size_t kTris = (size_t)(kDeltaTerms + kScoreTerms) * kDeltaTri;
+  static constexpr size_t kTris = (size_t)(kQ ? 2 : 1) * kDeltaTerms * kDeltaTri;
   // values: strides that spread the transposing reads over the banks
   static constexpr int kValStride = COLS + (Sh::kF32 ? 4 : 8);
   static constexpr size_t kVals = (size_t)kChunk * kValStride * (Sh::kF32 ? 4 : 2);
@@ -584,11 +584,11 @@ void delta_walk_kernel(DeltaParams p) {
   using Lds = DeltaLds<TI, KT, MODE, COLS>;
   constexpr int NT = Sh::kTerms, HT = 2 * KT;  // terms of inputs; 16-row tiles
   constexpr bool BACK = MODE == kDeltaBack || MODE == kDeltaSegBack, QUERY = Lds::kQ;
-  constexpr bool OUT = MODE == kDeltaOut || MODE == kDeltaOutF32;
+  constexpr bool OUT = MODE == kDeltaOut;
   constexpr bool CARRY = MODE == kDeltaSeg;  // transitions too
   constexpr bool SEG = CARRY || MODE == kDeltaSegBack;
   constexpr bool KEEP = MODE == kDeltaKeep || MODE == kDeltaBack;
-  constexpr int S = kDeltaTerms, YT = MODE == kDeltaOut ? 2 : S, QT = NT < YT ? NT : YT;
+  constexpr int S = kDeltaTerms;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
   bf16_t* sK = reinterpret_cast<bf16_t*>(smem_raw);
   bf16_t* sQ = sK + NT * Sh::kTile;  // (QUERY)
@@ -717,10 +717,9 @@ void delta_walk_kernel(DeltaParams p) {
               late[k][i >> 2][i & 3];
     }
     const int64_t first = vfirst + t0 * vstride;
-    if (MODE == kDeltaOut) leave_as(static_cast<bf16_t*>(p.out), first, len);
-    else if (MODE == kDeltaOutF32) leave_as(static_cast<float*>(p.out), first, len);
-    else if (MODE == kDeltaBack && p.out_bf16) leave_as(static_cast<bf16_t*>(p.out), first, len);
-    else if (MODE == kDeltaBack) leave_as(static_cast<float*>(p.out), first, len);
+    if ((OUT || MODE == kDeltaBack) && p.out_bf16)
+      leave_as(static_cast<bf16_t*>(p.out), first, len);
+    else if (OUT || MODE == kDeltaBack) leave_as(static_cast<float*>(p.out), first, len);
   };
   fetch(0);
 
@@ -789,11 +788,11 @@ void delta_walk_kernel(DeltaParams p) {
             if (t == rt && (BACK ? g4 + r < col : g4 + r > col)) sc[x][r] = 0.f;
           }
         }
-        bf8x v[YT];
-        split_tiles<YT>(sc[0], sc[1], v);
+        bf8x v[S];
+        split_tiles<S>(sc[0], sc[1], v);
         const int blk2 = BACK ? tri_block_t(rt, b) : tri_block(rt, b);
 #pragma unroll
-        for (int x = 0; x < YT; ++x)
+        for (int x = 0; x < S; ++x)
           *reinterpret_cast<bf8x*>(sS + x * kDeltaTri + (blk2 * 64 + lane_now) * 8) = v[x];
       };
       if constexpr (BACK) {
@@ -822,17 +821,12 @@ void delta_walk_kernel(DeltaParams p) {
       // two sets of operands where the registers allow it (with queries they spill: 64K-token
       // prompt's walk 833 us, with one set 732 us)
       constexpr int kSets = KEEP ? 2 : 1;
-      bf8x ak[kSets][4][NT], aq[kSets][4][QT];
+      bf8x ak[kSets][4][NT], aq[kSets][4][NT];
       auto rows = [&](int n) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           row_operand<Sh>(sK, 16 * t, n, lane, ak[n % kSets][t]);
-          if (OUT) {
-            bf8x a[NT];
-            row_operand<Sh>(sQ, 16 * t, n, lane, a);
-#pragma unroll
-            for (int i = 0; i < QT; ++i) aq[n % kSets][t][i] = a[i];
-          }
+          if (OUT) row_operand<Sh>(sQ, 16 * t, n, lane, aq[n % kSets][t]);
         }
       };
       if (kSets == 2) rows(0);
@@ -846,7 +840,7 @@ void delta_walk_kernel(DeltaParams p) {
 #pragma unroll
         for (int k = 0; k < CT; ++k) {
           mma_tiles<NT, S, 4>(ak[n % kSets], hb[k], z[k]);
-          if (OUT) mma_tiles<QT, YT, 4>(aq[n % kSets], hb[k], y[k]);
+          if (OUT) mma_tiles<NT, S, 4>(aq[n % kSets], hb[k], y[k]);
         }
       }
     }
@@ -919,7 +913,6 @@ void delta_walk_kernel(DeltaParams p) {
       }
     };
     using Three = std::integral_constant<int, S>;
-    using OfY = std::integral_constant<int, YT>;
     using OfInput = std::integral_constant<int, NT>;
     // state += columns of staged rows times values in terms
     auto update = [&](const bf16_t* tile_in, int m, auto& v) {
@@ -966,10 +959,10 @@ void delta_walk_kernel(DeltaParams p) {
       if (OUT) {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          bf8x ub[CT][YT];
+          bf8x ub[CT][S];
 #pragma unroll
-          for (int k = 0; k < CT; ++k) split_tiles<YT>(u[k][2 * m], u[k][2 * m + 1], ub[k]);
-          triangle(OfY(), OfY(), sS, m, ub, y);
+          for (int k = 0; k < CT; ++k) split_tiles<S>(u[k][2 * m], u[k][2 * m + 1], ub[k]);
+          triangle(Three(), Three(), sS, m, ub, y);
         }
       }
 #pragma unroll
@@ -1618,8 +1611,7 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
     case kPhasePrep: return delta_prep<TI, KT, LOOSE, false>(p, s);
     case kPhasePrepBack: return delta_prep<TI, KT, LOOSE, true>(p, s);
     case kPhaseOut:
-      return p.out_bf16 ? delta_walk<TI, KT, LOOSE, kDeltaOut>(p, s)
-                        : delta_walk<TI, KT, LOOSE, kDeltaOutF32>(p, s);
+      return delta_walk<TI, KT, LOOSE, kDeltaOut>(p, s);
     case kPhaseKeep: return delta_walk<TI, KT, LOOSE, kDeltaKeep>(p, s);
     case kPhaseBack: return delta_walk<TI, KT, LOOSE, kDeltaBack>(p, s);
     case kPhaseSeg: return delta_walk<TI, KT, LOOSE, kDeltaSeg>(p, s);
