@@ -630,7 +630,9 @@ typedef struct {
  * its sequence and head as NaN (one of v or h0 in its own column only), also across a
  * cleared state, and never an earlier token.
  * Magnitudes: products of decays over up to 64 tokens (where log_decay is above 0),
- * states, and the sums that make them and the results, below 1e38.
+ * states, and the sums that make them and the results, below 1e38; and, as long
+ * sequences are walked in segments, what decays above 0 and keys of beta |k|^2 > 2 make of
+ * a state of size one over the sequence, unless the state before is all zero.
  * h_final may be h0 itself; otherwise no output overlaps an input or another
  * output.
  * Constraints: B, L >= 0; H, G, N, P >= 1; H % G == 0; N <= 256 (128 with fp32

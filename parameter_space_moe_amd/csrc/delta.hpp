@@ -1623,7 +1623,8 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
 // transitions M (walking back: their transposes) and ends, in place.  Four waves take the
 // rows of 16 columns of one state in turn of 16-row tiles, in fp32 on the matrix units; the next
 // transition is on its way while one is applied.  Bound by its chain: 3.7 us per segment of
-// 128 x 128 (12 segments of 40 heads in 42-45 us).
+// 128 x 128 (12 segments of 40 heads in 42-45 us).  A transition that is not finite (growth
+// beyond fp32) leaves a column that is all zero so: 0 * NaN.
 template <int KT, bool BACK>
 __global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaParams p) {
   constexpr int N = 32 * KT, HT = 2 * KT, kMine = (HT + 3) / 4, kStride = N + 4;
@@ -1637,7 +1638,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaPara
   // (waves without a tile do the work of tile 0 again and keep nothing)
   auto tile = [&](int k) { return wave + 4 * k < HT ? wave + 4 * k : 0; };
   auto mine = [&](int k) { return wave + 4 * k < HT; };
-  f4x h[kMine], end[kMine], m[kMine][kPart];
+  f4x h[kMine], end[kMine], own_end[kMine], m[kMine][kPart];
   auto load_end = [&](int s) {
     const float* st = p.seg_state + (bh * p.nseg + s) * N * p.Pp + c;
 #pragma unroll
@@ -1689,7 +1690,7 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaPara
     __syncthreads();
     f4x a[kMine][kPart];
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) h[k] = end[k];
+    for (int k = 0; k < kMine; ++k) h[k] = own_end[k] = end[k];
     const bool more = s + 2 < p.nseg;
 #pragma unroll
     for (int part = 0; part < HT / kPart; ++part) {
@@ -1710,6 +1711,23 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaPara
         for (int r = 0; r < 4; ++r)
 #pragma unroll
           for (int k = 0; k < kMine; ++k) h[k] = mma16(a[k][n][r], b[r], h[k]);
+      }
+    }
+    bool wild = false;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) wild |= not_finite(h[k][r]);
+    if (__ballot(wild)) {
+      bool some = false;
+      for (int n = 4 * g; n < N; n += 16) {
+        const f4x b = *reinterpret_cast<const f4x*>(sH[s & 1] + col * kStride + n);
+        some |= !(b[0] == 0.f && b[1] == 0.f && b[2] == 0.f && b[3] == 0.f);
+      }
+      const uint64_t rows = __ballot(some);
+      if (((rows | rows >> 16 | rows >> 32 | rows >> 48) >> col & 1) == 0) {
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) h[k] = own_end[k];
       }
     }
   }
