@@ -665,9 +665,17 @@ typedef struct {
  * and head two states of (N rounded up to a power of two) x (P to a multiple of 64)
  * floats, two sets of 64 rows of P and 26 KB; and where heads share q and k and the
  * sequences are short, rows of dq and dk for parts of the heads.  Every output is
- * deterministic.  All inputs must be finite (log_decay
- * may be -INFINITY): an infinity or a NaN leaves the gradients of its sequence and
- * head, and of the heads that share its q and k, without meaning.
+ * deterministic.
+ * An infinity or a NaN of k, beta or a decay leaves NaN in dq, dk, dbeta and
+ * dlog_decay of its token and all later ones of its sequence and head, and, where
+ * dy from its token on or dh_final is not all zero, in dk, dbeta and dlog_decay of
+ * earlier tokens and, in the columns of P that this holds for, in dh0 and dv of
+ * earlier tokens.  Otherwise these are the gradients of the tokens before it: k, v,
+ * beta and decays behind the last token of a padded sequence may be anything.  One of
+ * v reaches dq, dk, dbeta and dlog_decay of its token and later ones; one of q or dy
+ * dk, dbeta, dlog_decay and dv of its token and earlier ones, dh0, and its own
+ * token's dq, one of dy its own column of dv and dh0 only.  (dk, dbeta, dlog_decay and dv
+ * of up to 63 tokens behind it may come out not finite, too.)
  * dh0 may be dh_final itself; otherwise no output overlaps an input or another
  * output.
  * Constraints: those of swimba_delta_rule, B * H * ceil(L / 64) < 2^23, and

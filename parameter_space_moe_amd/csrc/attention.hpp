@@ -278,6 +278,25 @@ struct RowStage {
     }
   }
 
+  // Zeros in their place.
+  __device__ __forceinline__ void drop_wild() {
+#pragma unroll
+    for (int i = 0; i < kRound; ++i)
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w = v[i][q][k];
+          if constexpr (sizeof(T) == 2) {
+            if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+            if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+          } else {
+            if ((w & 0x7f800000u) == 0x7f800000u) w = 0;
+          }
+          v[i][q][k] = w;
+        }
+  }
+
   __device__ __forceinline__ void store(int round, T* dst, int dst_stride) const {
     T* d = dst + row(round * kRound) * dst_stride + column();
     if (!LOOSE && len == kChunk && cols >= PAD) {  // nothing to leave out

@@ -452,6 +452,7 @@ int launch_delta_rule_backward(const swimba_delta_rule_grad_args* g, void* ws, i
   d.nc = p.nc;
   d.parts = r.parts;
   d.heads = a->H / a->G / r.parts;
+  d.gates = p.gates;
   d.states = at<float>(ws, r.off_states);
   d.adjoints = at<float>(ws, r.off_adj);
   d.o = at<float>(ws, r.off_o);

@@ -729,7 +729,8 @@ void delta_walk_kernel(DeltaParams p) {
     __syncthreads();  // everyone is done with the last chunk
     // tokens from the first bad one on leave the products
     const int bad = next_bad;
-    rk.len = rv.len = bad < len ? bad : len;
+    rk.len = bad < len ? bad : len;
+    if (!BACK) rv.len = rk.len;
     Rows::all(rk, sK);
     if (QUERY) Rows::all(rq, sQ);
     tri.store(sT, tid);
@@ -994,6 +995,23 @@ void delta_walk_kernel(DeltaParams p) {
         }
       }
     } else {
+      // A bad token reaches the adjoints and dV of those columns that anything behind it reaches
+      bool reached[CT];
+#pragma unroll
+      for (int k = 0; k < CT; ++k) {
+        reached[k] = false;
+        if (bad >= len) continue;  // (uniform)
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < HT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) some |= !(st[k][i][r] == 0.f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          some |= 16 * (i >> 2) + 4 * g + (i & 3) >= bad && !(vv[k][i >> 2][i & 3] == 0.f);
+        const uint64_t rows = __ballot(some);
+        reached[k] = ((rows | rows >> 16 | rows >> 32 | rows >> 48) >> (lane & 15) & 1) != 0;
+      }
       // dU = w K a + S^T dY, dV = T^T (beta dU)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -1041,6 +1059,15 @@ void delta_walk_kernel(DeltaParams p) {
       for (int k = 0; k < CT; ++k)
 #pragma unroll
         for (int t = 0; t < 4; ++t) late[k][t] = o[k][t];
+#pragma unroll
+      for (int k = 0; k < CT; ++k) {
+        if (bad >= len || !reached[k]) continue;
+        const float nan = __builtin_nanf("");
+#pragma unroll
+        for (int i = 0; i < HT; ++i) st[k][i] = f4x{nan, nan, nan, nan};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) late[k][t] = f4x{nan, nan, nan, nan};
+      }
     }
   }
   if (!SEG) leave(chunk_of(nj - 1));
@@ -1078,6 +1105,7 @@ struct DeltaGradParams {
   int B, L, H, G, N, P, Pp;
   int token_decay, nc;
   int parts, heads;                // workgroups of a group of heads that share q and k, heads each
+  const float* gates;              // [kDeltaGates] of each chunk and head, for its first bad token
   const float *states, *adjoints;  // [N', P'] before and behind each chunk
   const float *o, *dv;             // [64, P']
   void *dq, *dk;                   // [B, L, G, parts, N]
@@ -1140,6 +1168,9 @@ struct GradLds {
 // registers), slopes 10 %, their products with K and Q 10 % and the sums behind them, in one
 // wave, 20 %.  Two workgroups per CU (128 registers) spill: 4 x 2048 tokens, 24 heads of
 // 64 x 64 in 270 us instead of 170.
+// From the first bad token on (whose k, beta or decay is not finite) gradients are NaN; earlier
+// tokens see the chunk without it, and the NaN that the walk back leaves in dV and a where it
+// reaches them.
 template <typename TI, int KT, bool LOOSE>
 __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParams p) {
   using Sh = DeltaShape<TI, KT>;
@@ -1189,6 +1220,8 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
     typename Rows::Stage st;
     Rows::place(st, half ? p.q : p.k, rp, b, grp, t0, len, tid & (kGradThreads / 2 - 1));
     st.load(0);
+    static_assert(Rows::Stage::kRounds == 1, "rows in one round");
+    if (!half && st.wild()) st.drop_wild();
     Rows::all(st, half ? sQ : sK);
   }
 
@@ -1201,6 +1234,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
   Pack8 ro, rh[kStatePacks], ra[kStatePacks];
   Pack<TI> ry;
   float gt = 0.f, bt = 0.f, next_g = 0.f, next_b = 0.f;
+  int bad = kChunk, next_bad = kChunk;
   auto load8 = [](const float* at) {
     Pack8 v;
     v.a = *reinterpret_cast<const f4x*>(at);
@@ -1225,6 +1259,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
       rh[k] = load8(p.states + at);
       ra[k] = load8(p.adjoints + at);
     }
+    if (m == 0) next_bad = __float_as_int(p.gates[unit * kDeltaGates + 3 * kChunk + 1]);
     if (m == 0 && wave == 0 && lane < len) {
       const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h0 + i;
       next_g = p.token_decay ? p.g[at] : p.g[h0 + i];
@@ -1291,8 +1326,9 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
     for (int m = 0; m < blocks; ++m) {
       __syncthreads();  // everyone is done with the last ones
       if (m == 0) {
-        gt = next_g;
-        bt = next_b;
+        bad = next_bad;
+        gt = lane < bad ? next_g : 0.f;
+        bt = lane < bad ? next_b : 0.f;
         if (wave == 0) {
           const double d = (double)gt * 1.4426950408889634;
           const double sum = wave_prefix(d < (double)kLeastLog2 ? (double)kLeastLog2 : d);
@@ -1305,6 +1341,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
           gBeta[lane] = bt;
         }
       }
+      if (half == 0 && trow >= bad) ro.a = ro.b = f4x{0.f, 0.f, 0.f, 0.f};
       put(ro, (half ? sV : sO) + place(trow, tslot), kTokenTerm);
       if (half == 0) {
         const bool in = LOOSE || (trow < len && 32 * m + 8 * tslot < p.P);
@@ -1486,6 +1523,12 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
       for (int k = 0; k < KT; ++k) {
         dq[k] += reads[k] * er;
         dk[k] += written[k] * (ew * eb) - erased[k] * er;
+        if (bad < len) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (16 * rt + 4 * g + r >= bad) dq[k][r] = dk[k][r] = __builtin_nanf("");
+          }
+        }
       }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -1518,7 +1561,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
         const float down = cols[lane] + cols[64 + lane] + cols[128 + lane] + cols[192 + lane];
         const float wr = wrote[lane] + wrote[64 + lane];
         const int64_t at = ((int64_t)b * p.L + t0 + lane) * p.H + h;
-        if (lane < len) p.dbeta[at] = down + diag[lane] + wr;
+        if (lane < len) p.dbeta[at] = lane < bad ? down + diag[lane] + wr : __builtin_nanf("");
         const bool clear = lane < len && hw_exp2(gt * kLog2e) == 0.f;
         const double slope = (double)bt * down - (double)row[lane];
         const double upto = wave_prefix(slope) - slope;  // of the tokens before
@@ -1532,6 +1575,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
         for (int w = 0; w < kGradThreads / 64; ++w) ha += thru[w];
         double dg = (upto - base) + (last_lane(all_seen) - all_seen + sn) + (all_wrote - wb) +
                     (double)exp2_sum((double)gHi[63] + (double)gLo[63]) * ha;
+        if (lane >= bad) dg = __builtin_nan("");
         if (clear || lane >= len) dg = 0.0;
         if (p.dg != nullptr && lane < len) p.dg[at] = (float)dg;
         if (p.part != nullptr) {
@@ -1623,8 +1667,8 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
 // transitions M (walking back: their transposes) and ends, in place.  Four waves take the
 // rows of 16 columns of one state in turn of 16-row tiles, in fp32 on the matrix units; the next
 // transition is on its way while one is applied.  Bound by its chain: 3.7 us per segment of
-// 128 x 128 (12 segments of 40 heads in 42-45 us).  A transition that is not finite (growth
-// beyond fp32) leaves a column that is all zero so: 0 * NaN.
+// 128 x 128 (12 segments of 40 heads in 42-45 us).  A transition that is not finite (a bad token
+// in the segment, or growth beyond fp32) leaves a column that is all zero so: 0 * NaN.
 template <int KT, bool BACK>
 __global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaParams p) {
   constexpr int N = 32 * KT, HT = 2 * KT, kMine = (HT + 3) / 4, kStride = N + 4;
