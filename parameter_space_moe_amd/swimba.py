@@ -1137,6 +1137,14 @@ def delta_rule_workspace_bytes(q, k, v, log_decay, beta):
         return int(load().swimba_delta_rule_workspace_size(ctypes.byref(a)))
 
 
+def delta_rule_backward_workspace_bytes(q, k, v, log_decay, beta):
+    """Workspace bytes delta_rule_backward needs for these shapes."""
+    g = DeltaRuleGradArgs()
+    g.fwd = _delta_rule_args(q, k, v, log_decay, beta, None, None, None, need_y=False)
+    with torch.cuda.device(v.device):
+        return int(load().swimba_delta_rule_backward_workspace_size(ctypes.byref(g)))
+
+
 @_placed
 def delta_rule_backward(q, k, v, log_decay, beta, dy, h0=None, dh_final=None, want_dh0=True,
                         grad_dtype=torch.float32, out=None, workspace=None):
@@ -1288,6 +1296,15 @@ def norm_rotate(q, k, wq=None, wk=None, positions=None, rates=None, norm="rms", 
     a.out_dtype, a.q_out, a.k_out = _dt(q_out), _ptr(q_out), _ptr(k_out)
     _check("swimba_norm_rotate", load().swimba_norm_rotate(ctypes.byref(a), _current(q.device)))
     return q_out, k_out
+
+
+def norm_rotate_backward_workspace_bytes(q, k, wq=None, wk=None, positions=None, rates=None):
+    """Workspace bytes norm_rotate_backward needs for these shapes and weights."""
+    g = NormRotateGradArgs()
+    g.fwd = _norm_rotate_args(q, k, wq, wk, positions, rates, "rms", "halves", 1e-6, 1.0)
+    g.dwq, g.dwk = _ptr(wq), _ptr(wk)  # (only whether they are there)
+    with torch.cuda.device(q.device):
+        return int(load().swimba_norm_rotate_backward_workspace_size(ctypes.byref(g)))
 
 
 @_placed
