@@ -185,12 +185,13 @@ struct DeltaShape {
 };
 
 constexpr int kDeltaThreads = 256, kDeltaWaves = 4;
+constexpr int kWalkCols = 16 * kDeltaWaves;  // columns of a walk's workgroup, 16 of a wave
 
 // The staged rows of a chunk into LDS, in operand order and in terms; rows from `len` on
 // are zero.
-template <typename TI, int KT, bool LOOSE, int THREADS = kDeltaThreads>
+template <typename TI, int KT, bool LOOSE>
 struct DeltaRows {
-  using Stage = RowStage<TI, 32 * KT, THREADS, LOOSE>;
+  using Stage = RowStage<TI, 32 * KT, kDeltaThreads, LOOSE>;
   using Sh = DeltaShape<TI, KT>;
   static __device__ __forceinline__ void put(const Stage& st, int round, bf16_t* dst) {
     if (!LOOSE && st.len == kChunk && st.cols >= Sh::kRows) put_as<true>(st, round, dst);
@@ -519,14 +520,14 @@ enum DeltaMode {
   kDeltaSegBack = 4 // only a segment's adjoint before it from zero
 };
 
-template <typename TI, int KT, int MODE, int COLS>
+template <typename TI, int KT, int MODE>
 struct DeltaLds {
   using Sh = DeltaShape<TI, KT>;
   static constexpr bool kQ = MODE != kDeltaKeep && MODE != kDeltaSeg;
   static constexpr size_t kRows = (size_t)(kQ ? 2 : 1) * Sh::kTerms * Sh::kTile;
   static constexpr size_t kTris = (size_t)(kQ ? 2 : 1) * kDeltaTerms * kDeltaTri;
   // values: strides that spread the transposing reads over the banks
-  static constexpr int kValStride = COLS + (Sh::kF32 ? 4 : 8);
+  static constexpr int kValStride = kWalkCols + (Sh::kF32 ? 4 : 8);
   static constexpr size_t kVals = (size_t)kChunk * kValStride * (Sh::kF32 ? 4 : 2);
   static constexpr size_t kBytes =
       (kRows + kTris) * sizeof(bf16_t) + kVals + kDeltaGates * sizeof(float);
@@ -539,9 +540,8 @@ __device__ __forceinline__ T& lane_at(T* base, int64_t i, uint32_t off) {
 }
 
 // A triangle on its way to LDS, where it lies in terms.
-template <int THREADS>
 struct TriStage {
-  static constexpr int kN = kDeltaTri / 4 / THREADS;
+  static constexpr int THREADS = kDeltaThreads, kN = kDeltaTri / 4 / THREADS;
   static_assert(kN * 4 * THREADS == kDeltaTri, "whole rounds");
   f4x v[kN];
   __device__ __forceinline__ void load(const float* from, int tid) {
@@ -568,20 +568,20 @@ struct TriStage {
 // and 4.2 us as one of two; its matrix instructions are 1.3 us of that, vector issue and LDS
 // as much again each.  Eight waves on 128 columns share rows, T and scores, but their barriers
 // stop the whole CU: 256 heads of 128 x 128 over 4096 tokens 546 us, two workgroups 505.
-template <typename TI, int KT, int MODE>
+template <typename TI, int KT>
 constexpr int delta_waves_per_simd() {
   if (sizeof(TI) == 4 || KT > 4) return 1;
   return 2;
 }
 
-template <typename TI, int KT, bool LOOSE, int MODE, int W, int CT>
-__global__ __launch_bounds__(64 * W) __attribute__((
-    amdgpu_waves_per_eu(delta_waves_per_simd<TI, KT, MODE>(), delta_waves_per_simd<TI, KT, MODE>())))
+template <typename TI, int KT, bool LOOSE, int MODE>
+__global__ __launch_bounds__(kDeltaThreads) __attribute__((
+    amdgpu_waves_per_eu(delta_waves_per_simd<TI, KT>(), delta_waves_per_simd<TI, KT>())))
 void delta_walk_kernel(DeltaParams p) {
-  constexpr int THREADS = 64 * W, COLS = 16 * W * CT;
+  constexpr int THREADS = kDeltaThreads, COLS = kWalkCols;
   using Sh = DeltaShape<TI, KT>;
-  using Rows = DeltaRows<TI, KT, LOOSE, THREADS>;
-  using Lds = DeltaLds<TI, KT, MODE, COLS>;
+  using Rows = DeltaRows<TI, KT, LOOSE>;
+  using Lds = DeltaLds<TI, KT, MODE>;
   constexpr int NT = Sh::kTerms, HT = 2 * KT;  // terms of inputs; 16-row tiles
   constexpr bool BACK = MODE == kDeltaBack || MODE == kDeltaSegBack, QUERY = Lds::kQ;
   constexpr bool OUT = MODE == kDeltaOut;
@@ -614,7 +614,7 @@ void delta_walk_kernel(DeltaParams p) {
   const int bh = blk / segs, b = bh / p.H, h = bh - b * p.H;
   const bool unit_state = CARRY && tile >= p.ctiles;
   const int c0 = COLS * (unit_state ? tile - p.ctiles : tile);
-  const int cw = 16 * CT * wave + (lane & 15);  // this lane's first column in the workgroup
+  const int cw = 16 * wave + (lane & 15);  // this lane's first column in the workgroup
   const int width = unit_state ? 0 : p.P - c0;  // columns with values
   const int grp = h / (p.H / p.G);
   const int64_t vstride = (int64_t)p.H * p.P;
@@ -626,28 +626,26 @@ void delta_walk_kernel(DeltaParams p) {
   const int nj = high - low;
   auto chunk_of = [&](int j) { return BACK ? high - 1 - j : low + j; };
 
-  f4x st[CT][HT];
+  f4x st[HT];
 #pragma unroll
-  for (int k = 0; k < CT; ++k)
+  for (int i = 0; i < HT; ++i)
 #pragma unroll
-    for (int i = 0; i < HT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int n = 16 * i + 4 * g + r, cc = cw + 16 * k;
-        float v = 0.f;
-        if constexpr (SEG) {
-          v = unit_state && n == c0 + cc ? 1.f : 0.f;
-        } else if (p.nseg > 1) {
-          v = p.seg_state[(((int64_t)bh * p.nseg + seg) * (32 * KT) + n) * p.Pp + c0 + cc];
-        } else if (p.s0 != nullptr) {
-          if (cc < width && n < p.N) v = p.s0[state + (int64_t)n * p.P + c0 + cc];
-        }
-        st[k][i][r] = v;
+    for (int r = 0; r < 4; ++r) {
+      const int n = 16 * i + 4 * g + r;
+      float v = 0.f;
+      if constexpr (SEG) {
+        v = unit_state && n == c0 + cw ? 1.f : 0.f;
+      } else if (p.nseg > 1) {
+        v = p.seg_state[(((int64_t)bh * p.nseg + seg) * (32 * KT) + n) * p.Pp + c0 + cw];
+      } else if (p.s0 != nullptr) {
+        if (cw < width && n < p.N) v = p.s0[state + (int64_t)n * p.P + c0 + cw];
       }
+      st[i][r] = v;
+    }
 
   static_assert(Rows::Stage::kRounds == 1, "rows in one round");
   typename Rows::Stage rk, rq;
-  TriStage<THREADS> tri;
+  TriStage tri;
   using Vals = RowStage<TI, COLS, THREADS, LOOSE>;
   static_assert(Vals::kRounds == 1, "values in one round");
   Vals rv;
@@ -682,27 +680,23 @@ void delta_walk_kernel(DeltaParams p) {
     rv.load(0);
   };
   // A chunk's results, stored while the next one is worked on.
-  f4x late[CT][4];
+  f4x late[4];
   const uint32_t state_off = (uint32_t)(4 * g * p.Pp + c0 + cw) * 4u;  // of the workspace's rows
   auto leave_as = [&](auto* out, int64_t first, int len) {
     using TO = std::remove_pointer_t<decltype(out)>;
     const uint32_t off = (uint32_t)(4 * g * (uint32_t)vstride + (uint32_t)cw) * (uint32_t)sizeof(TO);
     out += first;
+    if (cw >= width) return;
+    if (len == kChunk) {
 #pragma unroll
-    for (int k = 0; k < CT; ++k) {
-      if (cw + 16 * k >= width) continue;
-      if (len == kChunk) {
+      for (int i = 0; i < 16; ++i)
+        lane_at(out, (16 * (i >> 2) + (i & 3)) * vstride, off) = from_f32<TO>(late[i >> 2][i & 3]);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          lane_at(out, (16 * (i >> 2) + (i & 3)) * vstride + 16 * k, off) =
-              from_f32<TO>(late[k][i >> 2][i & 3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (16 * (i >> 2) + 4 * g + (i & 3) < len)
-            lane_at(out, (16 * (i >> 2) + (i & 3)) * vstride + 16 * k, off) =
-                from_f32<TO>(late[k][i >> 2][i & 3]);
-      }
+      for (int i = 0; i < 16; ++i)
+        if (16 * (i >> 2) + 4 * g + (i & 3) < len)
+          lane_at(out, (16 * (i >> 2) + (i & 3)) * vstride, off) =
+              from_f32<TO>(late[i >> 2][i & 3]);
     }
   };
   auto leave = [&](int cc) {
@@ -710,11 +704,8 @@ void delta_walk_kernel(DeltaParams p) {
     if (KEEP) {
       float* to = p.rows + ((int64_t)bh * p.nc + cc) * kChunk * p.Pp;
 #pragma unroll
-      for (int k = 0; k < CT; ++k)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          lane_at(to, (int64_t)(16 * (i >> 2) + (i & 3)) * p.Pp + 16 * k, state_off) =
-              late[k][i >> 2][i & 3];
+      for (int i = 0; i < 16; ++i)
+        lane_at(to, (int64_t)(16 * (i >> 2) + (i & 3)) * p.Pp, state_off) = late[i >> 2][i & 3];
     }
     const int64_t first = vfirst + t0 * vstride;
     if ((OUT || MODE == kDeltaBack) && p.out_bf16)
@@ -744,19 +735,17 @@ void delta_walk_kernel(DeltaParams p) {
     if (KEEP) {
       float* to = p.states + unit * (32 * KT) * p.Pp;
 #pragma unroll
-      for (int k = 0; k < CT; ++k)
+      for (int i = 0; i < HT; ++i)
 #pragma unroll
-        for (int i = 0; i < HT; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            lane_at(to, (int64_t)(16 * i + r) * p.Pp + 16 * k, state_off) = st[k][i][r];
+        for (int r = 0; r < 4; ++r)
+          lane_at(to, (int64_t)(16 * i + r) * p.Pp, state_off) = st[i][r];
     }
     if (j + 1 < nj) fetch(j + 1);
 
     // The decayed scores of K Q^T (walking back: of Q K^T), whose accumulators are the triangle's
     // operand register for register: its six blocks of two tiles, two or three tiles per wave.
     if constexpr (QUERY) {
-      static_assert(W == 4, "blocks by wave");
+      static_assert(kDeltaWaves == 4, "blocks by wave");
       const int lane_now = apart(lane), col = lane_now & 15, g4 = 4 * (lane_now >> 4);
       auto block = [&](int rt, int b) {  // operand row tile, 32-block
         f4x sc[2];
@@ -810,14 +799,12 @@ void delta_walk_kernel(DeltaParams p) {
     }
 
     // K h, and Q h, the next rows on their way
-    f4x z[CT][4], y[CT][4];
+    f4x z[4], y[4];
 #pragma unroll
-    for (int k = 0; k < CT; ++k)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        z[k][t] = f4x{0.f, 0.f, 0.f, 0.f};
-        y[k][t] = f4x{0.f, 0.f, 0.f, 0.f};
-      }
+    for (int t = 0; t < 4; ++t) {
+      z[t] = f4x{0.f, 0.f, 0.f, 0.f};
+      y[t] = f4x{0.f, 0.f, 0.f, 0.f};
+    }
     {
       // two sets of operands where the registers allow it (with queries they spill: 64K-token
       // prompt's walk 833 us, with one set 732 us)
@@ -833,240 +820,200 @@ void delta_walk_kernel(DeltaParams p) {
       if (kSets == 2) rows(0);
 #pragma unroll
       for (int n = 0; n < KT; ++n) {
-        bf8x hb[CT][S];
-#pragma unroll
-        for (int k = 0; k < CT; ++k) split_tiles<S>(st[k][2 * n], st[k][2 * n + 1], hb[k]);
+        bf8x hb[S];
+        split_tiles<S>(st[2 * n], st[2 * n + 1], hb);
         if (kSets == 1) rows(n);
         else if (n + 1 < KT) rows(n + 1);
-#pragma unroll
-        for (int k = 0; k < CT; ++k) {
-          mma_tiles<NT, S, 4>(ak[n % kSets], hb[k], z[k]);
-          if (OUT) mma_tiles<NT, S, 4>(aq[n % kSets], hb[k], y[k]);
-        }
+        mma_tiles<NT, S, 4>(ak[n % kSets], hb, z);
+        if (OUT) mma_tiles<NT, S, 4>(aq[n % kSets], hb, y);
       }
     }
     if (QUERY) __syncthreads();  // the scores are there
 
     // this lane's columns of the values; an infinity or a NaN of v reaches its own column from
     // its token on
-    f4x vv[CT][4];
-    int limit[CT];
+    f4x vv[4];
+    float odd = 0.f;
 #pragma unroll
-    for (int k = 0; k < CT; ++k) {
-      float odd = 0.f;
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (Sh::kF32) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if constexpr (Sh::kF32) {
+        for (int r = 0; r < 4; ++r)
+          vv[t][r] = sV[(16 * t + 4 * g + r) * Lds::kValStride + cw];
+      } else {
+        typedef __attribute__((address_space(3))) s4x* lds_s4;
+        const int i = lane & 15;
+        const s4x q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s4)(sV + (16 * t + 4 * g + (i >> 2)) * Lds::kValStride + 16 * wave +
+                     4 * (i & 3)));
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            vv[k][t][r] = sV[(16 * t + 4 * g + r) * Lds::kValStride + cw + 16 * k];
-        } else {
-          typedef __attribute__((address_space(3))) s4x* lds_s4;
-          const int i = lane & 15;
-          const s4x q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s4)(sV + (16 * t + 4 * g + (i >> 2)) * Lds::kValStride + 16 * CT * wave +
-                       16 * k + 4 * (i & 3)));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) vv[k][t][r] = to_f32((bf16_t)q[r]);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) odd = fmaf(vv[k][t][r], 0.f, odd);
+        for (int r = 0; r < 4; ++r) vv[t][r] = to_f32((bf16_t)q[r]);
       }
-      limit[k] = bad;
-      if constexpr (!BACK) {
-        if (!unit_state && __ballot(!(odd == 0.f))) {
-          __builtin_amdgcn_sched_barrier(0);
-          int first = kChunk;
 #pragma unroll
-          for (int i = 15; i >= 0; --i)
-            if (not_finite(vv[k][i >> 2][i & 3])) first = 16 * (i >> 2) + 4 * g + (i & 3);
-          int o = __shfl_xor(first, 16);
-          first = o < first ? o : first;
-          o = __shfl_xor(first, 32);
-          first = o < first ? o : first;
+      for (int r = 0; r < 4; ++r) odd = fmaf(vv[t][r], 0.f, odd);
+    }
+    int limit = bad;
+    if constexpr (!BACK) {
+      if (!unit_state && __ballot(!(odd == 0.f))) {
+        __builtin_amdgcn_sched_barrier(0);
+        int first = kChunk;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (16 * (i >> 2) + 4 * g + (i & 3) >= first) vv[k][i >> 2][i & 3] = 0.f;
-          limit[k] = first < bad ? first : bad;
-        }
+        for (int i = 15; i >= 0; --i)
+          if (not_finite(vv[i >> 2][i & 3])) first = 16 * (i >> 2) + 4 * g + (i & 3);
+        int o = __shfl_xor(first, 16);
+        first = o < first ? o : first;
+        o = __shfl_xor(first, 32);
+        first = o < first ? o : first;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (16 * (i >> 2) + 4 * g + (i & 3) >= first) vv[i >> 2][i & 3] = 0.f;
+        limit = first < bad ? first : bad;
       }
     }
     auto gates = [&](int which, int t) {
       return *reinterpret_cast<const f4x*>(sG + which * kChunk + 16 * t + 4 * g);
     };
     // c += the triangle's (or its transpose's) product with values in terms
-    auto triangle = [&](auto nt, auto nb, const bf16_t* tri_in, int m, auto& v, f4x (*acc)[4]) {
-      constexpr int NA = decltype(nt)::value, NB = decltype(nb)::value;
+    auto triangle = [&](auto terms, const bf16_t* tri_in, int m, const bf8x* v, f4x* acc) {
+      constexpr int NB = decltype(terms)::value;
 #pragma unroll
       for (int t0 = 0; t0 < 4; t0 += 2) {  // operands of two tiles at a time
         if (BACK ? t0 >= 2 * m + 2 : t0 < 2 * m) continue;
-        bf8x a[2][NA];
+        bf8x a[2][S];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int blk2 = BACK ? tri_block_t(t0 + t, m) : tri_block(t0 + t, m);
 #pragma unroll
-          for (int s = 0; s < NA; ++s)
+          for (int s = 0; s < S; ++s)
             a[t][s] =
                 *reinterpret_cast<const bf8x*>(tri_in + s * kDeltaTri + blk2 * 512 + lane * 8);
         }
-#pragma unroll
-        for (int k = 0; k < CT; ++k) mma_tiles<NA, NB, 2>(a, v[k], acc[k] + t0);
+        mma_tiles<S, NB, 2>(a, v, acc + t0);
       }
     };
     using Three = std::integral_constant<int, S>;
     using OfInput = std::integral_constant<int, NT>;
     // state += columns of staged rows times values in terms
-    auto update = [&](const bf16_t* tile_in, int m, auto& v) {
+    auto update = [&](const bf16_t* tile_in, int m, const bf8x* v) {
       constexpr int kMost = 4, kAtOnce = NT == 1 ? (HT < kMost ? HT : kMost) : 2;
 #pragma unroll
       for (int i0 = 0; i0 < HT; i0 += kAtOnce) {
         bf8x a[kAtOnce][NT];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) column_operand<Sh>(tile_in, i0 + i, m, lane, a[i]);
-#pragma unroll
-        for (int k = 0; k < CT; ++k) mma_tiles<NT, S, kAtOnce>(a, v[k], st[k] + i0);
+        mma_tiles<NT, S, kAtOnce>(a, v, st + i0);
       }
     };
     const float carry = sG[3 * kChunk];
-    f4x o[CT][4];
+    f4x o[4];
 #pragma unroll
-    for (int k = 0; k < CT; ++k)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) o[k][t] = f4x{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) o[t] = f4x{0.f, 0.f, 0.f, 0.f};
     if constexpr (!BACK) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const f4x e = gates(0, t);
-#pragma unroll
-        for (int k = 0; k < CT; ++k) {
-          vv[k][t] -= e * z[k][t];
-          if (OUT) y[k][t] *= e;
-        }
+        vv[t] -= e * z[t];
+        if (OUT) y[t] *= e;
       }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x rb[CT][S];
-#pragma unroll
-        for (int k = 0; k < CT; ++k) split_tiles<S>(vv[k][2 * m], vv[k][2 * m + 1], rb[k]);
-        triangle(Three(), Three(), sT, m, rb, o);
+        bf8x rb[S];
+        split_tiles<S>(vv[2 * m], vv[2 * m + 1], rb);
+        triangle(Three(), sT, m, rb, o);
       }
-      f4x u[CT][4];
+      f4x u[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const f4x e = gates(2, t);
-#pragma unroll
-        for (int k = 0; k < CT; ++k) u[k][t] = e * o[k][t];
+        u[t] = e * o[t];
       }
       if (OUT) {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          bf8x ub[CT][S];
-#pragma unroll
-          for (int k = 0; k < CT; ++k) split_tiles<S>(u[k][2 * m], u[k][2 * m + 1], ub[k]);
-          triangle(Three(), Three(), sS, m, ub, y);
+          bf8x ub[S];
+          split_tiles<S>(u[2 * m], u[2 * m + 1], ub);
+          triangle(Three(), sS, m, ub, y);
         }
       }
 #pragma unroll
-      for (int k = 0; k < CT; ++k)
-#pragma unroll
-        for (int i = 0; i < HT; ++i) st[k][i] *= carry;
+      for (int i = 0; i < HT; ++i) st[i] *= carry;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x ub[CT][S];
+        bf8x ub[S];
         const f4x e0 = gates(1, 2 * m), e1 = gates(1, 2 * m + 1);
-#pragma unroll
-        for (int k = 0; k < CT; ++k) split_tiles<S>(u[k][2 * m] * e0, u[k][2 * m + 1] * e1, ub[k]);
+        split_tiles<S>(u[2 * m] * e0, u[2 * m + 1] * e1, ub);
         update(sK, m, ub);
       }
 #pragma unroll
-      for (int k = 0; k < CT; ++k) {
+      for (int t = 0; t < 4; ++t)
+        if (!SEG) late[t] = OUT ? y[t] : o[t];
+      if (limit < len) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          if (!SEG) late[k][t] = OUT ? y[k][t] : o[k][t];
-        if (limit[k] < len) {
+        for (int i = 0; i < HT; ++i)
 #pragma unroll
-          for (int i = 0; i < HT; ++i)
+          for (int r = 0; r < 4; ++r) st[i][r] = __builtin_nanf("");
 #pragma unroll
-            for (int r = 0; r < 4; ++r) st[k][i][r] = __builtin_nanf("");
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (16 * (i >> 2) + 4 * g + (i & 3) >= limit[k])
-              late[k][i >> 2][i & 3] = __builtin_nanf("");
-        }
+        for (int i = 0; i < 16; ++i)
+          if (16 * (i >> 2) + 4 * g + (i & 3) >= limit)
+            late[i >> 2][i & 3] = __builtin_nanf("");
       }
     } else {
       // A bad token reaches the adjoints and dV of those columns that anything behind it reaches
-      bool reached[CT];
-#pragma unroll
-      for (int k = 0; k < CT; ++k) {
-        reached[k] = false;
-        if (bad >= len) continue;  // (uniform)
+      bool reached = false;
+      if (bad < len) {  // (uniform)
         bool some = false;
 #pragma unroll
         for (int i = 0; i < HT; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) some |= !(st[k][i][r] == 0.f);
+          for (int r = 0; r < 4; ++r) some |= !(st[i][r] == 0.f);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          some |= 16 * (i >> 2) + 4 * g + (i & 3) >= bad && !(vv[k][i >> 2][i & 3] == 0.f);
+          some |= 16 * (i >> 2) + 4 * g + (i & 3) >= bad && !(vv[i >> 2][i & 3] == 0.f);
         const uint64_t rows = __ballot(some);
-        reached[k] = ((rows | rows >> 16 | rows >> 32 | rows >> 48) >> (lane & 15) & 1) != 0;
+        reached = ((rows | rows >> 16 | rows >> 32 | rows >> 48) >> (lane & 15) & 1) != 0;
       }
       // dU = w K a + S^T dY, dV = T^T (beta dU)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const f4x e = gates(1, t);
-#pragma unroll
-        for (int k = 0; k < CT; ++k) z[k][t] *= e;
+        z[t] *= e;
       }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x db[CT][NT];
-#pragma unroll
-        for (int k = 0; k < CT; ++k) split_tiles<NT>(vv[k][2 * m], vv[k][2 * m + 1], db[k]);
-        triangle(Three(), OfInput(), sS, m, db, z);
+        bf8x db[NT];
+        split_tiles<NT>(vv[2 * m], vv[2 * m + 1], db);
+        triangle(OfInput(), sS, m, db, z);
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const f4x e = gates(2, t);
-#pragma unroll
-        for (int k = 0; k < CT; ++k) z[k][t] *= e;
+        z[t] *= e;
       }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x ub[CT][S];
-#pragma unroll
-        for (int k = 0; k < CT; ++k) split_tiles<S>(z[k][2 * m], z[k][2 * m + 1], ub[k]);
-        triangle(Three(), Three(), sT, m, ub, o);
+        bf8x ub[S];
+        split_tiles<S>(z[2 * m], z[2 * m + 1], ub);
+        triangle(Three(), sT, m, ub, o);
       }
 #pragma unroll
-      for (int k = 0; k < CT; ++k)
-#pragma unroll
-        for (int i = 0; i < HT; ++i) st[k][i] *= carry;
+      for (int i = 0; i < HT; ++i) st[i] *= carry;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        bf8x yb[CT][S], vb[CT][S];
+        bf8x yb[S], vb[S];
         const f4x e0 = gates(0, 2 * m), e1 = gates(0, 2 * m + 1);
-#pragma unroll
-        for (int k = 0; k < CT; ++k) {
-          split_tiles<S>(vv[k][2 * m] * e0, vv[k][2 * m + 1] * e1, yb[k]);
-          split_tiles<S>(o[k][2 * m] * -e0, o[k][2 * m + 1] * -e1, vb[k]);
-        }
+        split_tiles<S>(vv[2 * m] * e0, vv[2 * m + 1] * e1, yb);
+        split_tiles<S>(o[2 * m] * -e0, o[2 * m + 1] * -e1, vb);
         update(sQ, m, yb);
         update(sK, m, vb);
       }
 #pragma unroll
-      for (int k = 0; k < CT; ++k)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) late[k][t] = o[k][t];
-#pragma unroll
-      for (int k = 0; k < CT; ++k) {
-        if (bad >= len || !reached[k]) continue;
+      for (int t = 0; t < 4; ++t) late[t] = o[t];
+      if (reached) {
         const float nan = __builtin_nanf("");
 #pragma unroll
-        for (int i = 0; i < HT; ++i) st[k][i] = f4x{nan, nan, nan, nan};
+        for (int i = 0; i < HT; ++i) st[i] = f4x{nan, nan, nan, nan};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) late[k][t] = f4x{nan, nan, nan, nan};
+        for (int t = 0; t < 4; ++t) late[t] = f4x{nan, nan, nan, nan};
       }
     }
   }
@@ -1075,25 +1022,20 @@ void delta_walk_kernel(DeltaParams p) {
     const int64_t at = (int64_t)bh * p.nseg + seg;
     const int ld = unit_state ? 32 * KT : p.Pp;
     float* to = unit_state ? p.seg_carry + at * (32 * KT) * (32 * KT) : p.seg_state + at * (32 * KT) * p.Pp;
+    if (c0 + cw >= ld) return;
 #pragma unroll
-    for (int k = 0; k < CT; ++k) {
-      if (c0 + cw + 16 * k >= ld) continue;
+    for (int i = 0; i < HT; ++i)
 #pragma unroll
-      for (int i = 0; i < HT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          to[(int64_t)(16 * i + 4 * g + r) * ld + c0 + cw + 16 * k] = st[k][i][r];
-    }
+      for (int r = 0; r < 4; ++r)
+        to[(int64_t)(16 * i + 4 * g + r) * ld + c0 + cw] = st[i][r];
   } else if (p.s_final != nullptr && seg == p.nseg - 1) {
 #pragma unroll
-    for (int k = 0; k < CT; ++k)
+    for (int i = 0; i < HT; ++i)
 #pragma unroll
-      for (int i = 0; i < HT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int n = 16 * i + 4 * g + r, cc = cw + 16 * k;
-          if (cc < width && n < p.N) p.s_final[state + (int64_t)n * p.P + c0 + cc] = st[k][i][r];
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int n = 16 * i + 4 * g + r;
+        if (cw < width && n < p.N) p.s_final[state + (int64_t)n * p.P + c0 + cw] = st[i][r];
+      }
   }
 }
 
@@ -1175,7 +1117,8 @@ template <typename TI, int KT, bool LOOSE>
 __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParams p) {
   using Sh = DeltaShape<TI, KT>;
   using Lds = GradLds<TI, KT>;
-  using Rows = DeltaRows<TI, KT, LOOSE, kGradThreads / 2>;
+  using Rows = DeltaRows<TI, KT, LOOSE>;
+  static_assert(kGradThreads == 2 * kDeltaThreads, "half of the threads for K, half for Q");
   constexpr int NT = Sh::kTerms, S = kDeltaTerms, N = Sh::kRows;
   constexpr int kTokenTerm = kChunk * 32, kStateTerm = N * 32;  // values of a term
   constexpr int kStatePacks = (N * 4 + kGradThreads - 1) / kGradThreads;
@@ -1218,7 +1161,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaGradParam
     rp.B = p.B;
     rp.L = p.L;
     typename Rows::Stage st;
-    Rows::place(st, half ? p.q : p.k, rp, b, grp, t0, len, tid & (kGradThreads / 2 - 1));
+    Rows::place(st, half ? p.q : p.k, rp, b, grp, t0, len, tid & (kDeltaThreads - 1));
     st.load(0);
     static_assert(Rows::Stage::kRounds == 1, "rows in one round");
     if (!half && st.wild()) st.drop_wild();
@@ -1618,19 +1561,16 @@ int delta_prep(const DeltaParams& p, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
-// Waves of a walk's workgroup and 16-column tiles of a wave.
-constexpr int kWalkWaves = 4, kWalkTiles = 1, kWalkCols = 16 * kWalkWaves * kWalkTiles;
-
 template <typename TI, int KT, bool LOOSE, int MODE>
 int delta_walk(const DeltaParams& p, hipStream_t s) {
-  constexpr int W = kWalkWaves, CT = kWalkTiles;
-  constexpr size_t lds = DeltaLds<TI, KT, MODE, kWalkCols>::kBytes;
+  constexpr size_t lds = DeltaLds<TI, KT, MODE>::kBytes;
   static_assert(lds <= 160 * 1024, "a CU's LDS");
   const int tiles = p.ctiles + (MODE == kDeltaSeg ? (32 * KT + kWalkCols - 1) / kWalkCols : 0);
   const int segs = MODE >= kDeltaSeg ? p.state_segs : p.nseg;
-  allow_dynamic_lds(delta_walk_kernel<TI, KT, LOOSE, MODE, W, CT>, lds);
-  hipLaunchKernelGGL((delta_walk_kernel<TI, KT, LOOSE, MODE, W, CT>),
-                     dim3((unsigned)((int64_t)p.B * p.H * segs * tiles)), dim3(64 * W), lds, s, p);
+  allow_dynamic_lds(delta_walk_kernel<TI, KT, LOOSE, MODE>, lds);
+  hipLaunchKernelGGL((delta_walk_kernel<TI, KT, LOOSE, MODE>),
+                     dim3((unsigned)((int64_t)p.B * p.H * segs * tiles)), dim3(kDeltaThreads), lds,
+                     s, p);
   return hipGetLastError() == hipSuccess ? SWIMBA_OK : SWIMBA_EHIP;
 }
 
@@ -1663,7 +1603,7 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
   }
 }
 
-// First states of the segments, h(i + 1) = M_i h(i) + end(i), from the state pass's
+// First states of the segments (two at least), h(i + 1) = M_i h(i) + end(i), from the state pass's
 // transitions M (walking back: their transposes) and ends, in place.  Four waves take the
 // rows of 16 columns of one state in turn of 16-row tiles, in fp32 on the matrix units; the next
 // transition is on its way while one is applied.  Bound by its chain: 3.7 us per segment of
@@ -1717,10 +1657,8 @@ __global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaPara
       }
     }
   }
-  if (p.nseg > 1) {
-    load_end(0);
-    load_part(0, 0);
-  }
+  load_end(0);
+  load_part(0, 0);
   for (int s = 0; s < p.nseg; ++s) {
     float* st = p.seg_state + (bh * p.nseg + s) * N * p.Pp + c;
 #pragma unroll
