@@ -1,6 +1,9 @@
 // The gated delta rule: host side of its phases (delta.hpp) and the single-token step.
 #include "delta.hpp"
 
+#include <algorithm>
+#include <cmath>
+
 namespace swimba {
 namespace {
 
@@ -52,40 +55,65 @@ constexpr size_t kGateBytes = kDeltaGates * sizeof(float);
 // Segments of the walks.  A walk's chunks follow each other; where the independent ones leave
 // CUs idle, they are cut into segments, whose transitions and ends are made first (a state
 // pass over the state's columns and as many more as it has rows) and joined.  Taken is the
-// number of the least time, in units of a chunk's walk by a workgroup that shares its CU.
-// Measured, whole against cut: 8 heads of 64 x 64 over 32768 tokens 1858 / 194 us in 32
-// segments, one head of 128 x 128 over 65536 tokens 4905 / 341 us in 48, 40 heads of 128 x 64
-// over 65536 tokens 5390 / 2000 us in 12, 256 heads of 128 x 128 over 4096 tokens 625 / 998 us
-// in 2.
+// number of the least time, summed up from measured ones.
 struct SegPlan {
   int nseg = 1, seg_chunks = 1;
 };
 
-// A step of `wgs` workgroups of which a CU holds up to `most`: `alone`, or `full` when it does.
-double step_time(double wgs, double alone, double full, int most, double cus) {
-  if (wgs <= cus) return alone;
-  const double each = wgs / cus;
-  if (most == 1) return alone * (each + 0.1);
-  if (each <= most) return alone + (full - alone) * (each < 2 ? 1.0 : each - 1) / (most - 1);
-  return full * (each / most + 0.1);
+// Microseconds of a chunk in a workgroup's walk, with up to one workgroup per CU and where it
+// shares its CU with another (traces of 16 chunks by 256 and by 512 workgroups; of fp32
+// inputs and of 256 keys a CU's LDS holds one), and of a link of a join forwards and back (8
+// heads of 64 columns, 32 segments).
+struct WalkTimes {
+  double out[2], keep[2], back[2], seg[2], seg_back[2], join[2];
+};
+constexpr WalkTimes kTimesBf16[4] = {
+    {{4.1, 5.8}, {2.6, 4.7}, {4.9, 7.0}, {2.1, 2.9}, {4.1, 5.7}, {0.75, 0.65}},  // 32 keys
+    {{4.8, 7.1}, {3.0, 6.1}, {5.4, 8.6}, {2.4, 3.5}, {4.5, 7.3}, {1.0, 0.9}},    // 64
+    {{6.2, 9.6}, {4.1, 8.6}, {7.0, 12.0}, {3.2, 4.8}, {5.7, 9.0}, {2.5, 2.6}},   // 128
+    {{10.0, 0}, {7.2, 0}, {11.4, 0}, {5.0, 0}, {9.5, 0}, {9.8, 54.0}}};          // 256
+constexpr WalkTimes kTimesF32[3] = {
+    {{5.4, 0}, {3.2, 0}, {6.0, 0}, {2.6, 0}, {5.0, 0}, {0.75, 0.65}},
+    {{6.9, 0}, {4.4, 0}, {7.7, 0}, {3.4, 0}, {6.4, 0}, {1.0, 0.9}},
+    {{10.1, 0}, {6.3, 0}, {11.3, 0}, {4.9, 0}, {10.2, 0}, {2.5, 2.6}}};
+constexpr double kJoinBytes = 4e6;  // of transitions and states, per microsecond
+constexpr double kTwoLaunches = 8;  // microseconds of the state pass and the join on their own
+
+// A chunk's step of `wgs` workgroups, in rounds of all that the CUs hold.
+double step_time(double wgs, const double (&us)[2], bool one, double cus) {
+  const double round = one ? cus : 2 * cus, whole = std::floor(wgs / round);
+  const double rest = wgs - whole * round, shared = one ? us[0] : us[1];
+  return whole * shared + (rest <= 0 ? 0.0 : rest <= cus ? us[0] : shared);
 }
 
+// Against the best of a sweep over 1 to 128 segments (16 shapes, both ways) its choice takes 4 %
+// more at most.  Whole walks, its choice and other cuts, forward: one head of 128 x 128 over
+// 65536 tokens 5342, 317 (64 segments), 592 (16), 417 us (128); 8 heads of 64 x 64 over 32768
+// tokens 2132, 197 (32), 264 (16), 271 (128); 40 heads of 128 x 64 over 65536 tokens 5721, 2030
+// (25), 2294 (5), 2452 (128); 256 heads of 128 x 128 over 4096 tokens 702 (whole), 1028 (2);
+// 8 heads of 256 x 128 over 8192 tokens 1015, 352 (11), 489 (20), and back 2084, 1357 (8),
+// 2142 (20), whose joins are its longest part.
 SegPlan plan_segments(const swimba_delta_rule_args* a, bool back, int dev) {
   const int64_t tiles = (a->P + kWalkCols - 1) / kWalkCols, bh = (int64_t)a->B * a->H;
-  const int64_t more = (padded_rows(a->N) + kWalkCols - 1) / kWalkCols;
+  const int rows = padded_rows(a->N), size = rows <= 32 ? 0 : rows <= 64 ? 1 : rows <= 128 ? 2 : 3;
+  const int64_t more = (rows + kWalkCols - 1) / kWalkCols;
   const int64_t nc = (a->L + kChunk - 1) / kChunk;
-  const double cus = device_cus(dev), join = 0.45;
-  const bool one = a->in_dtype == SWIMBA_F32 || a->N > 128;  // a CU's LDS
+  const double cus = device_cus(dev);
+  const bool f32 = a->in_dtype == SWIMBA_F32, one = f32 || rows > 128;
+  const WalkTimes& us = f32 ? kTimesF32[size] : kTimesBf16[size];
+  const double link = (double)(bh * tiles) * rows * (rows + 2 * kWalkCols) * sizeof(float) / kJoinBytes;
   auto time = [&](int64_t n) {
-    const double len = (double)((nc + n - 1) / n), w = (double)(bh * tiles * n);
-    const double walk = step_time(w, 0.6, 1.0, one ? 1 : 2, cus);
-    double t = walk * (back ? 2.2 : 1.0);
+    const double w = (double)(bh * tiles * n);
+    double chunk = back ? step_time(w, us.keep, one, cus) + step_time(w, us.back, one, cus)
+                        : step_time(w, us.out, one, cus);
+    double joins = 0;
     if (n > 1) {
-      const double states = (double)(bh * (tiles + more) * (back ? n : n - 1));
-      t += step_time(states, 0.45, 0.7, one ? 1 : 2, cus);
-      if (back) t += 0.9 * step_time(w * (double)(n - 1) / (double)n, 0.6, 1.0, one ? 1 : 2, cus);
+      chunk += step_time((double)(bh * (tiles + more) * (back ? n : n - 1)), us.seg, one, cus);
+      if (back) chunk += step_time((double)(bh * tiles * (n - 1)), us.seg_back, one, cus);
+      joins = (double)(n - 1) * std::max(us.join[0], link) + kTwoLaunches;
+      if (back) joins += (double)(n - 1) * std::max(us.join[1], link) + kTwoLaunches;
     }
-    return len * t + (n > 1 ? (double)n * join * (back ? 2 : 1) + 2.0 : 0.0);
+    return (double)((nc + n - 1) / n) * chunk + joins;
   };
   SegPlan best;
   best.seg_chunks = (int)nc;

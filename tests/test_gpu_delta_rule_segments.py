@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 CASES = [  # the last segment is shorter than the others, and a document ends inside a chunk
     ("bf16", (1, 1500, 2, 1, 128, 96), 411), ("bf16", (1, 1100, 2, 2, 128, 130), 300), ("f32", (1, 1300, 2, 1, 100, 70), 500),
-    ("bf16", (1, 1300, 4, 1, 64, 200), 0), ("f32", (2, 1000, 2, 2, 128, 128), 333), ("bf16", (1, 1200, 1, 1, 256, 72), 700)]
+    ("bf16", (1, 1300, 4, 1, 64, 200), 0), ("f32", (2, 1000, 2, 2, 128, 128), 333), ("bf16", (1, 2003, 1, 1, 256, 72), 700)]
 
 
 def segments(t):
