@@ -169,6 +169,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
   }
   __syncthreads();
   float dwq[2 * kPairs] = {}, dwk[2 * kPairs] = {};
+  const int dt = kRowsAtOnce / heads, dh = kRowsAtOnce - dt * heads;  // to a thread's next row
 
   for (int64_t grp = blockIdx.x; grp < p.groups; grp += gridDim.x) {
     const int64_t t0 = grp * p.tokens;
@@ -257,8 +258,9 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormParams p) {
         }
       }
       mine.store(static_cast<TO*>(isq ? p.oq : p.ok) + to, a, b);
-      h += kRowsAtOnce;
-      while (h >= heads) {
+      t += dt;
+      h += dh;
+      if (h >= heads) {
         h -= heads;
         ++t;
       }
