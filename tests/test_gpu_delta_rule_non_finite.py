@@ -92,6 +92,22 @@ def test_value_query_or_slope(dtype, N, P, L, bad):
             same(got["dh0"][:, 1], g["dh0"][:, 1], name)
 
 
+@pytest.mark.parametrize("bad", BAD[:2])
+def test_a_decay_per_head(bad):
+    d = to_dev(make(2, 300, 4, 2, 64, 40, form="head", seed=95))
+    g = backward(d)
+    d["g"][1] = bad
+    got = backward(d)
+    assert torch.isnan(got["dlog_decay"][1]) and torch.isnan(got["dh0"][:, 1]).all()
+    for n in ("dv", "dbeta"):
+        assert torch.isnan(got[n][:, :, 1]).all(), n
+        same(got[n][:, :, [0, 2, 3]], g[n][:, :, [0, 2, 3]], n)
+    same(got["dlog_decay"][[0, 2, 3]], g["dlog_decay"][[0, 2, 3]], "dlog_decay")
+    for n in ("dq", "dk"):
+        assert torch.isnan(got[n][:, :, 0]).all(), n
+        same(got[n][:, :, 1], g[n][:, :, 1], n)
+
+
 @pytest.mark.parametrize("dtype,N,P,L,s", [("bf16", 64, 64, 150, 70), ("f32", 33, 20, 150, 128), ("bf16", 128, 96, 1500, 801),
                                            ("f32", 48, 70, 1100, 1), ("bf16", 200, 24, 2000, 640)])
 @pytest.mark.parametrize("fill", [float("nan"), float("inf")])
