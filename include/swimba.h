@@ -662,8 +662,8 @@ typedef struct {
  * swimba_delta_rule_backward -- gradients of swimba_delta_rule, from its inputs (nothing
  * of the forward pass is kept).  Workspace as there, sized by
  * swimba_delta_rule_backward_workspace_size(g) for the same arguments: per 64 tokens
- * and head two states of (N rounded up to a power of two) x (P to a multiple of 64)
- * floats, two sets of 64 rows of P and 26 KB; and where heads share q and k and the
+ * and head two states of (N rounded up to a power of two, 32 at least) x (P to a
+ * multiple of 64) floats, two sets of 64 rows of P and 26 KB; and where heads share q and k and the
  * sequences are short, rows of dq and dk for parts of the heads.  Every output is
  * deterministic.
  * An infinity or a NaN of k, beta or a decay leaves NaN in dq, dk, dbeta and

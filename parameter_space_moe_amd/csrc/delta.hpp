@@ -564,10 +564,10 @@ struct TriStage {
 
 // Two workgroups of four waves share a CU where LDS and 256 registers suffice: the stages of a
 // chunk (rows to LDS, K h, T R, U, the state's update) follow each other, and one workgroup's
-// products run while the other waits.  A chunk of 128 keys and 64 columns takes 5.5 us alone
-// and 4.2 us as one of two; its matrix instructions are 1.3 us of that, vector issue and LDS
-// as much again each.  Eight waves on 128 columns share rows, T and scores, but their barriers
-// stop the whole CU: 256 heads of 128 x 128 over 4096 tokens 546 us, two workgroups 505.
+// products run while the other waits.  A chunk of 128 keys and 64 columns takes 6.2 us alone
+// and 4.8 us as one of two; its matrix instructions are 1.5 us of that, vector issue and LDS
+// about as much again each.  Eight waves on 128 columns share rows, T and scores, but their
+// barriers stop the whole CU: 8 % slower for 256 heads of 128 x 128 over 4096 tokens.
 template <typename TI, int KT>
 constexpr int delta_waves_per_simd() {
   if (sizeof(TI) == 4 || KT > 4) return 1;
@@ -806,8 +806,8 @@ void delta_walk_kernel(DeltaParams p) {
       y[t] = f4x{0.f, 0.f, 0.f, 0.f};
     }
     {
-      // two sets of operands where the registers allow it (with queries they spill: 64K-token
-      // prompt's walk 833 us, with one set 732 us)
+      // two sets of operands where the registers allow it (with queries one does as well: 64K-token
+      // prompt 2035 us, with two sets 2033)
       constexpr int kSets = KEEP ? 2 : 1;
       bf8x ak[kSets][4][NT], aq[kSets][4][NT];
       auto rows = [&](int n) {
@@ -1105,11 +1105,12 @@ struct GradLds {
 // of the keys; waves of half 0 also take row tile rt of F, of half 1 of E.  dY, O, dV, h
 // and a pass through LDS 32 columns at a time, split into terms once for all waves, the next
 // ones on their way in registers.
-// 2 x 4096 tokens, 32 heads of 128 x 128 over 4 key heads: 330-355 us, of which a head's four
+// 2 x 4096 tokens, 32 heads of 128 x 128 over 4 key heads: 331 us, of which a head's four
 // column blocks are 60 % (the three-term products, one workgroup per CU for want of LDS and
 // registers), slopes 10 %, their products with K and Q 10 % and the sums behind them, in one
-// wave, 20 %.  Two workgroups per CU (128 registers) spill: 4 x 2048 tokens, 24 heads of
-// 64 x 64 in 270 us instead of 170.
+// wave, 20 %.  Reading states, adjoints, O and dV in fp32 (805 MB there) alone would take 152 us
+// at the copy rate.  Two workgroups per CU (128 registers) spill: 60 % slower for 4 x 2048
+// tokens of 24 heads of 64 x 64, which take 163 us.
 // From the first bad token on (whose k, beta or decay is not finite) gradients are NaN; earlier
 // tokens see the chunk without it, and the NaN that the walk back leaves in dV and a where it
 // reaches them.
@@ -1606,8 +1607,9 @@ int delta_phase(const DeltaParams& p, int phase, hipStream_t s) {
 // First states of the segments (two at least), h(i + 1) = M_i h(i) + end(i), from the state pass's
 // transitions M (walking back: their transposes) and ends, in place.  Four waves take the
 // rows of 16 columns of one state in turn of 16-row tiles, in fp32 on the matrix units; the next
-// transition is on its way while one is applied.  Bound by its chain: 3.7 us per segment of
-// 128 x 128 (12 segments of 40 heads in 42-45 us).  A transition that is not finite (a bad token
+// transition is on its way while one is applied.  Bound by its chain: 2.5 to 3 us per segment of
+// 128 x 128 (25 segments of 40 heads of 64 columns in 73 us); of 256 x 256 9.8 us, and walking
+// back, where the operands spill, 54.  A transition that is not finite (a bad token
 // in the segment, or growth beyond fp32) leaves a column that is all zero so: 0 * NaN.
 template <int KT, bool BACK>
 __global__ __launch_bounds__(kDeltaThreads, 1) void delta_carry_kernel(DeltaParams p) {

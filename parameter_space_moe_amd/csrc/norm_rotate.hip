@@ -10,9 +10,11 @@
 // heads of a few tokens and makes these tokens' cosines and sines once, in LDS: the
 // angle is a product in 64 bits, whose whole turns are taken off before it is rounded (at
 // position 10^6 an fp32 angle would be off by 0.06).  Everything else is fp32.
-// 65536 tokens of 48 heads of 64, bf16, all turned: 148 us, 5.4 TB/s (a copy: 5.3).  32768
-// tokens of 36 heads of 128: forward 102 us, 5.9 TB/s (a part of it from the caches); backward
-// 175 us, 5.2 TB/s.  256 tokens of 80 heads of 128, not turned: 5.0 us.
+// 65536 tokens of 48 heads of 64, all turned, in bf16: 148 to 160 us, 5.0 to 5.4 TB/s (a copy:
+// 5.3), in fp32 307, 5.2 TB/s.  32768 tokens of 36 heads of 128, bf16: forward 106 to 111 us, 5.4 to
+// 5.7 TB/s (a part of it from the caches), backward 176 to 181 us, 5.0 to 5.1 TB/s.  256 tokens
+// of 80 heads of 128, not turned: 5.1 us.  Sizes that are no multiple of 16 move element by
+// element: 65536 tokens of 48 heads of 72 in 436 us in bf16 and 415 in fp32, backward 1070 and 695.
 #include "pack.hpp"
 #include "swimba_internal.hpp"
 
